@@ -1,0 +1,456 @@
+"""The operators of the NVFP4 key/value cache, as they are measured: listed
+cases, drawn cases of the same ranges, their inputs, the plain form of each
+operator in elementary torch operations (32 bits, rounded once at the end) and
+its definition in 64 bits.
+
+* append: RMS norm of every query and key head (optional), rotary positions
+  (half or interleaved pairs, the whole head or its first channels), keys and
+  values quantized to NVFP4 and stored into the paged cache; then the stored
+  entries are read back from their slots as the values they stand for.
+* attend: softmax attention of the queries over a paged NVFP4 cache: one
+  query per sequence (decode), a few (speculative tokens), or long ragged
+  chunks (prefill); grouped heads, causal, optionally a sliding window.
+
+Cache layout, [n_pages, n_kv_heads, page_size * D * 9 / 8] bytes per page and
+head: key codes [S][D/2], key scales [S][D/16], value codes
+[S/8][D/16][8 tokens][8 bytes], value scales [S/8][D/16][8 tokens]; E2M1 codes
+two to a byte (element 2j in the low nibble), one E4M3 scale per 16 channels,
+one fp32 global scale per KV head.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+_LEVELS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ------------------------------------------------------------------- cases
+
+def listed():
+    a = dict(op="append", page=64, D=128, rot=128, interleaved=False, norm=True, dtype="bf16")
+    t = dict(op="attend", page=64, D=128, ragged=False, window=0)
+    return [
+        # one decode step of one sequence: latency is everything
+        dict(a, name="append_1_token", T=1, Hq=64, Hkv=8),
+        # a decode batch padded for a captured graph (some slots are -1), fp32
+        # activations, interleaved pairs on half of the head, no norm, short pages
+        dict(a, name="append_decode_batch", T=61, Hq=24, Hkv=3, page=16, rot=64, interleaved=True, norm=False,
+             dtype="f32"),
+        # prompt chunks: narrow heads at an odd length, and a long one
+        dict(a, name="append_chunk_narrow", T=1031, Hq=20, Hkv=4, D=64, page=32, rot=64),
+        dict(a, name="append_prompt", T=8192, Hq=64, Hkv=8),
+        # one short conversation, one token: the smallest call
+        dict(t, name="attend_1_short", B=1, nq=1, kv=77, Hq=32, Hkv=8),
+        # one very long conversation: the cache has to be split over the whole GPU
+        dict(t, name="attend_1_long", B=1, nq=1, kv=131072, Hq=64, Hkv=8),
+        # a small batch, narrow heads in odd groups of three, short pages
+        dict(t, name="attend_batch_narrow", B=13, nq=1, kv=999, Hq=24, Hkv=8, D=64, page=16),
+        # the serving batch: ragged lengths, some sequences still empty
+        dict(t, name="attend_serving", B=128, nq=1, kv=8192, Hq=64, Hkv=8),
+        # a draft of four tokens checked at once
+        dict(t, name="attend_draft", B=32, nq=4, kv=4096, Hq=64, Hkv=8),
+        # sliding window, sixteen query heads on a KV head
+        dict(t, name="attend_window", B=48, nq=1, kv=16384, Hq=64, Hkv=4, page=128, window=1024),
+        # a prompt chunk on top of a cached prefix
+        dict(t, name="attend_chunk", B=1, nq=2048, kv=8192, Hq=64, Hkv=8),
+        # prompts of several users in one call, decoding ones among them
+        dict(t, name="attend_ragged_prompts", B=9, nq=1500, kv=2500, Hq=32, Hkv=8, ragged=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    Hkv = rng.randint(1, 8)
+    D = rng.choice((64, 128))
+    page = rng.choice((16, 32, 64, 128))
+    if rng.random() < 0.4:
+        return dict(op="append", T=_log(rng, 1, 8192), Hq=Hkv * rng.randint(1, 8), Hkv=Hkv, D=D, page=page,
+                    rot=rng.choice((D, D // 2)), interleaved=rng.random() < 0.5, norm=rng.random() < 0.6,
+                    dtype=rng.choice(("bf16", "bf16", "f32")))
+    kind = rng.choice(("one", "one", "few", "chunk"))
+    if kind == "one":
+        B, nq, kv = _log(rng, 1, 128), 1, _log(rng, 1, 32768)
+        G = rng.choice((1, 2, 3, 4, 5, 7, 8, 12, 16))
+    elif kind == "few":
+        B, nq, kv = _log(rng, 1, 32), rng.randint(2, 8), _log(rng, 16, 8192)
+        G = rng.choice((1, 2, 4, 5, 8))
+    else:
+        B, nq, kv = rng.randint(1, 6), _log(rng, 9, 1500), _log(rng, 9, 6000)
+        G = rng.choice((1, 2, 4, 6, 8))
+    if B * kv * Hkv > 128 * 4096 * 8:                  # no dearer than the largest listed case
+        kv = max(1, 128 * 4096 * 8 // (B * Hkv))
+    window = rng.choice((0, 0, 0, _log(rng, 16, 2048)))
+    return dict(op="attend", B=B, nq=nq, kv=max(kv, nq), Hq=Hkv * G, Hkv=Hkv, D=D, page=page,
+                ragged=kind == "chunk" and rng.random() < 0.7, window=window)
+
+
+def _lengths(case):
+    """(queries, cached tokens) of every sequence: part of the case."""
+    r = random.Random("%(B)d %(nq)d %(kv)d %(page)d" % case)
+    B, nq, kv = case["B"], case["nq"], case["kv"]
+    q, n = [], []
+    for b in range(B):
+        m = nq if not case["ragged"] or b == 0 else r.choice((1, r.randint(0, nq), r.randint(1, nq)))
+        L = kv if b == 0 else r.randint(m, kv)
+        if B >= 8 and b % 8 == 5 and nq == 1:
+            L = 0                                       # a padding sequence of the batch
+        q.append(m)
+        n.append(L)
+    return q, n
+
+
+def work(case):
+    D, Hq, Hkv = case["D"], case["Hq"], case["Hkv"]
+    entry = Hkv * 2 * D * 9 / 16                        # cache bytes of one token
+    if case["op"] == "append":
+        size = 2 if case["dtype"] == "bf16" else 4
+        T = case["T"]
+        per = (Hq + 2 * Hkv) * D * size + case["rot"] * 4 + 8 + Hq * D * 2 + 2 * entry + 2 * Hkv * D * 2
+        return {"bytes": T * per, "flops": T * D * (10 * Hq + 20 * Hkv)}
+    bytes_, flops = 0.0, 0.0
+    for m, L in zip(*_lengths(case)):
+        w = case["window"]
+        keys = min(L, w + m - 1) if w else L
+        bytes_ += keys * entry + 4 * math.ceil(keys / case["page"]) + m * Hq * (D * 4 + 4) + 8
+        pairs = 0
+        if m:
+            first = L - m + 1                           # keys seen by the first query, without the window
+            if w:
+                grow = max(0, min(m, w - first))        # queries that see fewer than w keys
+                pairs = grow * first + grow * (grow - 1) // 2 + (m - grow) * w
+            else:
+                pairs = m * first + m * (m - 1) // 2
+            pairs = max(pairs, 0)
+        flops += 4.0 * pairs * Hq * D
+    return {"bytes": bytes_, "flops": flops}
+
+
+# ------------------------------------------------------------------ inputs
+
+def _quantize(x, gsa):
+    """NVFP4 of fp32 x [..., D] under the global scale gsa (broadcast over the
+    rows): signed values of the codes and the E4M3 scales, both in fp32."""
+    y = (x / gsa).unflatten(-1, (-1, 16))
+    s = (y.abs().amax(-1, keepdim=True) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    r = y / torch.where(s > 0, s, torch.ones_like(s))
+    a = r.abs()
+    # to nearest, ties to the code with an even mantissa, saturating at 6
+    m = 0.5 * ((a > 0.25).float() + (a >= 0.75).float() + (a > 1.25).float() + (a >= 1.75).float())
+    m = m + (a > 2.5).float() + (a >= 3.5).float() + 2.0 * (a > 5.0).float()
+    m = torch.where(s > 0, m, torch.zeros_like(m))
+    return torch.copysign(m, r).flatten(-2), s.squeeze(-1)
+
+
+def _bits(values, scales):
+    """Codes two to a byte [..., D/2] and scale bytes [..., D/16]."""
+    a = values.abs()
+    c = (2 * a).to(torch.uint8) - (a > 2).to(torch.uint8) - 3 * (a > 4).to(torch.uint8) - (a == 4).to(torch.uint8)
+    c = c + 8 * torch.signbit(values).to(torch.uint8)
+    c = c.unflatten(-1, (-1, 2))
+    return c[..., 0] + 16 * c[..., 1], scales.to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _page_bytes(kc, ks, vc, vs):
+    """Codes [P, H, S, D/2] and scales [P, H, S, D/16] in the cache's layout."""
+    vc = vc.unflatten(3, (-1, 8)).unflatten(2, (-1, 8)).transpose(3, 4)
+    vs = vs.unflatten(2, (-1, 8)).transpose(3, 4)
+    return torch.cat([t.flatten(2) for t in (kc, ks, vc, vs)], dim=2)
+
+
+def _heavy(shape, g, dev, spread):
+    """Normal values whose last axis has a few louder channels."""
+    x = torch.randn(shape, generator=g, device=dev)
+    loud = torch.rand(shape[-1], generator=g, device=dev) < 0.04
+    return x * torch.where(loud, 3.0 * spread, spread)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed * 7919 + 17)
+    dev = torch.device("cuda")
+    D, Hq, Hkv, S = case["D"], case["Hq"], case["Hkv"], case["page"]
+    k_gsa = 0.002 + 0.002 * torch.rand(Hkv, generator=g, device=dev)
+    v_gsa = 0.001 + 0.001 * torch.rand(Hkv, generator=g, device=dev)
+    st = dict(case=case, D=D, Hq=Hq, Hkv=Hkv, S=S, k_gsa=k_gsa, v_gsa=v_gsa)
+    if case["op"] == "append":
+        T, rot = case["T"], case["rot"]
+        dt = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+        # one fused projection: q, k and v are views of its rows
+        qkv = _heavy((T, Hq + 2 * Hkv, D), g, dev, 1.0).to(dt)
+        st["q"], st["k"], st["v"] = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        n_pos = 16384
+        freq = 10000.0 ** (-torch.arange(0, rot, 2, device=dev, dtype=torch.float64) / rot)
+        angle = torch.arange(n_pos, device=dev, dtype=torch.float64)[:, None] * freq
+        st["cos"], st["sin"] = angle.cos().float().contiguous(), angle.sin().float().contiguous()
+        first = int(torch.randint(0, n_pos - T + 1, (1,), generator=g, device=dev))
+        if T <= 64:                                     # a decode batch: every token of another sequence
+            st["positions"] = torch.randint(0, n_pos, (T,), generator=g, device=dev, dtype=torch.int32)
+        else:
+            st["positions"] = torch.arange(first, first + T, device=dev, dtype=torch.int32)
+        n_pages = 2 * ((T + S - 1) // S) + 64
+        if T <= 64:
+            slots = torch.randperm(n_pages * S, generator=g, device=dev)[:T]
+            slots = torch.where(torch.rand(T, generator=g, device=dev) < (0.0 if T < 8 else 0.15), -1, slots)
+        else:                                           # consecutive tokens fill pages found anywhere
+            pages = torch.randperm(n_pages, generator=g, device=dev)
+            at = first % S + torch.arange(T, device=dev)
+            slots = pages[at // S] * S + at % S
+        st["slots"] = slots.to(torch.int32)
+        st["q_weight"] = st["k_weight"] = None
+        if case["norm"]:
+            st["q_weight"] = 1.0 + 0.2 * torch.randn(D, generator=g, device=dev)
+            st["k_weight"] = 1.0 + 0.2 * torch.randn(D, generator=g, device=dev)
+        st["eps"], st["interleaved"] = 1e-6, case["interleaved"]
+        if own:
+            import nvfp4_router_gate_gb300 as R
+            st["kv"] = R.Nvfp4KVCache(n_pages, Hkv, D, page_size=S, k_gsa=k_gsa, v_gsa=v_gsa)
+        return st
+    nq, kv = _lengths(case)
+    B = case["B"]
+    used = [(n + S - 1) // S for n in kv]
+    n_pages = sum(used) + 3
+    width = max(max(used), 1)
+    order = torch.randperm(n_pages, generator=g, device=dev).to(torch.int32)
+    kv_t = torch.tensor(kv, dtype=torch.int32, device=dev)
+    used_t = torch.tensor(used, device=dev)
+    col = torch.arange(width, device=dev)
+    at = (used_t.cumsum(0) - used_t)[:, None] + col
+    table = torch.where(col < used_t[:, None], order[at.clamp(max=n_pages - 1)], -1).to(torch.int32)
+    # what a page holds beyond its sequence's length is left from earlier use: any bytes
+    live = torch.zeros(n_pages, S, dtype=torch.bool, device=dev)
+    token = col[:, None] * S + torch.arange(S, device=dev)
+    owned = token < kv_t[:, None, None]
+    live[table.clamp(min=0)[table >= 0].long()] = owned[table >= 0]
+    parts = []
+    for gsa, spread in ((k_gsa, 1.0), (v_gsa, 0.5)):
+        v, s = _quantize(_heavy((n_pages, Hkv, S, D), g, dev, spread), gsa[:, None, None])
+        c, s = _bits(v, s)
+        junk = torch.randint(0, 256, (2, n_pages, Hkv, S, 1), generator=g, device=dev, dtype=torch.uint8)
+        keep = live[:, None, :, None]
+        parts += [torch.where(keep, c, junk[0]), torch.where(keep, s, junk[1] | 0x70)]
+        del v, s, c
+    st["cache"] = _page_bytes(*parts).contiguous()
+    del parts
+    T = sum(nq)
+    st["q"] = _heavy((T, Hq, D), g, dev, 1.5).to(torch.bfloat16)
+    st["page_table"], st["kv_lens"] = table.contiguous(), kv_t
+    cu = [0]
+    for m in nq:
+        cu.append(cu[-1] + m)
+    st["uniform"] = not case["ragged"]
+    st["cu_q"], st["max_q"] = torch.tensor(cu, dtype=torch.int32, device=dev), max(nq)
+    st["scale"], st["window"] = D ** -0.5, case["window"]
+    st["out"] = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    st["lse"] = torch.empty(T, Hq, dtype=torch.float32, device=dev)
+    if own:
+        import nvfp4_router_gate_gb300 as R
+        st["kv"] = R.Nvfp4KVCache(n_pages, Hkv, D, page_size=S, k_gsa=k_gsa, v_gsa=v_gsa, data=st["cache"],
+                                  n_heads=Hq, max_tokens=T, max_seqs=B)
+    return st
+
+
+# ------------------------------------------------------------------- calls
+
+def run(st):
+    if own:
+        kv = st["kv"]
+        if st["case"]["op"] == "append":
+            q = kv.append(st["q"], st["k"], st["v"], st["positions"], st["slots"], st["cos"], st["sin"],
+                          q_weight=st["q_weight"], k_weight=st["k_weight"], eps=st["eps"],
+                          interleaved=st["interleaved"])
+            k, v = kv.gather(st["slots"])
+            return {"q": q, "k": k, "v": v}
+        out, lse = kv.attend(st["q"], st["page_table"], st["kv_lens"], cu_q=None if st["uniform"] else st["cu_q"],
+                             max_q=st["max_q"], scale=st["scale"], window=st["window"], out=st["out"],
+                             lse=st["lse"])
+        return {"out": out, "lse": lse}
+    return _append(st) if st["case"]["op"] == "append" else _attend(st)
+
+
+def _halves(s):
+    """Sum over the last axis (a power of two): halves added to each other."""
+    if s.shape[-1] == 1:
+        return s
+    h = s.shape[-1] // 2
+    return _halves(s[..., :h] + s[..., h:])
+
+
+def _turn(x, weight, st):
+    """RMS norm of every head and rotation of its first channels, in fp32."""
+    x = x.float()
+    if weight is not None:
+        x = x * (1.0 / torch.sqrt(_halves(x * x) / st["D"] + st["eps"])) * weight
+    rot = st["case"]["rot"]
+    c, s = st["cos"][st["positions"].long()][:, None], st["sin"][st["positions"].long()][:, None]
+    t = x[..., :rot]
+    a, b = (t[..., 0::2], t[..., 1::2]) if st["interleaved"] else (t[..., :rot // 2], t[..., rot // 2:])
+    p, r = a * c - b * s, b * c + a * s
+    t = torch.stack((p, r), -1).flatten(-2) if st["interleaved"] else torch.cat((p, r), -1)
+    return torch.cat((t, x[..., rot:]), -1)
+
+
+def _append(st):
+    live = (st["slots"] >= 0)[:, None, None]
+    out = {"q": _turn(st["q"], st["q_weight"], st).to(torch.bfloat16)}
+    for name, x, gsa in (("k", _turn(st["k"], st["k_weight"], st), st["k_gsa"]), ("v", st["v"].float(), st["v_gsa"])):
+        c, s = _quantize(x, gsa[:, None])
+        val = c * s.repeat_interleave(16, -1) * gsa[:, None]
+        out[name] = torch.where(live, val, torch.zeros_like(val)).to(torch.bfloat16)
+    return out
+
+
+def _values(codes, scales, gsa):
+    """fp32 values of codes [..., D/2] and scale bytes [..., D/16]."""
+    lut = torch.tensor(_LEVELS + tuple(-v for v in _LEVELS), device=codes.device)
+    lo, hi = lut[(codes & 15).int()], lut[(codes >> 4).int()]
+    val = torch.stack((lo, hi), -1).flatten(-2)
+    return val * scales.view(torch.float8_e4m3fn).float().repeat_interleave(16, -1) * gsa
+
+
+def _attend(st):
+    D, S, Hkv, Hq = st["D"], st["S"], st["Hkv"], st["Hq"]
+    B, P = st["page_table"].shape
+    L, G, m = P * S, Hq // Hkv, st["max_q"]
+    pages = st["cache"][st["page_table"].clamp(min=0).long()].transpose(1, 2)          # [B, Hkv, P, bytes]
+    kc, ks, vc, vs = pages.split((S * D // 2, S * D // 16, S * D // 2, S * D // 16), -1)
+    key = torch.arange(L, device=pages.device)
+    live = key < st["kv_lens"][:, None]                                                 # [B, L]
+    k = _values(kc.reshape(B, Hkv, L, D // 2), ks.reshape(B, Hkv, L, D // 16), st["k_gsa"][:, None, None])
+    vc = vc.reshape(B, Hkv, L // 8, D // 16, 8, 8).transpose(3, 4).reshape(B, Hkv, L, D // 2)
+    vs = vs.reshape(B, Hkv, L // 8, D // 16, 8).transpose(3, 4).reshape(B, Hkv, L, D // 16)
+    v = _values(vc, vs, st["v_gsa"][:, None, None])
+    v = torch.where(live[:, None, :, None], v, torch.zeros_like(v))
+    cu, T = st["cu_q"].long(), st["q"].shape[0]
+    n_q = cu[1:] - cu[:-1]
+    i = torch.arange(m, device=pages.device)
+    token = (cu[:-1, None] + i).clamp(max=T - 1)                                        # [B, m]
+    q = st["q"].float()[token].unflatten(2, (Hkv, G)).transpose(1, 2).reshape(B, Hkv, m * G, D)
+    s = torch.matmul(q, k.transpose(-1, -2)) * st["scale"]                              # [B, Hkv, m G, L]
+    last = (st["kv_lens"].long() - n_q)[:, None] + i                                    # [B, m] own position
+    see = key <= last[..., None]
+    if st["window"]:
+        see = see & (key > last[..., None] - st["window"])
+    see = see.repeat_interleave(G, 1)[:, None]
+    s = torch.where(see, s, torch.full_like(s, -math.inf))
+    top = s.amax(-1, keepdim=True)
+    p = torch.exp(s - torch.where(top > -math.inf, top, torch.zeros_like(top)))
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p, v) / torch.where(total > 0, total, torch.ones_like(total))
+    lse = (torch.log(total) + top).squeeze(-1)
+    back = torch.searchsorted(cu, torch.arange(T, device=cu.device), right=True) - 1   # sequence of each token
+    idx = torch.arange(T, device=cu.device) - cu[back]
+    o = o.unflatten(2, (m, G)).permute(0, 2, 1, 3, 4).reshape(B, m, Hq, D)
+    lse = lse.unflatten(2, (m, G)).permute(0, 2, 1, 3).reshape(B, m, Hq)
+    return {"out": o[back, idx].to(torch.bfloat16), "lse": lse[back, idx]}
+
+
+# ------------------------------------------------------- definition, 64 bits
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        st = prepare(case, seed)
+    finally:
+        own = was
+    if case["op"] == "append":
+        return _append_64(case, st)
+    return _attend_64(case, st)
+
+
+def _e4m3_64(s):
+    """The nearest E4M3 values of s >= 0, ties to even, at most 448."""
+    e = torch.floor(torch.log2(s.clamp(min=2.0 ** -30))).clamp(min=-6.0)
+    step = torch.exp2(e - 3)
+    return (torch.round(s / step) * step).clamp(max=448.0)
+
+
+def _e2m1_64(a):
+    """The nearest E2M1 magnitudes of a >= 0, ties to even, at most 6."""
+    step = torch.where(a < 2.0, 0.5, torch.where(a < 4.0, 1.0, 2.0))
+    return (torch.round(a / step) * step).clamp(max=6.0)
+
+
+def _append_64(case, st):
+    rot, pos = case["rot"], st["positions"].long()
+    cos, sin = st["cos"].double()[pos], st["sin"].double()[pos]
+
+    def head(x, w):
+        x = x.double()
+        if w is not None:
+            x = x / torch.sqrt((x ** 2).mean(-1, keepdim=True) + case_eps) * w.double()
+        y = x.clone()
+        for j in range(rot // 2):
+            a, b = (2 * j, 2 * j + 1) if case["interleaved"] else (j, j + rot // 2)
+            c, s = cos[:, j, None], sin[:, j, None]
+            y[..., a] = x[..., a] * c - x[..., b] * s
+            y[..., b] = x[..., b] * c + x[..., a] * s
+        return y
+
+    case_eps = st["eps"]
+    res = {"q": head(st["q"], st["q_weight"])}
+    for name, x, gsa in (("k", head(st["k"], st["k_weight"]), st["k_gsa"]), ("v", st["v"].double(), st["v_gsa"])):
+        y = x / gsa.double()[:, None]
+        blk = y.reshape(*y.shape[:-1], -1, 16)
+        s = _e4m3_64(blk.abs().max(-1, keepdim=True).values / 6)
+        code = torch.where(s > 0, _e2m1_64(blk.abs() / torch.where(s > 0, s, torch.ones_like(s))), 0.0 * blk)
+        val = (torch.sign(blk) * code * s).reshape(y.shape) * gsa.double()[:, None]
+        val[st["slots"] < 0] = 0.0
+        res[name] = val
+    return res
+
+
+def _code_64(n):
+    """The value of 4-bit codes from their fields: sign, two exponent bits, one mantissa bit."""
+    e, f = (n >> 1) & 3, (n & 1).double()
+    mag = torch.where(e == 0, 0.5 * f, (1 + 0.5 * f) * torch.exp2(e.double() - 1))
+    return torch.where(n >= 8, -mag, mag)
+
+
+def _scale_64(b):
+    e, f = ((b >> 3) & 15).double(), (b & 7).double()
+    return torch.where(e == 0, f * 2.0 ** -9, (1 + f / 8) * torch.exp2(e - 7))
+
+
+def _attend_64(case, st):
+    D, S, Hkv, Hq, w = case["D"], case["page"], case["Hkv"], case["Hq"], case["window"]
+    G = Hq // Hkv
+    nq, kv = _lengths(case)
+    dev = st["cache"].device
+    res = torch.zeros(sum(nq), Hq, D, dtype=torch.float64, device=dev)
+    lse = torch.full((sum(nq), Hq), -math.inf, dtype=torch.float64, device=dev)
+    base = 0
+    for b, (m, n) in enumerate(zip(nq, kv)):
+        if m and n:
+            pages = st["cache"][st["page_table"][b, :(n + S - 1) // S].long()].long()
+            half = S * D // 2
+            kc = pages[..., :half].reshape(-1, Hkv, S, D // 2)
+            ks = pages[..., half:half + half // 8].reshape(-1, Hkv, S, D // 16)
+            vc = pages[..., half + half // 8:2 * half + half // 8].reshape(-1, Hkv, S // 8, D // 16, 8, 8)
+            vs = pages[..., 2 * half + half // 8:].reshape(-1, Hkv, S // 8, D // 16, 8)
+            for h in range(Hkv):
+                def rows(c, s, gsa):
+                    x = torch.stack((_code_64(c % 16), _code_64(c // 16)), -1).reshape(-1, D // 16, 16)
+                    return (x * _scale_64(s).reshape(-1, D // 16, 1)).reshape(-1, D)[:n] * gsa.double()
+                k = rows(kc[:, h], ks[:, h], st["k_gsa"][h])
+                v = rows(vc[:, h].permute(0, 1, 3, 2, 4), vs[:, h].permute(0, 1, 3, 2), st["v_gsa"][h])
+                for i in range(0, m, 512):
+                    j = min(m, i + 512)
+                    q = st["q"][base + i:base + j, h * G:(h + 1) * G].double()
+                    x = torch.einsum("igd,nd->ign", q, k) * st["scale"]
+                    own_pos = (n - m + torch.arange(i, j, device=dev))[:, None, None]
+                    key = torch.arange(n, device=dev)
+                    hide = (key > own_pos) | ((key <= own_pos - w) if w else (key < 0))
+                    x = x.masked_fill(hide, -math.inf)
+                    z = torch.logsumexp(x, -1)
+                    p = torch.exp(x - torch.where(z > -math.inf, z, torch.zeros_like(z))[..., None])
+                    res[base + i:base + j, h * G:(h + 1) * G] = torch.einsum("ign,nd->igd", p, v)
+                    lse[base + i:base + j, h * G:(h + 1) * G] = z
+        base += m
+    return {"out": res, "lse": lse}
