@@ -138,7 +138,8 @@ def _quantize(x, gsa):
     """NVFP4 of fp32 x [..., D] under the global scale gsa (broadcast over the
     rows): signed values of the codes and the E4M3 scales, both in fp32."""
     y = (x / gsa).unflatten(-1, (-1, 16))
-    s = (y.abs().amax(-1, keepdim=True) / 6.0).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    # a tensor divides; a Python scalar would multiply by its rounded reciprocal
+    s = (y.abs().amax(-1, keepdim=True) / y.new_full((), 6.0)).clamp(max=448.0).to(torch.float8_e4m3fn).float()
     r = y / torch.where(s > 0, s, torch.ones_like(s))
     a = r.abs()
     # to nearest, ties to the code with an even mantissa, saturating at 6
