@@ -16,6 +16,8 @@ Functions (same names as include/nvfp4_router.h):
   (``Nvfp4Linear`` keeps the packed weight and a workspace resident)
 * ``nvfp4_pack_experts(W [E, N, D])``, ``nvfp4_moe_gemm(x, ids, W_fp4, W_sf, w_gsa)`` -> y [T, k, N],
   ``nvfp4_moe_combine(y, w)`` -> out [T, N]
+* ``nvfp4_kv_append``, ``nvfp4_kv_attention``, ``nvfp4_kv_gather`` (include/nvfp4_kv_cache.h): the paged
+  NVFP4 key/value cache; ``Nvfp4KVCache`` keeps its pages, scales and workspace resident
 * ``router_gate_workspace_size``, ``router_gate_x_gsa``, ``nvfp4_quantize_workspace_size``,
   ``nvr_sf_bytes``, ``nvr_read_device_status``
 
@@ -38,7 +40,9 @@ __all__ = ["nvfp4_quantize_act", "nvfp4_pack_weight", "router_gate_topk", "route
            "NVR_FLAG_FORCE_TENSOR_CORE", "NVR_FLAG_FORCE_DECODE", "NVR_FLAG_SPLIT_K_2",
            "NVR_FLAG_SPLIT_K_4", "NVR_FLAG_SPLIT_K_8", "NVR_FLAG_SPLIT_N", "NVR_FLAG_STREAM", "NVR_FLAG_NO_COOPERATIVE", "new_workspace",
            "nvfp4_linear", "nvfp4_linear_workspace_size", "Nvfp4Linear", "nvfp4_pack_experts",
-           "nvfp4_moe_gemm", "nvfp4_moe_gemm_workspace_size", "nvfp4_moe_combine"]
+           "nvfp4_moe_gemm", "nvfp4_moe_gemm_workspace_size", "nvfp4_moe_combine", "nvfp4_kv_append",
+           "nvfp4_kv_gather", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size", "nvfp4_kv_page_bytes",
+           "Nvfp4KVCache", "rope_table"]
 
 _LAYOUTS = {"linear": _native.NVR_SF_LINEAR, "tiled": _native.NVR_SF_TILED}
 
@@ -360,3 +364,7 @@ class RouterGate:
                          self.raw, out_ids=ids, out_w=w, workspace=self.workspace, flags=flags,
                          stream=stream)
         return ids, w
+
+
+from .kv_cache import (Nvfp4KVCache, nvfp4_kv_append, nvfp4_kv_attention,  # noqa: E402
+                       nvfp4_kv_attention_workspace_size, nvfp4_kv_gather, nvfp4_kv_page_bytes, rope_table)

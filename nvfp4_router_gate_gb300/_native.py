@@ -1,4 +1,5 @@
-"""ctypes declarations of the C ABI in include/nvfp4_router.h.
+"""ctypes declarations of the C ABI in include/nvfp4_router.h and
+include/nvfp4_kv_cache.h.
 
 Loading the library needs no GPU; it fails loudly (RuntimeError) when the
 shared library has not been built.  There is no fallback of any kind.
@@ -41,7 +42,7 @@ _i32 = ctypes.c_int
 _u32 = ctypes.c_uint32
 _f32 = ctypes.c_float
 
-# name -> (restype, argtypes); the same list the header declares
+# name -> (restype, argtypes); the same list the headers declare
 SIGNATURES = {
     "nvr_status_string": (ctypes.c_char_p, [_i32]),
     "nvr_last_cuda_error": (ctypes.c_char_p, []),
@@ -67,6 +68,13 @@ SIGNATURES = {
     "nvfp4_moe_gemm_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
     "nvfp4_moe_gemm": (_i32, [_p, _i32, _i64, _i64, _p, _i32, _i64, _p, _p, _p, _i64, _p, _i32, _p, _sz, _p]),
     "nvfp4_moe_combine": (_i32, [_p, _i32, _i64, _i32, _i64, _p, _p, _p]),
+    "nvfp4_kv_page_bytes": (_sz, [_i32, _i32]),
+    "nvfp4_kv_append": (_i32, [_p, _i64, _p, _i64, _p, _i64, _i32, _i64, _i32, _i32, _i32, _p, _p, _p, _p, _i64,
+                               _i32, _i32, _p, _p, _f32, _p, _p, _p, _i64, _i32, _p, _p]),
+    "nvfp4_kv_gather": (_i32, [_p, _i64, _i32, _i32, _i32, _p, _i64, _p, _p, _p, _p, _i32, _p]),
+    "nvfp4_kv_attention_workspace_size": (_sz, [_i64, _i64, _i32, _i32, _i32]),
+    "nvfp4_kv_attention": (_i32, [_p, _i64, _i64, _i32, _i32, _i32, _p, _i64, _i32, _p, _i64, _i64, _p, _p, _i32, _p,
+                                  _p, _f32, _i32, _i32, _p, _p, _p, _sz, _p]),
     "router_gate_logits": (_i32, [_p, _i32, _i64, _i64, _p, _p, _p, _i64, _u32, _p, _p, _sz, _p]),
     "nvr_read_device_status": (_i32, [_p, _p, ctypes.POINTER(_i32)]),
     "nvr_set_profile_events": (_i32, [_p, _i32]),

@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libnvfp4_router.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["quantize.cu", "decode.cu", "gemm_topk.cu", "gemm_splitk.cu", "gemm_fused.cu", "abi.cu", "noalloc.cu",
-           "hash_router.cu", "gemm_stream.cu", "moe.cu", "selftest.cu"]
+           "hash_router.cu", "gemm_stream.cu", "moe.cu", "selftest.cu", "kv_cache.cu",
+           "kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I", INCLUDE]

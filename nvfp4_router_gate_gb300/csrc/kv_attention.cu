@@ -1,0 +1,811 @@
+// kv_attention.cu -- softmax attention over the paged NVFP4 key/value cache,
+// streaming form (sm_103a): up to 32 (query, head) columns share one pass over
+// their KV head's tokens.  One or a few queries per sequence: bound by the
+// cache's bytes.
+//
+// Mathematics.  For a column's query q and its visible tokens t
+//   s_t = scale * q . k_t,  m = max s_t,  p_t = exp(s_t - m),
+//   out = sum p_t v_t / sum p_t,  lse = m + log sum p_t,
+// in one pass: a running m, l = sum p and O = sum p v, rescaled when m moves;
+// partial (m, l, O) triples of disjoint token sets join by the same rescaling.
+// m is only moved when a score passes it by more than 8 (base 2): p_t stays
+// below 2^8, inside fp16, and most tiles skip the rescaling.
+//
+// Both products run transposed, S^T = K Q^T and O^T = V^T P^T: the tokens
+// (resp. channels) are the 16 rows of the matrix instruction and the columns
+// its 8 columns, so that 8 heads sharing a KV head fill it.  The cache's codes
+// become the A operand in registers: a 4-bit pair converts to half2 in one
+// instruction and takes its block scale in one multiply (code * scale has 6
+// significant bits and lies in [2^-10, 2688]: exact in fp16).  The contraction
+// may run over the channels (tokens) in any order as long as both operands
+// agree, so each lane takes the 16 bytes it loads as they are.
+//
+// Work: the 16 * NW-token tiles of all (sequence, column group, KV head) keys,
+// laid end to end, are cut into equal chunks, one per resident block; a key
+// cut by a chunk border leaves partials in the workspace and the last block to
+// arrive (ticket) joins them in chunk order, so results do not depend on timing.
+// One producer warp feeds a ring of tiles with bulk copies, a page of one KV head each.
+#include "kv_layout.cuh"
+#include "nvr_internal.h"
+#include "nvr_tcgen05.cuh"
+#include "../../include/nvfp4_kv_cache.h"
+
+namespace nvr {
+
+namespace {
+
+constexpr int kAttnMaxCtas = 2048;         // ticket words in the workspace
+constexpr int kAttnMaxCols = 16384;        // column slots of partials: blocks * columns, per side
+constexpr float kRescaleAt = 8.0f;
+
+struct AttnParams {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int64_t T;
+  int Hq, Hkv, G;
+  const uint8_t* cache;
+  int64_t n_pages;
+  int page_shift;
+  const int32_t* page_table;
+  int B, max_pages;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int max_q;
+  const float *k_gsa, *v_gsa;
+  float scale_log2;           // scale * log2(e)
+  int causal, window;
+  int groups;                 // column groups per sequence
+  __nv_bfloat16* out;
+  float* lse;
+  uint32_t* status;
+  uint32_t* tickets;
+  float* partials;            // [2 * blocks][NC][D + 2]: m, l, O
+  int min_chunk;              // fewest tiles of a block
+};
+
+// What the queries and the tokens of a column group are.
+struct Group {
+  int b, q0, n_q, kv;         // sequence, its first query row, its queries, its tokens
+  int c0, n_cols;             // first column, columns of the group (0: none)
+  int lo, hi;                 // tokens any of the columns sees: [lo, hi)
+  int tile0, tiles;
+};
+
+template <int NC, int TILE>
+__device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
+  Group g;
+  g.b = item / p.groups;
+  const int cg = item - g.b * p.groups;
+  g.kv = min(max(__ldg(p.kv_lens + g.b), 0), p.max_pages << p.page_shift);
+  if (p.cu_q) {
+    const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
+    const int64_t e = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b + 1)), a), p.T);
+    g.q0 = static_cast<int>(a);
+    g.n_q = static_cast<int>(min(e - a, static_cast<int64_t>(p.max_q)));
+  } else {
+    g.q0 = g.b * p.max_q;
+    g.n_q = p.max_q;
+  }
+  g.c0 = cg * NC;
+  g.n_cols = min(g.n_q * p.G - g.c0, NC);
+  if (g.n_cols <= 0) {
+    g.n_cols = 0;
+    g.lo = g.hi = g.tile0 = g.tiles = 0;
+    return g;
+  }
+  g.lo = 0;
+  g.hi = g.kv;
+  if (p.causal) {
+    const int first = g.kv - g.n_q + g.c0 / p.G;                       // position of the first column's query
+    const int last = g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G;
+    g.hi = max(last + 1, 0);
+    if (p.window > 0) g.lo = min(max(first + 1 - p.window, 0), g.hi);
+  }
+  g.tile0 = g.lo / TILE;
+  g.tiles = max((g.hi + TILE - 1) / TILE - g.tile0, 1);                // a group that sees nothing still writes its rows
+  return g;
+}
+
+// What a stage of the ring holds.
+struct Meta {
+  int item, head, tile;
+  int key_f0, key_tiles;      // the key's place in the flat order of tiles
+  uint32_t flags;
+  uint32_t live;              // bit s: the 16 tokens of warp s were loaded
+};
+constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4;
+
+// Waits for a phase of the barrier, one second at most.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, globaltimer_ns() + 1000000000ull, abort_flag);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+               "{%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D, int NT, int NW, int STAGES>
+struct AttnShape {
+  static constexpr int kTile = 16 * NW;
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kThreads = 32 * (NW + 1);
+  static constexpr int kStageBytes = kTile * D * 9 / 8;
+  static constexpr int kFrag = D / 4;                        // O registers of a lane per 8 columns
+  static constexpr int kJoinBytes = NW * kFrag * 32 * 4;     // one column tile of every warp
+  static constexpr int kQBytes = NT > 1 ? NT * (D / 16) * 64 * 4 : 0;
+  static constexpr int kSmem = STAGES * kStageBytes + kJoinBytes + kQBytes + 2 * NW * kCols * 4 +
+                               STAGES * static_cast<int>(sizeof(Meta)) + (2 * STAGES) * 8 + 64 + 128;
+};
+
+template <int D, int NT, int NW, int STAGES, int MINB>
+__global__ void __launch_bounds__(32 * (NW + 1), MINB)
+kv_attention_kernel(const AttnParams p) {
+  using Sh = AttnShape<D, NT, NW, STAGES>;
+  constexpr int TILE = Sh::kTile, NC = Sh::kCols, FR = Sh::kFrag;
+  constexpr int KS = D / 16;                                 // steps of the first product
+  constexpr int MT = D / 16;                                 // channel tiles of the second
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  float* s_join = reinterpret_cast<float*>(smem + STAGES * Sh::kStageBytes);          // [NW][FR][32]
+  uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + NW * FR * 32);                 // [NT][KS][32][2] (NT > 1)
+  float* s_m = reinterpret_cast<float*>(s_q + Sh::kQBytes / 4);                       // [NW][NC]
+  float* s_l = s_m + NW * NC;
+  Meta* s_meta = reinterpret_cast<Meta*>(s_l + NW * NC);
+  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_meta + STAGES) + 7) & ~uintptr_t(7));
+  uint64_t* empty = full + STAGES;
+  uint64_t* meet = empty + STAGES;                           // the consumer warps' barrier: bounded, unlike bar.sync
+  int* s_start = reinterpret_cast<int*>(meet + 1);     // item, offset inside it, total tiles
+  volatile int* abort_flag = s_start + 4;
+  int* s_flag = s_start + 5;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, NW); }
+    mbar_init(meet, NW);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- this block's chunk of the flat order: items in order, heads inside
+  // an item, tiles inside a head; each thread sums a run of items
+  const int n_items = p.B * p.groups;
+  const int per = (n_items + Sh::kThreads - 1) / Sh::kThreads;
+  int mine = 0;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += group_of<NC, TILE>(p, i).tiles * p.Hkv;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += a;
+  }
+  int* s_scan = reinterpret_cast<int*>(s_m);                 // NW + 1 words
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w <= NW; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
+  const int f0 = min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total));
+  const int f1 = min(f0 + chunk, total);
+  const int excl = before + incl - mine;
+  if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
+    int at = excl, i = tid * per;
+    for (;; ++i) {
+      const int n = group_of<NC, TILE>(p, i).tiles * p.Hkv;
+      if (f0 < at + n) break;
+      at += n;
+    }
+    s_start[0] = i;
+    s_start[1] = f0 - at;
+  }
+  __syncthreads();
+  if (f0 >= f1) return;
+
+  if (warp == NW) {
+    // -------------------------------------------------------------- producer
+    int item = s_start[0], off = s_start[1], f = f0, fill = 0;
+    const int S = 1 << p.page_shift;
+    const int part = min(S, TILE);                           // tokens of one copied piece
+    bool ok = true;
+    while (f < f1 && ok) {
+      const Group g = group_of<NC, TILE>(p, item);
+      const int n_key = g.tiles * p.Hkv;
+      const int32_t* table = p.page_table + static_cast<int64_t>(g.b) * p.max_pages;
+      while (off < n_key && f < f1) {
+        const int head = off / g.tiles, ti = off - head * g.tiles;
+        const int t0 = (g.tile0 + ti) * TILE;
+        const int st = fill % STAGES;
+        if (!wait_bounded(empty + st, ((fill / STAGES) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        // lane i looks after piece i of the tile (at most TILE / 16 pieces)
+        const int pt = t0 + lane * part;
+        int page = -1;
+        if (lane < TILE / part && pt < g.hi && pt + part > g.lo) page = __ldg(table + (pt >> p.page_shift));
+        const bool have = page >= 0 && page < p.n_pages;
+        const uint32_t got = __ballot_sync(0xFFFFFFFFu, have);
+        if (lane == 0) {
+          Meta m;
+          m.item = item; m.head = head; m.tile = g.tile0 + ti;
+          m.key_f0 = f - ti; m.key_tiles = g.tiles;
+          const uint32_t each = (1u << (part / 16)) - 1;
+          m.live = 0;
+          for (int i = 0; i < TILE / part; ++i)
+            if ((got >> i) & 1u) m.live |= each << (i * (part / 16));
+          m.flags = (ti == 0 || f == f0 ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u);
+          // every column sees every token of an inner tile
+          const int sure_hi = p.causal ? g.kv - g.n_q + g.c0 / p.G + 1 : g.kv;
+          const int sure_lo = p.window > 0 ? g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G + 1 - p.window : 0;
+          if (t0 + TILE > sure_hi || t0 < sure_lo || got != (1u << (TILE / part)) - 1u) m.flags |= kEdge;
+          s_meta[st] = m;
+          mbar_arrive_expect_tx(full + st, __popc(got) * part * (D * 9 / 8));
+        }
+        __syncwarp();
+        if (have) {
+          uint8_t* dst = smem + st * Sh::kStageBytes + lane * part * (D * 9 / 8);
+          const uint8_t* src = p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * KvPage<D>::bytes(S);
+          if (S <= TILE) {
+            bulk_load(dst, src, KvPage<D>::bytes(S), full + st);
+          } else {
+            const int o = pt & (S - 1);
+            bulk_load(dst, src + o * KvPage<D>::kCodeRow, part * KvPage<D>::kCodeRow, full + st);
+            bulk_load(dst + KvPage<D>::key_scales(part), src + KvPage<D>::key_scales(S) + o * KvPage<D>::kScaleRow,
+                      part * KvPage<D>::kScaleRow, full + st);
+            bulk_load(dst + KvPage<D>::value_codes(part), src + KvPage<D>::value_codes(S) + o * KvPage<D>::kCodeRow,
+                      part * KvPage<D>::kCodeRow, full + st);
+            bulk_load(dst + KvPage<D>::value_scales(part), src + KvPage<D>::value_scales(S) + o * KvPage<D>::kScaleRow,
+                      part * KvPage<D>::kScaleRow, full + st);
+          }
+        }
+        ++fill; ++off; ++f;
+      }
+      off = 0;
+      ++item;
+    }
+    if (!ok && lane == 0) {
+      report_timeout(p.status);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    if (*abort_flag) {
+      // copies in flight land before the block's memory goes away
+      const uint64_t drain = globaltimer_ns() + 1000000000ull;
+      for (int i = max(fill - STAGES, 0); i < fill; ++i)
+        while (!mbar_try_wait(full + i % STAGES, (i / STAGES) & 1))
+          if (globaltimer_ns() > drain) break;
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  const int r = lane >> 2, c = lane & 3;
+  const int S = 1 << p.page_shift, part = min(S, TILE);
+  // this warp's 16 tokens inside a stage
+  const int piece = warp * 16 / part, in_piece = warp * 16 % part;
+  const int piece_at = piece * part * (D * 9 / 8);
+  const int k_codes_at = piece_at + in_piece * (D / 2);
+  const int k_scales_at = piece_at + KvPage<D>::key_scales(part) + in_piece * (D / 16);
+  const int v_codes_at = piece_at + KvPage<D>::value_codes(part) + in_piece * (D / 2);
+  const int v_scales_at = piece_at + KvPage<D>::value_scales(part) + in_piece * (D / 16);
+
+  uint32_t qf[NT > 1 ? 1 : NT][KS][2];                       // B fragments of Q^T (shared memory for NT > 1)
+  float o[NT][MT][4];
+  float m_run[NT][2], l_run[NT][2], to_log2[NT][2];
+  int see_lo[NT][2], see_hi[NT][2];
+  Group g;
+  g.n_cols = 0;
+  uint32_t met = 0;
+  auto sync_consumers = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    const bool ok = __all_sync(0xFFFFFFFFu, wait_bounded(meet, met, abort_flag));
+    met ^= 1u;
+    return ok;
+  };
+  auto give_up = [&]() {
+    if (lane == 0) {
+      report_timeout(p.status);
+      *abort_flag = 1;
+    }
+  };
+  for (int f = f0, fill = 0; f < f1; ++f, ++fill) {
+    const int st = fill % STAGES;
+    if (!__all_sync(0xFFFFFFFFu, wait_bounded(full + st, (fill / STAGES) & 1, abort_flag))) return give_up();
+    const Meta meta = s_meta[st];
+    if (meta.flags & kFirst) {
+      g = group_of<NC, TILE>(p, meta.item);
+      const float k_gsa = __ldg(p.k_gsa + meta.head);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        // column 8 nt + r: its query row, scaled by a power of two into the
+        // upper range of fp16 (bf16 has fewer significant bits: exact, but for
+        // channels 2^28 below the row's largest, which lose their last bits)
+        const int col = g.c0 + 8 * nt + r;
+        const bool on = 8 * nt + r < g.n_cols;
+        const int iq = on ? col / p.G : 0, hq = meta.head * p.G + (on ? col - iq * p.G : 0);
+        const __nv_bfloat16* src = p.q + (g.q0 + iq) * p.q_stride + static_cast<int64_t>(hq) * D + c * (D / 4);
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 u = on ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+          w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+        }
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+        // up = 2^(14 - exponent of the largest): both it and its inverse are
+        // normal fp32 numbers for the biased exponents 16..254
+        const int e = min(max(static_cast<int>(big >> 7), 16), 254);
+        const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        const float down = p.scale_log2 * k_gsa * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t u = w[2 * ks + i];
+            b[i] = pack_f16(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xFFFF0000u) * up);
+          }
+          if (NT > 1) {
+            if (warp == nt % NW) {
+              s_q[((nt * KS + ks) * 32 + lane) * 2] = b[0];
+              s_q[((nt * KS + ks) * 32 + lane) * 2 + 1] = b[1];
+            }
+          } else {
+            qf[NT > 1 ? 0 : nt][ks][0] = b[0];
+            qf[NT > 1 ? 0 : nt][ks][1] = b[1];
+          }
+        }
+        // columns 8 nt + 2 c, + 1: what the accumulators of this lane need
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          to_log2[nt][i] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i) * 4);
+          const int n = 8 * nt + 2 * c + i;
+          const bool live = n < g.n_cols;
+          const int pos = g.kv - g.n_q + (g.c0 + (live ? n : 0)) / p.G;
+          see_hi[nt][i] = !live ? 0 : p.causal ? max(pos + 1, 0) : g.kv;
+          see_lo[nt][i] = live && p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
+          m_run[nt][i] = -INFINITY;
+          l_run[nt][i] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.0f;
+      }
+      if (NT > 1 && !sync_consumers()) return give_up();
+    }
+
+    const uint8_t* stage = smem + st * Sh::kStageBytes;
+    const bool loaded = (meta.live >> warp) & 1u;
+    if (loaded) {
+      // ------------------------------------------------ S^T = K Q^T, 16 tokens
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+      uint32_t kc[2][D / 32];                                // codes of tokens r, r + 8
+      uint32_t sc[2];                                        // their scales as half2
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + k_codes_at + (r + 8 * i) * 64 + c * 16);
+          kc[i][0] = u.x; kc[i][1] = u.y; kc[i][D / 32 - 2] = u.z; kc[i][D / 32 - 1] = u.w;
+          sc[i] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(stage + k_scales_at + (r + 8 * i) * 8 + 2 * c));
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(stage + k_codes_at + (r + 8 * i) * 32 + c * 8);
+          kc[i][0] = u.x; kc[i][1] = u.y;
+          const uint32_t b = stage[k_scales_at + (r + 8 * i) * 4 + c];
+          sc[i] = e4m3x2_to_f16(b | (b << 8));
+        }
+      }
+#pragma unroll
+      for (int wd = 0; wd < D / 32; ++wd) {                  // eight channels a lane: two steps
+        uint32_t a[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t s2 = D == 128 ? __byte_perm(sc[i], 0, wd < 2 ? 0x1010 : 0x3232) : sc[i];
+          e2m1x8_to_f16(kc[i][wd], a[i][0], a[i][1], a[i][2], a[i][3]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a[i][x] = h2_mul(a[i][x], s2);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ks = 2 * wd + h;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t b0, b1;
+            if (NT > 1) {
+              const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nt * KS + ks) * 32 + lane) * 2);
+              b0 = b.x; b1 = b.y;
+            } else {
+              b0 = qf[NT > 1 ? 0 : nt][ks][0];
+              b1 = qf[NT > 1 ? 0 : nt][ks][1];
+            }
+            mma16816(s[nt], a[0][2 * h], a[1][2 * h], a[0][2 * h + 1], a[1][2 * h + 1], b0, b1);
+          }
+        }
+      }
+      // ------------------------------------------------------ running softmax
+      const int t = meta.tile * TILE + warp * 16 + r;        // token of s[.][0..1]; t + 8: s[.][2..3]
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] *= to_log2[nt][i & 1];
+      if (meta.flags & kEdge) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int ti = t + (i >> 1) * 8;
+            if (ti < see_lo[nt][i & 1] || ti >= see_hi[nt][i & 1]) s[nt][i] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) above |= s[nt][i] > m_run[nt][i & 1] + kRescaleAt;
+      if (__any_sync(0xFFFFFFFFu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(s[nt][i], s[nt][i + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            const float now = fmaxf(m_run[nt][i], top);
+            const float shrink = now > m_run[nt][i] ? ex2(m_run[nt][i] - now) : 1.0f;   // ex2(-inf) = 0
+            m_run[nt][i] = now;
+            l_run[nt][i] *= shrink;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[nt][j][i] *= shrink;
+              o[nt][j][i + 2] *= shrink;
+            }
+          }
+      }
+      uint32_t pf[NT][2];                                    // B fragments of P^T
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // a column that has seen nothing yet: m is -inf, every p is 0
+          const float m = m_run[nt][i & 1];
+          e[i] = ex2(s[nt][i] - (m == -INFINITY ? 0.0f : m));
+        }
+        l_run[nt][0] += e[0] + e[2];
+        l_run[nt][1] += e[1] + e[3];
+        pf[nt][0] = transpose8x8(pack_f16(e[0], e[1]));
+        pf[nt][1] = transpose8x8(pack_f16(e[2], e[3]));
+      }
+      // ------------------------------------------------ O^T += V^T P^T
+      // Lane (r, c) holds, for tokens 2c, 2c+1 (+ 8), the 16 channels (D = 64:
+      // 8 channels) of its row r; nibbles of the two tokens are interleaved so
+      // that one converted pair is two tokens of one channel.
+      uint32_t sv[2];
+      uint32_t lo[2][D / 64], hi[2][D / 64];                 // even, odd channels; bytes: channel pairs
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int blk = D == 128 ? r : r >> 1;
+        sv[i] = e4m3x2_to_f16(
+            *reinterpret_cast<const uint16_t*>(stage + v_scales_at + i * (8 * D / 16) + blk * 8 + 2 * c));
+        if (meta.flags & kEdge) {
+          // a masked token's weight is 0; its scale must not be a NaN
+          const int tv = meta.tile * TILE + warp * 16 + 8 * i + 2 * c;
+          if (tv >= g.kv) sv[i] = 0;
+          else if (tv + 1 >= g.kv) sv[i] &= 0xFFFFu;
+        }
+        const uint8_t* vc = stage + v_codes_at + i * (8 * D / 2);
+        uint32_t x[D / 64], y[D / 64];                       // token 2c, token 2c + 1
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(vc + lane * 16);
+          x[0] = u.x; x[D / 64 - 1] = u.y; y[0] = u.z; y[D / 64 - 1] = u.w;
+        } else {
+          x[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + (r & 1) * 4);
+          y[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + 8 + (r & 1) * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          lo[i][k] = (x[k] & 0x0F0F0F0Fu) | ((y[k] << 4) & 0xF0F0F0F0u);
+          hi[i][k] = ((x[k] >> 4) & 0x0F0F0F0Fu) | (y[k] & 0xF0F0F0F0u);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {
+        uint32_t a[2][2][4];                                 // [token group][row half][step]
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e2m1x8_to_f16(lo[i][k], a[i][0][0], a[i][0][1], a[i][0][2], a[i][0][3]);
+          e2m1x8_to_f16(hi[i][k], a[i][1][0], a[i][1][1], a[i][1][2], a[i][1][3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) a[i][h][x] = h2_mul(a[i][h][x], sv[i]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(o[nt][4 * k + x], a[0][0][x], a[0][1][x], a[1][0][x], a[1][1][x], pf[nt][0], pf[nt][1]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + st);
+
+    if (!(meta.flags & kLast)) continue;
+    // ------------------------------------------------ end of a run of a key
+    // join the warps: m and l first, then O by column tile
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = l_run[nt][i];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        if (r == 0) {
+          s_m[warp * NC + 8 * nt + 2 * c + i] = m_run[nt][i];
+          s_l[warp * NC + 8 * nt + 2 * c + i] = l;
+        }
+      }
+    if (!sync_consumers()) return give_up();
+    const bool whole = meta.key_f0 >= f0 && meta.key_f0 + meta.key_tiles <= f1;
+    // a key's run: slot 0 when it starts with the chunk, else 1 (it ends it)
+    const int slot = 2 * blockIdx.x + (meta.key_f0 > f0 ? 1 : 0);
+    float* part_m = p.partials + static_cast<size_t>(slot) * NC * (D + 2);
+    float* part_l = part_m + NC;
+    float* part_o = part_l + NC;                             // [NC][D]
+    const float v_gsa = __ldg(p.v_gsa + meta.head);
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f}, mine2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = 8 * nt + 2 * c + i;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top[i] = fmaxf(top[i], s_m[w * NC + n]);
+        const float base = top[i] == -INFINITY ? 0.0f : top[i];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum[i] += s_l[w * NC + n] * ex2(s_m[w * NC + n] - base);
+        mine2[i] = ex2(s_m[warp * NC + n] - base);
+      }
+      // (NT is small: the copy keeps o indexed by constants)
+      float ov[MT][4];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+        if (x == nt)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ov[j][i] = o[x][j][i];
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_join[(warp * FR + 4 * j + i) * 32 + lane] = ov[j][i] * mine2[i & 1];
+      if (!sync_consumers()) return give_up();
+      // warp w sums its share of the fragment's registers over the warps
+      constexpr int SH = FR / NW;                            // >= 4: whole channel pairs
+      float v[SH];
+#pragma unroll
+      for (int x = 0; x < SH; ++x) v[x] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int x = 0; x < SH; ++x) v[x] += s_join[(w * FR + warp * SH + x) * 32 + lane];
+      // register 4 j + 2 e + i: channel (D / 8) r + 2 j + e of column 2 c + i
+      const int ch = (D / 8) * r + warp * SH / 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = 8 * nt + 2 * c + i;
+        if (n >= g.n_cols) continue;
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < SH / 2; ++x) {
+            // x = channel ch + x: register 4 (x / 2) + 2 (x % 2) + i
+            part_o[n * D + ch + x] = v[4 * (x / 2) + 2 * (x % 2) + i];
+          }
+          if (r == 0 && warp == 0) {
+            part_m[n] = top[i];
+            part_l[n] = sum[i];
+          }
+          continue;
+        }
+        const int col = g.c0 + n, iq = col / p.G;
+        const int64_t row = static_cast<int64_t>(g.q0 + iq) * p.Hq + meta.head * p.G + (col - iq * p.G);
+        const float inv = sum[i] > 0.0f ? __fdividef(v_gsa, sum[i]) : 0.0f;
+#pragma unroll
+        for (int x = 0; x < SH / 2; x += 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * x + i] * inv, v[2 * x + 2 + i] * inv);
+          *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + ch + x) = h;
+        }
+        if (p.lse && r == 0 && warp == 0)
+          p.lse[row] = sum[i] > 0.0f ? (top[i] + log2f(sum[i])) * 0.693147180559945309f : -INFINITY;
+      }
+      if (!sync_consumers()) return give_up();
+    }
+    if (whole) continue;
+
+    // ------------------------------------------------ join the chunks of a key
+    const int first = meta.key_f0 / chunk, last = (meta.key_f0 + meta.key_tiles - 1) / chunk;
+    __threadfence();
+    if (!sync_consumers()) return give_up();
+    if (tid == 0) {
+      const uint32_t n = atomicAdd(p.tickets + first, 1u);
+      const bool all = n == static_cast<uint32_t>(last - first);
+      if (all) p.tickets[first] = 0u;
+      *s_flag = all;
+    }
+    if (!sync_consumers()) return give_up();
+    if (!*s_flag) continue;
+    __threadfence();
+    const int tail = meta.key_f0 > static_cast<int64_t>(first) * chunk ? 1 : 0;   // the first block's slot
+    for (int n = 0; n < g.n_cols; ++n) {
+      float top = -INFINITY;
+      for (int b = first; b <= last; ++b)
+        top = fmaxf(top, __ldcg(p.partials + static_cast<size_t>(2 * b + (b == first ? tail : 0)) * NC * (D + 2) + n));
+      const float base = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, acc = 0.0f;
+      const int chn = tid;                                   // one channel per thread
+      for (int b = first; b <= last; ++b) {
+        const float* q = p.partials + static_cast<size_t>(2 * b + (b == first ? tail : 0)) * NC * (D + 2);
+        const float w = ex2(__ldcg(q + n) - base);
+        sum += w * __ldcg(q + NC + n);
+        if (chn < D) acc += w * __ldcg(q + 2 * NC + n * D + chn);
+      }
+      const int col = g.c0 + n, iq = col / p.G;
+      const int64_t row = static_cast<int64_t>(g.q0 + iq) * p.Hq + meta.head * p.G + (col - iq * p.G);
+      if (chn < D) p.out[row * D + chn] = __float2bfloat16_rn(sum > 0.0f ? acc * __fdividef(v_gsa, sum) : 0.0f);
+      if (p.lse && tid == 0) p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+    }
+  }
+}
+
+size_t a256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct AttnWs {
+  size_t tickets, partials, total;
+};
+AttnWs attn_ws_layout(int D) {
+  AttnWs L;
+  L.tickets = 256;
+  L.partials = a256(L.tickets + kAttnMaxCtas * 4);
+  L.total = a256(L.partials + size_t(2) * kAttnMaxCols * (D + 2) * 4);
+  return L;
+}
+
+template <int D, int NT, int NW, int STAGES, int MINB>
+nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
+  using Sh = AttnShape<D, NT, NW, STAGES>;
+  auto kernel = kv_attention_kernel<D, NT, NW, STAGES, MINB>;
+  static int per_sm[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
+  const int sms = device_sm_count();
+  if (sms <= 0) return NVR_ERR_CUDA;
+  if (!per_sm[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, Sh::kThreads, Sh::kSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    per_sm[dev] = n > 0 ? n : 1;
+  }
+  p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + Sh::kCols - 1) / Sh::kCols);
+  // the flat order of tiles is counted in 32 bits
+  const int64_t items = static_cast<int64_t>(p.B) * p.groups;
+  const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1);
+  if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
+  int64_t grid = static_cast<int64_t>(sms) * per_sm[dev];
+  if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
+  if (grid * Sh::kCols > kAttnMaxCols) grid = kAttnMaxCols / Sh::kCols;
+  if (grid > most) grid = most;
+  p.min_chunk = 2;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+template <int D>
+nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
+  // columns of a pass: as few as hold a sequence's queries, 32 at most
+  const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
+  if (cols <= 8) return launch_attn<D, 1, 4, 5, 3>(p, max_kv, s);
+  if (cols <= 16) return launch_attn<D, 2, 4, 5, 2>(p, max_kv, s);
+  if constexpr (D == 128) return launch_attn<D, 4, 8, 4, 1>(p, max_kv, s);
+  else return launch_attn<D, 4, 4, 5, 2>(p, max_kv, s);
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace
+
+}  // namespace nvr
+
+using namespace nvr;
+
+extern "C" size_t nvfp4_kv_attention_workspace_size(int64_t T_max, int64_t B_max, int Hq, int Hkv, int D) {
+  if (T_max < 0 || B_max < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || !kv_head_dim_ok(D)) return 0;
+  return attn_ws_layout(D).total;
+}
+
+extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_t T, int Hq, int Hkv, int D,
+                                         const uint8_t* cache, int64_t n_pages, int page_size,
+                                         const int32_t* page_table, int64_t B, int64_t max_pages,
+                                         const int32_t* kv_lens, const int32_t* cu_q, int max_q, const float* k_gsa,
+                                         const float* v_gsa, float scale, int causal, int window, void* out,
+                                         float* lse, void* workspace, size_t ws_bytes, nvr_stream_t stream) {
+  if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hkv > 65536 || Hq / Hkv > 65536) return NVR_ERR_INVALID_ARG;
+  if (n_pages < 1 || max_pages < 0 || max_q < 0 || window < 0 || (window > 0 && !causal)) return NVR_ERR_INVALID_ARG;
+  if (!(scale > -INFINITY && scale < INFINITY)) return NVR_ERR_INVALID_ARG;
+  if (!kv_head_dim_ok(D) || !kv_page_size_ok(page_size)) return NVR_ERR_UNSUPPORTED;
+  if (!cache || !k_gsa || !v_gsa || !workspace) return NVR_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !out || !kv_lens || B < 1 || max_q < 1 || (max_pages > 0 && !page_table)))
+    return NVR_ERR_INVALID_ARG;
+  if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
+  if (T > 0 && (q_stride < static_cast<int64_t>(Hq) * D || q_stride % 8)) return NVR_ERR_INVALID_ARG;
+  if (T > INT32_MAX || B > INT32_MAX || max_pages * page_size > INT32_MAX) return NVR_ERR_UNSUPPORTED;
+  if (off16(q) || off16(cache) || off16(out) || off4(page_table) || off4(kv_lens) || off4(cu_q) || off4(k_gsa) ||
+      off4(v_gsa) || off4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return NVR_ERR_ALIGNMENT;
+  const AttnWs L = attn_ws_layout(D);
+  if (ws_bytes < L.total) return NVR_ERR_WORKSPACE;
+  if (T == 0) return NVR_OK;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  AttnParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q); p.q_stride = q_stride; p.T = T;
+  p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.cache = cache; p.n_pages = n_pages;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  p.page_table = page_table; p.B = static_cast<int>(B); p.max_pages = static_cast<int>(max_pages);
+  p.kv_lens = kv_lens; p.cu_q = cu_q; p.max_q = max_q;
+  p.k_gsa = k_gsa; p.v_gsa = v_gsa;
+  p.scale_log2 = scale * 1.44269504088896341f;
+  p.causal = causal != 0; p.window = window;
+  p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
+  p.status = reinterpret_cast<uint32_t*>(w + kWsStatus);
+  p.tickets = reinterpret_cast<uint32_t*>(w + L.tickets);
+  p.partials = reinterpret_cast<float*>(w + L.partials);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int max_kv = static_cast<int>(max_pages) * page_size;
+  return D == 128 ? dispatch_attn<128>(p, max_kv, s) : dispatch_attn<64>(p, max_kv, s);
+}

@@ -155,15 +155,30 @@ struct QuantScale {
   int mode;      // 0: gsa == 0 (all zero), 1: fast (Markstein), 2: IEEE divide
 };
 
-__device__ __forceinline__ QuantScale make_quant_scale(float amax) {
+__device__ __forceinline__ QuantScale quant_scale_of(float gsa) {
   QuantScale q;
-  q.gsa = __fdiv_rn(amax, kGsaDivisor);
+  q.gsa = gsa;
   q.rgsa = q.gsa > 0.0f ? __frcp_rn(q.gsa) : 0.0f;
   // Markstein's hypotheses need gsa and 1/gsa inside [2^-80, 2^80]
   const float lo = 8.27180613e-25f;   // 2^-80
   const float hi = 1.20892582e+24f;   // 2^80
   q.mode = (q.gsa == 0.0f) ? 0 : ((q.gsa >= lo && q.gsa <= hi) ? 1 : 2);
   return q;
+}
+
+__device__ __forceinline__ QuantScale make_quant_scale(float amax) {
+  return quant_scale_of(__fdiv_rn(amax, kGsaDivisor));
+}
+
+// RN(x / gsa), and the E4M3 scale byte of a block whose largest magnitude is
+// amax (see quant_block16 for why the short division is exact).
+__device__ __forceinline__ float quant_divide(float x, const QuantScale& qs) {
+  return qs.mode == 1 ? div_rn(x, qs.gsa, qs.rgsa) : __fdiv_rn(x, qs.gsa);
+}
+__device__ __forceinline__ uint32_t quant_scale_byte(float amax, const QuantScale& qs) {
+  if (qs.mode == 0) return 0;
+  const float r6 = 0.16666667163372039794921875f;       // RN(1/6)
+  return e4m3_byte(div_rn_short(quant_divide(amax, qs), 6.0f, r6));
 }
 
 // One block of input: 16 values widened to fp32, plus the sign of every

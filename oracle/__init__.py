@@ -32,6 +32,7 @@ taken.  Modules:
   nibble packing and the 128x4 scale-factor tile layout.
 * ``gemm``     -- logits of the dequantized operands in float64.
 * ``router``   -- sigmoid, bias-corrected top-k, renormalised routed weights.
+* ``kv_cache`` -- the paged NVFP4 key/value cache and the attention over it.
 * ``compare``  -- the tolerance rules used by the parity tests.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test in
@@ -41,4 +42,4 @@ which is "parity unpinned" beyond the floating-point error bound used in
 documented).
 """
 
-from . import formats, quantize, gemm, router, compare, pipeline, hash_router, moe  # noqa: F401
+from . import formats, quantize, gemm, router, compare, pipeline, hash_router, moe, kv_cache  # noqa: F401
