@@ -20,7 +20,7 @@
 // may run over the channels (tokens) in any order as long as both operands
 // agree, so each lane takes the 16 bytes it loads as they are.
 //
-// Work: the 16 * NW-token tiles of all (sequence, column group, KV head) keys,
+// Work: the tiles (16 tokens for each of MW groups of each of NW warps) of all (sequence, column group, KV head) keys,
 // laid end to end, are cut into equal chunks, one per resident block; a key
 // cut by a chunk border leaves partials in the workspace and the last block to
 // arrive (ticket) joins them in chunk order, so results do not depend on timing.
@@ -34,9 +34,15 @@ namespace nvr {
 
 namespace {
 
-constexpr int kAttnMaxCtas = 2048;         // ticket words in the workspace
+constexpr int kAttnMaxCtas = 2048;         // blocks; two ticket words each in the workspace
+constexpr int kJoinAlone = 40;             // parts of a key that one block joins at once
+constexpr int kJoinRun = 16;               // beyond that, the parts joined first
 constexpr int kAttnMaxCols = 16384;        // column slots of partials: blocks * columns, per side
 constexpr float kRescaleAt = 8.0f;
+// Starting and ending a key costs a block about as much as this many tiles
+// (queries, joining the warps, storing): counted in the chunks, so that blocks
+// with many short keys get fewer tiles.
+constexpr int kKeyCost = 1;
 
 struct AttnParams {
   const __nv_bfloat16* q;
@@ -106,12 +112,19 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
   return g;
 }
 
-// What a stage of the ring holds.
-struct Meta {
-  int item, head, tile;
+// A key's length in the flat order: its tiles, then kKeyCost places without work.
+__device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kKeyCost : 0; }
+
+// What a stage of the ring holds (everything about its key, so that nothing of
+// it stays in the consumers' registers); a run's first stage brings the queries.
+struct alignas(16) Meta {
+  uint32_t flags;             // kFirst, kLast, kEdge
+  uint32_t live;              // bit i: tokens 16 i .. 16 i + 15 of the tile were loaded
+  int tile, head;
   int key_f0, key_tiles;      // the key's place in the flat order of tiles
-  uint32_t flags;
-  uint32_t live;              // bit s: the 16 tokens of warp s were loaded
+  int kv, n_q, q0, iq0, rem0, n_cols;   // the first column is head rem0 of the group's query iq0
+  float k_gsa, v_gsa;
+  int pad[2];
 };
 constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4;
 
@@ -147,37 +160,42 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, int NT, int NW, int STAGES>
+template <int D, int NT, int NW, int MW, int STAGES>
 struct AttnShape {
-  static constexpr int kTile = 16 * NW;
+  static constexpr int kTile = 16 * NW * MW;
   static constexpr int kCols = 8 * NT;
   static constexpr int kThreads = 32 * (NW + 1);
   static constexpr int kStageBytes = kTile * D * 9 / 8;
   static constexpr int kFrag = D / 4;                        // O registers of a lane per 8 columns
-  static constexpr int kJoinBytes = NW * kFrag * 32 * 4;     // one column tile of every warp
+  static constexpr int kShare = kFrag / NW;                  // of them, those a warp joins
+  static constexpr int kJoinBytes = NW * (NW - 1) * kShare * 32 * 4;
   static constexpr int kQBytes = NT > 1 ? NT * (D / 16) * 64 * 4 : 0;
   static constexpr int kSmem = STAGES * kStageBytes + kJoinBytes + kQBytes + 2 * NW * kCols * 4 +
-                               STAGES * static_cast<int>(sizeof(Meta)) + (2 * STAGES) * 8 + 64 + 128;
+                               STAGES * (static_cast<int>(sizeof(Meta)) + kCols * D * 2) + (2 * STAGES + 3) * 8 + 64 + 128;
 };
 
-template <int D, int NT, int NW, int STAGES, int MINB>
+template <int D, int NT, int NW, int MW, int STAGES, int MINB>
 __global__ void __launch_bounds__(32 * (NW + 1), MINB)
 kv_attention_kernel(const AttnParams p) {
-  using Sh = AttnShape<D, NT, NW, STAGES>;
-  constexpr int TILE = Sh::kTile, NC = Sh::kCols, FR = Sh::kFrag;
+  using Sh = AttnShape<D, NT, NW, MW, STAGES>;
+  constexpr int TILE = Sh::kTile, NC = Sh::kCols, SH = Sh::kShare;
+  static_assert(D == 64 || D == 128, "the fragment loads are written for these");
+  static_assert(TILE <= 256 && 32 * NW >= D && Sh::kStageBytes % 128 == 0, "tile plan");
   constexpr int KS = D / 16;                                 // steps of the first product
   constexpr int MT = D / 16;                                 // channel tiles of the second
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  float* s_join = reinterpret_cast<float*>(smem + STAGES * Sh::kStageBytes);          // [NW][FR][32]
-  uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + NW * FR * 32);                 // [NT][KS][32][2] (NT > 1)
+  float* s_join = reinterpret_cast<float*>(smem + STAGES * Sh::kStageBytes);          // [NW][NW - 1][SH][32]
+  uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + Sh::kJoinBytes / 4);                 // [NT][KS][32][2] (NT > 1)
   float* s_m = reinterpret_cast<float*>(s_q + Sh::kQBytes / 4);                       // [NW][NC]
   float* s_l = s_m + NW * NC;
-  Meta* s_meta = reinterpret_cast<Meta*>(s_l + NW * NC);
-  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_meta + STAGES) + 7) & ~uintptr_t(7));
+  uint8_t* s_raw = reinterpret_cast<uint8_t*>(s_l + NW * NC);                         // [STAGES][NC][D] bf16 queries
+  Meta* s_meta = reinterpret_cast<Meta*>(s_raw + STAGES * NC * D * 2);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_meta + STAGES);
   uint64_t* empty = full + STAGES;
   uint64_t* meet = empty + STAGES;                           // the consumer warps' barrier: bounded, unlike bar.sync
-  int* s_start = reinterpret_cast<int*>(meet + 1);     // item, offset inside it, total tiles
+  uint64_t* join_free = meet + 1;                            // the join buffer has been read
+  int* s_start = reinterpret_cast<int*>(meet + 2);           // item, offset inside it, whether the chunk has work
   volatile int* abort_flag = s_start + 4;
   int* s_flag = s_start + 5;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,6 +203,7 @@ kv_attention_kernel(const AttnParams p) {
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, NW); }
     mbar_init(meet, NW);
+    mbar_init(join_free, NW);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -196,7 +215,7 @@ kv_attention_kernel(const AttnParams p) {
   const int n_items = p.B * p.groups;
   const int per = (n_items + Sh::kThreads - 1) / Sh::kThreads;
   int mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += group_of<NC, TILE>(p, i).tiles * p.Hkv;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost(group_of<NC, TILE>(p, i)) * p.Hkv;
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -217,53 +236,87 @@ kv_attention_kernel(const AttnParams p) {
   const int excl = before + incl - mine;
   if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
     int at = excl, i = tid * per;
+    Group g;
     for (;; ++i) {
-      const int n = group_of<NC, TILE>(p, i).tiles * p.Hkv;
+      g = group_of<NC, TILE>(p, i);
+      const int n = key_cost(g) * p.Hkv;
       if (f0 < at + n) break;
       at += n;
     }
     s_start[0] = i;
     s_start[1] = f0 - at;
+    // the last chunk may hold nothing but the last key's places without work
+    const int ti = (f0 - at) % key_cost(g);
+    s_start[2] = ti < g.tiles || f1 - f0 > key_cost(g) - ti;
   }
   __syncthreads();
-  if (f0 >= f1) return;
+  if (f0 >= f1 || !s_start[2]) return;
 
   if (warp == NW) {
     // -------------------------------------------------------------- producer
-    int item = s_start[0], off = s_start[1], f = f0, fill = 0;
+    int item = s_start[0], off = s_start[1], f = f0, fill = 0, st = 0;
+    uint32_t parity = 1;
     const int S = 1 << p.page_shift;
     const int part = min(S, TILE);                           // tokens of one copied piece
+    const int pieces = TILE / part;
     bool ok = true;
+    Group next = group_of<NC, TILE>(p, item);
     while (f < f1 && ok) {
-      const Group g = group_of<NC, TILE>(p, item);
-      const int n_key = g.tiles * p.Hkv;
+      const Group g = next;
+      // (read ahead: its loads are not waited for here)
+      if (item + 1 < n_items) next = group_of<NC, TILE>(p, item + 1);
+      const int cost = key_cost(g), n_item = cost * p.Hkv;
       const int32_t* table = p.page_table + static_cast<int64_t>(g.b) * p.max_pages;
-      while (off < n_key && f < f1) {
-        const int head = off / g.tiles, ti = off - head * g.tiles;
+      int head = off / max(cost, 1), ti = off - head * cost;
+      const int iq0 = g.c0 / p.G, rem0 = g.c0 - iq0 * p.G;
+      // every column sees every token of a tile inside [sure_lo, sure_hi)
+      const int sure_hi = p.causal ? g.kv - g.n_q + iq0 + 1 : g.kv;
+      const int sure_lo = p.window > 0 ? g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G + 1 - p.window : 0;
+      // 32 entries of the page table in the lanes, the next 32 on their way
+      int at = -1, pages = -1, pages_next = -1;
+      int scaled = -1;                                       // the head whose scales are at hand
+      float k_gsa = 0.0f, v_gsa = 0.0f;
+      auto entries = [&](int x) { return x + lane < p.max_pages ? __ldg(table + x + lane) : -1; };
+      while (off < n_item && f < f1) {
+        if (ti >= g.tiles) {                                 // places without work
+          const int skip = min(cost - ti, f1 - f);
+          off += skip; f += skip;
+          ti = 0; ++head;
+          continue;
+        }
         const int t0 = (g.tile0 + ti) * TILE;
-        const int st = fill % STAGES;
-        if (!wait_bounded(empty + st, ((fill / STAGES) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        const int x = t0 >> p.page_shift;                    // the tile's first page: its pages share a group of 32
+        if ((x & ~31) != at) {
+          pages = at >= 0 && (x & ~31) == at + 32 ? pages_next : entries(x & ~31);
+          at = x & ~31;
+          pages_next = entries(at + 32);
+        }
         // lane i looks after piece i of the tile (at most TILE / 16 pieces)
         const int pt = t0 + lane * part;
-        int page = -1;
-        if (lane < TILE / part && pt < g.hi && pt + part > g.lo) page = __ldg(table + (pt >> p.page_shift));
-        const bool have = page >= 0 && page < p.n_pages;
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, (x & 31) + min(lane, pieces - 1));
+        const bool have = lane < pieces && pt < g.hi && pt + part > g.lo && page >= 0 && page < p.n_pages;
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(empty + st, parity, abort_flag))) { ok = false; break; }
         const uint32_t got = __ballot_sync(0xFFFFFFFFu, have);
+        const bool first = ti == 0 || f == f0;
+        if (scaled != head) {
+          k_gsa = __ldg(p.k_gsa + head);
+          v_gsa = __ldg(p.v_gsa + head);
+          scaled = head;
+        }
         if (lane == 0) {
-          Meta m;
-          m.item = item; m.head = head; m.tile = g.tile0 + ti;
+          Meta m = {};
+          m.head = head; m.tile = g.tile0 + ti;
           m.key_f0 = f - ti; m.key_tiles = g.tiles;
+          m.kv = g.kv; m.n_q = g.n_q; m.q0 = g.q0; m.iq0 = iq0; m.rem0 = rem0; m.n_cols = g.n_cols;
+          m.k_gsa = k_gsa; m.v_gsa = v_gsa;
           const uint32_t each = (1u << (part / 16)) - 1;
           m.live = 0;
-          for (int i = 0; i < TILE / part; ++i)
+          for (int i = 0; i < pieces; ++i)
             if ((got >> i) & 1u) m.live |= each << (i * (part / 16));
-          m.flags = (ti == 0 || f == f0 ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u);
-          // every column sees every token of an inner tile
-          const int sure_hi = p.causal ? g.kv - g.n_q + g.c0 / p.G + 1 : g.kv;
-          const int sure_lo = p.window > 0 ? g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G + 1 - p.window : 0;
-          if (t0 + TILE > sure_hi || t0 < sure_lo || got != (1u << (TILE / part)) - 1u) m.flags |= kEdge;
+          m.flags = (first ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u);
+          if (t0 + TILE > sure_hi || t0 < sure_lo || got != (1u << pieces) - 1u) m.flags |= kEdge;
           s_meta[st] = m;
-          mbar_arrive_expect_tx(full + st, __popc(got) * part * (D * 9 / 8));
+          mbar_arrive_expect_tx(full + st, __popc(got) * part * (D * 9 / 8) + (first ? g.n_cols * D * 2 : 0));
         }
         __syncwarp();
         if (have) {
@@ -282,7 +335,18 @@ kv_attention_kernel(const AttnParams p) {
                       part * KvPage<D>::kScaleRow, full + st);
           }
         }
-        ++fill; ++off; ++f;
+        if (first) {
+          // the columns of one query are heads next to each other: lane i
+          // copies those of the group's i-th query
+          const int iq = iq0 + lane;
+          const int from = max(g.c0, iq * p.G), to = min(g.c0 + g.n_cols, (iq + 1) * p.G);
+          if (from < to)
+            bulk_load(s_raw + (st * NC + from - g.c0) * D * 2,
+                      p.q + (g.q0 + iq) * p.q_stride + static_cast<int64_t>(head * p.G + from - iq * p.G) * D,
+                      (to - from) * D * 2, full + st);
+        }
+        if (++st == STAGES) { st = 0; parity ^= 1u; }
+        ++fill; ++off; ++f; ++ti;
       }
       off = 0;
       ++item;
@@ -305,20 +369,21 @@ kv_attention_kernel(const AttnParams p) {
   // ---------------------------------------------------------------- consumers
   const int r = lane >> 2, c = lane & 3;
   const int S = 1 << p.page_shift, part = min(S, TILE);
-  // this warp's 16 tokens inside a stage
-  const int piece = warp * 16 / part, in_piece = warp * 16 % part;
-  const int piece_at = piece * part * (D * 9 / 8);
-  const int k_codes_at = piece_at + in_piece * (D / 2);
-  const int k_scales_at = piece_at + KvPage<D>::key_scales(part) + in_piece * (D / 16);
-  const int v_codes_at = piece_at + KvPage<D>::value_codes(part) + in_piece * (D / 2);
-  const int v_scales_at = piece_at + KvPage<D>::value_scales(part) + in_piece * (D / 16);
+  // this warp's groups of 16 tokens inside a stage
+  int k_codes_at[MW], k_scales_at[MW], v_codes_at[MW], v_scales_at[MW];
+#pragma unroll
+  for (int u = 0; u < MW; ++u) {
+    const int t = (warp * MW + u) * 16;
+    const int piece_at = t / part * part * (D * 9 / 8), in_piece = t % part;
+    k_codes_at[u] = piece_at + in_piece * (D / 2);
+    k_scales_at[u] = piece_at + KvPage<D>::key_scales(part) + in_piece * (D / 16);
+    v_codes_at[u] = piece_at + KvPage<D>::value_codes(part) + in_piece * (D / 2);
+    v_scales_at[u] = piece_at + KvPage<D>::value_scales(part) + in_piece * (D / 16);
+  }
 
   uint32_t qf[NT > 1 ? 1 : NT][KS][2];                       // B fragments of Q^T (shared memory for NT > 1)
   float o[NT][MT][4];
-  float m_run[NT][2], l_run[NT][2], to_log2[NT][2];
-  int see_lo[NT][2], see_hi[NT][2];
-  Group g;
-  g.n_cols = 0;
+  float m_neg[NT][2], l_run[NT][2], to_log2[NT][2];         // -m: +inf until a token is seen
   uint32_t met = 0;
   auto sync_consumers = [&]() {
     __syncwarp();
@@ -333,26 +398,32 @@ kv_attention_kernel(const AttnParams p) {
       *abort_flag = 1;
     }
   };
-  for (int f = f0, fill = 0; f < f1; ++f, ++fill) {
-    const int st = fill % STAGES;
-    if (!__all_sync(0xFFFFFFFFu, wait_bounded(full + st, (fill / STAGES) & 1, abort_flag))) return give_up();
-    const Meta meta = s_meta[st];
-    if (meta.flags & kFirst) {
-      g = group_of<NC, TILE>(p, meta.item);
-      const float k_gsa = __ldg(p.k_gsa + meta.head);
+  // small numerators only: exact in fp32 (the quotient's distance from an
+  // integer is at least 1 / (2 G), far above the rounding of a product below 2^18)
+  const float inv_G = 1.0f / static_cast<float>(p.G);
+  auto div_G = [&](int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_G); };
+  uint32_t joined = 1;
+  int st = 0;
+  uint32_t parity = 0;
+  for (bool more = true; more;) {
+    if (!__all_sync(0xFFFFFFFFu, wait_bounded(full + st, parity, abort_flag))) return give_up();
+    const Meta& meta = s_meta[st];
+    const uint32_t flags = meta.flags;
+    const int tile = meta.tile;
+    if (flags & kFirst) {
+      const int n_cols = meta.n_cols;
+      const float k_gsa = meta.k_gsa;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         // column 8 nt + r: its query row, scaled by a power of two into the
         // upper range of fp16 (bf16 has fewer significant bits: exact, but for
         // channels 2^28 below the row's largest, which lose their last bits)
-        const int col = g.c0 + 8 * nt + r;
-        const bool on = 8 * nt + r < g.n_cols;
-        const int iq = on ? col / p.G : 0, hq = meta.head * p.G + (on ? col - iq * p.G : 0);
-        const __nv_bfloat16* src = p.q + (g.q0 + iq) * p.q_stride + static_cast<int64_t>(hq) * D + c * (D / 4);
+        const bool on = 8 * nt + r < n_cols;
+        const uint8_t* src = s_raw + (st * NC + 8 * nt + r) * D * 2 + c * (D / 2);
         uint32_t w[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint4 u = on ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = on ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
           w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
         uint32_t big = 0;
@@ -387,12 +458,7 @@ kv_attention_kernel(const AttnParams p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           to_log2[nt][i] = __shfl_sync(0xFFFFFFFFu, down, (2 * c + i) * 4);
-          const int n = 8 * nt + 2 * c + i;
-          const bool live = n < g.n_cols;
-          const int pos = g.kv - g.n_q + (g.c0 + (live ? n : 0)) / p.G;
-          see_hi[nt][i] = !live ? 0 : p.causal ? max(pos + 1, 0) : g.kv;
-          see_lo[nt][i] = live && p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
-          m_run[nt][i] = -INFINITY;
+          m_neg[nt][i] = INFINITY;
           l_run[nt][i] = 0.0f;
         }
 #pragma unroll
@@ -404,39 +470,45 @@ kv_attention_kernel(const AttnParams p) {
     }
 
     const uint8_t* stage = smem + st * Sh::kStageBytes;
-    const bool loaded = (meta.live >> warp) & 1u;
-    if (loaded) {
-      // ------------------------------------------------ S^T = K Q^T, 16 tokens
-      float s[NT][4];
+    const uint32_t live = (meta.live >> (warp * MW)) & ((1u << MW) - 1u);
+    if (live) {
+      // --------------------------------------- S^T = K Q^T, MW times 16 tokens
+      float s[MW][NT][4], s1[MW][NT][4];                     // even and odd steps: two chains of products
+      uint32_t kc[MW][2][D / 32];                            // codes of tokens r, r + 8
+      uint32_t sc[MW][2];                                    // their scales as half2
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < MW; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
-      uint32_t kc[2][D / 32];                                // codes of tokens r, r + 8
-      uint32_t sc[2];                                        // their scales as half2
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(stage + k_codes_at + (r + 8 * i) * 64 + c * 16);
-          kc[i][0] = u.x; kc[i][1] = u.y; kc[i][D / 32 - 2] = u.z; kc[i][D / 32 - 1] = u.w;
-          sc[i] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(stage + k_scales_at + (r + 8 * i) * 8 + 2 * c));
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(stage + k_codes_at + (r + 8 * i) * 32 + c * 8);
-          kc[i][0] = u.x; kc[i][1] = u.y;
-          const uint32_t b = stage[k_scales_at + (r + 8 * i) * 4 + c];
-          sc[i] = e4m3x2_to_f16(b | (b << 8));
+          for (int i = 0; i < 4; ++i) s[u][nt][i] = s1[u][nt][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + k_codes_at[u] + (r + 8 * i) * 64 + c * 16);
+            kc[u][i][0] = x.x; kc[u][i][1] = x.y; kc[u][i][D / 32 - 2] = x.z; kc[u][i][D / 32 - 1] = x.w;
+            sc[u][i] =
+                e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(stage + k_scales_at[u] + (r + 8 * i) * 8 + 2 * c));
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(stage + k_codes_at[u] + (r + 8 * i) * 32 + c * 8);
+            kc[u][i][0] = x.x; kc[u][i][1] = x.y;
+            const uint32_t b = stage[k_scales_at[u] + (r + 8 * i) * 4 + c];
+            sc[u][i] = e4m3x2_to_f16(b | (b << 8));
+          }
         }
       }
 #pragma unroll
       for (int wd = 0; wd < D / 32; ++wd) {                  // eight channels a lane: two steps
-        uint32_t a[2][4];
+        uint32_t a[MW][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t s2 = D == 128 ? __byte_perm(sc[i], 0, wd < 2 ? 0x1010 : 0x3232) : sc[i];
-          e2m1x8_to_f16(kc[i][wd], a[i][0], a[i][1], a[i][2], a[i][3]);
+        for (int u = 0; u < MW; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) a[i][x] = h2_mul(a[i][x], s2);
-        }
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t s2 = D == 128 ? __byte_perm(sc[u][i], 0, wd < 2 ? 0x1010 : 0x3232) : sc[u][i];
+            e2m1x8_to_f16(kc[u][i][wd], a[u][i][0], a[u][i][1], a[u][i][2], a[u][i][3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) a[u][i][x] = h2_mul(a[u][i][x], s2);
+          }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int ks = 2 * wd + h;
@@ -450,42 +522,76 @@ kv_attention_kernel(const AttnParams p) {
               b0 = qf[NT > 1 ? 0 : nt][ks][0];
               b1 = qf[NT > 1 ? 0 : nt][ks][1];
             }
-            mma16816(s[nt], a[0][2 * h], a[1][2 * h], a[0][2 * h + 1], a[1][2 * h + 1], b0, b1);
+#pragma unroll
+            for (int u = 0; u < MW; ++u)
+              mma16816(h ? s1[u][nt] : s[u][nt], a[u][0][2 * h], a[u][1][2 * h], a[u][0][2 * h + 1], a[u][1][2 * h + 1], b0, b1);
           }
         }
       }
       // ------------------------------------------------------ running softmax
-      const int t = meta.tile * TILE + warp * 16 + r;        // token of s[.][0..1]; t + 8: s[.][2..3]
-      bool above = false;
+      const int t = tile * TILE + warp * MW * 16 + r;        // token of s[0][.][0..1]; t + 8: s[0][.][2..3]
+      float v[MW][NT][4];                                    // scores relative to m, base 2
+      auto relative = [&]() {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < MW; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] *= to_log2[nt][i & 1];
-      if (meta.flags & kEdge) {
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[u][nt][i] = fmaf(s[u][nt][i], to_log2[nt][i & 1], m_neg[nt][i & 1]);
+        if (flags & kEdge) {
+          const int n_cols = meta.n_cols, kv = meta.kv, first = kv - meta.n_q + meta.iq0, rem0 = meta.rem0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // the tokens [lo, hi) that the column sees
+              const int n = 8 * nt + 2 * c + i;
+              const int pos = first + div_G(rem0 + min(n, n_cols - 1));
+              const int hi = n >= n_cols ? 0 : p.causal ? pos + 1 : kv;
+              const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+#pragma unroll
+              for (int u = 0; u < MW; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int ti = t + 16 * u + 8 * k;
+                  if (!((live >> u) & 1u) || ti < lo || ti >= hi) v[u][nt][i + 2 * k] = -INFINITY;
+                }
+            }
+        }
+      };
+#pragma unroll
+      for (int u = 0; u < MW; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ti = t + (i >> 1) * 8;
-            if (ti < see_lo[nt][i & 1] || ti >= see_hi[nt][i & 1]) s[nt][i] = -INFINITY;
-          }
-      }
+          for (int i = 0; i < 4; ++i) s[u][nt][i] += s1[u][nt][i];
+      relative();
+      float high = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < MW; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) above |= s[nt][i] > m_run[nt][i & 1] + kRescaleAt;
-      if (__any_sync(0xFFFFFFFFu, above)) {
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) high = fmaxf(high, v[u][nt][i]);
+      if (__any_sync(0xFFFFFFFFu, high > kRescaleAt)) {
+        // move m to the largest score so far
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(s[nt][i], s[nt][i + 2]);
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < MW; ++u)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                // (a masked score is -inf here, any other is taken from s again)
+                if (v[u][nt][i + 2 * k] > -INFINITY) top = fmaxf(top, s[u][nt][i + 2 * k] * to_log2[nt][i]);
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            const float now = fmaxf(m_run[nt][i], top);
-            const float shrink = now > m_run[nt][i] ? ex2(m_run[nt][i] - now) : 1.0f;   // ex2(-inf) = 0
-            m_run[nt][i] = now;
+            const float now = fminf(m_neg[nt][i], -top);
+            const float shrink = now < m_neg[nt][i] ? ex2(now - m_neg[nt][i]) : 1.0f;   // ex2(-inf) = 0
+            m_neg[nt][i] = now;
             l_run[nt][i] *= shrink;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
@@ -493,79 +599,87 @@ kv_attention_kernel(const AttnParams p) {
               o[nt][j][i + 2] *= shrink;
             }
           }
+        relative();
       }
-      uint32_t pf[NT][2];                                    // B fragments of P^T
+      uint32_t pf[MW][NT][2];                                // B fragments of P^T
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
+      for (int u = 0; u < MW; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // a column that has seen nothing yet: m is -inf, every p is 0
-          const float m = m_run[nt][i & 1];
-          e[i] = ex2(s[nt][i] - (m == -INFINITY ? 0.0f : m));
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = ex2(v[u][nt][i]);
+          l_run[nt][0] += e[0] + e[2];
+          l_run[nt][1] += e[1] + e[3];
+          pf[u][nt][0] = transpose8x8(pack_f16(e[0], e[1]));
+          pf[u][nt][1] = transpose8x8(pack_f16(e[2], e[3]));
         }
-        l_run[nt][0] += e[0] + e[2];
-        l_run[nt][1] += e[1] + e[3];
-        pf[nt][0] = transpose8x8(pack_f16(e[0], e[1]));
-        pf[nt][1] = transpose8x8(pack_f16(e[2], e[3]));
-      }
       // ------------------------------------------------ O^T += V^T P^T
       // Lane (r, c) holds, for tokens 2c, 2c+1 (+ 8), the 16 channels (D = 64:
       // 8 channels) of its row r; nibbles of the two tokens are interleaved so
       // that one converted pair is two tokens of one channel.
-      uint32_t sv[2];
-      uint32_t lo[2][D / 64], hi[2][D / 64];                 // even, odd channels; bytes: channel pairs
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int blk = D == 128 ? r : r >> 1;
-        sv[i] = e4m3x2_to_f16(
-            *reinterpret_cast<const uint16_t*>(stage + v_scales_at + i * (8 * D / 16) + blk * 8 + 2 * c));
-        if (meta.flags & kEdge) {
-          // a masked token's weight is 0; its scale must not be a NaN
-          const int tv = meta.tile * TILE + warp * 16 + 8 * i + 2 * c;
-          if (tv >= g.kv) sv[i] = 0;
-          else if (tv + 1 >= g.kv) sv[i] &= 0xFFFFu;
-        }
-        const uint8_t* vc = stage + v_codes_at + i * (8 * D / 2);
-        uint32_t x[D / 64], y[D / 64];                       // token 2c, token 2c + 1
-        if (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(vc + lane * 16);
-          x[0] = u.x; x[D / 64 - 1] = u.y; y[0] = u.z; y[D / 64 - 1] = u.w;
-        } else {
-          x[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + (r & 1) * 4);
-          y[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + 8 + (r & 1) * 4);
+      for (int u = 0; u < MW; ++u) {
+        uint32_t sv[2];
+        uint32_t lo[2][D / 64], hi[2][D / 64];               // even, odd channels; bytes: channel pairs
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int blk = D == 128 ? r : r >> 1;
+          sv[i] = e4m3x2_to_f16(
+              *reinterpret_cast<const uint16_t*>(stage + v_scales_at[u] + i * (8 * D / 16) + blk * 8 + 2 * c));
+          if (flags & kEdge) {
+            // a masked token's weight is 0; its scale must not be a NaN
+            const int tv = tile * TILE + (warp * MW + u) * 16 + 8 * i + 2 * c, kv = meta.kv;
+            if (tv >= kv || !((live >> u) & 1u)) sv[i] = 0;
+            else if (tv + 1 >= kv) sv[i] &= 0xFFFFu;
+          }
+          const uint8_t* vc = stage + v_codes_at[u] + i * (8 * D / 2);
+          uint32_t x[D / 64], y[D / 64];                     // token 2c, token 2c + 1
+          if (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vc + lane * 16);
+            x[0] = w.x; x[D / 64 - 1] = w.y; y[0] = w.z; y[D / 64 - 1] = w.w;
+          } else {
+            x[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + (r & 1) * 4);
+            y[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + 8 + (r & 1) * 4);
+          }
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            lo[i][k] = (x[k] & 0x0F0F0F0Fu) | ((y[k] << 4) & 0xF0F0F0F0u);
+            hi[i][k] = ((x[k] >> 4) & 0x0F0F0F0Fu) | (y[k] & 0xF0F0F0F0u);
+          }
         }
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          lo[i][k] = (x[k] & 0x0F0F0F0Fu) | ((y[k] << 4) & 0xF0F0F0F0u);
-          hi[i][k] = ((x[k] >> 4) & 0x0F0F0F0Fu) | (y[k] & 0xF0F0F0F0u);
+          uint32_t a[2][2][4];                               // [token group][row half][step]
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            e2m1x8_to_f16(lo[i][k], a[i][0][0], a[i][0][1], a[i][0][2], a[i][0][3]);
+            e2m1x8_to_f16(hi[i][k], a[i][1][0], a[i][1][1], a[i][1][2], a[i][1][3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) a[i][h][x] = h2_mul(a[i][h][x], sv[i]);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[nt][4 * k + x], a[0][0][x], a[0][1][x], a[1][0][x], a[1][1][x], pf[u][nt][0], pf[u][nt][1]);
         }
-      }
-#pragma unroll
-      for (int k = 0; k < D / 64; ++k) {
-        uint32_t a[2][2][4];                                 // [token group][row half][step]
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          e2m1x8_to_f16(lo[i][k], a[i][0][0], a[i][0][1], a[i][0][2], a[i][0][3]);
-          e2m1x8_to_f16(hi[i][k], a[i][1][0], a[i][1][1], a[i][1][2], a[i][1][3]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) a[i][h][x] = h2_mul(a[i][h][x], sv[i]);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][4 * k + x], a[0][0][x], a[0][1][x], a[1][0][x], a[1][1][x], pf[nt][0], pf[nt][1]);
       }
     }
+    const bool run_ends = flags & kLast;
+    const int head = meta.head, key_f0 = meta.key_f0, key_tiles = meta.key_tiles, n_cols = meta.n_cols;
+    const int q0 = meta.q0 + meta.iq0, rem0 = meta.rem0;
+    const float v_gsa = meta.v_gsa;
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + st);
-
-    if (!(meta.flags & kLast)) continue;
+    if (++st == STAGES) { st = 0; parity ^= 1u; }
+    if (!run_ends) continue;
     // ------------------------------------------------ end of a run of a key
-    // join the warps: m and l first, then O by column tile
+    // the last run of the chunk is one that ends with it, or with the last key's tiles before it
+    more = key_f0 + key_tiles + kKeyCost < f1;
+    // join the warps: every warp gives the others their shares of its O registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,120 +688,198 @@ kv_attention_kernel(const AttnParams p) {
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-        if (r == 0) {
-          s_m[warp * NC + 8 * nt + 2 * c + i] = m_run[nt][i];
-          s_l[warp * NC + 8 * nt + 2 * c + i] = l;
-        }
+        l_run[nt][i] = l;
       }
-    if (!sync_consumers()) return give_up();
-    const bool whole = meta.key_f0 >= f0 && meta.key_f0 + meta.key_tiles <= f1;
+    const bool whole = key_f0 >= f0 && key_f0 + key_tiles <= f1;
     // a key's run: slot 0 when it starts with the chunk, else 1 (it ends it)
-    const int slot = 2 * blockIdx.x + (meta.key_f0 > f0 ? 1 : 0);
+    const int slot = 2 * blockIdx.x + (key_f0 > f0 ? 1 : 0);
     float* part_m = p.partials + static_cast<size_t>(slot) * NC * (D + 2);
     float* part_l = part_m + NC;
     float* part_o = part_l + NC;                             // [NC][D]
-    const float v_gsa = __ldg(p.v_gsa + meta.head);
-#pragma unroll 1
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f}, mine2[2];
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(join_free, joined, abort_flag))) return give_up();
+      joined ^= 1u;
+      if (r == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s_m[warp * NC + 8 * nt + 2 * c + i] = -m_neg[nt][i];
+          s_l[warp * NC + 8 * nt + 2 * c + i] = l_run[nt][i];
+        }
+      }
+      float v[SH];
+#pragma unroll
+      for (int d = 0; d < NW; ++d) {
+        float* dst = s_join + (d * (NW - 1) + (warp < d ? warp : warp - 1)) * SH * 32 + lane;
+#pragma unroll
+        for (int x = 0; x < SH; ++x) {
+          const int reg = d * SH + x;
+          const float y = o[nt][reg / 4][reg % 4];
+          if (d == warp) v[x] = y;
+          else dst[x * 32] = y;
+        }
+      }
+      if (!sync_consumers()) return give_up();
+      float top[2], sum[2], w_of[NW][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int n = 8 * nt + 2 * c + i;
+        top[i] = s_m[n];
+        sum[i] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) top[i] = fmaxf(top[i], s_m[w * NC + n]);
+        for (int w = 1; w < NW; ++w) top[i] = fmaxf(top[i], s_m[w * NC + n]);
         const float base = top[i] == -INFINITY ? 0.0f : top[i];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) sum[i] += s_l[w * NC + n] * ex2(s_m[w * NC + n] - base);
-        mine2[i] = ex2(s_m[warp * NC + n] - base);
+        for (int w = 0; w < NW; ++w) {
+          w_of[w][i] = ex2(s_m[w * NC + n] - base);
+          sum[i] += s_l[w * NC + n] * w_of[w][i];
+        }
       }
-      // (NT is small: the copy keeps o indexed by constants)
-      float ov[MT][4];
-#pragma unroll
-      for (int x = 0; x < NT; ++x)
-        if (x == nt)
-#pragma unroll
-          for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ov[j][i] = o[x][j][i];
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_join[(warp * FR + 4 * j + i) * 32 + lane] = ov[j][i] * mine2[i & 1];
-      if (!sync_consumers()) return give_up();
-      // warp w sums its share of the fragment's registers over the warps
-      constexpr int SH = FR / NW;                            // >= 4: whole channel pairs
-      float v[SH];
-#pragma unroll
-      for (int x = 0; x < SH; ++x) v[x] = 0.0f;
+      static_assert(SH >= 4 && SH % 4 == 0, "a warp joins whole pairs of channels");
+      float own[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < NW; ++w)
+        if (w == warp) { own[0] = w_of[w][0]; own[1] = w_of[w][1]; }
 #pragma unroll
-        for (int x = 0; x < SH; ++x) v[x] += s_join[(w * FR + warp * SH + x) * 32 + lane];
+      for (int x = 0; x < SH; ++x) v[x] *= own[x & 1];
+#pragma unroll
+      for (int k = 0; k < NW - 1; ++k) {
+        // slot k of this warp came from warp k, or k + 1 beyond its own place
+        const float w0 = k < warp ? w_of[k][0] : w_of[k + 1][0], w1 = k < warp ? w_of[k][1] : w_of[k + 1][1];
+#pragma unroll
+        for (int x = 0; x < SH; ++x) v[x] += s_join[((warp * (NW - 1) + k) * SH + x) * 32 + lane] * (x & 1 ? w1 : w0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_free);
       // register 4 j + 2 e + i: channel (D / 8) r + 2 j + e of column 2 c + i
       const int ch = (D / 8) * r + warp * SH / 2;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int n = 8 * nt + 2 * c + i;
-        if (n >= g.n_cols) continue;
+        if (n >= n_cols) continue;
         if (!whole) {
 #pragma unroll
-          for (int x = 0; x < SH / 2; ++x) {
-            // x = channel ch + x: register 4 (x / 2) + 2 (x % 2) + i
-            part_o[n * D + ch + x] = v[4 * (x / 2) + 2 * (x % 2) + i];
-          }
+          for (int x = 0; x < SH / 2; x += 2)
+            *reinterpret_cast<float2*>(part_o + n * D + ch + x) = make_float2(v[2 * x + i], v[2 * x + 2 + i]);
           if (r == 0 && warp == 0) {
             part_m[n] = top[i];
             part_l[n] = sum[i];
           }
           continue;
         }
-        const int col = g.c0 + n, iq = col / p.G;
-        const int64_t row = static_cast<int64_t>(g.q0 + iq) * p.Hq + meta.head * p.G + (col - iq * p.G);
+        const int dq = div_G(rem0 + n);
+        const int64_t row = static_cast<int64_t>(q0 + dq) * p.Hq + head * p.G + (rem0 + n - dq * p.G);
         const float inv = sum[i] > 0.0f ? __fdividef(v_gsa, sum[i]) : 0.0f;
 #pragma unroll
         for (int x = 0; x < SH / 2; x += 2) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * x + i] * inv, v[2 * x + 2 + i] * inv);
-          *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + ch + x) = h;
+          const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * x + i] * inv, v[2 * x + 2 + i] * inv);
+          *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + ch + x) = y;
         }
         if (p.lse && r == 0 && warp == 0)
           p.lse[row] = sum[i] > 0.0f ? (top[i] + log2f(sum[i])) * 0.693147180559945309f : -INFINITY;
       }
-      if (!sync_consumers()) return give_up();
     }
     if (whole) continue;
 
     // ------------------------------------------------ join the chunks of a key
-    const int first = meta.key_f0 / chunk, last = (meta.key_f0 + meta.key_tiles - 1) / chunk;
-    __threadfence();
-    if (!sync_consumers()) return give_up();
-    if (tid == 0) {
-      const uint32_t n = atomicAdd(p.tickets + first, 1u);
-      const bool all = n == static_cast<uint32_t>(last - first);
-      if (all) p.tickets[first] = 0u;
-      *s_flag = all;
-    }
-    if (!sync_consumers()) return give_up();
-    if (!*s_flag) continue;
-    __threadfence();
-    const int tail = meta.key_f0 > static_cast<int64_t>(first) * chunk ? 1 : 0;   // the first block's slot
-    for (int n = 0; n < g.n_cols; ++n) {
+    // Part i lies in the first slot of chunk first + i, but the first part of
+    // a key that starts inside its chunk.  The last chunk to arrive joins all
+    // parts; of more than kJoinAlone parts, runs of kJoinRun are joined first,
+    // each by its last chunk, into the run's first part.
+    const int first = key_f0 / chunk, n_parts = (key_f0 + key_tiles - 1) / chunk - first + 1;
+    const int tail = key_f0 > static_cast<int64_t>(first) * chunk ? 1 : 0;
+    const int me = static_cast<int>(blockIdx.x) - first;
+    auto part_at = [&](int i) {
+      return p.partials + static_cast<size_t>(2 * (first + i) + (i == 0 ? tail : 0)) * NC * (D + 2);
+    };
+    // 32 NW / NC lanes share a column: each takes D / lanes channels, and looks
+    // after the (m, l) of every lanes-th part
+    auto join_parts = [&](int i0, int n, int step, bool store) {
+      constexpr int LC = 32 * NW / NC, CH = D / LC;
+      static_assert(LC <= 32 && CH % 4 == 0, "columns divide the warps");
+      const int n_col = tid / LC, sub = tid % LC;
       float top = -INFINITY;
-      for (int b = first; b <= last; ++b)
-        top = fmaxf(top, __ldcg(p.partials + static_cast<size_t>(2 * b + (b == first ? tail : 0)) * NC * (D + 2) + n));
+      for (int i = sub; i < n; i += LC) top = fmaxf(top, __ldcg(part_at(i0 + i * step) + n_col));
+#pragma unroll
+      for (int d = LC / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
       const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f, acc = 0.0f;
-      const int chn = tid;                                   // one channel per thread
-      for (int b = first; b <= last; ++b) {
-        const float* q = p.partials + static_cast<size_t>(2 * b + (b == first ? tail : 0)) * NC * (D + 2);
-        const float w = ex2(__ldcg(q + n) - base);
-        sum += w * __ldcg(q + NC + n);
-        if (chn < D) acc += w * __ldcg(q + 2 * NC + n * D + chn);
+      float sum = 0.0f, acc[CH];
+#pragma unroll
+      for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
+      for (int b = 0; b < n; b += LC) {
+        float w = 0.0f;
+        if (b + sub < n) {
+          const float* src = part_at(i0 + (b + sub) * step) + n_col;
+          w = ex2(__ldcg(src) - base);
+          sum += w * __ldcg(src + NC);
+        }
+        const int m = min(LC, n - b);
+#pragma unroll 8
+        for (int i = 0; i < m; ++i) {
+          const float wi = __shfl_sync(0xFFFFFFFFu, w, i, LC);
+          const float* src = part_at(i0 + (b + i) * step) + 2 * NC + n_col * D + sub * CH;
+#pragma unroll
+          for (int x = 0; x < CH; x += 4) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + x));
+            acc[x] += wi * y.x; acc[x + 1] += wi * y.y; acc[x + 2] += wi * y.z; acc[x + 3] += wi * y.w;
+          }
+        }
       }
-      const int col = g.c0 + n, iq = col / p.G;
-      const int64_t row = static_cast<int64_t>(g.q0 + iq) * p.Hq + meta.head * p.G + (col - iq * p.G);
-      if (chn < D) p.out[row * D + chn] = __float2bfloat16_rn(sum > 0.0f ? acc * __fdividef(v_gsa, sum) : 0.0f);
-      if (p.lse && tid == 0) p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+#pragma unroll
+      for (int d = LC / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if (n_col >= n_cols) return;
+      if (!store) {
+        float* dst = part_at(i0);
+        if (sub == 0) {
+          dst[n_col] = top;
+          dst[NC + n_col] = sum;
+        }
+#pragma unroll
+        for (int x = 0; x < CH; x += 4)
+          *reinterpret_cast<float4*>(dst + 2 * NC + n_col * D + sub * CH + x) =
+              make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
+        return;
+      }
+      const int dq = div_G(rem0 + n_col);
+      const int64_t row = static_cast<int64_t>(q0 + dq) * p.Hq + head * p.G + (rem0 + n_col - dq * p.G);
+      const float inv = sum > 0.0f ? __fdividef(v_gsa, sum) : 0.0f;
+#pragma unroll
+      for (int x = 0; x < CH; x += 2)
+        *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + sub * CH + x) =
+            __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
+      if (p.lse && sub == 0) p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+    };
+    // every consumer's stores so far, then the ticket; true for the last of `n`
+    bool failed = false;
+    auto last_of = [&](uint32_t* ticket, int n) {
+      __threadfence();
+      failed |= !sync_consumers();
+      if (tid == 0 && !failed) {
+        const bool all = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
+        if (all) *ticket = 0u;
+        *s_flag = all;
+      }
+      failed |= !sync_consumers();
+      const bool all = *s_flag;
+      __threadfence();
+      return all;
+    };
+    if (n_parts <= kJoinAlone) {
+      const bool all = last_of(p.tickets + 2 * first, n_parts);
+      if (failed) return give_up();
+      if (all) join_parts(0, n_parts, 1, true);
+    } else {
+      const int run = me / kJoinRun * kJoinRun, n_runs = (n_parts + kJoinRun - 1) / kJoinRun;
+      bool all = last_of(p.tickets + 2 * (first + run) + 1, min(kJoinRun, n_parts - run));
+      if (failed) return give_up();
+      if (all) {
+        join_parts(run, min(kJoinRun, n_parts - run), 1, false);
+        all = last_of(p.tickets + 2 * first, n_runs);
+        if (failed) return give_up();
+        if (all) join_parts(0, n_runs, kJoinRun, true);
+      }
     }
+    // s_flag is written again only after the next run's barriers
   }
 }
 
@@ -699,15 +891,15 @@ struct AttnWs {
 AttnWs attn_ws_layout(int D) {
   AttnWs L;
   L.tickets = 256;
-  L.partials = a256(L.tickets + kAttnMaxCtas * 4);
+  L.partials = a256(L.tickets + kAttnMaxCtas * 8);
   L.total = a256(L.partials + size_t(2) * kAttnMaxCols * (D + 2) * 4);
   return L;
 }
 
-template <int D, int NT, int NW, int STAGES, int MINB>
+template <int D, int NT, int NW, int MW, int STAGES, int MINB>
 nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
-  using Sh = AttnShape<D, NT, NW, STAGES>;
-  auto kernel = kv_attention_kernel<D, NT, NW, STAGES, MINB>;
+  using Sh = AttnShape<D, NT, NW, MW, STAGES>;
+  auto kernel = kv_attention_kernel<D, NT, NW, MW, STAGES, MINB>;
   static int per_sm[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
@@ -724,7 +916,7 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + Sh::kCols - 1) / Sh::kCols);
   // the flat order of tiles is counted in 32 bits
   const int64_t items = static_cast<int64_t>(p.B) * p.groups;
-  const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1);
+  const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1 + kKeyCost);
   if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
   int64_t grid = static_cast<int64_t>(sms) * per_sm[dev];
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
@@ -748,10 +940,10 @@ template <int D>
 nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   // columns of a pass: as few as hold a sequence's queries, 32 at most
   const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
-  if (cols <= 8) return launch_attn<D, 1, 4, 5, 3>(p, max_kv, s);
-  if (cols <= 16) return launch_attn<D, 2, 4, 5, 2>(p, max_kv, s);
-  if constexpr (D == 128) return launch_attn<D, 4, 8, 4, 1>(p, max_kv, s);
-  else return launch_attn<D, 4, 4, 5, 2>(p, max_kv, s);
+  if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3>(p, max_kv, s);
+  if (cols <= 16) return launch_attn<D, 2, 4, 2, 3, 2>(p, max_kv, s);
+  if constexpr (D == 128) return launch_attn<D, 4, 4, 2, 4, 1>(p, max_kv, s);
+  else return launch_attn<D, 4, 4, 2, 3, 2>(p, max_kv, s);
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
