@@ -25,92 +25,20 @@
 // cut by a chunk border leaves partials in the workspace and the last block to
 // arrive (ticket) joins them in chunk order, so results do not depend on timing.
 // One producer warp feeds a ring of tiles with bulk copies, a page of one KV head each.
-#include "kv_layout.cuh"
-#include "nvr_internal.h"
-#include "nvr_tcgen05.cuh"
+#include "kv_attention.cuh"
 #include "../../include/nvfp4_kv_cache.h"
 
 namespace nvr {
 
 namespace {
 
-constexpr int kAttnMaxCtas = 2048;         // blocks; two ticket words each in the workspace
+constexpr int kStreamCols = 16;            // more columns of a sequence go to the tensor-memory kernel
 constexpr int kJoinAlone = 40;             // parts of a key that one block joins at once
 constexpr int kJoinRun = 16;               // beyond that, the parts joined first
-constexpr int kAttnMaxCols = 16384;        // column slots of partials: blocks * columns, per side
-constexpr float kRescaleAt = 8.0f;
 // Starting and ending a key costs a block about as much as this many tiles
 // (queries, joining the warps, storing): counted in the chunks, so that blocks
 // with many short keys get fewer tiles.
 constexpr int kKeyCost = 1;
-
-struct AttnParams {
-  const __nv_bfloat16* q;
-  int64_t q_stride;
-  int64_t T;
-  int Hq, Hkv, G;
-  const uint8_t* cache;
-  int64_t n_pages;
-  int page_shift;
-  const int32_t* page_table;
-  int B, max_pages;
-  const int32_t* kv_lens;
-  const int32_t* cu_q;
-  int max_q;
-  const float *k_gsa, *v_gsa;
-  float scale_log2;           // scale * log2(e)
-  int causal, window;
-  int groups;                 // column groups per sequence
-  __nv_bfloat16* out;
-  float* lse;
-  uint32_t* status;
-  uint32_t* tickets;
-  float* partials;            // [2 * blocks][NC][D + 2]: m, l, O
-  int min_chunk;              // fewest tiles of a block
-};
-
-// What the queries and the tokens of a column group are.
-struct Group {
-  int b, q0, n_q, kv;         // sequence, its first query row, its queries, its tokens
-  int c0, n_cols;             // first column, columns of the group (0: none)
-  int lo, hi;                 // tokens any of the columns sees: [lo, hi)
-  int tile0, tiles;
-};
-
-template <int NC, int TILE>
-__device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
-  Group g;
-  g.b = item / p.groups;
-  const int cg = item - g.b * p.groups;
-  g.kv = min(max(__ldg(p.kv_lens + g.b), 0), p.max_pages << p.page_shift);
-  if (p.cu_q) {
-    const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
-    const int64_t e = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b + 1)), a), p.T);
-    g.q0 = static_cast<int>(a);
-    g.n_q = static_cast<int>(min(e - a, static_cast<int64_t>(p.max_q)));
-  } else {
-    g.q0 = g.b * p.max_q;
-    g.n_q = p.max_q;
-  }
-  g.c0 = cg * NC;
-  g.n_cols = min(g.n_q * p.G - g.c0, NC);
-  if (g.n_cols <= 0) {
-    g.n_cols = 0;
-    g.lo = g.hi = g.tile0 = g.tiles = 0;
-    return g;
-  }
-  g.lo = 0;
-  g.hi = g.kv;
-  if (p.causal) {
-    const int first = g.kv - g.n_q + g.c0 / p.G;                       // position of the first column's query
-    const int last = g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G;
-    g.hi = max(last + 1, 0);
-    if (p.window > 0) g.lo = min(max(first + 1 - p.window, 0), g.hi);
-  }
-  g.tile0 = g.lo / TILE;
-  g.tiles = max((g.hi + TILE - 1) / TILE - g.tile0, 1);                // a group that sees nothing still writes its rows
-  return g;
-}
 
 // A key's length in the flat order: its tiles, then kKeyCost places without work.
 __device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kKeyCost : 0; }
@@ -127,24 +55,6 @@ struct alignas(16) Meta {
   int pad[2];
 };
 constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4;
-
-// Waits for a phase of the barrier, one second at most.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, globaltimer_ns() + 1000000000ull, abort_flag);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -398,10 +308,8 @@ kv_attention_kernel(const AttnParams p) {
       *abort_flag = 1;
     }
   };
-  // small numerators only: exact in fp32 (the quotient's distance from an
-  // integer is at least 1 / (2 G), far above the rounding of a product below 2^18)
   const float inv_G = 1.0f / static_cast<float>(p.G);
-  auto div_G = [&](int x) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_G); };
+  auto div_G = [&](int x) { return div_small(x, inv_G); };
   uint32_t joined = 1;
   int st = 0;
   uint32_t parity = 0;
@@ -415,9 +323,7 @@ kv_attention_kernel(const AttnParams p) {
       const float k_gsa = meta.k_gsa;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        // column 8 nt + r: its query row, scaled by a power of two into the
-        // upper range of fp16 (bf16 has fewer significant bits: exact, but for
-        // channels 2^28 below the row's largest, which lose their last bits)
+        // column 8 nt + r: its query row in fp16
         const bool on = 8 * nt + r < n_cols;
         const uint8_t* src = s_raw + (st * NC + 8 * nt + r) * D * 2 + c * (D / 2);
         uint32_t w[D / 8];
@@ -431,11 +337,9 @@ kv_attention_kernel(const AttnParams p) {
         for (int i = 0; i < D / 8; ++i) big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
         big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
         big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-        // up = 2^(14 - exponent of the largest): both it and its inverse are
-        // normal fp32 numbers for the biased exponents 16..254
-        const int e = min(max(static_cast<int>(big >> 7), 16), 254);
-        const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-        const float down = p.scale_log2 * k_gsa * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        float up, down;
+        query_scale(big, up, down);
+        down *= p.scale_log2 * k_gsa;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t b[2];
@@ -891,8 +795,8 @@ struct AttnWs {
 AttnWs attn_ws_layout(int D) {
   AttnWs L;
   L.tickets = 256;
-  L.partials = a256(L.tickets + kAttnMaxCtas * 8);
-  L.total = a256(L.partials + size_t(2) * kAttnMaxCols * (D + 2) * 4);
+  L.partials = a256(L.tickets + kAttnMaxCtas * 16);
+  L.total = a256(L.partials + size_t(2) * kPrefillMaxCtas * kPrefillCols * (D + 2) * 4);
   return L;
 }
 
@@ -975,7 +879,9 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
     return NVR_ERR_INVALID_ARG;
   if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (q_stride < static_cast<int64_t>(Hq) * D || q_stride % 8)) return NVR_ERR_INVALID_ARG;
-  if (T > INT32_MAX || B > INT32_MAX || max_pages * page_size > INT32_MAX) return NVR_ERR_UNSUPPORTED;
+  if (T > INT32_MAX || B > INT32_MAX || max_pages * page_size > INT32_MAX - 1024 ||
+      static_cast<int64_t>(max_q) * (Hq / Hkv) > INT32_MAX - 1024)
+    return NVR_ERR_UNSUPPORTED;
   if (off16(q) || off16(cache) || off16(out) || off4(page_table) || off4(kv_lens) || off4(cu_q) || off4(k_gsa) ||
       off4(v_gsa) || off4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return NVR_ERR_ALIGNMENT;
@@ -999,5 +905,6 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   p.partials = reinterpret_cast<float*>(w + L.partials);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int max_kv = static_cast<int>(max_pages) * page_size;
+  if (static_cast<int64_t>(max_q) * p.G > kStreamCols) return launch_kv_prefill(p, D, max_kv, s);
   return D == 128 ? dispatch_attn<128>(p, max_kv, s) : dispatch_attn<64>(p, max_kv, s);
 }

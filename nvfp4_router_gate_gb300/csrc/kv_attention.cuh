@@ -1,0 +1,129 @@
+// kv_attention.cuh -- what the two attention kernels over the NVFP4 key/value
+// cache share: parameters, the rows and tokens of a column group, and small
+// device functions (sm_103a).
+#pragma once
+
+#include "kv_layout.cuh"
+#include "nvr_internal.h"
+#include "nvr_tcgen05.cuh"
+
+namespace nvr {
+
+// The running maximum of a row moves when a score passes it by this much (base
+// 2): the softmax weights stay below 2^8, inside fp16.
+constexpr float kRescaleAt = 8.0f;
+
+struct AttnParams {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int64_t T;
+  int Hq, Hkv, G;
+  const uint8_t* cache;
+  int64_t n_pages;
+  int page_shift;
+  const int32_t* page_table;
+  int B, max_pages;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  int max_q;
+  const float *k_gsa, *v_gsa;
+  float scale_log2;           // scale * log2(e)
+  int causal, window;
+  int groups;                 // column groups per sequence
+  __nv_bfloat16* out;
+  float* lse;
+  uint32_t* status;
+  uint32_t* tickets;
+  float* partials;            // [2 * blocks][NC][D + 2]: m, l, O
+  int min_chunk;              // fewest tiles of a block
+};
+
+// What the queries and the tokens of a column group are.
+struct Group {
+  int b, q0, n_q, kv;         // sequence, its first query row, its queries, its tokens
+  int c0, n_cols;             // first column, columns of the group (0: none)
+  int lo, hi;                 // tokens any of the columns sees: [lo, hi)
+  int tile0, tiles;
+};
+
+template <int NC, int TILE>
+__device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
+  Group g;
+  g.b = item / p.groups;
+  const int cg = item - g.b * p.groups;
+  g.kv = min(max(__ldg(p.kv_lens + g.b), 0), p.max_pages << p.page_shift);
+  if (p.cu_q) {
+    const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
+    const int64_t e = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b + 1)), a), p.T);
+    g.q0 = static_cast<int>(a);
+    g.n_q = static_cast<int>(min(e - a, static_cast<int64_t>(p.max_q)));
+  } else {
+    g.q0 = g.b * p.max_q;
+    g.n_q = p.max_q;
+  }
+  g.c0 = cg * NC;
+  g.n_cols = min(g.n_q * p.G - g.c0, NC);
+  if (g.n_cols <= 0) {
+    g.n_cols = 0;
+    g.lo = g.hi = g.tile0 = g.tiles = 0;
+    return g;
+  }
+  g.lo = 0;
+  g.hi = g.kv;
+  if (p.causal) {
+    const int first = g.kv - g.n_q + g.c0 / p.G;                       // position of the first column's query
+    const int last = g.kv - g.n_q + (g.c0 + g.n_cols - 1) / p.G;
+    g.hi = max(last + 1, 0);
+    if (p.window > 0) g.lo = min(max(first + 1 - p.window, 0), g.hi);
+  }
+  g.tile0 = g.lo / TILE;
+  g.tiles = max((g.hi + TILE - 1) / TILE - g.tile0, 1);                // a group that sees nothing still writes its rows
+  return g;
+}
+
+// Waits for a phase of the barrier, one second at most.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, globaltimer_ns() + 1000000000ull, abort_flag);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// x / G for the small numerators of a group (below 2^17, G at most 2^16):
+// exact in fp32, the quotient's distance from an integer is at least 1 / (2 G).
+__device__ __forceinline__ int div_small(int x, float inv_G) {
+  return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_G);
+}
+
+// 2^(14 - exponent of the largest magnitude) brings a row of bf16 queries into
+// the upper range of fp16 (fewer significant bits: exact, but for channels 2^28
+// below the largest, which lose their last bits).  `big`: the largest magnitude's
+// bf16 bits; up and its inverse are normal fp32 numbers.
+__device__ __forceinline__ void query_scale(uint32_t big, float& up, float& down) {
+  const int e = min(max(static_cast<int>(big >> 7), 16), 254);
+  up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+  down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+}
+
+// Workspace of an attention call (csrc/kv_attention.cu): control words, two
+// ticket words for every block and column half, the partial results.
+constexpr int kAttnMaxCtas = 2048;
+constexpr int kPrefillMaxCtas = 160;       // blocks of the tensor-memory kernel
+constexpr int kPrefillCols = 256;          // its columns
+constexpr int kAttnMaxCols = 16384;        // columns * blocks of the streaming kernel at most
+static_assert(kPrefillMaxCtas * kPrefillCols >= kAttnMaxCols, "the partials hold either kernel's");
+
+// The tensor-memory kernel (csrc/kv_prefill.cu).
+nvr_status launch_kv_prefill(AttnParams& p, int D, int max_kv, cudaStream_t s);
+
+}  // namespace nvr

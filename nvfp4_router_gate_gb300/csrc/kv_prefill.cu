@@ -1,0 +1,896 @@
+// kv_prefill.cu -- softmax attention over the paged NVFP4 key/value cache for
+// many (query, head) columns (sm_103a): prompt chunks, drafts of many tokens.
+// Bound by the tensor cores: 4 D multiply-adds' worth of flops for every column
+// and token against 9/8 D bytes of cache read once for 256 columns.
+//
+// Mathematics: as csrc/kv_attention.cu (running maximum moved in steps, fp32
+// sums, fp16 weights).  Here S = Q K^T and O += P V run on tcgen05 with the
+// columns as the 128 rows of an accumulator in tensor memory: a thread owns a
+// row, so that its maximum and sum need no exchange.
+//
+// A block (one per SM) takes 256 columns of a sequence that share a KV head as
+// two row tiles and walks the tokens in tiles of 128:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: read S from tensor memory,
+//                   write P (fp16) over it, rescale O when the maximum moves,
+//                   store the rows at the end of a key;
+//   warps 8-11      expand the cache: codes and scales from the pages to
+//                   registers one tile ahead, code * scale (exact in fp16) into
+//                   swizzled shared memory, two stages of K and of V;
+//   warp 12         issues the products, alternating the row tiles, so that one
+//                   tile's softmax runs under the other's products;
+//   warp 13         walks the work and hands every role its runs.
+// A group of at most 128 columns uses both halves as well: the same rows in
+// both, each taking every other token tile, joined at the end.
+//
+// Tensor memory, 512 columns: S0 | S1 (128 each, P over the first half of its
+// S), O0 | O1 (D each).  S of the next tile follows P V of this one in issue
+// order, so S is never overwritten early and a complete S implies the earlier
+// P V complete.
+//
+// The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
+// equal chunks, one per block, partial rows joined by the last block to arrive.
+#include "kv_attention.cuh"
+
+namespace nvr {
+
+namespace {
+
+constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
+constexpr int kPThreads = 512;
+constexpr int kPKeyUnits = 2;              // cost of starting and ending a key, in single tiles
+constexpr int kPJoinAlone = 24;            // parts joined at once (the weights' table lies in a query tile)
+constexpr int kPJoinRun = 16;              // beyond that, joined first
+constexpr int kRuns = 3;                   // runs handed out ahead
+constexpr int kLive = 4;
+
+// A key's stretch of tiles in this block's chunk.
+struct alignas(16) Run {
+  int tiles;                               // -1: the end
+  int tile0, b, head;
+  int kv, n_q, q0, n_cols;
+  int iq0, rem0, lo, hi;
+  int dual;                                // both halves on different rows (else on alternate tiles)
+  int first, n_parts, tail;                // the key's first chunk, its chunks, whether it starts inside it
+  float k_gsa, v_gsa;
+  int pad[2];
+};
+
+template <int D>
+struct PrefillSmem {
+  static constexpr int kTileBytes = kPTile * D * 2;          // fp16 rows in 128-byte swizzled atoms of 64 channels
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTileBytes;
+  static constexpr int kV = kK + 2 * kTileBytes;
+  static constexpr int kRunsAt = kV + 2 * kTileBytes;
+  static constexpr int kRowAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));   // per row: m, l of half 1; 1 / l of both
+  static constexpr int kBarAt = kRowAt + 4 * kPTile * 4;
+  static constexpr int kTotal = kBarAt + 40 * 8 + 64 + 1024;
+};
+
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  // D fp32 (1 in bits 4-5), A and B fp16 (0), B transposed in bit 16, N >> 3 in
+  // bits 17-22, M >> 4 in bits 24-28
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] . B[smem], fp16 operands.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// The same with A in tensor memory (two fp16 of a row to a column).
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
+    tmem_store16(taddr + 16 * h, r);
+  }
+}
+
+// Chunks of the flat order: a tile costs one unit, two when both halves work
+// on different rows of it.
+__device__ __forceinline__ int tile_units(const Group& g) { return g.n_cols > kPTile ? 2 : 1; }
+__device__ __forceinline__ int key_units(const Group& g) {
+  return g.tiles ? g.tiles * tile_units(g) + kPKeyUnits : 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+kv_prefill_kernel(const AttnParams p) {
+  using Sm = PrefillSmem<D>;
+  constexpr int NC = kPrefillCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Run* s_runs = reinterpret_cast<Run*>(smem + Sm::kRunsAt);
+  float* s_row = reinterpret_cast<float*>(smem + Sm::kRowAt);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBarAt);
+  uint64_t *run_full = bars, *run_empty = run_full + kRuns, *k_full = run_empty + kRuns, *k_empty = k_full + 2,
+           *v_full = k_empty + 2, *v_empty = v_full + 2, *q_full = v_empty + 2, *s_full = q_full + 2,
+           *p_full = s_full + 2, *o_full = p_full + 2, *meet = o_full + 2, *x_ready = meet + 2, *x_full = x_ready + 1,
+           *x_free = x_full + 1, *drained = x_free + 1;
+  int* s_words = reinterpret_cast<int*>(drained + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
+  volatile int* abort_flag = s_words + 1;
+  int* s_start = s_words + 2;                                // item, offset inside it
+  int* s_flag = s_words + 4;                                 // per half: the last block to arrive
+  volatile uint32_t* s_live = reinterpret_cast<volatile uint32_t*>(s_words + 6);   // [kLive] tokens in groups of 16
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, 13); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 4); mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
+      mbar_init(q_full + i, 4); mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4); mbar_init(o_full + i, 1);
+      mbar_init(meet + i, 4);
+    }
+    mbar_init(x_ready, 4); mbar_init(x_full, 4); mbar_init(x_free, 4); mbar_init(drained, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < kLive; ++i) s_live[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc(tmem_holder, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- this block's chunk of the flat order
+  const int n_items = p.B * p.groups;
+  const int per = (n_items + kPThreads - 1) / kPThreads;
+  int mine = 0;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_units(group_of<NC, kPTile>(p, i)) * p.Hkv;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += a;
+  }
+  if (lane == 31) reinterpret_cast<int*>(s_row)[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = 0, total = 0;
+  for (int w = 0; w < kPThreads / 32; ++w) {
+    const int x = reinterpret_cast<int*>(s_row)[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
+  const int f0 = min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total));
+  const int f1 = min(f0 + chunk, total);
+  const int excl = before + incl - mine;
+  if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
+    int at = excl, i = tid * per;
+    for (;; ++i) {
+      const int n = key_units(group_of<NC, kPTile>(p, i)) * p.Hkv;
+      if (f0 < at + n) break;
+      at += n;
+    }
+    s_start[0] = i;
+    s_start[1] = f0 - at;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_holder;
+
+  auto give_up = [&]() {
+    if (lane == 0) {
+      report_timeout(p.status);
+      *abort_flag = 1;
+    }
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag)) != 0;
+  };
+
+  if (f0 < f1) {
+    if (warp == 13) {
+      // ------------------------------------------------------------ the walk
+      int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
+      bool ok = true;
+      auto hand_out = [&](const Run& r) {
+        const int s = n_run % kRuns;
+        if (!wait_all(run_empty + s, ((n_run / kRuns) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          s_runs[s] = r;
+          mbar_arrive(run_full + s);
+        }
+        __syncwarp();
+        ++n_run;
+        return true;
+      };
+      Group next = group_of<NC, kPTile>(p, item);
+      while (f < f1 && ok) {
+        const Group g = next;
+        if (item + 1 < n_items) next = group_of<NC, kPTile>(p, item + 1);
+        const int cost = key_units(g), u = tile_units(g);
+        while (off < cost * p.Hkv && f < f1 && ok) {
+          const int head = off / cost, at = off - head * cost;
+          const int key_f0 = f - at, end = min(f1, key_f0 + cost);
+          // tiles that start inside [f, end)
+          const int ta = min((at + u - 1) / u, g.tiles), tb = min((end - key_f0 + u - 1) / u, g.tiles);
+          if (ta < tb) {
+            Run r = {};
+            r.tiles = tb - ta;
+            r.tile0 = g.tile0 + ta; r.b = g.b; r.head = head;
+            r.kv = g.kv; r.n_q = g.n_q; r.q0 = g.q0; r.n_cols = g.n_cols;
+            r.iq0 = g.c0 / p.G; r.rem0 = g.c0 - r.iq0 * p.G; r.lo = g.lo; r.hi = g.hi;
+            r.dual = u == 2;
+            r.first = key_f0 / chunk;
+            r.n_parts = (key_f0 + u * (g.tiles - 1)) / chunk - r.first + 1;
+            r.tail = key_f0 > static_cast<int64_t>(r.first) * chunk;
+            r.k_gsa = __ldg(p.k_gsa + head);
+            r.v_gsa = __ldg(p.v_gsa + head);
+            ok = hand_out(r);
+          }
+          off += end - f;
+          f = end;
+        }
+        off = 0;
+        ++item;
+      }
+      if (ok) {
+        Run r = {};
+        r.tiles = -1;
+        ok = hand_out(r);
+      }
+      if (!ok) give_up();
+    } else if (warp < 13) {
+      int n_run = 0;
+      Run run;
+      // the next run, or false (with run.tiles == -1 at the end)
+      auto take = [&]() {
+        const int s = n_run % kRuns;
+        if (!wait_all(run_full + s, (n_run / kRuns) & 1)) return false;
+        run = s_runs[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(run_empty + s);
+        ++n_run;
+        return true;
+      };
+      if (warp == 12) {
+        // -------------------------------------------------------- the products
+        const uint32_t id_s = idesc_f16(128, kPTile, false), id_o = idesc_f16(128, D, true);
+        int tk = 0, tv = 0;                                  // tiles of K and V taken
+        uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+        auto products = [&]() -> bool {
+          auto score = [&](int w, int stage) {
+            if (elect_one()) {
+              const uint32_t q = smem_u32(smem + Sm::kQ + w * Sm::kTileBytes);
+              const uint32_t k = smem_u32(smem + Sm::kK + stage * Sm::kTileBytes);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t o = (i / 4) * (kPTile * 128) + (i % 4) * 32;
+                tc_mma_f16(tmem + w * kPTile, desc_kmajor_sw128(q + o), desc_kmajor_sw128(k + o), id_s, i != 0);
+              }
+            }
+            __syncwarp();
+          };
+          auto weigh = [&](int w, int stage, bool add) {
+            if (elect_one()) {
+              const uint32_t v = smem_u32(smem + Sm::kV + stage * Sm::kTileBytes);
+#pragma unroll
+              for (int i = 0; i < kPTile / 16; ++i)
+                // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
+                tc_mma_f16_ta(tmem + 2 * kPTile + w * D, tmem + w * kPTile + 8 * i,
+                              smem_desc(v + i * 2048, kPTile * 128, 1024, 2), id_o, add || i != 0);
+            }
+            __syncwarp();
+          };
+          auto commit = [&](uint64_t* bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+          };
+          auto have = [&](uint64_t* bar, uint32_t parity) {
+            const bool ok = wait_all(bar, parity);
+            tc_fence_after();
+            return ok;
+          };
+          for (;;) {
+            if (!take()) return false;
+            const int n = run.tiles;
+            if (n < 0) return true;
+            const int k0 = tk, v0 = tv;
+            tk += n;
+            tv += n;
+            auto k_ready = [&](int j) { return have(k_full + (k0 + j) % 2, ((k0 + j) / 2) & 1); };
+            auto v_ready = [&](int j) { return have(v_full + (v0 + j) % 2, ((v0 + j) / 2) & 1); };
+            auto q_ready = [&](int w) { const bool ok = have(q_full + w, ph_q[w]); ph_q[w] ^= 1u; return ok; };
+            auto p_ready = [&](int w) { const bool ok = have(p_full + w, ph_p[w]); ph_p[w] ^= 1u; return ok; };
+            if (run.dual) {
+              if (!q_ready(0) || !k_ready(0)) return false;
+              score(0, k0 % 2);
+              commit(s_full);
+              if (!q_ready(1)) return false;
+              score(1, k0 % 2);
+              commit(s_full + 1);
+              commit(k_empty + k0 % 2);
+              for (int j = 0; j < n; ++j) {
+                if (!v_ready(j) || !p_ready(0)) return false;
+                weigh(0, (v0 + j) % 2, j > 0);
+                if (j + 1 < n) {
+                  if (!k_ready(j + 1)) return false;
+                  score(0, (k0 + j + 1) % 2);
+                  commit(s_full);
+                } else {
+                  commit(o_full);
+                }
+                if (!p_ready(1)) return false;
+                weigh(1, (v0 + j) % 2, j > 0);
+                commit(v_empty + (v0 + j) % 2);
+                if (j + 1 < n) {
+                  score(1, (k0 + j + 1) % 2);
+                  commit(s_full + 1);
+                  commit(k_empty + (k0 + j + 1) % 2);
+                } else {
+                  commit(o_full + 1);
+                }
+              }
+            } else {
+              for (int j = 0; j < min(n, 2); ++j) {
+                if (!q_ready(j) || !k_ready(j)) return false;
+                score(j, (k0 + j) % 2);
+                commit(s_full + j);
+                commit(k_empty + (k0 + j) % 2);
+              }
+              for (int j = 0; j < n; ++j) {
+                const int w = j & 1;
+                if (!v_ready(j) || !p_ready(w)) return false;
+                weigh(w, (v0 + j) % 2, j > 1);
+                commit(v_empty + (v0 + j) % 2);
+                if (j + 2 < n) {
+                  if (!k_ready(j + 2)) return false;
+                  score(w, (k0 + j + 2) % 2);
+                  commit(s_full + w);
+                  commit(k_empty + (k0 + j + 2) % 2);
+                } else {
+                  commit(o_full + w);
+                }
+              }
+            }
+          }
+        };
+        if (!products()) give_up();
+        // nothing of this block's is under way when the tensor memory goes back
+        if (elect_one()) tc_commit(drained);
+        __syncwarp();
+        wait_all(drained, 0);
+      } else if (warp >= 8) {
+        // ---------------------------------------------------- expanding the cache
+        const int w = warp - 8, tok = lane & 7, qd = lane >> 3;
+        const int S = 1 << p.page_shift;
+        int n_tile = 0;                                      // tiles expanded
+        constexpr int BL = D / 64;                           // blocks of 16 channels a lane takes of a token
+        auto expand = [&]() -> bool {
+          for (;;) {
+            if (!take()) return false;
+            if (run.tiles < 0) return true;
+            const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
+            uint2 kc[4][BL], vc[4][BL];
+            uint32_t ks[4], vs[4];
+            const uint8_t* base[4];                          // the pages of this warp's groups of eight tokens, or null
+            int at = -1, entries = -1;
+            auto find = [&](int tile) {
+              const int x = (tile * kPTile) >> p.page_shift; // the tile's first page
+              if ((x & ~31) != at) {
+                at = x & ~31;
+                entries = at + lane < p.max_pages ? __ldg(table + at + lane) : -1;
+              }
+              uint32_t live = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = tile * kPTile + 32 * w + 8 * i;
+                const int page = __shfl_sync(0xFFFFFFFFu, entries, (t >> p.page_shift) - at);
+                const bool ok = t < run.hi && t + 8 > run.lo && page >= 0 && page < p.n_pages;
+                base[i] = ok ? p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S) : nullptr;
+                if (page >= 0 && page < p.n_pages) live |= 1u << (i / 2);
+              }
+              return live;
+            };
+            auto load_k = [&](int tile) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = tile * kPTile + 32 * w + 8 * i + tok, o = t & (S - 1);
+                ks[i] = 0;
+#pragma unroll
+                for (int x = 0; x < BL; ++x) kc[i][x] = make_uint2(0u, 0u);
+                if (base[i] && t < run.kv) {
+                  const uint8_t* c = base[i] + o * (D / 2) + qd * (8 * BL);
+                  const uint8_t* s = base[i] + KvPage<D>::key_scales(S) + o * (D / 16) + qd * BL;
+                  if (BL == 2) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(c));
+                    kc[i][0] = make_uint2(u.x, u.y);
+                    kc[i][BL - 1] = make_uint2(u.z, u.w);
+                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
+                  } else {
+                    kc[i][0] = __ldg(reinterpret_cast<const uint2*>(c));
+                    ks[i] = __ldg(s);
+                  }
+                }
+              }
+            };
+            auto load_v = [&](int tile) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = tile * kPTile + 32 * w + 8 * i + tok, o = t & (S - 1);
+                vs[i] = 0;
+#pragma unroll
+                for (int x = 0; x < BL; ++x) {
+                  vc[i][x] = make_uint2(0u, 0u);
+                  if (base[i] && t < run.kv) {
+                    vc[i][x] = __ldg(reinterpret_cast<const uint2*>(
+                        base[i] + KvPage<D>::value_codes(S) + KvPage<D>::value_code(o, qd * BL + x)));
+                    vs[i] |= static_cast<uint32_t>(__ldg(base[i] + KvPage<D>::value_scales(S) +
+                                                         KvPage<D>::value_scale(o, qd * BL + x)))
+                             << (8 * x);
+                  }
+                }
+              }
+            };
+            auto put = [&](uint8_t* tile, const uint2 (&c)[4][BL], const uint32_t (&s)[4]) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = 32 * w + 8 * i + tok;
+                const uint32_t s2 = e4m3x2_to_f16(s[i]);
+#pragma unroll
+                for (int x = 0; x < BL; ++x) {
+                  const uint32_t sb = __byte_perm(s2, 0, x == 0 ? 0x1010 : 0x3232);
+                  uint32_t a[8];
+                  e2m1x8_to_f16(c[i][x].x, a[0], a[1], a[2], a[3]);
+                  e2m1x8_to_f16(c[i][x].y, a[4], a[5], a[6], a[7]);
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) a[y] = h2_mul(a[y], sb);
+                  const int blk = qd * BL + x;               // channels 16 blk ..
+                  uint8_t* row = tile + (blk / 4) * (kPTile * 128) + t * 128;
+                  const int ch = 2 * (blk % 4);
+                  *reinterpret_cast<uint4*>(row + ((ch ^ tok) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                  *reinterpret_cast<uint4*>(row + (((ch + 1) ^ tok) << 4)) = make_uint4(a[4], a[5], a[6], a[7]);
+                }
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            };
+            uint32_t live = find(run.tile0);
+            load_k(run.tile0);
+            load_v(run.tile0);
+            for (int j = 0; j < run.tiles; ++j, ++n_tile) {
+              const int st = n_tile % 2;
+              const uint32_t ph = ((n_tile / 2) & 1) ^ 1;
+              if (!wait_all(k_empty + st, ph)) return false;
+              put(smem + Sm::kK + st * Sm::kTileBytes, kc, ks);
+              // this warp's byte of the word: its two groups of 16 tokens
+              if (lane == 0) {
+                reinterpret_cast<volatile uint8_t*>(s_live + n_tile % kLive)[w] = static_cast<uint8_t>(live);
+                mbar_arrive(k_full + st);
+              }
+              const int more = run.tile0 + j + 1;
+              uint32_t live_next = 0;
+              if (j + 1 < run.tiles) {
+                live_next = find(more);
+                load_k(more);
+              }
+              if (!wait_all(v_empty + st, ph)) return false;
+              put(smem + Sm::kV + st * Sm::kTileBytes, vc, vs);
+              if (lane == 0) mbar_arrive(v_full + st);
+              if (j + 1 < run.tiles) load_v(more);
+              live = live_next;
+            }
+          }
+        };
+        if (!expand()) give_up();
+      } else {
+        // ------------------------------------------------------------- softmax
+        const int w = warp >> 2, wl = warp & 3, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+        const uint32_t t_s = tmem + lanes + w * kPTile, t_o = tmem + lanes + 2 * kPTile + w * D;
+        const float inv_G = 1.0f / static_cast<float>(p.G);
+        uint32_t ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
+        int n_tile = 0;                                      // tiles before the run
+        auto sync_half = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(meet + w);
+          const bool ok = wait_all(meet + w, ph_meet);
+          ph_meet ^= 1u;
+          return ok;
+        };
+        auto softmax = [&]() -> bool {
+          for (;;) {
+            if (!take()) return false;
+            if (run.tiles < 0) return true;
+            const int n_my = run.dual ? run.tiles : (run.tiles + 1 - w) / 2;
+            const int col = run.dual ? w * kPTile + row : row;
+            const bool on = col < run.n_cols;
+            const int dq = div_small(run.rem0 + (on ? col : 0), inv_G);
+            const int pos = run.kv - run.n_q + run.iq0 + dq;
+            const int hq = run.head * p.G + run.rem0 + (on ? col : 0) - dq * p.G;
+            const int64_t q_row = run.q0 + run.iq0 + dq;
+            const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
+            const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+            float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
+            if (n_my > 0) {
+              // the row's query in fp16, scaled into its range, into the swizzled tile
+              const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row * p.q_stride + static_cast<int64_t>(hq) * D);
+              uint4 u[D / 8];
+              uint32_t big = 0;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                u[i] = on ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) big = max(big, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+              }
+              float up, down;
+              query_scale(big, up, down);
+              to_log2 = down * (p.scale_log2 * run.k_gsa);
+              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes + row * 128;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+                *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + (((i % 8) ^ (row & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(q_full + w);
+            }
+            for (int i = 0; i < n_my; ++i) {
+              const int j = run.dual ? i : 2 * i + w;
+              const int t0 = (run.tile0 + j) * kPTile;
+              if (!wait_all(s_full + w, ph_s)) return false;
+              ph_s ^= 1u;
+              tc_fence_after();
+              const uint32_t bytes = s_live[(n_tile + j) % kLive];
+              // bit i: tokens 16 i .. of the tile are in the cache
+              const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
+              const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
+              uint32_t pr[kPTile / 2];
+              float high, sum;
+              auto visible = [&](int c) { return t0 + c < hi && t0 + c >= lo && ((live >> (c / 16)) & 1u); };
+              auto weights = [&]() {
+                high = -INFINITY;
+                uint64_t sum2 = f2_pack(0.0f, 0.0f);
+                const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
+#pragma unroll
+                for (int c = 0; c < kPTile; c += 32) {
+                  float s[32];
+                  tmem_load32(t_s + c, s);
+                  if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                      const float v = fmaf(s[x], to_log2, m_neg);
+                      s[x] = visible(c + x) ? v : -INFINITY;
+                    }
+                  } else {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                      const uint64_t v = f2_fma(f2_pack(s[x], s[x + 1]), k2, m2);
+                      s[x] = f2_lo(v);
+                      s[x + 1] = f2_hi(v);
+                    }
+                  }
+#pragma unroll
+                  for (int x = 0; x < 32; x += 2) {
+                    high = fmaxf(high, fmaxf(s[x], s[x + 1]));
+                    const float a = ex2(s[x]), b = ex2(s[x + 1]);
+                    sum2 = f2_add(sum2, f2_pack(a, b));
+                    pr[(c + x) / 2] = pack_f16(a, b);
+                  }
+                }
+                sum = f2_lo(sum2) + f2_hi(sum2);
+              };
+              weights();
+              if (__any_sync(0xFFFFFFFFu, high > kRescaleAt)) {
+                // move the maximum to the largest score so far
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kPTile; c += 32) {
+                  float s[32];
+                  tmem_load32(t_s + c, s);
+#pragma unroll
+                  for (int x = 0; x < 32; ++x)
+                    if (!masked || visible(c + x)) top = fmaxf(top, s[x] * to_log2);
+                }
+                const float now = fminf(m_neg, -top);
+                const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                m_neg = now;
+                l *= shrink;
+                if (i > 0) {
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_load32(t_o + c, o);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] *= shrink;
+                    tmem_store32(t_o + c, o);
+                  }
+                }
+                weights();
+              }
+              l += sum;
+#pragma unroll
+              for (int c = 0; c < kPTile / 2; c += 16) {
+                uint32_t x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+                tmem_store16(t_s + c, x);
+              }
+              tmem_store_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_full + w);
+            }
+            n_tile += run.tiles;
+            if (n_my > 0) {
+              if (!wait_all(o_full + w, ph_o)) return false;
+              ph_o ^= 1u;
+              tc_fence_after();
+            }
+            float m = -m_neg;
+            // ---- both halves on one set of rows: half 1 hands its rows over
+            const bool cross = !run.dual && run.tiles > 1;
+            float keep = 1.0f, other = 0.0f;
+            float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + row * D;   // the query tiles, now free
+            if (cross) {
+              if (w == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_ready);         // (its scores are done with the queries)
+                if (!wait_all(x_full, ph_x)) return false;
+                const float m1 = s_row[row], l1 = s_row[kPTile + row];
+                const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
+                keep = ex2(m - base);
+                other = ex2(m1 - base);
+                l = l * keep + l1 * other;
+                m = top;
+              } else {
+                if (!wait_all(x_ready, ph_x)) return false;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  float o[32];
+                  tmem_load32(t_o + c, o);
+#pragma unroll
+                  for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
+                        make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                }
+                s_row[row] = m;
+                s_row[kPTile + row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_full);
+                if (!wait_all(x_free, ph_x)) return false;
+              }
+              ph_x ^= 1u;
+            }
+            if (!run.dual && w == 1) {
+              tc_fence_before();
+              continue;
+            }
+            const bool whole = run.n_parts == 1;
+            auto part_at = [&](int i) {
+              return p.partials + static_cast<size_t>(2 * (run.first + i) + (i == 0 ? run.tail : 0)) * NC * (D + 2);
+            };
+            const int me = static_cast<int>(blockIdx.x) - run.first;
+            float* part = part_at(me);
+            const int64_t out_row = q_row * p.Hq + hq;
+            const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_load32(t_o + c, o);
+              if (cross) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4) {
+                  const float4 y = *reinterpret_cast<const float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4));
+                  o[x] = o[x] * keep + y.x * other;
+                  o[x + 1] = o[x + 1] * keep + y.y * other;
+                  o[x + 2] = o[x + 2] * keep + y.z * other;
+                  o[x + 3] = o[x + 3] * keep + y.w * other;
+                }
+              }
+              if (on && whole) {
+                // (a row that saw nothing has l = 0; what lies in its accumulator is finite)
+                uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c);
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) {
+                  uint32_t h[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(o[x + 2 * k] * inv, o[x + 2 * k + 1] * inv);
+                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                  }
+                  dst[x / 8] = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+              } else if (on) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  *reinterpret_cast<float4*>(part + 2 * NC + col * D + c + x) =
+                      make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+              }
+              __syncwarp();                                  // (the next load is the whole warp's)
+            }
+            tc_fence_before();
+            if (cross) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(x_free);
+            }
+            if (whole) {
+              if (on && p.lse)
+                p.lse[out_row] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+              continue;
+            }
+            if (on) {
+              part[col] = m;
+              part[NC + col] = l;
+            }
+            // ---- join the chunks of the key, this half's rows
+            const int rows = min(run.n_cols - w * kPTile, kPTile), row0 = w * kPTile;
+            float* s_w = reinterpret_cast<float*>(smem + Sm::kQ + w * Sm::kTileBytes);   // [parts][128]
+            float* s_inv = s_row + 2 * kPTile + w * kPTile;
+            auto join_parts = [&](int i0, int n, int step, bool store) -> bool {
+              if (row < rows) {
+                float top = -INFINITY, all = 0.0f;
+                for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(part_at(i0 + i * step) + row0 + row));
+                const float base = top == -INFINITY ? 0.0f : top;
+                for (int i = 0; i < n; ++i) {
+                  const float* src = part_at(i0 + i * step) + row0 + row;
+                  const float x = ex2(__ldcg(src) - base);
+                  s_w[i * kPTile + row] = x;
+                  all += x * __ldcg(src + NC);
+                }
+                if (store) {
+                  s_inv[row] = all > 0.0f ? __fdividef(run.v_gsa, all) : 0.0f;
+                  if (p.lse) p.lse[out_row] = all > 0.0f ? (top + log2f(all)) * 0.693147180559945309f : -INFINITY;
+                } else {
+                  part_at(i0)[row0 + row] = top;
+                  part_at(i0)[NC + row0 + row] = all;
+                }
+              }
+              if (!sync_half()) return false;
+              constexpr int V = D / 4;                       // vectors of a row
+              for (int e0 = row; e0 < rows * V; e0 += 4 * kPTile) {
+                float4 acc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = 0; i < n; ++i) {
+                  const float* src = part_at(i0 + i * step) + 2 * NC + row0 * D;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const int e = e0 + k * kPTile;
+                    if (e < rows * V) {
+                      const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + e);
+                      const float x = s_w[i * kPTile + e / V];
+                      acc[k].x += x * y.x; acc[k].y += x * y.y; acc[k].z += x * y.z; acc[k].w += x * y.w;
+                    }
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int e = e0 + k * kPTile;
+                  if (e >= rows * V) continue;
+                  const int r = e / V, x = (e - r * V) * 4;
+                  if (!store) {
+                    *reinterpret_cast<float4*>(part_at(i0) + 2 * NC + (row0 + r) * D + x) = acc[k];
+                    continue;
+                  }
+                  const int rq = div_small(run.rem0 + row0 + r, inv_G);
+                  const int64_t dst = (static_cast<int64_t>(run.q0 + run.iq0 + rq) * p.Hq + run.head * p.G + run.rem0 +
+                                       row0 + r - rq * p.G) * D + x;
+                  const float f = s_inv[r];
+                  const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * f, acc[k].y * f);
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * f, acc[k].w * f);
+                  *reinterpret_cast<uint2*>(p.out + dst) =
+                      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                }
+              }
+              return sync_half();                            // (the table is free again)
+            };
+            // every store of the half so far, then the ticket
+            auto last_of = [&](uint32_t* ticket, int n, bool& all) -> bool {
+              __threadfence();
+              if (!sync_half()) return false;
+              if (row == 0) {
+                const bool y = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
+                if (y) *ticket = 0u;
+                s_flag[w] = y;
+              }
+              if (!sync_half()) return false;
+              all = s_flag[w];
+              __threadfence();
+              return true;
+            };
+            // tickets of chunk c: 4 c + 2 half, and the next one for the runs of parts
+            bool all = false;
+            if (run.n_parts <= kPJoinAlone) {
+              if (!last_of(p.tickets + 4 * run.first + 2 * w, run.n_parts, all)) return false;
+              if (all && !join_parts(0, run.n_parts, 1, true)) return false;
+            } else {
+              const int r0 = me / kPJoinRun * kPJoinRun, n_runs = (run.n_parts + kPJoinRun - 1) / kPJoinRun;
+              const int n = min(kPJoinRun, run.n_parts - r0);
+              if (!last_of(p.tickets + 4 * (run.first + r0) + 2 * w + 1, n, all)) return false;
+              if (all) {
+                if (!join_parts(r0, n, 1, false)) return false;
+                if (!last_of(p.tickets + 4 * run.first + 2 * w, n_runs, all)) return false;
+                if (all && !join_parts(0, n_runs, kPJoinRun, true)) return false;
+              }
+            }
+          }
+        };
+        if (!softmax()) give_up();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+nvr_status launch(AttnParams& p, int max_kv, cudaStream_t s) {
+  using Sm = PrefillSmem<D>;
+  static_assert(Sm::kTotal <= 227 * 1024, "shared memory");
+  static_assert(kPJoinAlone * kPTile * 4 <= Sm::kTileBytes, "the table of weights lies in a query tile");
+  static_assert((kPrefillMaxCtas + kPJoinRun - 1) / kPJoinRun <= kPJoinAlone, "two levels of joining are enough");
+  static bool attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
+  const int sms = device_sm_count();
+  if (sms <= 0) return NVR_ERR_CUDA;
+  if (!attr_set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kTotal);
+    if (e != cudaSuccess) return cuda_status(e);
+    attr_set[dev] = true;
+  }
+  p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + kPrefillCols - 1) / kPrefillCols);
+  const int64_t items = static_cast<int64_t>(p.B) * p.groups;
+  const int64_t most = items * p.Hkv * (2 * ((max_kv + kPTile - 1) / kPTile + 1) + kPKeyUnits);
+  if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
+  int64_t grid = sms < kPrefillMaxCtas ? sms : kPrefillMaxCtas;
+  if (grid > most) grid = most;
+  p.min_chunk = 4;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = Sm::kTotal;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, p));
+}
+
+}  // namespace
+
+nvr_status launch_kv_prefill(AttnParams& p, int D, int max_kv, cudaStream_t s) {
+  return D == 128 ? launch<128>(p, max_kv, s) : launch<64>(p, max_kv, s);
+}
+
+}  // namespace nvr
