@@ -29,6 +29,8 @@
 //
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
 // equal chunks, one per block, partial rows joined by the last block to arrive.
+#include <type_traits>
+
 #include "kv_attention.cuh"
 
 namespace nvr {
@@ -42,6 +44,7 @@ constexpr int kPJoinAlone = 24;            // parts joined at once (the weights'
 constexpr int kPJoinRun = 16;              // beyond that, joined first
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;
+constexpr float kMostSum = 256.0f;         // 2^kRescaleAt
 
 // A key's stretch of tiles in this block's chunk.
 struct alignas(16) Run {
@@ -99,15 +102,42 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
-    tmem_store16(taddr + 16 * h, r);
-  }
+// 32 columns of this warp's lanes without the wait, and the wait: the registers
+// pass through it so that nothing reads them early.
+__device__ __forceinline__ void tmem_load32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
 }
+__device__ __forceinline__ void tmem_load32_finish(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :: "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void registers_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+// Registers of a thread, of the 128 each is launched with: softmax (two groups
+// of four warps), expansion, the rest.
+constexpr int kRegsSoftmax = 168, kRegsExpand = 104, kRegsRest = 72;
+static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsRest <= 4 * 128, "what the block was launched with");
 
 // Chunks of the flat order: a tile costs one unit, two when both halves work
 // on different rows of it.
@@ -205,7 +235,21 @@ kv_prefill_kernel(const AttnParams p) {
   };
 
   if (f0 < f1) {
-    if (warp == 13) {
+      int n_taken = 0;
+      Run run;
+      // the next run, or false (with run.tiles == -1 at the end)
+      auto take = [&]() {
+        const int s = n_taken % kRuns;
+        if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return false;
+        run = s_runs[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(run_empty + s);
+        ++n_taken;
+        return true;
+      };
+    if (warp >= 12) {
+      registers_shrink<kRegsRest>();
+      if (warp == 13) {
       // ------------------------------------------------------------ the walk
       int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
       bool ok = true;
@@ -256,20 +300,7 @@ kv_prefill_kernel(const AttnParams p) {
         ok = hand_out(r);
       }
       if (!ok) give_up();
-    } else if (warp < 13) {
-      int n_run = 0;
-      Run run;
-      // the next run, or false (with run.tiles == -1 at the end)
-      auto take = [&]() {
-        const int s = n_run % kRuns;
-        if (!wait_all(run_full + s, (n_run / kRuns) & 1)) return false;
-        run = s_runs[s];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(run_empty + s);
-        ++n_run;
-        return true;
-      };
-      if (warp == 12) {
+      } else if (warp == 12) {
         // -------------------------------------------------------- the products
         const uint32_t id_s = idesc_f16(128, kPTile, false), id_o = idesc_f16(128, D, true);
         int tk = 0, tv = 0;                                  // tiles of K and V taken
@@ -376,12 +407,25 @@ kv_prefill_kernel(const AttnParams p) {
         if (elect_one()) tc_commit(drained);
         __syncwarp();
         wait_all(drained, 0);
-      } else if (warp >= 8) {
+      }
+    } else if (warp >= 8) {
+        registers_shrink<kRegsExpand>();
         // ---------------------------------------------------- expanding the cache
         const int w = warp - 8, tok = lane & 7, qd = lane >> 3;
         const int S = 1 << p.page_shift;
         int n_tile = 0;                                      // tiles expanded
         constexpr int BL = D / 64;                           // blocks of 16 channels a lane takes of a token
+        // Where this lane's codes and scales lie in the page of its warp's halves of
+        // 16 tokens: the same in every tile, a tile holds whole pages or lies in one
+        int k_code[2], k_scale[2], v_code[2], v_scale[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int o = ((32 * w + 16 * h) & (S - 1)) + tok;
+          k_code[h] = o * (D / 2) + qd * 8 * BL;
+          k_scale[h] = KvPage<D>::key_scales(S) + o * (D / 16) + qd * BL;
+          v_code[h] = KvPage<D>::value_codes(S) + KvPage<D>::value_code(o, qd * BL);
+          v_scale[h] = KvPage<D>::value_scales(S) + KvPage<D>::value_scale(o, qd * BL);
+        }
         auto expand = [&]() -> bool {
           for (;;) {
             if (!take()) return false;
@@ -389,8 +433,9 @@ kv_prefill_kernel(const AttnParams p) {
             const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
             uint2 kc[4][BL], vc[4][BL];
             uint32_t ks[4], vs[4];
-            const uint8_t* base[4];                          // the pages of this warp's groups of eight tokens, or null
+            const uint8_t* base[2];                          // of this warp's halves of 16 tokens, or null
             int at = -1, entries = -1;
+            // the pages of a tile: the halves' addresses, and which are in the cache
             auto find = [&](int tile) {
               const int x = (tile * kPTile) >> p.page_shift; // the tile's first page
               if ((x & ~31) != at) {
@@ -399,54 +444,57 @@ kv_prefill_kernel(const AttnParams p) {
               }
               uint32_t live = 0;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = tile * kPTile + 32 * w + 8 * i;
+              for (int h = 0; h < 2; ++h) {
+                const int t = tile * kPTile + 32 * w + 16 * h;
                 const int page = __shfl_sync(0xFFFFFFFFu, entries, (t >> p.page_shift) - at);
-                const bool ok = t < run.hi && t + 8 > run.lo && page >= 0 && page < p.n_pages;
-                base[i] = ok ? p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S) : nullptr;
-                if (page >= 0 && page < p.n_pages) live |= 1u << (i / 2);
+                const bool ok = page >= 0 && page < p.n_pages;
+                base[h] = ok && t < run.hi && t + 16 > run.lo
+                              ? p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S)
+                              : nullptr;
+                live |= ok ? 1u << h : 0u;
               }
               return live;
             };
-            auto load_k = [&](int tile) {
+            // tokens past the sequence's length are zeros (whatever their bytes)
+            auto load_k_as = [&](auto all, int tile) {         // all: every token of the warp's is there
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int t = tile * kPTile + 32 * w + 8 * i + tok, o = t & (S - 1);
-                ks[i] = 0;
-#pragma unroll
-                for (int x = 0; x < BL; ++x) kc[i][x] = make_uint2(0u, 0u);
-                if (base[i] && t < run.kv) {
-                  const uint8_t* c = base[i] + o * (D / 2) + qd * (8 * BL);
-                  const uint8_t* s = base[i] + KvPage<D>::key_scales(S) + o * (D / 16) + qd * BL;
-                  if (BL == 2) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(c));
-                    kc[i][0] = make_uint2(u.x, u.y);
-                    kc[i][BL - 1] = make_uint2(u.z, u.w);
-                    ks[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
-                  } else {
-                    kc[i][0] = __ldg(reinterpret_cast<const uint2*>(c));
-                    ks[i] = __ldg(s);
-                  }
+                const bool ok = all || (base[i / 2] && tile * kPTile + 32 * w + 8 * i + tok < run.kv);
+                const uint8_t* c = base[i / 2] + (k_code[i / 2] + (i % 2) * 8 * (D / 2));
+                const uint8_t* s = base[i / 2] + (k_scale[i / 2] + (i % 2) * 8 * (D / 16));
+                if (BL == 2) {
+                  const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(c)) : make_uint4(0u, 0u, 0u, 0u);
+                  kc[i][0] = make_uint2(u.x, u.y);
+                  kc[i][BL - 1] = make_uint2(u.z, u.w);
+                  ks[i] = ok ? __ldg(reinterpret_cast<const uint16_t*>(s)) : 0;
+                } else {
+                  kc[i][0] = ok ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
+                  ks[i] = ok ? __ldg(s) : 0;
                 }
               }
             };
-            auto load_v = [&](int tile) {
+            auto load_v_as = [&](auto all, int tile) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int t = tile * kPTile + 32 * w + 8 * i + tok, o = t & (S - 1);
+                const bool ok = all || (base[i / 2] && tile * kPTile + 32 * w + 8 * i + tok < run.kv);
+                const uint8_t* c = base[i / 2] + (v_code[i / 2] + (i % 2) * 8 * (D / 2));
+                const uint8_t* s = base[i / 2] + (v_scale[i / 2] + (i % 2) * 8 * (D / 16));
                 vs[i] = 0;
 #pragma unroll
                 for (int x = 0; x < BL; ++x) {
-                  vc[i][x] = make_uint2(0u, 0u);
-                  if (base[i] && t < run.kv) {
-                    vc[i][x] = __ldg(reinterpret_cast<const uint2*>(
-                        base[i] + KvPage<D>::value_codes(S) + KvPage<D>::value_code(o, qd * BL + x)));
-                    vs[i] |= static_cast<uint32_t>(__ldg(base[i] + KvPage<D>::value_scales(S) +
-                                                         KvPage<D>::value_scale(o, qd * BL + x)))
-                             << (8 * x);
-                  }
+                  vc[i][x] = ok ? __ldg(reinterpret_cast<const uint2*>(c + 64 * x)) : make_uint2(0u, 0u);
+                  vs[i] |= (ok ? static_cast<uint32_t>(__ldg(s + 8 * x)) : 0u) << (8 * x);
                 }
               }
+            };
+            auto full = [&](int tile) { return base[0] && base[1] && tile * kPTile + 32 * w + 32 <= run.kv; };
+            auto load_k = [&](int tile) {
+              if (full(tile)) load_k_as(std::true_type{}, tile);
+              else load_k_as(std::false_type{}, tile);
+            };
+            auto load_v = [&](int tile) {
+              if (full(tile)) load_v_as(std::true_type{}, tile);
+              else load_v_as(std::false_type{}, tile);
             };
             auto put = [&](uint8_t* tile, const uint2 (&c)[4][BL], const uint32_t (&s)[4]) {
 #pragma unroll
@@ -499,7 +547,8 @@ kv_prefill_kernel(const AttnParams p) {
           }
         };
         if (!expand()) give_up();
-      } else {
+    } else {
+        registers_grow<kRegsSoftmax>();
         // ------------------------------------------------------------- softmax
         const int w = warp >> 2, wl = warp & 3, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
@@ -514,23 +563,29 @@ kv_prefill_kernel(const AttnParams p) {
           ph_meet ^= 1u;
           return ok;
         };
-        auto softmax = [&]() -> bool {
-          for (;;) {
-            if (!take()) return false;
-            if (run.tiles < 0) return true;
+        // One run; it stays in shared memory meanwhile, its fields are read where
+        // they are needed.
+        auto one_run = [&](const volatile Run& run) -> bool {
             const int n_my = run.dual ? run.tiles : (run.tiles + 1 - w) / 2;
             const int col = run.dual ? w * kPTile + row : row;
             const bool on = col < run.n_cols;
-            const int dq = div_small(run.rem0 + (on ? col : 0), inv_G);
-            const int pos = run.kv - run.n_q + run.iq0 + dq;
-            const int hq = run.head * p.G + run.rem0 + (on ? col : 0) - dq * p.G;
-            const int64_t q_row = run.q0 + run.iq0 + dq;
+            // the row's query and head (recomputed where they are needed)
+            auto quotient = [&]() { return div_small(run.rem0 + (on ? col : 0), inv_G); };
+            auto head_of = [&](int dq) { return run.head * p.G + run.rem0 + (on ? col : 0) - dq * p.G; };
+            auto out_row = [&]() {
+              const int dq = quotient();
+              return static_cast<int64_t>(run.q0 + run.iq0 + dq) * p.Hq + head_of(dq);
+            };
+            const bool any_on = __any_sync(0xFFFFFFFFu, on);
+            const int pos = run.kv - run.n_q + run.iq0 + quotient();
             const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
             const int lo = p.window > 0 ? pos + 1 - p.window : 0;
             float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
             if (n_my > 0) {
               // the row's query in fp16, scaled into its range, into the swizzled tile
-              const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row * p.q_stride + static_cast<int64_t>(hq) * D);
+              const int dq = quotient();
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  p.q + (run.q0 + run.iq0 + dq) * p.q_stride + static_cast<int64_t>(head_of(dq)) * D);
               uint4 u[D / 8];
               uint32_t big = 0;
 #pragma unroll
@@ -564,72 +619,89 @@ kv_prefill_kernel(const AttnParams p) {
               if (!wait_all(s_full + w, ph_s)) return false;
               ph_s ^= 1u;
               tc_fence_after();
+              if (!any_on) {
+                // (rows that nobody asked for: their P may be anything)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + w);
+                continue;
+              }
               const uint32_t bytes = s_live[(n_tile + j) % kLive];
               // bit i: tokens 16 i .. of the tile are in the cache
               const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
               const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
+              // bit x: the row sees token t0 + c + x (c a multiple of 32)
+              const int from = lo - t0, to = hi - t0;
+              auto seen32 = [&](int c) {
+                const int a = min(max(from - c, 0), 32), b = min(max(to - c, 0), 32);
+                const uint32_t m = (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
+                const uint32_t two = live >> (c / 16);
+                return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
+              };
               uint32_t pr[kPTile / 2];
-              float high, sum;
-              auto visible = [&](int c) { return t0 + c < hi && t0 + c >= lo && ((live >> (c / 16)) & 1u); };
-              auto weights = [&]() {
-                high = -INFINITY;
+              float sum;
+              auto weights = [&](auto hidden) {                // hidden: some tokens are not seen
                 uint64_t sum2 = f2_pack(0.0f, 0.0f);
                 const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
+                uint32_t s[2][32];
+                tmem_load32_start(t_s, s[0]);
 #pragma unroll
                 for (int c = 0; c < kPTile; c += 32) {
-                  float s[32];
-                  tmem_load32(t_s + c, s);
-                  if (masked) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                      const float v = fmaf(s[x], to_log2, m_neg);
-                      s[x] = visible(c + x) ? v : -INFINITY;
-                    }
-                  } else {
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                      const uint64_t v = f2_fma(f2_pack(s[x], s[x + 1]), k2, m2);
-                      s[x] = f2_lo(v);
-                      s[x + 1] = f2_hi(v);
-                    }
-                  }
+                  uint32_t (&now)[32] = s[(c / 32) % 2];
+                  tmem_load32_finish(now);
+                  if (c + 32 < kPTile) tmem_load32_start(t_s + c + 32, s[(c / 32 + 1) % 2]);
+                  const uint32_t see = hidden ? seen32(c) : 0xFFFFFFFFu;
 #pragma unroll
                   for (int x = 0; x < 32; x += 2) {
-                    high = fmaxf(high, fmaxf(s[x], s[x + 1]));
-                    const float a = ex2(s[x]), b = ex2(s[x + 1]);
+                    const uint64_t v = f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+                    float v0 = f2_lo(v), v1 = f2_hi(v);
+                    if (hidden) {
+                      v0 = see & (1u << x) ? v0 : -INFINITY;
+                      v1 = see & (2u << x) ? v1 : -INFINITY;
+                    }
+                    const float a = ex2(v0), b = ex2(v1);
                     sum2 = f2_add(sum2, f2_pack(a, b));
                     pr[(c + x) / 2] = pack_f16(a, b);
                   }
                 }
                 sum = f2_lo(sum2) + f2_hi(sum2);
               };
-              weights();
-              if (__any_sync(0xFFFFFFFFu, high > kRescaleAt)) {
-                // move the maximum to the largest score so far
-                float top = -INFINITY;
+              // A tile whose weights add up to more than 2^kRescaleAt holds a score
+              // far above m (a weight above 2, at least): no maximum is taken of the
+              // others.  (m at or above every score: at most 128 weights of 1.)
+              for (bool move = i == 0;; move = true) {
+                if (move) {
+                  // m moves to the largest score so far
+                  float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kPTile; c += 32) {
-                  float s[32];
-                  tmem_load32(t_s + c, s);
+                  for (int c = 0; c < kPTile; c += 32) {
+                    uint32_t s[32];
+                    tmem_load32_start(t_s + c, s);
+                    tmem_load32_finish(s);
+                    const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
 #pragma unroll
-                  for (int x = 0; x < 32; ++x)
-                    if (!masked || visible(c + x)) top = fmaxf(top, s[x] * to_log2);
-                }
-                const float now = fminf(m_neg, -top);
-                const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-                m_neg = now;
-                l *= shrink;
-                if (i > 0) {
+                    for (int x = 0; x < 32; ++x)
+                      top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
+                  }
+                  const float now = fminf(m_neg, -top);
+                  const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                  m_neg = now;
+                  l *= shrink;
+                  if (i > 0) {
 #pragma unroll 1
-                  for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tmem_load32(t_o + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                      float o[16];
+                      uint32_t y[16];
+                      tmem_load16(t_o + c, o);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] *= shrink;
-                    tmem_store32(t_o + c, o);
+                      for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
+                      tmem_store16(t_o + c, y);
+                    }
                   }
                 }
-                weights();
+                if (masked) weights(std::true_type{});
+                else weights(std::false_type{});
+                if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
               }
               l += sum;
 #pragma unroll
@@ -687,7 +759,7 @@ kv_prefill_kernel(const AttnParams p) {
             }
             if (!run.dual && w == 1) {
               tc_fence_before();
-              continue;
+              return true;
             }
             const bool whole = run.n_parts == 1;
             auto part_at = [&](int i) {
@@ -695,7 +767,6 @@ kv_prefill_kernel(const AttnParams p) {
             };
             const int me = static_cast<int>(blockIdx.x) - run.first;
             float* part = part_at(me);
-            const int64_t out_row = q_row * p.Hq + hq;
             const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -713,7 +784,7 @@ kv_prefill_kernel(const AttnParams p) {
               }
               if (on && whole) {
                 // (a row that saw nothing has l = 0; what lies in its accumulator is finite)
-                uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * D + c);
+                uint4* dst = reinterpret_cast<uint4*>(p.out + out_row() * D + c);
 #pragma unroll
                 for (int x = 0; x < 32; x += 8) {
                   uint32_t h[4];
@@ -739,8 +810,8 @@ kv_prefill_kernel(const AttnParams p) {
             }
             if (whole) {
               if (on && p.lse)
-                p.lse[out_row] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
-              continue;
+                p.lse[out_row()] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+              return true;
             }
             if (on) {
               part[col] = m;
@@ -763,7 +834,7 @@ kv_prefill_kernel(const AttnParams p) {
                 }
                 if (store) {
                   s_inv[row] = all > 0.0f ? __fdividef(run.v_gsa, all) : 0.0f;
-                  if (p.lse) p.lse[out_row] = all > 0.0f ? (top + log2f(all)) * 0.693147180559945309f : -INFINITY;
+                  if (p.lse) p.lse[out_row()] = all > 0.0f ? (top + log2f(all)) * 0.693147180559945309f : -INFINITY;
                 } else {
                   part_at(i0)[row0 + row] = top;
                   part_at(i0)[NC + row0 + row] = all;
@@ -771,15 +842,16 @@ kv_prefill_kernel(const AttnParams p) {
               }
               if (!sync_half()) return false;
               constexpr int V = D / 4;                       // vectors of a row
-              for (int e0 = row; e0 < rows * V; e0 += 4 * kPTile) {
-                float4 acc[4];
+              constexpr int K = 8;                           // vectors a thread has under way
+              for (int e0 = row; e0 < rows * V; e0 += K * kPTile) {
+                float4 acc[K];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) {
                   const float* src = part_at(i0 + i * step) + 2 * NC + row0 * D;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
+                  for (int k = 0; k < K; ++k) {
                     const int e = e0 + k * kPTile;
                     if (e < rows * V) {
                       const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + e);
@@ -789,7 +861,7 @@ kv_prefill_kernel(const AttnParams p) {
                   }
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < K; ++k) {
                   const int e = e0 + k * kPTile;
                   if (e >= rows * V) continue;
                   const int r = e / V, x = (e - r * V) * 4;
@@ -838,10 +910,19 @@ kv_prefill_kernel(const AttnParams p) {
                 if (all && !join_parts(0, n_runs, kPJoinRun, true)) return false;
               }
             }
+            return true;
+        };
+        auto softmax = [&]() -> bool {
+          for (;; ++n_taken) {
+            const int s = n_taken % kRuns;
+            if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return false;
+            if (s_runs[s].tiles < 0) return true;
+            if (!one_run(s_runs[s])) return false;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(run_empty + s);
           }
         };
         if (!softmax()) give_up();
-      }
     }
   }
   tc_fence_before();
