@@ -79,7 +79,7 @@ struct AttnShape {
   static constexpr int kFrag = D / 4;                        // O registers of a lane per 8 columns
   static constexpr int kShare = kFrag / NW;                  // of them, those a warp joins
   static constexpr int kJoinBytes = NW * (NW - 1) * kShare * 32 * 4;
-  static constexpr int kQBytes = NT > 1 ? NT * (D / 16) * 64 * 4 : 0;
+  static constexpr int kQBytes = NT * (D / 16) * 64 * 4;
   static constexpr int kSmem = STAGES * kStageBytes + kJoinBytes + kQBytes + 2 * NW * kCols * 4 +
                                STAGES * (static_cast<int>(sizeof(Meta)) + kCols * D * 2) + (2 * STAGES + 3) * 8 + 64 + 128;
 };
@@ -96,7 +96,7 @@ kv_attention_kernel(const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   float* s_join = reinterpret_cast<float*>(smem + STAGES * Sh::kStageBytes);          // [NW][NW - 1][SH][32]
-  uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + Sh::kJoinBytes / 4);                 // [NT][KS][32][2] (NT > 1)
+  uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + Sh::kJoinBytes / 4);                 // [NT][KS][32][2]: B fragments of Q^T
   float* s_m = reinterpret_cast<float*>(s_q + Sh::kQBytes / 4);                       // [NW][NC]
   float* s_l = s_m + NW * NC;
   uint8_t* s_raw = reinterpret_cast<uint8_t*>(s_l + NW * NC);                         // [STAGES][NC][D] bf16 queries
@@ -170,11 +170,15 @@ kv_attention_kernel(const AttnParams p) {
     const int part = min(S, TILE);                           // tokens of one copied piece
     const int pieces = TILE / part;
     bool ok = true;
-    Group next = group_of<NC, TILE>(p, item);
-    while (f < f1 && ok) {
+    Group next = {};
+    for (bool primed = false; f < f1 && ok;) {
       const Group g = next;
       // (read ahead: its loads are not waited for here)
-      if (item + 1 < n_items) next = group_of<NC, TILE>(p, item + 1);
+      next = group_of<NC, TILE>(p, min(primed ? item + 1 : item, n_items - 1));
+      if (!primed) {
+        primed = true;
+        continue;
+      }
       const int cost = key_cost(g), n_item = cost * p.Hkv;
       const int32_t* table = p.page_table + static_cast<int64_t>(g.b) * p.max_pages;
       int head = off / max(cost, 1), ti = off - head * cost;
@@ -291,7 +295,6 @@ kv_attention_kernel(const AttnParams p) {
     v_scales_at[u] = piece_at + KvPage<D>::value_scales(part) + in_piece * (D / 16);
   }
 
-  uint32_t qf[NT > 1 ? 1 : NT][KS][2];                       // B fragments of Q^T (shared memory for NT > 1)
   float o[NT][MT][4];
   float m_neg[NT][2], l_run[NT][2], to_log2[NT][2];         // -m: +inf until a token is seen
   uint32_t met = 0;
@@ -348,15 +351,8 @@ kv_attention_kernel(const AttnParams p) {
             const uint32_t u = w[2 * ks + i];
             b[i] = pack_f16(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xFFFF0000u) * up);
           }
-          if (NT > 1) {
-            if (warp == nt % NW) {
-              s_q[((nt * KS + ks) * 32 + lane) * 2] = b[0];
-              s_q[((nt * KS + ks) * 32 + lane) * 2 + 1] = b[1];
-            }
-          } else {
-            qf[NT > 1 ? 0 : nt][ks][0] = b[0];
-            qf[NT > 1 ? 0 : nt][ks][1] = b[1];
-          }
+          if (warp == nt % NW)
+            *reinterpret_cast<uint2*>(s_q + ((nt * KS + ks) * 32 + lane) * 2) = make_uint2(b[0], b[1]);
         }
         // columns 8 nt + 2 c, + 1: what the accumulators of this lane need
 #pragma unroll
@@ -370,7 +366,7 @@ kv_attention_kernel(const AttnParams p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.0f;
       }
-      if (NT > 1 && !sync_consumers()) return give_up();
+      if (!sync_consumers()) return give_up();
     }
 
     const uint8_t* stage = smem + st * Sh::kStageBytes;
@@ -418,17 +414,10 @@ kv_attention_kernel(const AttnParams p) {
           const int ks = 2 * wd + h;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b0, b1;
-            if (NT > 1) {
-              const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nt * KS + ks) * 32 + lane) * 2);
-              b0 = b.x; b1 = b.y;
-            } else {
-              b0 = qf[NT > 1 ? 0 : nt][ks][0];
-              b1 = qf[NT > 1 ? 0 : nt][ks][1];
-            }
+            const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((nt * KS + ks) * 32 + lane) * 2);
 #pragma unroll
             for (int u = 0; u < MW; ++u)
-              mma16816(h ? s1[u][nt] : s[u][nt], a[u][0][2 * h], a[u][1][2 * h], a[u][0][2 * h + 1], a[u][1][2 * h + 1], b0, b1);
+              mma16816(h ? s1[u][nt] : s[u][nt], a[u][0][2 * h], a[u][1][2 * h], a[u][0][2 * h + 1], a[u][1][2 * h + 1], b.x, b.y);
           }
         }
       }
@@ -768,20 +757,16 @@ kv_attention_kernel(const AttnParams p) {
       __threadfence();
       return all;
     };
-    if (n_parts <= kJoinAlone) {
-      const bool all = last_of(p.tickets + 2 * first, n_parts);
+    const bool two = n_parts > kJoinAlone;
+    const int r0 = two ? me / kJoinRun * kJoinRun : 0;
+#pragma unroll 1
+    for (int level = two ? 1 : 0; level >= 0; --level) {
+      const int i0 = level ? r0 : 0, step = two && !level ? kJoinRun : 1;
+      const int n = level ? min(kJoinRun, n_parts - r0) : two ? (n_parts + kJoinRun - 1) / kJoinRun : n_parts;
+      const bool all = last_of(p.tickets + 2 * (first + i0) + level, n);
       if (failed) return give_up();
-      if (all) join_parts(0, n_parts, 1, true);
-    } else {
-      const int run = me / kJoinRun * kJoinRun, n_runs = (n_parts + kJoinRun - 1) / kJoinRun;
-      bool all = last_of(p.tickets + 2 * (first + run) + 1, min(kJoinRun, n_parts - run));
-      if (failed) return give_up();
-      if (all) {
-        join_parts(run, min(kJoinRun, n_parts - run), 1, false);
-        all = last_of(p.tickets + 2 * first, n_runs);
-        if (failed) return give_up();
-        if (all) join_parts(0, n_runs, kJoinRun, true);
-      }
+      if (!all) break;
+      join_parts(i0, n, step, level == 0);
     }
     // s_flag is written again only after the next run's barriers
   }

@@ -18,7 +18,8 @@
 //                   swizzled shared memory, two stages of K and of V;
 //   warp 12         issues the products, alternating the row tiles, so that one
 //                   tile's softmax runs under the other's products;
-//   warp 13         walks the work and hands every role its runs.
+//   warp 13         walks the work and hands every role its runs;
+//   warp 14         fetches the pages of the coming tiles into L2.
 // A group of at most 128 columns uses both halves as well: the same rows in
 // both, each taking every other token tile, joined at the end.
 //
@@ -39,11 +40,12 @@ namespace {
 
 constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
 constexpr int kPThreads = 512;
-constexpr int kPKeyUnits = 2;              // cost of starting and ending a key, in single tiles
+constexpr int kPKeyUnits = 8;              // cost of starting and ending a key, in single tiles
 constexpr int kPJoinAlone = 24;            // parts joined at once (the weights' table lies in a query tile)
 constexpr int kPJoinRun = 16;              // beyond that, joined first
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;
+constexpr int kAhead = 6;                  // tiles fetched into L2 before they are expanded
 constexpr float kMostSum = 256.0f;         // 2^kRescaleAt
 
 // A key's stretch of tiles in this block's chunk.
@@ -159,26 +161,28 @@ kv_prefill_kernel(const AttnParams p) {
   uint64_t *run_full = bars, *run_empty = run_full + kRuns, *k_full = run_empty + kRuns, *k_empty = k_full + 2,
            *v_full = k_empty + 2, *v_empty = v_full + 2, *q_full = v_empty + 2, *s_full = q_full + 2,
            *p_full = s_full + 2, *o_full = p_full + 2, *meet = o_full + 2, *x_ready = meet + 2, *x_full = x_ready + 1,
-           *x_free = x_full + 1, *drained = x_free + 1;
-  int* s_words = reinterpret_cast<int*>(drained + 1);
+           *x_free = x_full + 1, *drained = x_free + 1, *q_raw = drained + 1;
+  int* s_words = reinterpret_cast<int*>(q_raw + 2);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
   volatile int* abort_flag = s_words + 1;
   int* s_start = s_words + 2;                                // item, offset inside it
   int* s_flag = s_words + 4;                                 // per half: the last block to arrive
+  volatile int* s_done = s_words + 10;                       // tiles expanded
   volatile uint32_t* s_live = reinterpret_cast<volatile uint32_t*>(s_words + 6);   // [kLive] tokens in groups of 16
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, 13); }
+    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, 14); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4); mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
       mbar_init(q_full + i, 4); mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4); mbar_init(o_full + i, 1);
-      mbar_init(meet + i, 4);
+      mbar_init(meet + i, 4); mbar_init(q_raw + i, 4);
     }
     mbar_init(x_ready, 4); mbar_init(x_full, 4); mbar_init(x_free, 4); mbar_init(drained, 1);
     *abort_flag = 0;
+    *s_done = 0;
     for (int i = 0; i < kLive; ++i) s_live[i] = 0;
     fence_mbar_init();
   }
@@ -264,10 +268,14 @@ kv_prefill_kernel(const AttnParams p) {
         ++n_run;
         return true;
       };
-      Group next = group_of<NC, kPTile>(p, item);
-      while (f < f1 && ok) {
+      Group next = {};
+      for (bool primed = false; f < f1 && ok;) {
         const Group g = next;
-        if (item + 1 < n_items) next = group_of<NC, kPTile>(p, item + 1);
+        next = group_of<NC, kPTile>(p, min(primed ? item + 1 : item, n_items - 1));
+        if (!primed) {
+          primed = true;
+          continue;
+        }
         const int cost = key_units(g), u = tile_units(g);
         while (off < cost * p.Hkv && f < f1 && ok) {
           const int head = off / cost, at = off - head * cost;
@@ -349,56 +357,35 @@ kv_prefill_kernel(const AttnParams p) {
             auto v_ready = [&](int j) { return have(v_full + (v0 + j) % 2, ((v0 + j) / 2) & 1); };
             auto q_ready = [&](int w) { const bool ok = have(q_full + w, ph_q[w]); ph_q[w] ^= 1u; return ok; };
             auto p_ready = [&](int w) { const bool ok = have(p_full + w, ph_p[w]); ph_p[w] ^= 1u; return ok; };
+            // Row tile w: O += P V of its tile `cur`, then S of its tile `nxt`; both row
+            // tiles walk all tiles (dual) or every other.  K and V of a tile wait for
+            // its first reader and are free after its last.
+            auto step = [&](bool dual, int w, int cur, int nxt) -> bool {
+              const bool first = !dual || w == 0, last = !dual || w == 1;
+              if (cur >= 0) {
+                if ((first && !v_ready(cur)) || !p_ready(w)) return false;
+                weigh(w, (v0 + cur) % 2, cur > (dual ? 0 : 1));
+                if (last) commit(v_empty + (v0 + cur) % 2);
+              }
+              if (nxt < n) {
+                if (nxt < (dual ? 1 : 2) && !q_ready(w)) return false;
+                if (first && !k_ready(nxt)) return false;
+                score(w, (k0 + nxt) % 2);
+                commit(s_full + w);
+                if (last) commit(k_empty + (k0 + nxt) % 2);
+              } else if (cur >= 0) {
+                commit(o_full + w);
+              }
+              return true;
+            };
             if (run.dual) {
-              if (!q_ready(0) || !k_ready(0)) return false;
-              score(0, k0 % 2);
-              commit(s_full);
-              if (!q_ready(1)) return false;
-              score(1, k0 % 2);
-              commit(s_full + 1);
-              commit(k_empty + k0 % 2);
-              for (int j = 0; j < n; ++j) {
-                if (!v_ready(j) || !p_ready(0)) return false;
-                weigh(0, (v0 + j) % 2, j > 0);
-                if (j + 1 < n) {
-                  if (!k_ready(j + 1)) return false;
-                  score(0, (k0 + j + 1) % 2);
-                  commit(s_full);
-                } else {
-                  commit(o_full);
-                }
-                if (!p_ready(1)) return false;
-                weigh(1, (v0 + j) % 2, j > 0);
-                commit(v_empty + (v0 + j) % 2);
-                if (j + 1 < n) {
-                  score(1, (k0 + j + 1) % 2);
-                  commit(s_full + 1);
-                  commit(k_empty + (k0 + j + 1) % 2);
-                } else {
-                  commit(o_full + 1);
-                }
-              }
+#pragma unroll 1
+              for (int j = -1; j < n; ++j)
+                if (!step(true, 0, j, j + 1) || !step(true, 1, j, j + 1)) return false;
             } else {
-              for (int j = 0; j < min(n, 2); ++j) {
-                if (!q_ready(j) || !k_ready(j)) return false;
-                score(j, (k0 + j) % 2);
-                commit(s_full + j);
-                commit(k_empty + (k0 + j) % 2);
-              }
-              for (int j = 0; j < n; ++j) {
-                const int w = j & 1;
-                if (!v_ready(j) || !p_ready(w)) return false;
-                weigh(w, (v0 + j) % 2, j > 1);
-                commit(v_empty + (v0 + j) % 2);
-                if (j + 2 < n) {
-                  if (!k_ready(j + 2)) return false;
-                  score(w, (k0 + j + 2) % 2);
-                  commit(s_full + w);
-                  commit(k_empty + (k0 + j + 2) % 2);
-                } else {
-                  commit(o_full + w);
-                }
-              }
+#pragma unroll 1
+              for (int j = -2; j < n; ++j)
+                if (!step(false, j & 1, j, j + 2)) return false;
             }
           }
         };
@@ -407,6 +394,29 @@ kv_prefill_kernel(const AttnParams p) {
         if (elect_one()) tc_commit(drained);
         __syncwarp();
         wait_all(drained, 0);
+      } else if (warp == 14) {
+        // ------------------------------- the pages of the coming tiles into L2
+        // (the expanding warps read one tile ahead, less than a trip to memory)
+        const int S = 1 << p.page_shift, pieces = kPTile / S;
+        int n_tile = 0;
+        bool ok = true;
+        while (ok) {
+          ok = take() && run.tiles >= 0;
+          const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
+          for (int j = 0; ok && j < run.tiles; ++j, ++n_tile) {
+            const uint64_t limit = globaltimer_ns() + 1000000000ull;
+            while (n_tile > *s_done + kAhead && !*abort_flag && globaltimer_ns() < limit) __nanosleep(100);
+            const int t = (run.tile0 + j) * kPTile + lane * S;
+            if (lane < pieces && t < run.hi && t + S > run.lo) {
+              const int page = __ldg(table + (t >> p.page_shift));
+              if (page >= 0 && page < p.n_pages)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                             :: "l"(p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S)),
+                                "r"(KvPage<D>::bytes(S)) : "memory");
+            }
+            __syncwarp();
+          }
+        }
       }
     } else if (warp >= 8) {
         registers_shrink<kRegsExpand>();
@@ -415,109 +425,110 @@ kv_prefill_kernel(const AttnParams p) {
         const int S = 1 << p.page_shift;
         int n_tile = 0;                                      // tiles expanded
         constexpr int BL = D / 64;                           // blocks of 16 channels a lane takes of a token
-        // Where this lane's codes and scales lie in the page of its warp's halves of
-        // 16 tokens: the same in every tile, a tile holds whole pages or lies in one
-        int k_code[2], k_scale[2], v_code[2], v_scale[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int o = ((32 * w + 16 * h) & (S - 1)) + tok;
-          k_code[h] = o * (D / 2) + qd * 8 * BL;
-          k_scale[h] = KvPage<D>::key_scales(S) + o * (D / 16) + qd * BL;
-          v_code[h] = KvPage<D>::value_codes(S) + KvPage<D>::value_code(o, qd * BL);
-          v_scale[h] = KvPage<D>::value_scales(S) + KvPage<D>::value_scale(o, qd * BL);
-        }
+        // Where this lane's codes and scales lie in the page of its warp's first 16
+        // tokens, and how much further the other 16 are when they share the page
+        // (pages of 32 tokens or more): the same in every tile, a tile holds whole
+        // pages or lies in one
+        const int o0 = ((32 * w) & (S - 1)) + tok;
+        const uint32_t k_code = o0 * (D / 2) + qd * 8 * BL, k_scale = KvPage<D>::key_scales(S) + o0 * (D / 16) + qd * BL;
+        const uint32_t v_code = KvPage<D>::value_codes(S) + KvPage<D>::value_code(o0, qd * BL);
+        const uint32_t v_scale = KvPage<D>::value_scales(S) + KvPage<D>::value_scale(o0, qd * BL);
+        const bool one_page = S >= 32;
+        const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * KvPage<D>::bytes(S);
         auto expand = [&]() -> bool {
           for (;;) {
             if (!take()) return false;
             if (run.tiles < 0) return true;
             const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
             uint2 kc[4][BL], vc[4][BL];
-            uint32_t ks[4], vs[4];
-            const uint8_t* base[2];                          // of this warp's halves of 16 tokens, or null
+            uint32_t ks[4], vs[4][BL], k_mask[4], v_mask[4];
+            // A half without its page reads the first page of the cache, under scales
+            // of zero; so do tokens past the sequence's length (whatever their bytes).
+            const uint8_t* head_at = p.cache + static_cast<int64_t>(run.head) * KvPage<D>::bytes(S);
+            const uint8_t* base[2];                          // this head in the pages of the warp's two halves
+            int limit[2];                                    // the tokens of a half below this have scales
             int at = -1, entries = -1;
-            // the pages of a tile: the halves' addresses, and which are in the cache
+            // the pages of a tile; which are in the cache
             auto find = [&](int tile) {
               const int x = (tile * kPTile) >> p.page_shift; // the tile's first page
               if ((x & ~31) != at) {
                 at = x & ~31;
                 entries = at + lane < p.max_pages ? __ldg(table + at + lane) : -1;
               }
-              uint32_t live = 0;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int t = tile * kPTile + 32 * w + 16 * h;
-                const int page = __shfl_sync(0xFFFFFFFFu, entries, (t >> p.page_shift) - at);
-                const bool ok = page >= 0 && page < p.n_pages;
-                base[h] = ok && t < run.hi && t + 16 > run.lo
-                              ? p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S)
-                              : nullptr;
-                live |= ok ? 1u << h : 0u;
+              const int t = tile * kPTile + 32 * w, e = (t >> p.page_shift) - at;
+              int page = __shfl_sync(0xFFFFFFFFu, entries, e);
+              bool ok = page >= 0 && page < p.n_pages;
+              uint32_t live = ok ? 3u : 0u;
+              ok = ok && t < run.hi && t + 32 > run.lo;
+              base[0] = base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
+              limit[0] = limit[1] = ok ? run.kv : 0;
+              if (!one_page) {                               // pages of 16: the second half's is the next
+                page = __shfl_sync(0xFFFFFFFFu, entries, e + 1);
+                ok = page >= 0 && page < p.n_pages;
+                live = (live & 1u) | (ok ? 2u : 0u);
+                ok = ok && t + 16 < run.hi && t + 32 > run.lo;
+                base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
+                limit[1] = ok ? run.kv : 0;
               }
               return live;
             };
-            // tokens past the sequence's length are zeros (whatever their bytes)
-            auto load_k_as = [&](auto all, int tile) {         // all: every token of the warp's is there
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const bool ok = all || (base[i / 2] && tile * kPTile + 32 * w + 8 * i + tok < run.kv);
-                const uint8_t* c = base[i / 2] + (k_code[i / 2] + (i % 2) * 8 * (D / 2));
-                const uint8_t* s = base[i / 2] + (k_scale[i / 2] + (i % 2) * 8 * (D / 16));
-                if (BL == 2) {
-                  const uint4 u = ok ? __ldg(reinterpret_cast<const uint4*>(c)) : make_uint4(0u, 0u, 0u, 0u);
-                  kc[i][0] = make_uint2(u.x, u.y);
-                  kc[i][BL - 1] = make_uint2(u.z, u.w);
-                  ks[i] = ok ? __ldg(reinterpret_cast<const uint16_t*>(s)) : 0;
-                } else {
-                  kc[i][0] = ok ? __ldg(reinterpret_cast<const uint2*>(c)) : make_uint2(0u, 0u);
-                  ks[i] = ok ? __ldg(s) : 0;
-                }
-              }
-            };
-            auto load_v_as = [&](auto all, int tile) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const bool ok = all || (base[i / 2] && tile * kPTile + 32 * w + 8 * i + tok < run.kv);
-                const uint8_t* c = base[i / 2] + (v_code[i / 2] + (i % 2) * 8 * (D / 2));
-                const uint8_t* s = base[i / 2] + (v_scale[i / 2] + (i % 2) * 8 * (D / 16));
-                vs[i] = 0;
-#pragma unroll
-                for (int x = 0; x < BL; ++x) {
-                  vc[i][x] = ok ? __ldg(reinterpret_cast<const uint2*>(c + 64 * x)) : make_uint2(0u, 0u);
-                  vs[i] |= (ok ? static_cast<uint32_t>(__ldg(s + 8 * x)) : 0u) << (8 * x);
-                }
-              }
-            };
-            auto full = [&](int tile) { return base[0] && base[1] && tile * kPTile + 32 * w + 32 <= run.kv; };
+            const int step_c = one_page ? 16 * (D / 2) : 0, step_s = one_page ? 16 * (D / 16) : 0;
             auto load_k = [&](int tile) {
-              if (full(tile)) load_k_as(std::true_type{}, tile);
-              else load_k_as(std::false_type{}, tile);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* c = base[h] + (k_code + h * step_c);
+                const uint8_t* s = base[h] + (k_scale + h * step_s);
+                const int t = tile * kPTile + 32 * w + 16 * h + tok;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (BL == 2) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(c + i * 8 * (D / 2)));
+                    kc[2 * h + i][0] = make_uint2(u.x, u.y);
+                    kc[2 * h + i][BL - 1] = make_uint2(u.z, u.w);
+                    ks[2 * h + i] = __ldg(reinterpret_cast<const uint16_t*>(s + i * 8 * (D / 16)));
+                  } else {
+                    kc[2 * h + i][0] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2)));
+                    ks[2 * h + i] = __ldg(s + i * 8 * (D / 16));
+                  }
+                  k_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
+                }
+              }
             };
             auto load_v = [&](int tile) {
-              if (full(tile)) load_v_as(std::true_type{}, tile);
-              else load_v_as(std::false_type{}, tile);
-            };
-            auto put = [&](uint8_t* tile, const uint2 (&c)[4][BL], const uint32_t (&s)[4]) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = 32 * w + 8 * i + tok;
-                const uint32_t s2 = e4m3x2_to_f16(s[i]);
+              for (int h = 0; h < 2; ++h) {
+                const uint8_t* c = base[h] + (v_code + h * step_c);
+                const uint8_t* s = base[h] + (v_scale + h * step_s);
+                const int t = tile * kPTile + 32 * w + 16 * h + tok;
 #pragma unroll
-                for (int x = 0; x < BL; ++x) {
-                  const uint32_t sb = __byte_perm(s2, 0, x == 0 ? 0x1010 : 0x3232);
-                  uint32_t a[8];
-                  e2m1x8_to_f16(c[i][x].x, a[0], a[1], a[2], a[3]);
-                  e2m1x8_to_f16(c[i][x].y, a[4], a[5], a[6], a[7]);
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                  for (int y = 0; y < 8; ++y) a[y] = h2_mul(a[y], sb);
-                  const int blk = qd * BL + x;               // channels 16 blk ..
-                  uint8_t* row = tile + (blk / 4) * (kPTile * 128) + t * 128;
-                  const int ch = 2 * (blk % 4);
-                  *reinterpret_cast<uint4*>(row + ((ch ^ tok) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                  *reinterpret_cast<uint4*>(row + (((ch + 1) ^ tok) << 4)) = make_uint4(a[4], a[5], a[6], a[7]);
+                  for (int x = 0; x < BL; ++x) {
+                    vc[2 * h + i][x] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2) + 64 * x));
+                    vs[2 * h + i][x] = __ldg(s + i * 8 * (D / 16) + 8 * x);
+                  }
+                  v_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
                 }
               }
-              fence_proxy_async_smem();
-              __syncwarp();
+            };
+            // one group of eight tokens: codes times scales into the swizzled tile
+            auto put = [&](uint8_t* tile, int i, const uint2 (&c)[BL], uint32_t two) {
+              const uint32_t s2 = e4m3x2_to_f16(two);
+              uint8_t* row = tile + (32 * w + 8 * i + tok) * 128;
+#pragma unroll
+              for (int x = 0; x < BL; ++x) {
+                const uint32_t sb = __byte_perm(s2, 0, x == 0 ? 0x1010 : 0x3232);
+                uint32_t a[8];
+                e2m1x8_to_f16(c[x].x, a[0], a[1], a[2], a[3]);
+                e2m1x8_to_f16(c[x].y, a[4], a[5], a[6], a[7]);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) a[y] = h2_mul(a[y], sb);
+                const int blk = qd * BL + x;                 // channels 16 blk ..
+                uint8_t* atom = row + (blk / 4) * (kPTile * 128);
+                const int ch = 2 * (blk % 4);
+                *reinterpret_cast<uint4*>(atom + ((ch ^ tok) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4*>(atom + (((ch + 1) ^ tok) << 4)) = make_uint4(a[4], a[5], a[6], a[7]);
+              }
             };
             uint32_t live = find(run.tile0);
             load_k(run.tile0);
@@ -526,7 +537,10 @@ kv_prefill_kernel(const AttnParams p) {
               const int st = n_tile % 2;
               const uint32_t ph = ((n_tile / 2) & 1) ^ 1;
               if (!wait_all(k_empty + st, ph)) return false;
-              put(smem + Sm::kK + st * Sm::kTileBytes, kc, ks);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) put(smem + Sm::kK + st * Sm::kTileBytes, i, kc[i], ks[i] & k_mask[i]);
+              fence_proxy_async_smem();
+              __syncwarp();
               // this warp's byte of the word: its two groups of 16 tokens
               if (lane == 0) {
                 reinterpret_cast<volatile uint8_t*>(s_live + n_tile % kLive)[w] = static_cast<uint8_t>(live);
@@ -539,8 +553,13 @@ kv_prefill_kernel(const AttnParams p) {
                 load_k(more);
               }
               if (!wait_all(v_empty + st, ph)) return false;
-              put(smem + Sm::kV + st * Sm::kTileBytes, vc, vs);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                put(smem + Sm::kV + st * Sm::kTileBytes, i, vc[i], (vs[i][0] | (vs[i][BL - 1] << 8)) & v_mask[i]);
+              fence_proxy_async_smem();
+              __syncwarp();
               if (lane == 0) mbar_arrive(v_full + st);
+              if (w == 0 && lane == 0) *s_done = n_tile + 1;
               if (j + 1 < run.tiles) load_v(more);
               live = live_next;
             }
@@ -554,7 +573,7 @@ kv_prefill_kernel(const AttnParams p) {
         const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
         const uint32_t t_s = tmem + lanes + w * kPTile, t_o = tmem + lanes + 2 * kPTile + w * D;
         const float inv_G = 1.0f / static_cast<float>(p.G);
-        uint32_t ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
+        uint32_t ph_q = 0, ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
         int n_tile = 0;                                      // tiles before the run
         auto sync_half = [&]() {
           __syncwarp();
@@ -581,24 +600,42 @@ kv_prefill_kernel(const AttnParams p) {
             const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
             const int lo = p.window > 0 ? pos + 1 - p.window : 0;
             float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
+            constexpr int RL = D / 8, RI = 32 / RL;          // lanes of a row of bf16, rows the warp stores at once
             if (n_my > 0) {
-              // the row's query in fp16, scaled into its range, into the swizzled tile
-              const int dq = quotient();
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  p.q + (run.q0 + run.iq0 + dq) * p.q_stride + static_cast<int64_t>(head_of(dq)) * D);
+              // The half's query rows: copied raw into the tile, one bulk copy a row,
+              // then a row a thread, scaled into fp16's range, into the swizzled
+              // tile.  Vector f(i) of a row is its thread's i-th: with f(i) = i xor
+              // (x times the row) in GF(8), both f and f xor the row (the swizzle)
+              // take all values over eight rows: neither side has bank conflicts.
+              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
+              fence_proxy_async_smem();                      // (rows have left from there)
+              if (!sync_half()) return false;
+              const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on);
+              if (lane == 0) mbar_arrive_expect_tx(q_raw + w, __popc(rows_on) * D * 2);
+              __syncwarp();
+              if (on) {
+                const int dq = quotient();
+                bulk_load(tile + row * D * 2,
+                          p.q + (run.q0 + run.iq0 + dq) * p.q_stride + static_cast<int64_t>(head_of(dq)) * D, D * 2,
+                          q_raw + w);
+              }
+              if (!wait_all(q_raw + w, ph_q)) return false;
+              ph_q ^= 1u;
+              const int turn = ((row << 1) ^ (row & 4 ? 3 : 0)) & 7;
               uint4 u[D / 8];
               uint32_t big = 0;
 #pragma unroll
               for (int i = 0; i < D / 8; ++i) {
-                u[i] = on ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                u[i] = on ? *reinterpret_cast<const uint4*>(tile + row * D * 2 + ((i & 8) | ((i ^ turn) & 7)) * 16)
+                          : make_uint4(0u, 0u, 0u, 0u);
                 const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) big = max(big, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
               }
+              if (!sync_half()) return false;
               float up, down;
               query_scale(big, up, down);
               to_log2 = down * (p.scale_log2 * run.k_gsa);
-              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes + row * 128;
 #pragma unroll
               for (int i = 0; i < D / 8; ++i) {
                 const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
@@ -606,8 +643,8 @@ kv_prefill_kernel(const AttnParams p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
-                *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + (((i % 8) ^ (row & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + row * 128 +
+                                          (((i ^ turn ^ row) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
               }
               fence_proxy_async_smem();
               __syncwarp();
@@ -768,6 +805,29 @@ kv_prefill_kernel(const AttnParams p) {
             const int me = static_cast<int>(blockIdx.x) - run.first;
             float* part = part_at(me);
             const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
+            // The rows leave through shared memory (the query tile, now free; the
+            // handed-over rows, behind their reader), so that the warp stores whole
+            // lines: bf16 results in one pass, fp32 partial rows in two.  16-byte
+            // vectors are swizzled by the row inside every 128 bytes.
+            const int pitch = cross ? D * 4 : D * 2;
+            uint8_t* rows_at = smem + Sm::kQ + (cross ? 0 : w * Sm::kTileBytes) + wl * 32 * pitch;
+            const int64_t row_at = whole ? out_row() * D : static_cast<int64_t>(col) * D;
+            auto put_vector = [&](int i, uint4 v) {
+              *reinterpret_cast<uint4*>(rows_at + lane * pitch + (((i & ~7) | ((i ^ lane) & 7)) << 4)) = v;
+            };
+            // every row's RL vectors, to element `at` of each row's place
+            auto store_rows = [&](auto* base, int at, int per_vector) {
+              __syncwarp();
+#pragma unroll 2
+              for (int r0 = 0; r0 < 32; r0 += RI) {
+                const int r = r0 + lane / RL, i = lane % RL;
+                const int64_t to = __shfl_sync(0xFFFFFFFFu, row_at, r);
+                const bool there = __shfl_sync(0xFFFFFFFFu, static_cast<int>(on), r) != 0;
+                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + r * pitch + (((i & ~7) | ((i ^ r) & 7)) << 4));
+                if (there) *reinterpret_cast<uint4*>(base + to + at + i * per_vector) = v;
+              }
+              __syncwarp();
+            };
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float o[32];
@@ -782,9 +842,8 @@ kv_prefill_kernel(const AttnParams p) {
                   o[x + 3] = o[x + 3] * keep + y.w * other;
                 }
               }
-              if (on && whole) {
+              if (whole) {
                 // (a row that saw nothing has l = 0; what lies in its accumulator is finite)
-                uint4* dst = reinterpret_cast<uint4*>(p.out + out_row() * D + c);
 #pragma unroll
                 for (int x = 0; x < 32; x += 8) {
                   uint32_t h[4];
@@ -793,16 +852,17 @@ kv_prefill_kernel(const AttnParams p) {
                     const __nv_bfloat162 y = __floats2bfloat162_rn(o[x + 2 * k] * inv, o[x + 2 * k + 1] * inv);
                     h[k] = *reinterpret_cast<const uint32_t*>(&y);
                   }
-                  dst[x / 8] = make_uint4(h[0], h[1], h[2], h[3]);
+                  put_vector((c + x) / 8, make_uint4(h[0], h[1], h[2], h[3]));
                 }
-              } else if (on) {
+              } else {
 #pragma unroll
                 for (int x = 0; x < 32; x += 4)
-                  *reinterpret_cast<float4*>(part + 2 * NC + col * D + c + x) =
-                      make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                  put_vector((c % (D / 2) + x) / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
+                                                              __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+                if ((c + 32) % (D / 2) == 0) store_rows(part + 2 * NC, c + 32 - D / 2, 4);
               }
-              __syncwarp();                                  // (the next load is the whole warp's)
             }
+            if (whole) store_rows(p.out, 0, 8);
             tc_fence_before();
             if (cross) {
               __syncwarp();
@@ -842,7 +902,7 @@ kv_prefill_kernel(const AttnParams p) {
               }
               if (!sync_half()) return false;
               constexpr int V = D / 4;                       // vectors of a row
-              constexpr int K = 8;                           // vectors a thread has under way
+              constexpr int K = 4;                           // vectors a thread has under way
               for (int e0 = row; e0 < rows * V; e0 += K * kPTile) {
                 float4 acc[K];
 #pragma unroll
@@ -896,19 +956,17 @@ kv_prefill_kernel(const AttnParams p) {
               return true;
             };
             // tickets of chunk c: 4 c + 2 half, and the next one for the runs of parts
-            bool all = false;
-            if (run.n_parts <= kPJoinAlone) {
-              if (!last_of(p.tickets + 4 * run.first + 2 * w, run.n_parts, all)) return false;
-              if (all && !join_parts(0, run.n_parts, 1, true)) return false;
-            } else {
-              const int r0 = me / kPJoinRun * kPJoinRun, n_runs = (run.n_parts + kPJoinRun - 1) / kPJoinRun;
-              const int n = min(kPJoinRun, run.n_parts - r0);
-              if (!last_of(p.tickets + 4 * (run.first + r0) + 2 * w + 1, n, all)) return false;
-              if (all) {
-                if (!join_parts(r0, n, 1, false)) return false;
-                if (!last_of(p.tickets + 4 * run.first + 2 * w, n_runs, all)) return false;
-                if (all && !join_parts(0, n_runs, kPJoinRun, true)) return false;
-              }
+            const bool two = run.n_parts > kPJoinAlone;
+            const int r0 = two ? me / kPJoinRun * kPJoinRun : 0;
+#pragma unroll 1
+            for (int level = two ? 1 : 0; level >= 0; --level) {
+              const int i0 = level ? r0 : 0, step = two && !level ? kPJoinRun : 1;
+              const int n = level ? min(kPJoinRun, run.n_parts - r0)
+                                  : two ? (run.n_parts + kPJoinRun - 1) / kPJoinRun : run.n_parts;
+              bool all = false;
+              if (!last_of(p.tickets + 4 * (run.first + i0) + 2 * w + level, n, all)) return false;
+              if (!all) break;
+              if (!join_parts(i0, n, step, level == 0)) return false;
             }
             return true;
         };
