@@ -13,7 +13,7 @@ namespace nvr {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 // How a head's channels are paired by the rotation.
 enum : int {
@@ -39,18 +39,33 @@ struct AppendParams {
   int64_t n_slots;
   int page_shift;       // page_size == 1 << page_shift
   __nv_bfloat16* q_out;
-  int quads_q, quads_kv, parts;
+  int quads_q, quads_kv;           // groups of four heads
+  int parts_q, parts_kv;           // warps for a token's queries, its keys (values)
 };
 
+// Four channels as they lie in memory, and as two fp32 pairs.
 template <bool kBF16>
-__device__ __forceinline__ float4 load4(const void* base, int64_t at) {
-  if (kBF16) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
+struct Raw {
+  uint2 u;
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at));
   }
-  return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at));
-}
+  __device__ __forceinline__ void widen(uint64_t (&x)[2]) const {
+    x[0] = f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u));
+    x[1] = f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+  }
+};
+template <>
+struct Raw<false> {
+  float4 u;
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at));
+  }
+  __device__ __forceinline__ void widen(uint64_t (&x)[2]) const {
+    x[0] = f2_pack(u.x, u.y);
+    x[1] = f2_pack(u.z, u.w);
+  }
+};
 
 template <bool kBF16>
 __device__ __forceinline__ float load1(const void* base, int64_t at) {
@@ -58,197 +73,284 @@ __device__ __forceinline__ float load1(const void* base, int64_t at) {
   return __ldg(static_cast<const float*>(base) + at);
 }
 
-// One warp: `quads_per_part` groups of four heads of one token, eight lanes to
-// a head.  Lane l of the eight holds channels 4 l + 32 j + i (j < D / 32, i < 4):
-// the first levels of the norm's halving sum (D/2 .. 32 apart) and the usual
-// half pairs of the rotation are then inside one lane, 16, 8 and 4 apart are
-// lanes 4, 2 and 1 away, and a 16-channel scale block is four lanes.
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// a b + c d and a b - c d with every product rounded: scalar operations, which
+// are never contracted (a packed product feeding a packed sum was, nvcc 13.0).
+__device__ __forceinline__ uint64_t f2_mul_add_mul(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
+  return f2_pack(__fadd_rn(__fmul_rn(f2_lo(a), f2_lo(b)), __fmul_rn(f2_lo(c), f2_lo(d))),
+                 __fadd_rn(__fmul_rn(f2_hi(a), f2_hi(b)), __fmul_rn(f2_hi(c), f2_hi(d))));
+}
+__device__ __forceinline__ uint64_t f2_mul_sub_mul(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
+  return f2_pack(__fsub_rn(__fmul_rn(f2_lo(a), f2_lo(b)), __fmul_rn(f2_lo(c), f2_lo(d))),
+                 __fsub_rn(__fmul_rn(f2_hi(a), f2_hi(b)), __fmul_rn(f2_hi(c), f2_hi(d))));
+}
+
+__device__ __forceinline__ uint64_t shfl_xor2(uint64_t v, int d) {
+  return f2_pack(__shfl_xor_sync(0xFFFFFFFFu, f2_lo(v), d), __shfl_xor_sync(0xFFFFFFFFu, f2_hi(v), d));
+}
+
+// E2M1 codes of four values under the block scale s of global scale qs, the
+// quantizer's exact arithmetic; magnitudes are cut where the quotient is still
+// far from overflow (they saturate from 2688 gsa on).
+__device__ __noinline__ uint32_t codes4_exact(float4 v, float gsa, float s) {
+  const QuantScale qs = quant_scale_of(gsa);
+  const float cut = __fmul_rn(gsa, 4096.0f), rs = __frcp_rn(s);
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  float c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = div_rn_short(quant_divide(fmaxf(fminf(x[i], cut), -cut), qs), s, rs);
+  return e2m1_pack8(c[0], c[1], c[2], c[3], 0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+// A warp takes one token and a run of groups of four heads of its queries, keys
+// or values, eight lanes to a head.  Lane l of the eight holds channels
+// 4 l + 32 j + i (j < D / 32, i < 4): the first levels of the norm's halving sum
+// (D/2 .. 32 apart) and the usual half pairs of the rotation are then inside one
+// lane, 16, 8 and 4 apart are lanes 4, 2 and 1 away, and a 16-channel scale block
+// is four lanes.  Every operation is rounded by itself; the next group's loads are
+// under way meanwhile, the rows of the tables and the weights stay in registers.
 template <int D, bool kBF16, int kRot>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 6)
 kv_append_kernel(const AppendParams p) {
   constexpr int J = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, l8 = lane & 7, hq4 = lane >> 3;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / p.parts;
-  if (t >= p.T) return;
-  const int part = static_cast<int>(unit - t * p.parts);
-  const int n_quads = p.quads_q + 2 * p.quads_kv;
-  const int q0 = static_cast<int>(static_cast<int64_t>(n_quads) * part / p.parts);
-  const int q1 = static_cast<int>(static_cast<int64_t>(n_quads) * (part + 1) / p.parts);
-  const int64_t pos = p.rot ? __ldg(p.positions + t) : 0;
-  const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.n_pos);
-  const int64_t slot = pos_ok ? __ldg(p.slots + t) : -1;
-  const bool stored = slot >= 0 && slot < p.n_slots;
-  const int half = p.rot / 2;
-  const float* cosr = p.cos + (pos_ok ? pos : 0) * half;
-  const float* sinr = p.sin + (pos_ok ? pos : 0) * half;
+  int64_t unit = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  // section 0: queries, 1: keys, 2: values, one after the other over all tokens
+  // (the warps of a block then do equal work); this warp's groups [g0, g1)
+  const int64_t n_q = p.T * p.parts_q, n_kv = p.T * p.parts_kv;
+  const int sec = unit < n_q ? 0 : unit < n_q + n_kv ? 1 : 2;
+  if (unit >= n_q + 2 * n_kv) return;
+  unit -= sec == 0 ? 0 : n_q + (sec - 1) * n_kv;
+  const int64_t t = unit / (sec == 0 ? p.parts_q : p.parts_kv);
+  const int sub = static_cast<int>(unit - t * (sec == 0 ? p.parts_q : p.parts_kv));
+  const int groups = sec == 0 ? p.quads_q : p.quads_kv, parts = sec == 0 ? p.parts_q : p.parts_kv;
+  const int g0 = groups * sub / parts, g1 = groups * (sub + 1) / parts;
+  const int n_heads = sec == 0 ? p.Hq : p.Hkv;
+  const void* base = sec == 0 ? p.q : sec == 1 ? p.k : p.v;
+  const int64_t row = t * (sec == 0 ? p.q_stride : sec == 1 ? p.k_stride : p.v_stride) + 4 * l8;
+  int head = 4 * g0 + hq4;                       // of this lane; heads past the last read the first
+  Raw<kBF16> nxt[J];
+  auto load = [&](int h) {
+    const int64_t at = row + static_cast<int64_t>(h < n_heads ? h : 0) * D;
+#pragma unroll
+    for (int j = 0; j < J; ++j) nxt[j].load(base, at + 32 * j);
+  };
+  load(head);
 
-  // this lane's rows of the tables, kept over the heads of the token
+  const int64_t pos = p.rot ? __ldg(p.positions + t) : 0;
+  const int64_t slot = __ldg(p.slots + t);
+  const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.n_pos);
+  if (sec > 0 && (!pos_ok || slot < 0 || slot >= p.n_slots)) return;      // nothing is stored
+  const int half = p.rot / 2;
+  const float* weight = sec == 0 ? p.q_weight : sec == 1 ? p.k_weight : nullptr;
   constexpr int kCs = kRot == kRotHalf64 ? 2 : kRot == kRotHalf32 ? 1 : J;
-  float cs[kCs][4], sn[kCs][4];
+  uint64_t cs[kCs][2], sn[kCs][2]; // this lane's channels, pairs of neighbours
+  if (sec < 2) {
+    const float* cosr = p.cos + (pos_ok ? pos : 0) * half;
+    const float* sinr = p.sin + (pos_ok ? pos : 0) * half;
 #pragma unroll
-  for (int j = 0; j < kCs; ++j) {
-    if (kRot == kRotHalf32 || kRot == kRotHalf64) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cosr + 4 * l8 + 32 * j));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(sinr + 4 * l8 + 32 * j));
-      cs[j][0] = c.x; cs[j][1] = c.y; cs[j][2] = c.z; cs[j][3] = c.w;
-      sn[j][0] = s.x; sn[j][1] = s.y; sn[j][2] = s.z; sn[j][3] = s.w;
-    } else {
+    for (int j = 0; j < kCs; ++j) {
+      float c[4], s[4];
+      if (kRot == kRotHalf32 || kRot == kRotHalf64) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(cosr + 4 * l8 + 32 * j));
+        const float4 sv = __ldg(reinterpret_cast<const float4*>(sinr + 4 * l8 + 32 * j));
+        c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+        s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 4 * l8 + 32 * j + i;
-        const int f = kRot == kRotInterleaved ? e / 2 : (e < half ? e : e - half);
-        const bool on = e < p.rot;
-        cs[j][i] = on ? __ldg(cosr + f) : 1.0f;
-        sn[j][i] = on ? __ldg(sinr + f) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * l8 + 32 * j + i;
+          const int f = kRot == kRotInterleaved ? e / 2 : (e < half ? e : e - half);
+          const bool on = e < p.rot;
+          c[i] = on ? __ldg(cosr + f) : 1.0f;
+          s[i] = on ? __ldg(sinr + f) : 0.0f;
+          // interleaved: the even channel of a pair takes -sin of the odd one
+          if (kRot == kRotInterleaved && i % 2 == 0) s[i] = -s[i];
+        }
       }
+      cs[j][0] = f2_pack(c[0], c[1]); cs[j][1] = f2_pack(c[2], c[3]);
+      sn[j][0] = f2_pack(s[0], s[1]); sn[j][1] = f2_pack(s[2], s[3]);
     }
   }
 
-  for (int qd = q0; qd < q1; ++qd) {
-    // section 0: queries, 1: keys, 2: values
-    const int sec = qd < p.quads_q ? 0 : (qd < p.quads_q + p.quads_kv ? 1 : 2);
-    const int head = 4 * (qd - (sec == 0 ? 0 : sec == 1 ? p.quads_q : p.quads_q + p.quads_kv)) + hq4;
-    const int n_heads = sec == 0 ? p.Hq : p.Hkv;
-    const bool live = head < n_heads;
-    const void* base = sec == 0 ? p.q : sec == 1 ? p.k : p.v;
-    const int64_t row = t * (sec == 0 ? p.q_stride : sec == 1 ? p.k_stride : p.v_stride) +
-                        static_cast<int64_t>(live ? head : 0) * D;
-    float x[J][4];
+  // x of head h: norm and rotation
+  auto turn = [&](uint64_t (&x)[J][2], int h) {
+    float r = 1.0f;
+    if (weight) {
+      uint64_t u[J][2];                          // squares of chunks j and j + J / 2, added
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const float4 a = load4<kBF16>(base, row + 4 * l8 + 32 * j);
-      x[j][0] = a.x; x[j][1] = a.y; x[j][2] = a.z; x[j][3] = a.w;
+      for (int j = 0; j < J / 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          u[j][i] = f2_mul_add_mul(x[j][i], x[j][i], x[j + J / 2][i], x[j + J / 2][i]);
+#pragma unroll
+      for (int k = J / 4; k > 0; k >>= 1)
+#pragma unroll
+        for (int j = 0; j < k; ++j) {
+          u[j][0] = f2_add(u[j][0], u[j + k][0]);
+          u[j][1] = f2_add(u[j][1], u[j + k][1]);
+        }
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) {
+        u[0][0] = f2_add(u[0][0], shfl_xor2(u[0][0], d));
+        u[0][1] = f2_add(u[0][1], shfl_xor2(u[0][1], d));
+      }
+      const uint64_t two = f2_add(u[0][0], u[0][1]);
+      const float ss = __fadd_rn(f2_lo(two), f2_hi(two));
+      r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), p.eps)));
+      const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(weight + 4 * l8 + 32 * j));
+        x[j][0] = f2_mul(f2_mul(x[j][0], r2), f2_pack(w.x, w.y));
+        x[j][1] = f2_mul(f2_mul(x[j][1], r2), f2_pack(w.z, w.w));
+      }
     }
-    if (sec < 2) {
-      const float* weight = sec == 0 ? p.q_weight : p.k_weight;
-      float r = 1.0f;
-      if (weight) {
-        float s[4];
+    if (kRot == kRotHalf32 || kRot == kRotHalf64) {
+      constexpr int o = kRot == kRotHalf64 ? 2 : 1;
+#pragma unroll
+      for (int j = 0; j < (J >= 2 * o ? o : 0); ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t a = x[j][i], b = x[j + o][i];
+          x[j][i] = f2_mul_sub_mul(a, cs[j][i], b, sn[j][i]);
+          x[j + o][i] = f2_mul_add_mul(b, cs[j][i], a, sn[j][i]);
+        }
+    } else if (kRot == kRotInterleaved) {
+      // (a, b) -> (a c + b (-s), b c + a s)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t turned =
+              f2_mul_add_mul(x[j][i], cs[j][i], f2_pack(f2_hi(x[j][i]), f2_lo(x[j][i])), sn[j][i]);
+          if (4 * l8 + 32 * j + 2 * i < p.rot) x[j][i] = turned;
+        }
+    } else if (p.rot) {
+      // the partner channel is another lane's: read it again and put it through
+      // the same norm
+      const int64_t at = row - 4 * l8 + static_cast<int64_t>(h < n_heads ? h : 0) * D;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float u[J];
-#pragma unroll
-          for (int j = 0; j < J; ++j) u[j] = __fmul_rn(x[j][i], x[j][i]);
-#pragma unroll
-          for (int h = J / 2; h > 0; h >>= 1)
-#pragma unroll
-            for (int j = 0; j < h; ++j) u[j] = __fadd_rn(u[j], u[j + h]);
-          s[i] = u[0];
+          const int e = 4 * l8 + 32 * j + i;
+          const uint64_t xv = x[j][i / 2], cv = cs[j][i / 2], sv = sn[j][i / 2];
+          y[i] = i % 2 ? f2_hi(xv) : f2_lo(xv);
+          if (e < p.rot) {
+            const int f = e < half ? e + half : e - half;
+            float z = load1<kBF16>(base, at + f);
+            if (weight) z = __fmul_rn(__fmul_rn(z, r), __ldg(weight + f));
+            const float xc = __fmul_rn(y[i], i % 2 ? f2_hi(cv) : f2_lo(cv));
+            const float zs = __fmul_rn(z, i % 2 ? f2_hi(sv) : f2_lo(sv));
+            y[i] = e < half ? __fsub_rn(xc, zs) : __fadd_rn(xc, zs);
+          }
         }
-#pragma unroll
-        for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] = __fadd_rn(s[i], __shfl_xor_sync(0xFFFFFFFFu, s[i], d));
-        const float ss = __fadd_rn(__fadd_rn(s[0], s[2]), __fadd_rn(s[1], s[3]));
-        r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), p.eps)));
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(weight + 4 * l8 + 32 * j));
-          x[j][0] = __fmul_rn(__fmul_rn(x[j][0], r), w.x);
-          x[j][1] = __fmul_rn(__fmul_rn(x[j][1], r), w.y);
-          x[j][2] = __fmul_rn(__fmul_rn(x[j][2], r), w.z);
-          x[j][3] = __fmul_rn(__fmul_rn(x[j][3], r), w.w);
-        }
-      }
-      if (kRot == kRotHalf32 || kRot == kRotHalf64) {
-        constexpr int o = kRot == kRotHalf64 ? 2 : 1;
-#pragma unroll
-        for (int j = 0; j < (J >= 2 * o ? o : 0); ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[j][i], b = x[j + o][i];
-            x[j][i] = __fsub_rn(__fmul_rn(a, cs[j][i]), __fmul_rn(b, sn[j][i]));
-            x[j + o][i] = __fadd_rn(__fmul_rn(b, cs[j][i]), __fmul_rn(a, sn[j][i]));
-          }
-      } else if (kRot == kRotInterleaved) {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            if (4 * l8 + 32 * j + i < p.rot) {
-              const float a = x[j][i], b = x[j][i + 1];
-              x[j][i] = __fsub_rn(__fmul_rn(a, cs[j][i]), __fmul_rn(b, sn[j][i]));
-              x[j][i + 1] = __fadd_rn(__fmul_rn(b, cs[j][i]), __fmul_rn(a, sn[j][i]));
-            }
-          }
-      } else {
-        // the partner channel is another lane's: read it again and put it
-        // through the same norm
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 4 * l8 + 32 * j + i;
-            if (e < p.rot) {
-              const int f = e < half ? e + half : e - half;
-              float y = load1<kBF16>(base, row + f);
-              if (weight) y = __fmul_rn(__fmul_rn(y, r), __ldg(weight + f));
-              const float xc = __fmul_rn(x[j][i], cs[j][i]), ys = __fmul_rn(y, sn[j][i]);
-              x[j][i] = e < half ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
-            }
-          }
+        x[j][0] = f2_pack(y[0], y[1]);
+        x[j][1] = f2_pack(y[2], y[3]);
       }
     }
-    if (sec == 0) {
-      if (live) {
-        __nv_bfloat16* o = p.q_out + (t * p.Hq + head) * D + 4 * l8;
+  };
+
+  if (sec == 0) {
+    __nv_bfloat16* out = p.q_out + t * p.Hq * D + static_cast<int64_t>(head) * D + 4 * l8;
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+      uint64_t x[J][2];
+#pragma unroll
+      for (int j = 0; j < J; ++j) nxt[j].widen(x[j]);
+      const int now = head;
+      head += 4;
+      if (g + 1 < g1) load(head);
+      turn(x, now);
+      if (now < n_heads) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(x[j][0], x[j][1]), hi = __floats2bfloat162_rn(x[j][2], x[j][3]);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(f2_lo(x[j][0]), f2_hi(x[j][0])),
+                               hi = __floats2bfloat162_rn(f2_lo(x[j][1]), f2_hi(x[j][1]));
           uint2 u = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
           if (!pos_ok) u = make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(o + 32 * j) = u;
+          *reinterpret_cast<uint2*>(out + 32 * j) = u;
         }
       }
-      continue;
+      out += 4 * D;
     }
-    if (!stored) continue;                       // warp-uniform: one token per warp
-    const float gsa = __ldg((sec == 1 ? p.k_gsa : p.v_gsa) + (live ? head : 0));
+    return;
+  }
+
+  const int S = 1 << p.page_shift, tok = static_cast<int>(slot) & (S - 1);
+  // codes and scales of this token's first block; 16 channels on they are
+  // code_step and scale_step bytes further
+  const bool key = sec == 1;
+  const int code_at = key ? tok * KvPage<D>::kCodeRow : KvPage<D>::value_codes(S) + KvPage<D>::value_code(tok, 0);
+  const int scale_at = key ? KvPage<D>::key_scales(S) + tok * KvPage<D>::kScaleRow
+                           : KvPage<D>::value_scales(S) + KvPage<D>::value_scale(tok, 0);
+  const int code_step = key ? 8 : 64, scale_step = key ? 1 : 8;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    uint64_t x[J][2];
+#pragma unroll
+    for (int j = 0; j < J; ++j) nxt[j].widen(x[j]);
+    const int now = head;
+    head += 4;
+    if (g + 1 < g1) load(head);
+    if (key) turn(x, now);
+    const bool live = now < n_heads;
+    const float gsa = __ldg((key ? p.k_gsa : p.v_gsa) + (live ? now : 0));
     const QuantScale qs = quant_scale_of(gsa);
-    // beyond 2688 gsa every magnitude gets the largest scale and code: cut where
-    // the quotient is still far from overflow
-    const float cut = __fmul_rn(gsa, 4096.0f);
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] = fmaxf(fminf(x[j][i], cut), -cut);
-    const int S = 1 << p.page_shift, tok = static_cast<int>(slot) & (S - 1);
-    uint8_t* page = p.cache + ((slot >> p.page_shift) * p.Hkv + head) * KvPage<D>::bytes(S);
+    uint8_t* page = p.cache + ((slot >> p.page_shift) * p.Hkv + now) * KvPage<D>::bytes(S);
+    // The four lanes of a block have the largest magnitude of each of their J
+    // blocks; lane j of them finds the scale of block j.  RN(|x| / gsa) is
+    // monotone: a block's largest quotient is that of its largest magnitude.
+    float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      // RN(|x| / gsa) is monotone: the block's largest quotient is the quotient
-      // of its largest magnitude
-      float m = fmaxf(fmaxf(fabsf(x[j][0]), fabsf(x[j][1])), fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+      float m = fmaxf(fmaxf(fabsf(f2_lo(x[j][0])), fabsf(f2_hi(x[j][0]))),
+                      fmaxf(fabsf(f2_lo(x[j][1])), fabsf(f2_hi(x[j][1]))));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const uint32_t byte = quant_scale_byte(m, qs);
+      if ((l8 & 3) == j) amax = m;
+    }
+    const uint32_t my_byte = quant_scale_byte(fminf(amax, __fmul_rn(gsa, 4096.0f)), qs);
+    const float my_c = my_byte ? __fmul_rn(qs.rgsa, __frcp_rn(e4m3_value(my_byte))) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t byte = __shfl_sync(0xFFFFFFFFu, my_byte, (lane & ~3) + j);
+      const float c = __shfl_sync(0xFFFFFFFFu, my_c, (lane & ~3) + j);
       uint32_t code = 0;
       if (byte) {
-        const float s = e4m3_value(byte), rs = __frcp_rn(s);
-        float c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = div_rn_short(quant_divide(x[j][i], qs), s, rs);
-        code = e2m1_pack8(c[0], c[1], c[2], c[3], 0.0f, 0.0f, 0.0f, 0.0f);
+        // x c brackets the exact quotient when c is off by a little more than all
+        // roundings: equal codes on both sides are the exact ones (as in
+        // quant_block16_bracket)
+        const float c_lo = __fmul_rn(c, 0.99999904632568359375f), c_hi = __fmul_rn(c, 1.00000095367431640625f);
+        const uint64_t lo2 = f2_pack(c_lo, c_lo), hi2 = f2_pack(c_hi, c_hi);
+        const uint64_t a0 = f2_mul(x[j][0], lo2), a1 = f2_mul(x[j][1], lo2);
+        const uint64_t b0 = f2_mul(x[j][0], hi2), b1 = f2_mul(x[j][1], hi2);
+        code = e2m1_pack8(f2_lo(a0), f2_hi(a0), f2_lo(a1), f2_hi(a1), f2_lo(b0), f2_hi(b0), f2_lo(b1), f2_hi(b1));
+        const bool same = (code >> 16) == (code & 0xFFFFu) && qs.mode == 1;
+        code &= 0xFFFFu;
+        if (!same)
+          code = codes4_exact(make_float4(f2_lo(x[j][0]), f2_hi(x[j][0]), f2_lo(x[j][1]), f2_hi(x[j][1])), gsa,
+                              e4m3_value(byte));
         // the conversion gives +0 for a negative value that rounds to zero
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code |= (__float_as_uint(x[j][i]) >> 31) << (4 * i + 3);
+        code |= (__float_as_uint(f2_lo(x[j][0])) >> 31 << 3) | (__float_as_uint(f2_hi(x[j][0])) >> 31 << 7) |
+                (__float_as_uint(f2_lo(x[j][1])) >> 31 << 11) | (__float_as_uint(f2_hi(x[j][1])) >> 31 << 15);
       }
+      __syncwarp();
       // the block's eight code bytes to its first lane
       code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 16;
       const uint32_t hi = __shfl_down_sync(0xFFFFFFFFu, code, 2);
       if (live && (l8 & 3) == 0) {
         const int b = 2 * j + (l8 >> 2);
-        if (sec == 1) {
-          *reinterpret_cast<uint2*>(page + tok * KvPage<D>::kCodeRow + 8 * b) = make_uint2(code, hi);
-          page[KvPage<D>::key_scales(S) + tok * KvPage<D>::kScaleRow + b] = static_cast<uint8_t>(byte);
-        } else {
-          *reinterpret_cast<uint2*>(page + KvPage<D>::value_codes(S) + KvPage<D>::value_code(tok, b)) =
-              make_uint2(code, hi);
-          page[KvPage<D>::value_scales(S) + KvPage<D>::value_scale(tok, b)] = static_cast<uint8_t>(byte);
-        }
+        *reinterpret_cast<uint2*>(page + code_at + b * code_step) = make_uint2(code, hi);
+        page[scale_at + b * scale_step] = static_cast<uint8_t>(byte);
       }
     }
   }
@@ -387,13 +489,14 @@ extern "C" nvr_status nvfp4_kv_append(const void* q, int64_t q_stride, const voi
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.quads_q = (Hq + 3) / 4;
   p.quads_kv = (Hkv + 3) / 4;
-  // A warp takes a part of one token's groups of four heads.  While a group per
-  // warp does not fill the GPU (eight warps of work per scheduler), every
-  // group gets its own warp; beyond that a warp takes about five, so that the
-  // rows of the tables are loaded once for them.
+  // While a group of four heads per warp does not fill the GPU, every group gets
+  // its own warp (latency); beyond that a warp takes up to sixteen groups of queries,
+  // four of keys or of values, which share the rows of the tables and the weights.
   const int n_quads = p.quads_q + 2 * p.quads_kv;
-  p.parts = T * n_quads <= static_cast<int64_t>(sms) * 32 ? n_quads : (n_quads + 4) / 5;
-  const int64_t units = T * p.parts;
+  const bool few = T * n_quads <= static_cast<int64_t>(sms) * 32;
+  p.parts_q = few ? p.quads_q : (p.quads_q + 15) / 16;
+  p.parts_kv = few ? p.quads_kv : (p.quads_kv + 3) / 4;
+  const int64_t units = T * (p.parts_q + 2 * p.parts_kv);
   const int64_t blocks = (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   if (blocks > INT32_MAX) return NVR_ERR_UNSUPPORTED;
   int kind = kRotAny;

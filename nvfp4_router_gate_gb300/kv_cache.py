@@ -14,8 +14,10 @@ import math
 
 import torch
 
-from . import _dev, _dtype_code, _stream, new_workspace
+from . import _dtype_code, new_workspace, nvr_read_device_status
 from . import _native
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def nvfp4_kv_page_bytes(page_size, D):
@@ -27,146 +29,168 @@ def nvfp4_kv_attention_workspace_size(T_max, B_max, n_heads, n_kv_heads, D):
     return int(_native.lib().nvfp4_kv_attention_workspace_size(T_max, B_max, n_heads, n_kv_heads, D))
 
 
-def _page_size(cache, D):
-    """The page size of a cache [n_pages, n_kv_heads, page_bytes] uint8."""
-    if cache.dtype != torch.uint8 or cache.dim() != 3:
-        raise TypeError("cache must be uint8 [n_pages, n_kv_heads, page_bytes]")
-    return cache.shape[2] * 8 // (9 * D)
+def _raw_stream(stream):
+    """The stream's handle; the current stream of the current device for None
+    (its handle straight from torch: a Stream object costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _refuse(t, dtype, n, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() != n:
+        raise ValueError("%s has %d elements, not %d" % (name, t.numel(), n))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _ptr(t, dtype, n, name):
+    """Pointer of a contiguous CUDA tensor of n elements (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        _refuse(t, dtype, n, name)
+    return t.data_ptr()
 
 
 def _heads(t, name):
     """Pointer and token stride of [T, heads, D] with contiguous heads."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     T, H, D = t.shape
     s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+    if s[2] != 1 or (H > 1 and s[1] != D):
         raise ValueError("%s must have contiguous heads (a token stride is allowed)" % name)
     return t.data_ptr(), (s[0] if T > 1 else H * D)
 
 
-def _typed(t, dtype, name):
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    return _dev(t, name)
+class _Pages:
+    """A cache's geometry and pointers: checked once, used by every call."""
+
+    def __init__(self, cache, k_gsa, v_gsa, D):
+        if cache.dtype != _U8 or cache.dim() != 3:
+            raise TypeError("cache must be uint8 [n_pages, n_kv_heads, page_bytes]")
+        self.n_pages, self.Hkv, nbytes = cache.shape
+        self.D, self.S = D, nbytes * 8 // (9 * D)
+        self.data = _ptr(cache, _U8, cache.numel(), "cache")
+        self.k_gsa, self.v_gsa = _ptr(k_gsa, _F32, self.Hkv, "k_gsa"), _ptr(v_gsa, _F32, self.Hkv, "v_gsa")
 
 
-def _length(t, n, name):
-    if t.numel() != n:
-        raise ValueError("%s has %d elements, not %d" % (name, t.numel(), n))
-
-
-def nvfp4_kv_append(q, k, v, positions, slots, cos, sin, cache, k_gsa, v_gsa, q_weight=None, k_weight=None,
-                    eps=1e-6, interleaved=False, q_out=None, stream=None):
-    """RMS norm of the heads of q [T, Hq, D] and k [T, Hkv, D] (where a weight
-    is given), rotary positions, and k and v quantized into the cache's slots.
-    cos and sin are [n_pos, rot/2] (None: no rotation); returns q_out [T, Hq, D]
-    bf16 (None for q None)."""
+def _append(pages, q, k, v, positions, slots, cos, sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+            q_out=None, stream=None):
     T, Hkv, D = k.shape
-    if tuple(v.shape) != (T, Hkv, D) or v.dtype != k.dtype:
+    if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have one shape and type")
+    if Hkv != pages.Hkv or D != pages.D:
+        raise ValueError("the cache holds %d KV heads of %d channels, k has %d of %d" % (pages.Hkv, pages.D, Hkv, D))
     kp, ks = _heads(k, "k")
     vp, vs = _heads(v, "v")
     Hq, qp, qs, op = 0, None, 0, None
     if q is not None:
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
             raise ValueError("q must be [T, heads, D] of k's type")
+        Hq = q.shape[1]
         qp, qs = _heads(q, "q")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=k.device)
-        op = _typed(q_out, torch.bfloat16, "q_out")
-        _length(q_out, T * Hq * D, "q_out")
-    S = _page_size(cache, D)
-    if cache.shape[1] != Hkv:
-        raise ValueError("the cache has %d KV heads, k has %d" % (cache.shape[1], Hkv))
-    _length(slots, T, "slots")
-    _length(k_gsa, Hkv, "k_gsa")
-    _length(v_gsa, Hkv, "v_gsa")
-    rot, n_pos = 0, 0
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=k.device)
+        op = _ptr(q_out, _BF16, T * Hq * D, "q_out")
+    rot = n_pos = 0
     if cos is not None:
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        if sin.shape != cos.shape:
-            raise ValueError("cos and sin must have one shape")
-        _length(positions, T, "positions")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _length(w, D, name)
-    f32, i32 = torch.float32, torch.int32
+        n_pos, half = cos.shape
+        rot = 2 * half
+        if sin is None or positions is None:
+            raise ValueError("cos needs sin and positions")
+    n = n_pos * rot // 2
     st = _native.lib().nvfp4_kv_append(
-        qp, qs, kp, ks, vp, vs, _dtype_code(k), T, Hq, Hkv, D, _typed(positions, i32, "positions"),
-        _typed(slots, i32, "slots"), _typed(cos, f32, "cos"), _typed(sin, f32, "sin"), n_pos, rot, int(interleaved),
-        _typed(q_weight, f32, "q_weight"), _typed(k_weight, f32, "k_weight"), float(eps),
-        _typed(k_gsa, f32, "k_gsa"), _typed(v_gsa, f32, "v_gsa"), _dev(cache, "cache"), cache.shape[0], S, op,
-        _stream(stream))
-    _native.check("nvfp4_kv_append", st)
+        qp, qs, kp, ks, vp, vs, _dtype_code(k), T, Hq, Hkv, D,
+        _ptr(positions, _I32, T, "positions") if rot else None, _ptr(slots, _I32, T, "slots"),
+        _ptr(cos, _F32, n, "cos"), _ptr(sin, _F32, n, "sin") if rot else None, n_pos, rot, interleaved,
+        _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight"), eps, pages.k_gsa, pages.v_gsa,
+        pages.data, pages.n_pages, pages.S, op, _raw_stream(stream))
+    if st:
+        _native.check("nvfp4_kv_append", st)
     return q_out
 
 
-def nvfp4_kv_gather(cache, slots, k_gsa, v_gsa, D, out_dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
-    """The values that the slots stand for: k and v [n, Hkv, D] (zeros for a
-    slot outside the cache)."""
-    n, Hkv = slots.numel(), cache.shape[1]
-    if k_out is None:
-        k_out = torch.empty((n, Hkv, D), dtype=out_dtype, device=cache.device)
-    if v_out is None:
-        v_out = torch.empty((n, Hkv, D), dtype=k_out.dtype, device=cache.device)
-    if v_out.dtype != k_out.dtype:
-        raise TypeError("k_out and v_out must have one type")
-    for t, m, name in ((k_out, n * Hkv * D, "k_out"), (v_out, n * Hkv * D, "v_out"), (k_gsa, Hkv, "k_gsa"),
-                       (v_gsa, Hkv, "v_gsa")):
-        _length(t, m, name)
+def nvfp4_kv_append(q, k, v, positions, slots, cos, sin, cache, k_gsa, v_gsa, **kw):
+    """RMS norm of the heads of q [T, Hq, D] and k [T, Hkv, D] (where q_weight,
+    k_weight [D] are given, with eps=1e-6), rotary positions, and k and v
+    quantized into the cache's slots.  cos and sin are [n_pos, rot/2] (None: no
+    rotation), paired by halves or interleaved=True; returns q_out [T, Hq, D] bf16
+    (None for q None)."""
+    return _append(_Pages(cache, k_gsa, v_gsa, k.shape[2]), q, k, v, positions, slots, cos, sin, **kw)
+
+
+def _gather(pages, slots, out_dtype=_BF16, k_out=None, v_out=None, stream=None):
+    n = slots.numel()
+    if k_out is None and v_out is None:
+        shape, dev = (n, pages.Hkv, pages.D), slots.device
+        k_out, v_out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+    elif k_out is None or v_out is None:
+        raise ValueError("pass both k_out and v_out, or neither")
+    m, dt = n * pages.Hkv * pages.D, k_out.dtype
     st = _native.lib().nvfp4_kv_gather(
-        _dev(cache, "cache"), cache.shape[0], _page_size(cache, D), Hkv, D, _typed(slots, torch.int32, "slots"), n,
-        _typed(k_gsa, torch.float32, "k_gsa"), _typed(v_gsa, torch.float32, "v_gsa"), _dev(k_out, "k_out"),
-        _dev(v_out, "v_out"), _dtype_code(k_out), _stream(stream))
-    _native.check("nvfp4_kv_gather", st)
+        pages.data, pages.n_pages, pages.S, pages.Hkv, pages.D, _ptr(slots, _I32, n, "slots"), n, pages.k_gsa,
+        pages.v_gsa, _ptr(k_out, dt, m, "k_out"), _ptr(v_out, dt, m, "v_out"), _dtype_code(k_out),
+        _raw_stream(stream))
+    if st:
+        _native.check("nvfp4_kv_gather", st)
     return k_out, v_out
 
 
-def nvfp4_kv_attention(q, cache, page_table, kv_lens, k_gsa, v_gsa, cu_q=None, max_q=None, scale=None, causal=True,
-                       window=0, out=None, lse=None, workspace=None, stream=None):
-    """Attention of q [T, Hq, D] bf16 over the cached tokens of the sequences
-    in page_table [B, max_pages] and kv_lens [B].  cu_q [B + 1] (with max_q, the
-    most queries of a sequence) gives each sequence's rows of q; without it every
-    sequence has T / B queries.  Returns (out [T, Hq, D] bf16, lse); lse [T, Hq]
-    fp32 is written when it is given."""
+def nvfp4_kv_gather(cache, slots, k_gsa, v_gsa, D, **kw):
+    """The values that the slots stand for: k and v [n, Hkv, D] of out_dtype
+    (bfloat16 or float32) or into k_out and v_out; zeros for a slot outside the
+    cache."""
+    return _gather(_Pages(cache, k_gsa, v_gsa, D), slots, **kw)
+
+
+def _attend(pages, q, page_table, kv_lens, cu_q=None, max_q=None, scale=None, causal=True, window=0, out=None,
+            lse=None, workspace=None, ws=None, stream=None):
     T, Hq, D = q.shape
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    if D != pages.D:
+        raise ValueError("the cache holds heads of %d channels, q has %d" % (pages.D, D))
     B, max_pages = page_table.shape
-    Hkv = cache.shape[1]
     if cu_q is None:
         if B == 0 or T % B:
             raise ValueError("%d queries for %d sequences: pass cu_q" % (T, B))
         max_q = T // B
-    else:
-        _length(cu_q, B + 1, "cu_q")
-        if max_q is None:
-            raise ValueError("cu_q needs max_q, the most queries of a sequence")
-    _length(kv_lens, B, "kv_lens")
-    _length(k_gsa, Hkv, "k_gsa")
-    _length(v_gsa, Hkv, "v_gsa")
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _length(out, T * Hq * D, "out")
-    if lse is not None:
-        _length(lse, T * Hq, "lse")
-    if workspace is None:
-        workspace = new_workspace(nvfp4_kv_attention_workspace_size(T, B, Hq, Hkv, D), q.device)
+    elif max_q is None:
+        raise ValueError("cu_q needs max_q, the most queries of a sequence")
     qp, qs = _heads(q, "q")
-    f32, i32 = torch.float32, torch.int32
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+    if ws is None:
+        nbytes = workspace.numel()
+        ws = _ptr(workspace, _U8, nbytes, "workspace"), nbytes
     st = _native.lib().nvfp4_kv_attention(
-        qp, qs, T, Hq, Hkv, D, _dev(cache, "cache"), cache.shape[0], _page_size(cache, D),
-        _typed(page_table, i32, "page_table"), B, max_pages, _typed(kv_lens, i32, "kv_lens"),
-        _typed(cu_q, i32, "cu_q"), int(max_q), _typed(k_gsa, f32, "k_gsa"), _typed(v_gsa, f32, "v_gsa"),
-        float(D ** -0.5 if scale is None else scale), int(causal), int(window),
-        _typed(out, torch.bfloat16, "out"), _typed(lse, f32, "lse"), _dev(workspace, "workspace"),
-        workspace.numel(), _stream(stream))
-    _native.check("nvfp4_kv_attention", st)
+        qp, qs, T, Hq, pages.Hkv, D, pages.data, pages.n_pages, pages.S,
+        _ptr(page_table, _I32, B * max_pages, "page_table"), B, max_pages, _ptr(kv_lens, _I32, B, "kv_lens"),
+        _ptr(cu_q, _I32, B + 1, "cu_q"), max_q, pages.k_gsa, pages.v_gsa, D ** -0.5 if scale is None else scale,
+        causal, window, _ptr(out, _BF16, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1],
+        _raw_stream(stream))
+    if st:
+        _native.check("nvfp4_kv_attention", st)
     return out, lse
+
+
+def nvfp4_kv_attention(q, cache, page_table, kv_lens, k_gsa, v_gsa, workspace=None, **kw):
+    """Attention of q [T, Hq, D] bf16 over the cached tokens of the sequences
+    in page_table [B, max_pages] and kv_lens [B].  cu_q [B + 1] (with max_q, the
+    most queries of a sequence) gives each sequence's rows of q; without it every
+    sequence has T / B queries.  scale defaults to D ** -0.5, causal to True,
+    window to 0 (none).  Returns (out [T, Hq, D] bf16, lse); lse [T, Hq] fp32 is
+    written when it is given."""
+    T, Hq, D = q.shape
+    if q.dtype is not _BF16:
+        raise TypeError("q must be bfloat16, got %s" % q.dtype)
+    if workspace is None:
+        workspace = new_workspace(nvfp4_kv_attention_workspace_size(T, page_table.shape[0], Hq, cache.shape[1], D),
+                                  q.device)
+    return _attend(_Pages(cache, k_gsa, v_gsa, D), q, page_table, kv_lens, workspace=workspace, **kw)
 
 
 class Nvfp4KVCache:
@@ -196,6 +220,9 @@ class Nvfp4KVCache:
         self.n_heads = int(n_heads or n_kv_heads)
         self.workspace = new_workspace(nvfp4_kv_attention_workspace_size(
             self.max_tokens, self.max_seqs, self.n_heads, self.n_kv_heads, self.head_dim), dev)
+        # (the buffers are this object's: checked once)
+        self._pages = _Pages(self.data, self.k_gsa, self.v_gsa, self.head_dim) if self.data.is_cuda else None
+        self._ws = self.workspace.data_ptr(), self.workspace.numel()
 
     def _scale(self, g, dev):
         if not isinstance(g, torch.Tensor):
@@ -204,23 +231,29 @@ class Nvfp4KVCache:
 
     def append(self, q, k, v, positions, slots, cos, sin, **kw):
         """nvfp4_kv_append into this cache."""
-        return nvfp4_kv_append(q, k, v, positions, slots, cos, sin, self.data, self.k_gsa, self.v_gsa, **kw)
+        if self._pages is None:
+            raise ValueError("the cache must be on a GPU")
+        return _append(self._pages, q, k, v, positions, slots, cos, sin, **kw)
 
     def gather(self, slots, **kw):
         """nvfp4_kv_gather from this cache."""
-        return nvfp4_kv_gather(self.data, slots, self.k_gsa, self.v_gsa, self.head_dim, **kw)
+        if self._pages is None:
+            raise ValueError("the cache must be on a GPU")
+        return _gather(self._pages, slots, **kw)
 
     def attend(self, q, page_table, kv_lens, **kw):
         """nvfp4_kv_attention over this cache."""
         if q.shape[0] > self.max_tokens or page_table.shape[0] > self.max_seqs or q.shape[1] != self.n_heads:
             raise ValueError("%d tokens of %d heads in %d sequences: the workspace is for %d, %d and %d" % (
                 q.shape[0], q.shape[1], page_table.shape[0], self.max_tokens, self.n_heads, self.max_seqs))
-        return nvfp4_kv_attention(q, self.data, page_table, kv_lens, self.k_gsa, self.v_gsa,
-                                  workspace=self.workspace, **kw)
+        if q.dtype is not _BF16:
+            raise TypeError("q must be bfloat16, got %s" % q.dtype)
+        if self._pages is None:
+            raise ValueError("the cache must be on a GPU")
+        return _attend(self._pages, q, page_table, kv_lens, ws=self._ws, **kw)
 
     def status(self, stream=None):
         """The workspace status word (0 ok, 6: a bounded wait timed out)."""
-        from . import nvr_read_device_status
         return nvr_read_device_status(self.workspace, stream)
 
 
