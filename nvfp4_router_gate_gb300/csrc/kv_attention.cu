@@ -33,8 +33,6 @@ namespace nvr {
 namespace {
 
 constexpr int kStreamCols = 16;            // more columns of a sequence go to the tensor-memory kernel
-constexpr int kJoinAlone = 40;             // parts of a key that one block joins at once
-constexpr int kJoinRun = 16;               // beyond that, the parts joined first
 // Starting and ending a key costs a block about as much as this many tiles
 // (queries, joining the warps, storing): counted in the chunks, so that blocks
 // with many short keys get fewer tiles.
@@ -46,15 +44,16 @@ __device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.til
 // What a stage of the ring holds (everything about its key, so that nothing of
 // it stays in the consumers' registers); a run's first stage brings the queries.
 struct alignas(16) Meta {
-  uint32_t flags;             // kFirst, kLast, kEdge
+  uint32_t flags;
   uint32_t live;              // bit i: tokens 16 i .. 16 i + 15 of the tile were loaded
   int tile, head;
-  int key_f0, key_tiles;      // the key's place in the flat order of tiles
   int kv, n_q, q0, iq0, rem0, n_cols;   // the first column is head rem0 of the group's query iq0
   float k_gsa, v_gsa;
   int pad[2];
 };
-constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4;
+// a run's first and last tile; a tile that some column does not see whole; the
+// run is all of its key; the block's last run; the key starts inside the chunk
+constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4, kWhole = 8, kDone = 16, kTail = 32;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -107,7 +106,6 @@ kv_attention_kernel(const AttnParams p) {
   uint64_t* join_free = meet + 1;                            // the join buffer has been read
   int* s_start = reinterpret_cast<int*>(meet + 2);           // item, offset inside it, whether the chunk has work
   volatile int* abort_flag = s_start + 4;
-  int* s_flag = s_start + 5;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -160,6 +158,7 @@ kv_attention_kernel(const AttnParams p) {
     s_start[2] = ti < g.tiles || f1 - f0 > key_cost(g) - ti;
   }
   __syncthreads();
+  if (tid == 32 * NW) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
   if (f0 >= f1 || !s_start[2]) return;
 
   if (warp == NW) {
@@ -220,34 +219,37 @@ kv_attention_kernel(const AttnParams p) {
         if (lane == 0) {
           Meta m = {};
           m.head = head; m.tile = g.tile0 + ti;
-          m.key_f0 = f - ti; m.key_tiles = g.tiles;
+          const int key_f0 = f - ti, key_end = key_f0 + g.tiles;
           m.kv = g.kv; m.n_q = g.n_q; m.q0 = g.q0; m.iq0 = iq0; m.rem0 = rem0; m.n_cols = g.n_cols;
           m.k_gsa = k_gsa; m.v_gsa = v_gsa;
           const uint32_t each = (1u << (part / 16)) - 1;
           m.live = 0;
           for (int i = 0; i < pieces; ++i)
             if ((got >> i) & 1u) m.live |= each << (i * (part / 16));
-          m.flags = (first ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u);
+          m.flags = (first ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u) |
+                    (key_f0 >= f0 && key_end <= f1 ? kWhole : 0u) | (key_end + kKeyCost >= f1 ? kDone : 0u) |
+                    (key_f0 > f0 ? kTail : 0u);
+          if (key_f0 >= f0 && key_end > f1 && first)         // this block holds the key's first part
+            p.joins[blockIdx.x] = {(key_end - 1) / chunk - key_f0 / chunk + 1, key_f0 > f0, g.q0 + iq0, rem0, g.n_cols,
+                                   head, v_gsa, 0};
           if (t0 + TILE > sure_hi || t0 < sure_lo || got != (1u << pieces) - 1u) m.flags |= kEdge;
           s_meta[st] = m;
           mbar_arrive_expect_tx(full + st, __popc(got) * part * (D * 9 / 8) + (first ? g.n_cols * D * 2 : 0));
         }
         __syncwarp();
         if (have) {
-          uint8_t* dst = smem + st * Sh::kStageBytes + lane * part * (D * 9 / 8);
+          // the four regions of the page (or of the part of it in this tile) into
+          // those of the tile: every lane's place in a stage is then a constant
+          uint8_t* dst = smem + st * Sh::kStageBytes;
           const uint8_t* src = p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * KvPage<D>::bytes(S);
-          if (S <= TILE) {
-            bulk_load(dst, src, KvPage<D>::bytes(S), full + st);
-          } else {
-            const int o = pt & (S - 1);
-            bulk_load(dst, src + o * KvPage<D>::kCodeRow, part * KvPage<D>::kCodeRow, full + st);
-            bulk_load(dst + KvPage<D>::key_scales(part), src + KvPage<D>::key_scales(S) + o * KvPage<D>::kScaleRow,
-                      part * KvPage<D>::kScaleRow, full + st);
-            bulk_load(dst + KvPage<D>::value_codes(part), src + KvPage<D>::value_codes(S) + o * KvPage<D>::kCodeRow,
-                      part * KvPage<D>::kCodeRow, full + st);
-            bulk_load(dst + KvPage<D>::value_scales(part), src + KvPage<D>::value_scales(S) + o * KvPage<D>::kScaleRow,
-                      part * KvPage<D>::kScaleRow, full + st);
-          }
+          const int o = pt & (S - 1), d = lane * part;
+          bulk_load(dst + d * KvPage<D>::kCodeRow, src + o * KvPage<D>::kCodeRow, part * KvPage<D>::kCodeRow, full + st);
+          bulk_load(dst + KvPage<D>::key_scales(TILE) + d * KvPage<D>::kScaleRow,
+                    src + KvPage<D>::key_scales(S) + o * KvPage<D>::kScaleRow, part * KvPage<D>::kScaleRow, full + st);
+          bulk_load(dst + KvPage<D>::value_codes(TILE) + d * KvPage<D>::kCodeRow,
+                    src + KvPage<D>::value_codes(S) + o * KvPage<D>::kCodeRow, part * KvPage<D>::kCodeRow, full + st);
+          bulk_load(dst + KvPage<D>::value_scales(TILE) + d * KvPage<D>::kScaleRow,
+                    src + KvPage<D>::value_scales(S) + o * KvPage<D>::kScaleRow, part * KvPage<D>::kScaleRow, full + st);
         }
         if (first) {
           // the columns of one query are heads next to each other: lane i
@@ -282,18 +284,12 @@ kv_attention_kernel(const AttnParams p) {
 
   // ---------------------------------------------------------------- consumers
   const int r = lane >> 2, c = lane & 3;
-  const int S = 1 << p.page_shift, part = min(S, TILE);
-  // this warp's groups of 16 tokens inside a stage
-  int k_codes_at[MW], k_scales_at[MW], v_codes_at[MW], v_scales_at[MW];
-#pragma unroll
-  for (int u = 0; u < MW; ++u) {
-    const int t = (warp * MW + u) * 16;
-    const int piece_at = t / part * part * (D * 9 / 8), in_piece = t % part;
-    k_codes_at[u] = piece_at + in_piece * (D / 2);
-    k_scales_at[u] = piece_at + KvPage<D>::key_scales(part) + in_piece * (D / 16);
-    v_codes_at[u] = piece_at + KvPage<D>::value_codes(part) + in_piece * (D / 2);
-    v_scales_at[u] = piece_at + KvPage<D>::value_scales(part) + in_piece * (D / 16);
-  }
+  // this lane's places in a stage, for the warp's first 16 tokens (the other
+  // tokens and fragments are constants further): key codes, both scales, value codes
+  const int codes_at = warp * MW * 16 * (D / 2) + lane * (D / 8);
+  const int scales_at = warp * MW * 16 * (D / 16) + (D == 128 ? 2 * lane : lane);
+  const int v_codes_at = warp * MW * 16 * (D / 2) + (D == 128 ? lane * 16 : (r >> 1) * 64 + c * 16 + (r & 1) * 4);
+  const int v_scales_at = warp * MW * 16 * (D / 16) + (D == 128 ? 2 * lane : (r >> 1) * 8 + 2 * c);
 
   float o[NT][MT][4];
   float m_neg[NT][2], l_run[NT][2], to_log2[NT][2];         // -m: +inf until a token is seen
@@ -320,7 +316,6 @@ kv_attention_kernel(const AttnParams p) {
     if (!__all_sync(0xFFFFFFFFu, wait_bounded(full + st, parity, abort_flag))) return give_up();
     const Meta& meta = s_meta[st];
     const uint32_t flags = meta.flags;
-    const int tile = meta.tile;
     if (flags & kFirst) {
       const int n_cols = meta.n_cols;
       const float k_gsa = meta.k_gsa;
@@ -384,15 +379,16 @@ kv_attention_kernel(const AttnParams p) {
           for (int i = 0; i < 4; ++i) s[u][nt][i] = s1[u][nt][i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const int tok = 16 * u + 8 * i;                    // of the warp's, for lane row 0
           if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + k_codes_at[u] + (r + 8 * i) * 64 + c * 16);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + codes_at + tok * 64);
             kc[u][i][0] = x.x; kc[u][i][1] = x.y; kc[u][i][D / 32 - 2] = x.z; kc[u][i][D / 32 - 1] = x.w;
-            sc[u][i] =
-                e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(stage + k_scales_at[u] + (r + 8 * i) * 8 + 2 * c));
+            sc[u][i] = e4m3x2_to_f16(
+                *reinterpret_cast<const uint16_t*>(stage + KvPage<D>::key_scales(TILE) + scales_at + tok * 8));
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(stage + k_codes_at[u] + (r + 8 * i) * 32 + c * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(stage + codes_at + tok * 32);
             kc[u][i][0] = x.x; kc[u][i][1] = x.y;
-            const uint32_t b = stage[k_scales_at[u] + (r + 8 * i) * 4 + c];
+            const uint32_t b = stage[KvPage<D>::key_scales(TILE) + scales_at + tok * 4];
             sc[u][i] = e4m3x2_to_f16(b | (b << 8));
           }
         }
@@ -422,7 +418,6 @@ kv_attention_kernel(const AttnParams p) {
         }
       }
       // ------------------------------------------------------ running softmax
-      const int t = tile * TILE + warp * MW * 16 + r;        // token of s[0][.][0..1]; t + 8: s[0][.][2..3]
       float v[MW][NT][4];                                    // scores relative to m, base 2
       auto relative = [&]() {
 #pragma unroll
@@ -432,6 +427,8 @@ kv_attention_kernel(const AttnParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[u][nt][i] = fmaf(s[u][nt][i], to_log2[nt][i & 1], m_neg[nt][i & 1]);
         if (flags & kEdge) {
+          // token of v[0][.][0..1]; t + 8: v[0][.][2..3]
+          const int t = meta.tile * TILE + warp * MW * 16 + r;
           const int n_cols = meta.n_cols, kv = meta.kv, first = kv - meta.n_q + meta.iq0, rem0 = meta.rem0;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -517,23 +514,23 @@ kv_attention_kernel(const AttnParams p) {
         uint32_t lo[2][D / 64], hi[2][D / 64];               // even, odd channels; bytes: channel pairs
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int blk = D == 128 ? r : r >> 1;
+          const int tok = 16 * u + 8 * i;
           sv[i] = e4m3x2_to_f16(
-              *reinterpret_cast<const uint16_t*>(stage + v_scales_at[u] + i * (8 * D / 16) + blk * 8 + 2 * c));
+              *reinterpret_cast<const uint16_t*>(stage + KvPage<D>::value_scales(TILE) + v_scales_at + tok * (D / 16)));
           if (flags & kEdge) {
             // a masked token's weight is 0; its scale must not be a NaN
-            const int tv = tile * TILE + (warp * MW + u) * 16 + 8 * i + 2 * c, kv = meta.kv;
+            const int tv = meta.tile * TILE + warp * MW * 16 + tok + 2 * c, kv = meta.kv;
             if (tv >= kv || !((live >> u) & 1u)) sv[i] = 0;
             else if (tv + 1 >= kv) sv[i] &= 0xFFFFu;
           }
-          const uint8_t* vc = stage + v_codes_at[u] + i * (8 * D / 2);
+          const uint8_t* vc = stage + KvPage<D>::value_codes(TILE) + v_codes_at + tok * (D / 2);
           uint32_t x[D / 64], y[D / 64];                     // token 2c, token 2c + 1
           if (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vc + lane * 16);
+            const uint4 w = *reinterpret_cast<const uint4*>(vc);
             x[0] = w.x; x[D / 64 - 1] = w.y; y[0] = w.z; y[D / 64 - 1] = w.w;
           } else {
-            x[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + (r & 1) * 4);
-            y[0] = *reinterpret_cast<const uint32_t*>(vc + blk * 64 + c * 16 + 8 + (r & 1) * 4);
+            x[0] = *reinterpret_cast<const uint32_t*>(vc);
+            y[0] = *reinterpret_cast<const uint32_t*>(vc + 8);
           }
 #pragma unroll
           for (int k = 0; k < D / 64; ++k) {
@@ -561,17 +558,17 @@ kv_attention_kernel(const AttnParams p) {
         }
       }
     }
-    const bool run_ends = flags & kLast;
-    const int head = meta.head, key_f0 = meta.key_f0, key_tiles = meta.key_tiles, n_cols = meta.n_cols;
-    const int q0 = meta.q0 + meta.iq0, rem0 = meta.rem0;
-    const float v_gsa = meta.v_gsa;
+    int head = 0, q0 = 0, rem0 = 0, n_cols = 0;
+    float v_gsa = 0.0f;
+    if (flags & kLast) {
+      q0 = meta.q0 + meta.iq0; head = meta.head; rem0 = meta.rem0; n_cols = meta.n_cols; v_gsa = meta.v_gsa;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + st);
     if (++st == STAGES) { st = 0; parity ^= 1u; }
-    if (!run_ends) continue;
+    if (!(flags & kLast)) continue;
     // ------------------------------------------------ end of a run of a key
-    // the last run of the chunk is one that ends with it, or with the last key's tiles before it
-    more = key_f0 + key_tiles + kKeyCost < f1;
+    more = !(flags & kDone);
     // join the warps: every warp gives the others their shares of its O registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -583,9 +580,9 @@ kv_attention_kernel(const AttnParams p) {
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
         l_run[nt][i] = l;
       }
-    const bool whole = key_f0 >= f0 && key_f0 + key_tiles <= f1;
+    const bool whole = flags & kWhole;
     // a key's run: slot 0 when it starts with the chunk, else 1 (it ends it)
-    const int slot = 2 * blockIdx.x + (key_f0 > f0 ? 1 : 0);
+    const int slot = 2 * blockIdx.x + (flags & kTail ? 1 : 0);
     float* part_m = p.partials + static_cast<size_t>(slot) * NC * (D + 2);
     float* part_l = part_m + NC;
     float* part_o = part_l + NC;                             // [NC][D]
@@ -672,115 +669,18 @@ kv_attention_kernel(const AttnParams p) {
           p.lse[row] = sum[i] > 0.0f ? (top[i] + log2f(sum[i])) * 0.693147180559945309f : -INFINITY;
       }
     }
-    if (whole) continue;
-
-    // ------------------------------------------------ join the chunks of a key
-    // Part i lies in the first slot of chunk first + i, but the first part of
-    // a key that starts inside its chunk.  The last chunk to arrive joins all
-    // parts; of more than kJoinAlone parts, runs of kJoinRun are joined first,
-    // each by its last chunk, into the run's first part.
-    const int first = key_f0 / chunk, n_parts = (key_f0 + key_tiles - 1) / chunk - first + 1;
-    const int tail = key_f0 > static_cast<int64_t>(first) * chunk ? 1 : 0;
-    const int me = static_cast<int>(blockIdx.x) - first;
-    auto part_at = [&](int i) {
-      return p.partials + static_cast<size_t>(2 * (first + i) + (i == 0 ? tail : 0)) * NC * (D + 2);
-    };
-    // 32 NW / NC lanes share a column: each takes D / lanes channels, and looks
-    // after the (m, l) of every lanes-th part
-    auto join_parts = [&](int i0, int n, int step, bool store) {
-      constexpr int LC = 32 * NW / NC, CH = D / LC;
-      static_assert(LC <= 32 && CH % 4 == 0, "columns divide the warps");
-      const int n_col = tid / LC, sub = tid % LC;
-      float top = -INFINITY;
-      for (int i = sub; i < n; i += LC) top = fmaxf(top, __ldcg(part_at(i0 + i * step) + n_col));
-#pragma unroll
-      for (int d = LC / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f, acc[CH];
-#pragma unroll
-      for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
-      for (int b = 0; b < n; b += LC) {
-        float w = 0.0f;
-        if (b + sub < n) {
-          const float* src = part_at(i0 + (b + sub) * step) + n_col;
-          w = ex2(__ldcg(src) - base);
-          sum += w * __ldcg(src + NC);
-        }
-        const int m = min(LC, n - b);
-#pragma unroll 8
-        for (int i = 0; i < m; ++i) {
-          const float wi = __shfl_sync(0xFFFFFFFFu, w, i, LC);
-          const float* src = part_at(i0 + (b + i) * step) + 2 * NC + n_col * D + sub * CH;
-#pragma unroll
-          for (int x = 0; x < CH; x += 4) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + x));
-            acc[x] += wi * y.x; acc[x + 1] += wi * y.y; acc[x + 2] += wi * y.z; acc[x + 3] += wi * y.w;
-          }
-        }
-      }
-#pragma unroll
-      for (int d = LC / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      if (n_col >= n_cols) return;
-      if (!store) {
-        float* dst = part_at(i0);
-        if (sub == 0) {
-          dst[n_col] = top;
-          dst[NC + n_col] = sum;
-        }
-#pragma unroll
-        for (int x = 0; x < CH; x += 4)
-          *reinterpret_cast<float4*>(dst + 2 * NC + n_col * D + sub * CH + x) =
-              make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
-        return;
-      }
-      const int dq = div_G(rem0 + n_col);
-      const int64_t row = static_cast<int64_t>(q0 + dq) * p.Hq + head * p.G + (rem0 + n_col - dq * p.G);
-      const float inv = sum > 0.0f ? __fdividef(v_gsa, sum) : 0.0f;
-#pragma unroll
-      for (int x = 0; x < CH; x += 2)
-        *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + sub * CH + x) =
-            __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
-      if (p.lse && sub == 0) p.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
-    };
-    // every consumer's stores so far, then the ticket; true for the last of `n`
-    bool failed = false;
-    auto last_of = [&](uint32_t* ticket, int n) {
-      __threadfence();
-      failed |= !sync_consumers();
-      if (tid == 0 && !failed) {
-        const bool all = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
-        if (all) *ticket = 0u;
-        *s_flag = all;
-      }
-      failed |= !sync_consumers();
-      const bool all = *s_flag;
-      __threadfence();
-      return all;
-    };
-    const bool two = n_parts > kJoinAlone;
-    const int r0 = two ? me / kJoinRun * kJoinRun : 0;
-#pragma unroll 1
-    for (int level = two ? 1 : 0; level >= 0; --level) {
-      const int i0 = level ? r0 : 0, step = two && !level ? kJoinRun : 1;
-      const int n = level ? min(kJoinRun, n_parts - r0) : two ? (n_parts + kJoinRun - 1) / kJoinRun : n_parts;
-      const bool all = last_of(p.tickets + 2 * (first + i0) + level, n);
-      if (failed) return give_up();
-      if (!all) break;
-      join_parts(i0, n, step, level == 0);
-    }
-    // s_flag is written again only after the next run's barriers
   }
 }
 
 size_t a256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct AttnWs {
-  size_t tickets, partials, total;
+  size_t joins, partials, total;
 };
 AttnWs attn_ws_layout(int D) {
   AttnWs L;
-  L.tickets = 256;
-  L.partials = a256(L.tickets + kAttnMaxCtas * 16);
+  L.joins = 256;
+  L.partials = a256(L.joins + kAttnMaxCtas * sizeof(KeyJoin));
   L.total = a256(L.partials + size_t(2) * kPrefillMaxCtas * kPrefillCols * (D + 2) * 4);
   return L;
 }
@@ -822,7 +722,10 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (max_kv <= Sh::kTile) return NVR_OK;                    // keys of one tile are never cut
+  return launch_kv_join(p, D, static_cast<int>(grid), Sh::kCols, items * p.Hkv, s);
 }
 
 template <int D>
@@ -886,7 +789,7 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   p.causal = causal != 0; p.window = window;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
   p.status = reinterpret_cast<uint32_t*>(w + kWsStatus);
-  p.tickets = reinterpret_cast<uint32_t*>(w + L.tickets);
+  p.joins = reinterpret_cast<KeyJoin*>(w + L.joins);
   p.partials = reinterpret_cast<float*>(w + L.partials);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int max_kv = static_cast<int>(max_pages) * page_size;

@@ -13,6 +13,16 @@ namespace nvr {
 // 2): the softmax weights stay below 2^8, inside fp16.
 constexpr float kRescaleAt = 8.0f;
 
+// A key that a chunk border cuts, written by the block of its first chunk: its
+// parts, whether the first lies in its block's second slot, its rows.
+struct KeyJoin {
+  int n_parts, tail;
+  int q0, rem0, n_cols;       // the first column is head rem0 of the KV head's at query row q0
+  int head;
+  float v_gsa;
+  int pad;
+};
+
 struct AttnParams {
   const __nv_bfloat16* q;
   int64_t q_stride;
@@ -33,8 +43,10 @@ struct AttnParams {
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
-  uint32_t* tickets;
-  float* partials;            // [2 * blocks][NC][D + 2]: m, l, O
+  KeyJoin* joins;             // [blocks]
+  // [2 * blocks][NC m, NC l, NC x D O]: a block's first run is in its slot 0 when it
+  // is part of a cut key, its last one in slot 1 unless the key starts the chunk
+  float* partials;
   int min_chunk;              // fewest tiles of a block
 };
 
@@ -122,13 +134,17 @@ __device__ __forceinline__ void query_scale(uint32_t big, float& up, float& down
   down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
 
-// Workspace of an attention call (csrc/kv_attention.cu): control words, two
-// ticket words for every block and column half, the partial results.
+// Workspace of an attention call (csrc/kv_attention.cu): control words, the cut
+// keys, the partial results.
 constexpr int kAttnMaxCtas = 2048;
 constexpr int kPrefillMaxCtas = 160;       // blocks of the tensor-memory kernel
 constexpr int kPrefillCols = 256;          // its columns
 constexpr int kAttnMaxCols = 16384;        // columns * blocks of the streaming kernel at most
 static_assert(kPrefillMaxCtas * kPrefillCols >= kAttnMaxCols, "the partials hold either kernel's");
+
+// Joins the cut keys of `blocks` blocks, of `keys` keys at most (csrc/kv_join.cu);
+// the last launch of a call.
+nvr_status launch_kv_join(const AttnParams& p, int D, int blocks, int NC, int64_t keys, cudaStream_t s);
 
 // The tensor-memory kernel (csrc/kv_prefill.cu).
 nvr_status launch_kv_prefill(AttnParams& p, int D, int max_kv, cudaStream_t s);

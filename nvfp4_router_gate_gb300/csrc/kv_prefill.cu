@@ -29,7 +29,7 @@
 // P V complete.
 //
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
-// equal chunks, one per block, partial rows joined by the last block to arrive.
+// equal chunks, one per block, the rows of cut keys joined by csrc/kv_join.cu.
 #include <type_traits>
 
 #include "kv_attention.cuh"
@@ -41,8 +41,6 @@ namespace {
 constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
 constexpr int kPThreads = 512;
 constexpr int kPKeyUnits = 8;              // cost of starting and ending a key, in single tiles
-constexpr int kPJoinAlone = 24;            // parts joined at once (the weights' table lies in a query tile)
-constexpr int kPJoinRun = 16;              // beyond that, joined first
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;
 constexpr int kAhead = 6;                  // tiles fetched into L2 before they are expanded
@@ -55,9 +53,9 @@ struct alignas(16) Run {
   int kv, n_q, q0, n_cols;
   int iq0, rem0, lo, hi;
   int dual;                                // both halves on different rows (else on alternate tiles)
-  int first, n_parts, tail;                // the key's first chunk, its chunks, whether it starts inside it
+  int whole, slot;                         // all of its key, or a part: in this slot
   float k_gsa, v_gsa;
-  int pad[2];
+  int pad[3];
 };
 
 template <int D>
@@ -67,8 +65,8 @@ struct PrefillSmem {
   static constexpr int kK = kQ + 2 * kTileBytes;
   static constexpr int kV = kK + 2 * kTileBytes;
   static constexpr int kRunsAt = kV + 2 * kTileBytes;
-  static constexpr int kRowAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));   // per row: m, l of half 1; 1 / l of both
-  static constexpr int kBarAt = kRowAt + 4 * kPTile * 4;
+  static constexpr int kRowAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));   // per row: m, l of half 1
+  static constexpr int kBarAt = kRowAt + 2 * kPTile * 4;
   static constexpr int kTotal = kBarAt + 40 * 8 + 64 + 1024;
 };
 
@@ -166,7 +164,6 @@ kv_prefill_kernel(const AttnParams p) {
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
   volatile int* abort_flag = s_words + 1;
   int* s_start = s_words + 2;                                // item, offset inside it
-  int* s_flag = s_words + 4;                                 // per half: the last block to arrive
   volatile int* s_done = s_words + 10;                       // tiles expanded
   volatile uint32_t* s_live = reinterpret_cast<volatile uint32_t*>(s_words + 6);   // [kLive] tokens in groups of 16
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -238,6 +235,7 @@ kv_prefill_kernel(const AttnParams p) {
     return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag)) != 0;
   };
 
+  if (tid == 13 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
   if (f0 < f1) {
       int n_taken = 0;
       Run run;
@@ -289,11 +287,15 @@ kv_prefill_kernel(const AttnParams p) {
             r.kv = g.kv; r.n_q = g.n_q; r.q0 = g.q0; r.n_cols = g.n_cols;
             r.iq0 = g.c0 / p.G; r.rem0 = g.c0 - r.iq0 * p.G; r.lo = g.lo; r.hi = g.hi;
             r.dual = u == 2;
-            r.first = key_f0 / chunk;
-            r.n_parts = (key_f0 + u * (g.tiles - 1)) / chunk - r.first + 1;
-            r.tail = key_f0 > static_cast<int64_t>(r.first) * chunk;
+            const int first_chunk = key_f0 / chunk, n_parts = (key_f0 + u * (g.tiles - 1)) / chunk - first_chunk + 1;
+            const int inside = key_f0 > f0;
+            r.whole = n_parts == 1;
+            r.slot = 2 * blockIdx.x + inside;
             r.k_gsa = __ldg(p.k_gsa + head);
             r.v_gsa = __ldg(p.v_gsa + head);
+            // this block holds a cut key's first part
+            if (lane == 0 && n_parts > 1 && ta == 0)
+              p.joins[blockIdx.x] = {n_parts, inside, g.q0 + r.iq0, r.rem0, g.n_cols, head, r.v_gsa, 0};
             ok = hand_out(r);
           }
           off += end - f;
@@ -798,12 +800,8 @@ kv_prefill_kernel(const AttnParams p) {
               tc_fence_before();
               return true;
             }
-            const bool whole = run.n_parts == 1;
-            auto part_at = [&](int i) {
-              return p.partials + static_cast<size_t>(2 * (run.first + i) + (i == 0 ? run.tail : 0)) * NC * (D + 2);
-            };
-            const int me = static_cast<int>(blockIdx.x) - run.first;
-            float* part = part_at(me);
+            const bool whole = run.whole;
+            float* part = p.partials + static_cast<size_t>(run.slot) * NC * (D + 2);
             const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
             // The rows leave through shared memory (the query tile, now free; the
             // handed-over rows, behind their reader), so that the warp stores whole
@@ -871,102 +869,9 @@ kv_prefill_kernel(const AttnParams p) {
             if (whole) {
               if (on && p.lse)
                 p.lse[out_row()] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
-              return true;
-            }
-            if (on) {
+            } else if (on) {
               part[col] = m;
               part[NC + col] = l;
-            }
-            // ---- join the chunks of the key, this half's rows
-            const int rows = min(run.n_cols - w * kPTile, kPTile), row0 = w * kPTile;
-            float* s_w = reinterpret_cast<float*>(smem + Sm::kQ + w * Sm::kTileBytes);   // [parts][128]
-            float* s_inv = s_row + 2 * kPTile + w * kPTile;
-            auto join_parts = [&](int i0, int n, int step, bool store) -> bool {
-              if (row < rows) {
-                float top = -INFINITY, all = 0.0f;
-                for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(part_at(i0 + i * step) + row0 + row));
-                const float base = top == -INFINITY ? 0.0f : top;
-                for (int i = 0; i < n; ++i) {
-                  const float* src = part_at(i0 + i * step) + row0 + row;
-                  const float x = ex2(__ldcg(src) - base);
-                  s_w[i * kPTile + row] = x;
-                  all += x * __ldcg(src + NC);
-                }
-                if (store) {
-                  s_inv[row] = all > 0.0f ? __fdividef(run.v_gsa, all) : 0.0f;
-                  if (p.lse) p.lse[out_row()] = all > 0.0f ? (top + log2f(all)) * 0.693147180559945309f : -INFINITY;
-                } else {
-                  part_at(i0)[row0 + row] = top;
-                  part_at(i0)[NC + row0 + row] = all;
-                }
-              }
-              if (!sync_half()) return false;
-              constexpr int V = D / 4;                       // vectors of a row
-              constexpr int K = 4;                           // vectors a thread has under way
-              for (int e0 = row; e0 < rows * V; e0 += K * kPTile) {
-                float4 acc[K];
-#pragma unroll
-                for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                for (int i = 0; i < n; ++i) {
-                  const float* src = part_at(i0 + i * step) + 2 * NC + row0 * D;
-#pragma unroll
-                  for (int k = 0; k < K; ++k) {
-                    const int e = e0 + k * kPTile;
-                    if (e < rows * V) {
-                      const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + e);
-                      const float x = s_w[i * kPTile + e / V];
-                      acc[k].x += x * y.x; acc[k].y += x * y.y; acc[k].z += x * y.z; acc[k].w += x * y.w;
-                    }
-                  }
-                }
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                  const int e = e0 + k * kPTile;
-                  if (e >= rows * V) continue;
-                  const int r = e / V, x = (e - r * V) * 4;
-                  if (!store) {
-                    *reinterpret_cast<float4*>(part_at(i0) + 2 * NC + (row0 + r) * D + x) = acc[k];
-                    continue;
-                  }
-                  const int rq = div_small(run.rem0 + row0 + r, inv_G);
-                  const int64_t dst = (static_cast<int64_t>(run.q0 + run.iq0 + rq) * p.Hq + run.head * p.G + run.rem0 +
-                                       row0 + r - rq * p.G) * D + x;
-                  const float f = s_inv[r];
-                  const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * f, acc[k].y * f);
-                  const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * f, acc[k].w * f);
-                  *reinterpret_cast<uint2*>(p.out + dst) =
-                      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-                }
-              }
-              return sync_half();                            // (the table is free again)
-            };
-            // every store of the half so far, then the ticket
-            auto last_of = [&](uint32_t* ticket, int n, bool& all) -> bool {
-              __threadfence();
-              if (!sync_half()) return false;
-              if (row == 0) {
-                const bool y = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
-                if (y) *ticket = 0u;
-                s_flag[w] = y;
-              }
-              if (!sync_half()) return false;
-              all = s_flag[w];
-              __threadfence();
-              return true;
-            };
-            // tickets of chunk c: 4 c + 2 half, and the next one for the runs of parts
-            const bool two = run.n_parts > kPJoinAlone;
-            const int r0 = two ? me / kPJoinRun * kPJoinRun : 0;
-#pragma unroll 1
-            for (int level = two ? 1 : 0; level >= 0; --level) {
-              const int i0 = level ? r0 : 0, step = two && !level ? kPJoinRun : 1;
-              const int n = level ? min(kPJoinRun, run.n_parts - r0)
-                                  : two ? (run.n_parts + kPJoinRun - 1) / kPJoinRun : run.n_parts;
-              bool all = false;
-              if (!last_of(p.tickets + 4 * (run.first + i0) + 2 * w + level, n, all)) return false;
-              if (!all) break;
-              if (!join_parts(i0, n, step, level == 0)) return false;
             }
             return true;
         };
@@ -993,8 +898,6 @@ template <int D>
 nvr_status launch(AttnParams& p, int max_kv, cudaStream_t s) {
   using Sm = PrefillSmem<D>;
   static_assert(Sm::kTotal <= 227 * 1024, "shared memory");
-  static_assert(kPJoinAlone * kPTile * 4 <= Sm::kTileBytes, "the table of weights lies in a query tile");
-  static_assert((kPrefillMaxCtas + kPJoinRun - 1) / kPJoinRun <= kPJoinAlone, "two levels of joining are enough");
   static bool attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
@@ -1023,7 +926,9 @@ nvr_status launch(AttnParams& p, int max_kv, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, p));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, p);
+  if (e != cudaSuccess) return cuda_status(e);
+  return launch_kv_join(p, D, static_cast<int>(grid), kPrefillCols, items * p.Hkv, s);
 }
 
 }  // namespace
