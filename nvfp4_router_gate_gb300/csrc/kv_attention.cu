@@ -32,7 +32,7 @@ namespace nvr {
 
 namespace {
 
-constexpr int kStreamCols = 16;            // more columns of a sequence go to the tensor-memory kernel
+constexpr int kStreamCols = 32;            // more columns of a sequence go to the tensor-memory kernel
 // Starting and ending a key costs a block about as much as this many tiles
 // (queries, joining the warps, storing): counted in the chunks, so that blocks
 // with many short keys get fewer tiles.
@@ -730,12 +730,10 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
 
 template <int D>
 nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
-  // columns of a pass: as few as hold a sequence's queries, 32 at most
+  // sixteen columns at a time where eight do not hold a sequence's queries
   const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
   if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3>(p, max_kv, s);
-  if (cols <= 16) return launch_attn<D, 2, 4, 2, 3, 2>(p, max_kv, s);
-  if constexpr (D == 128) return launch_attn<D, 4, 4, 2, 4, 1>(p, max_kv, s);
-  else return launch_attn<D, 4, 4, 2, 3, 2>(p, max_kv, s);
+  return launch_attn<D, 2, 4, 2, 3, 2>(p, max_kv, s);
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }

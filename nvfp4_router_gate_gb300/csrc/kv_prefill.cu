@@ -40,7 +40,11 @@ namespace {
 
 constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
 constexpr int kPThreads = 512;
-constexpr int kPKeyUnits = 8;              // cost of starting and ending a key, in single tiles
+// Starting and ending a key (queries in, rows out, an empty pipeline) costs about
+// as much as this many tiles (prompts of nine users: 3, 4, 6 tiles 151, 148, 151 us).
+// A tile costs the same whether both halves work on it (two row tiles) or one: the
+// expansion of its keys and values is shared.
+constexpr int kPKeyCost = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;
 constexpr int kAhead = 6;                  // tiles fetched into L2 before they are expanded
@@ -136,15 +140,11 @@ __device__ __forceinline__ void registers_shrink() {
 }
 // Registers of a thread, of the 128 each is launched with: softmax (two groups
 // of four warps), expansion, the rest.
-constexpr int kRegsSoftmax = 168, kRegsExpand = 104, kRegsRest = 72;
+constexpr int kRegsSoftmax = 144, kRegsExpand = 128, kRegsRest = 96;
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsRest <= 4 * 128, "what the block was launched with");
 
-// Chunks of the flat order: a tile costs one unit, two when both halves work
-// on different rows of it.
-__device__ __forceinline__ int tile_units(const Group& g) { return g.n_cols > kPTile ? 2 : 1; }
-__device__ __forceinline__ int key_units(const Group& g) {
-  return g.tiles ? g.tiles * tile_units(g) + kPKeyUnits : 0;
-}
+// A key's length in the flat order: its tiles, then places without work.
+__device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kPKeyCost : 0; }
 
 template <int D>
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -191,7 +191,7 @@ kv_prefill_kernel(const AttnParams p) {
   const int n_items = p.B * p.groups;
   const int per = (n_items + kPThreads - 1) / kPThreads;
   int mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_units(group_of<NC, kPTile>(p, i)) * p.Hkv;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost(group_of<NC, kPTile>(p, i)) * p.Hkv;
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -215,7 +215,7 @@ kv_prefill_kernel(const AttnParams p) {
   if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
     int at = excl, i = tid * per;
     for (;; ++i) {
-      const int n = key_units(group_of<NC, kPTile>(p, i)) * p.Hkv;
+      const int n = key_cost(group_of<NC, kPTile>(p, i)) * p.Hkv;
       if (f0 < at + n) break;
       at += n;
     }
@@ -274,20 +274,19 @@ kv_prefill_kernel(const AttnParams p) {
           primed = true;
           continue;
         }
-        const int cost = key_units(g), u = tile_units(g);
+        const int cost = key_cost(g);
         while (off < cost * p.Hkv && f < f1 && ok) {
           const int head = off / cost, at = off - head * cost;
           const int key_f0 = f - at, end = min(f1, key_f0 + cost);
-          // tiles that start inside [f, end)
-          const int ta = min((at + u - 1) / u, g.tiles), tb = min((end - key_f0 + u - 1) / u, g.tiles);
+          const int ta = min(at, g.tiles), tb = min(end - key_f0, g.tiles);
           if (ta < tb) {
             Run r = {};
             r.tiles = tb - ta;
             r.tile0 = g.tile0 + ta; r.b = g.b; r.head = head;
             r.kv = g.kv; r.n_q = g.n_q; r.q0 = g.q0; r.n_cols = g.n_cols;
             r.iq0 = g.c0 / p.G; r.rem0 = g.c0 - r.iq0 * p.G; r.lo = g.lo; r.hi = g.hi;
-            r.dual = u == 2;
-            const int first_chunk = key_f0 / chunk, n_parts = (key_f0 + u * (g.tiles - 1)) / chunk - first_chunk + 1;
+            r.dual = g.n_cols > kPTile;
+            const int first_chunk = key_f0 / chunk, n_parts = (key_f0 + g.tiles - 1) / chunk - first_chunk + 1;
             const int inside = key_f0 > f0;
             r.whole = n_parts == 1;
             r.slot = 2 * blockIdx.x + inside;
@@ -911,11 +910,11 @@ nvr_status launch(AttnParams& p, int max_kv, cudaStream_t s) {
   }
   p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + kPrefillCols - 1) / kPrefillCols);
   const int64_t items = static_cast<int64_t>(p.B) * p.groups;
-  const int64_t most = items * p.Hkv * (2 * ((max_kv + kPTile - 1) / kPTile + 1) + kPKeyUnits);
+  const int64_t most = items * p.Hkv * ((max_kv + kPTile - 1) / kPTile + 1 + kPKeyCost);
   if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
   int64_t grid = sms < kPrefillMaxCtas ? sms : kPrefillMaxCtas;
   if (grid > most) grid = most;
-  p.min_chunk = 4;
+  p.min_chunk = 2;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
