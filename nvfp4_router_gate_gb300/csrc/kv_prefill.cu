@@ -71,7 +71,7 @@ struct PrefillSmem {
   static constexpr int kRunsAt = kV + 2 * kTileBytes;
   static constexpr int kRowAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));   // per row: m, l of half 1
   static constexpr int kBarAt = kRowAt + 2 * kPTile * 4;
-  static constexpr int kTotal = kBarAt + 40 * 8 + 64 + 1024;
+  static constexpr int kTotal = kBarAt + 48 * 8 + 64 + 1024;
 };
 
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -81,22 +81,32 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] . B[smem], fp16 operands.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// The two words of a matrix descriptor: 128-byte swizzle, 8-row groups 1024 bytes
+// apart; the low one holds the address and the distance of 64-channel atoms (used
+// by the transposed operand alone).  The next step of a product is an addition to
+// the low word: the issuing warp's instructions are on the critical path.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(const void* tile, uint32_t atom_distance) {
+  return ((smem_u32(tile) & 0x3FFFFu) >> 4) | ((atom_distance >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] . B[smem], fp16 operands; descriptors by their low words.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                            bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHigh)
       : "memory");
 }
 // The same with A in tensor memory (two fp16 of a row to a column).
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
                                               bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHigh)
       : "memory");
 }
 
@@ -159,8 +169,9 @@ kv_prefill_kernel(const AttnParams p) {
   uint64_t *run_full = bars, *run_empty = run_full + kRuns, *k_full = run_empty + kRuns, *k_empty = k_full + 2,
            *v_full = k_empty + 2, *v_empty = v_full + 2, *q_full = v_empty + 2, *s_full = q_full + 2,
            *p_full = s_full + 2, *o_full = p_full + 2, *meet = o_full + 2, *x_ready = meet + 2, *x_full = x_ready + 1,
-           *x_free = x_full + 1, *drained = x_free + 1, *q_raw = drained + 1;
-  int* s_words = reinterpret_cast<int*>(q_raw + 2);
+           *x_free = x_full + 1, *drained = x_free + 1, *q_raw = drained + 1, *h_full = q_raw + 2,
+           *p_half = h_full + 2;
+  int* s_words = reinterpret_cast<int*>(p_half + 2);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
   volatile int* abort_flag = s_words + 1;
   int* s_start = s_words + 2;                                // item, offset inside it
@@ -175,7 +186,7 @@ kv_prefill_kernel(const AttnParams p) {
       mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
       mbar_init(q_full + i, 4); mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4); mbar_init(o_full + i, 1);
-      mbar_init(meet + i, 4); mbar_init(q_raw + i, 4);
+      mbar_init(meet + i, 4); mbar_init(q_raw + i, 4); mbar_init(h_full + i, 1); mbar_init(p_half + i, 4);
     }
     mbar_init(x_ready, 4); mbar_init(x_full, 4); mbar_init(x_free, 4); mbar_init(drained, 1);
     *abort_flag = 0;
@@ -315,26 +326,29 @@ kv_prefill_kernel(const AttnParams p) {
         int tk = 0, tv = 0;                                  // tiles of K and V taken
         uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
         auto products = [&]() -> bool {
+          const uint32_t q_low = desc_low(smem + Sm::kQ, 16), k_low = desc_low(smem + Sm::kK, 16);
+          const uint32_t v_low = desc_low(smem + Sm::kV, kPTile * 128);
+          constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
           auto score = [&](int w, int stage) {
+            const uint32_t q = q_low + w * kTileLow, k = k_low + stage * kTileLow, d = tmem + w * kPTile;
             if (elect_one()) {
-              const uint32_t q = smem_u32(smem + Sm::kQ + w * Sm::kTileBytes);
-              const uint32_t k = smem_u32(smem + Sm::kK + stage * Sm::kTileBytes);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                const uint32_t o = (i / 4) * (kPTile * 128) + (i % 4) * 32;
-                tc_mma_f16(tmem + w * kPTile, desc_kmajor_sw128(q + o), desc_kmajor_sw128(k + o), id_s, i != 0);
+                const uint32_t o = ((i / 4) * (kPTile * 128) + (i % 4) * 32) >> 4;
+                tc_mma_f16(d, q + o, k + o, id_s, i != 0);
               }
             }
             __syncwarp();
           };
-          auto weigh = [&](int w, int stage, bool add) {
+          auto weigh = [&](int w, int stage, bool add, int half) {
+            const uint32_t v = v_low + stage * kTileLow, d = tmem + 2 * kPTile + w * D, a = tmem + w * kPTile;
             if (elect_one()) {
-              const uint32_t v = smem_u32(smem + Sm::kV + stage * Sm::kTileBytes);
 #pragma unroll
-              for (int i = 0; i < kPTile / 16; ++i)
+              for (int k = 0; k < kPTile / 32; ++k) {
                 // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-                tc_mma_f16_ta(tmem + 2 * kPTile + w * D, tmem + w * kPTile + 8 * i,
-                              smem_desc(v + i * 2048, kPTile * 128, 1024, 2), id_o, add || i != 0);
+                const int i = half * (kPTile / 32) + k;
+                tc_mma_f16_ta(d, a + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
+              }
             }
             __syncwarp();
           };
@@ -357,15 +371,19 @@ kv_prefill_kernel(const AttnParams p) {
             auto k_ready = [&](int j) { return have(k_full + (k0 + j) % 2, ((k0 + j) / 2) & 1); };
             auto v_ready = [&](int j) { return have(v_full + (v0 + j) % 2, ((v0 + j) / 2) & 1); };
             auto q_ready = [&](int w) { const bool ok = have(q_full + w, ph_q[w]); ph_q[w] ^= 1u; return ok; };
-            auto p_ready = [&](int w) { const bool ok = have(p_full + w, ph_p[w]); ph_p[w] ^= 1u; return ok; };
+            auto p_ready = [&](int w, int half) { return have((half ? p_full : p_half) + w, ph_p[w]); };
             // Row tile w: O += P V of its tile `cur`, then S of its tile `nxt`; both row
             // tiles walk all tiles (dual) or every other.  K and V of a tile wait for
             // its first reader and are free after its last.
             auto step = [&](bool dual, int w, int cur, int nxt) -> bool {
               const bool first = !dual || w == 0, last = !dual || w == 1;
               if (cur >= 0) {
-                if ((first && !v_ready(cur)) || !p_ready(w)) return false;
-                weigh(w, (v0 + cur) % 2, cur > (dual ? 0 : 1));
+                if ((first && !v_ready(cur)) || !p_ready(w, 0)) return false;
+                weigh(w, (v0 + cur) % 2, cur > (dual ? 0 : 1), 0);
+                commit(h_full + w);
+                if (!p_ready(w, 1)) return false;
+                ph_p[w] ^= 1u;
+                weigh(w, (v0 + cur) % 2, true, 1);
                 if (last) commit(v_empty + (v0 + cur) % 2);
               }
               if (nxt < n) {
@@ -574,7 +592,7 @@ kv_prefill_kernel(const AttnParams p) {
         const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
         const uint32_t t_s = tmem + lanes + w * kPTile, t_o = tmem + lanes + 2 * kPTile + w * D;
         const float inv_G = 1.0f / static_cast<float>(p.G);
-        uint32_t ph_q = 0, ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
+        uint32_t ph_h = 0, ph_q = 0, ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
         int n_tile = 0;                                      // tiles before the run
         auto sync_half = [&]() {
           __syncwarp();
@@ -661,7 +679,11 @@ kv_prefill_kernel(const AttnParams p) {
                 // (rows that nobody asked for: their P may be anything)
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + w);
+                if (lane == 0) {
+                  mbar_arrive(p_half + w);
+                  mbar_arrive(p_full + w);
+                }
+                ph_h ^= 1u;
                 continue;
               }
               const uint32_t bytes = s_live[(n_tile + j) % kLive];
@@ -676,83 +698,95 @@ kv_prefill_kernel(const AttnParams p) {
                 const uint32_t two = live >> (c / 16);
                 return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
               };
-              uint32_t pr[kPTile / 2];
-              float sum;
-              auto weights = [&](auto hidden) {                // hidden: some tokens are not seen
-                uint64_t sum2 = f2_pack(0.0f, 0.0f);
-                const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
-                uint32_t s[2][32];
-                tmem_load32_start(t_s, s[0]);
-#pragma unroll
-                for (int c = 0; c < kPTile; c += 32) {
-                  uint32_t (&now)[32] = s[(c / 32) % 2];
-                  tmem_load32_finish(now);
-                  if (c + 32 < kPTile) tmem_load32_start(t_s + c + 32, s[(c / 32 + 1) % 2]);
-                  const uint32_t see = hidden ? seen32(c) : 0xFFFFFFFFu;
-#pragma unroll
-                  for (int x = 0; x < 32; x += 2) {
-                    const uint64_t v = f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
-                    float v0 = f2_lo(v), v1 = f2_hi(v);
-                    if (hidden) {
-                      v0 = see & (1u << x) ? v0 : -INFINITY;
-                      v1 = see & (2u << x) ? v1 : -INFINITY;
-                    }
-                    const float a = ex2(v0), b = ex2(v1);
-                    sum2 = f2_add(sum2, f2_pack(a, b));
-                    pr[(c + x) / 2] = pack_f16(a, b);
-                  }
-                }
-                sum = f2_lo(sum2) + f2_hi(sum2);
-              };
-              // A tile whose weights add up to more than 2^kRescaleAt holds a score
-              // far above m (a weight above 2, at least): no maximum is taken of the
-              // others.  (m at or above every score: at most 128 weights of 1.)
-              for (bool move = i == 0;; move = true) {
-                if (move) {
-                  // m moves to the largest score so far
-                  float top = -INFINITY;
+              // In two halves of 64 tokens: P V of the first starts under the second.
 #pragma unroll 1
-                  for (int c = 0; c < kPTile; c += 32) {
-                    uint32_t s[32];
-                    tmem_load32_start(t_s + c, s);
-                    tmem_load32_finish(s);
-                    const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
+              for (int c0 = 0; c0 < kPTile; c0 += kPTile / 2) {
+                uint32_t pr[kPTile / 4];
+                float sum;
+                auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
+                  uint64_t sum2 = f2_pack(0.0f, 0.0f);
+                  const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
+                  uint32_t s[2][32];
+                  tmem_load32_start(t_s + c0, s[0]);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                      top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
-                  }
-                  const float now = fminf(m_neg, -top);
-                  const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-                  m_neg = now;
-                  l *= shrink;
-                  if (i > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                      float o[16];
-                      uint32_t y[16];
-                      tmem_load16(t_o + c, o);
+                  for (int c = 0; c < kPTile / 2; c += 32) {
+                    uint32_t (&now)[32] = s[(c / 32) % 2];
+                    tmem_load32_finish(now);
+                    if (c + 32 < kPTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
+                    const uint32_t see = hidden ? seen32(c0 + c) : 0xFFFFFFFFu;
 #pragma unroll
-                      for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
-                      tmem_store16(t_o + c, y);
+                    for (int x = 0; x < 32; x += 2) {
+                      const uint64_t v =
+                          f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+                      float v0 = f2_lo(v), v1 = f2_hi(v);
+                      if (hidden) {
+                        v0 = see & (1u << x) ? v0 : -INFINITY;
+                        v1 = see & (2u << x) ? v1 : -INFINITY;
+                      }
+                      const float a = ex2(v0), b = ex2(v1);
+                      sum2 = f2_add(sum2, f2_pack(a, b));
+                      pr[(c + x) / 2] = pack_f16(a, b);
                     }
                   }
+                  sum = f2_lo(sum2) + f2_hi(sum2);
+                };
+                // Weights that add up to more than 2^kRescaleAt hold a score far above m
+                // (a weight above 4, at least): no maximum is taken of the others.  (m at
+                // or above every score: at most 64 weights of 1.)
+                for (bool move = i == 0 && c0 == 0;; move = true) {
+                  if (move) {
+                    // m moves to the largest score so far (of the tokens not yet weighed)
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = c0; c < kPTile; c += 32) {
+                      uint32_t s[32];
+                      tmem_load32_start(t_s + c, s);
+                      tmem_load32_finish(s);
+                      const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
+#pragma unroll
+                      for (int x = 0; x < 32; ++x)
+                        top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
+                    }
+                    const float now = fminf(m_neg, -top);
+                    const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                    m_neg = now;
+                    l *= shrink;
+                    if (i > 0 || c0 > 0) {
+                      // (earlier tiles are in O, S came after them; the first half may be on its way)
+                      if (c0 > 0) {
+                        if (!wait_all(h_full + w, ph_h)) return false;
+                        tc_fence_after();
+                      }
+#pragma unroll 1
+                      for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        uint32_t y[16];
+                        tmem_load16(t_o + c, o);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
+                        tmem_store16(t_o + c, y);
+                      }
+                    }
+                  }
+                  if (masked) weights(std::true_type{});
+                  else weights(std::false_type{});
+                  if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
                 }
-                if (masked) weights(std::true_type{});
-                else weights(std::false_type{});
-                if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
-              }
-              l += sum;
+                l += sum;
+                // P over the columns of S that have been read
 #pragma unroll
-              for (int c = 0; c < kPTile / 2; c += 16) {
-                uint32_t x[16];
+                for (int c = 0; c < kPTile / 4; c += 16) {
+                  uint32_t x[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-                tmem_store16(t_s + c, x);
+                  for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+                  tmem_store16(t_s + c0 / 2 + c, x);
+                }
+                tmem_store_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive((c0 ? p_full : p_half) + w);
               }
-              tmem_store_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(p_full + w);
+              ph_h ^= 1u;
             }
             n_tile += run.tiles;
             if (n_my > 0) {
