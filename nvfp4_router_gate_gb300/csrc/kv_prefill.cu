@@ -59,7 +59,8 @@ struct alignas(16) Run {
   int dual;                                // both halves on different rows (else on alternate tiles)
   int whole, slot;                         // all of its key, or a part: in this slot
   float k_gsa, v_gsa;
-  int pad[3];
+  int col0;                                // the column of half 1's row 0 (half 0's: column 0)
+  int pad[2];
 };
 
 template <int D>
@@ -297,6 +298,9 @@ kv_prefill_kernel(const AttnParams p) {
             r.kv = g.kv; r.n_q = g.n_q; r.q0 = g.q0; r.n_cols = g.n_cols;
             r.iq0 = g.c0 / p.G; r.rem0 = g.c0 - r.iq0 * p.G; r.lo = g.lo; r.hi = g.hi;
             r.dual = g.n_cols > kPTile;
+            // (up to half a tile's columns: half 1 has them in its upper rows, whose
+            // warps run on the other two of the SM's four schedulers)
+            r.col0 = r.dual ? kPTile : g.n_cols <= kPTile / 2 ? -kPTile / 2 : 0;
             const int first_chunk = key_f0 / chunk, n_parts = (key_f0 + g.tiles - 1) / chunk - first_chunk + 1;
             const int inside = key_f0 > f0;
             r.whole = n_parts == 1;
@@ -605,8 +609,8 @@ kv_prefill_kernel(const AttnParams p) {
         // they are needed.
         auto one_run = [&](const volatile Run& run) -> bool {
             const int n_my = run.dual ? run.tiles : (run.tiles + 1 - w) / 2;
-            const int col = run.dual ? w * kPTile + row : row;
-            const bool on = col < run.n_cols;
+            const int col = w == 0 ? row : row + run.col0;
+            const bool on = static_cast<uint32_t>(col) < static_cast<uint32_t>(run.n_cols);
             // the row's query and head (recomputed where they are needed)
             auto quotient = [&]() { return div_small(run.rem0 + (on ? col : 0), inv_G); };
             auto head_of = [&](int dq) { return run.head * p.G + run.rem0 + (on ? col : 0) - dq * p.G; };
@@ -798,13 +802,14 @@ kv_prefill_kernel(const AttnParams p) {
             // ---- both halves on one set of rows: half 1 hands its rows over
             const bool cross = !run.dual && run.tiles > 1;
             float keep = 1.0f, other = 0.0f;
-            float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + row * D;   // the query tiles, now free
+            const int x_row = col & (kPTile - 1);
+            float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + x_row * D;   // the query tiles, now free
             if (cross) {
               if (w == 0) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x_ready);         // (its scores are done with the queries)
                 if (!wait_all(x_full, ph_x)) return false;
-                const float m1 = s_row[row], l1 = s_row[kPTile + row];
+                const float m1 = s_row[x_row], l1 = s_row[kPTile + x_row];
                 const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
                 keep = ex2(m - base);
                 other = ex2(m1 - base);
@@ -821,8 +826,8 @@ kv_prefill_kernel(const AttnParams p) {
                     *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
                         make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                 }
-                s_row[row] = m;
-                s_row[kPTile + row] = l;
+                s_row[x_row] = m;
+                s_row[kPTile + x_row] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x_full);
                 if (!wait_all(x_free, ph_x)) return false;

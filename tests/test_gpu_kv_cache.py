@@ -360,3 +360,75 @@ def test_cache_past_four_gigabytes():
     out, _ = kv.attend(q, _dev(table), _dev(np.array([n], np.int32)), lse=lse)
     ref = K.attention(q32.astype(np.float64), *K.load(small, np.arange(n), S, D, g, g), D ** -0.5)
     assert K.check_attention(out.float().cpu().numpy(), lse.cpu().numpy(), ref, n, np.abs(v).max()) == (0, 0)
+
+
+COLUMNS = [  # lens, n_q, H, G, D, S, window: 17 to 256 (query, head) columns of a sequence
+    ([400, 90], [3, 3], 2, 8, 128, 64, 0), ([400, 90], [4, 4], 2, 8, 64, 32, 0), ([700, 300], [33, 33], 2, 1, 128, 16, 0),
+    ([600, 129], [6, 6], 1, 8, 128, 128, 0), ([600, 129], [8, 8], 1, 8, 64, 16, 0), ([500, 260, 7], [13, 13, 13], 2, 5, 128, 32, 0),
+    ([900], [16], 1, 8, 128, 64, 200), ([640, 900], [9, 9], 2, 16, 64, 128, 130), ([900, 400], [12, 12], 1, 20, 128, 16, 0),
+    ([300, 2000], [16, 16], 2, 16, 128, 64, 0), ([40, 41], [17, 17], 1, 4, 64, 64, 7),
+]
+
+
+@pytest.mark.parametrize("case", COLUMNS, ids=lambda c: "n%d_q%d_H%d_G%d_D%d_S%d_w%d" % (max(c[0]), max(c[1]), *c[2:]))
+def test_columns_of_a_few_queries(case):
+    test_several_queries_per_sequence(case)
+
+
+@pytest.mark.parametrize("m", [1, 4, 8, 30])
+def test_one_sequence_in_many_parts(m):
+    """A single KV head: every block takes part of one key; a window cuts the others off."""
+    rng = np.random.default_rng(20 + m)
+    C = Cached(rng, [20000], 1, 128, 64)
+    q, q32 = _queries(rng, m, 8, 128, loud=4.0)
+    for window in (0, 6000):
+        out, lse = C.run(q, window=window)
+        C.check(q32, [m], out, lse, window=window)
+
+
+@pytest.mark.parametrize("m", [1, 6, 50])
+@pytest.mark.parametrize("rising", [False, True])
+def test_maximum_moves_inside_a_tile(m, rising):
+    """Scores that rise (or fall) by some powers of two every few tokens."""
+    rng = np.random.default_rng(30 + m)
+    C = Cached(rng, [500, 333], 1, 128, 32, spread=0.2)
+    q, q32 = _queries(rng, 2 * m, 4, 128, loud=0.2)
+    # every sequence's token t gets entry c in its first channel: 4-bit values on a coarse grid
+    for b, n in enumerate(C.lens):
+        k = C.k[b].copy()
+        ramp = np.arange(n) if rising else np.arange(n)[::-1]
+        k[:, 0, :16] = ((ramp // 5) * 0.01)[:, None]
+        kc, ks = K.entry(k.astype(np.float32), C.kg)
+        vc, vs = K.entry(C.v[b].astype(np.float32), C.vg)
+        slots = C.table[b, np.arange(n) // 32] * 32 + np.arange(n) % 32
+        host = C.cache.cpu().numpy()
+        K.store(host, slots, kc, ks, vc, vs, 32)
+        C.cache = _dev(host)
+        C.k[b], C.v[b] = K.load(host, slots, 32, 128, C.kg, C.vg)
+    q[..., :16], q32[..., :16] = 32.0, 32.0
+    out, lse = C.run(q)
+    C.check(q32, [m] * 2, out, lse)
+
+
+@pytest.mark.parametrize("m", [1, 5, 40])
+def test_pages_before_the_window_may_be_freed(m):
+    rng = np.random.default_rng(40 + m)
+    C = Cached(rng, [700, 90], 2, 64, 16)
+    q, q32 = _queries(rng, 2 * m, 16, 64)
+    table = C.table.copy()
+    table[0, :(700 - m + 1 - 100) // 16] = -1                          # pages that no query sees
+    C.args = (_dev(table), C.args[1])
+    out, lse = C.run(q, window=100)
+    C.check(q32, [m] * 2, out, lse, window=100)
+
+
+def test_workspace_is_used_again_by_calls_of_other_shapes():
+    import nvfp4_router_gate_gb300 as R
+    rng = np.random.default_rng(50)
+    C = Cached(rng, [3000, 200, 900], 2, 128, 64)
+    ws = R.new_workspace(R.nvfp4_kv_attention_workspace_size(300, 3, 16, 2, 128))
+    for m in (1, 40, 3, 1, 100, 1):
+        q, q32 = _queries(rng, 3 * m, 16, 128)
+        out, lse = C.run(q, workspace=ws)
+        C.check(q32, [m] * 3, out, lse, rows=4)
+    assert R.nvr_read_device_status(ws) == 0
