@@ -33,13 +33,17 @@ namespace nvr {
 namespace {
 
 constexpr int kStreamCols = 32;            // more columns of a sequence go to the tensor-memory kernel
-// Starting and ending a key costs a block about as much as this many tiles
-// (queries, joining the warps, storing): counted in the chunks, so that blocks
-// with many short keys get fewer tiles.
-constexpr int kKeyCost = 1;
+// Starting and ending a key (queries, joining the warps, storing) costs a block
+// about as much as this many tiles: 1.5 us beside 1.4 us for a tile with eight
+// columns, 3.0 beside 1.4 with sixteen (least squares over the blocks of the serving
+// batch and of 32 sequences with four queries).  Counted in the chunks, so that
+// blocks with many short keys get fewer tiles.
+template <int NT>
+constexpr int kKeyCost = NT;
 
 // A key's length in the flat order: its tiles, then kKeyCost places without work.
-__device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kKeyCost : 0; }
+template <int NT>
+__device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kKeyCost<NT> : 0; }
 
 // What a stage of the ring holds (everything about its key, so that nothing of
 // it stays in the consumers' registers); a run's first stage brings the queries.
@@ -123,7 +127,7 @@ kv_attention_kernel(const AttnParams p) {
   const int n_items = p.B * p.groups;
   const int per = (n_items + Sh::kThreads - 1) / Sh::kThreads;
   int mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost(group_of<NC, TILE>(p, i)) * p.Hkv;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost<NT>(group_of<NC, TILE>(p, i)) * p.Hkv;
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -147,15 +151,15 @@ kv_attention_kernel(const AttnParams p) {
     Group g;
     for (;; ++i) {
       g = group_of<NC, TILE>(p, i);
-      const int n = key_cost(g) * p.Hkv;
+      const int n = key_cost<NT>(g) * p.Hkv;
       if (f0 < at + n) break;
       at += n;
     }
     s_start[0] = i;
     s_start[1] = f0 - at;
     // the last chunk may hold nothing but the last key's places without work
-    const int ti = (f0 - at) % key_cost(g);
-    s_start[2] = ti < g.tiles || f1 - f0 > key_cost(g) - ti;
+    const int ti = (f0 - at) % key_cost<NT>(g);
+    s_start[2] = ti < g.tiles || f1 - f0 > key_cost<NT>(g) - ti;
   }
   __syncthreads();
   if (tid == 32 * NW) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
@@ -178,7 +182,7 @@ kv_attention_kernel(const AttnParams p) {
         primed = true;
         continue;
       }
-      const int cost = key_cost(g), n_item = cost * p.Hkv;
+      const int cost = key_cost<NT>(g), n_item = cost * p.Hkv;
       const int32_t* table = p.page_table + static_cast<int64_t>(g.b) * p.max_pages;
       int head = off / max(cost, 1), ti = off - head * cost;
       const int iq0 = g.c0 / p.G, rem0 = g.c0 - iq0 * p.G;
@@ -227,7 +231,7 @@ kv_attention_kernel(const AttnParams p) {
           for (int i = 0; i < pieces; ++i)
             if ((got >> i) & 1u) m.live |= each << (i * (part / 16));
           m.flags = (first ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u) |
-                    (key_f0 >= f0 && key_end <= f1 ? kWhole : 0u) | (key_end + kKeyCost >= f1 ? kDone : 0u) |
+                    (key_f0 >= f0 && key_end <= f1 ? kWhole : 0u) | (key_end + kKeyCost<NT> >= f1 ? kDone : 0u) |
                     (key_f0 > f0 ? kTail : 0u);
           if (key_f0 >= f0 && key_end > f1 && first)         // this block holds the key's first part
             p.joins[blockIdx.x] = {(key_end - 1) / chunk - key_f0 / chunk + 1, key_f0 > f0, g.q0 + iq0, rem0, g.n_cols,
@@ -705,7 +709,7 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + Sh::kCols - 1) / Sh::kCols);
   // the flat order of tiles is counted in 32 bits
   const int64_t items = static_cast<int64_t>(p.B) * p.groups;
-  const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1 + kKeyCost);
+  const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1 + kKeyCost<NT>);
   if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
   int64_t grid = static_cast<int64_t>(sms) * per_sm[dev];
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
