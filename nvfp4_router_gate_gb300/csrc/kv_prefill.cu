@@ -69,7 +69,8 @@ struct PrefillSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTileBytes;
   static constexpr int kV = kK + 2 * kTileBytes;
-  static constexpr int kRunsAt = kV + 2 * kTileBytes;
+  static constexpr int kOut = kV + 2 * kTileBytes;           // 128 bytes of each row on their way out
+  static constexpr int kRunsAt = kOut + 2 * kPTile * 128;
   static constexpr int kRowAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));   // per row: m, l of half 1
   static constexpr int kBarAt = kRowAt + 2 * kPTile * 4;
   static constexpr int kTotal = kBarAt + 48 * 8 + 64 + 1024;
@@ -141,19 +142,6 @@ __device__ __forceinline__ void tmem_load32_finish(uint32_t (&r)[32]) {
   asm volatile("" : "+r"(r[30]), "+r"(r[31]) :: "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void registers_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
-}
-template <int N>
-__device__ __forceinline__ void registers_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
-}
-// Registers of a thread, of the 128 each is launched with: softmax (two groups
-// of four warps), expansion, the rest.
-constexpr int kRegsSoftmax = 144, kRegsExpand = 128, kRegsRest = 96;
-static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsRest <= 4 * 128, "what the block was launched with");
-
 // A key's length in the flat order: its tiles, then places without work.
 __device__ __forceinline__ int key_cost(const Group& g) { return g.tiles ? g.tiles + kPKeyCost : 0; }
 
@@ -171,8 +159,8 @@ kv_prefill_kernel(const AttnParams p) {
            *v_full = k_empty + 2, *v_empty = v_full + 2, *q_full = v_empty + 2, *s_full = q_full + 2,
            *p_full = s_full + 2, *o_full = p_full + 2, *meet = o_full + 2, *x_ready = meet + 2, *x_full = x_ready + 1,
            *x_free = x_full + 1, *drained = x_free + 1, *q_raw = drained + 1, *h_full = q_raw + 2,
-           *p_half = h_full + 2;
-  int* s_words = reinterpret_cast<int*>(p_half + 2);
+           *p_half = h_full + 2, *q_empty = p_half + 2;
+  int* s_words = reinterpret_cast<int*>(q_empty + 2);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
   volatile int* abort_flag = s_words + 1;
   int* s_start = s_words + 2;                                // item, offset inside it
@@ -181,13 +169,14 @@ kv_prefill_kernel(const AttnParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, 14); }
+    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, 15); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4); mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 4); mbar_init(v_empty + i, 1);
       mbar_init(q_full + i, 4); mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4); mbar_init(o_full + i, 1);
-      mbar_init(meet + i, 4); mbar_init(q_raw + i, 4); mbar_init(h_full + i, 1); mbar_init(p_half + i, 4);
+      mbar_init(meet + i, 4); mbar_init(q_raw + i, 1); mbar_init(h_full + i, 1); mbar_init(p_half + i, 4);
+      mbar_init(q_empty + i, 5);
     }
     mbar_init(x_ready, 4); mbar_init(x_full, 4); mbar_init(x_free, 4); mbar_init(drained, 1);
     *abort_flag = 0;
@@ -262,7 +251,6 @@ kv_prefill_kernel(const AttnParams p) {
         return true;
       };
     if (warp >= 12) {
-      registers_shrink<kRegsRest>();
       if (warp == 13) {
       // ------------------------------------------------------------ the walk
       int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
@@ -395,6 +383,7 @@ kv_prefill_kernel(const AttnParams p) {
                 if (first && !k_ready(nxt)) return false;
                 score(w, (k0 + nxt) % 2);
                 commit(s_full + w);
+                if (nxt + (dual ? 1 : 2) >= n) commit(q_empty + w);
                 if (last) commit(k_empty + (k0 + nxt) % 2);
               } else if (cur >= 0) {
                 commit(o_full + w);
@@ -440,9 +429,44 @@ kv_prefill_kernel(const AttnParams p) {
             __syncwarp();
           }
         }
+      } else {
+        // -------------- the query rows of the coming run, raw into the halves' tiles
+        const float inv_G = 1.0f / static_cast<float>(p.G);
+        uint32_t sent[2] = {0, 0};
+        auto queries = [&]() -> bool {
+          for (;;) {
+            if (!take()) return false;
+            if (run.tiles < 0) return true;
+            for (int w = 0; w < 2; ++w) {
+              if (!run.dual && run.tiles <= w) continue;
+              if (!wait_all(q_empty + w, (sent[w] & 1) ^ 1)) return false;
+              ++sent[w];
+              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
+              // the columns [from, to) are in the tile; a query's lie next to each other
+              const int c0 = w ? run.col0 : 0, from = max(c0, 0), to = min(c0 + kPTile, run.n_cols);
+              if (lane == 0) mbar_arrive_expect_tx(q_raw + w, (to - from) * D * 2);
+              __syncwarp();
+              for (int dq = div_small(run.rem0 + from, inv_G) + lane; dq * p.G - run.rem0 < to; dq += 32) {
+                const int a = max(from, dq * p.G - run.rem0), b = min(to, (dq + 1) * p.G - run.rem0);
+                bulk_load(tile + (a - c0) * D * 2,
+                          p.q + (run.q0 + run.iq0 + dq) * p.q_stride +
+                              static_cast<int64_t>(run.head * p.G + run.rem0 + a - dq * p.G) * D,
+                          (b - a) * D * 2, q_raw + w);
+              }
+              __syncwarp();
+            }
+          }
+        };
+        if (!queries()) give_up();
+        if (*abort_flag) {
+          // copies in flight land before the block's memory goes away
+          const uint64_t drain = globaltimer_ns() + 1000000000ull;
+          for (int w = 0; w < 2; ++w)
+            while (sent[w] && !mbar_try_wait(q_raw + w, (sent[w] - 1) & 1))
+              if (globaltimer_ns() > drain) break;
+        }
       }
     } else if (warp >= 8) {
-        registers_shrink<kRegsExpand>();
         // ---------------------------------------------------- expanding the cache
         const int w = warp - 8, tok = lane & 7, qd = lane >> 3;
         const int S = 1 << p.page_shift;
@@ -590,7 +614,6 @@ kv_prefill_kernel(const AttnParams p) {
         };
         if (!expand()) give_up();
     } else {
-        registers_grow<kRegsSoftmax>();
         // ------------------------------------------------------------- softmax
         const int w = warp >> 2, wl = warp & 3, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
@@ -605,262 +628,270 @@ kv_prefill_kernel(const AttnParams p) {
           ph_meet ^= 1u;
           return ok;
         };
-        // One run; it stays in shared memory meanwhile, its fields are read where
-        // they are needed.
-        auto one_run = [&](const volatile Run& run) -> bool {
-            const int n_my = run.dual ? run.tiles : (run.tiles + 1 - w) / 2;
-            const int col = w == 0 ? row : row + run.col0;
-            const bool on = static_cast<uint32_t>(col) < static_cast<uint32_t>(run.n_cols);
-            // the row's query and head (recomputed where they are needed)
-            auto quotient = [&]() { return div_small(run.rem0 + (on ? col : 0), inv_G); };
-            auto head_of = [&](int dq) { return run.head * p.G + run.rem0 + (on ? col : 0) - dq * p.G; };
-            auto out_row = [&]() {
-              const int dq = quotient();
-              return static_cast<int64_t>(run.q0 + run.iq0 + dq) * p.Hq + head_of(dq);
-            };
-            const bool any_on = __any_sync(0xFFFFFFFFu, on);
-            const int pos = run.kv - run.n_q + run.iq0 + quotient();
-            const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
-            const int lo = p.window > 0 ? pos + 1 - p.window : 0;
-            float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
-            constexpr int RL = D / 8, RI = 32 / RL;          // lanes of a row of bf16, rows the warp stores at once
-            if (n_my > 0) {
-              // The half's query rows: copied raw into the tile, one bulk copy a row,
-              // then a row a thread, scaled into fp16's range, into the swizzled
-              // tile.  Vector f(i) of a row is its thread's i-th: with f(i) = i xor
-              // (x times the row) in GF(8), both f and f xor the row (the swizzle)
-              // take all values over eight rows: neither side has bank conflicts.
-              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
-              fence_proxy_async_smem();                      // (rows have left from there)
-              if (!sync_half()) return false;
-              const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on);
-              if (lane == 0) mbar_arrive_expect_tx(q_raw + w, __popc(rows_on) * D * 2);
+        // A run stays in shared memory meanwhile: its fields are read where they are needed.
+        auto my_tiles = [&](const volatile Run& run) { return run.dual ? run.tiles : (run.tiles + 1 - w) / 2; };
+        auto col_of = [&](const volatile Run& run) { return w == 0 ? row : row + run.col0; };
+        auto is_on = [&](const volatile Run& run) {
+          return static_cast<uint32_t>(col_of(run)) < static_cast<uint32_t>(run.n_cols);
+        };
+        // the query of the row, and its row of the result
+        auto quotient = [&](const volatile Run& run) {
+          return div_small(run.rem0 + (is_on(run) ? col_of(run) : 0), inv_G);
+        };
+        auto out_row = [&](const volatile Run& run) {
+          const int dq = quotient(run);
+          return static_cast<int64_t>(run.q0 + run.iq0 + dq) * p.Hq + run.head * p.G + run.rem0 +
+                 (is_on(run) ? col_of(run) : 0) - dq * p.G;
+        };
+        float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
+        // ---- a run's queries: the raw row of each thread, scaled into fp16's range,
+        // into the swizzled tile.  Vector f(i) of a row is its thread's i-th: with f(i)
+        // = i xor (x times the row) in GF(8), both f and f xor the row (the swizzle)
+        // take all values over eight rows: neither side has bank conflicts.
+        auto start = [&](const volatile Run& run) -> bool {
+          if (my_tiles(run) == 0) return true;
+          uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
+          if (!wait_all(q_raw + w, ph_q)) return false;
+          ph_q ^= 1u;
+          const bool on = is_on(run);
+          const int turn = ((row << 1) ^ (row & 4 ? 3 : 0)) & 7;
+          uint4 u[D / 8];
+          uint32_t big2 = 0;                                 // the largest magnitudes of the even and odd channels
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            u[i] = on ? *reinterpret_cast<const uint4*>(tile + row * D * 2 + ((i & 8) | ((i ^ turn) & 7)) * 16)
+                      : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              asm("max.u16x2 %0, %0, %1;" : "+r"(big2) : "r"(v[k] & 0x7FFF7FFFu));
+          }
+          if (!sync_half()) return false;
+          float up, down;
+          query_scale(max(big2 & 0xFFFFu, big2 >> 16), up, down);
+          to_log2 = down * (p.scale_log2 * run.k_gsa);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+            *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + row * 128 + (((i ^ turn ^ row) & 7) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(q_full + w);
+            if (run.dual) mbar_arrive(q_empty + w);          // (this half has nothing more to do with the tile)
+          }
+          return true;
+        };
+        // ---- its tiles
+        auto weigh = [&](const volatile Run& run) -> bool {
+          const int n_my = my_tiles(run);
+          const bool on = is_on(run), any_on = __any_sync(0xFFFFFFFFu, on);
+          const int pos = run.kv - run.n_q + run.iq0 + quotient(run);
+          const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
+          const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+          m_neg = INFINITY;
+          l = 0.0f;
+          for (int i = 0; i < n_my; ++i) {
+            const int j = run.dual ? i : 2 * i + w;
+            const int t0 = (run.tile0 + j) * kPTile;
+            if (!wait_all(s_full + w, ph_s)) return false;
+            ph_s ^= 1u;
+            tc_fence_after();
+            if (!any_on) {
+              // (rows that nobody asked for: their P may be anything)
+              tc_fence_before();
               __syncwarp();
-              if (on) {
-                const int dq = quotient();
-                bulk_load(tile + row * D * 2,
-                          p.q + (run.q0 + run.iq0 + dq) * p.q_stride + static_cast<int64_t>(head_of(dq)) * D, D * 2,
-                          q_raw + w);
-              }
-              if (!wait_all(q_raw + w, ph_q)) return false;
-              ph_q ^= 1u;
-              const int turn = ((row << 1) ^ (row & 4 ? 3 : 0)) & 7;
-              uint4 u[D / 8];
-              uint32_t big = 0;
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                u[i] = on ? *reinterpret_cast<const uint4*>(tile + row * D * 2 + ((i & 8) | ((i ^ turn) & 7)) * 16)
-                          : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) big = max(big, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
-              }
-              if (!sync_half()) return false;
-              float up, down;
-              query_scale(big, up, down);
-              to_log2 = down * (p.scale_log2 * run.k_gsa);
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
-                *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + row * 128 +
-                                          (((i ^ turn ^ row) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(q_full + w);
-            }
-            for (int i = 0; i < n_my; ++i) {
-              const int j = run.dual ? i : 2 * i + w;
-              const int t0 = (run.tile0 + j) * kPTile;
-              if (!wait_all(s_full + w, ph_s)) return false;
-              ph_s ^= 1u;
-              tc_fence_after();
-              if (!any_on) {
-                // (rows that nobody asked for: their P may be anything)
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                  mbar_arrive(p_half + w);
-                  mbar_arrive(p_full + w);
-                }
-                ph_h ^= 1u;
-                continue;
-              }
-              const uint32_t bytes = s_live[(n_tile + j) % kLive];
-              // bit i: tokens 16 i .. of the tile are in the cache
-              const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
-              const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
-              // bit x: the row sees token t0 + c + x (c a multiple of 32)
-              const int from = lo - t0, to = hi - t0;
-              auto seen32 = [&](int c) {
-                const int a = min(max(from - c, 0), 32), b = min(max(to - c, 0), 32);
-                const uint32_t m = (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
-                const uint32_t two = live >> (c / 16);
-                return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
-              };
-              // In two halves of 64 tokens: P V of the first starts under the second.
-#pragma unroll 1
-              for (int c0 = 0; c0 < kPTile; c0 += kPTile / 2) {
-                uint32_t pr[kPTile / 4];
-                float sum;
-                auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
-                  uint64_t sum2 = f2_pack(0.0f, 0.0f);
-                  const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
-                  uint32_t s[2][32];
-                  tmem_load32_start(t_s + c0, s[0]);
-#pragma unroll
-                  for (int c = 0; c < kPTile / 2; c += 32) {
-                    uint32_t (&now)[32] = s[(c / 32) % 2];
-                    tmem_load32_finish(now);
-                    if (c + 32 < kPTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
-                    const uint32_t see = hidden ? seen32(c0 + c) : 0xFFFFFFFFu;
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                      const uint64_t v =
-                          f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
-                      float v0 = f2_lo(v), v1 = f2_hi(v);
-                      if (hidden) {
-                        v0 = see & (1u << x) ? v0 : -INFINITY;
-                        v1 = see & (2u << x) ? v1 : -INFINITY;
-                      }
-                      const float a = ex2(v0), b = ex2(v1);
-                      sum2 = f2_add(sum2, f2_pack(a, b));
-                      pr[(c + x) / 2] = pack_f16(a, b);
-                    }
-                  }
-                  sum = f2_lo(sum2) + f2_hi(sum2);
-                };
-                // Weights that add up to more than 2^kRescaleAt hold a score far above m
-                // (a weight above 4, at least): no maximum is taken of the others.  (m at
-                // or above every score: at most 64 weights of 1.)
-                for (bool move = i == 0 && c0 == 0;; move = true) {
-                  if (move) {
-                    // m moves to the largest score so far (of the tokens not yet weighed)
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = c0; c < kPTile; c += 32) {
-                      uint32_t s[32];
-                      tmem_load32_start(t_s + c, s);
-                      tmem_load32_finish(s);
-                      const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
-#pragma unroll
-                      for (int x = 0; x < 32; ++x)
-                        top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
-                    }
-                    const float now = fminf(m_neg, -top);
-                    const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-                    m_neg = now;
-                    l *= shrink;
-                    if (i > 0 || c0 > 0) {
-                      // (earlier tiles are in O, S came after them; the first half may be on its way)
-                      if (c0 > 0) {
-                        if (!wait_all(h_full + w, ph_h)) return false;
-                        tc_fence_after();
-                      }
-#pragma unroll 1
-                      for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        uint32_t y[16];
-                        tmem_load16(t_o + c, o);
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
-                        tmem_store16(t_o + c, y);
-                      }
-                    }
-                  }
-                  if (masked) weights(std::true_type{});
-                  else weights(std::false_type{});
-                  if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
-                }
-                l += sum;
-                // P over the columns of S that have been read
-#pragma unroll
-                for (int c = 0; c < kPTile / 4; c += 16) {
-                  uint32_t x[16];
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-                  tmem_store16(t_s + c0 / 2 + c, x);
-                }
-                tmem_store_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive((c0 ? p_full : p_half) + w);
+              if (lane == 0) {
+                mbar_arrive(p_half + w);
+                mbar_arrive(p_full + w);
               }
               ph_h ^= 1u;
+              continue;
             }
-            n_tile += run.tiles;
-            if (n_my > 0) {
-              if (!wait_all(o_full + w, ph_o)) return false;
-              ph_o ^= 1u;
-              tc_fence_after();
-            }
-            float m = -m_neg;
-            // ---- both halves on one set of rows: half 1 hands its rows over
-            const bool cross = !run.dual && run.tiles > 1;
-            float keep = 1.0f, other = 0.0f;
-            const int x_row = col & (kPTile - 1);
-            float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + x_row * D;   // the query tiles, now free
-            if (cross) {
-              if (w == 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(x_ready);         // (its scores are done with the queries)
-                if (!wait_all(x_full, ph_x)) return false;
-                const float m1 = s_row[x_row], l1 = s_row[kPTile + x_row];
-                const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
-                keep = ex2(m - base);
-                other = ex2(m1 - base);
-                l = l * keep + l1 * other;
-                m = top;
-              } else {
-                if (!wait_all(x_ready, ph_x)) return false;
+            const uint32_t bytes = s_live[(n_tile + j) % kLive];
+            // bit i: tokens 16 i .. of the tile are in the cache
+            const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
+            const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
+            // bit x: the row sees token t0 + c + x (c a multiple of 32)
+            const int from = lo - t0, to = hi - t0;
+            auto seen32 = [&](int c) {
+              const int a = min(max(from - c, 0), 32), b = min(max(to - c, 0), 32);
+              const uint32_t m = (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
+              const uint32_t two = live >> (c / 16);
+              return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
+            };
+            // In two halves of 64 tokens: P V of the first starts under the second.
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  float o[32];
-                  tmem_load32(t_o + c, o);
+            for (int c0 = 0; c0 < kPTile; c0 += kPTile / 2) {
+              uint32_t pr[kPTile / 4];
+              float sum;
+              auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
+                uint64_t sum2 = f2_pack(0.0f, 0.0f);
+                const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
+                uint32_t s[2][32];
+                tmem_load32_start(t_s + c0, s[0]);
 #pragma unroll
-                  for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
-                        make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                for (int c = 0; c < kPTile / 2; c += 32) {
+                  uint32_t (&now)[32] = s[(c / 32) % 2];
+                  tmem_load32_finish(now);
+                  if (c + 32 < kPTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
+                  const uint32_t see = hidden ? seen32(c0 + c) : 0xFFFFFFFFu;
+#pragma unroll
+                  for (int x = 0; x < 32; x += 2) {
+                    const uint64_t v =
+                        f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+                    float v0 = f2_lo(v), v1 = f2_hi(v);
+                    if (hidden) {
+                      v0 = see & (1u << x) ? v0 : -INFINITY;
+                      v1 = see & (2u << x) ? v1 : -INFINITY;
+                    }
+                    const float a = ex2(v0), b = ex2(v1);
+                    sum2 = f2_add(sum2, f2_pack(a, b));
+                    pr[(c + x) / 2] = pack_f16(a, b);
+                  }
                 }
-                s_row[x_row] = m;
-                s_row[kPTile + x_row] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(x_full);
-                if (!wait_all(x_free, ph_x)) return false;
+                sum = f2_lo(sum2) + f2_hi(sum2);
+              };
+              // Weights that add up to more than 2^kRescaleAt hold a score far above m
+              // (a weight above 4, at least): no maximum is taken of the others.  (m at
+              // or above every score: at most 64 weights of 1.)
+              for (bool move = i == 0 && c0 == 0;; move = true) {
+                if (move) {
+                  // m moves to the largest score so far, this half's included
+                  float top = -INFINITY;
+#pragma unroll 1
+                  for (int c = c0; c < c0 + kPTile / 2; c += 32) {
+                    uint32_t s[32];
+                    tmem_load32_start(t_s + c, s);
+                    tmem_load32_finish(s);
+                    const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                      top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
+                  }
+                  const float now = fminf(m_neg, -top);
+                  const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                  m_neg = now;
+                  l *= shrink;
+                  if (i > 0 || c0 > 0) {
+                    // (earlier tiles are in O, S came after them; the first half may be on its way)
+                    if (c0 > 0) {
+                      if (!wait_all(h_full + w, ph_h)) return false;
+                      tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                      float o[16];
+                      uint32_t y[16];
+                      tmem_load16(t_o + c, o);
+#pragma unroll
+                      for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
+                      tmem_store16(t_o + c, y);
+                    }
+                  }
+                }
+                if (masked) weights(std::true_type{});
+                else weights(std::false_type{});
+                if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
               }
-              ph_x ^= 1u;
-            }
-            if (!run.dual && w == 1) {
+              l += sum;
+              // P over the columns of S that have been read
+#pragma unroll
+              for (int c = 0; c < kPTile / 4; c += 16) {
+                uint32_t x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+                tmem_store16(t_s + c0 / 2 + c, x);
+              }
+              tmem_store_wait();
               tc_fence_before();
-              return true;
+              __syncwarp();
+              if (lane == 0) mbar_arrive((c0 ? p_full : p_half) + w);
             }
+            ph_h ^= 1u;
+          }
+          n_tile += run.tiles;
+          if (n_my > 0) {
+            if (!wait_all(o_full + w, ph_o)) return false;
+            ph_o ^= 1u;
+            tc_fence_after();
+          }
+          return true;
+        };
+        // ---- its rows
+        auto finish = [&](const volatile Run& run) -> bool {
+          const int col = col_of(run);
+          const bool on = is_on(run);
+          float m = -m_neg;
+          // both halves on one set of rows: half 1 hands its rows over, through the
+          // query tiles (their scores are complete)
+          const bool cross = !run.dual && run.tiles > 1;
+          float keep = 1.0f, other = 0.0f;
+          const int x_row = col & (kPTile - 1);
+          float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + x_row * D;
+          if (cross) {
+            if (w == 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(x_ready);           // (its scores are done with the queries)
+              if (!wait_all(x_full, ph_x)) return false;
+              const float m1 = s_row[x_row], l1 = s_row[kPTile + x_row];
+              const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
+              keep = ex2(m - base);
+              other = ex2(m1 - base);
+              l = l * keep + l1 * other;
+              m = top;
+            } else {
+              if (!wait_all(x_ready, ph_x)) return false;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_load32(t_o + c, o);
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
+                      make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+              }
+              s_row[x_row] = m;
+              s_row[kPTile + x_row] = l;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(x_full);
+              if (!wait_all(x_free, ph_x)) return false;
+            }
+            ph_x ^= 1u;
+          }
+          if (run.dual || w == 0) {
             const bool whole = run.whole;
             float* part = p.partials + static_cast<size_t>(run.slot) * NC * (D + 2);
             const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
-            // The rows leave through shared memory (the query tile, now free; the
-            // handed-over rows, behind their reader), so that the warp stores whole
-            // lines: bf16 results in one pass, fp32 partial rows in two.  16-byte
-            // vectors are swizzled by the row inside every 128 bytes.
-            const int pitch = cross ? D * 4 : D * 2;
-            uint8_t* rows_at = smem + Sm::kQ + (cross ? 0 : w * Sm::kTileBytes) + wl * 32 * pitch;
-            const int64_t row_at = whole ? out_row() * D : static_cast<int64_t>(col) * D;
+            // 128 bytes of each row at a time through shared memory, so that the warp
+            // stores whole lines; 16-byte vectors are swizzled by the row
+            uint8_t* rows_at = smem + Sm::kOut + warp * 32 * 128;
+            // (a lane stores vector lane % 8 of every fourth row)
+            const int64_t row_at = whole ? out_row(run) * (D * 2) : static_cast<int64_t>(col) * (D * 4);
+            const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on) >> (lane / 8);
+            uint8_t* base = whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part + 2 * NC);
+            uint8_t* to[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              to[i] = base + __shfl_sync(0xFFFFFFFFu, row_at, 4 * i + lane / 8) + (lane % 8) * 16;
             auto put_vector = [&](int i, uint4 v) {
-              *reinterpret_cast<uint4*>(rows_at + lane * pitch + (((i & ~7) | ((i ^ lane) & 7)) << 4)) = v;
+              *reinterpret_cast<uint4*>(rows_at + lane * 128 + (((i ^ lane) & 7) << 4)) = v;
             };
-            // every row's RL vectors, to element `at` of each row's place
-            auto store_rows = [&](auto* base, int at, int per_vector) {
+            // every row's eight vectors, to byte `at` of each row's place
+            auto store_rows = [&](int at) {
               __syncwarp();
-#pragma unroll 2
-              for (int r0 = 0; r0 < 32; r0 += RI) {
-                const int r = r0 + lane / RL, i = lane % RL;
-                const int64_t to = __shfl_sync(0xFFFFFFFFu, row_at, r);
-                const bool there = __shfl_sync(0xFFFFFFFFu, static_cast<int>(on), r) != 0;
-                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + r * pitch + (((i & ~7) | ((i ^ r) & 7)) << 4));
-                if (there) *reinterpret_cast<uint4*>(base + to + at + i * per_vector) = v;
+              const int r = lane / 8;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + (4 * i + r) * 128 +
+                                                                (((lane ^ (4 * i + r)) & 7) << 4));
+                if ((rows_on >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = v;
               }
               __syncwarp();
             };
@@ -888,37 +919,44 @@ kv_prefill_kernel(const AttnParams p) {
                     const __nv_bfloat162 y = __floats2bfloat162_rn(o[x + 2 * k] * inv, o[x + 2 * k + 1] * inv);
                     h[k] = *reinterpret_cast<const uint32_t*>(&y);
                   }
-                  put_vector((c + x) / 8, make_uint4(h[0], h[1], h[2], h[3]));
+                  put_vector((c % 64 + x) / 8, make_uint4(h[0], h[1], h[2], h[3]));
                 }
+                if (c % 64) store_rows((c - 32) * 2);
               } else {
 #pragma unroll
                 for (int x = 0; x < 32; x += 4)
-                  put_vector((c % (D / 2) + x) / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
-                                                              __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
-                if ((c + 32) % (D / 2) == 0) store_rows(part + 2 * NC, c + 32 - D / 2, 4);
+                  put_vector(x / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
+                                               __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+                store_rows(c * 4);
               }
             }
-            if (whole) store_rows(p.out, 0, 8);
-            tc_fence_before();
             if (cross) {
               __syncwarp();
               if (lane == 0) mbar_arrive(x_free);
             }
             if (whole) {
               if (on && p.lse)
-                p.lse[out_row()] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+                p.lse[out_row(run)] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
             } else if (on) {
               part[col] = m;
               part[NC + col] = l;
             }
-            return true;
+          }
+          tc_fence_before();
+          if (!run.dual && my_tiles(run) > 0) {
+            fence_proxy_async_smem();                        // (rows went through the query tiles)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty + w);
+          }
+          return true;
         };
         auto softmax = [&]() -> bool {
-          for (;; ++n_taken) {
-            const int s = n_taken % kRuns;
-            if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return false;
-            if (s_runs[s].tiles < 0) return true;
-            if (!one_run(s_runs[s])) return false;
+          for (int n = 0;; ++n) {
+            const int s = n % kRuns;
+            if (!wait_all(run_full + s, (n / kRuns) & 1)) return false;
+            const volatile Run& run = s_runs[s];
+            if (run.tiles < 0) return true;
+            if (!start(run) || !weigh(run) || !finish(run)) return false;
             __syncwarp();
             if (lane == 0) mbar_arrive(run_empty + s);
           }
