@@ -3,11 +3,12 @@
 //
 //   m = max m_i,  w_i = 2^(m_i - m),  out = sum w_i O_i / sum w_i l_i,
 //   lse = (m + log2 sum w_i l_i) / log2 e
-// for every row, over the parts i of its key in chunk order.  A row has one warp,
-// or four that take every fourth part where keys have many (one long sequence: 57
-// parts); D / 32 channels a lane, the (m, l) of 32 parts in the lanes, eight parts'
-// vectors under way.  Bound by the latency of three or four dependent reads from
-// L2; blocks without a cut key leave at once.
+// for every row, over the parts i of its key in chunk order; D / 32 channels a lane.
+// Bound by the latency of a few dependent reads from L2, so a warp has as many on
+// their way as it can: of keys with few parts it takes four rows at a time, the (m, l)
+// of eight parts of each in its lanes; of a key with many (one long sequence: 57
+// parts) four warps share one row, each taking every fourth part, the (m, l) of 32
+// of them in the lanes.  Blocks without a cut key leave at once.
 #include "kv_attention.cuh"
 
 namespace nvr {
@@ -15,104 +16,198 @@ namespace nvr {
 namespace {
 
 constexpr int kJoinWarps = 4;
+constexpr int kJoinRows = 4;               // rows a warp takes at a time
 
-template <int D, int WPR>                        // warps of a row
+// The place of a row: its query's row and its head.
+__device__ __forceinline__ int64_t out_row(const KeyJoin& k, int n, int Hq, int G) {
+  const int dq = div_small(k.rem0 + n, 1.0f / static_cast<float>(G));
+  return static_cast<int64_t>(k.q0 + dq) * Hq + k.head * G + (k.rem0 + n - dq * G);
+}
+
+template <int CH>
+__device__ __forceinline__ void load_channels(const float* src, float (&y)[CH]) {
+  if (CH == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(src);
+    y[0] = v.x; y[1] = v.y; y[CH - 2] = v.z; y[CH - 1] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(src);
+    y[0] = v.x; y[1] = v.y;
+  }
+}
+
+template <int CH>
+__device__ __forceinline__ void store_channels(__nv_bfloat16* dst, const float (&acc)[CH], float inv) {
+#pragma unroll
+  for (int x = 0; x < CH; x += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + x) = __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
+}
+
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+}
+
+// Part i of a key is in the first slot of its block, but the key's first one if the
+// key starts inside the chunk.
+__device__ __forceinline__ const float* part_of(const float* partials, const KeyJoin& k, int i, size_t slot) {
+  return partials + (2 * (blockIdx.x + static_cast<size_t>(i)) + (i == 0 ? k.tail : 0)) * slot;
+}
+
+template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-kv_join_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ partials, int NC, int Hq, int G,
-               __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-  constexpr int CH = D / 32;
-  __shared__ float s_top[kJoinWarps], s_sum[kJoinWarps], s_acc[WPR > 1 ? kJoinWarps : 1][32][CH];
+kv_join_few_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ partials, int NC, int Hq, int G,
+                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  constexpr int CH = D / 32, R = kJoinRows, P = 32 / R;      // rows of a warp, parts at a time
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const KeyJoin k = joins[blockIdx.x];
   if (k.n_parts < 2) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % WPR;
-  const float inv_G = 1.0f / static_cast<float>(G);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t slot = static_cast<size_t>(NC) * (D + 2);
-  // part i is in the first slot of its block, but the key's first one if the key
-  // starts inside the chunk
-  auto part_at = [&](int i) { return partials + (2 * (blockIdx.x + i) + (i == 0 ? k.tail : 0)) * slot; };
-  const int parts = (k.n_parts - mine + WPR - 1) / WPR;      // this warp's: mine, mine + WPR, ...
-  constexpr int RB = kJoinWarps / WPR;                       // rows of the block at a time
-  for (int n = blockIdx.y * RB + warp / WPR; n < k.n_cols; n += gridDim.y * RB) {
-    float top = -INFINITY, sum = 0.0f, acc[CH];
+  const int n0 = (blockIdx.y * (blockDim.x / 32) + warp) * R;
+  if (n0 >= k.n_cols) return;
+  const int mine = n0 + lane / P;                            // this lane's row among the (m, l)
+  float top = -INFINITY, sum = 0.0f, acc[R][CH];
 #pragma unroll
-    for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
-    for (int b = 0; b < parts; b += 32) {
-      const int m = min(32, parts - b);
-      float w = -INFINITY, l = 0.0f;
-      if (lane < m) {
-        const float* src = part_at((b + lane) * WPR + mine) + n;
-        w = src[0];
-        l = src[NC];
-      }
-      float high = fmaxf(top, w);
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
-      const float base = high == -INFINITY ? 0.0f : high, shrink = ex2(top - base);
-      top = high;
-      w = ex2(w - base);
-      sum = sum * shrink + w * l;
+    for (int x = 0; x < CH; ++x) acc[r][x] = 0.0f;
+  // (rows past the last: the last row again, not stored)
+  auto load = [&](int i, float (&y)[R][CH]) {
 #pragma unroll
-      for (int x = 0; x < CH; ++x) acc[x] *= shrink;
-      for (int i0 = 0; i0 < m; i0 += 8) {
-        float y[8][CH];
+    for (int r = 0; r < R; ++r)
+      load_channels<CH>(part_of(partials, k, i, slot) + 2 * NC + min(n0 + r, k.n_cols - 1) * D + lane * CH, y[r]);
+  };
+  float y[2][R][CH];
+  load(0, y[0]);
+  load(1, y[1]);
+  for (int b = 0; b < k.n_parts; b += P) {
+    const int m = min(P, k.n_parts - b);
+    float w = -INFINITY, l = 0.0f;
+    if (lane % P < m && mine < k.n_cols) {
+      const float* src = part_of(partials, k, b + lane % P, slot) + mine;
+      w = src[0];
+      l = src[NC];
+    }
+    float high = fmaxf(top, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // (past the end: the last part, under a weight of zero)
-          const float* src = part_at((b + min(i0 + i, m - 1)) * WPR + mine) + 2 * NC + n * D + lane * CH;
-          if (CH == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            y[i][0] = v.x; y[i][1] = v.y; y[i][CH - 2] = v.z; y[i][CH - 1] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            y[i][0] = v.x; y[i][1] = v.y;
-          }
-        }
+    for (int d = P / 2; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
+    const float base = high == -INFINITY ? 0.0f : high, shrink = ex2(top - base);
+    top = high;
+    w = ex2(w - base);
+    sum = sum * shrink + w * l;
+    if (b > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float wi = __shfl_sync(0xFFFFFFFFu, w, i0 + i);
+      for (int r = 0; r < R; ++r) {
+        const float f = __shfl_sync(0xFFFFFFFFu, shrink, r * P);
 #pragma unroll
-          for (int x = 0; x < CH; ++x) acc[x] += wi * y[i][x];
-        }
+        for (int x = 0; x < CH; ++x) acc[r][x] *= f;
       }
     }
+    for (int i0 = 0; i0 < m; i0 += 2) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (WPR > 1) {
-      // the warps of the row, in order
-      __syncthreads();                                       // (the last row's are read)
-      if (lane == 0) {
-        s_top[warp] = top;
-        s_sum[warp] = sum;
+      for (int i = 0; i < 2; ++i) {
+        // (past the end of the batch: a weight of zero)
+        const float wi = i0 + i < m ? w : 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float f = __shfl_sync(0xFFFFFFFFu, wi, r * P + ((i0 + i) % P));
+#pragma unroll
+          for (int x = 0; x < CH; ++x) acc[r][x] += f * y[i][r][x];
+        }
       }
-#pragma unroll
-      for (int x = 0; x < CH; ++x) s_acc[WPR > 1 ? warp : 0][lane][x] = acc[x];
-      __syncthreads();
-      if (mine) continue;
-#pragma unroll
-      for (int i = 1; i < WPR; ++i) top = fmaxf(top, s_top[warp + i]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      sum = 0.0f;
-#pragma unroll
-      for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WPR; ++i) {
-        const float w = ex2(s_top[warp + i] - base);
-        sum += w * s_sum[warp + i];
-#pragma unroll
-        for (int x = 0; x < CH; ++x) acc[x] += w * s_acc[WPR > 1 ? warp + i : 0][lane][x];
+      if (b + i0 + 2 < k.n_parts) {
+        load(b + i0 + 2, y[0]);
+        load(min(b + i0 + 3, k.n_parts - 1), y[1]);
       }
     }
-    const int dq = div_small(k.rem0 + n, inv_G);
-    const int64_t row = static_cast<int64_t>(k.q0 + dq) * Hq + k.head * G + (k.rem0 + n - dq * G);
-    const float inv = sum > 0.0f ? __fdividef(k.v_gsa, sum) : 0.0f;
-    __nv_bfloat16* dst = out + row * D + lane * CH;
-#pragma unroll
-    for (int x = 0; x < CH; x += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + x) = __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
-    if (lse && lane == 0) lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
   }
+#pragma unroll
+  for (int d = P / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float s = __shfl_sync(0xFFFFFFFFu, sum, r * P);
+    if (n0 + r < k.n_cols)
+      store_channels<CH>(out + out_row(k, n0 + r, Hq, G) * D + lane * CH, acc[r], s > 0.0f ? __fdividef(k.v_gsa, s) : 0.0f);
+  }
+  if (lse && lane % P == 0 && mine < k.n_cols) lse[out_row(k, mine, Hq, G)] = lse_of(top, sum);
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+kv_join_many_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ partials, int NC, int Hq, int G,
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  constexpr int CH = D / 32, W = kJoinWarps;
+  __shared__ float s_top[W], s_sum[W], s_acc[W][32][CH];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const KeyJoin k = joins[blockIdx.x];
+  if (k.n_parts < 2) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t slot = static_cast<size_t>(NC) * (D + 2);
+  const int parts = (k.n_parts - warp + W - 1) / W;          // this warp's: warp, warp + W, ...
+  const int n = blockIdx.y;
+  if (n >= k.n_cols) return;
+  float top = -INFINITY, sum = 0.0f, acc[CH];
+#pragma unroll
+  for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
+  for (int b = 0; b < parts; b += 32) {
+    const int m = min(32, parts - b);
+    float w = -INFINITY, l = 0.0f;
+    if (lane < m) {
+      const float* src = part_of(partials, k, (b + lane) * W + warp, slot) + n;
+      w = src[0];
+      l = src[NC];
+    }
+    float high = fmaxf(top, w);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
+    const float base = high == -INFINITY ? 0.0f : high, shrink = ex2(top - base);
+    top = high;
+    w = ex2(w - base);
+    sum = sum * shrink + w * l;
+#pragma unroll
+    for (int x = 0; x < CH; ++x) acc[x] *= shrink;
+    for (int i0 = 0; i0 < m; i0 += 8) {
+      float y[8][CH];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        // (past the end: the last part, under a weight of zero)
+        load_channels<CH>(part_of(partials, k, (b + min(i0 + i, m - 1)) * W + warp, slot) + 2 * NC + n * D + lane * CH, y[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl_sync(0xFFFFFFFFu, w, i0 + i);
+#pragma unroll
+        for (int x = 0; x < CH; ++x) acc[x] += wi * y[i][x];
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  // the warps of the row, in order
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_sum[warp] = sum;
+  }
+#pragma unroll
+  for (int x = 0; x < CH; ++x) s_acc[warp][lane][x] = acc[x];
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int i = 1; i < W; ++i) top = fmaxf(top, s_top[i]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  sum = 0.0f;
+#pragma unroll
+  for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float w = ex2(s_top[i] - base);
+    sum += w * s_sum[i];
+#pragma unroll
+    for (int x = 0; x < CH; ++x) acc[x] += w * s_acc[i][lane][x];
+  }
+  const int64_t row = out_row(k, n, Hq, G);
+  store_channels<CH>(out + row * D + lane * CH, acc, sum > 0.0f ? __fdividef(k.v_gsa, sum) : 0.0f);
+  if (lse && lane == 0) lse[row] = lse_of(top, sum);
 }
 
 }  // namespace
@@ -123,13 +218,12 @@ nvr_status launch_kv_join(const AttnParams& p, int D, int blocks, int NC, int64_
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // A key has about blocks / keys parts.  From eight on a row gets a block (one
-  // sequence of 131072 tokens, 57 parts: 49.6 -> 41.1 us for the call); below it a
-  // warp, two rows (of 256 columns four) to a warp, so that there are few blocks
-  // with nothing to do.
+  // sequence of 131072 tokens, 57 parts: 49.6 -> 41.1 us for the call).
   const bool many = keys * 8 <= blocks;
-  const int rows = many ? 1 : (NC > 32 ? 4 : 2) * kJoinWarps;
+  const int warps = many ? kJoinWarps : NC / kJoinRows < kJoinWarps ? NC / kJoinRows : kJoinWarps;
+  const int rows = many ? 1 : warps * kJoinRows;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((NC + rows - 1) / rows));
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.blockDim = dim3(32 * warps);
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
@@ -137,8 +231,8 @@ nvr_status launch_kv_join(const AttnParams& p, int D, int blocks, int NC, int64_
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<const KeyJoin*>(p.joins),
                                           static_cast<const float*>(p.partials), NC, p.Hq, p.G, p.out, p.lse));
   };
-  if (many) return D == 128 ? go(kv_join_kernel<128, 4>) : go(kv_join_kernel<64, 4>);
-  return D == 128 ? go(kv_join_kernel<128, 1>) : go(kv_join_kernel<64, 1>);
+  if (many) return D == 128 ? go(kv_join_many_kernel<128>) : go(kv_join_many_kernel<64>);
+  return D == 128 ? go(kv_join_few_kernel<128>) : go(kv_join_few_kernel<64>);
 }
 
 }  // namespace nvr

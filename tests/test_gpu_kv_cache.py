@@ -386,6 +386,21 @@ def test_one_sequence_in_many_parts(m):
         C.check(q32, [m], out, lse, window=window)
 
 
+@pytest.mark.parametrize("m", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_long_sequence_among_short_ones(m, D):
+    """One key in many parts beside many that nothing cuts."""
+    rng = np.random.default_rng(60 + m)
+    lens = [30] * 30 + [12000] + [50] * 30
+    C = Cached(rng, lens, 1, D, 128)
+    n_q = [1] * 61
+    n_q[30] = m
+    q, q32 = _queries(rng, sum(n_q), 4, D, loud=3.0)
+    cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+    out, lse = C.run(q, cu_q=_dev(cu), max_q=m)
+    C.check(q32, n_q, out, lse)
+
+
 @pytest.mark.parametrize("m", [1, 6, 50])
 @pytest.mark.parametrize("rising", [False, True])
 def test_maximum_moves_inside_a_tile(m, rising):
