@@ -110,7 +110,10 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  * multiple of Hkv.  Scores, softmax statistics and outputs are accumulated in
  * fp32; the weights p_t enter the second product as fp16, relative to a running
  * maximum; results do not depend on the order in which the GPU runs the
- * blocks.
+ * blocks.  One kernel and, unless no key can be cut over blocks, a second one that
+ * joins the parts of those that were.  The workspace's size depends on D alone (T_max,
+ * B_max and the heads are checked): partial results of the resident blocks.  A bounded
+ * wait that runs out sets the workspace's status word (nvr_read_device_status).
  */
 size_t nvfp4_kv_attention_workspace_size(int64_t T_max, int64_t B_max, int Hq, int Hkv, int D);
 nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_t T, int Hq, int Hkv, int D,

@@ -1,7 +1,7 @@
 // kv_attention.cu -- softmax attention over the paged NVFP4 key/value cache,
-// streaming form (sm_103a): up to 32 (query, head) columns share one pass over
+// streaming form (sm_103a): 8 or 16 (query, head) columns share one pass over
 // their KV head's tokens.  One or a few queries per sequence: bound by the
-// cache's bytes.
+// cache's bytes, from 16 columns on by the warp-level matrix instructions.
 //
 // Mathematics.  For a column's query q and its visible tokens t
 //   s_t = scale * q . k_t,  m = max s_t,  p_t = exp(s_t - m),
@@ -9,7 +9,9 @@
 // in one pass: a running m, l = sum p and O = sum p v, rescaled when m moves;
 // partial (m, l, O) triples of disjoint token sets join by the same rescaling.
 // m is only moved when a score passes it by more than 8 (base 2): p_t stays
-// below 2^8, inside fp16, and most tiles skip the rescaling.
+// below 2^8, inside fp16 (the one rounding below 32 bits: the second product's
+// operands are fp16, their errors 2^-11 of each weight), and most tiles skip the
+// rescaling.
 //
 // Both products run transposed, S^T = K Q^T and O^T = V^T P^T: the tokens
 // (resp. channels) are the 16 rows of the matrix instruction and the columns
@@ -20,11 +22,20 @@
 // may run over the channels (tokens) in any order as long as both operands
 // agree, so each lane takes the 16 bytes it loads as they are.
 //
-// Work: the tiles (16 tokens for each of MW groups of each of NW warps) of all (sequence, column group, KV head) keys,
-// laid end to end, are cut into equal chunks, one per resident block; a key
-// cut by a chunk border leaves partials in the workspace and the last block to
-// arrive (ticket) joins them in chunk order, so results do not depend on timing.
-// One producer warp feeds a ring of tiles with bulk copies, a page of one KV head each.
+// Work: the tiles (16 tokens for each of MW groups of each of NW warps) of all
+// (sequence, column group, KV head) keys, laid end to end, are cut into equal
+// chunks, one per resident block; a key cut by a chunk border leaves partials in
+// the workspace, joined in chunk order by csrc/kv_join.cu, so that results do not
+// depend on timing.  One producer warp feeds a ring of tiles with bulk copies, a
+// page of one KV head each.
+//
+// Measured (D = 128, 8 KV heads of 8 heads): 128 sequences of up to 8192 tokens 121
+// us, 4.5 TB/s, 0.67 of the copy bandwidth (0.88 of it between the first tiles and the
+// first blocks to finish; the blocks' times spread by 12 %, memory is not shared out
+// evenly); one sequence of 131072 tokens 41 us, 3.7 TB/s; 32 sequences of up to 4096
+// tokens with four queries 59 us.  A tile of 128 tokens takes a block 1.4 us with
+// eight columns (three blocks an SM) and with sixteen (two: 1024 of the 1400 clocks a
+// tile has are the matrix instructions').
 #include "kv_attention.cuh"
 #include "../../include/nvfp4_kv_cache.h"
 
@@ -32,7 +43,13 @@ namespace nvr {
 
 namespace {
 
-constexpr int kStreamCols = 32;            // more columns of a sequence go to the tensor-memory kernel
+// More columns of a sequence go to the tensor-memory kernel: from there on it is
+// faster although it works on 128 rows whatever their number.  32 sequences of up to
+// 4096 tokens, this kernel / that one, us, by columns: D = 128: 16: 37.9 / 64.1, 24:
+// 63.7 / 68.7, 32: 59.4 / 63.5, 48: 82.2 / 63.7, 64: 113 / 66.4; D = 64: 24: 46.9 /
+// 53.8, 32: 45.3 / 50.8, 48: 60.8 / 49.6.  Four sequences of 600: 32: 13.1 / 16.9, 64:
+// 14.7 / 17.0.
+constexpr int kStreamCols = 32;
 // Starting and ending a key (queries, joining the warps, storing) costs a block
 // about as much as this many tiles: 1.5 us beside 1.4 us for a tile with eight
 // columns, 3.0 beside 1.4 with sixteen (least squares over the blocks of the serving
@@ -142,7 +159,7 @@ kv_attention_kernel(const AttnParams p) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinChunk);
   const int f0 = min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total));
   const int f1 = min(f0 + chunk, total);
   const int excl = before + incl - mine;
@@ -715,7 +732,6 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
   if (grid * Sh::kCols > kAttnMaxCols) grid = kAttnMaxCols / Sh::kCols;
   if (grid > most) grid = most;
-  p.min_chunk = 2;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -734,7 +750,10 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
 
 template <int D>
 nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
-  // sixteen columns at a time where eight do not hold a sequence's queries
+  // Sixteen columns at a time, two blocks an SM, where eight (three blocks) do not hold
+  // a sequence's queries: 16 columns of 32 sequences of up to 4096 tokens 37.9 us, as
+  // twice eight 45.6; 32 columns 59.4 and 78.4.  Eight columns as half of sixteen: the
+  // serving batch 164 us instead of 121, the long sequence 52 instead of 41.
   const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
   if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3>(p, max_kv, s);
   return launch_attn<D, 2, 4, 2, 3, 2>(p, max_kv, s);

@@ -13,6 +13,9 @@ namespace nvr {
 // 2): the softmax weights stay below 2^8, inside fp16.
 constexpr float kRescaleAt = 8.0f;
 
+// Fewest places of a block in the flat order of the tiles.
+constexpr int kMinChunk = 2;
+
 // A key that a chunk border cuts, written by the block of its first chunk: its
 // parts, whether the first lies in its block's second slot, its rows.
 struct KeyJoin {
@@ -47,7 +50,6 @@ struct AttnParams {
   // [2 * blocks][NC m, NC l, NC x D O]: a block's first run is in its slot 0 when it
   // is part of a cut key, its last one in slot 1 unless the key starts the chunk
   float* partials;
-  int min_chunk;              // fewest tiles of a block
 };
 
 // What the queries and the tokens of a column group are.

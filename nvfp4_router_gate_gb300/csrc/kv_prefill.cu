@@ -1,7 +1,7 @@
 // kv_prefill.cu -- softmax attention over the paged NVFP4 key/value cache for
 // many (query, head) columns (sm_103a): prompt chunks, drafts of many tokens.
-// Bound by the tensor cores: 4 D multiply-adds' worth of flops for every column
-// and token against 9/8 D bytes of cache read once for 256 columns.
+// Bound by the tensor cores: 4 D flops for every column and token against 9/8 D
+// bytes of cache read once for 256 columns.
 //
 // Mathematics: as csrc/kv_attention.cu (running maximum moved in steps, fp32
 // sums, fp16 weights).  Here S = Q K^T and O += P V run on tcgen05 with the
@@ -10,26 +10,39 @@
 //
 // A block (one per SM) takes 256 columns of a sequence that share a KV head as
 // two row tiles and walks the tokens in tiles of 128:
-//   warps 0-3, 4-7  softmax of row tile 0 and 1: read S from tensor memory,
-//                   write P (fp16) over it, rescale O when the maximum moves,
-//                   store the rows at the end of a key;
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: scale the queries into fp16, read S
+//                   from tensor memory, write P (fp16) over it, rescale O when the
+//                   maximum moves, store the rows at the end of a key;
 //   warps 8-11      expand the cache: codes and scales from the pages to
 //                   registers one tile ahead, code * scale (exact in fp16) into
 //                   swizzled shared memory, two stages of K and of V;
 //   warp 12         issues the products, alternating the row tiles, so that one
 //                   tile's softmax runs under the other's products;
 //   warp 13         walks the work and hands every role its runs;
-//   warp 14         fetches the pages of the coming tiles into L2.
+//   warp 14         fetches the pages of the coming tiles into L2;
+//   warp 15         copies the query rows of the coming run into shared memory, the
+//                   heads of a query in one bulk copy (a copy a row: each run 4 us longer).
 // A group of at most 128 columns uses both halves as well: the same rows in
 // both, each taking every other token tile, joined at the end.
 //
 // Tensor memory, 512 columns: S0 | S1 (128 each, P over the first half of its
 // S), O0 | O1 (D each).  S of the next tile follows P V of this one in issue
 // order, so S is never overwritten early and a complete S implies the earlier
-// P V complete.
+// P V complete.  P comes in two halves of 64 tokens: P V of the first runs under
+// the softmax of the second.
 //
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
 // equal chunks, one per block, the rows of cut keys joined by csrc/kv_join.cu.
+//
+// Measured (D = 128, 8 KV heads): 2048 queries of 64 heads over 8192 tokens 388 us,
+// 1242 TFLOP/s, 0.65 of the cuBLAS bf16 rate; nine ragged prompts of up to 1500
+// queries of 32 heads over 2500 tokens 112 us.  A tile of 128 tokens and 256 columns takes
+// 1.8 us (3400 clocks; its products 2050): each row tile's softmax 2200 clocks and
+// then 1000 of waiting for its next S, which the full tensor memory leaves no room to
+// make earlier.  A run of a key costs 4.6 us on top (queries in, rows out).  Tried and
+// slower: loops around the issue of the products (510 us for the chunk), unrolled
+// halves of the softmax (450: fetching the instructions), eight warps that expand
+// (450: 96 registers a thread), other splits of the registers (equal).
 #include <type_traits>
 
 #include "kv_attention.cuh"
@@ -41,12 +54,12 @@ namespace {
 constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
 constexpr int kPThreads = 512;
 // Starting and ending a key (queries in, rows out, an empty pipeline) costs about
-// as much as this many tiles (prompts of nine users: 3, 4, 6 tiles 151, 148, 151 us).
-// A tile costs the same whether both halves work on it (two row tiles) or one: the
-// expansion of its keys and values is shared.
+// as much as this many tiles: 7 us beside 1.9 us for a tile of two row tiles and 1.4 for
+// one (least squares over the blocks of the ragged prompts; 3, 4, 5 tiles: 127, 126.5,
+// 130 us for them).
 constexpr int kPKeyCost = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
-constexpr int kLive = 4;
+constexpr int kLive = 4;                   // tiles whose live tokens are kept: expanded at most three ahead
 constexpr int kAhead = 6;                  // tiles fetched into L2 before they are expanded
 constexpr float kMostSum = 256.0f;         // 2^kRescaleAt
 
@@ -209,7 +222,7 @@ kv_prefill_kernel(const AttnParams p) {
     if (w < warp) before += x;
     total += x;
   }
-  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinChunk);
   const int f0 = min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total));
   const int f1 = min(f0 + chunk, total);
   const int excl = before + incl - mine;
@@ -238,20 +251,19 @@ kv_prefill_kernel(const AttnParams p) {
 
   if (tid == 13 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
   if (f0 < f1) {
-      int n_taken = 0;
-      Run run;
-      // the next run, or false (with run.tiles == -1 at the end)
-      auto take = [&]() {
-        const int s = n_taken % kRuns;
-        if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return false;
-        run = s_runs[s];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(run_empty + s);
-        ++n_taken;
-        return true;
-      };
-    if (warp >= 12) {
-      if (warp == 13) {
+    int n_taken = 0;
+    Run run;
+    // the next run, or false (with run.tiles == -1 at the end)
+    auto take = [&]() {
+      const int s = n_taken % kRuns;
+      if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return false;
+      run = s_runs[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(run_empty + s);
+      ++n_taken;
+      return true;
+    };
+    if (warp == 13) {
       // ------------------------------------------------------------ the walk
       int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
       bool ok = true;
@@ -312,656 +324,655 @@ kv_prefill_kernel(const AttnParams p) {
         ok = hand_out(r);
       }
       if (!ok) give_up();
-      } else if (warp == 12) {
-        // -------------------------------------------------------- the products
-        const uint32_t id_s = idesc_f16(128, kPTile, false), id_o = idesc_f16(128, D, true);
-        int tk = 0, tv = 0;                                  // tiles of K and V taken
-        uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
-        auto products = [&]() -> bool {
-          const uint32_t q_low = desc_low(smem + Sm::kQ, 16), k_low = desc_low(smem + Sm::kK, 16);
-          const uint32_t v_low = desc_low(smem + Sm::kV, kPTile * 128);
-          constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
-          auto score = [&](int w, int stage) {
-            const uint32_t q = q_low + w * kTileLow, k = k_low + stage * kTileLow, d = tmem + w * kPTile;
-            if (elect_one()) {
+    } else if (warp == 12) {
+      // -------------------------------------------------------- the products
+      const uint32_t id_s = idesc_f16(128, kPTile, false), id_o = idesc_f16(128, D, true);
+      int tk = 0, tv = 0;                                  // tiles of K and V taken
+      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0};
+      auto products = [&]() -> bool {
+        const uint32_t q_low = desc_low(smem + Sm::kQ, 16), k_low = desc_low(smem + Sm::kK, 16);
+        const uint32_t v_low = desc_low(smem + Sm::kV, kPTile * 128);
+        constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
+        auto score = [&](int w, int stage) {
+          const uint32_t q = q_low + w * kTileLow, k = k_low + stage * kTileLow, d = tmem + w * kPTile;
+          if (elect_one()) {
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint32_t o = ((i / 4) * (kPTile * 128) + (i % 4) * 32) >> 4;
-                tc_mma_f16(d, q + o, k + o, id_s, i != 0);
-              }
-            }
-            __syncwarp();
-          };
-          auto weigh = [&](int w, int stage, bool add, int half) {
-            const uint32_t v = v_low + stage * kTileLow, d = tmem + 2 * kPTile + w * D, a = tmem + w * kPTile;
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < kPTile / 32; ++k) {
-                // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-                const int i = half * (kPTile / 32) + k;
-                tc_mma_f16_ta(d, a + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
-              }
-            }
-            __syncwarp();
-          };
-          auto commit = [&](uint64_t* bar) {
-            if (elect_one()) tc_commit(bar);
-            __syncwarp();
-          };
-          auto have = [&](uint64_t* bar, uint32_t parity) {
-            const bool ok = wait_all(bar, parity);
-            tc_fence_after();
-            return ok;
-          };
-          for (;;) {
-            if (!take()) return false;
-            const int n = run.tiles;
-            if (n < 0) return true;
-            const int k0 = tk, v0 = tv;
-            tk += n;
-            tv += n;
-            auto k_ready = [&](int j) { return have(k_full + (k0 + j) % 2, ((k0 + j) / 2) & 1); };
-            auto v_ready = [&](int j) { return have(v_full + (v0 + j) % 2, ((v0 + j) / 2) & 1); };
-            auto q_ready = [&](int w) { const bool ok = have(q_full + w, ph_q[w]); ph_q[w] ^= 1u; return ok; };
-            auto p_ready = [&](int w, int half) { return have((half ? p_full : p_half) + w, ph_p[w]); };
-            // Row tile w: O += P V of its tile `cur`, then S of its tile `nxt`; both row
-            // tiles walk all tiles (dual) or every other.  K and V of a tile wait for
-            // its first reader and are free after its last.
-            auto step = [&](bool dual, int w, int cur, int nxt) -> bool {
-              const bool first = !dual || w == 0, last = !dual || w == 1;
-              if (cur >= 0) {
-                if ((first && !v_ready(cur)) || !p_ready(w, 0)) return false;
-                weigh(w, (v0 + cur) % 2, cur > (dual ? 0 : 1), 0);
-                commit(h_full + w);
-                if (!p_ready(w, 1)) return false;
-                ph_p[w] ^= 1u;
-                weigh(w, (v0 + cur) % 2, true, 1);
-                if (last) commit(v_empty + (v0 + cur) % 2);
-              }
-              if (nxt < n) {
-                if (nxt < (dual ? 1 : 2) && !q_ready(w)) return false;
-                if (first && !k_ready(nxt)) return false;
-                score(w, (k0 + nxt) % 2);
-                commit(s_full + w);
-                if (nxt + (dual ? 1 : 2) >= n) commit(q_empty + w);
-                if (last) commit(k_empty + (k0 + nxt) % 2);
-              } else if (cur >= 0) {
-                commit(o_full + w);
-              }
-              return true;
-            };
-            if (run.dual) {
-#pragma unroll 1
-              for (int j = -1; j < n; ++j)
-                if (!step(true, 0, j, j + 1) || !step(true, 1, j, j + 1)) return false;
-            } else {
-#pragma unroll 1
-              for (int j = -2; j < n; ++j)
-                if (!step(false, j & 1, j, j + 2)) return false;
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t o = ((i / 4) * (kPTile * 128) + (i % 4) * 32) >> 4;
+              tc_mma_f16(d, q + o, k + o, id_s, i != 0);
             }
           }
-        };
-        if (!products()) give_up();
-        // nothing of this block's is under way when the tensor memory goes back
-        if (elect_one()) tc_commit(drained);
-        __syncwarp();
-        wait_all(drained, 0);
-      } else if (warp == 14) {
-        // ------------------------------- the pages of the coming tiles into L2
-        // (the expanding warps read one tile ahead, less than a trip to memory)
-        const int S = 1 << p.page_shift, pieces = kPTile / S;
-        int n_tile = 0;
-        bool ok = true;
-        while (ok) {
-          ok = take() && run.tiles >= 0;
-          const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
-          for (int j = 0; ok && j < run.tiles; ++j, ++n_tile) {
-            const uint64_t limit = globaltimer_ns() + 1000000000ull;
-            while (n_tile > *s_done + kAhead && !*abort_flag && globaltimer_ns() < limit) __nanosleep(100);
-            const int t = (run.tile0 + j) * kPTile + lane * S;
-            if (lane < pieces && t < run.hi && t + S > run.lo) {
-              const int page = __ldg(table + (t >> p.page_shift));
-              if (page >= 0 && page < p.n_pages)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
-                             :: "l"(p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S)),
-                                "r"(KvPage<D>::bytes(S)) : "memory");
-            }
-            __syncwarp();
-          }
-        }
-      } else {
-        // -------------- the query rows of the coming run, raw into the halves' tiles
-        const float inv_G = 1.0f / static_cast<float>(p.G);
-        uint32_t sent[2] = {0, 0};
-        auto queries = [&]() -> bool {
-          for (;;) {
-            if (!take()) return false;
-            if (run.tiles < 0) return true;
-            for (int w = 0; w < 2; ++w) {
-              if (!run.dual && run.tiles <= w) continue;
-              if (!wait_all(q_empty + w, (sent[w] & 1) ^ 1)) return false;
-              ++sent[w];
-              uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
-              // the columns [from, to) are in the tile; a query's lie next to each other
-              const int c0 = w ? run.col0 : 0, from = max(c0, 0), to = min(c0 + kPTile, run.n_cols);
-              if (lane == 0) mbar_arrive_expect_tx(q_raw + w, (to - from) * D * 2);
-              __syncwarp();
-              for (int dq = div_small(run.rem0 + from, inv_G) + lane; dq * p.G - run.rem0 < to; dq += 32) {
-                const int a = max(from, dq * p.G - run.rem0), b = min(to, (dq + 1) * p.G - run.rem0);
-                bulk_load(tile + (a - c0) * D * 2,
-                          p.q + (run.q0 + run.iq0 + dq) * p.q_stride +
-                              static_cast<int64_t>(run.head * p.G + run.rem0 + a - dq * p.G) * D,
-                          (b - a) * D * 2, q_raw + w);
-              }
-              __syncwarp();
-            }
-          }
-        };
-        if (!queries()) give_up();
-        if (*abort_flag) {
-          // copies in flight land before the block's memory goes away
-          const uint64_t drain = globaltimer_ns() + 1000000000ull;
-          for (int w = 0; w < 2; ++w)
-            while (sent[w] && !mbar_try_wait(q_raw + w, (sent[w] - 1) & 1))
-              if (globaltimer_ns() > drain) break;
-        }
-      }
-    } else if (warp >= 8) {
-        // ---------------------------------------------------- expanding the cache
-        const int w = warp - 8, tok = lane & 7, qd = lane >> 3;
-        const int S = 1 << p.page_shift;
-        int n_tile = 0;                                      // tiles expanded
-        constexpr int BL = D / 64;                           // blocks of 16 channels a lane takes of a token
-        // Where this lane's codes and scales lie in the page of its warp's first 16
-        // tokens, and how much further the other 16 are when they share the page
-        // (pages of 32 tokens or more): the same in every tile, a tile holds whole
-        // pages or lies in one
-        const int o0 = ((32 * w) & (S - 1)) + tok;
-        const uint32_t k_code = o0 * (D / 2) + qd * 8 * BL, k_scale = KvPage<D>::key_scales(S) + o0 * (D / 16) + qd * BL;
-        const uint32_t v_code = KvPage<D>::value_codes(S) + KvPage<D>::value_code(o0, qd * BL);
-        const uint32_t v_scale = KvPage<D>::value_scales(S) + KvPage<D>::value_scale(o0, qd * BL);
-        const bool one_page = S >= 32;
-        const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * KvPage<D>::bytes(S);
-        auto expand = [&]() -> bool {
-          for (;;) {
-            if (!take()) return false;
-            if (run.tiles < 0) return true;
-            const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
-            uint2 kc[4][BL], vc[4][BL];
-            uint32_t ks[4], vs[4][BL], k_mask[4], v_mask[4];
-            // A half without its page reads the first page of the cache, under scales
-            // of zero; so do tokens past the sequence's length (whatever their bytes).
-            const uint8_t* head_at = p.cache + static_cast<int64_t>(run.head) * KvPage<D>::bytes(S);
-            const uint8_t* base[2];                          // this head in the pages of the warp's two halves
-            int limit[2];                                    // the tokens of a half below this have scales
-            int at = -1, entries = -1;
-            // the pages of a tile; which are in the cache
-            auto find = [&](int tile) {
-              const int x = (tile * kPTile) >> p.page_shift; // the tile's first page
-              if ((x & ~31) != at) {
-                at = x & ~31;
-                entries = at + lane < p.max_pages ? __ldg(table + at + lane) : -1;
-              }
-              const int t = tile * kPTile + 32 * w, e = (t >> p.page_shift) - at;
-              int page = __shfl_sync(0xFFFFFFFFu, entries, e);
-              bool ok = page >= 0 && page < p.n_pages;
-              uint32_t live = ok ? 3u : 0u;
-              ok = ok && t < run.hi && t + 32 > run.lo;
-              base[0] = base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
-              limit[0] = limit[1] = ok ? run.kv : 0;
-              if (!one_page) {                               // pages of 16: the second half's is the next
-                page = __shfl_sync(0xFFFFFFFFu, entries, e + 1);
-                ok = page >= 0 && page < p.n_pages;
-                live = (live & 1u) | (ok ? 2u : 0u);
-                ok = ok && t + 16 < run.hi && t + 32 > run.lo;
-                base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
-                limit[1] = ok ? run.kv : 0;
-              }
-              return live;
-            };
-            const int step_c = one_page ? 16 * (D / 2) : 0, step_s = one_page ? 16 * (D / 16) : 0;
-            auto load_k = [&](int tile) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint8_t* c = base[h] + (k_code + h * step_c);
-                const uint8_t* s = base[h] + (k_scale + h * step_s);
-                const int t = tile * kPTile + 32 * w + 16 * h + tok;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (BL == 2) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(c + i * 8 * (D / 2)));
-                    kc[2 * h + i][0] = make_uint2(u.x, u.y);
-                    kc[2 * h + i][BL - 1] = make_uint2(u.z, u.w);
-                    ks[2 * h + i] = __ldg(reinterpret_cast<const uint16_t*>(s + i * 8 * (D / 16)));
-                  } else {
-                    kc[2 * h + i][0] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2)));
-                    ks[2 * h + i] = __ldg(s + i * 8 * (D / 16));
-                  }
-                  k_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
-                }
-              }
-            };
-            auto load_v = [&](int tile) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint8_t* c = base[h] + (v_code + h * step_c);
-                const uint8_t* s = base[h] + (v_scale + h * step_s);
-                const int t = tile * kPTile + 32 * w + 16 * h + tok;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                  for (int x = 0; x < BL; ++x) {
-                    vc[2 * h + i][x] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2) + 64 * x));
-                    vs[2 * h + i][x] = __ldg(s + i * 8 * (D / 16) + 8 * x);
-                  }
-                  v_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
-                }
-              }
-            };
-            // one group of eight tokens: codes times scales into the swizzled tile
-            auto put = [&](uint8_t* tile, int i, const uint2 (&c)[BL], uint32_t two) {
-              const uint32_t s2 = e4m3x2_to_f16(two);
-              uint8_t* row = tile + (32 * w + 8 * i + tok) * 128;
-#pragma unroll
-              for (int x = 0; x < BL; ++x) {
-                const uint32_t sb = __byte_perm(s2, 0, x == 0 ? 0x1010 : 0x3232);
-                uint32_t a[8];
-                e2m1x8_to_f16(c[x].x, a[0], a[1], a[2], a[3]);
-                e2m1x8_to_f16(c[x].y, a[4], a[5], a[6], a[7]);
-#pragma unroll
-                for (int y = 0; y < 8; ++y) a[y] = h2_mul(a[y], sb);
-                const int blk = qd * BL + x;                 // channels 16 blk ..
-                uint8_t* atom = row + (blk / 4) * (kPTile * 128);
-                const int ch = 2 * (blk % 4);
-                *reinterpret_cast<uint4*>(atom + ((ch ^ tok) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4*>(atom + (((ch + 1) ^ tok) << 4)) = make_uint4(a[4], a[5], a[6], a[7]);
-              }
-            };
-            uint32_t live = find(run.tile0);
-            load_k(run.tile0);
-            load_v(run.tile0);
-            for (int j = 0; j < run.tiles; ++j, ++n_tile) {
-              const int st = n_tile % 2;
-              const uint32_t ph = ((n_tile / 2) & 1) ^ 1;
-              if (!wait_all(k_empty + st, ph)) return false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) put(smem + Sm::kK + st * Sm::kTileBytes, i, kc[i], ks[i] & k_mask[i]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              // this warp's byte of the word: its two groups of 16 tokens
-              if (lane == 0) {
-                reinterpret_cast<volatile uint8_t*>(s_live + n_tile % kLive)[w] = static_cast<uint8_t>(live);
-                mbar_arrive(k_full + st);
-              }
-              const int more = run.tile0 + j + 1;
-              uint32_t live_next = 0;
-              if (j + 1 < run.tiles) {
-                live_next = find(more);
-                load_k(more);
-              }
-              if (!wait_all(v_empty + st, ph)) return false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                put(smem + Sm::kV + st * Sm::kTileBytes, i, vc[i], (vs[i][0] | (vs[i][BL - 1] << 8)) & v_mask[i]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(v_full + st);
-              if (w == 0 && lane == 0) *s_done = n_tile + 1;
-              if (j + 1 < run.tiles) load_v(more);
-              live = live_next;
-            }
-          }
-        };
-        if (!expand()) give_up();
-    } else {
-        // ------------------------------------------------------------- softmax
-        const int w = warp >> 2, wl = warp & 3, row = tid & 127;
-        const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
-        const uint32_t t_s = tmem + lanes + w * kPTile, t_o = tmem + lanes + 2 * kPTile + w * D;
-        const float inv_G = 1.0f / static_cast<float>(p.G);
-        uint32_t ph_h = 0, ph_q = 0, ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
-        int n_tile = 0;                                      // tiles before the run
-        auto sync_half = [&]() {
           __syncwarp();
-          if (lane == 0) mbar_arrive(meet + w);
-          const bool ok = wait_all(meet + w, ph_meet);
-          ph_meet ^= 1u;
+        };
+        auto weigh = [&](int w, int stage, bool add, int half) {
+          const uint32_t v = v_low + stage * kTileLow, d = tmem + 2 * kPTile + w * D, a = tmem + w * kPTile;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kPTile / 32; ++k) {
+              // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
+              const int i = half * (kPTile / 32) + k;
+              tc_mma_f16_ta(d, a + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
+            }
+          }
+          __syncwarp();
+        };
+        auto commit = [&](uint64_t* bar) {
+          if (elect_one()) tc_commit(bar);
+          __syncwarp();
+        };
+        auto have = [&](uint64_t* bar, uint32_t parity) {
+          const bool ok = wait_all(bar, parity);
+          tc_fence_after();
           return ok;
         };
-        // A run stays in shared memory meanwhile: its fields are read where they are needed.
-        auto my_tiles = [&](const volatile Run& run) { return run.dual ? run.tiles : (run.tiles + 1 - w) / 2; };
-        auto col_of = [&](const volatile Run& run) { return w == 0 ? row : row + run.col0; };
-        auto is_on = [&](const volatile Run& run) {
-          return static_cast<uint32_t>(col_of(run)) < static_cast<uint32_t>(run.n_cols);
-        };
-        // the query of the row, and its row of the result
-        auto quotient = [&](const volatile Run& run) {
-          return div_small(run.rem0 + (is_on(run) ? col_of(run) : 0), inv_G);
-        };
-        auto out_row = [&](const volatile Run& run) {
-          const int dq = quotient(run);
-          return static_cast<int64_t>(run.q0 + run.iq0 + dq) * p.Hq + run.head * p.G + run.rem0 +
-                 (is_on(run) ? col_of(run) : 0) - dq * p.G;
-        };
-        float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
-        // ---- a run's queries: the raw row of each thread, scaled into fp16's range,
-        // into the swizzled tile.  Vector f(i) of a row is its thread's i-th: with f(i)
-        // = i xor (x times the row) in GF(8), both f and f xor the row (the swizzle)
-        // take all values over eight rows: neither side has bank conflicts.
-        auto start = [&](const volatile Run& run) -> bool {
-          if (my_tiles(run) == 0) return true;
-          uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
-          if (!wait_all(q_raw + w, ph_q)) return false;
-          ph_q ^= 1u;
-          const bool on = is_on(run);
-          const int turn = ((row << 1) ^ (row & 4 ? 3 : 0)) & 7;
-          uint4 u[D / 8];
-          uint32_t big2 = 0;                                 // the largest magnitudes of the even and odd channels
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            u[i] = on ? *reinterpret_cast<const uint4*>(tile + row * D * 2 + ((i & 8) | ((i ^ turn) & 7)) * 16)
-                      : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              asm("max.u16x2 %0, %0, %1;" : "+r"(big2) : "r"(v[k] & 0x7FFF7FFFu));
-          }
-          if (!sync_half()) return false;
-          float up, down;
-          query_scale(max(big2 & 0xFFFFu, big2 >> 16), up, down);
-          to_log2 = down * (p.scale_log2 * run.k_gsa);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
-            *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + row * 128 + (((i ^ turn ^ row) & 7) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(q_full + w);
-            if (run.dual) mbar_arrive(q_empty + w);          // (this half has nothing more to do with the tile)
-          }
-          return true;
-        };
-        // ---- its tiles
-        auto weigh = [&](const volatile Run& run) -> bool {
-          const int n_my = my_tiles(run);
-          const bool on = is_on(run), any_on = __any_sync(0xFFFFFFFFu, on);
-          const int pos = run.kv - run.n_q + run.iq0 + quotient(run);
-          const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
-          const int lo = p.window > 0 ? pos + 1 - p.window : 0;
-          m_neg = INFINITY;
-          l = 0.0f;
-          for (int i = 0; i < n_my; ++i) {
-            const int j = run.dual ? i : 2 * i + w;
-            const int t0 = (run.tile0 + j) * kPTile;
-            if (!wait_all(s_full + w, ph_s)) return false;
-            ph_s ^= 1u;
-            tc_fence_after();
-            if (!any_on) {
-              // (rows that nobody asked for: their P may be anything)
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(p_half + w);
-                mbar_arrive(p_full + w);
-              }
-              ph_h ^= 1u;
-              continue;
+        for (;;) {
+          if (!take()) return false;
+          const int n = run.tiles;
+          if (n < 0) return true;
+          const int k0 = tk, v0 = tv;
+          tk += n;
+          tv += n;
+          auto k_ready = [&](int j) { return have(k_full + (k0 + j) % 2, ((k0 + j) / 2) & 1); };
+          auto v_ready = [&](int j) { return have(v_full + (v0 + j) % 2, ((v0 + j) / 2) & 1); };
+          auto q_ready = [&](int w) { const bool ok = have(q_full + w, ph_q[w]); ph_q[w] ^= 1u; return ok; };
+          auto p_ready = [&](int w, int half) { return have((half ? p_full : p_half) + w, ph_p[w]); };
+          // Row tile w: O += P V of its tile `cur`, then S of its tile `nxt`; both row
+          // tiles walk all tiles (dual) or every other.  K and V of a tile wait for
+          // its first reader and are free after its last.
+          auto step = [&](bool dual, int w, int cur, int nxt) -> bool {
+            const bool first = !dual || w == 0, last = !dual || w == 1;
+            if (cur >= 0) {
+              if ((first && !v_ready(cur)) || !p_ready(w, 0)) return false;
+              weigh(w, (v0 + cur) % 2, cur > (dual ? 0 : 1), 0);
+              commit(h_full + w);
+              if (!p_ready(w, 1)) return false;
+              ph_p[w] ^= 1u;
+              weigh(w, (v0 + cur) % 2, true, 1);
+              if (last) commit(v_empty + (v0 + cur) % 2);
             }
-            const uint32_t bytes = s_live[(n_tile + j) % kLive];
-            // bit i: tokens 16 i .. of the tile are in the cache
-            const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
-            const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
-            // bit x: the row sees token t0 + c + x (c a multiple of 32)
-            const int from = lo - t0, to = hi - t0;
-            auto seen32 = [&](int c) {
-              const int a = min(max(from - c, 0), 32), b = min(max(to - c, 0), 32);
-              const uint32_t m = (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
-              const uint32_t two = live >> (c / 16);
-              return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
-            };
-            // In two halves of 64 tokens: P V of the first starts under the second.
+            if (nxt < n) {
+              if (nxt < (dual ? 1 : 2) && !q_ready(w)) return false;
+              if (first && !k_ready(nxt)) return false;
+              score(w, (k0 + nxt) % 2);
+              commit(s_full + w);
+              if (nxt + (dual ? 1 : 2) >= n) commit(q_empty + w);
+              if (last) commit(k_empty + (k0 + nxt) % 2);
+            } else if (cur >= 0) {
+              commit(o_full + w);
+            }
+            return true;
+          };
+          if (run.dual) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < kPTile; c0 += kPTile / 2) {
-              uint32_t pr[kPTile / 4];
-              float sum;
-              auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
-                uint64_t sum2 = f2_pack(0.0f, 0.0f);
-                const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
-                uint32_t s[2][32];
-                tmem_load32_start(t_s + c0, s[0]);
+            for (int j = -1; j < n; ++j)
+              if (!step(true, 0, j, j + 1) || !step(true, 1, j, j + 1)) return false;
+          } else {
+#pragma unroll 1
+            for (int j = -2; j < n; ++j)
+              if (!step(false, j & 1, j, j + 2)) return false;
+          }
+        }
+      };
+      if (!products()) give_up();
+      // nothing of this block's is under way when the tensor memory goes back
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      wait_all(drained, 0);
+    } else if (warp == 14) {
+      // ------------------------------- the pages of the coming tiles into L2
+      // (the expanding warps read one tile ahead, less than a trip to memory)
+      const int S = 1 << p.page_shift, pieces = kPTile / S;
+      int n_tile = 0;
+      bool ok = true;
+      while (ok) {
+        ok = take() && run.tiles >= 0;
+        const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
+        for (int j = 0; ok && j < run.tiles; ++j, ++n_tile) {
+          const uint64_t limit = globaltimer_ns() + 1000000000ull;
+          while (n_tile > *s_done + kAhead && !*abort_flag && globaltimer_ns() < limit) __nanosleep(100);
+          const int t = (run.tile0 + j) * kPTile + lane * S;
+          if (lane < pieces && t < run.hi && t + S > run.lo) {
+            const int page = __ldg(table + (t >> p.page_shift));
+            if (page >= 0 && page < p.n_pages)
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                           :: "l"(p.cache + (static_cast<int64_t>(page) * p.Hkv + run.head) * KvPage<D>::bytes(S)),
+                              "r"(KvPage<D>::bytes(S)) : "memory");
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == 15) {
+      // -------------- the query rows of the coming run, raw into the halves' tiles
+      const float inv_G = 1.0f / static_cast<float>(p.G);
+      uint32_t sent[2] = {0, 0};
+      auto queries = [&]() -> bool {
+        for (;;) {
+          if (!take()) return false;
+          if (run.tiles < 0) return true;
+          for (int w = 0; w < 2; ++w) {
+            if (!run.dual && run.tiles <= w) continue;
+            if (!wait_all(q_empty + w, (sent[w] & 1) ^ 1)) return false;
+            ++sent[w];
+            uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
+            // the columns [from, to) are in the tile; a query's lie next to each other
+            const int c0 = w ? run.col0 : 0, from = max(c0, 0), to = min(c0 + kPTile, run.n_cols);
+            if (lane == 0) mbar_arrive_expect_tx(q_raw + w, (to - from) * D * 2);
+            __syncwarp();
+            for (int dq = div_small(run.rem0 + from, inv_G) + lane; dq * p.G - run.rem0 < to; dq += 32) {
+              const int a = max(from, dq * p.G - run.rem0), b = min(to, (dq + 1) * p.G - run.rem0);
+              bulk_load(tile + (a - c0) * D * 2,
+                        p.q + (run.q0 + run.iq0 + dq) * p.q_stride +
+                            static_cast<int64_t>(run.head * p.G + run.rem0 + a - dq * p.G) * D,
+                        (b - a) * D * 2, q_raw + w);
+            }
+            __syncwarp();
+          }
+        }
+      };
+      if (!queries()) give_up();
+      if (*abort_flag) {
+        // copies in flight land before the block's memory goes away
+        const uint64_t drain = globaltimer_ns() + 1000000000ull;
+        for (int w = 0; w < 2; ++w)
+          while (sent[w] && !mbar_try_wait(q_raw + w, (sent[w] - 1) & 1))
+            if (globaltimer_ns() > drain) break;
+      }
+    } else if (warp >= 8) {
+      // ---------------------------------------------------- expanding the cache
+      const int w = warp - 8, tok = lane & 7, qd = lane >> 3;
+      const int S = 1 << p.page_shift;
+      int n_tile = 0;                                      // tiles expanded
+      constexpr int BL = D / 64;                           // blocks of 16 channels a lane takes of a token
+      // Where this lane's codes and scales lie in the page of its warp's first 16
+      // tokens, and how much further the other 16 are when they share the page
+      // (pages of 32 tokens or more): the same in every tile, a tile holds whole
+      // pages or lies in one
+      const int o0 = ((32 * w) & (S - 1)) + tok;
+      const uint32_t k_code = o0 * (D / 2) + qd * 8 * BL, k_scale = KvPage<D>::key_scales(S) + o0 * (D / 16) + qd * BL;
+      const uint32_t v_code = KvPage<D>::value_codes(S) + KvPage<D>::value_code(o0, qd * BL);
+      const uint32_t v_scale = KvPage<D>::value_scales(S) + KvPage<D>::value_scale(o0, qd * BL);
+      const bool one_page = S >= 32;
+      const uint32_t page_stride = static_cast<uint32_t>(p.Hkv) * KvPage<D>::bytes(S);
+      auto expand = [&]() -> bool {
+        for (;;) {
+          if (!take()) return false;
+          if (run.tiles < 0) return true;
+          const int32_t* table = p.page_table + static_cast<int64_t>(run.b) * p.max_pages;
+          uint2 kc[4][BL], vc[4][BL];
+          uint32_t ks[4], vs[4][BL], k_mask[4], v_mask[4];
+          // A half without its page reads the first page of the cache, under scales
+          // of zero; so do tokens past the sequence's length (whatever their bytes).
+          const uint8_t* head_at = p.cache + static_cast<int64_t>(run.head) * KvPage<D>::bytes(S);
+          const uint8_t* base[2];                          // this head in the pages of the warp's two halves
+          int limit[2];                                    // the tokens of a half below this have scales
+          int at = -1, entries = -1;
+          // the pages of a tile; which are in the cache
+          auto find = [&](int tile) {
+            const int x = (tile * kPTile) >> p.page_shift; // the tile's first page
+            if ((x & ~31) != at) {
+              at = x & ~31;
+              entries = at + lane < p.max_pages ? __ldg(table + at + lane) : -1;
+            }
+            const int t = tile * kPTile + 32 * w, e = (t >> p.page_shift) - at;
+            int page = __shfl_sync(0xFFFFFFFFu, entries, e);
+            bool ok = page >= 0 && page < p.n_pages;
+            uint32_t live = ok ? 3u : 0u;
+            ok = ok && t < run.hi && t + 32 > run.lo;
+            base[0] = base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
+            limit[0] = limit[1] = ok ? run.kv : 0;
+            if (!one_page) {                               // pages of 16: the second half's is the next
+              page = __shfl_sync(0xFFFFFFFFu, entries, e + 1);
+              ok = page >= 0 && page < p.n_pages;
+              live = (live & 1u) | (ok ? 2u : 0u);
+              ok = ok && t + 16 < run.hi && t + 32 > run.lo;
+              base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
+              limit[1] = ok ? run.kv : 0;
+            }
+            return live;
+          };
+          const int step_c = one_page ? 16 * (D / 2) : 0, step_s = one_page ? 16 * (D / 16) : 0;
+          auto load_k = [&](int tile) {
 #pragma unroll
-                for (int c = 0; c < kPTile / 2; c += 32) {
-                  uint32_t (&now)[32] = s[(c / 32) % 2];
-                  tmem_load32_finish(now);
-                  if (c + 32 < kPTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
-                  const uint32_t see = hidden ? seen32(c0 + c) : 0xFFFFFFFFu;
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* c = base[h] + (k_code + h * step_c);
+              const uint8_t* s = base[h] + (k_scale + h * step_s);
+              const int t = tile * kPTile + 32 * w + 16 * h + tok;
 #pragma unroll
-                  for (int x = 0; x < 32; x += 2) {
-                    const uint64_t v =
-                        f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
-                    float v0 = f2_lo(v), v1 = f2_hi(v);
-                    if (hidden) {
-                      v0 = see & (1u << x) ? v0 : -INFINITY;
-                      v1 = see & (2u << x) ? v1 : -INFINITY;
-                    }
-                    const float a = ex2(v0), b = ex2(v1);
-                    sum2 = f2_add(sum2, f2_pack(a, b));
-                    pr[(c + x) / 2] = pack_f16(a, b);
-                  }
+              for (int i = 0; i < 2; ++i) {
+                if (BL == 2) {
+                  const uint4 u = __ldg(reinterpret_cast<const uint4*>(c + i * 8 * (D / 2)));
+                  kc[2 * h + i][0] = make_uint2(u.x, u.y);
+                  kc[2 * h + i][BL - 1] = make_uint2(u.z, u.w);
+                  ks[2 * h + i] = __ldg(reinterpret_cast<const uint16_t*>(s + i * 8 * (D / 16)));
+                } else {
+                  kc[2 * h + i][0] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2)));
+                  ks[2 * h + i] = __ldg(s + i * 8 * (D / 16));
                 }
-                sum = f2_lo(sum2) + f2_hi(sum2);
-              };
-              // Weights that add up to more than 2^kRescaleAt hold a score far above m
-              // (a weight above 4, at least): no maximum is taken of the others.  (m at
-              // or above every score: at most 64 weights of 1.)
-              for (bool move = i == 0 && c0 == 0;; move = true) {
-                if (move) {
-                  // m moves to the largest score so far, this half's included
-                  float top = -INFINITY;
-#pragma unroll 1
-                  for (int c = c0; c < c0 + kPTile / 2; c += 32) {
-                    uint32_t s[32];
-                    tmem_load32_start(t_s + c, s);
-                    tmem_load32_finish(s);
-                    const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
+                k_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
+              }
+            }
+          };
+          auto load_v = [&](int tile) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                      top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
-                  }
-                  const float now = fminf(m_neg, -top);
-                  const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-                  m_neg = now;
-                  l *= shrink;
-                  if (i > 0 || c0 > 0) {
-                    // (earlier tiles are in O, S came after them; the first half may be on its way)
-                    if (c0 > 0) {
-                      if (!wait_all(h_full + w, ph_h)) return false;
-                      tc_fence_after();
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                      float o[16];
-                      uint32_t y[16];
-                      tmem_load16(t_o + c, o);
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* c = base[h] + (v_code + h * step_c);
+              const uint8_t* s = base[h] + (v_scale + h * step_s);
+              const int t = tile * kPTile + 32 * w + 16 * h + tok;
 #pragma unroll
-                      for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
-                      tmem_store16(t_o + c, y);
-                    }
-                  }
+              for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int x = 0; x < BL; ++x) {
+                  vc[2 * h + i][x] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2) + 64 * x));
+                  vs[2 * h + i][x] = __ldg(s + i * 8 * (D / 16) + 8 * x);
                 }
-                if (masked) weights(std::true_type{});
-                else weights(std::false_type{});
-                if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
+                v_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
               }
-              l += sum;
-              // P over the columns of S that have been read
+            }
+          };
+          // one group of eight tokens: codes times scales into the swizzled tile
+          auto put = [&](uint8_t* tile, int i, const uint2 (&c)[BL], uint32_t two) {
+            const uint32_t s2 = e4m3x2_to_f16(two);
+            uint8_t* row = tile + (32 * w + 8 * i + tok) * 128;
 #pragma unroll
-              for (int c = 0; c < kPTile / 4; c += 16) {
-                uint32_t x[16];
+            for (int x = 0; x < BL; ++x) {
+              const uint32_t sb = __byte_perm(s2, 0, x == 0 ? 0x1010 : 0x3232);
+              uint32_t a[8];
+              e2m1x8_to_f16(c[x].x, a[0], a[1], a[2], a[3]);
+              e2m1x8_to_f16(c[x].y, a[4], a[5], a[6], a[7]);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-                tmem_store16(t_s + c0 / 2 + c, x);
-              }
-              tmem_store_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive((c0 ? p_full : p_half) + w);
+              for (int y = 0; y < 8; ++y) a[y] = h2_mul(a[y], sb);
+              const int blk = qd * BL + x;                 // channels 16 blk ..
+              uint8_t* atom = row + (blk / 4) * (kPTile * 128);
+              const int ch = 2 * (blk % 4);
+              *reinterpret_cast<uint4*>(atom + ((ch ^ tok) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+              *reinterpret_cast<uint4*>(atom + (((ch + 1) ^ tok) << 4)) = make_uint4(a[4], a[5], a[6], a[7]);
+            }
+          };
+          uint32_t live = find(run.tile0);
+          load_k(run.tile0);
+          load_v(run.tile0);
+          for (int j = 0; j < run.tiles; ++j, ++n_tile) {
+            const int st = n_tile % 2;
+            const uint32_t ph = ((n_tile / 2) & 1) ^ 1;
+            if (!wait_all(k_empty + st, ph)) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(smem + Sm::kK + st * Sm::kTileBytes, i, kc[i], ks[i] & k_mask[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            // this warp's byte of the word: its two groups of 16 tokens
+            if (lane == 0) {
+              reinterpret_cast<volatile uint8_t*>(s_live + n_tile % kLive)[w] = static_cast<uint8_t>(live);
+              mbar_arrive(k_full + st);
+            }
+            const int more = run.tile0 + j + 1;
+            uint32_t live_next = 0;
+            if (j + 1 < run.tiles) {
+              live_next = find(more);
+              load_k(more);
+            }
+            if (!wait_all(v_empty + st, ph)) return false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              put(smem + Sm::kV + st * Sm::kTileBytes, i, vc[i], (vs[i][0] | (vs[i][BL - 1] << 8)) & v_mask[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full + st);
+            if (w == 0 && lane == 0) *s_done = n_tile + 1;
+            if (j + 1 < run.tiles) load_v(more);
+            live = live_next;
+          }
+        }
+      };
+      if (!expand()) give_up();
+    } else {
+      // ------------------------------------------------------------- softmax
+      const int w = warp >> 2, wl = warp & 3, row = tid & 127;
+      const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+      const uint32_t t_s = tmem + lanes + w * kPTile, t_o = tmem + lanes + 2 * kPTile + w * D;
+      const float inv_G = 1.0f / static_cast<float>(p.G);
+      uint32_t ph_h = 0, ph_q = 0, ph_s = 0, ph_o = 0, ph_meet = 0, ph_x = 0;
+      int n_tile = 0;                                      // tiles before the run
+      auto sync_half = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(meet + w);
+        const bool ok = wait_all(meet + w, ph_meet);
+        ph_meet ^= 1u;
+        return ok;
+      };
+      // A run stays in shared memory meanwhile: its fields are read where they are needed.
+      auto my_tiles = [&](const volatile Run& run) { return run.dual ? run.tiles : (run.tiles + 1 - w) / 2; };
+      auto col_of = [&](const volatile Run& run) { return w == 0 ? row : row + run.col0; };
+      auto is_on = [&](const volatile Run& run) {
+        return static_cast<uint32_t>(col_of(run)) < static_cast<uint32_t>(run.n_cols);
+      };
+      // the query of the row, and its row of the result
+      auto quotient = [&](const volatile Run& run) {
+        return div_small(run.rem0 + (is_on(run) ? col_of(run) : 0), inv_G);
+      };
+      auto out_row = [&](const volatile Run& run) {
+        const int dq = quotient(run);
+        return static_cast<int64_t>(run.q0 + run.iq0 + dq) * p.Hq + run.head * p.G + run.rem0 +
+               (is_on(run) ? col_of(run) : 0) - dq * p.G;
+      };
+      float to_log2 = 0.0f, m_neg = INFINITY, l = 0.0f;
+      // ---- a run's queries: the raw row of each thread, scaled into fp16's range,
+      // into the swizzled tile.  Vector f(i) of a row is its thread's i-th: with f(i)
+      // = i xor (x times the row) in GF(8), both f and f xor the row (the swizzle)
+      // take all values over eight rows: neither side has bank conflicts.
+      auto start = [&](const volatile Run& run) -> bool {
+        if (my_tiles(run) == 0) return true;
+        uint8_t* tile = smem + Sm::kQ + w * Sm::kTileBytes;
+        if (!wait_all(q_raw + w, ph_q)) return false;
+        ph_q ^= 1u;
+        const bool on = is_on(run);
+        const int turn = ((row << 1) ^ (row & 4 ? 3 : 0)) & 7;
+        uint4 u[D / 8];
+        uint32_t big2 = 0;                                 // the largest magnitudes of the even and odd channels
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          u[i] = on ? *reinterpret_cast<const uint4*>(tile + row * D * 2 + ((i & 8) | ((i ^ turn) & 7)) * 16)
+                    : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            asm("max.u16x2 %0, %0, %1;" : "+r"(big2) : "r"(v[k] & 0x7FFF7FFFu));
+        }
+        if (!sync_half()) return false;
+        float up, down;
+        query_scale(max(big2 & 0xFFFFu, big2 >> 16), up, down);
+        to_log2 = down * (p.scale_log2 * run.k_gsa);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack_f16(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+          *reinterpret_cast<uint4*>(tile + (i / 8) * (kPTile * 128) + row * 128 + (((i ^ turn ^ row) & 7) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_full + w);
+          if (run.dual) mbar_arrive(q_empty + w);          // (this half has nothing more to do with the tile)
+        }
+        return true;
+      };
+      // ---- its tiles
+      auto weigh = [&](const volatile Run& run) -> bool {
+        const int n_my = my_tiles(run);
+        const bool on = is_on(run), any_on = __any_sync(0xFFFFFFFFu, on);
+        const int pos = run.kv - run.n_q + run.iq0 + quotient(run);
+        const int hi = !on ? 0 : p.causal ? pos + 1 : run.kv;
+        const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+        m_neg = INFINITY;
+        l = 0.0f;
+        for (int i = 0; i < n_my; ++i) {
+          const int j = run.dual ? i : 2 * i + w;
+          const int t0 = (run.tile0 + j) * kPTile;
+          if (!wait_all(s_full + w, ph_s)) return false;
+          ph_s ^= 1u;
+          tc_fence_after();
+          if (!any_on) {
+            // (rows that nobody asked for: their P may be anything)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(p_half + w);
+              mbar_arrive(p_full + w);
             }
             ph_h ^= 1u;
+            continue;
           }
-          n_tile += run.tiles;
-          if (n_my > 0) {
-            if (!wait_all(o_full + w, ph_o)) return false;
-            ph_o ^= 1u;
-            tc_fence_after();
-          }
-          return true;
-        };
-        // ---- its rows
-        auto finish = [&](const volatile Run& run) -> bool {
-          const int col = col_of(run);
-          const bool on = is_on(run);
-          float m = -m_neg;
-          // both halves on one set of rows: half 1 hands its rows over, through the
-          // query tiles (their scores are complete)
-          const bool cross = !run.dual && run.tiles > 1;
-          float keep = 1.0f, other = 0.0f;
-          const int x_row = col & (kPTile - 1);
-          float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + x_row * D;
-          if (cross) {
-            if (w == 0) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(x_ready);           // (its scores are done with the queries)
-              if (!wait_all(x_full, ph_x)) return false;
-              const float m1 = s_row[x_row], l1 = s_row[kPTile + x_row];
-              const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
-              keep = ex2(m - base);
-              other = ex2(m1 - base);
-              l = l * keep + l1 * other;
-              m = top;
-            } else {
-              if (!wait_all(x_ready, ph_x)) return false;
+          const uint32_t bytes = s_live[(n_tile + j) % kLive];
+          // bit i: tokens 16 i .. of the tile are in the cache
+          const uint32_t live = (bytes & 3u) | ((bytes >> 6) & 0xCu) | ((bytes >> 12) & 0x30u) | ((bytes >> 18) & 0xC0u);
+          const bool masked = __any_sync(0xFFFFFFFFu, t0 + kPTile > hi || t0 < lo || live != 0xFFu);
+          // bit x: the row sees token t0 + c + x (c a multiple of 32)
+          const int from = lo - t0, to = hi - t0;
+          auto seen32 = [&](int c) {
+            const int a = min(max(from - c, 0), 32), b = min(max(to - c, 0), 32);
+            const uint32_t m = (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
+            const uint32_t two = live >> (c / 16);
+            return m & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
+          };
+          // In two halves of 64 tokens: P V of the first starts under the second.
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_load32(t_o + c, o);
+          for (int c0 = 0; c0 < kPTile; c0 += kPTile / 2) {
+            uint32_t pr[kPTile / 4];
+            float sum;
+            auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
+              uint64_t sum2 = f2_pack(0.0f, 0.0f);
+              const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(m_neg, m_neg);
+              uint32_t s[2][32];
+              tmem_load32_start(t_s + c0, s[0]);
 #pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                  *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
-                      make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+              for (int c = 0; c < kPTile / 2; c += 32) {
+                uint32_t (&now)[32] = s[(c / 32) % 2];
+                tmem_load32_finish(now);
+                if (c + 32 < kPTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
+                const uint32_t see = hidden ? seen32(c0 + c) : 0xFFFFFFFFu;
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                  const uint64_t v =
+                      f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+                  float v0 = f2_lo(v), v1 = f2_hi(v);
+                  if (hidden) {
+                    v0 = see & (1u << x) ? v0 : -INFINITY;
+                    v1 = see & (2u << x) ? v1 : -INFINITY;
+                  }
+                  const float a = ex2(v0), b = ex2(v1);
+                  sum2 = f2_add(sum2, f2_pack(a, b));
+                  pr[(c + x) / 2] = pack_f16(a, b);
+                }
               }
-              s_row[x_row] = m;
-              s_row[kPTile + x_row] = l;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(x_full);
-              if (!wait_all(x_free, ph_x)) return false;
+              sum = f2_lo(sum2) + f2_hi(sum2);
+            };
+            // Weights that add up to more than 2^kRescaleAt hold a score far above m
+            // (a weight above 4, at least): no maximum is taken of the others.  (m at
+            // or above every score: at most 64 weights of 1.)
+            for (bool move = i == 0 && c0 == 0;; move = true) {
+              if (move) {
+                // m moves to the largest score so far, this half's included
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = c0; c < c0 + kPTile / 2; c += 32) {
+                  uint32_t s[32];
+                  tmem_load32_start(t_s + c, s);
+                  tmem_load32_finish(s);
+                  const uint32_t see = masked ? seen32(c) : 0xFFFFFFFFu;
+#pragma unroll
+                  for (int x = 0; x < 32; ++x)
+                    top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
+                }
+                const float now = fminf(m_neg, -top);
+                const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                m_neg = now;
+                l *= shrink;
+                if (i > 0 || c0 > 0) {
+                  // (earlier tiles are in O, S came after them; the first half may be on its way)
+                  if (c0 > 0) {
+                    if (!wait_all(h_full + w, ph_h)) return false;
+                    tc_fence_after();
+                  }
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    uint32_t y[16];
+                    tmem_load16(t_o + c, o);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
+                    tmem_store16(t_o + c, y);
+                  }
+                }
+              }
+              if (masked) weights(std::true_type{});
+              else weights(std::false_type{});
+              if (move || !__any_sync(0xFFFFFFFFu, sum > kMostSum)) break;
             }
-            ph_x ^= 1u;
+            l += sum;
+            // P over the columns of S that have been read
+#pragma unroll
+            for (int c = 0; c < kPTile / 4; c += 16) {
+              uint32_t x[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+              tmem_store16(t_s + c0 / 2 + c, x);
+            }
+            tmem_store_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive((c0 ? p_full : p_half) + w);
           }
-          if (run.dual || w == 0) {
-            const bool whole = run.whole;
-            float* part = p.partials + static_cast<size_t>(run.slot) * NC * (D + 2);
-            const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
-            // 128 bytes of each row at a time through shared memory, so that the warp
-            // stores whole lines; 16-byte vectors are swizzled by the row
-            uint8_t* rows_at = smem + Sm::kOut + warp * 32 * 128;
-            // (a lane stores vector lane % 8 of every fourth row)
-            const int64_t row_at = whole ? out_row(run) * (D * 2) : static_cast<int64_t>(col) * (D * 4);
-            const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on) >> (lane / 8);
-            uint8_t* base = whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part + 2 * NC);
-            uint8_t* to[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              to[i] = base + __shfl_sync(0xFFFFFFFFu, row_at, 4 * i + lane / 8) + (lane % 8) * 16;
-            auto put_vector = [&](int i, uint4 v) {
-              *reinterpret_cast<uint4*>(rows_at + lane * 128 + (((i ^ lane) & 7) << 4)) = v;
-            };
-            // every row's eight vectors, to byte `at` of each row's place
-            auto store_rows = [&](int at) {
-              __syncwarp();
-              const int r = lane / 8;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + (4 * i + r) * 128 +
-                                                                (((lane ^ (4 * i + r)) & 7) << 4));
-                if ((rows_on >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = v;
-              }
-              __syncwarp();
-            };
+          ph_h ^= 1u;
+        }
+        n_tile += run.tiles;
+        if (n_my > 0) {
+          if (!wait_all(o_full + w, ph_o)) return false;
+          ph_o ^= 1u;
+          tc_fence_after();
+        }
+        return true;
+      };
+      // ---- its rows
+      auto finish = [&](const volatile Run& run) -> bool {
+        const int col = col_of(run);
+        const bool on = is_on(run);
+        float m = -m_neg;
+        // both halves on one set of rows: half 1 hands its rows over, through the
+        // query tiles (their scores are complete)
+        const bool cross = !run.dual && run.tiles > 1;
+        float keep = 1.0f, other = 0.0f;
+        const int x_row = col & (kPTile - 1);
+        float* x_rows = reinterpret_cast<float*>(smem + Sm::kQ) + x_row * D;
+        if (cross) {
+          if (w == 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_ready);           // (its scores are done with the queries)
+            if (!wait_all(x_full, ph_x)) return false;
+            const float m1 = s_row[x_row], l1 = s_row[kPTile + x_row];
+            const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.0f : top;
+            keep = ex2(m - base);
+            other = ex2(m1 - base);
+            l = l * keep + l1 * other;
+            m = top;
+          } else {
+            if (!wait_all(x_ready, ph_x)) return false;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float o[32];
               tmem_load32(t_o + c, o);
-              if (cross) {
 #pragma unroll
-                for (int x = 0; x < 32; x += 4) {
-                  const float4 y = *reinterpret_cast<const float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4));
-                  o[x] = o[x] * keep + y.x * other;
-                  o[x + 1] = o[x + 1] * keep + y.y * other;
-                  o[x + 2] = o[x + 2] * keep + y.z * other;
-                  o[x + 3] = o[x + 3] * keep + y.w * other;
-                }
-              }
-              if (whole) {
-                // (a row that saw nothing has l = 0; what lies in its accumulator is finite)
-#pragma unroll
-                for (int x = 0; x < 32; x += 8) {
-                  uint32_t h[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(o[x + 2 * k] * inv, o[x + 2 * k + 1] * inv);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
-                  }
-                  put_vector((c % 64 + x) / 8, make_uint4(h[0], h[1], h[2], h[3]));
-                }
-                if (c % 64) store_rows((c - 32) * 2);
-              } else {
-#pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                  put_vector(x / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
-                                               __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
-                store_rows(c * 4);
-              }
+              for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4)) =
+                    make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
             }
+            s_row[x_row] = m;
+            s_row[kPTile + x_row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full);
+            if (!wait_all(x_free, ph_x)) return false;
+          }
+          ph_x ^= 1u;
+        }
+        if (run.dual || w == 0) {
+          const bool whole = run.whole;
+          float* part = p.partials + static_cast<size_t>(run.slot) * NC * (D + 2);
+          const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
+          // 128 bytes of each row at a time through shared memory, so that the warp
+          // stores whole lines; 16-byte vectors are swizzled by the row
+          uint8_t* rows_at = smem + Sm::kOut + warp * 32 * 128;
+          // (a lane stores vector lane % 8 of every fourth row)
+          const int64_t row_at = whole ? out_row(run) * (D * 2) : static_cast<int64_t>(col) * (D * 4);
+          const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on) >> (lane / 8);
+          uint8_t* base = whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part + 2 * NC);
+          uint8_t* to[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            to[i] = base + __shfl_sync(0xFFFFFFFFu, row_at, 4 * i + lane / 8) + (lane % 8) * 16;
+          auto put_vector = [&](int i, uint4 v) {
+            *reinterpret_cast<uint4*>(rows_at + lane * 128 + (((i ^ lane) & 7) << 4)) = v;
+          };
+          // every row's eight vectors, to byte `at` of each row's place
+          auto store_rows = [&](int at) {
+            __syncwarp();
+            const int r = lane / 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(rows_at + (4 * i + r) * 128 +
+                                                              (((lane ^ (4 * i + r)) & 7) << 4));
+              if ((rows_on >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = v;
+            }
+            __syncwarp();
+          };
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_load32(t_o + c, o);
             if (cross) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(x_free);
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(x_rows + c + (((x / 4) ^ (row & 7)) * 4));
+                o[x] = o[x] * keep + y.x * other;
+                o[x + 1] = o[x + 1] * keep + y.y * other;
+                o[x + 2] = o[x + 2] * keep + y.z * other;
+                o[x + 3] = o[x + 3] * keep + y.w * other;
+              }
             }
             if (whole) {
-              if (on && p.lse)
-                p.lse[out_row(run)] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
-            } else if (on) {
-              part[col] = m;
-              part[NC + col] = l;
+              // (a row that saw nothing has l = 0; what lies in its accumulator is finite)
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) {
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 y = __floats2bfloat162_rn(o[x + 2 * k] * inv, o[x + 2 * k + 1] * inv);
+                  h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                put_vector((c % 64 + x) / 8, make_uint4(h[0], h[1], h[2], h[3]));
+              }
+              if (c % 64) store_rows((c - 32) * 2);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4)
+                put_vector(x / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
+                                             __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+              store_rows(c * 4);
             }
           }
-          tc_fence_before();
-          if (!run.dual && my_tiles(run) > 0) {
-            fence_proxy_async_smem();                        // (rows went through the query tiles)
+          if (cross) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_empty + w);
+            if (lane == 0) mbar_arrive(x_free);
           }
-          return true;
-        };
-        auto softmax = [&]() -> bool {
-          for (int n = 0;; ++n) {
-            const int s = n % kRuns;
-            if (!wait_all(run_full + s, (n / kRuns) & 1)) return false;
-            const volatile Run& run = s_runs[s];
-            if (run.tiles < 0) return true;
-            if (!start(run) || !weigh(run) || !finish(run)) return false;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(run_empty + s);
+          if (whole) {
+            if (on && p.lse)
+              p.lse[out_row(run)] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+          } else if (on) {
+            part[col] = m;
+            part[NC + col] = l;
           }
-        };
-        if (!softmax()) give_up();
+        }
+        tc_fence_before();
+        if (!run.dual && my_tiles(run) > 0) {
+          fence_proxy_async_smem();                        // (rows went through the query tiles)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_empty + w);
+        }
+        return true;
+      };
+      auto softmax = [&]() -> bool {
+        for (int n = 0;; ++n) {
+          const int s = n % kRuns;
+          if (!wait_all(run_full + s, (n / kRuns) & 1)) return false;
+          const volatile Run& run = s_runs[s];
+          if (run.tiles < 0) return true;
+          if (!start(run) || !weigh(run) || !finish(run)) return false;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(run_empty + s);
+        }
+      };
+      if (!softmax()) give_up();
     }
   }
   tc_fence_before();
@@ -991,7 +1002,6 @@ nvr_status launch(AttnParams& p, int max_kv, cudaStream_t s) {
   if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
   int64_t grid = sms < kPrefillMaxCtas ? sms : kPrefillMaxCtas;
   if (grid > most) grid = most;
-  p.min_chunk = 2;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
