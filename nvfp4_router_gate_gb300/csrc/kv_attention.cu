@@ -814,6 +814,7 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   p.partials = reinterpret_cast<float*>(w + L.partials);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int max_kv = static_cast<int>(max_pages) * page_size;
+  if (window >= max_kv) p.window = 0;                        // (hides nothing, and may be near 2^31)
   if (static_cast<int64_t>(max_q) * p.G > kStreamCols) return launch_kv_prefill(p, D, max_kv, s);
   return D == 128 ? dispatch_attn<128>(p, max_kv, s) : dispatch_attn<64>(p, max_kv, s);
 }

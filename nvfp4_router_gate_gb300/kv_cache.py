@@ -18,6 +18,7 @@ from . import _dtype_code, new_workspace, nvr_read_device_status
 from . import _native
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_empty = torch.empty
 
 
 def nvfp4_kv_page_bytes(page_size, D):
@@ -56,15 +57,14 @@ def _ptr(t, dtype, n, name):
     return t.data_ptr()
 
 
-def _heads(t, name):
-    """Pointer and token stride of [T, heads, D] with contiguous heads."""
+def _heads(t, T, H, D, name):
+    """Pointer and token stride of t [T, H, D] with contiguous heads."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    T, H, D = t.shape
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
         raise ValueError("%s must have contiguous heads (a token stride is allowed)" % name)
-    return t.data_ptr(), (s[0] if T > 1 else H * D)
+    return t.data_ptr(), (s0 if T > 1 else H * D)
 
 
 class _Pages:
@@ -76,27 +76,33 @@ class _Pages:
         self.n_pages, self.Hkv, nbytes = cache.shape
         self.D, self.S = D, nbytes * 8 // (9 * D)
         self.data = _ptr(cache, _U8, cache.numel(), "cache")
+        self.lib = _native.lib()
         self.k_gsa, self.v_gsa = _ptr(k_gsa, _F32, self.Hkv, "k_gsa"), _ptr(v_gsa, _F32, self.Hkv, "v_gsa")
 
 
 def _append(pages, q, k, v, positions, slots, cos, sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
             q_out=None, stream=None):
-    T, Hkv, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
+    shape, dt = k.shape, k.dtype
+    T, Hkv, D = shape
+    if v.shape != shape or v.dtype is not dt:
         raise ValueError("k and v must have one shape and type")
     if Hkv != pages.Hkv or D != pages.D:
         raise ValueError("the cache holds %d KV heads of %d channels, k has %d of %d" % (pages.Hkv, pages.D, Hkv, D))
-    kp, ks = _heads(k, "k")
-    vp, vs = _heads(v, "v")
+    kp, ks = _heads(k, T, Hkv, D, "k")
+    vp, vs = _heads(v, T, Hkv, D, "v")
     Hq, qp, qs, op = 0, None, 0, None
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+        if q.dim() != 3 or q.dtype is not dt:
             raise ValueError("q must be [T, heads, D] of k's type")
-        Hq = q.shape[1]
-        qp, qs = _heads(q, "q")
+        Tq, Hq, Dq = q.shape
+        if Tq != T or Dq != D:
+            raise ValueError("q must be [T, heads, D] of k's type")
+        qp, qs = _heads(q, T, Hq, D, "q")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=k.device)
-        op = _ptr(q_out, _BF16, T * Hq * D, "q_out")
+            q_out = _empty((T, Hq, D), dtype=_BF16, device=k.device)
+            op = q_out.data_ptr()
+        else:
+            op = _ptr(q_out, _BF16, T * Hq * D, "q_out")
     rot = n_pos = 0
     if cos is not None:
         n_pos, half = cos.shape
@@ -104,11 +110,12 @@ def _append(pages, q, k, v, positions, slots, cos, sin, q_weight=None, k_weight=
         if sin is None or positions is None:
             raise ValueError("cos needs sin and positions")
     n = n_pos * rot // 2
-    st = _native.lib().nvfp4_kv_append(
+    st = pages.lib.nvfp4_kv_append(
         qp, qs, kp, ks, vp, vs, _dtype_code(k), T, Hq, Hkv, D,
         _ptr(positions, _I32, T, "positions") if rot else None, _ptr(slots, _I32, T, "slots"),
-        _ptr(cos, _F32, n, "cos"), _ptr(sin, _F32, n, "sin") if rot else None, n_pos, rot, interleaved,
-        _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight"), eps, pages.k_gsa, pages.v_gsa,
+        _ptr(cos, _F32, n, "cos") if rot else None, _ptr(sin, _F32, n, "sin") if rot else None, n_pos, rot, interleaved,
+        None if q_weight is None else _ptr(q_weight, _F32, D, "q_weight"),
+        None if k_weight is None else _ptr(k_weight, _F32, D, "k_weight"), eps, pages.k_gsa, pages.v_gsa,
         pages.data, pages.n_pages, pages.S, op, _raw_stream(stream))
     if st:
         _native.check("nvfp4_kv_append", st)
@@ -125,17 +132,21 @@ def nvfp4_kv_append(q, k, v, positions, slots, cos, sin, cache, k_gsa, v_gsa, **
 
 
 def _gather(pages, slots, out_dtype=_BF16, k_out=None, v_out=None, stream=None):
-    n = slots.numel()
+    n, Hkv, D = slots.numel(), pages.Hkv, pages.D
+    sp = _ptr(slots, _I32, n, "slots")
     if k_out is None and v_out is None:
-        shape, dev = (n, pages.Hkv, pages.D), slots.device
-        k_out, v_out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+        if out_dtype is not _BF16 and out_dtype is not _F32:
+            raise TypeError("out_dtype must be bfloat16 or float32, got %s" % out_dtype)
+        shape, dev = (n, Hkv, D), slots.device
+        k_out, v_out = _empty(shape, dtype=out_dtype, device=dev), _empty(shape, dtype=out_dtype, device=dev)
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
     elif k_out is None or v_out is None:
         raise ValueError("pass both k_out and v_out, or neither")
-    m, dt = n * pages.Hkv * pages.D, k_out.dtype
-    st = _native.lib().nvfp4_kv_gather(
-        pages.data, pages.n_pages, pages.S, pages.Hkv, pages.D, _ptr(slots, _I32, n, "slots"), n, pages.k_gsa,
-        pages.v_gsa, _ptr(k_out, dt, m, "k_out"), _ptr(v_out, dt, m, "v_out"), _dtype_code(k_out),
-        _raw_stream(stream))
+    else:
+        m, dt = n * Hkv * D, k_out.dtype
+        kp, vp = _ptr(k_out, dt, m, "k_out"), _ptr(v_out, dt, m, "v_out")
+    st = pages.lib.nvfp4_kv_gather(pages.data, pages.n_pages, pages.S, Hkv, D, sp, n, pages.k_gsa, pages.v_gsa, kp, vp,
+                                   _dtype_code(k_out), _raw_stream(stream))
     if st:
         _native.check("nvfp4_kv_gather", st)
     return k_out, v_out
@@ -160,17 +171,17 @@ def _attend(pages, q, page_table, kv_lens, cu_q=None, max_q=None, scale=None, ca
         max_q = T // B
     elif max_q is None:
         raise ValueError("cu_q needs max_q, the most queries of a sequence")
-    qp, qs = _heads(q, "q")
+    qp, qs = _heads(q, T, Hq, D, "q")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+        out = _empty((T, Hq, D), dtype=_BF16, device=q.device)
     if ws is None:
         nbytes = workspace.numel()
         ws = _ptr(workspace, _U8, nbytes, "workspace"), nbytes
-    st = _native.lib().nvfp4_kv_attention(
+    st = pages.lib.nvfp4_kv_attention(
         qp, qs, T, Hq, pages.Hkv, D, pages.data, pages.n_pages, pages.S,
         _ptr(page_table, _I32, B * max_pages, "page_table"), B, max_pages, _ptr(kv_lens, _I32, B, "kv_lens"),
-        _ptr(cu_q, _I32, B + 1, "cu_q"), max_q, pages.k_gsa, pages.v_gsa, D ** -0.5 if scale is None else scale,
-        causal, window, _ptr(out, _BF16, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1],
+        None if cu_q is None else _ptr(cu_q, _I32, B + 1, "cu_q"), max_q, pages.k_gsa, pages.v_gsa, D ** -0.5 if scale is None else scale,
+        causal, window, _ptr(out, _BF16, T * Hq * D, "out"), None if lse is None else _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1],
         _raw_stream(stream))
     if st:
         _native.check("nvfp4_kv_attention", st)

@@ -242,6 +242,16 @@ def test_several_queries_per_sequence(case):
     C.check(q32, n_q, out, lse, window=window)
 
 
+@pytest.mark.parametrize("m", [4, 70])
+def test_window_without_end(m):
+    """The largest window hides nothing, from queries in front of the first token either."""
+    rng = np.random.default_rng(70 + m)
+    C = Cached(rng, [3, 200], 1, 128, 16)
+    q, q32 = _queries(rng, 2 * m, 8, 128)
+    out, lse = C.run(q, window=2 ** 31 - 1)
+    C.check(q32, [m] * 2, out, lse)
+
+
 def test_long_chunk_spot_rows():
     rng = np.random.default_rng(11)
     C = Cached(rng, [3000, 700], 2, 128, 64)
