@@ -786,11 +786,11 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   if (!cache || !k_gsa || !v_gsa || !workspace) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (!q || !out || !kv_lens || B < 1 || max_q < 1 || (max_pages > 0 && !page_table)))
     return NVR_ERR_INVALID_ARG;
-  if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (q_stride < static_cast<int64_t>(Hq) * D || q_stride % 8)) return NVR_ERR_INVALID_ARG;
-  if (T > INT32_MAX || B > INT32_MAX || max_pages * page_size > INT32_MAX - 1024 ||
+  if (T > INT32_MAX || B > INT32_MAX || max_pages > (INT32_MAX - 1024) / page_size ||
       static_cast<int64_t>(max_q) * (Hq / Hkv) > INT32_MAX - 1024)
     return NVR_ERR_UNSUPPORTED;
+  if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
   if (off16(q) || off16(cache) || off16(out) || off4(page_table) || off4(kv_lens) || off4(cu_q) || off4(k_gsa) ||
       off4(v_gsa) || off4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return NVR_ERR_ALIGNMENT;

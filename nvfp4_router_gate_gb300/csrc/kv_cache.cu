@@ -467,7 +467,7 @@ extern "C" nvr_status nvfp4_kv_append(const void* q, int64_t q_stride, const voi
   if (!k_gsa || !v_gsa || !cache) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (!k || !v || !slots || (Hq > 0 && (!q || !q_out)))) return NVR_ERR_INVALID_ARG;
   if (T > 0 && rot > 0 && (!positions || !cos || !sin)) return NVR_ERR_INVALID_ARG;
-  if (n_pages * page_size > INT32_MAX) return NVR_ERR_UNSUPPORTED;     // slots are int32
+  if (n_pages > INT32_MAX / page_size) return NVR_ERR_UNSUPPORTED;     // slots are int32
   const int vec = dt == NVR_BF16 ? 8 : 4;                              // elements of 16 bytes
   if ((Hq > 0 && (q_stride < static_cast<int64_t>(Hq) * D || q_stride % vec)) ||
       k_stride < static_cast<int64_t>(Hkv) * D || k_stride % vec || v_stride < static_cast<int64_t>(Hkv) * D ||
@@ -525,7 +525,7 @@ extern "C" nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int
   if (!kv_head_dim_ok(D) || !kv_page_size_ok(page_size)) return NVR_ERR_UNSUPPORTED;
   if (!cache || !k_gsa || !v_gsa) return NVR_ERR_INVALID_ARG;
   if (n > 0 && (!slots || !k_out || !v_out)) return NVR_ERR_INVALID_ARG;
-  if (n_pages * page_size > INT32_MAX) return NVR_ERR_UNSUPPORTED;
+  if (n_pages > INT32_MAX / page_size) return NVR_ERR_UNSUPPORTED;
   if (off16(cache) || off16(k_out) || off16(v_out) || off4(slots) || off4(k_gsa) || off4(v_gsa))
     return NVR_ERR_ALIGNMENT;
   if (n == 0) return NVR_OK;

@@ -118,6 +118,21 @@ def test_append_extreme_magnitudes_saturate():
     assert np.array_equal(cache.cpu().numpy(), want)
 
 
+def test_append_under_a_scale_of_zero_stores_zeros():
+    import nvfp4_router_gate_gb300 as R
+    rng = np.random.default_rng(80)
+    x = rng.standard_normal((3, 2, 128)).astype(np.float32)
+    g = np.array([0.0, 2e-3], np.float32)
+    cache = _dev(np.full((1, 2, 16 * 144), 255, np.uint8))
+    d = to_device(x, "f32")
+    slots = np.array([0, 5, 15], np.int32)
+    R.nvfp4_kv_append(None, d, d, None, _dev(slots), None, None, cache, _dev(g), _dev(g))
+    kc, ks = K.entry(x, g)
+    assert not kc[:, 0].any() and not ks[:, 0].any()
+    want = K.store(np.full((1, 2, 16 * 144), 255, np.uint8), slots, kc, ks, kc, ks, 16)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 def test_append_needs_no_queries_and_no_tokens():
     import nvfp4_router_gate_gb300 as R
     kv = R.Nvfp4KVCache(2, 2, 64, page_size=16)
