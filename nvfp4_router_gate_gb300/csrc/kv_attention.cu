@@ -24,18 +24,18 @@
 //
 // Work: the tiles (16 tokens for each of MW groups of each of NW warps) of all
 // (sequence, column group, KV head) keys, laid end to end, are cut into equal
-// chunks, one per resident block; a key cut by a chunk border leaves partials in
+// chunks, one per resident team; a key cut by a chunk border leaves partials in
 // the workspace, joined in chunk order by csrc/kv_join.cu, so that results do not
 // depend on timing.  One producer warp feeds a ring of tiles with bulk copies, a
 // page of one KV head each.
 //
-// Measured (D = 128, 8 KV heads of 8 heads): 128 sequences of up to 8192 tokens 121
-// us, 4.5 TB/s, 0.67 of the copy bandwidth (0.88 of it between the first tiles and the
-// first blocks to finish; the blocks' times spread by 12 %, memory is not shared out
+// Measured (D = 128, 8 KV heads of 8 heads): 128 sequences of up to 8192 tokens 118
+// us, 4.7 TB/s, 0.69 of the copy bandwidth (0.88 of it between the first tiles and the
+// first teams to finish; the teams' times spread by 12 %, memory is not shared out
 // evenly); one sequence of 131072 tokens 41 us, 3.7 TB/s; 32 sequences of up to 4096
-// tokens with four queries 59 us.  A tile of 128 tokens takes a block 1.4 us with
-// eight columns (three blocks an SM) and with sixteen (two: 1024 of the 1400 clocks a
-// tile has are the matrix instructions').
+// tokens with four queries 59.5 us.  A tile of 128 tokens takes a team 1.4 us with
+// eight columns (three teams an SM) and with sixteen (two: 1024 of the 1400 clocks a
+// tile has are the matrix instructions).
 #include "kv_attention.cuh"
 #include "../../include/nvfp4_kv_cache.h"
 
@@ -50,11 +50,11 @@ namespace {
 // 53.8, 32: 45.3 / 50.8, 48: 60.8 / 49.6.  Four sequences of 600: 32: 13.1 / 16.9, 64:
 // 14.7 / 17.0.
 constexpr int kStreamCols = 32;
-// Starting and ending a key (queries, joining the warps, storing) costs a block
+// Starting and ending a key (queries, joining the warps, storing) costs a team
 // about as much as this many tiles: 1.5 us beside 1.4 us for a tile with eight
-// columns, 3.0 beside 1.4 with sixteen (least squares over the blocks of the serving
+// columns, 3.0 beside 1.4 with sixteen (least squares over the teams of the serving
 // batch and of 32 sequences with four queries).  Counted in the chunks, so that
-// blocks with many short keys get fewer tiles.
+// teams with many short keys get fewer tiles.
 template <int NT>
 constexpr int kKeyCost = NT;
 
@@ -70,11 +70,12 @@ struct alignas(16) Meta {
   int tile, head;
   int kv, n_q, q0, iq0, rem0, n_cols;   // the first column is head rem0 of the group's query iq0
   float k_gsa, v_gsa;
-  int pad[2];
+  int slot;                   // of the run's partial results
+  int pad;
 };
 // a run's first and last tile; a tile that some column does not see whole; the
-// run is all of its key; the block's last run; the key starts inside the chunk
-constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4, kWhole = 8, kDone = 16, kTail = 32;
+// run is all of its key; the team's last run
+constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4, kWhole = 8, kDone = 16;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -100,12 +101,18 @@ struct AttnShape {
   static constexpr int kShare = kFrag / NW;                  // of them, those a warp joins
   static constexpr int kJoinBytes = NW * (NW - 1) * kShare * 32 * 4;
   static constexpr int kQBytes = NT * (D / 16) * 64 * 4;
-  static constexpr int kSmem = STAGES * kStageBytes + kJoinBytes + kQBytes + 2 * NW * kCols * 4 +
-                               STAGES * (static_cast<int>(sizeof(Meta)) + kCols * D * 2) + (2 * STAGES + 3) * 8 + 64 + 128;
+  static constexpr int kTeamBytes = (STAGES * kStageBytes + kJoinBytes + kQBytes + 2 * NW * kCols * 4 +
+                               STAGES * (static_cast<int>(sizeof(Meta)) + kCols * D * 2) + (2 * STAGES + 3) * 8 + 64 + 127) / 128 * 128;
 };
 
-template <int D, int NT, int NW, int MW, int STAGES, int MINB>
-__global__ void __launch_bounds__(32 * (NW + 1), MINB)
+// A block is `TEAMS` teams of NW consumer warps and a producer, each with its own ring
+// and its own share of the work.  Eight columns: three teams in a block that fills the
+// SM.  (As three blocks of five warps they fit only if their fifth warps go to different
+// schedulers, and beside leftovers of an earlier kernel some did not: a share then
+// began when another had ended.)  Sixteen: two blocks of one team, whose registers do
+// not suffice for more addressing (draft 59.5 us, as one block 64.5).
+template <int D, int NT, int NW, int MW, int STAGES, int TEAMS, int BLOCKS>
+__global__ void __launch_bounds__(32 * TEAMS * (NW + 1), BLOCKS)
 kv_attention_kernel(const AttnParams p) {
   using Sh = AttnShape<D, NT, NW, MW, STAGES>;
   constexpr int TILE = Sh::kTile, NC = Sh::kCols, SH = Sh::kShare;
@@ -114,7 +121,13 @@ kv_attention_kernel(const AttnParams p) {
   constexpr int KS = D / 16;                                 // steps of the first product
   constexpr int MT = D / 16;                                 // channel tiles of the second
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  // (uniform in the warp, and known to be)
+  const int team = TEAMS == 1 ? 0 : __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) / Sh::kThreads, 0);
+  const int tid = threadIdx.x - team * Sh::kThreads, warp = tid >> 5, lane = tid & 31;
+  // shares are dealt to the SMs in turn
+  const int share = team * gridDim.x + blockIdx.x, shares = TEAMS * gridDim.x;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127)) +
+                  team * Sh::kTeamBytes;
   float* s_join = reinterpret_cast<float*>(smem + STAGES * Sh::kStageBytes);          // [NW][NW - 1][SH][32]
   uint32_t* s_q = reinterpret_cast<uint32_t*>(s_join + Sh::kJoinBytes / 4);                 // [NT][KS][32][2]: B fragments of Q^T
   float* s_m = reinterpret_cast<float*>(s_q + Sh::kQBytes / 4);                       // [NW][NC]
@@ -127,7 +140,6 @@ kv_attention_kernel(const AttnParams p) {
   uint64_t* join_free = meet + 1;                            // the join buffer has been read
   int* s_start = reinterpret_cast<int*>(meet + 2);           // item, offset inside it, whether the chunk has work
   volatile int* abort_flag = s_start + 4;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, NW); }
@@ -159,8 +171,8 @@ kv_attention_kernel(const AttnParams p) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinChunk);
-  const int f0 = min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total));
+  const int chunk = max((total + shares - 1) / shares, kMinChunk);
+  const int f0 = min(static_cast<int64_t>(share) * chunk, static_cast<int64_t>(total));
   const int f1 = min(f0 + chunk, total);
   const int excl = before + incl - mine;
   if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
@@ -179,7 +191,7 @@ kv_attention_kernel(const AttnParams p) {
     s_start[2] = ti < g.tiles || f1 - f0 > key_cost<NT>(g) - ti;
   }
   __syncthreads();
-  if (tid == 32 * NW) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
+  if (tid == 32 * NW) p.joins[share].n_parts = 0;            // (until this team turns out to start a cut key)
   if (f0 >= f1 || !s_start[2]) return;
 
   if (warp == NW) {
@@ -243,15 +255,16 @@ kv_attention_kernel(const AttnParams p) {
           const int key_f0 = f - ti, key_end = key_f0 + g.tiles;
           m.kv = g.kv; m.n_q = g.n_q; m.q0 = g.q0; m.iq0 = iq0; m.rem0 = rem0; m.n_cols = g.n_cols;
           m.k_gsa = k_gsa; m.v_gsa = v_gsa;
+          // slot 0 when the key's run starts with the chunk, else 1 (it ends it)
+          m.slot = 2 * share + (key_f0 > f0);
           const uint32_t each = (1u << (part / 16)) - 1;
           m.live = 0;
           for (int i = 0; i < pieces; ++i)
             if ((got >> i) & 1u) m.live |= each << (i * (part / 16));
           m.flags = (first ? kFirst : 0u) | (ti == g.tiles - 1 || f == f1 - 1 ? kLast : 0u) |
-                    (key_f0 >= f0 && key_end <= f1 ? kWhole : 0u) | (key_end + kKeyCost<NT> >= f1 ? kDone : 0u) |
-                    (key_f0 > f0 ? kTail : 0u);
+                    (key_f0 >= f0 && key_end <= f1 ? kWhole : 0u) | (key_end + kKeyCost<NT> >= f1 ? kDone : 0u);
           if (key_f0 >= f0 && key_end > f1 && first)         // this block holds the key's first part
-            p.joins[blockIdx.x] = {(key_end - 1) / chunk - key_f0 / chunk + 1, key_f0 > f0, g.q0 + iq0, rem0, g.n_cols,
+            p.joins[share] = {(key_end - 1) / chunk - key_f0 / chunk + 1, key_f0 > f0, g.q0 + iq0, rem0, g.n_cols,
                                    head, v_gsa, 0};
           if (t0 + TILE > sure_hi || t0 < sure_lo || got != (1u << pieces) - 1u) m.flags |= kEdge;
           s_meta[st] = m;
@@ -579,10 +592,10 @@ kv_attention_kernel(const AttnParams p) {
         }
       }
     }
-    int head = 0, q0 = 0, rem0 = 0, n_cols = 0;
+    int head = 0, q0 = 0, rem0 = 0, n_cols = 0, slot = 0;
     float v_gsa = 0.0f;
     if (flags & kLast) {
-      q0 = meta.q0 + meta.iq0; head = meta.head; rem0 = meta.rem0; n_cols = meta.n_cols; v_gsa = meta.v_gsa;
+      q0 = meta.q0 + meta.iq0; head = meta.head; rem0 = meta.rem0; n_cols = meta.n_cols; v_gsa = meta.v_gsa; slot = meta.slot;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + st);
@@ -602,8 +615,6 @@ kv_attention_kernel(const AttnParams p) {
         l_run[nt][i] = l;
       }
     const bool whole = flags & kWhole;
-    // a key's run: slot 0 when it starts with the chunk, else 1 (it ends it)
-    const int slot = 2 * blockIdx.x + (flags & kTail ? 1 : 0);
     float* part_m = p.partials + static_cast<size_t>(slot) * NC * (D + 2);
     float* part_l = part_m + NC;
     float* part_o = part_l + NC;                             // [NC][D]
@@ -701,62 +712,61 @@ struct AttnWs {
 AttnWs attn_ws_layout(int D) {
   AttnWs L;
   L.joins = 256;
-  L.partials = a256(L.joins + kAttnMaxCtas * sizeof(KeyJoin));
+  L.partials = a256(L.joins + kAttnMaxShares * sizeof(KeyJoin));
   L.total = a256(L.partials + size_t(2) * kPrefillMaxCtas * kPrefillCols * (D + 2) * 4);
   return L;
 }
 
-template <int D, int NT, int NW, int MW, int STAGES, int MINB>
+template <int D, int NT, int NW, int MW, int STAGES, int TEAMS, int BLOCKS>
 nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   using Sh = AttnShape<D, NT, NW, MW, STAGES>;
-  auto kernel = kv_attention_kernel<D, NT, NW, MW, STAGES, MINB>;
-  static int per_sm[kMaxDevices] = {};
+  auto kernel = kv_attention_kernel<D, NT, NW, MW, STAGES, TEAMS, BLOCKS>;
+  constexpr int kSmem = TEAMS * Sh::kTeamBytes + 128;
+  static_assert(kSmem <= 227 * 1024 && BLOCKS * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  static bool attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
   const int sms = device_sm_count();
   if (sms <= 0) return NVR_ERR_CUDA;
-  if (!per_sm[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (!attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return cuda_status(e);
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, Sh::kThreads, Sh::kSmem);
-    if (e != cudaSuccess) return cuda_status(e);
-    per_sm[dev] = n > 0 ? n : 1;
+    attr_set[dev] = true;
   }
   p.groups = static_cast<int>((static_cast<int64_t>(p.max_q) * p.G + Sh::kCols - 1) / Sh::kCols);
   // the flat order of tiles is counted in 32 bits
   const int64_t items = static_cast<int64_t>(p.B) * p.groups;
   const int64_t most = items * p.Hkv * ((max_kv + Sh::kTile - 1) / Sh::kTile + 1 + kKeyCost<NT>);
   if (items >= (int64_t(1) << 30) || most >= (int64_t(1) << 31) - (1 << 24)) return NVR_ERR_UNSUPPORTED;
-  int64_t grid = static_cast<int64_t>(sms) * per_sm[dev];
-  if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
-  if (grid * Sh::kCols > kAttnMaxCols) grid = kAttnMaxCols / Sh::kCols;
+  int64_t grid = sms * BLOCKS;
+  if (grid * TEAMS > kAttnMaxShares) grid = kAttnMaxShares / TEAMS;
+  if (grid * TEAMS * Sh::kCols > kAttnMaxCols) grid = kAttnMaxCols / Sh::kCols / TEAMS;
   if (grid > most) grid = most;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(Sh::kThreads);
-  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.blockDim = dim3(TEAMS * Sh::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_status(e);
   if (max_kv <= Sh::kTile) return NVR_OK;                    // keys of one tile are never cut
-  return launch_kv_join(p, D, static_cast<int>(grid), Sh::kCols, items * p.Hkv, s);
+  return launch_kv_join(p, D, static_cast<int>(grid) * TEAMS, Sh::kCols, items * p.Hkv, s);
 }
 
 template <int D>
 nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
-  // Sixteen columns at a time, two blocks an SM, where eight (three blocks) do not hold
+  // Sixteen columns at a time, two teams an SM, where eight (three teams) do not hold
   // a sequence's queries: 16 columns of 32 sequences of up to 4096 tokens 37.9 us, as
   // twice eight 45.6; 32 columns 59.4 and 78.4.  Eight columns as half of sixteen: the
   // serving batch 164 us instead of 121, the long sequence 52 instead of 41.
   const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
-  if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3>(p, max_kv, s);
-  return launch_attn<D, 2, 4, 2, 3, 2>(p, max_kv, s);
+  if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3, 1>(p, max_kv, s);
+  return launch_attn<D, 2, 4, 2, 3, 1, 2>(p, max_kv, s);
 }
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }

@@ -138,10 +138,10 @@ __device__ __forceinline__ void query_scale(uint32_t big, float& up, float& down
 
 // Workspace of an attention call (csrc/kv_attention.cu): control words, the cut
 // keys, the partial results.
-constexpr int kAttnMaxCtas = 2048;
+constexpr int kAttnMaxShares = 2048;    // teams of the streaming kernel at most
 constexpr int kPrefillMaxCtas = 160;       // blocks of the tensor-memory kernel
 constexpr int kPrefillCols = 256;          // its columns
-constexpr int kAttnMaxCols = 16384;        // columns * blocks of the streaming kernel at most
+constexpr int kAttnMaxCols = 16384;        // columns * teams of the streaming kernel at most
 static_assert(kPrefillMaxCtas * kPrefillCols >= kAttnMaxCols, "the partials hold either kernel's");
 
 // Joins the cut keys of `blocks` blocks, of `keys` keys at most (csrc/kv_join.cu);
