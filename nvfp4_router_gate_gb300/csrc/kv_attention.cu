@@ -1,7 +1,8 @@
 // kv_attention.cu -- softmax attention over the paged NVFP4 key/value cache,
 // streaming form (sm_103a): 8 or 16 (query, head) columns share one pass over
 // their KV head's tokens.  One or a few queries per sequence: bound by the
-// cache's bytes, from 16 columns on by the warp-level matrix instructions.
+// cache's bytes, with 16 columns by the latency of the few warps that their
+// accumulators leave registers for.
 //
 // Mathematics.  For a column's query q and its visible tokens t
 //   s_t = scale * q . k_t,  m = max s_t,  p_t = exp(s_t - m),
@@ -34,8 +35,9 @@
 // first teams to finish; the teams' times spread by 12 %, memory is not shared out
 // evenly); one sequence of 131072 tokens 41 us, 3.7 TB/s; 32 sequences of up to 4096
 // tokens with four queries 59.5 us.  A tile of 128 tokens takes a team 1.4 us with
-// eight columns (three teams an SM) and with sixteen (two: 1024 of the 1400 clocks a
-// tile has are the matrix instructions).
+// eight columns (three teams an SM, issue slots 60 % busy) and with sixteen (two teams:
+// issue slots 44 %, matrix pipe 27 %; tiles of 64 tokens, with two teams or with three
+// at 128 registers, were slower: 67.7 and 71.4 us instead of 59.5).
 #include "kv_attention.cuh"
 #include "../../include/nvfp4_kv_cache.h"
 
