@@ -77,9 +77,10 @@ kv_join_few_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ 
     for (int r = 0; r < R; ++r)
       load_channels<CH>(part_of(partials, k, i, slot) + 2 * NC + min(n0 + r, k.n_cols - 1) * D + lane * CH, y[r]);
   };
-  float y[2][R][CH];
-  load(0, y[0]);
-  load(1, y[1]);
+  constexpr int N = 4;                                       // parts whose channels are on their way
+  float y[N][R][CH];
+#pragma unroll
+  for (int i = 0; i < N; ++i) load(min(i, k.n_parts - 1), y[i]);
   for (int b = 0; b < k.n_parts; b += P) {
     const int m = min(P, k.n_parts - b);
     float w = -INFINITY, l = 0.0f;
@@ -103,9 +104,9 @@ kv_join_few_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ 
         for (int x = 0; x < CH; ++x) acc[r][x] *= f;
       }
     }
-    for (int i0 = 0; i0 < m; i0 += 2) {
+    for (int i0 = 0; i0 < m; i0 += N) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         // (past the end of the batch: a weight of zero)
         const float wi = i0 + i < m ? w : 0.0f;
 #pragma unroll
@@ -115,9 +116,9 @@ kv_join_few_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ 
           for (int x = 0; x < CH; ++x) acc[r][x] += f * y[i][r][x];
         }
       }
-      if (b + i0 + 2 < k.n_parts) {
-        load(b + i0 + 2, y[0]);
-        load(min(b + i0 + 3, k.n_parts - 1), y[1]);
+      if (b + i0 + N < k.n_parts) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) load(min(b + i0 + N + i, k.n_parts - 1), y[i]);
       }
     }
   }
@@ -145,69 +146,70 @@ kv_join_many_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t slot = static_cast<size_t>(NC) * (D + 2);
   const int parts = (k.n_parts - warp + W - 1) / W;          // this warp's: warp, warp + W, ...
-  const int n = blockIdx.y;
-  if (n >= k.n_cols) return;
-  float top = -INFINITY, sum = 0.0f, acc[CH];
+  for (int n = blockIdx.y; n < k.n_cols; n += gridDim.y) {
+    float top = -INFINITY, sum = 0.0f, acc[CH];
 #pragma unroll
-  for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
-  for (int b = 0; b < parts; b += 32) {
-    const int m = min(32, parts - b);
-    float w = -INFINITY, l = 0.0f;
-    if (lane < m) {
-      const float* src = part_of(partials, k, (b + lane) * W + warp, slot) + n;
-      w = src[0];
-      l = src[NC];
-    }
-    float high = fmaxf(top, w);
+    for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
+    for (int b = 0; b < parts; b += 32) {
+      const int m = min(32, parts - b);
+      float w = -INFINITY, l = 0.0f;
+      if (lane < m) {
+        const float* src = part_of(partials, k, (b + lane) * W + warp, slot) + n;
+        w = src[0];
+        l = src[NC];
+      }
+      float high = fmaxf(top, w);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
-    const float base = high == -INFINITY ? 0.0f : high, shrink = ex2(top - base);
-    top = high;
-    w = ex2(w - base);
-    sum = sum * shrink + w * l;
+      for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, d));
+      const float base = high == -INFINITY ? 0.0f : high, shrink = ex2(top - base);
+      top = high;
+      w = ex2(w - base);
+      sum = sum * shrink + w * l;
 #pragma unroll
-    for (int x = 0; x < CH; ++x) acc[x] *= shrink;
-    for (int i0 = 0; i0 < m; i0 += 8) {
-      float y[8][CH];
+      for (int x = 0; x < CH; ++x) acc[x] *= shrink;
+      for (int i0 = 0; i0 < m; i0 += 8) {
+        float y[8][CH];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        // (past the end: the last part, under a weight of zero)
-        load_channels<CH>(part_of(partials, k, (b + min(i0 + i, m - 1)) * W + warp, slot) + 2 * NC + n * D + lane * CH, y[i]);
+        for (int i = 0; i < 8; ++i)
+          // (past the end: the last part, under a weight of zero)
+          load_channels<CH>(part_of(partials, k, (b + min(i0 + i, m - 1)) * W + warp, slot) + 2 * NC + n * D + lane * CH, y[i]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float wi = __shfl_sync(0xFFFFFFFFu, w, i0 + i);
+        for (int i = 0; i < 8; ++i) {
+          const float wi = __shfl_sync(0xFFFFFFFFu, w, i0 + i);
 #pragma unroll
-        for (int x = 0; x < CH; ++x) acc[x] += wi * y[i][x];
+          for (int x = 0; x < CH; ++x) acc[x] += wi * y[i][x];
+        }
       }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    // the warps of the row, in order
+    __syncthreads();                                         // (the last row's are read)
+    if (lane == 0) {
+      s_top[warp] = top;
+      s_sum[warp] = sum;
+    }
+#pragma unroll
+    for (int x = 0; x < CH; ++x) s_acc[warp][lane][x] = acc[x];
+    __syncthreads();
+    if (warp) continue;
+#pragma unroll
+    for (int i = 1; i < W; ++i) top = fmaxf(top, s_top[i]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float w = ex2(s_top[i] - base);
+      sum += w * s_sum[i];
+#pragma unroll
+      for (int x = 0; x < CH; ++x) acc[x] += w * s_acc[i][lane][x];
+    }
+    const int64_t row = out_row(k, n, Hq, G);
+    store_channels<CH>(out + row * D + lane * CH, acc, sum > 0.0f ? __fdividef(k.v_gsa, sum) : 0.0f);
+    if (lse && lane == 0) lse[row] = lse_of(top, sum);
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  // the warps of the row, in order
-  if (lane == 0) {
-    s_top[warp] = top;
-    s_sum[warp] = sum;
-  }
-#pragma unroll
-  for (int x = 0; x < CH; ++x) s_acc[warp][lane][x] = acc[x];
-  __syncthreads();
-  if (warp) return;
-#pragma unroll
-  for (int i = 1; i < W; ++i) top = fmaxf(top, s_top[i]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  sum = 0.0f;
-#pragma unroll
-  for (int x = 0; x < CH; ++x) acc[x] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float w = ex2(s_top[i] - base);
-    sum += w * s_sum[i];
-#pragma unroll
-    for (int x = 0; x < CH; ++x) acc[x] += w * s_acc[i][lane][x];
-  }
-  const int64_t row = out_row(k, n, Hq, G);
-  store_channels<CH>(out + row * D + lane * CH, acc, sum > 0.0f ? __fdividef(k.v_gsa, sum) : 0.0f);
-  if (lse && lane == 0) lse[row] = lse_of(top, sum);
 }
 
 }  // namespace
@@ -217,12 +219,18 @@ nvr_status launch_kv_join(const AttnParams& p, int D, int blocks, int NC, int64_
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // A key has about blocks / keys parts.  From eight on a row gets a block (one
-  // sequence of 131072 tokens, 57 parts: 49.6 -> 41.1 us for the call).
-  const bool many = keys * 8 <= blocks;
-  const int warps = many ? kJoinWarps : NC / kJoinRows < kJoinWarps ? NC / kJoinRows : kJoinWarps;
-  const int rows = many ? 1 : warps * kJoinRows;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((NC + rows - 1) / rows));
+  // A key has about blocks / keys parts and at most `cols` rows.  From eight parts on (32,
+  // where a key has many rows to share out) a row gets a block: one sequence of 131072
+  // tokens, 57 parts: 49.6 -> 41.1 us for the call.  At most 64 rows of a key at once: of
+  // the blocks most have no key, and 152 x 256 of them took 35 us (two sequences of 695
+  // tokens, 16 queries of 24 and 6 heads: 45.6 -> 13.2 us).
+  const int64_t all = static_cast<int64_t>(p.max_q) * p.G;
+  const int cols = static_cast<int>(all < NC ? all : NC);
+  const bool many = keys * (cols > 32 ? 32 : 8) <= blocks;
+  const int warps = many || cols > kJoinRows * (kJoinWarps - 1) ? kJoinWarps : (cols + kJoinRows - 1) / kJoinRows;
+  const int rows = warps * kJoinRows;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
+                     static_cast<unsigned>(many ? (cols < 64 ? cols : 64) : (cols + rows - 1) / rows));
   cfg.blockDim = dim3(32 * warps);
   cfg.stream = s;
   cfg.attrs = pdl;
