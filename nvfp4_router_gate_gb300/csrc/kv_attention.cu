@@ -52,6 +52,12 @@ namespace {
 // 53.8, 32: 45.3 / 50.8, 48: 60.8 / 49.6.  Four sequences of 600: 32: 13.1 / 16.9, 64:
 // 14.7 / 17.0.
 constexpr int kStreamCols = 32;
+// But a call of at most this many tiles an SM (128 tokens and 16 columns each, by the
+// page tables' width) stays here: it starts and ends sooner.  This kernel / that one,
+// us: one sequence of 2 KV heads, 128 columns, 600 tokens (80 tiles) 12.4 / 15.6; 512
+// columns, 1500 tokens (768) 14.8 / 18.0; four of 8 heads, 256 columns, 130 tokens (1024)
+// 16.8 / 17.4; 128 columns, 600 tokens (1280) 17.9 / 16.9; 256, 600 (2560) 26.5 / 19.2.
+constexpr int kStreamTiles = 6;
 // Starting and ending a key (queries, joining the warps, storing) costs a team
 // about as much as this many tiles: 1.5 us beside 1.4 us for a tile with eight
 // columns, 3.0 beside 1.4 with sixteen (least squares over the teams of the serving
@@ -827,6 +833,10 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int max_kv = static_cast<int>(max_pages) * page_size;
   if (window >= max_kv) p.window = 0;                        // (hides nothing, and may be near 2^31)
-  if (static_cast<int64_t>(max_q) * p.G > kStreamCols) return launch_kv_prefill(p, D, max_kv, s);
+  const int sms = device_sm_count();
+  if (sms <= 0) return NVR_ERR_CUDA;
+  const int64_t cols = static_cast<int64_t>(max_q) * p.G;
+  const double tiles = static_cast<double>(B) * Hkv * static_cast<double>((cols + 15) / 16) * ((max_kv + 127) / 128);
+  if (cols > kStreamCols && tiles > kStreamTiles * sms) return launch_kv_prefill(p, D, max_kv, s);
   return D == 128 ? dispatch_attn<128>(p, max_kv, s) : dispatch_attn<64>(p, max_kv, s);
 }

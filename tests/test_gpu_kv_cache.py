@@ -156,6 +156,8 @@ def test_append_needs_no_queries_and_no_tokens():
 class Cached:
     """A cache of random entries, the rest of its bytes random (NaN scales too)."""
 
+    pad = 0                                                            # unused columns of the page table
+
     def __init__(self, rng, lens, H, D, S, spare=3, first_page=0, spread=1.0):
         self.lens, self.H, self.D, self.S = np.array(lens, np.int32), H, D, S
         used = [(int(n) + S - 1) // S for n in lens]
@@ -163,7 +165,7 @@ class Cached:
         self.kg, self.vg = ((0.002 + 0.002 * rng.random(H)).astype(np.float32) for _ in range(2))
         cache = rng.integers(0, 256, (n_pages, H, S * D * 9 // 8)).astype(np.uint8)
         order = rng.permutation(n_pages)
-        self.table = np.full((len(lens), max(max(used), 1) + 1), -1, np.int32)
+        self.table = np.full((len(lens), max(max(used), 1) + 1 + self.pad), -1, np.int32)
         self.k, self.v = [], []
         at = 0
         for b, n in enumerate(lens):
@@ -472,3 +474,33 @@ def test_workspace_is_used_again_by_calls_of_other_shapes():
         out, lse = C.run(q, workspace=ws)
         C.check(q32, [m] * 3, out, lse, rows=4)
     assert R.nvr_read_device_status(ws) == 0
+
+
+# The same through the tensor-memory kernel, which takes the calls of many columns whose
+# page tables are wide.
+
+@pytest.fixture
+def wide(monkeypatch):
+    monkeypatch.setattr(Cached, "pad", 4096)
+
+
+@pytest.mark.parametrize("case", MANY + COLUMNS, ids=lambda c: "n%d_q%d_H%d_G%d_D%d_S%d_w%d" % (max(c[0]), max(c[1]), *c[2:]))
+def test_wide_tables(wide, case):
+    test_several_queries_per_sequence(case)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m", [40, 90])
+def test_wide_tables_without_causal_mask(wide, D, m):
+    test_without_causal_mask(D, m)
+
+
+def test_wide_tables_extremes(wide):
+    test_large_scores_and_tiny_queries(40)
+    test_pages_outside_the_cache_are_not_seen(40)
+    test_maximum_moves_inside_a_tile(50, True)
+    test_maximum_moves_inside_a_tile(50, False)
+    test_pages_before_the_window_may_be_freed(40)
+    test_window_without_end(70)
+    test_workspace_is_used_again_by_calls_of_other_shapes()
+    test_one_long_sequence_among_short_ones(40, 128)
