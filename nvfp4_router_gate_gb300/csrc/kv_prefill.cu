@@ -34,15 +34,17 @@
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
 // equal chunks, one per block, the rows of cut keys joined by csrc/kv_join.cu.
 //
-// Measured (D = 128, 8 KV heads): 2048 queries of 64 heads over 8192 tokens 388 us,
-// 1242 TFLOP/s, 0.65 of the cuBLAS bf16 rate; nine ragged prompts of up to 1500
-// queries of 32 heads over 2500 tokens 112 us.  A tile of 128 tokens and 256 columns takes
+// Measured (D = 128, 8 KV heads): 2048 queries of 64 heads over 8192 tokens 383 us,
+// 1256 TFLOP/s, 0.66 of the cuBLAS bf16 rate; nine ragged prompts of up to 1500
+// queries of 32 heads over 2500 tokens 111 us.  A tile of 128 tokens and 256 columns takes
 // 1.8 us (3400 clocks; its products 2050): each row tile's softmax 2200 clocks and
 // then 1000 of waiting for its next S, which the full tensor memory leaves no room to
 // make earlier.  A run of a key costs 4.6 us on top (queries in, rows out).  Tried and
 // slower: loops around the issue of the products (510 us for the chunk), unrolled
 // halves of the softmax (450: fetching the instructions), eight warps that expand
-// (450: 96 registers a thread), other splits of the registers (equal).
+// (450: 96 registers a thread), other splits of the registers (equal), scores in
+// halves of 64 tokens that are made while the other half is weighed (536), S loaded a
+// half ahead (388).
 #include <type_traits>
 
 #include "kv_attention.cuh"
