@@ -53,7 +53,7 @@ namespace {
 // 14.7 / 17.0.
 constexpr int kStreamCols = 32;
 // But a call of at most this many tiles an SM (128 tokens and 16 columns each, by the
-// page tables' width) stays here: it starts and ends sooner.  This kernel / that one,
+// page tables' width and the window) stays here: it starts and ends sooner.  This kernel / that one,
 // us: one sequence of 2 KV heads, 128 columns, 600 tokens (80 tiles) 12.4 / 15.6; 512
 // columns, 1500 tokens (768) 14.8 / 18.0; four of 8 heads, 256 columns, 130 tokens (1024)
 // 16.8 / 17.4; 128 columns, 600 tokens (1280) 17.9 / 16.9; 256, 600 (2560) 26.5 / 19.2.
@@ -836,7 +836,9 @@ extern "C" nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_
   const int sms = device_sm_count();
   if (sms <= 0) return NVR_ERR_CUDA;
   const int64_t cols = static_cast<int64_t>(max_q) * p.G;
-  const double tiles = static_cast<double>(B) * Hkv * static_cast<double>((cols + 15) / 16) * ((max_kv + 127) / 128);
+  // (16 columns are at most 16 queries: they see a window and 15 tokens more)
+  const int seen = p.window > 0 && p.window < max_kv - 16 ? p.window + 15 : max_kv;
+  const double tiles = static_cast<double>(B) * Hkv * static_cast<double>((cols + 15) / 16) * ((seen + 127) / 128);
   if (cols > kStreamCols && tiles > kStreamTiles * sms) return launch_kv_prefill(p, D, max_kv, s);
   return D == 128 ? dispatch_attn<128>(p, max_kv, s) : dispatch_attn<64>(p, max_kv, s);
 }

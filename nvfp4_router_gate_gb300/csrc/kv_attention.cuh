@@ -16,8 +16,8 @@ constexpr float kRescaleAt = 8.0f;
 // Fewest places of a block in the flat order of the tiles.
 constexpr int kMinChunk = 2;
 
-// A key that a chunk border cuts, written by the block of its first chunk: its
-// parts, whether the first lies in its block's second slot, its rows.
+// A key that a chunk border cuts, written by the share (a block's or a team's) that has
+// its first chunk: its parts, whether the first lies in the share's second slot, its rows.
 struct KeyJoin {
   int n_parts, tail;
   int q0, rem0, n_cols;       // the first column is head rem0 of the KV head's at query row q0
@@ -46,8 +46,8 @@ struct AttnParams {
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
-  KeyJoin* joins;             // [blocks]
-  // [2 * blocks][NC m, NC l, NC x D O]: a block's first run is in its slot 0 when it
+  KeyJoin* joins;             // [shares]
+  // [2 * shares][NC m, NC l, NC x D O]: a share's first run is in its slot 0 when it
   // is part of a cut key, its last one in slot 1 unless the key starts the chunk
   float* partials;
 };

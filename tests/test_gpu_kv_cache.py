@@ -504,3 +504,25 @@ def test_wide_tables_extremes(wide):
     test_window_without_end(70)
     test_workspace_is_used_again_by_calls_of_other_shapes()
     test_one_long_sequence_among_short_ones(40, 128)
+
+
+@pytest.mark.parametrize("D,S,window", [(128, 64, 1), (64, 16, 40), (128, 128, 130), (64, 32, 300), (128, 16, 77)])
+def test_windows_of_many_columns(D, S, window):
+    rng = np.random.default_rng(90 + window)
+    n_q = [220, 150, 1, 64, 0, 200]
+    lens = [220, 700, 500, 64, 33, 130]                                # the last has more queries than tokens
+    C = Cached(rng, lens, 4, D, S)
+    table = C.table.copy()
+    table[1, :(700 - 150 + 1 - window) // S] = -1                      # pages in front of every window
+    C.args = (_dev(table), C.args[1])
+    q, q32 = _queries(rng, sum(n_q), 32, D)
+    out, lse = C.run(q, cu_q=_dev(np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)), max_q=max(n_q), window=window)
+    at = 0
+    for b, m in enumerate(n_q):
+        for i in sorted({0, 1, m // 2, m - 2, m - 1} & set(range(m))):
+            n = lens[b] - m + 1 + i                                    # what a query at this place may see
+            kk, vv = C.k[b][:max(n, 0)], C.v[b][:max(n, 0)]
+            ref = K.attention(q32[at + i:at + i + 1].astype(np.float64), kk, vv, D ** -0.5, window=window)
+            vmax = np.abs(C.v[b]).max()
+            assert K.check_attention(out[at + i:at + i + 1], lse[at + i:at + i + 1], ref, max(n, 0), vmax) == (0, 0), (b, i)
+        at += m
