@@ -79,7 +79,7 @@ struct alignas(16) Meta {
   int kv, n_q, q0, iq0, rem0, n_cols;   // the first column is head rem0 of the group's query iq0
   float k_gsa, v_gsa;
   int slot;                   // of the run's partial results
-  int pad;
+  int lo, hi;                 // the tokens that some column sees
 };
 // a run's first and last tile; a tile that some column does not see whole; the
 // run is all of its key; the team's last run
@@ -125,7 +125,7 @@ kv_attention_kernel(const AttnParams p) {
   using Sh = AttnShape<D, NT, NW, MW, STAGES>;
   constexpr int TILE = Sh::kTile, NC = Sh::kCols, SH = Sh::kShare;
   static_assert(D == 64 || D == 128, "the fragment loads are written for these");
-  static_assert(TILE <= 256 && 32 * NW >= D && Sh::kStageBytes % 128 == 0, "tile plan");
+  static_assert(TILE <= 256 && MW == 2 && 32 * NW >= D && Sh::kStageBytes % 128 == 0, "tile plan");
   constexpr int KS = D / 16;                                 // steps of the first product
   constexpr int MT = D / 16;                                 // channel tiles of the second
   extern __shared__ uint8_t smem_raw[];
@@ -262,7 +262,7 @@ kv_attention_kernel(const AttnParams p) {
           m.head = head; m.tile = g.tile0 + ti;
           const int key_f0 = f - ti, key_end = key_f0 + g.tiles;
           m.kv = g.kv; m.n_q = g.n_q; m.q0 = g.q0; m.iq0 = iq0; m.rem0 = rem0; m.n_cols = g.n_cols;
-          m.k_gsa = k_gsa; m.v_gsa = v_gsa;
+          m.k_gsa = k_gsa; m.v_gsa = v_gsa; m.lo = g.lo; m.hi = g.hi;
           // slot 0 when the key's run starts with the chunk, else 1 (it ends it)
           m.slot = 2 * share + (key_f0 > f0);
           const uint32_t each = (1u << (part / 16)) - 1;
@@ -409,6 +409,20 @@ kv_attention_kernel(const AttnParams p) {
     const uint8_t* stage = smem + st * Sh::kStageBytes;
     const uint32_t live = (meta.live >> (warp * MW)) & ((1u << MW) - 1u);
     if (live) {
+      if (flags & kEdge) {
+        // The weight of a token that no column sees is 0, its value's scale must not be
+        // a NaN (stale memory, a page given back, anything): lane i zeroes that of the
+        // warp's token i.
+        const int t = meta.tile * TILE + warp * MW * 16 + lane;
+        if (t < meta.lo || t >= meta.hi || !((live >> (lane / 16)) & 1u)) {
+          uint8_t* at = smem + st * Sh::kStageBytes + KvPage<D>::value_scales(TILE) +
+                        KvPage<D>::value_scale(warp * MW * 16 + lane, 0);
+#pragma unroll
+          for (int b = 0; b < D / 16; ++b) at[KvPage<D>::value_scale(0, b)] = 0;
+          fence_proxy_async_smem();                          // (the next copy into the stage comes after)
+        }
+        __syncwarp();
+      }
       // --------------------------------------- S^T = K Q^T, MW times 16 tokens
       float s[MW][NT][4], s1[MW][NT][4];                     // even and odd steps: two chains of products
       uint32_t kc[MW][2][D / 32];                            // codes of tokens r, r + 8
@@ -559,12 +573,6 @@ kv_attention_kernel(const AttnParams p) {
           const int tok = 16 * u + 8 * i;
           sv[i] = e4m3x2_to_f16(
               *reinterpret_cast<const uint16_t*>(stage + KvPage<D>::value_scales(TILE) + v_scales_at + tok * (D / 16)));
-          if (flags & kEdge) {
-            // a masked token's weight is 0; its scale must not be a NaN
-            const int tv = meta.tile * TILE + warp * MW * 16 + tok + 2 * c, kv = meta.kv;
-            if (tv >= kv || !((live >> u) & 1u)) sv[i] = 0;
-            else if (tv + 1 >= kv) sv[i] &= 0xFFFFu;
-          }
           const uint8_t* vc = stage + KvPage<D>::value_codes(TILE) + v_codes_at + tok * (D / 2);
           uint32_t x[D / 64], y[D / 64];                     // token 2c, token 2c + 1
           if (D == 128) {

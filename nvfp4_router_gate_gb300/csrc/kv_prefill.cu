@@ -503,10 +503,11 @@ kv_prefill_kernel(const AttnParams p) {
           uint2 kc[4][BL], vc[4][BL];
           uint32_t ks[4], vs[4][BL], k_mask[4], v_mask[4];
           // A half without its page reads the first page of the cache, under scales
-          // of zero; so do tokens past the sequence's length (whatever their bytes).
+          // of zero; so do the values of tokens outside [lo, hi), which no column sees
+          // (whatever their bytes: a NaN scale would pass through a weight of zero).
           const uint8_t* head_at = p.cache + static_cast<int64_t>(run.head) * KvPage<D>::bytes(S);
           const uint8_t* base[2];                          // this head in the pages of the warp's two halves
-          int limit[2];                                    // the tokens of a half below this have scales
+          int limit[2];                                    // the tokens of a half from run.lo to this have scales
           int at = -1, entries = -1;
           // the pages of a tile; which are in the cache
           auto find = [&](int tile) {
@@ -519,16 +520,16 @@ kv_prefill_kernel(const AttnParams p) {
             int page = __shfl_sync(0xFFFFFFFFu, entries, e);
             bool ok = page >= 0 && page < p.n_pages;
             uint32_t live = ok ? 3u : 0u;
-            ok = ok && t < run.hi && t + 32 > run.lo;
+            ok = ok && t < run.hi && t + (one_page ? 32 : 16) > run.lo;
             base[0] = base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
-            limit[0] = limit[1] = ok ? run.kv : 0;
+            limit[0] = limit[1] = ok ? run.hi : 0;
             if (!one_page) {                               // pages of 16: the second half's is the next
               page = __shfl_sync(0xFFFFFFFFu, entries, e + 1);
               ok = page >= 0 && page < p.n_pages;
               live = (live & 1u) | (ok ? 2u : 0u);
               ok = ok && t + 16 < run.hi && t + 32 > run.lo;
               base[1] = head_at + static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_stride;
-              limit[1] = ok ? run.kv : 0;
+              limit[1] = ok ? run.hi : 0;
             }
             return live;
           };
@@ -567,7 +568,7 @@ kv_prefill_kernel(const AttnParams p) {
                   vc[2 * h + i][x] = __ldg(reinterpret_cast<const uint2*>(c + i * 8 * (D / 2) + 64 * x));
                   vs[2 * h + i][x] = __ldg(s + i * 8 * (D / 16) + 8 * x);
                 }
-                v_mask[2 * h + i] = t + 8 * i < limit[h] ? 0xFFFFu : 0u;
+                v_mask[2 * h + i] = t + 8 * i < limit[h] && t + 8 * i >= run.lo ? 0xFFFFu : 0u;
               }
             }
           };

@@ -1,0 +1,70 @@
+"""What the key/value cache's calls promise beside their values: which bytes
+may reach a result, rows that no sequence covers, streams, workspaces and the
+buffers of an Nvfp4KVCache."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+from oracle import kv_cache as K  # noqa: E402
+from test_gpu_kv_cache import Cached, _dev, _queries  # noqa: E402
+
+
+class Wide(Cached):
+    """Its page tables are wide: calls of more than 32 columns without a window take the tensor-memory kernel."""
+    pad = 4096
+
+
+def _takes_tensor_memory(B, H, cols, tokens):
+    """The size rule of csrc/kv_attention.cu for calls of more than 32 columns: tokens is the tables' width, or the
+    window and 15 more."""
+    tiles = B * H * -(-cols // 16) * -(-tokens // 128)
+    return cols > 32 and tiles > 6 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _overwrite(C, b, tokens, byte, keys=True):
+    """Bytes of tokens of sequence b (their codes and scales) in the cache."""
+    host = C.cache.cpu().numpy()
+    n, H, D = len(tokens), C.H, C.D
+    slots = C.table[b, tokens // C.S] * C.S + tokens % C.S
+    if not keys:
+        kc, ks = _entry_bytes(host, slots, C.S, D)
+    else:
+        kc, ks = np.full((n, H, D // 2), byte, np.uint8), np.full((n, H, D // 16), byte, np.uint8)
+    K.store(host, slots, kc, ks, np.full((n, H, D // 2), byte, np.uint8), np.full((n, H, D // 16), byte, np.uint8), C.S)
+    C.cache = _dev(host)
+
+
+def _entry_bytes(host, slots, S, D):
+    """Key codes and scales as they lie in the cache."""
+    at = K.region_offsets(S, D)[0]
+    page = host[slots // S]
+    t = (slots % S)[:, None, None]
+    row, head = np.arange(len(slots))[:, None, None], np.arange(host.shape[1])[None, :, None]
+    return (page[row, head, t * (D // 2) + np.arange(D // 2)], page[row, head, at + t * (D // 16) + np.arange(D // 16)])
+
+
+# m queries a sequence, KV heads, heads of each: one query and a few through the
+# streaming kernel, many columns through the tensor-memory kernel
+FORMS = [(1, 2, 8), (5, 1, 3), (40, 8, 16)]
+
+
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+@pytest.mark.parametrize("D,S", [(128, 16), (128, 32), (64, 16), (64, 64), (128, 128)])
+@pytest.mark.parametrize("m,H,G", FORMS)
+def test_bytes_before_the_window_do_not_reach_the_output(m, H, G, D, S, byte):
+    """Every token in front of the first query's window holds NaN scales, its page's id still in the table."""
+    rng = np.random.default_rng(100 + m + S + D)
+    window = 100
+    lens = [window + m - 1 + n for n in (5, 18, 300, 411)]             # the windows start at 5, 18, 300 and 411
+    if m == 40:
+        assert _takes_tensor_memory(len(lens), H, m * G, window + 15)
+    C = Cached(rng, lens, H, D, S)
+    for b, n in enumerate(lens):
+        _overwrite(C, b, np.arange(n - m + 1 - window), byte)
+    q, q32 = _queries(rng, m * len(lens), H * G, D)
+    out, lse = C.run(q, window=window)
+    C.check(q32, [m] * len(lens), out, lse, window=window, rows=4)
