@@ -105,10 +105,10 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  *   out          out [T, Hq, D] bf16, 16-byte aligned
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    nvfp4_kv_attention_workspace_size(...) bytes, zeroed once
- * A query that sees no token gets zeros and lse = -inf.  What the cache holds
- * of tokens that no query sees (any bytes: past the length, in front of the
- * first window, in the same page as seen ones or not) does not reach the output.
- * Hq is a
+ * A query that sees no token gets zeros and lse = -inf, one with a NaN among its
+ * channels NaNs in both.  What the cache holds of tokens that no query sees (any
+ * bytes: past the length, in front of the first window, in the same page as seen
+ * ones or not) does not reach the output.  Hq is a
  * multiple of Hkv.  Scores, softmax statistics and outputs are accumulated in
  * fp32; the weights p_t enter the second product as fp16, relative to a running
  * maximum; results do not depend on the order in which the GPU runs the

@@ -707,14 +707,14 @@ kv_attention_kernel(const AttnParams p) {
         }
         const int dq = div_G(rem0 + n);
         const int64_t row = static_cast<int64_t>(q0 + dq) * p.Hq + head * p.G + (rem0 + n - dq * p.G);
-        const float inv = sum[i] > 0.0f ? __fdividef(v_gsa, sum[i]) : 0.0f;
+        const float inv = out_factor(v_gsa, sum[i]);
 #pragma unroll
         for (int x = 0; x < SH / 2; x += 2) {
           const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * x + i] * inv, v[2 * x + 2 + i] * inv);
           *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + ch + x) = y;
         }
         if (p.lse && r == 0 && warp == 0)
-          p.lse[row] = sum[i] > 0.0f ? (top[i] + log2f(sum[i])) * 0.693147180559945309f : -INFINITY;
+          p.lse[row] = lse_of(top[i], sum[i]);
       }
     }
   }

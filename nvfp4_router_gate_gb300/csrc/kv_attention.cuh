@@ -120,6 +120,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return d;
 }
 
+// What a row's result is multiplied by, and its lse: a row that sees no token has a sum
+// of 0 (zeros and -inf), one with a NaN among its scores a NaN, which both keep.
+__device__ __forceinline__ float out_factor(float v_gsa, float sum) {
+  return sum == 0.0f ? 0.0f : __fdividef(v_gsa, sum);
+}
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+}
+
 // x / G for the small numerators of a group (below 2^17, G at most 2^16):
 // exact in fp32, the quotient's distance from an integer is at least 1 / (2 G).
 __device__ __forceinline__ int div_small(int x, float inv_G) {

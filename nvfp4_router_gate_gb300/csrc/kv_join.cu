@@ -42,10 +42,6 @@ __device__ __forceinline__ void store_channels(__nv_bfloat16* dst, const float (
     *reinterpret_cast<__nv_bfloat162*>(dst + x) = __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
 }
 
-__device__ __forceinline__ float lse_of(float top, float sum) {
-  return sum > 0.0f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
-}
-
 // Part i of a key is in the first slot of its block, but the key's first one if the
 // key starts inside the chunk.
 __device__ __forceinline__ const float* part_of(const float* partials, const KeyJoin& k, int i, size_t slot) {
@@ -128,7 +124,7 @@ kv_join_few_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__ 
   for (int r = 0; r < R; ++r) {
     const float s = __shfl_sync(0xFFFFFFFFu, sum, r * P);
     if (n0 + r < k.n_cols)
-      store_channels<CH>(out + out_row(k, n0 + r, Hq, G) * D + lane * CH, acc[r], s > 0.0f ? __fdividef(k.v_gsa, s) : 0.0f);
+      store_channels<CH>(out + out_row(k, n0 + r, Hq, G) * D + lane * CH, acc[r], out_factor(k.v_gsa, s));
   }
   if (lse && lane % P == 0 && mine < k.n_cols) lse[out_row(k, mine, Hq, G)] = lse_of(top, sum);
 }
@@ -207,7 +203,7 @@ kv_join_many_kernel(const KeyJoin* __restrict__ joins, const float* __restrict__
       for (int x = 0; x < CH; ++x) acc[x] += w * s_acc[i][lane][x];
     }
     const int64_t row = out_row(k, n, Hq, G);
-    store_channels<CH>(out + row * D + lane * CH, acc, sum > 0.0f ? __fdividef(k.v_gsa, sum) : 0.0f);
+    store_channels<CH>(out + row * D + lane * CH, acc, out_factor(k.v_gsa, sum));
     if (lse && lane == 0) lse[row] = lse_of(top, sum);
   }
 }

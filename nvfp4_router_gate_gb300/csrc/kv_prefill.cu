@@ -882,7 +882,7 @@ kv_prefill_kernel(const AttnParams p) {
         if (run.dual || w == 0) {
           const bool whole = run.whole;
           float* part = p.partials + static_cast<size_t>(run.slot) * NC * (D + 2);
-          const float inv = l > 0.0f ? __fdividef(run.v_gsa, l) : 0.0f;
+          const float inv = out_factor(run.v_gsa, l);
           // 128 bytes of each row at a time through shared memory, so that the warp
           // stores whole lines; 16-byte vectors are swizzled by the row
           uint8_t* rows_at = smem + Sm::kOut + warp * 32 * 128;
@@ -949,8 +949,7 @@ kv_prefill_kernel(const AttnParams p) {
             if (lane == 0) mbar_arrive(x_free);
           }
           if (whole) {
-            if (on && p.lse)
-              p.lse[out_row(run)] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            if (on && p.lse) p.lse[out_row(run)] = lse_of(m, l);
           } else if (on) {
             part[col] = m;
             part[NC + col] = l;

@@ -68,3 +68,19 @@ def test_bytes_before_the_window_do_not_reach_the_output(m, H, G, D, S, byte):
     q, q32 = _queries(rng, m * len(lens), H * G, D)
     out, lse = C.run(q, window=window)
     C.check(q32, [m] * len(lens), out, lse, window=window, rows=4)
+
+
+@pytest.mark.parametrize("form", [(Cached, [90, 40], 1), (Cached, [20000, 3], 1), (Wide, [600, 64], 40)],
+                         ids=["one", "many_parts", "many_columns"])
+def test_nan_queries_have_a_nan_lse(form):
+    kind, lens, m = form
+    rng = np.random.default_rng(150 + m)
+    C = kind(rng, lens, 1, 128, 64)
+    q, q32 = _queries(rng, 2 * m, 8, 128)
+    bad = (m // 2, 3)                                                  # (query, head) of the first sequence
+    q[bad[0], bad[1], 17] = float("nan")
+    out, lse = C.run(q)
+    assert np.isnan(out[bad]).all() and np.isnan(lse[bad])
+    assert np.count_nonzero(np.isnan(lse)) == 1 and np.count_nonzero(np.isnan(out).any(axis=-1)) == 1
+    ref = K.attention(q32[m:].astype(np.float64), C.k[1], C.v[1], 128 ** -0.5)
+    assert K.check_attention(out[m:], lse[m:], ref, lens[1], np.abs(C.v[1]).max()) == (0, 0)
