@@ -108,8 +108,8 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  * A query that sees no token gets zeros and lse = -inf, one with a NaN among its
  * channels NaNs in both.  What the cache holds of tokens that no query sees (any
  * bytes: past the length, in front of the first window, in the same page as seen
- * ones or not) does not reach the output.  Hq is a
- * multiple of Hkv.  Scores, softmax statistics and outputs are accumulated in
+ * ones or not) does not reach the output; a NaN in a key's or value's scales reaches
+ * the queries that see the token, no others.  Hq is a multiple of Hkv.  Scores, softmax statistics and outputs are accumulated in
  * fp32; the weights p_t enter the second product as fp16, relative to a running
  * maximum; results do not depend on the order in which the GPU runs the
  * blocks.  One kernel and, unless no key can be cut over blocks, a second one that

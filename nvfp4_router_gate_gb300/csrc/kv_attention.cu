@@ -85,6 +85,9 @@ struct alignas(16) Meta {
 // run is all of its key; the team's last run
 constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4, kWhole = 8, kDone = 16;
 
+// Byte i is 0xFF where bit i of the low four is set.
+__device__ __forceinline__ uint32_t bytes_of(uint32_t bits) { return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu; }
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -351,6 +354,12 @@ kv_attention_kernel(const AttnParams p) {
   };
   const float inv_G = 1.0f / static_cast<float>(p.G);
   auto div_G = [&](int x) { return div_small(x, inv_G); };
+  // the tokens [lo, hi) that column n sees
+  auto sees = [&](const Meta& meta, int n, int& lo, int& hi) {
+    const int pos = meta.kv - meta.n_q + meta.iq0 + div_G(meta.rem0 + min(n, meta.n_cols - 1));
+    hi = n >= meta.n_cols ? 0 : p.causal ? pos + 1 : meta.kv;
+    lo = p.window > 0 ? pos + 1 - p.window : 0;
+  };
   uint32_t joined = 1;
   int st = 0;
   uint32_t parity = 0;
@@ -410,16 +419,36 @@ kv_attention_kernel(const AttnParams p) {
     const uint32_t live = (meta.live >> (warp * MW)) & ((1u << MW) - 1u);
     if (live) {
       if (flags & kEdge) {
-        // The weight of a token that no column sees is 0, its value's scale must not be
-        // a NaN (stale memory, a page given back, anything): lane i zeroes that of the
-        // warp's token i.
-        const int t = meta.tile * TILE + warp * MW * 16 + lane;
-        if (t < meta.lo || t >= meta.hi || !((live >> (lane / 16)) & 1u)) {
-          uint8_t* at = smem + st * Sh::kStageBytes + KvPage<D>::value_scales(TILE) +
-                        KvPage<D>::value_scale(warp * MW * 16 + lane, 0);
-#pragma unroll
-          for (int b = 0; b < D / 16; ++b) at[KvPage<D>::value_scale(0, b)] = 0;
+        // The weight of a token that a column does not see is 0, its value's scale must
+        // not be a NaN.  A lane looks after the eight scales of one channel block of
+        // tokens tg .. tg + 7: those of tokens that no column sees (stale memory, a page
+        // given back, anything) become zero, and so do NaNs, which go straight to the
+        // columns that do see their token.
+        const int t0 = meta.tile * TILE + warp * MW * 16, in = lane / (D / 16) * 8, tg = t0 + in;
+        uint32_t bad = 0;                                    // tokens of the warp's with a NaN
+        if (in < 32) {
+          uint2* at = reinterpret_cast<uint2*>(smem + st * Sh::kStageBytes + KvPage<D>::value_scales(TILE) +
+                                               KvPage<D>::value_scale(warp * MW * 16 + in, lane % (D / 16)));
+          const uint32_t see = (live >> (in / 16)) & 1u ? tokens32(tg, meta.lo, meta.hi) : 0u;
+          const uint2 x = *at;
+          const uint32_t s0 = bytes_of(see), s1 = bytes_of(see >> 4);
+          const uint32_t n0 = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s0, n1 = __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s1;
+          *at = make_uint2(x.x & s0 & ~n0, x.y & s1 & ~n1);
           fence_proxy_async_smem();                          // (the next copy into the stage comes after)
+          if (n0 | n1) bad = ((((n0 & 0x01010101u) * 0x10204080u) >> 28) | (((n1 & 0x01010101u) * 0x10204080u) >> 28) << 4) << in;
+        }
+        bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+        if (bad) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              int lo, hi;
+              sees(meta, 8 * nt + 2 * c + i, lo, hi);
+              if (!(bad & tokens32(t0, lo, hi))) continue;
+#pragma unroll
+              for (int j = 0; j < MT; ++j) o[nt][j][i] = o[nt][j][i + 2] = NAN;
+            }
         }
         __syncwarp();
       }
@@ -485,16 +514,12 @@ kv_attention_kernel(const AttnParams p) {
         if (flags & kEdge) {
           // token of v[0][.][0..1]; t + 8: v[0][.][2..3]
           const int t = meta.tile * TILE + warp * MW * 16 + r;
-          const int n_cols = meta.n_cols, kv = meta.kv, first = kv - meta.n_q + meta.iq0, rem0 = meta.rem0;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              // the tokens [lo, hi) that the column sees
-              const int n = 8 * nt + 2 * c + i;
-              const int pos = first + div_G(rem0 + min(n, n_cols - 1));
-              const int hi = n >= n_cols ? 0 : p.causal ? pos + 1 : kv;
-              const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+              int lo, hi;
+              sees(meta, 8 * nt + 2 * c + i, lo, hi);
 #pragma unroll
               for (int u = 0; u < MW; ++u)
 #pragma unroll

@@ -129,6 +129,12 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
   return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
 }
 
+// Bit i: token t + i is in [lo, hi).
+__device__ __forceinline__ uint32_t tokens32(int t, int lo, int hi) {
+  const int a = min(max(lo - t, 0), 32), b = min(max(hi - t, 0), 32);
+  return (a < 32 ? 0xFFFFFFFFu << a : 0u) & (b > 0 ? 0xFFFFFFFFu >> (32 - b) : 0u);
+}
+
 // x / G for the small numerators of a group (below 2^17, G at most 2^16):
 // exact in fp32, the quotient's distance from an integer is at least 1 / (2 G).
 __device__ __forceinline__ int div_small(int x, float inv_G) {

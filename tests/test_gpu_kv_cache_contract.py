@@ -70,6 +70,36 @@ def test_bytes_before_the_window_do_not_reach_the_output(m, H, G, D, S, byte):
     C.check(q32, [m] * len(lens), out, lse, window=window, rows=4)
 
 
+@pytest.mark.parametrize("D,S,window", [(128, 64, 0), (64, 16, 0), (128, 16, 33), (64, 128, 50)])
+@pytest.mark.parametrize("m,H,G", FORMS[1:])
+def test_a_nan_value_reaches_the_queries_that_see_it(m, H, G, D, S, window):
+    """One value of a sequence has NaN scales: queries that see it get NaNs, the others what they get without it."""
+    rng = np.random.default_rng(130 + m + S)
+    lens = [m, 150, 290, 333]
+    C = (Wide if window == 0 else Cached)(rng, lens, H, D, S)
+    if m == 40:
+        assert _takes_tensor_memory(len(lens), H, m * G, window + 15 if window else C.table.shape[1] * S)
+    back = [m // 2, 2, m - 1, m // 3 + (window if window else 0)]     # tokens behind the newest
+    for b, n in enumerate(lens):
+        _overwrite(C, b, np.array([n - 1 - back[b]]), 0x7F, keys=False)
+    q, q32 = _queries(rng, m * len(lens), H * G, D)
+    out, lse = C.run(q, window=window)
+    blind = 0
+    for b, n in enumerate(lens):
+        for i in range(m):
+            pos, t, row = n - m + i, n - 1 - back[b], b * m + i
+            sees = t <= pos and (not window or t > pos - window)
+            blind += not sees
+            assert np.isnan(out[row]).all() if sees else np.isfinite(out[row]).all(), (b, i)
+            if 2 < i < m - 3 and i % 7:
+                continue
+            ref = K.attention(q32[row:row + 1].astype(np.float64), C.k[b][:pos + 1], C.v[b][:pos + 1], D ** -0.5,
+                              window=window)
+            got = ref[0] if sees else out[row:row + 1]                 # the lse is that of the scores
+            assert K.check_attention(got, lse[row:row + 1], ref, pos + 1, np.abs(C.v[b]).max()) == (0, 0), (b, i)
+    assert blind > 0
+
+
 @pytest.mark.parametrize("form", [(Cached, [90, 40], 1), (Cached, [20000, 3], 1), (Wide, [600, 64], 40)],
                          ids=["one", "many_parts", "many_columns"])
 def test_nan_queries_have_a_nan_lse(form):
