@@ -5,14 +5,15 @@
 // accumulators leave registers for.
 //
 // Mathematics.  For a column's query q and its visible tokens t
-//   s_t = scale * q . k_t,  m = max s_t,  p_t = exp(s_t - m),
+//   s_t = scale * q . k_t,  m = max s_t - 7 ln 2,  p_t = exp(s_t - m),
 //   out = sum p_t v_t / sum p_t,  lse = m + log sum p_t,
 // in one pass: a running m, l = sum p and O = sum p v, rescaled when m moves;
 // partial (m, l, O) triples of disjoint token sets join by the same rescaling.
-// m is only moved when a score passes it by more than 8 (base 2): p_t stays
-// below 2^8, inside fp16 (the one rounding below 32 bits: the second product's
-// operands are fp16, their errors 2^-11 of each weight), and most tiles skip the
-// rescaling.
+// m is only moved when a weight passes 2^15 (a score the largest one so far by 8,
+// base 2), so that most tiles skip the rescaling.  The one rounding below 32 bits: the
+// second product's operands are fp16, the errors 2^-11 of each weight and 2^-25 below
+// the normal range, which is 2^-32 of the largest weight (m 7 above that: 2^-25, and
+// 131072 tokens beside a dominant one could lose 2^-8 of the result).
 //
 // Both products run transposed, S^T = K Q^T and O^T = V^T P^T: the tokens
 // (resp. channels) are the 16 rows of the matrix instruction and the columns
@@ -544,8 +545,8 @@ kv_attention_kernel(const AttnParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) high = fmaxf(high, v[u][nt][i]);
-      if (__any_sync(0xFFFFFFFFu, high > kRescaleAt)) {
-        // move m to the largest score so far
+      if (__any_sync(0xFFFFFFFFu, high > kMostWeight)) {
+        // set m by the largest score so far
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -560,7 +561,7 @@ kv_attention_kernel(const AttnParams p) {
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            const float now = fminf(m_neg[nt][i], -top);
+            const float now = fminf(m_neg[nt][i], kLift - top);
             const float shrink = now < m_neg[nt][i] ? ex2(now - m_neg[nt][i]) : 1.0f;   // ex2(-inf) = 0
             m_neg[nt][i] = now;
             l_run[nt][i] *= shrink;

@@ -9,9 +9,12 @@
 
 namespace nvr {
 
-// The running maximum of a row moves when a score passes it by this much (base
-// 2): the softmax weights stay below 2^8, inside fp16.
-constexpr float kRescaleAt = 8.0f;
+// A row's weights are 2^(s - m) with m set to its largest score less kLift (base 2), and
+// set again when one passes 2^kMostWeight: between those of the largest score at the
+// upper end of fp16 (2^16) and the smallest that its subnormals hold lie 2^32, so that
+// the many small weights beside a dominant token still count.
+constexpr float kLift = 7.0f;
+constexpr float kMostWeight = 15.0f;
 
 // Fewest places of a block in the flat order of the tiles.
 constexpr int kMinChunk = 2;

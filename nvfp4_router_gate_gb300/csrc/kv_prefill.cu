@@ -63,7 +63,7 @@ constexpr int kPKeyCost = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;                   // tiles whose live tokens are kept: expanded at most three ahead
 constexpr int kAhead = 6;                  // tiles fetched into L2 before they are expanded
-constexpr float kMostSum = 256.0f;         // 2^kRescaleAt
+constexpr float kMostSum = 32768.0f;       // 2^kMostWeight
 
 // A key's stretch of tiles in this block's chunk.
 struct alignas(16) Run {
@@ -783,12 +783,13 @@ kv_prefill_kernel(const AttnParams p) {
               }
               sum = f2_lo(sum2) + f2_hi(sum2);
             };
-            // Weights that add up to more than 2^kRescaleAt hold a score far above m
-            // (a weight above 4, at least): no maximum is taken of the others.  (m at
-            // or above every score: at most 64 weights of 1.)
+            // Weights that add up to more than 2^kMostWeight hold a score far above the
+            // largest that m was set by (a weight above 4 times its 2^kLift, at least): no
+            // maximum is taken of the others.  (No score above it: at most 64 weights of
+            // 2^kLift.)
             for (bool move = i == 0 && c0 == 0;; move = true) {
               if (move) {
-                // m moves to the largest score so far, this half's included
+                // m is set by the largest score so far, this half's included
                 float top = -INFINITY;
 #pragma unroll 1
                 for (int c = c0; c < c0 + kPTile / 2; c += 32) {
@@ -800,7 +801,7 @@ kv_prefill_kernel(const AttnParams p) {
                   for (int x = 0; x < 32; ++x)
                     top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
                 }
-                const float now = fminf(m_neg, -top);
+                const float now = fminf(m_neg, kLift - top);
                 const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
                 m_neg = now;
                 l *= shrink;

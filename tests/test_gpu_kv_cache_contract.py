@@ -114,3 +114,30 @@ def test_nan_queries_have_a_nan_lse(form):
     assert np.count_nonzero(np.isnan(lse)) == 1 and np.count_nonzero(np.isnan(out).any(axis=-1)) == 1
     ref = K.attention(q32[m:].astype(np.float64), C.k[1], C.v[1], 128 ** -0.5)
     assert K.check_attention(out[m:], lse[m:], ref, lens[1], np.abs(C.v[1]).max()) == (0, 0)
+
+
+@pytest.mark.parametrize("kind,n,m", [(Cached, 20000, 1), (Cached, 900, 3), (Wide, 3000, 40)])
+def test_tokens_beside_a_dominant_one(kind, n, m):
+    """A first token of weight 1, whose value is 0, beside many of weight about 2^-27 each.
+
+    Tolerance: the oracle's, but for the absolute rounding of the fp16 weights: 2^-25 a token below the normal
+    range, relative to a largest weight of at least 2^7: n 2^-32 v_max."""
+    rng = np.random.default_rng(160 + m)
+    C = kind(rng, [n], 1, 128, 64)
+    k, v = np.zeros((n, 1, 128), np.float32), np.full((n, 1, 128), 0.5, np.float32)
+    k[0, :, 0], v[0] = 27 * np.log(2.0) / 8, 0.0
+    (kc, ks), (vc, vs) = K.entry(k, C.kg), K.entry(v, C.vg)
+    slots = C.table[0, np.arange(n) // 64] * 64 + np.arange(n) % 64
+    host = K.store(C.cache.cpu().numpy(), slots, kc, ks, vc, vs, 64)
+    C.cache = _dev(host)
+    k, v = K.load(host, slots, 64, 128, C.kg, C.vg)
+    q32 = np.zeros((m, 4, 128), np.float32)
+    q32[..., 0] = 8.0
+    out, lse = C.run(_dev(q32).to(torch.bfloat16), scale=1.0)
+    o, z, mag, big = K.attention(q32.astype(np.float64), k, v, 1.0)
+    assert 2.0 ** -29 * n < np.abs(o[-1]).max() < 2.0 ** -26 * n
+    e = 2.0 * 2.0 ** -16 * big + 2.0 ** -20
+    tol = mag * (2 * e + 2.0 ** -11 + n * 2.0 ** -23)[..., None] + n * 2.0 ** -32 * np.abs(v).max()
+    tol = tol + 2.0 ** -8 * (np.abs(o) + tol)
+    assert (np.abs(out - o) <= tol).all(), (out.ravel()[:4], o.ravel()[:4])
+    assert (np.abs(lse - z) <= e + n * 2.0 ** -24 + np.abs(z) * 2.0 ** -21).all()
