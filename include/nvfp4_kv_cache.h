@@ -101,7 +101,10 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  *   kv_lens      [B] int32, taken within [0, max_pages * page_size]
  *   cu_q         [B + 1] int32: sequence b's queries are rows
  *                cu_q[b]..cu_q[b + 1] of q, at most max_q of them; or NULL: every
- *                sequence has max_q queries (T == B * max_q)
+ *                sequence has max_q queries (T == B * max_q).  Values are taken within
+ *                [0, T] and must not decrease (else some rows are unspecified).  Rows that
+ *                no sequence covers (in front of the first one, behind the last one, past
+ *                max_q in one) get zeros and lse = -inf.
  *   out          out [T, Hq, D] bf16, 16-byte aligned
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    nvfp4_kv_attention_workspace_size(...) bytes, zeroed once

@@ -204,6 +204,7 @@ kv_attention_kernel(const AttnParams p) {
   }
   __syncthreads();
   if (tid == 32 * NW) p.joins[share].n_parts = 0;            // (until this team turns out to start a cut key)
+  if (p.cu_q && warp < NW) clear_uncovered<D>(p, share * NW + warp, shares * NW);
   if (f0 >= f1 || !s_start[2]) return;
 
   if (warp == NW) {

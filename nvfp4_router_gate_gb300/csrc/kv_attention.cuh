@@ -98,6 +98,39 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
   return g;
 }
 
+// Zeros, and an lse of -inf, for the rows that no sequence covers: in front of the first
+// one, behind the last one (a batch padded for a captured graph), past max_q in one.  By
+// the warps `unit` of `units`, while the first loads of the work are under way.
+template <int D>
+__device__ __forceinline__ void clear_uncovered(const AttnParams& p, int unit, int units) {
+  const int lane = threadIdx.x & 31, T = static_cast<int>(p.T);
+  auto row_of = [&](int b) { return min(max(__ldg(p.cu_q + b), 0), T); };
+  auto clear = [&](int64_t from, int64_t to, int step) {
+#pragma unroll 1
+    for (int64_t r = from; r < to; r += step) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + r * p.Hq * D);
+#pragma unroll 1
+      for (int i = lane; i < p.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!p.lse) continue;
+#pragma unroll 1
+      for (int i = lane; i < p.Hq; i += 32) p.lse[r * p.Hq + i] = -INFINITY;
+    }
+  };
+  const int first = row_of(0), last = row_of(p.B);
+  clear(unit, first, units);
+  clear(static_cast<int64_t>(last) + unit, T, units);
+#pragma unroll 1
+  for (int64_t b0 = static_cast<int64_t>(unit) * 32; b0 < p.B; b0 += static_cast<int64_t>(units) * 32) {
+    const int b = static_cast<int>(min(b0 + lane, static_cast<int64_t>(p.B - 1))), a = row_of(b), e = row_of(b + 1);
+    uint32_t over = __ballot_sync(0xFFFFFFFFu, b0 + lane < p.B && e - a > p.max_q);
+#pragma unroll 1
+    for (; over; over &= over - 1) {
+      const int l = __ffs(over) - 1;
+      clear(static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, a, l)) + p.max_q, __shfl_sync(0xFFFFFFFFu, e, l), 1);
+    }
+  }
+}
+
 // Waits for a phase of the barrier, about a second at most: a try that fails
 // takes 4 us on this GPU (measured), and 2^18 of them are made.  A count keeps the
 // wait to a few instructions; there are many waits, and the kernels' rarely run

@@ -253,6 +253,7 @@ kv_prefill_kernel(const AttnParams p) {
   };
 
   if (tid == 13 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
+  if (p.cu_q && warp < 8) clear_uncovered<D>(p, blockIdx.x * 8 + warp, gridDim.x * 8);
   if (f0 < f1) {
     int n_taken = 0;
     Run run;

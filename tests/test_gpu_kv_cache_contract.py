@@ -141,3 +141,22 @@ def test_tokens_beside_a_dominant_one(kind, n, m):
     tol = tol + 2.0 ** -8 * (np.abs(o) + tol)
     assert (np.abs(out - o) <= tol).all(), (out.ravel()[:4], o.ravel()[:4])
     assert (np.abs(lse - z) <= e + n * 2.0 ** -24 + np.abs(z) * 2.0 ** -21).all()
+
+
+# ------------------------------------------------------- rows of sequences
+
+@pytest.mark.parametrize("kind", [Cached, Wide])
+def test_rows_that_no_sequence_covers_are_zero(kind):
+    """In front of the first sequence, between the last one and T (a batch padded for a captured graph)."""
+    rng = np.random.default_rng(170)
+    lens = [50, 0, 333]
+    C = kind(rng, lens, 2, 128, 32)
+    cu = np.array([3, 10, 10, 15], np.int32)
+    T = 700
+    q, q32 = _queries(rng, T, 16, 128)
+    out = torch.full((T, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = C.run(q, cu_q=_dev(cu), max_q=8, out=out)
+    covered = np.zeros(T, bool)
+    covered[3:15] = True
+    assert not out[~covered].any() and np.isneginf(lse[~covered]).all()
+    C.check(q32[3:15], [7, 0, 5], out[3:15], lse[3:15])
