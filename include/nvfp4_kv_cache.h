@@ -105,6 +105,8 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  *                [0, T] and must not decrease (else some rows are unspecified).  Rows that
  *                no sequence covers (in front of the first one, behind the last one, past
  *                max_q in one) get zeros and lse = -inf.
+ *                Rows past max_q still count as queries: those in front of them keep
+ *                their positions.
  *   out          out [T, Hq, D] bf16, 16-byte aligned
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    nvfp4_kv_attention_workspace_size(...) bytes, zeroed once

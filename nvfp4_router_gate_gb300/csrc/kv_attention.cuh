@@ -57,7 +57,7 @@ struct AttnParams {
 
 // What the queries and the tokens of a column group are.
 struct Group {
-  int b, q0, n_q, kv;         // sequence, its first query row, its queries, its tokens
+  int b, q0, n_q, kv;         // sequence, its first query row, its queries (max_q of them have columns), its tokens
   int c0, n_cols;             // first column, columns of the group (0: none)
   int lo, hi;                 // tokens any of the columns sees: [lo, hi)
   int tile0, tiles;
@@ -73,13 +73,13 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, int item) {
     const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
     const int64_t e = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b + 1)), a), p.T);
     g.q0 = static_cast<int>(a);
-    g.n_q = static_cast<int>(min(e - a, static_cast<int64_t>(p.max_q)));
+    g.n_q = static_cast<int>(e - a);
   } else {
     g.q0 = g.b * p.max_q;
     g.n_q = p.max_q;
   }
   g.c0 = cg * NC;
-  g.n_cols = min(g.n_q * p.G - g.c0, NC);
+  g.n_cols = min(min(g.n_q, p.max_q) * p.G - g.c0, NC);
   if (g.n_cols <= 0) {
     g.n_cols = 0;
     g.lo = g.hi = g.tile0 = g.tiles = 0;

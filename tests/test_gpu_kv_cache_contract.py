@@ -160,3 +160,21 @@ def test_rows_that_no_sequence_covers_are_zero(kind):
     covered[3:15] = True
     assert not out[~covered].any() and np.isneginf(lse[~covered]).all()
     C.check(q32[3:15], [7, 0, 5], out[3:15], lse[3:15])
+
+
+@pytest.mark.parametrize("kind", [Cached, Wide])
+def test_sequences_of_more_than_max_q_rows_keep_their_positions(kind):
+    rng = np.random.default_rng(171)
+    n_q, most = [10, 5, 20, 6], 6
+    lens = [40, 90, 20, 300]
+    C = kind(rng, lens, 2, 64, 16)
+    cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+    q, q32 = _queries(rng, cu[-1], 16, 64)
+    out = torch.full((cu[-1], 16, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out, lse = C.run(q, cu_q=_dev(cu), max_q=most, out=out)
+    for b, (m, n) in enumerate(zip(n_q, lens)):
+        at, keep = cu[b], min(m, most)
+        ref = K.attention(q32[at:at + m].astype(np.float64), C.k[b], C.v[b], 64 ** -0.5)
+        ref = [x[:keep] for x in ref]
+        assert K.check_attention(out[at:at + keep], lse[at:at + keep], ref, n, np.abs(C.v[b]).max()) == (0, 0), b
+        assert not out[at + keep:at + m].any() and np.isneginf(lse[at + keep:at + m]).all(), b
