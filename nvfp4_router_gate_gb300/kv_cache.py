@@ -210,7 +210,9 @@ class Nvfp4KVCache:
     ``k_gsa`` and ``v_gsa`` are the global scales (a number or [n_kv_heads]
     fp32, max|x| / 2688 of calibration data per head); ``data`` an existing
     [n_pages, n_kv_heads, page_bytes] uint8 cache.  ``n_heads``,
-    ``max_tokens`` and ``max_seqs`` size the attention workspace.
+    ``max_tokens`` and ``max_seqs`` size the attention workspace, which serves
+    one stream at a time: calls of ``attend`` that may run at once each need
+    another one (``workspace=``, zeroed once).
     """
 
     def __init__(self, n_pages, n_kv_heads, head_dim, page_size=64, k_gsa=1.0, v_gsa=1.0, data=None, n_heads=None,
@@ -252,8 +254,8 @@ class Nvfp4KVCache:
             raise ValueError("the cache must be on a GPU")
         return _gather(self._pages, slots, **kw)
 
-    def attend(self, q, page_table, kv_lens, **kw):
-        """nvfp4_kv_attention over this cache."""
+    def attend(self, q, page_table, kv_lens, workspace=None, **kw):
+        """nvfp4_kv_attention over this cache, with its own workspace unless one is given."""
         if q.shape[0] > self.max_tokens or page_table.shape[0] > self.max_seqs or q.shape[1] != self.n_heads:
             raise ValueError("%d tokens of %d heads in %d sequences: the workspace is for %d, %d and %d" % (
                 q.shape[0], q.shape[1], page_table.shape[0], self.max_tokens, self.n_heads, self.max_seqs))
@@ -261,7 +263,8 @@ class Nvfp4KVCache:
             raise TypeError("q must be bfloat16, got %s" % q.dtype)
         if self._pages is None:
             raise ValueError("the cache must be on a GPU")
-        return _attend(self._pages, q, page_table, kv_lens, ws=self._ws, **kw)
+        return _attend(self._pages, q, page_table, kv_lens, workspace=workspace,
+                       ws=self._ws if workspace is None else None, **kw)
 
     def status(self, stream=None):
         """The workspace status word (0 ok, 6: a bounded wait timed out)."""

@@ -178,3 +178,31 @@ def test_sequences_of_more_than_max_q_rows_keep_their_positions(kind):
         ref = [x[:keep] for x in ref]
         assert K.check_attention(out[at:at + keep], lse[at:at + keep], ref, n, np.abs(C.v[b]).max()) == (0, 0), b
         assert not out[at + keep:at + m].any() and np.isneginf(lse[at + keep:at + m]).all(), b
+
+
+# ------------------------------------------------------ the object's buffers
+
+def _object(C, **kw):
+    import nvfp4_router_gate_gb300 as R
+    return R.Nvfp4KVCache(C.cache.shape[0], C.H, C.D, page_size=C.S, k_gsa=_dev(C.kg), v_gsa=_dev(C.vg), data=C.cache, **kw)
+
+
+def _attend(kv, C, q, **kw):
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    out, lse = kv.attend(q, *C.args, lse=lse, **kw)
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy(), lse.cpu().numpy()
+
+
+def test_attend_takes_the_callers_workspace():
+    rng = np.random.default_rng(190)
+    C = Cached(rng, [9000], 1, 128, 64)                                # one key in many parts
+    kv = _object(C, n_heads=8)
+    q, q32 = _queries(rng, 1, 8, 128)
+    mine = torch.zeros_like(kv.workspace)
+    C.check(q32, [1], *_attend(kv, C, q, workspace=mine))
+    assert bool(mine.any()) and not bool(kv.workspace.any())
+    C.check(q32, [1], *_attend(kv, C, q))
+    assert bool(kv.workspace.any())
+    with pytest.raises(Exception, match="workspace"):
+        kv.attend(q, *C.args, workspace=mine[:256])
