@@ -68,9 +68,11 @@ def _heads(t, T, H, D, name):
 
 
 class _Pages:
-    """A cache's geometry and pointers: checked once, used by every call."""
+    """A cache's geometry and pointers (and the tensors behind them): checked
+    once, used by every call."""
 
     def __init__(self, cache, k_gsa, v_gsa, D):
+        self.tensors = cache, k_gsa, v_gsa
         if cache.dtype != _U8 or cache.dim() != 3:
             raise TypeError("cache must be uint8 [n_pages, n_kv_heads, page_bytes]")
         self.n_pages, self.Hkv, nbytes = cache.shape
@@ -212,7 +214,9 @@ class Nvfp4KVCache:
     [n_pages, n_kv_heads, page_bytes] uint8 cache.  ``n_heads``,
     ``max_tokens`` and ``max_seqs`` size the attention workspace, which serves
     one stream at a time: calls of ``attend`` that may run at once each need
-    another one (``workspace=``, zeroed once).
+    another one (``workspace=``, zeroed once).  The attributes ``data``,
+    ``k_gsa``, ``v_gsa`` and ``workspace`` may be set: later calls use the new
+    buffers (a captured graph keeps the old ones' addresses).
     """
 
     def __init__(self, n_pages, n_kv_heads, head_dim, page_size=64, k_gsa=1.0, v_gsa=1.0, data=None, n_heads=None,
@@ -227,15 +231,53 @@ class Nvfp4KVCache:
             data = torch.zeros(shape, dtype=torch.uint8, device=dev)
         elif tuple(data.shape) != shape:
             raise ValueError("data is %s, not %s" % (tuple(data.shape), shape))
-        self.data = data
-        self.k_gsa, self.v_gsa = (self._scale(g, dev) for g in (k_gsa, v_gsa))
         self.max_tokens, self.max_seqs = int(max_tokens), int(max_seqs)
         self.n_heads = int(n_heads or n_kv_heads)
+        self._bind(data, self._scale(k_gsa, dev), self._scale(v_gsa, dev))
         self.workspace = new_workspace(nvfp4_kv_attention_workspace_size(
             self.max_tokens, self.max_seqs, self.n_heads, self.n_kv_heads, self.head_dim), dev)
-        # (the buffers are this object's: checked once)
-        self._pages = _Pages(self.data, self.k_gsa, self.v_gsa, self.head_dim) if self.data.is_cuda else None
-        self._ws = self.workspace.data_ptr(), self.workspace.numel()
+
+    def _bind(self, data, k_gsa, v_gsa):
+        # (checked here, not in every call)
+        self._pages = _Pages(data, k_gsa, v_gsa, self.head_dim) if data.is_cuda else None
+        self._data, self._k_gsa, self._v_gsa = data, k_gsa, v_gsa
+
+    @property
+    def data(self):
+        return self._data
+
+    @data.setter
+    def data(self, data):
+        if data.dim() != 3 or data.shape[1:] != self._data.shape[1:] or data.device != self._data.device:
+            raise ValueError("data must be [n_pages, %d, %d] on %s" % (*self._data.shape[1:], self._data.device))
+        self._bind(data, self._k_gsa, self._v_gsa)
+
+    @property
+    def k_gsa(self):
+        return self._k_gsa
+
+    @k_gsa.setter
+    def k_gsa(self, g):
+        self._bind(self._data, self._scale(g, self._data.device), self._v_gsa)
+
+    @property
+    def v_gsa(self):
+        return self._v_gsa
+
+    @v_gsa.setter
+    def v_gsa(self, g):
+        self._bind(self._data, self._k_gsa, self._scale(g, self._data.device))
+
+    @property
+    def workspace(self):
+        return self._workspace
+
+    @workspace.setter
+    def workspace(self, workspace):
+        n = workspace.numel()
+        if workspace.dtype != _U8 or not workspace.is_contiguous() or workspace.device != self._data.device:
+            raise ValueError("workspace must be contiguous uint8 on %s" % self._data.device)
+        self._workspace, self._ws = workspace, (workspace.data_ptr(), n)
 
     def _scale(self, g, dev):
         if not isinstance(g, torch.Tensor):

@@ -206,3 +206,36 @@ def test_attend_takes_the_callers_workspace():
     assert bool(kv.workspace.any())
     with pytest.raises(Exception, match="workspace"):
         kv.attend(q, *C.args, workspace=mine[:256])
+
+
+def test_buffers_may_be_replaced():
+    import nvfp4_router_gate_gb300 as R
+    rng = np.random.default_rng(191)
+    C, other = Cached(rng, [70, 5], 2, 128, 16), Cached(rng, [70, 5], 2, 128, 16)
+    q, q32 = _queries(rng, 2, 4, 128)
+    kv = _object(C, n_heads=4)
+    kept = kv.data, kv.k_gsa, kv.v_gsa, kv.workspace                   # (alive: a stale pointer would still be readable)
+    C.check(q32, [1, 1], *_attend(kv, C, q))
+    kv.data, kv.k_gsa, kv.v_gsa = other.cache, _dev(other.kg), _dev(other.vg)
+    other.check(q32, [1, 1], *_attend(kv, other, q))
+    pos = np.arange(70)
+    slots = (other.table[0, pos // 16] * 16 + pos % 16).astype(np.int32)
+    k, v = kv.gather(_dev(slots), out_dtype=torch.float32)
+    assert np.array_equal(k.cpu().numpy(), other.k[0].astype(np.float32))
+    assert np.array_equal(v.cpu().numpy(), other.v[0].astype(np.float32))
+    # a number of calibration stands for all heads; stored bytes go by it
+    kv.k_gsa = 0.25
+    assert kv.k_gsa.tolist() == [0.25, 0.25]
+    x = (rng.standard_normal((1, 2, 128))).astype(np.float32)
+    kv.append(None, _dev(x), _dev(x), None, _dev(slots[:1]), None, None)
+    got = kv.gather(_dev(slots[:1]), out_dtype=torch.float32)
+    for g, gsa in zip(got, (np.full(2, 0.25, np.float32), other.vg)):
+        c, s = K.entry(x, gsa)
+        page = K.store(np.zeros((1, 2, 16 * 144), np.uint8), [0], c, s, c, s, 16)
+        assert np.array_equal(g.cpu().numpy(), K.load(page, [0], 16, 128, gsa, gsa)[0].astype(np.float32))
+    kv.workspace = torch.zeros_like(kv.workspace)
+    with pytest.raises(ValueError):
+        kv.data = other.cache[:, :1]
+    with pytest.raises((ValueError, RuntimeError)):
+        kv.v_gsa = torch.ones(3)
+    assert len(kept) == 4 and isinstance(kv, R.Nvfp4KVCache)
