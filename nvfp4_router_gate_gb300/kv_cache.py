@@ -76,7 +76,9 @@ class _Pages:
         if cache.dtype != _U8 or cache.dim() != 3:
             raise TypeError("cache must be uint8 [n_pages, n_kv_heads, page_bytes]")
         self.n_pages, self.Hkv, nbytes = cache.shape
-        self.D, self.S = D, nbytes * 8 // (9 * D)
+        self.D, self.S = D, nbytes * 8 // (9 * max(D, 1))
+        if nbytes == 0 or nvfp4_kv_page_bytes(self.S, D) != nbytes:
+            raise ValueError("no page_size has pages of %d bytes for heads of %d channels" % (nbytes, D))
         self.data = _ptr(cache, _U8, cache.numel(), "cache")
         self.lib = _native.lib()
         self.k_gsa, self.v_gsa = _ptr(k_gsa, _F32, self.Hkv, "k_gsa"), _ptr(v_gsa, _F32, self.Hkv, "v_gsa")
