@@ -214,8 +214,10 @@ class Nvfp4KVCache:
     ``k_gsa`` and ``v_gsa`` are the global scales (a number or [n_kv_heads]
     fp32, max|x| / 2688 of calibration data per head); ``data`` an existing
     [n_pages, n_kv_heads, page_bytes] uint8 cache.  ``n_heads``,
-    ``max_tokens`` and ``max_seqs`` size the attention workspace, which serves
-    one stream at a time: calls of ``attend`` that may run at once each need
+    ``max_tokens`` and ``max_seqs`` are the query heads, queries and sequences
+    that calls of ``attend`` are expected to have; larger calls work as well
+    (the attention workspace's size goes by ``head_dim`` alone).  The workspace
+    serves one stream at a time: calls of ``attend`` that may run at once each need
     another one (``workspace=``, zeroed once).  The attributes ``data``,
     ``k_gsa``, ``v_gsa`` and ``workspace`` may be set: later calls use the new
     buffers (a captured graph keeps the old ones' addresses).
@@ -235,9 +237,12 @@ class Nvfp4KVCache:
             raise ValueError("data is %s, not %s" % (tuple(data.shape), shape))
         self.max_tokens, self.max_seqs = int(max_tokens), int(max_seqs)
         self.n_heads = int(n_heads or n_kv_heads)
+        ws_bytes = nvfp4_kv_attention_workspace_size(self.max_tokens, self.max_seqs, self.n_heads, self.n_kv_heads,
+                                                     self.head_dim)
+        if ws_bytes == 0:
+            raise ValueError("%d query heads do not share %d KV heads" % (self.n_heads, self.n_kv_heads))
         self._bind(data, self._scale(k_gsa, dev), self._scale(v_gsa, dev))
-        self.workspace = new_workspace(nvfp4_kv_attention_workspace_size(
-            self.max_tokens, self.max_seqs, self.n_heads, self.n_kv_heads, self.head_dim), dev)
+        self.workspace = new_workspace(ws_bytes, dev)
 
     def _bind(self, data, k_gsa, v_gsa):
         # (checked here, not in every call)
@@ -300,9 +305,6 @@ class Nvfp4KVCache:
 
     def attend(self, q, page_table, kv_lens, workspace=None, **kw):
         """nvfp4_kv_attention over this cache, with its own workspace unless one is given."""
-        if q.shape[0] > self.max_tokens or page_table.shape[0] > self.max_seqs or q.shape[1] != self.n_heads:
-            raise ValueError("%d tokens of %d heads in %d sequences: the workspace is for %d, %d and %d" % (
-                q.shape[0], q.shape[1], page_table.shape[0], self.max_tokens, self.n_heads, self.max_seqs))
         if q.dtype is not _BF16:
             raise TypeError("q must be bfloat16, got %s" % q.dtype)
         if self._pages is None:

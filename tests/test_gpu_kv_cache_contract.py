@@ -239,3 +239,13 @@ def test_buffers_may_be_replaced():
     with pytest.raises((ValueError, RuntimeError)):
         kv.v_gsa = torch.ones(3)
     assert len(kept) == 4 and isinstance(kv, R.Nvfp4KVCache)
+
+
+def test_calls_larger_than_expected_use_the_same_workspace():
+    """Its size goes by the channels of a head alone."""
+    rng = np.random.default_rng(192)
+    C = Cached(rng, [300], 2, 128, 64)
+    kv = _object(C)
+    q, q32 = _queries(rng, 260, 8, 128)
+    C.check(q32, [260], *_attend(kv, C, q), rows=8)
+    assert kv.status() == 0

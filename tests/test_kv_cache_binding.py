@@ -18,3 +18,10 @@ def test_pages_of_no_page_size_are_refused(nbytes, D):
     with pytest.raises(ValueError, match="page_size"):
         R.nvfp4_kv_append(None, torch.zeros(1, 3, D), torch.zeros(1, 3, D), None, torch.zeros(1, dtype=torch.int32),
                           None, None, cache, g, g)
+
+
+def test_heads_that_do_not_share_the_kv_heads_are_refused():
+    _lib()
+    assert R.Nvfp4KVCache(2, 2, 64, page_size=16, n_heads=6, device="cpu").n_heads == 6
+    with pytest.raises(ValueError, match="heads"):
+        R.Nvfp4KVCache(2, 2, 64, page_size=16, n_heads=7, device="cpu")
