@@ -170,9 +170,9 @@ def _attend(pages, q, page_table, kv_lens, cu_q=None, max_q=None, scale=None, ca
         raise ValueError("the cache holds heads of %d channels, q has %d" % (pages.D, D))
     B, max_pages = page_table.shape
     if cu_q is None:
-        if B == 0 or T % B:
+        if T % B if B else T:
             raise ValueError("%d queries for %d sequences: pass cu_q" % (T, B))
-        max_q = T // B
+        max_q = T // B if B else 0
     elif max_q is None:
         raise ValueError("cu_q needs max_q, the most queries of a sequence")
     qp, qs = _heads(q, T, Hq, D, "q")

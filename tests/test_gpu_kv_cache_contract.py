@@ -249,3 +249,16 @@ def test_calls_larger_than_expected_use_the_same_workspace():
     q, q32 = _queries(rng, 260, 8, 128)
     C.check(q32, [260], *_attend(kv, C, q), rows=8)
     assert kv.status() == 0
+
+
+def test_empty_batches():
+    rng = np.random.default_rng(193)
+    C = Cached(rng, [5], 2, 64, 16)
+    kv = _object(C)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for B in (0, 3):
+        out, _ = kv.attend(q, torch.zeros(B, 2, **i32), torch.zeros(B, **i32))
+        assert out.shape == (0, 4, 64)
+    with pytest.raises(ValueError):
+        kv.attend(torch.empty(2, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, 2, **i32), torch.zeros(0, **i32))
