@@ -7,9 +7,11 @@
 
 ``Nvfp4KVCache`` keeps the pages, the global scales and the attention
 workspace resident: its calls allocate nothing but outputs the caller does not
-pass (CUDA-graph capturable).
+pass (CUDA-graph capturable).  What a call with ``stream=`` allocates belongs to
+that stream.
 """
 
+import contextlib
 import math
 
 import torch
@@ -19,6 +21,15 @@ from . import _native
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _empty = torch.empty
+
+
+def _on(stream):
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _empty_on(stream, shape, **kw):
+    with _on(stream):
+        return _empty(shape, **kw)
 
 
 def nvfp4_kv_page_bytes(page_size, D):
@@ -103,7 +114,8 @@ def _append(pages, q, k, v, positions, slots, cos, sin, q_weight=None, k_weight=
             raise ValueError("q must be [T, heads, D] of k's type")
         qp, qs = _heads(q, T, Hq, D, "q")
         if q_out is None:
-            q_out = _empty((T, Hq, D), dtype=_BF16, device=k.device)
+            q_out = (_empty((T, Hq, D), dtype=_BF16, device=k.device) if stream is None else
+                     _empty_on(stream, (T, Hq, D), dtype=_BF16, device=k.device))
             op = q_out.data_ptr()
         else:
             op = _ptr(q_out, _BF16, T * Hq * D, "q_out")
@@ -142,7 +154,10 @@ def _gather(pages, slots, out_dtype=_BF16, k_out=None, v_out=None, stream=None):
         if out_dtype is not _BF16 and out_dtype is not _F32:
             raise TypeError("out_dtype must be bfloat16 or float32, got %s" % out_dtype)
         shape, dev = (n, Hkv, D), slots.device
-        k_out, v_out = _empty(shape, dtype=out_dtype, device=dev), _empty(shape, dtype=out_dtype, device=dev)
+        if stream is None:
+            k_out, v_out = _empty(shape, dtype=out_dtype, device=dev), _empty(shape, dtype=out_dtype, device=dev)
+        else:
+            k_out, v_out = (_empty_on(stream, shape, dtype=out_dtype, device=dev) for _ in range(2))
         kp, vp = k_out.data_ptr(), v_out.data_ptr()
     elif k_out is None or v_out is None:
         raise ValueError("pass both k_out and v_out, or neither")
@@ -177,7 +192,8 @@ def _attend(pages, q, page_table, kv_lens, cu_q=None, max_q=None, scale=None, ca
         raise ValueError("cu_q needs max_q, the most queries of a sequence")
     qp, qs = _heads(q, T, Hq, D, "q")
     if out is None:
-        out = _empty((T, Hq, D), dtype=_BF16, device=q.device)
+        out = (_empty((T, Hq, D), dtype=_BF16, device=q.device) if stream is None else
+               _empty_on(stream, (T, Hq, D), dtype=_BF16, device=q.device))
     if ws is None:
         nbytes = workspace.numel()
         ws = _ptr(workspace, _U8, nbytes, "workspace"), nbytes
@@ -192,7 +208,7 @@ def _attend(pages, q, page_table, kv_lens, cu_q=None, max_q=None, scale=None, ca
     return out, lse
 
 
-def nvfp4_kv_attention(q, cache, page_table, kv_lens, k_gsa, v_gsa, workspace=None, **kw):
+def nvfp4_kv_attention(q, cache, page_table, kv_lens, k_gsa, v_gsa, workspace=None, stream=None, **kw):
     """Attention of q [T, Hq, D] bf16 over the cached tokens of the sequences
     in page_table [B, max_pages] and kv_lens [B].  cu_q [B + 1] (with max_q, the
     most queries of a sequence) gives each sequence's rows of q; without it every
@@ -203,9 +219,11 @@ def nvfp4_kv_attention(q, cache, page_table, kv_lens, k_gsa, v_gsa, workspace=No
     if q.dtype is not _BF16:
         raise TypeError("q must be bfloat16, got %s" % q.dtype)
     if workspace is None:
-        workspace = new_workspace(nvfp4_kv_attention_workspace_size(T, page_table.shape[0], Hq, cache.shape[1], D),
-                                  q.device)
-    return _attend(_Pages(cache, k_gsa, v_gsa, D), q, page_table, kv_lens, workspace=workspace, **kw)
+        # (zeroed on the stream that uses it)
+        with _on(stream) if stream is not None else contextlib.nullcontext():
+            workspace = new_workspace(nvfp4_kv_attention_workspace_size(T, page_table.shape[0], Hq, cache.shape[1], D),
+                                      q.device)
+    return _attend(_Pages(cache, k_gsa, v_gsa, D), q, page_table, kv_lens, workspace=workspace, stream=stream, **kw)
 
 
 class Nvfp4KVCache:

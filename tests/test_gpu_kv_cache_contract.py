@@ -262,3 +262,38 @@ def test_empty_batches():
         assert out.shape == (0, 4, 64)
     with pytest.raises(ValueError):
         kv.attend(torch.empty(2, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, 2, **i32), torch.zeros(0, **i32))
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """Calls on another stream while the current one is busy: nothing of theirs waits for it or is written by it."""
+    import nvfp4_router_gate_gb300 as R
+    rng = np.random.default_rng(194)
+    C = Cached(rng, [9000], 1, 128, 64)
+    q, q32 = _queries(rng, 1, 8, 128)
+    kg, vg, lse = _dev(C.kg), _dev(C.vg), torch.empty(1, 8, device="cuda")
+    slots = _dev((C.table[0, :1] * 64).astype(np.int32))
+    s = torch.cuda.Stream()
+
+    def calls():
+        return (R.nvfp4_kv_attention(q, C.cache, *C.args, kg, vg, lse=lse, stream=s)[0],
+                *R.nvfp4_kv_gather(C.cache, slots, kg, vg, 128, out_dtype=torch.float32, stream=s))
+
+    torch.cuda.synchronize()
+    calls()                                                            # (the kernels are loaded)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), s):                    # free memory of either stream is not zero
+        with torch.cuda.stream(stream):
+            torch.full((128 << 20,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)                                     # about a fifth of a second
+    done = torch.cuda.Event()
+    done.record()
+    out, k, v = calls()
+    s.synchronize()
+    assert not done.query()
+    with torch.cuda.stream(s):
+        out, lse, k, v = (t.float().cpu().numpy() for t in (out, lse, k, v))
+    assert not done.query()
+    torch.cuda.synchronize()
+    C.check(q32, [1], out, lse)
+    assert np.array_equal(k, C.k[0][:1].astype(np.float32)) and np.array_equal(v, C.v[0][:1].astype(np.float32))
