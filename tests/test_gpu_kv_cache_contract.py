@@ -180,6 +180,29 @@ def test_sequences_of_more_than_max_q_rows_keep_their_positions(kind):
         assert not out[at + keep:at + m].any() and np.isneginf(lse[at + keep:at + m]).all(), b
 
 
+# ------------------------------------------------- windows of many columns
+
+@pytest.mark.parametrize("D,S,window", [(128, 64, 100), (64, 16, 33), (128, 32, 1), (64, 128, 200), (128, 16, 300)])
+def test_windows_through_the_tensor_memory_kernel(D, S, window):
+    rng = np.random.default_rng(180 + window)
+    n_q, lens, H, G = [64, 300, 0, 33, 1, 150], [64, 640, 7, 500, 400, 60], 8, 4
+    assert _takes_tensor_memory(len(lens), H, max(n_q) * G, window + 15)
+    C = Cached(rng, lens, H, D, S)
+    table = C.table.copy()
+    for b, (m, n) in enumerate(zip(n_q, lens)):
+        if m:
+            table[b, :max(n - m + 1 - window, 0) // S] = -1            # pages in front of every window
+    C.args = (_dev(table), C.args[1])
+    q, q32 = _queries(rng, sum(n_q), H * G, D)
+    cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+    out, lse = C.run(q, cu_q=_dev(cu), max_q=max(n_q), window=window)
+    for b, (m, n) in enumerate(zip(n_q, lens)):
+        for i in sorted({0, m // 2, m - 1} & set(range(m))):
+            row, see = cu[b] + i, max(n - m + 1 + i, 0)
+            ref = K.attention(q32[row:row + 1].astype(np.float64), C.k[b][:see], C.v[b][:see], D ** -0.5, window=window)
+            assert K.check_attention(out[row:row + 1], lse[row:row + 1], ref, see, np.abs(C.v[b]).max()) == (0, 0), (b, i)
+
+
 # ------------------------------------------------------ the object's buffers
 
 def _object(C, **kw):
