@@ -55,10 +55,11 @@ namespace {
 
 constexpr int kPTile = 128;                // tokens of a tile, rows of a row tile
 constexpr int kPThreads = 512;
-// Starting and ending a key (queries in, rows out, an empty pipeline) costs about
-// as much as this many tiles: 7 us beside 1.9 us for a tile of two row tiles and 1.4 for
-// one (least squares over the blocks of the ragged prompts; 3, 4, 5 tiles: 127, 126.5,
-// 130 us for them).
+// Starting and ending a key (queries in, rows out, an empty pipeline) counts as this many
+// tiles: 4.6 us beside 1.8 us for a tile of two row tiles and 1.4 for one.  2, 3, 4, 5
+// tiles, us: the ragged prompts above 121, 113.5, 113.2, 116; 32 sequences of up to 4096
+// tokens with eight queries of 64 heads 85, 71.7, 68.9, 68.5; six prompts of up to 700
+// queries of 48 heads over 5000 tokens 135, 134.5, 135.5, 135; the chunk 387, 386, 386, 388.
 constexpr int kPKeyCost = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kLive = 4;                   // tiles whose live tokens are kept: expanded at most three ahead
@@ -577,8 +578,8 @@ kv_prefill_kernel(const AttnParams p) {
           // one group of eight tokens: codes times scales into the swizzled tile
           uint32_t odd = 0;
           // (A value's NaN would reach the columns that do not see it, through a weight of
-          // zero: its scale becomes finite, the run's rows get their NaNs at its end.  387
-          // and 114.5 us for the chunk and the ragged prompts below, 384 and 111 without.)
+          // zero: its scale becomes finite, the run's rows get their NaNs at its end.  386
+          // and 113 us for the chunk and the ragged prompts, 384 and 111 without.)
           auto put = [&](uint8_t* tile, int i, const uint2 (&c)[BL], uint32_t two, bool value) {
             uint32_t s2 = e4m3x2_to_f16(two);
             if (value) {
