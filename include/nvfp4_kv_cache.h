@@ -56,7 +56,7 @@ size_t nvfp4_kv_page_bytes(int page_size, int D);
  *   rot          rotated channels, the first `rot` of a head: even, 0..D.
  *   interleaved  0: channel i pairs with i + rot/2; 1: 2i pairs with 2i + 1
  *   q_weight, k_weight  [D] fp32 or NULL (no norm of that side)
- *   q_out        out [T, Hq, D] bf16
+ *   q_out        out [T, Hq, D] bf16; must not overlap q, k or v
  * Arithmetic, fp32 rounded to nearest at every step so that the stored bits are
  * a function of the inputs alone:
  *   x *= 1 / sqrt(sum(x^2) / D + eps), then x *= weight; the sum halves the
@@ -77,8 +77,8 @@ nvr_status nvfp4_kv_append(const void* q, int64_t q_stride, const void* k, int64
 
 /*
  * nvfp4_kv_gather -- the values that n slots stand for: k_out and v_out
- * [n, Hkv, D], bf16 or fp32 (out_dt), code * scale * gsa rounded once; zeros
- * for a slot outside the cache.  One kernel, no workspace.
+ * [n, Hkv, D], bf16 or fp32 (out_dt), code * scale * gsa rounded to fp32, and for
+ * bf16 from there; zeros for a slot outside the cache.  One kernel, no workspace.
  */
 nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size, int Hkv, int D,
                            const int32_t* slots, int64_t n, const float* k_gsa, const float* v_gsa, void* k_out,
@@ -96,31 +96,33 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  *   q            [T, Hq, D] bf16, heads contiguous, tokens q_stride elements
  *                apart (16-byte aligned, q_stride a multiple of 8)
  *   page_table   [B, max_pages] int32: sequence b's token t lies in page
- *                page_table[b, t / page_size]; entries past its length are not
- *                read; tokens of a page id outside [0, n_pages) are not seen
+ *                page_table[b, t / page_size]; entries past its length are
+ *                not used (some are read, inside the table); tokens of a page
+ *                id outside [0, n_pages) are not seen
  *   kv_lens      [B] int32, taken within [0, max_pages * page_size]
  *   cu_q         [B + 1] int32: sequence b's queries are rows
  *                cu_q[b]..cu_q[b + 1] of q, at most max_q of them; or NULL: every
  *                sequence has max_q queries (T == B * max_q).  Values are taken within
  *                [0, T] and must not decrease (else some rows are unspecified).  Rows that
  *                no sequence covers (in front of the first one, behind the last one, past
- *                max_q in one) get zeros and lse = -inf.
- *                Rows past max_q still count as queries: those in front of them keep
- *                their positions.
+ *                max_q in one) get zeros and lse = -inf; rows past max_q count as
+ *                queries for the positions of those in front of them.
  *   out          out [T, Hq, D] bf16, 16-byte aligned
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    nvfp4_kv_attention_workspace_size(...) bytes, zeroed once
  * A query that sees no token gets zeros and lse = -inf, one with a NaN among its
  * channels NaNs in both.  What the cache holds of tokens that no query sees (any
  * bytes: past the length, in front of the first window, in the same page as seen
- * ones or not) does not reach the output; a NaN in a key's or value's scales reaches
- * the queries that see the token, no others.  Hq is a multiple of Hkv.  Scores, softmax statistics and outputs are accumulated in
- * fp32; the weights p_t enter the second product as fp16, relative to a running
- * maximum; results do not depend on the order in which the GPU runs the
- * blocks.  One kernel and, unless no key can be cut over blocks, a second one that
- * joins the parts of those that were.  The workspace's size depends on D alone (T_max,
- * B_max and the heads are checked): partial results of the resident blocks.  A bounded
- * wait that runs out sets the workspace's status word (nvr_read_device_status).
+ * ones or not) does not reach the output; a NaN in a key's or value's scales
+ * reaches the queries that see the token, no others.  Hq is a multiple of Hkv.
+ * Scores, softmax statistics and outputs are accumulated in fp32; the weights p_t
+ * enter the second product as fp16, relative to a running maximum (a weight below
+ * 2^-32 of the largest is lost there); results do not depend on the order in which
+ * the GPU runs the blocks.  One kernel and, unless no key can be cut over blocks, a
+ * second one that joins the parts of those that were.  The workspace's size depends
+ * on D alone (T_max, B_max and the heads are checked): partial results of the
+ * resident blocks.  A bounded wait that runs out sets the workspace's status word
+ * (nvr_read_device_status).
  */
 size_t nvfp4_kv_attention_workspace_size(int64_t T_max, int64_t B_max, int Hq, int Hkv, int D);
 nvr_status nvfp4_kv_attention(const void* q, int64_t q_stride, int64_t T, int Hq, int Hkv, int D,
