@@ -31,14 +31,14 @@
 // depend on timing.  One producer warp feeds a ring of tiles with bulk copies, a
 // page of one KV head each.
 //
-// Measured (D = 128, 8 KV heads of 8 heads): 128 sequences of up to 8192 tokens 118
-// us, 4.7 TB/s, 0.69 of the copy bandwidth (0.88 of it between the first tiles and the
+// Measured (D = 128, 8 KV heads of 8 heads): 128 sequences of up to 8192 tokens 114
+// us, 4.8 TB/s, 0.71 of the copy bandwidth (0.88 of it between the first tiles and the
 // first teams to finish; the teams' times spread by 12 %, memory is not shared out
 // evenly); one sequence of 131072 tokens 41 us, 3.7 TB/s; 32 sequences of up to 4096
-// tokens with four queries 59.5 us.  A tile of 128 tokens takes a team 1.4 us with
+// tokens with four queries 61 us.  A tile of 128 tokens takes a team 1.4 us with
 // eight columns (three teams an SM, issue slots 60 % busy) and with sixteen (two teams:
 // issue slots 44 %, matrix pipe 27 %; tiles of 64 tokens, with two teams or with three
-// at 128 registers, were slower: 67.7 and 71.4 us instead of 59.5).
+// at 128 registers, were slower: 67.7 and 71.4 us where this took 59.5).
 #include "kv_attention.cuh"
 #include "../../include/nvfp4_kv_cache.h"
 
@@ -48,16 +48,16 @@ namespace {
 
 // More columns of a sequence go to the tensor-memory kernel: from there on it is
 // faster although it works on 128 rows whatever their number.  32 sequences of up to
-// 4096 tokens, this kernel / that one, us, by columns: D = 128: 16: 37.9 / 64.1, 24:
-// 63.7 / 68.7, 32: 59.4 / 63.5, 48: 82.2 / 63.7, 64: 113 / 66.4; D = 64: 24: 46.9 /
-// 53.8, 32: 45.3 / 50.8, 48: 60.8 / 49.6.  Four sequences of 600: 32: 13.1 / 16.9, 64:
-// 14.7 / 17.0.
+// 4096 tokens, this kernel / that one, us, by columns: D = 128: 16: 38.6 / 65.1, 24:
+// 64.5 / 69.7, 32: 61.1 / 65.2, 48: 83.5 / 67.1, 64: 117 / 68.4; D = 64: 24: 47.5 /
+// 54.2, 32: 47.0 / 49.7, 48: 62.1 / 50.2.  Four sequences of 600: 32: 13.1 / 15.4, 64:
+// 14.7 / 15.9.
 constexpr int kStreamCols = 32;
 // But a call of at most this many tiles an SM (128 tokens and 16 columns each, by the
 // page tables' width and the window) stays here: it starts and ends sooner.  This kernel / that one,
-// us: one sequence of 2 KV heads, 128 columns, 600 tokens (80 tiles) 12.4 / 15.6; 512
-// columns, 1500 tokens (768) 14.8 / 18.0; four of 8 heads, 256 columns, 130 tokens (1024)
-// 16.8 / 17.4; 128 columns, 600 tokens (1280) 17.9 / 16.9; 256, 600 (2560) 26.5 / 19.2.
+// us: one sequence of 2 KV heads, 128 columns, 600 tokens (80 tiles) 12.6 / 14.8; 512
+// columns, 1500 tokens (768) 14.9 / 17.5; four of 8 heads, 256 columns, 130 tokens (1024)
+// 17.1 / 17.0; 128 columns, 600 tokens (1280) 18.3 / 16.4; 256, 600 (2560) 25.5 / 18.7.
 constexpr int kStreamTiles = 6;
 // Starting and ending a key (queries, joining the warps, storing) costs a team
 // about as much as this many tiles: 1.5 us beside 1.4 us for a tile with eight
@@ -86,8 +86,11 @@ struct alignas(16) Meta {
 // run is all of its key; the team's last run
 constexpr uint32_t kFirst = 1, kLast = 2, kEdge = 4, kWhole = 8, kDone = 16;
 
-// Byte i is 0xFF where bit i of the low four is set.
-__device__ __forceinline__ uint32_t bytes_of(uint32_t bits) { return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu; }
+// Byte i is 0xFF where bit i of the low four is set, and back.
+__device__ __forceinline__ uint32_t bytes_of(uint32_t bits) {
+  return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu;
+}
+__device__ __forceinline__ uint32_t bits_of(uint32_t bytes) { return (bytes & 0x01010101u) * 0x10204080u >> 28; }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -425,7 +428,7 @@ kv_attention_kernel(const AttnParams p) {
         // not be a NaN.  A lane looks after the eight scales of one channel block of
         // tokens tg .. tg + 7: those of tokens that no column sees (stale memory, a page
         // given back, anything) become zero, and so do NaNs, which go straight to the
-        // columns that do see their token.
+        // columns that do see their token.  (32 sequences with four queries 59.5 -> 60.4 us.)
         const int t0 = meta.tile * TILE + warp * MW * 16, in = lane / (D / 16) * 8, tg = t0 + in;
         uint32_t bad = 0;                                    // tokens of the warp's with a NaN
         if (in < 32) {
@@ -434,10 +437,11 @@ kv_attention_kernel(const AttnParams p) {
           const uint32_t see = (live >> (in / 16)) & 1u ? tokens32(tg, meta.lo, meta.hi) : 0u;
           const uint2 x = *at;
           const uint32_t s0 = bytes_of(see), s1 = bytes_of(see >> 4);
-          const uint32_t n0 = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s0, n1 = __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s1;
+          const uint32_t n0 = __vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s0;
+          const uint32_t n1 = __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) & s1;
           *at = make_uint2(x.x & s0 & ~n0, x.y & s1 & ~n1);
           fence_proxy_async_smem();                          // (the next copy into the stage comes after)
-          if (n0 | n1) bad = ((((n0 & 0x01010101u) * 0x10204080u) >> 28) | (((n1 & 0x01010101u) * 0x10204080u) >> 28) << 4) << in;
+          if (n0 | n1) bad = (bits_of(n0) | bits_of(n1) << 4) << in;
         }
         bad = __reduce_or_sync(0xFFFFFFFFu, bad);
         if (bad) {
@@ -804,9 +808,9 @@ nvr_status launch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
 template <int D>
 nvr_status dispatch_attn(AttnParams& p, int max_kv, cudaStream_t s) {
   // Sixteen columns at a time, two teams an SM, where eight (three teams) do not hold
-  // a sequence's queries: 16 columns of 32 sequences of up to 4096 tokens 37.9 us, as
-  // twice eight 45.6; 32 columns 59.4 and 78.4.  Eight columns as half of sixteen: the
-  // serving batch 164 us instead of 121, the long sequence 52 instead of 41.
+  // a sequence's queries: 16 columns of 32 sequences of up to 4096 tokens 38.6 us, as
+  // twice eight 46.0; 32 columns 61.1 and 81.4.  Eight columns as half of sixteen: the
+  // serving batch 165 us instead of 113.5, the long sequence 51 instead of 41.
   const int64_t cols = static_cast<int64_t>(p.max_q) * p.G;
   if (cols <= 8) return launch_attn<D, 1, 4, 2, 3, 3, 1>(p, max_kv, s);
   return launch_attn<D, 2, 4, 2, 3, 1, 2>(p, max_kv, s);

@@ -34,9 +34,9 @@
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
 // equal chunks, one per block, the rows of cut keys joined by csrc/kv_join.cu.
 //
-// Measured (D = 128, 8 KV heads): 2048 queries of 64 heads over 8192 tokens 383 us,
-// 1256 TFLOP/s, 0.66 of the cuBLAS bf16 rate; nine ragged prompts of up to 1500
-// queries of 32 heads over 2500 tokens 111 us.  A tile of 128 tokens and 256 columns takes
+// Measured (D = 128, 8 KV heads): 2048 queries of 64 heads over 8192 tokens 385 us,
+// 1249 TFLOP/s, 0.66 of the cuBLAS bf16 rate; nine ragged prompts of up to 1500
+// queries of 32 heads over 2500 tokens 113 us.  A tile of 128 tokens and 256 columns takes
 // 1.8 us (3400 clocks; its products 2050): each row tile's softmax 2200 clocks and
 // then 1000 of waiting for its next S, which the full tensor memory leaves no room to
 // make earlier.  A run of a key costs 4.6 us on top (queries in, rows out).  Tried and
@@ -44,7 +44,7 @@
 // halves of the softmax (450: fetching the instructions), eight warps that expand
 // (450: 96 registers a thread), other splits of the registers (equal), scores in
 // halves of 64 tokens that are made while the other half is weighed (536), S loaded a
-// half ahead (388).
+// half ahead (388), each where this took 383.
 #include <type_traits>
 
 #include "kv_attention.cuh"
@@ -57,7 +57,7 @@ constexpr int kPTile = 128;                // tokens of a tile, rows of a row ti
 constexpr int kPThreads = 512;
 // Starting and ending a key (queries in, rows out, an empty pipeline) counts as this many
 // tiles: 4.6 us beside 1.8 us for a tile of two row tiles and 1.4 for one.  2, 3, 4, 5
-// tiles, us: the ragged prompts above 121, 113.5, 113.2, 116; 32 sequences of up to 4096
+// tiles, us: the ragged prompts above 121, 113.5, 113, 116; 32 sequences of up to 4096
 // tokens with eight queries of 64 heads 85, 71.7, 68.9, 68.5; six prompts of up to 700
 // queries of 48 heads over 5000 tokens 135, 134.5, 135.5, 135; the chunk 387, 386, 386, 388.
 constexpr int kPKeyCost = 4;
