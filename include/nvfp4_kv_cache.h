@@ -110,6 +110,8 @@ nvr_status nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int page_size,
  *   out          out [T, Hq, D] bf16, 16-byte aligned
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    nvfp4_kv_attention_workspace_size(...) bytes, zeroed once
+ * Calls whose work does not fit 31 bits (B * Hkv * columns / 16 * tokens of the page
+ * table's width / 128) are NVR_ERR_UNSUPPORTED.
  * A query that sees no token gets zeros and lse = -inf, one with a NaN among its
  * channels NaNs in both.  What the cache holds of tokens that no query sees (any
  * bytes: past the length, in front of the first window, in the same page as seen
