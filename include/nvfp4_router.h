@@ -82,7 +82,7 @@ typedef enum {
   NVR_ERR_TIMEOUT = 6
 } nvr_status;
 
-typedef enum { NVR_BF16 = 0, NVR_F32 = 1 } nvr_dtype;
+typedef enum { NVR_BF16 = 0, NVR_F32 = 1, NVR_F16 = 2 } nvr_dtype;
 
 typedef enum { NVR_SF_LINEAR = 0, NVR_SF_TILED = 1 } nvr_sf_layout;
 

@@ -18,6 +18,8 @@ Functions (same names as include/nvfp4_router.h):
   ``nvfp4_moe_combine(y, w)`` -> out [T, N]
 * ``nvfp4_kv_append``, ``nvfp4_kv_attention``, ``nvfp4_kv_gather`` (include/nvfp4_kv_cache.h): the paged
   NVFP4 key/value cache; ``Nvfp4KVCache`` keeps its pages, scales and workspace resident
+* ``prompt_rope``, ``prompt_attention`` (include/nvfp4_prompt.h): rotary positions with several axes, attention
+  of packed prompts over their own 16-bit keys and values (``PromptAttention`` keeps a workspace resident)
 * ``router_gate_workspace_size``, ``router_gate_x_gsa``, ``nvfp4_quantize_workspace_size``,
   ``nvr_sf_bytes``, ``nvr_read_device_status``
 
@@ -42,7 +44,8 @@ __all__ = ["nvfp4_quantize_act", "nvfp4_pack_weight", "router_gate_topk", "route
            "nvfp4_linear", "nvfp4_linear_workspace_size", "Nvfp4Linear", "nvfp4_pack_experts",
            "nvfp4_moe_gemm", "nvfp4_moe_gemm_workspace_size", "nvfp4_moe_combine", "nvfp4_kv_append",
            "nvfp4_kv_gather", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_size", "nvfp4_kv_page_bytes",
-           "Nvfp4KVCache", "rope_table"]
+           "Nvfp4KVCache", "rope_table", "prompt_rope", "rope_axes", "rope_axes_table", "prompt_attention",
+           "prompt_attention_workspace_size", "PromptAttention"]
 
 _LAYOUTS = {"linear": _native.NVR_SF_LINEAR, "tiled": _native.NVR_SF_TILED}
 
@@ -368,3 +371,5 @@ class RouterGate:
 
 from .kv_cache import (Nvfp4KVCache, nvfp4_kv_append, nvfp4_kv_attention,  # noqa: E402
                        nvfp4_kv_attention_workspace_size, nvfp4_kv_gather, nvfp4_kv_page_bytes, rope_table)
+from .prompt import (PromptAttention, prompt_attention, prompt_attention_workspace_size, prompt_rope,  # noqa: E402
+                     rope_axes, rope_axes_table)

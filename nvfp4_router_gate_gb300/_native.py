@@ -1,5 +1,5 @@
-"""ctypes declarations of the C ABI in include/nvfp4_router.h and
-include/nvfp4_kv_cache.h.
+"""ctypes declarations of the C ABI in include/nvfp4_router.h,
+include/nvfp4_kv_cache.h and include/nvfp4_prompt.h.
 
 Loading the library needs no GPU; it fails loudly (RuntimeError) when the
 shared library has not been built.  There is no fallback of any kind.
@@ -21,6 +21,7 @@ NVR_ERR_TIMEOUT = 6
 
 NVR_BF16 = 0
 NVR_F32 = 1
+NVR_F16 = 2                 # heads of a prompt only
 NVR_SF_LINEAR = 0
 NVR_SF_TILED = 1
 
@@ -75,6 +76,11 @@ SIGNATURES = {
     "nvfp4_kv_attention_workspace_size": (_sz, [_i64, _i64, _i32, _i32, _i32]),
     "nvfp4_kv_attention": (_i32, [_p, _i64, _i64, _i32, _i32, _i32, _p, _i64, _i32, _p, _i64, _i64, _p, _p, _i32, _p,
                                   _p, _f32, _i32, _i32, _p, _p, _p, _sz, _p]),
+    "prompt_rope": (_i32, [_p, _i64, _p, _i64, _i32, _i64, _i32, _i32, _i32, _p, _i64, _i32, ctypes.c_char_p, _p, _p,
+                           _i64, _i32, _i32, _p, _p, _f32, _p, _i64, _p, _i64, _i32, _p]),
+    "prompt_attention_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "prompt_attention": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i32, _i64, _i64, _i32, _i32, _i32, _p,
+                                _p, _i64, _i32, _i32, _f32, _i32, _i32, _p, _p, _p, _p, _p, _sz, _p]),
     "router_gate_logits": (_i32, [_p, _i32, _i64, _i64, _p, _p, _p, _i64, _u32, _p, _p, _sz, _p]),
     "nvr_read_device_status": (_i32, [_p, _p, ctypes.POINTER(_i32)]),
     "nvr_set_profile_events": (_i32, [_p, _i32]),

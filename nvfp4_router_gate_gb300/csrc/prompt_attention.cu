@@ -1,0 +1,1041 @@
+// prompt_attention.cu -- softmax attention of packed prompts of different lengths
+// over their own 16-bit keys and values (sm_103a): prompt_attention.
+// Bound by the tensor cores: 4 D flops for every (query, head) and seen token.
+//
+// Mathematics: as csrc/kv_prefill.cu -- S = Q K^T and O += P V on tcgen05 with 128
+// rows (query, head) of an accumulator in tensor memory, a thread a row; the running
+// maximum moves in steps, sums and statistics in fp32, the weights P rounded to the
+// values' type.
+//
+// A block (one per SM) takes 256 rows of a sequence that share a KV head as two row
+// tiles (qt queries of Gt heads each) and walks the tokens in tiles of 128:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: read S from tensor memory, write P
+//                   over it, rescale O when the maximum moves;
+//   warps 8-11      the rows out: O from tensor memory, scaled, joined with the prefix,
+//                   stored, while the softmax warps are at the next rows already;
+//   warp 12         issues the products, alternating the row tiles, so that one
+//                   tile's softmax runs under the other's products;
+//   warp 13         walks the work and hands every role its runs;
+//   warp 14         copies queries, keys and values into swizzled shared memory (TMA);
+//   warp 15         looks tiles with masked tokens over for infinities and NaNs among
+//                   the values: a weight of zero would make NaNs of them.  They become
+//                   zeros; the rows that see them get them back at the end.
+//
+// Tensor memory, 512 columns: S0 | S1 (128 each, P over the first half of its
+// S), O0 | O1 (D each).  S of the next tile follows P V of this one in issue
+// order, so S is never overwritten early and a complete S implies the earlier
+// P V complete.  P comes in two halves of 64 tokens: P V of the first runs under
+// the softmax of the second.  The products of a run's last tile and of the next
+// run's first one are issued alternately as well: the pipeline does not drain.
+//
+// The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
+// equal chunks, one per block, the rows of cut keys joined by csrc/prompt_join.cu.
+#include <type_traits>
+
+#include "../../include/nvfp4_prompt.h"
+#include "prompt_attention.cuh"
+
+namespace nvr {
+
+namespace {
+
+constexpr int kPaThreads = 512;
+constexpr int kPaKeyCost = 1;              // starting and ending a key counts as this many tiles
+constexpr int kPaMinChunk = 2;             // fewest places of a block in the flat order of the tiles
+constexpr int kPaWhole = 4;                // keys of at most this many tiles are not cut
+constexpr int kRuns = 3;                   // runs handed out ahead
+constexpr int kConsumers = 15;             // warps that read a run
+
+struct alignas(16) Run {
+  int tiles;                               // -1: the end
+  int tile0;                               // first tile of the sequence
+  int head;                                // head group
+  int q0, k0;                              // first query's row, the sequence's first key row
+  int n_q, pos0, kmax;                     // queries, position of the first one, keys that exist
+  int first[2], last[2];                   // tiles of each row tile: [first, last)
+  int free_to, free_from;                  // tiles inside [free_from, free_to) of the tokens are seen by every row
+  int whole, slot;                         // all of its key, or a part: in this slot
+  int bad;                                 // values of the run were not finite
+  int pad;
+};
+
+template <int D>
+struct PaSmem {
+  static constexpr int kTileBytes = kPaTile * D * 2;         // rows in 128-byte swizzled atoms of 64 channels
+  static constexpr int kSlots = D == 128 ? 4 : 8;            // tiles of keys and of values, alternately
+  static constexpr int kQ = 0;
+  static constexpr int kKV = kQ + 2 * kTileBytes;
+  static constexpr int kOut = kKV + kSlots * kTileBytes;     // 128 bytes of each row on their way out
+  static constexpr int kStat = kOut + kPaTile * 128;         // per row tile and row: m, l
+  static constexpr int kRunsAt = kStat + 2 * 2 * kPaTile * 4;
+  static constexpr int kBarAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));
+  static constexpr int kTotal = kBarAt + (2 * kRuns + 3 * kSlots + 2 * 9 + 1) * 8 + 64 + 1024;
+};
+
+// D fp32 (1 in bits 4-5), A and B bf16 (1) or fp16 (0) in bits 7-9 and 10-12, B
+// transposed in bit 16, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+template <bool kF16>
+__device__ __forceinline__ uint32_t idesc_16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (kF16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn_major ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The two words of a matrix descriptor: 128-byte swizzle, 8-row groups 1024 bytes
+// apart; the low one holds the address and the distance of 64-channel atoms (used
+// by the transposed operand alone).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(const void* tile, uint32_t atom_distance) {
+  return ((smem_u32(tile) & 0x3FFFFu) >> 4) | ((atom_distance >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] . B[smem]; descriptors by their low words.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(kDescHigh)
+      : "memory");
+}
+// The same with A in tensor memory (two 16-bit values of a row to a column).
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(kDescHigh)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 32 columns of this warp's lanes without the wait, and the wait: the registers
+// pass through it so that nothing reads them early.
+__device__ __forceinline__ void tmem_load32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load32_finish(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :: "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]) :: "memory");
+}
+
+// A key's length in the flat order: its tiles, then places without work.
+__device__ __forceinline__ int key_cost(const PromptGroup& g) { return g.n > 0 ? g.tiles + kPaKeyCost : 0; }
+
+// Zeros, and an lse of -inf, for the rows that no sequence covers: in front of the first
+// one, behind the last one (a batch padded for a captured graph), past max_q in one.
+template <int D>
+__device__ __forceinline__ void clear_rows(const PromptParams& p, int unit, int units) {
+  const int lane = threadIdx.x & 31, T = static_cast<int>(p.T);
+  auto row_of = [&](int b) { return min(max(__ldg(p.cu_q + b), 0), T); };
+  auto clear = [&](int64_t from, int64_t to, int step) {
+#pragma unroll 1
+    for (int64_t r = from; r < to; r += step) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + r * p.Hq * D);
+#pragma unroll 1
+      for (int i = lane; i < p.Hq * (D / 8); i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!p.lse) continue;
+#pragma unroll 1
+      for (int i = lane; i < p.Hq; i += 32) p.lse[r * p.Hq + i] = -INFINITY;
+    }
+  };
+  const int first = row_of(0), last = row_of(p.B);
+  clear(unit, first, units);
+  clear(static_cast<int64_t>(last) + unit, T, units);
+#pragma unroll 1
+  for (int64_t b0 = static_cast<int64_t>(unit) * 32; b0 < p.B; b0 += static_cast<int64_t>(units) * 32) {
+    const int b = static_cast<int>(min(b0 + lane, static_cast<int64_t>(p.B - 1))), a = row_of(b), e = row_of(b + 1);
+    uint32_t over = __ballot_sync(0xFFFFFFFFu, b0 + lane < p.B && e - a > p.max_q);
+#pragma unroll 1
+    for (; over; over &= over - 1) {
+      const int l = __ffs(over) - 1;
+      clear(static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, a, l)) + p.max_q, __shfl_sync(0xFFFFFFFFu, e, l), 1);
+    }
+  }
+}
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kPaThreads, 1)
+prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+  using Sm = PaSmem<D>;
+  constexpr int NS = Sm::kSlots;
+  // A row's weights are 2^(s - m), m set to its largest score less kRise and set again when
+  // 64 of them add up to more than kMostSum.  fp16: as csrc/kv_attention.cuh, most of its
+  // range lies below; bf16 has fp32's range, and results need room above the weights.
+  constexpr float kRise = kF16 ? kLift : 0.0f;
+  constexpr float kMostSum = 32768.0f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Run* s_runs = reinterpret_cast<Run*>(smem + Sm::kRunsAt);
+  float* s_stat = reinterpret_cast<float*>(smem + Sm::kStat);          // [row tile][m, l][row]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBarAt);
+  uint64_t *run_full = bars, *run_empty = run_full + kRuns, *kv_full = run_empty + kRuns, *kv_empty = kv_full + NS,
+           *v_clean = kv_empty + NS, *q_full = v_clean + NS, *q_empty = q_full + 2, *s_full = q_empty + 2,
+           *p_half = s_full + 2, *p_full = p_half + 2, *h_full = p_full + 2, *o_full = h_full + 2,
+           *o_empty = o_full + 2, *stat_full = o_empty + 2, *drained = stat_full + 2;
+  int* s_words = reinterpret_cast<int*>(drained + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
+  volatile int* abort_flag = s_words + 1;
+  int* s_start = s_words + 2;                                // item, offset inside it
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, kConsumers); }
+    for (int i = 0; i < NS; ++i) { mbar_init(kv_full + i, 1); mbar_init(kv_empty + i, 1 + i % 2); mbar_init(v_clean + i, 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1); mbar_init(q_empty + i, 1); mbar_init(s_full + i, 1);
+      mbar_init(p_half + i, 4); mbar_init(p_full + i, 4); mbar_init(h_full + i, 1);
+      mbar_init(o_full + i, 1); mbar_init(o_empty + i, 4); mbar_init(stat_full + i, 4);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) tmem_alloc(tmem_holder, 512);
+  if (warp == 14 && lane < 3) tma_prefetch_map(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_k : &p.tm_v);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- this block's chunk of the flat order
+  const int n_items = p.B * p.groups;
+  const int per = (n_items + kPaThreads - 1) / kPaThreads;
+  int mine = 0;
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost(prompt_group(p, i)) * p.Hv;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += a;
+  }
+  if (lane == 31) reinterpret_cast<int*>(s_stat)[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = 0, total = 0;
+  for (int w = 0; w < kPaThreads / 32; ++w) {
+    const int x = reinterpret_cast<int*>(s_stat)[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kPaMinChunk);
+  const int f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
+  const int f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
+  const int excl = before + incl - mine;
+  if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
+    int at = excl, i = tid * per;
+    for (;; ++i) {
+      const int n = key_cost(prompt_group(p, i)) * p.Hv;
+      if (f0 < at + n) break;
+      at += n;
+    }
+    s_start[0] = i;
+    s_start[1] = f0 - at;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_holder;
+
+  auto give_up = [&]() {
+    if (lane == 0) {
+      report_timeout(p.status);
+      *abort_flag = 1;
+    }
+  };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag)) != 0;
+  };
+
+  if (tid == 13 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
+  if (p.cu_q && warp >= 8 && warp < 12) clear_rows<D>(p, blockIdx.x * 4 + warp - 8, gridDim.x * 4);
+  if (f0 < f1) {
+    // the next run to this warp, or null; its last reader frees it
+    int n_taken = 0;
+    auto take = [&]() -> const volatile Run* {
+      const int s = n_taken % kRuns;
+      if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return nullptr;
+      ++n_taken;
+      return s_runs + s;
+    };
+    auto give_back = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(run_empty + (n_taken - 1) % kRuns);
+    };
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (warp == 13) {
+      // ------------------------------------------------------------ the walk
+      int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
+      bool ok = true;
+      auto hand_out = [&](const Run& r) {
+        const int s = n_run % kRuns;
+        if (!wait_all(run_empty + s, ((n_run / kRuns) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          s_runs[s] = r;
+          mbar_arrive(run_full + s);
+        }
+        __syncwarp();
+        ++n_run;
+        return true;
+      };
+      PromptGroup next = prompt_group(p, item);
+      for (; f < f1 && ok; ++item) {
+        const PromptGroup g = next;
+        next = prompt_group(p, min(item + 1, n_items - 1));
+        const int cost = key_cost(g);
+        while (off < cost * p.Hv && f < f1 && ok) {
+          const int head = off / cost, at = off - head * cost;
+          const int key_f0 = f - at, end = min(f1, key_f0 + cost);
+          int ta = min(at, g.tiles), tb = min(end - key_f0, g.tiles);
+          const bool uncut = g.tiles <= kPaWhole;
+          if (uncut) {
+            ta = 0;
+            tb = g.tiles;
+          }
+          if (uncut ? at == 0 : ta < tb) {
+            Run r = {};
+            r.tiles = tb - ta;
+            r.tile0 = g.tile0 + ta;
+            r.head = head;
+            r.q0 = g.q0 + g.i0; r.k0 = g.k0;
+            r.n_q = g.n; r.pos0 = g.shift + g.i0; r.kmax = g.kmax;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              r.first[w] = min(max(g.first[w] - ta, 0), r.tiles);
+              r.last[w] = max(min(g.last[w] - ta, r.tiles), r.first[w]);
+            }
+            r.free_to = seen_end(p, r.pos0, g.kmax);
+            r.free_from = seen_begin(p, r.pos0 + g.n - 1);
+            const int first_chunk = key_f0 / chunk, n_parts = uncut ? 1 : (key_f0 + g.tiles - 1) / chunk - first_chunk + 1;
+            const int inside = key_f0 > f0;
+            r.whole = n_parts == 1;
+            r.slot = 2 * blockIdx.x + inside;
+            // this block holds a cut key's first part
+            if (lane == 0 && n_parts > 1 && ta == 0)
+              p.joins[blockIdx.x] = {n_parts, inside, r.q0, g.n, head * p.Gt, {0, 0, 0}};
+            ok = hand_out(r);
+          }
+          off += end - f;
+          f = end;
+        }
+        off = 0;
+      }
+      if (ok) {
+        Run r = {};
+        r.tiles = -1;
+        ok = hand_out(r);
+      }
+      if (!ok) give_up();
+    } else if (warp == 12) {
+      // -------------------------------------------------------- the products
+      const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
+      const uint32_t q_low = desc_low(smem + Sm::kQ, 16), k_low = desc_low(smem + Sm::kKV, 16);
+      const uint32_t v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
+      constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
+      auto score = [&](int w, int slot) {
+        const uint32_t q = q_low + w * kTileLow, k = k_low + slot * kTileLow, d = tmem + w * kPaTile;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
+            tc_mma_ss(d, q + o, k + o, id_s, i != 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto weigh = [&](int w, int slot, bool add, int half) {
+        const uint32_t v = v_low + slot * kTileLow, d = tmem + 2 * kPaTile + w * D, a = tmem + w * kPaTile;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kPaTile / 32; ++k) {
+            // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
+            const int i = half * (kPaTile / 32) + k;
+            tc_mma_ts(d, a + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      auto have = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_all(bar, parity);
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_o[2] = {1, 1}, ph_clean[NS / 2] = {};
+      int n_tile = 0;                                      // tiles whose scores were issued
+      // a tile in work: bit 0-1: the row tiles it is of; 2-3: their first, 4-5: their last; 6: masked
+      auto products = [&]() -> bool {
+        uint32_t prev = 0;
+        const volatile Run* run = nullptr;
+        int j = 0, n = 0, first[2], last[2], tile0 = 0, free_from = 0, free_to = 0;
+        for (bool more = true; more || prev;) {
+          uint32_t cur = 0;
+          while (more && j >= n) {
+            if (run) give_back();
+            run = take();
+            if (!run) return false;
+            n = run->tiles;
+            j = 0;
+            if (n < 0) { more = false; break; }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) { first[w] = run->first[w]; last[w] = run->last[w]; }
+            tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
+          }
+          if (more) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              if (j >= first[w] && j < last[w])
+                cur |= (1u << w) | (j == first[w] ? 4u << w : 0u) | (j + 1 == last[w] ? 16u << w : 0u);
+            const int t0 = (tile0 + j) * kPaTile;
+            if (t0 < free_from || t0 + kPaTile > free_to) cur |= 64u;
+            ++j;
+          }
+          const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
+          const uint32_t v_phase = ((2 * n_tile - 1) / NS) & 1, k_phase = ((2 * n_tile) / NS) & 1;
+          if (prev) {
+            if (!have(kv_full + v_slot, v_phase)) return false;
+            if (prev & 64u) {
+              if (!have(v_clean + v_slot, ph_clean[v_slot / 2])) return false;
+              ph_clean[v_slot / 2] ^= 1u;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (prev & (1u << w)) {
+              if (prev & (4u << w)) {
+                if (!have(o_empty + w, ph_o[w])) return false;
+                ph_o[w] ^= 1u;
+              }
+              if (!have(p_half + w, ph_p[w])) return false;
+              weigh(w, v_slot, !(prev & (4u << w)), 0);
+              commit(h_full + w);
+              if (!have(p_full + w, ph_p[w])) return false;
+              ph_p[w] ^= 1u;
+              weigh(w, v_slot, true, 1);
+              if (prev & (16u << w)) commit(o_full + w);
+            }
+            if (cur && w == 0 && !have(kv_full + k_slot, k_phase)) return false;
+            if (cur & (1u << w)) {
+              if (cur & (4u << w)) {
+                if (!have(q_full + w, ph_q[w])) return false;
+                ph_q[w] ^= 1u;
+              }
+              score(w, k_slot);
+              commit(s_full + w);
+              if (cur & (16u << w)) commit(q_empty + w);
+            }
+          }
+          if (prev) commit(kv_empty + v_slot);
+          if (cur) {
+            commit(kv_empty + k_slot);
+            ++n_tile;
+          }
+          prev = cur;
+        }
+        give_back();
+        return true;
+      };
+      if (!products()) give_up();
+      // nothing of this block's is under way when the tensor memory goes back
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      wait_all(drained, 0);
+    } else if (warp == 14) {
+      // ------------------------------------------ queries, keys and values in
+      uint32_t sent_q[2] = {0, 0};
+      int n_load = 0;
+      auto copies = [&]() -> bool {
+        auto tile = [&](const CUtensorMap* map, int head, int row) {
+          const int s = n_load % NS;
+          if (!wait_all(kv_empty + s, ((n_load / NS) & 1) ^ 1)) return false;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(kv_full + s, Sm::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem + Sm::kKV + s * Sm::kTileBytes + c * (kPaTile * 128), map, 64 * c, head, row, kv_full + s);
+          }
+          __syncwarp();
+          ++n_load;
+          return true;
+        };
+        for (;;) {
+          const volatile Run* run = take();
+          if (!run) return false;
+          const int n = run->tiles;
+          if (n < 0) break;
+          const int head = run->head, row0 = run->k0 + run->tile0 * kPaTile, kv_head = head / p.chunks;
+          auto queries = [&](int w) {
+            if (run->first[w] >= run->last[w]) return true;
+            if (!wait_all(q_empty + w, (sent_q[w] & 1) ^ 1)) return false;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(q_full + w, p.Gt * p.qt * D * 2);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem + Sm::kQ + w * Sm::kTileBytes + c * (kPaTile * 128), &p.tm_q, 64 * c, head * p.Gt,
+                            run->q0 + w * p.qt, q_full + w);
+            }
+            __syncwarp();
+            ++sent_q[w];
+            return true;
+          };
+          for (int j = 0; j < n; ++j) {
+            if (!tile(&p.tm_k, kv_head, row0 + j * kPaTile)) return false;
+            if (j == 0 && (!queries(0) || !queries(1))) return false;
+            if (!tile(&p.tm_v, kv_head, row0 + j * kPaTile)) return false;
+          }
+          give_back();
+        }
+        give_back();
+        return true;
+      };
+      if (!copies()) give_up();
+      if (*abort_flag) {
+        // copies in flight land before the block's memory goes away
+        const uint64_t drain = globaltimer_ns() + 1000000000ull;
+        for (int i = max(n_load - NS, 0); i < n_load; ++i)
+          while (!mbar_try_wait(kv_full + i % NS, (i / NS) & 1))
+            if (globaltimer_ns() > drain) break;
+        for (int w = 0; w < 2; ++w)
+          while (sent_q[w] && !mbar_try_wait(q_full + w, (sent_q[w] - 1) & 1))
+            if (globaltimer_ns() > drain) break;
+      }
+    } else if (warp == 15) {
+      // ------------------------------------- values that are not finite, to zeros
+      constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u;
+      int n_tile = 0;
+      auto look = [&]() -> bool {
+        for (;;) {
+          const volatile Run* run = take();
+          if (!run) return false;
+          const int n = run->tiles;
+          if (n < 0) break;
+          for (int j = 0; j < n; ++j, ++n_tile) {
+            const int t0 = (run->tile0 + j) * kPaTile, s = (2 * n_tile + 1) % NS;
+            // (every tile in turn: a barrier's phases are told apart by their parity alone)
+            if (!wait_all(kv_full + s, ((2 * n_tile + 1) / NS) & 1)) return false;
+            if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
+              arrive(kv_empty + s);
+              continue;
+            }
+            uint4* tile = reinterpret_cast<uint4*>(smem + Sm::kKV + s * Sm::kTileBytes);
+            // A half whose exponent is all ones leaves its top bit clear below
+            uint32_t finite = 0x80008000u;
+#pragma unroll 8
+            for (int i = lane; i < Sm::kTileBytes / 16; i += 32) {
+              const uint4 u = tile[i];
+              finite &= (~u.x & kExp) + kExp;
+              finite &= (~u.y & kExp) + kExp;
+              finite &= (~u.z & kExp) + kExp;
+              finite &= (~u.w & kExp) + kExp;
+            }
+            if (__any_sync(0xFFFFFFFFu, finite != 0x80008000u)) {
+              for (int i = lane; i < Sm::kTileBytes / 16; i += 32) {
+                uint4 u = tile[i];
+                uint32_t* x = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((x[k] & kExp & 0xFFFFu) == (kExp & 0xFFFFu)) x[k] &= 0xFFFF0000u;
+                  if ((x[k] & kExp & 0xFFFF0000u) == (kExp & 0xFFFF0000u)) x[k] &= 0xFFFFu;
+                }
+                tile[i] = u;
+              }
+              if (lane == 0) const_cast<volatile Run*>(run)->bad = 1;
+            }
+            fence_proxy_async_smem();
+            arrive(v_clean + s);
+            arrive(kv_empty + s);
+          }
+          give_back();
+        }
+        give_back();
+        return true;
+      };
+      if (!look()) give_up();
+    } else if (warp >= 8) {
+      // ------------------------------------------------------------ the rows out
+      const int wl = warp - 8, row = tid & 127;
+      const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+      const int iq = row / p.Gt, g = row - iq * p.Gt;
+      uint8_t* rows_at = smem + Sm::kOut + wl * 32 * 128;
+      uint32_t ph[2] = {0, 0};
+      auto put_vector = [&](int i, uint4 v) {
+        *reinterpret_cast<uint4*>(rows_at + lane * 128 + (((i ^ lane) & 7) << 4)) = v;
+      };
+      auto rows_out = [&]() -> bool {
+        for (;;) {
+          const volatile Run* run = take();
+          if (!run) return false;
+          if (run->tiles < 0) break;
+          for (int w = 0; w < 2; ++w) {
+            const int dq = w * p.qt + iq;                  // the row's query in the group
+            const bool on = iq < p.qt && dq < run->n_q;
+            if (w * p.qt >= run->n_q) continue;
+            const bool any = run->first[w] < run->last[w], whole = run->whole;
+            const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
+            float m = -INFINITY, l = 0.0f;
+            if (any) {
+              if (!wait_all(stat_full + w, ph[w])) return false;
+              m = s_stat[w * 2 * kPaTile + row];
+              l = s_stat[w * 2 * kPaTile + kPaTile + row];
+              if (!wait_all(o_full + w, ph[w])) return false;
+              ph[w] ^= 1u;
+              tc_fence_after();
+            }
+            const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
+            float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
+            if (whole && p.prefix_lse && on) {
+              float f_own;
+              z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
+              f *= f_own;
+            }
+            // O of 32 channels; the infinities and NaNs among the values that the row sees are added
+            auto load = [&](int c, float (&o)[32]) {
+              if (any) tmem_load32(t_o + c, o);
+              else {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+              }
+              if (!run->bad) return;
+              const int pos = run->pos0 + dq, kmax = run->kmax;
+              const int hi = on ? seen_end(p, pos, kmax) : 0, lo = on ? seen_begin(p, pos) : 0;
+              const uint16_t* v = p.v + static_cast<int64_t>(run->head / p.chunks) * p.v_head + c;
+#pragma unroll 1
+              for (int j = run->first[w]; j < run->last[w]; ++j) {
+                const int t0 = (run->tile0 + j) * kPaTile;
+                if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) continue;
+#pragma unroll 1
+                for (int t = t0; t < min(t0 + kPaTile, kmax); ++t) {
+                  const uint4* src = reinterpret_cast<const uint4*>(v + (run->k0 + static_cast<int64_t>(t)) * p.v_stride);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint4 u = __ldg(src + i);
+                    const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const float2 f2 = unpack_16<kF16>(y[k]);
+                      if (t >= lo && t < hi) {
+                        if (!(fabsf(f2.x) < INFINITY)) o[8 * i + 2 * k] += f2.x;
+                        if (!(fabsf(f2.y) < INFINITY)) o[8 * i + 2 * k + 1] += f2.y;
+                      }
+                    }
+                  }
+                }
+              }
+            };
+            // (a lane stores vector lane % 8 of every fourth row)
+            float* part = p.partials + static_cast<size_t>(run->slot) * kPaRows * (D + 2);
+            uint8_t* base = whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part + 2 * kPaRows);
+            const int64_t row_at = whole ? out_row * (D * 2) : static_cast<int64_t>(w * kPaTile + row) * (D * 4);
+            const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on) >> (lane / 8);
+            uint8_t* to[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              to[i] = base + __shfl_sync(0xFFFFFFFFu, row_at, 4 * i + lane / 8) + (lane % 8) * 16;
+            auto store_rows = [&](int at) {
+              __syncwarp();
+              const int r = lane / 8;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + (4 * i + r) * 128 +
+                                                                (((lane ^ (4 * i + r)) & 7) << 4));
+                if ((rows_on >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = v;
+              }
+              __syncwarp();
+            };
+            if (whole) {
+              uint32_t h[D / 2];
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                load(c, o);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] *= f;
+                if (f_before != 0.0f) {
+                  const uint4* prev = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint4 u = prev[i];
+                    const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const float2 v = unpack_16<kF16>(y[k]);
+                      o[8 * i + 2 * k] = fmaf(v.x, f_before, o[8 * i + 2 * k]);
+                      o[8 * i + 2 * k + 1] = fmaf(v.y, f_before, o[8 * i + 2 * k + 1]);
+                    }
+                  }
+                }
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) h[(c + x) / 2] = pack_16<kF16>(o[x], o[x + 1]);
+              }
+              if (any) {
+                tc_fence_before();
+                arrive(o_empty + w);
+              }
+#pragma unroll
+              for (int c = 0; c < D; c += 64) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int x = c / 2 + 4 * i;
+                  put_vector(i, make_uint4(h[x], h[x + 1], h[x + 2], h[x + 3]));
+                }
+                store_rows(c * 2);
+              }
+              if (on && p.lse) p.lse[out_row] = z;
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                load(c, o);
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  put_vector(x / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
+                                               __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+                store_rows(c * 4);
+              }
+              if (any) {
+                tc_fence_before();
+                arrive(o_empty + w);
+              }
+              if (on) {
+                part[w * kPaTile + row] = m;
+                part[kPaRows + w * kPaTile + row] = l;
+              }
+            }
+          }
+          give_back();
+        }
+        give_back();
+        return true;
+      };
+      if (!rows_out()) give_up();
+    } else {
+      // ------------------------------------------------------------- softmax
+      const int w = warp >> 2, wl = warp & 3, row = tid & 127;
+      const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+      const uint32_t t_s = tmem + lanes + w * kPaTile, t_o = tmem + lanes + 2 * kPaTile + w * D;
+      const int iq = row / p.Gt;
+      const float to_log2 = p.scale_log2;
+      uint32_t ph_s = 0, ph_h = 0, ph_stat = 1;
+      // ---- a run's tiles
+      auto weigh = [&](const volatile Run& run) -> bool {
+        const int j0 = run.first[w], j1 = run.last[w];
+        if (j0 >= j1) return true;
+        const int dq = w * p.qt + iq;
+        const bool on = iq < p.qt && dq < run.n_q, any_on = __any_sync(0xFFFFFFFFu, on);
+        // (rows that nobody asked for see all: nothing of theirs matters, nothing is masked for them)
+        const int pos = run.pos0 + dq, kmax = run.kmax;
+        const int hi = on ? seen_end(p, pos, kmax) : INT32_MAX, lo = on ? seen_begin(p, pos) : 0;
+        float m_neg = on ? INFINITY : 0.0f, l = 0.0f;
+        for (int j = j0; j < j1; ++j) {
+          const int t0 = (run.tile0 + j) * kPaTile;
+          if (!wait_all(s_full + w, ph_s)) return false;
+          ph_s ^= 1u;
+          tc_fence_after();
+          if (!any_on) {
+            // (their P may be anything)
+            tc_fence_before();
+            arrive(p_half + w);
+            arrive(p_full + w);
+            ph_h ^= 1u;
+            continue;
+          }
+          const int from = lo - t0, to = hi - t0;          // tokens of the tile that the row sees
+          const bool masked = __any_sync(0xFFFFFFFFu, to < kPaTile || from > 0);
+          // In two halves of 64 tokens: P V of the first starts under the second.
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPaTile; c0 += kPaTile / 2) {
+            uint32_t pr[kPaTile / 4];
+            float sum;
+            auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
+              uint64_t sum2 = f2_pack(0.0f, 0.0f);
+              const float add = m_neg == INFINITY ? 0.0f : m_neg;      // (nothing but -inf seen so far)
+              const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
+              uint32_t s[2][32];
+              tmem_load32_start(t_s + c0, s[0]);
+#pragma unroll
+              for (int c = 0; c < kPaTile / 2; c += 32) {
+                uint32_t (&now)[32] = s[(c / 32) % 2];
+                tmem_load32_finish(now);
+                if (c + 32 < kPaTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
+                const uint32_t see = hidden ? tokens32(c0 + c, from, to) : 0xFFFFFFFFu;
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                  const uint64_t v =
+                      f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+                  float v0 = f2_lo(v), v1 = f2_hi(v);
+                  if (hidden) {
+                    v0 = see & (1u << x) ? v0 : -INFINITY;
+                    v1 = see & (2u << x) ? v1 : -INFINITY;
+                  }
+                  const float a = ex2(v0), b = ex2(v1);
+                  sum2 = f2_add(sum2, f2_pack(a, b));
+                  pr[(c + x) / 2] = pack_16<kF16>(a, b);
+                }
+              }
+              sum = f2_lo(sum2) + f2_hi(sum2);
+            };
+            // The maximum is looked for by rows that see tokens here and none before, and again
+            // where weights add up to more than kMostSum (or to no number).
+            // (each row by itself: what lies in one does not change another's roundings)
+            bool need = m_neg == INFINITY && from < c0 + kPaTile / 2 && to > c0, moved = !on;
+#pragma unroll 1
+            for (;;) {
+              if (__any_sync(0xFFFFFFFFu, need)) {
+                // m is set by the largest score so far, this half's included
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = c0; c < c0 + kPaTile / 2; c += 32) {
+                  uint32_t s[32];
+                  tmem_load32_start(t_s + c, s);
+                  tmem_load32_finish(s);
+                  const uint32_t see = masked ? tokens32(c, from, to) : 0xFFFFFFFFu;
+#pragma unroll
+                  for (int x = 0; x < 32; ++x)
+                    top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
+                }
+                const float now = need ? fminf(m_neg, kRise - top) : m_neg;
+                moved = moved || need;
+                const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+                m_neg = now;
+                l *= shrink;
+                if (j > j0 || c0 > 0) {
+                  // (earlier tiles are in O, S came after them; the first half may be on its way)
+                  if (c0 > 0) {
+                    if (!wait_all(h_full + w, ph_h)) return false;
+                    tc_fence_after();
+                  }
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    uint32_t y[16];
+                    tmem_load16(t_o + c, o);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
+                    tmem_store16(t_o + c, y);
+                  }
+                }
+              }
+              if (masked) weights(std::true_type{});
+              else weights(std::false_type{});
+              need = !moved && !(sum <= kMostSum);
+              if (!__any_sync(0xFFFFFFFFu, need)) break;
+            }
+            l += sum;
+            // P over the columns of S that have been read
+#pragma unroll
+            for (int c = 0; c < kPaTile / 4; c += 16) {
+              uint32_t x[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+              tmem_store16(t_s + c0 / 2 + c, x);
+            }
+            tmem_store_wait();
+            tc_fence_before();
+            arrive((c0 ? p_full : p_half) + w);
+          }
+          ph_h ^= 1u;
+        }
+        // (o_empty: the statistics of the run before have been read as well)
+        if (!wait_all(o_empty + w, ph_stat)) return false;
+        ph_stat ^= 1u;
+        s_stat[w * 2 * kPaTile + row] = -m_neg;
+        s_stat[w * 2 * kPaTile + kPaTile + row] = l;
+        arrive(stat_full + w);
+        return true;
+      };
+      auto softmax = [&]() -> bool {
+        for (;;) {
+          const volatile Run* run = take();
+          if (!run) return false;
+          if (run->tiles < 0) break;
+          if (!weigh(*run)) return false;
+          give_back();
+        }
+        give_back();
+        return true;
+      };
+      if (!softmax()) give_up();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+constexpr size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
+constexpr size_t kWsJoins = 256;
+constexpr size_t kWsPartials = a256(kWsJoins + kPaMaxCtas * sizeof(PromptJoin));
+constexpr size_t ws_total(int D) { return a256(kWsPartials + size_t(2) * kPaMaxCtas * kPaRows * (D + 2) * 4); }
+
+// [rows][heads][D] of 16-bit values, boxes of 64 channels, box_heads and box_rows.
+bool encode_heads(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_t heads, int D, int64_t row_stride,
+                  int64_t head_stride, uint32_t box_heads, uint32_t box_rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  // (the distance of the only one of a kind is never used; it has to be valid)
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : D) * 2,
+                                 static_cast<cuuint64_t>(rows > 1 ? row_stride : D) * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_rows}, step[3] = {1, 1, 1};
+  return encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kF16>
+nvr_status launch(PromptParams& p, cudaStream_t s) {
+  using Sm = PaSmem<D>;
+  static_assert(Sm::kTotal <= 227 * 1024, "shared memory");
+  static bool attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return NVR_ERR_CUDA;
+  const int sms = device_sm_count();
+  if (sms <= 0) return NVR_ERR_CUDA;
+  if (!attr_set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(prompt_attention_kernel<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kTotal);
+    if (e != cudaSuccess) return cuda_status(e);
+    attr_set[dev] = true;
+  }
+  p.groups = (p.max_q + 2 * p.qt - 1) / (2 * p.qt);
+  // the tiles of a key at most: of all keys, or of a window over the group's queries
+  int64_t tiles = (static_cast<int64_t>(p.max_k) + kPaTile - 1) / kPaTile;
+  if (p.window > 0) {
+    const int64_t w = (static_cast<int64_t>(p.window) + 2 * p.qt + kPaTile - 2) / kPaTile + 1;
+    if (w < tiles) tiles = w;
+  }
+  const int64_t items = static_cast<int64_t>(p.B) * p.groups;
+  const int64_t most = items * p.Hv * (tiles + kPaKeyCost);
+  if (items >= (int64_t(1) << 30) || tiles >= (int64_t(1) << 24) || most >= (int64_t(1) << 31) - (1 << 24))
+    return NVR_ERR_UNSUPPORTED;
+  int64_t grid = sms < kPaMaxCtas ? sms : kPaMaxCtas;
+  if (grid > (most + kPaMinChunk - 1) / kPaMinChunk) grid = (most + kPaMinChunk - 1) / kPaMinChunk;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = Sm::kTotal;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, kF16>, p);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (tiles <= kPaWhole) return NVR_OK;
+  return launch_prompt_join(p, D, kF16, static_cast<int>(grid), sms, s);
+}
+
+}  // namespace
+
+}  // namespace nvr
+
+using namespace nvr;
+
+extern "C" size_t prompt_attention_workspace_size(int Hq, int Hkv, int D) {
+  if (Hkv < 1 || Hq < 1 || Hq % Hkv || (D != 64 && D != 128)) return 0;
+  return ws_total(D);
+}
+
+extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+                                       int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride,
+                                       int64_t v_head_stride, nvr_dtype dt, int64_t T, int64_t Tk, int Hq, int Hkv,
+                                       int D, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int max_q,
+                                       int max_k, float scale, int causal, int window, const void* prefix_out,
+                                       const float* prefix_lse, void* out, float* lse, void* workspace,
+                                       size_t ws_bytes, nvr_stream_t stream) {
+  if (T < 0 || Tk < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65536) return NVR_ERR_INVALID_ARG;
+  if (dt != NVR_BF16 && dt != NVR_F16) return NVR_ERR_INVALID_ARG;
+  if (max_q < 0 || max_k < 0 || window < 0 || (window > 0 && !causal)) return NVR_ERR_INVALID_ARG;
+  if (!(scale > -INFINITY && scale < INFINITY)) return NVR_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return NVR_ERR_UNSUPPORTED;
+  if (!workspace || (prefix_out != nullptr) != (prefix_lse != nullptr)) return NVR_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !out || B < 1 || max_q < 1)) return NVR_ERR_INVALID_ARG;
+  if (Tk > 0 && (!k || !v)) return NVR_ERR_INVALID_ARG;
+  if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1 || max_q > INT32_MAX - 1024)
+    return NVR_ERR_UNSUPPORTED;
+  if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
+  if (!cu_k && Tk != T) return NVR_ERR_INVALID_ARG;
+  // heads may lie in any order, 16 bytes apart at least, but not in front of the first
+  auto bad = [&](int64_t rows, int64_t heads, int64_t stride, int64_t head_stride) {
+    return (rows > 1 && (stride < D || stride % 8)) || (heads > 1 && (head_stride < D || head_stride % 8)) ||
+           stride >= (int64_t(1) << 38) || head_stride >= (int64_t(1) << 38);
+  };
+  if (bad(T, Hq, q_stride, q_head_stride) || bad(Tk, Hkv, k_stride, k_head_stride) ||
+      bad(Tk, Hkv, v_stride, v_head_stride))
+    return NVR_ERR_INVALID_ARG;
+  if (off16(q) || off16(k) || off16(v) || off16(out) || off16(prefix_out) || off4(cu_q) || off4(cu_k) || off4(lse) ||
+      off4(prefix_lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return NVR_ERR_ALIGNMENT;
+  if (ws_bytes < ws_total(D)) return NVR_ERR_WORKSPACE;
+  if (T == 0) return NVR_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PromptParams p;
+  p.T = T; p.Tk = Tk;
+  p.Hq = Hq; p.G = Hq / Hkv;
+  // Heads of a KV head that share a row tile: the most that divide them and fill 7/8 of its
+  // 128 rows with whole queries (one always does).
+  p.Gt = 1;
+  for (int g = 2; g <= p.G && g <= kPaTile; ++g)
+    if (p.G % g == 0 && kPaTile / g * g >= kPaTile * 7 / 8) p.Gt = g;
+  p.qt = kPaTile / p.Gt;
+  p.chunks = p.G / p.Gt;
+  p.Hv = Hq / p.Gt;
+  p.cu_q = cu_q; p.cu_k = cu_k;
+  p.B = static_cast<int>(B); p.max_q = max_q;
+  p.max_k = cu_k ? max_k : max_q;
+  if (p.max_k > Tk) p.max_k = static_cast<int>(Tk);
+  p.scale_log2 = scale * 1.44269504088896341f;
+  p.causal = causal != 0;
+  p.window = window >= Tk ? 0 : window;                      // (then it hides nothing)
+  p.v = static_cast<const uint16_t*>(v); p.v_stride = v_stride; p.v_head = v_head_stride;
+  p.prefix_out = static_cast<const uint16_t*>(prefix_out); p.prefix_lse = prefix_lse;
+  p.out = static_cast<uint16_t*>(out); p.lse = lse;
+  p.status = reinterpret_cast<uint32_t*>(ws + kWsStatus);
+  p.joins = reinterpret_cast<PromptJoin*>(ws + kWsJoins);
+  p.partials = reinterpret_cast<float*>(ws + kWsPartials);
+  const bool f16 = dt == NVR_F16;
+  // (without keys nothing is loaded: the maps are of the queries, to be valid)
+  const bool keys = Tk > 0;
+  if (!encode_heads(&p.tm_q, q, f16, T, Hq, D, q_stride, q_head_stride, p.Gt, p.qt) ||
+      !encode_heads(&p.tm_k, keys ? k : q, f16, keys ? Tk : 1, keys ? Hkv : 1, D, k_stride, k_head_stride, 1, kPaTile) ||
+      !encode_heads(&p.tm_v, keys ? v : q, f16, keys ? Tk : 1, keys ? Hkv : 1, D, v_stride, v_head_stride, 1, kPaTile))
+    return NVR_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 128) return f16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  return f16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+}

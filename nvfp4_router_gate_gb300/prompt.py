@@ -1,0 +1,261 @@
+"""A prompt's operators beside the NVFP4 key/value cache: Python binding of
+include/nvfp4_prompt.h.
+
+* ``prompt_rope(q, k, positions, cos, sin, axes, ...)`` -> (q_out, k_out): RMS norm of the heads
+  and rotary positions with several axes
+* ``rope_axes(sections, turns=False)`` -> the axis of each pair
+* ``rope_axes_table(n_pos, sections, ...)`` -> (cos, sin) with frequencies of each axis's own
+* ``prompt_attention(q, k, v, ...)`` -> (out, lse): attention of packed prompts over their own
+  16-bit keys and values
+
+``PromptAttention`` keeps the workspace resident: its calls allocate nothing but
+outputs the caller does not pass (CUDA-graph capturable).  What a call with
+``stream=`` allocates belongs to that stream.
+"""
+
+import contextlib
+
+import torch
+
+from . import _native, new_workspace, nvr_read_device_status
+from .kv_cache import _empty, _empty_on, _on, _ptr, _raw_stream
+
+_BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
+_CODES = {_BF16: _native.NVR_BF16, _F32: _native.NVR_F32, _F16: _native.NVR_F16}
+_MAX_AXES = 8
+
+
+def _here(t, name):
+    """The tensor's device, which has to be the current one (launches go there)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch._C._cuda_getDevice()))
+    return t.device
+
+
+def _same(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, not %s" % (name, t.device, dev))
+
+
+def _rows(t, T, H, D, name):
+    """Token stride of t [T, H, D] with contiguous heads."""
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
+        raise ValueError("%s must have contiguous heads (a token stride is allowed)" % name)
+    return s0 if T > 1 else H * D
+
+
+def rope_axes(sections, turns=False):
+    """The axis of each pair of channels, where axis a has sections[a] pairs: the axes
+    one after the other, or (turns) taking turns for as long as they have pairs left."""
+    left = [int(n) for n in sections]
+    if not left or len(left) > _MAX_AXES or min(left) < 0:
+        raise ValueError("sections must be the pairs of 1 to %d axes" % _MAX_AXES)
+    if not turns:
+        return tuple(a for a, n in enumerate(left) for _ in range(n))
+    return tuple(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
+def rope_axes_table(n_pos, sections, turns=False, base=10000.0, device=None):
+    """cos and sin [n_pos, pairs] fp32 for rope_axes(sections, turns) where every axis has
+    frequencies of its own: pair j of the n of an axis turns by pos * base^(-j / n).
+    (Where the axes share one row of frequencies, rope_table gives the table.)"""
+    axes, seen, freq = rope_axes(sections, turns), {}, []
+    for a in axes:
+        j = seen[a] = seen.get(a, -1) + 1
+        freq.append(float(base) ** (-j / int(sections[a])))
+    freq = torch.tensor(freq, dtype=torch.float64, device=device or "cuda")
+    angle = torch.arange(n_pos, dtype=torch.float64, device=freq.device)[:, None] * freq
+    return angle.cos().float().contiguous(), angle.sin().float().contiguous()
+
+
+def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                q_out=None, k_out=None, out_dtype=None, stream=None):
+    """RMS norm of the heads of q [T, Hq, D] and k [T, Hkv, D] (where q_weight, k_weight
+    [D] are given) and rotary positions with several axes: pair i of a head turns by
+    column i of row positions[axes[i]] of cos and sin [n_pos, pairs].  positions is
+    [n_axes, T] int32 (or [T], one axis); axes a sequence of ints (``rope_axes``; None:
+    the first axis for all pairs).  cos None: no rotation.  q or k may be None.  Types:
+    bfloat16, float16 or float32; out_dtype (or q_out and k_out, which may be q and k
+    themselves) the same, or a 16-bit one for float32 heads.  Returns (q_out, k_out)."""
+    some = q if q is not None else k
+    dev = _here(some, "q" if q is not None else "k")
+    if some.dim() != 3:
+        raise ValueError("heads must be [T, heads, D]")
+    T, _, D = some.shape
+    dt = some.dtype
+    if dt not in _CODES:
+        raise TypeError("heads must be bfloat16, float16 or float32, got %s" % dt)
+    for t in (q_out, k_out):
+        if t is not None:
+            out_dtype = t.dtype if out_dtype is None else out_dtype
+    out_dtype = dt if out_dtype is None else out_dtype
+    if out_dtype is not dt and (dt is not _F32 or out_dtype not in _CODES):
+        raise TypeError("heads of %s do not become %s" % (dt, out_dtype))
+    args = []
+    outs = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError("%s_out without %s" % (name, name))
+            args.append((None, 0, 0, None, 0))
+            outs.append(None)
+            continue
+        if x.dim() != 3 or x.dtype is not dt or x.shape[0] != T or x.shape[2] != D or x.device != dev:
+            raise ValueError("%s must be [T, heads, D] of one type and device with the other" % name)
+        H = x.shape[1]
+        xs = _rows(x, T, H, D, name)
+        if out is None:
+            out = (_empty((T, H, D), dtype=out_dtype, device=dev) if stream is None else
+                   _empty_on(stream, (T, H, D), dtype=out_dtype, device=dev))
+        elif out.shape != x.shape or out.dtype is not out_dtype or out.device != dev:
+            raise ValueError("%s_out must be %s of %s on %s" % (name, tuple(x.shape), out_dtype, dev))
+        args.append((x.data_ptr(), xs, H, out.data_ptr(), _rows(out, T, H, D, name + "_out")))
+        outs.append(out)
+    rot = n_pos = n_axes = step = 0
+    code = None
+    if cos is not None:
+        if sin is None or positions is None or cos.dim() != 2:
+            raise ValueError("cos [n_pos, pairs] needs sin and positions")
+        n_pos, pairs = cos.shape
+        rot = 2 * pairs
+        if positions.dim() == 1:
+            positions = positions[None]
+        if positions.dim() != 2 or positions.dtype is not _I32 or positions.shape[1] != T or (T > 1 and positions.stride(1) != 1):
+            raise ValueError("positions must be int32 [n_axes, T], the tokens next to each other")
+        n_axes, step = positions.shape[0], positions.stride(0)
+        axes = (0,) * pairs if axes is None else axes
+        if len(axes) != pairs:
+            raise ValueError("%d axes for %d pairs" % (len(axes), pairs))
+        if not 1 <= n_axes <= _MAX_AXES or (pairs and not 0 <= min(axes) <= max(axes) < n_axes):
+            raise ValueError("axes must be in [0, %d), positions of 1 to %d axes" % (n_axes, _MAX_AXES))
+        code = bytes(axes)
+        _same(dev, positions=positions, cos=cos, sin=sin)
+    _same(dev, q_weight=q_weight, k_weight=k_weight)
+    n = n_pos * rot // 2
+    (qp, qs, Hq, qo, qos), (kp, ks, Hkv, ko, kos) = args
+    st = _native.lib().prompt_rope(
+        qp, qs, kp, ks, _CODES[dt], T, Hq, Hkv, D, positions.data_ptr() if rot else None, step, n_axes, code,
+        _ptr(cos, _F32, n, "cos") if rot else None, _ptr(sin, _F32, n, "sin") if rot else None, n_pos, rot,
+        bool(interleaved), _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight"), eps, qo, qos, ko, kos,
+        _CODES[out_dtype], _raw_stream(stream))
+    if st:
+        _native.check("prompt_rope", st)
+    return outs[0], outs[1]
+
+
+def prompt_attention_workspace_size(n_heads, n_kv_heads, D):
+    return int(_native.lib().prompt_attention_workspace_size(n_heads, n_kv_heads, D))
+
+
+def _offsets(cu, name):
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError("%s must be [B + 1]" % name)
+    return cu.shape[0] - 1
+
+
+def _attend(q, k, v, ws, cu_q=None, max_q=None, cu_k=None, max_k=None, scale=None, causal=True, window=0, prefix=None,
+            out=None, lse=None, stream=None):
+    dev = q.device
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or q.dtype not in (_BF16, _F16):
+        raise TypeError("q, k and v must be bfloat16 or float16, all three the same")
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("q must be [T, heads, D], k and v [Tk, n_kv_heads, D]")
+    T, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D:
+        raise ValueError("q has heads of %d channels, k of %d" % (D, Dk))
+    if cu_q is not None:
+        B = _offsets(cu_q, "cu_q")
+        if max_q is None:
+            raise ValueError("cu_q needs max_q, the most queries of a sequence")
+    elif max_q is None:
+        B, max_q = (1, T) if cu_k is None else (_offsets(cu_k, "cu_k"), None)
+        if max_q is None:
+            if T % B if B else T:
+                raise ValueError("%d queries for %d sequences: pass cu_q" % (T, B))
+            max_q = T // B if B else 0
+    else:
+        if max_q < 1 or T % max_q:
+            raise ValueError("%d queries are not sequences of %d: pass cu_q" % (T, max_q))
+        B = T // max_q
+    if cu_k is not None:
+        if _offsets(cu_k, "cu_k") != B:
+            raise ValueError("cu_k is of %d sequences, not %d" % (cu_k.shape[0] - 1, B))
+        if max_k is None:
+            raise ValueError("cu_k needs max_k, the most keys of a sequence")
+    elif Tk != T:
+        raise ValueError("%d keys for %d queries: pass cu_k" % (Tk, T))
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.device != dev:
+            raise ValueError("%s is on %s, not %s" % (name, t.device, dev))
+        if t.stride(2) != 1:
+            raise ValueError("%s must have contiguous channels" % name)
+    po = pl = None
+    if prefix is not None:
+        po, pl = _ptr(prefix[0], q.dtype, T * Hq * D, "prefix out"), _ptr(prefix[1], _F32, T * Hq, "prefix lse")
+        _same(dev, prefix=prefix[0], prefix_lse=prefix[1])
+    if out is None:
+        out = (_empty((T, Hq, D), dtype=q.dtype, device=dev) if stream is None else
+               _empty_on(stream, (T, Hq, D), dtype=q.dtype, device=dev))
+    _same(dev, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    st = _native.lib().prompt_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+        v.stride(1), _CODES[q.dtype], T, Tk, Hq, Hkv, D, _ptr(cu_q, _I32, B + 1, "cu_q"), _ptr(cu_k, _I32, B + 1, "cu_k"), B,
+        max_q, max_k or 0, D ** -0.5 if scale is None else scale, causal, window, po, pl,
+        _ptr(out, q.dtype, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1], _raw_stream(stream))
+    if st:
+        _native.check("prompt_attention", st)
+    return out, lse
+
+
+def prompt_attention(q, k, v, workspace=None, stream=None, **kw):
+    """Attention of q [T, Hq, D] over k and v [Tk, Hkv, D] (bfloat16 or float16; any token
+    and head strides) of packed sequences: cu_q [B + 1] int32 (with max_q, the most queries
+    of a sequence) gives each one's rows of q, cu_k (with max_k) those of k and v; without
+    cu_k they are cu_q's.  Without cu_q all sequences have max_q queries (without max_q,
+    either: one sequence).  scale defaults to D ** -0.5, causal to True (queries are a
+    sequence's last positions), window to 0 (none).  prefix=(out, lse) of the same queries
+    over other keys is joined with the result.  Returns (out [T, Hq, D], lse); lse [T, Hq]
+    fp32 is written when it is given."""
+    dev = _here(q, "q")
+    if workspace is None:
+        n = prompt_attention_workspace_size(q.shape[1], k.shape[1], q.shape[2])
+        # (zeroed on the stream that uses it)
+        with _on(stream) if stream is not None else contextlib.nullcontext():
+            workspace = new_workspace(n, dev)
+    _same(dev, workspace=workspace)
+    n = workspace.numel()
+    return _attend(q, k, v, (_ptr(workspace, _U8, n, "workspace"), n), stream=stream, **kw)
+
+
+class PromptAttention:
+    """prompt_attention with its workspace resident, for n_heads query heads on
+    n_kv_heads KV heads of head_dim channels.  The workspace serves one stream at a
+    time: calls that may run at once each need another one (``workspace=``, zeroed
+    once), graphs that may be replayed at once among them."""
+
+    def __init__(self, n_heads, n_kv_heads, head_dim, device=None):
+        n = prompt_attention_workspace_size(n_heads, n_kv_heads, head_dim)
+        if n == 0:
+            raise ValueError("%d query heads on %d KV heads of %d channels are not supported" % (
+                n_heads, n_kv_heads, head_dim))
+        self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+        self.workspace = new_workspace(n, torch.device(device or "cuda"))
+
+    def __call__(self, q, k, v, workspace=None, **kw):
+        dev = _here(q, "q")
+        if q.dim() != 3 or k.dim() != 3 or q.shape[1:] != (self.n_heads, self.head_dim) or k.shape[1] != self.n_kv_heads:
+            raise ValueError("q must be [T, %d, %d] and k [Tk, %d, %d]" % (
+                self.n_heads, self.head_dim, self.n_kv_heads, self.head_dim))
+        ws = self.workspace if workspace is None else workspace
+        _same(dev, workspace=ws)
+        n = ws.numel()
+        return _attend(q, k, v, (_ptr(ws, _U8, n, "workspace"), n), **kw)
+
+    def status(self, stream=None):
+        """The workspace status word (0 ok, 6: a bounded wait timed out)."""
+        return nvr_read_device_status(self.workspace, stream)
