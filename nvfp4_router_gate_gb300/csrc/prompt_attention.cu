@@ -13,10 +13,10 @@
 //                   over it, rescale O when the maximum moves;
 //   warps 8-11      the rows out: O from tensor memory, scaled, joined with the prefix,
 //                   stored, while the softmax warps are at the next rows already;
-//   warp 12         issues the products, alternating the row tiles, so that one
-//                   tile's softmax runs under the other's products;
-//   warp 13         walks the work and hands every role its runs;
-//   warp 14         copies queries, keys and values into swizzled shared memory (TMA);
+//   warps 12, 13    issue the products of row tile 0 and 1, so that one tile's softmax
+//                   runs under the other's products;
+//   warp 14         walks the work, hands every role its runs and copies their queries,
+//                   keys and values into swizzled shared memory (TMA);
 //   warp 15         looks tiles with masked tokens over for infinities and NaNs among
 //                   the values: a weight of zero would make NaNs of them.  They become
 //                   zeros; the rows that see them get them back at the end.
@@ -44,7 +44,7 @@ constexpr int kPaKeyCost = 1;              // starting and ending a key counts a
 constexpr int kPaMinChunk = 2;             // fewest places of a block in the flat order of the tiles
 constexpr int kPaWhole = 4;                // keys of at most this many tiles are not cut
 constexpr int kRuns = 3;                   // runs handed out ahead
-constexpr int kConsumers = 15;             // warps that read a run
+constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
 struct alignas(16) Run {
   int tiles;                               // -1: the end
@@ -206,13 +206,13 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
 
   if (tid == 0) {
     for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, kConsumers); }
-    for (int i = 0; i < NS; ++i) { mbar_init(kv_full + i, 1); mbar_init(kv_empty + i, 1 + i % 2); mbar_init(v_clean + i, 1); }
+    for (int i = 0; i < NS; ++i) { mbar_init(kv_full + i, 1); mbar_init(kv_empty + i, 2 + i % 2); mbar_init(v_clean + i, 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1); mbar_init(q_empty + i, 1); mbar_init(s_full + i, 1);
       mbar_init(p_half + i, 4); mbar_init(p_full + i, 4); mbar_init(h_full + i, 1);
       mbar_init(o_full + i, 1); mbar_init(o_empty + i, 4); mbar_init(stat_full + i, 4);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -269,7 +269,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag)) != 0;
   };
 
-  if (tid == 13 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
+  if (tid == 14 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
   if (p.cu_q && warp >= 8 && warp < 12) clear_rows<D>(p, blockIdx.x * 4 + warp - 8, gridDim.x * 4);
   if (f0 < f1) {
     // the next run to this warp, or null; its last reader frees it
@@ -289,10 +289,124 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
       if (lane == 0) mbar_arrive(bar);
     };
 
-    if (warp == 13) {
-      // ------------------------------------------------------------ the walk
-      int item = s_start[0], off = s_start[1], f = f0, n_run = 0;
-      bool ok = true;
+    if (warp == 12 || warp == 13) {
+      // -------------------------------------------------------- the products
+      // (a warp for each row tile: neither waits for the other's softmax)
+      const int w = warp - 12;
+      const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
+      const uint32_t q_low = desc_low(smem + Sm::kQ, 16) + w * (Sm::kTileBytes >> 4);
+      const uint32_t k_low = desc_low(smem + Sm::kKV, 16), v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
+      const uint32_t t_s = tmem + w * kPaTile, t_o = tmem + 2 * kPaTile + w * D;
+      constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
+      auto score = [&](int slot) {
+        const uint32_t k = k_low + slot * kTileLow;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
+            tc_mma_ss(t_s, q_low + o, k + o, id_s, i != 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto weigh = [&](int slot, bool add, int half) {
+        const uint32_t v = v_low + slot * kTileLow;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kPaTile / 32; ++k) {
+            // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
+            const int i = half * (kPaTile / 32) + k;
+            tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      auto have = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_all(bar, parity);
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t ph_q = 0, ph_p = 0, ph_o = 1, ph_clean[NS / 2] = {};
+      int n_tile = 0;                                      // tiles whose scores were issued (or passed by)
+      auto products = [&]() -> bool {
+        // the tile whose weights come next: 1, 2 its row tile's first, 4 its last one, 8 masked; 16 passed by
+        uint32_t prev = 0;
+        const volatile Run* run = nullptr;
+        int j = 0, n = 0, first = 0, last = 0, tile0 = 0, free_from = 0, free_to = 0;
+        for (bool more = true; more || prev;) {
+          uint32_t cur = 0;
+          while (more && j >= n) {
+            if (run) give_back();
+            run = take();
+            if (!run) return false;
+            n = run->tiles;
+            j = 0;
+            if (n < 0) { more = false; break; }
+            first = run->first[w]; last = run->last[w];
+            tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
+          }
+          if (more) {
+            cur = j >= first && j < last ? 1u | (j == first ? 2u : 0u) | (j + 1 == last ? 4u : 0u) : 16u;
+            const int t0 = (tile0 + j) * kPaTile;
+            if (t0 < free_from || t0 + kPaTile > free_to) cur |= 8u;
+            ++j;
+          }
+          const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
+          const uint32_t v_phase = ((2 * n_tile - 1) / NS) & 1, k_phase = ((2 * n_tile) / NS) & 1;
+          if (prev) {
+            // (passed by as well: a barrier's phases are told apart by their parity alone)
+            if (!have(kv_full + v_slot, v_phase)) return false;
+            if (prev & 8u) {
+              if (!have(v_clean + v_slot, ph_clean[v_slot / 2])) return false;
+              ph_clean[v_slot / 2] ^= 1u;
+            }
+            if (prev & 1u) {
+              if (prev & 2u) {
+                if (!have(o_empty + w, ph_o)) return false;
+                ph_o ^= 1u;
+              }
+              if (!have(p_half + w, ph_p)) return false;
+              weigh(v_slot, !(prev & 2u), 0);
+              commit(h_full + w);
+              if (!have(p_full + w, ph_p)) return false;
+              ph_p ^= 1u;
+              weigh(v_slot, true, 1);
+              if (prev & 4u) commit(o_full + w);
+            }
+            commit(kv_empty + v_slot);
+          }
+          if (cur) {
+            if (!have(kv_full + k_slot, k_phase)) return false;
+            if (cur & 1u) {
+              if (cur & 2u) {
+                if (!have(q_full + w, ph_q)) return false;
+                ph_q ^= 1u;
+              }
+              score(k_slot);
+              commit(s_full + w);
+              if (cur & 4u) commit(q_empty + w);
+            }
+            commit(kv_empty + k_slot);
+            ++n_tile;
+          }
+          prev = cur;
+        }
+        give_back();
+        return true;
+      };
+      if (!products()) give_up();
+      // nothing of this block's is under way when the tensor memory goes back
+      if (elect_one()) tc_commit(drained);
+      __syncwarp();
+      wait_all(drained, 0);
+    } else if (warp == 14) {
+      // ------------- the walk, and the queries, keys and values of its runs in
+      uint32_t sent_q[2] = {0, 0};
+      int n_load = 0, n_run = 0;
       auto hand_out = [&](const Run& r) {
         const int s = n_run % kRuns;
         if (!wait_all(run_empty + s, ((n_run / kRuns) & 1) ^ 1)) return false;
@@ -304,6 +418,44 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
         ++n_run;
         return true;
       };
+      auto tile = [&](const CUtensorMap* map, int head, int row) {
+        const int s = n_load % NS;
+        if (!wait_all(kv_empty + s, ((n_load / NS) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(kv_full + s, Sm::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(smem + Sm::kKV + s * Sm::kTileBytes + c * (kPaTile * 128), map, 64 * c, head, row, kv_full + s);
+        }
+        __syncwarp();
+        ++n_load;
+        return true;
+      };
+      auto queries = [&](const Run& r, int w) {
+        if (r.first[w] >= r.last[w]) return true;
+        if (!wait_all(q_empty + w, (sent_q[w] & 1) ^ 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + w, p.Gt * p.qt * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(smem + Sm::kQ + w * Sm::kTileBytes + c * (kPaTile * 128), &p.tm_q, 64 * c, r.head * p.Gt,
+                        r.q0 + w * p.qt, q_full + w);
+        }
+        __syncwarp();
+        ++sent_q[w];
+        return true;
+      };
+      auto copies = [&](const Run& r) {
+        const int row0 = r.k0 + r.tile0 * kPaTile, kv_head = r.head / p.chunks;
+        for (int j = 0; j < r.tiles; ++j) {
+          if (!tile(&p.tm_k, kv_head, row0 + j * kPaTile)) return false;
+          if (j == 0 && (!queries(r, 0) || !queries(r, 1))) return false;
+          if (!tile(&p.tm_v, kv_head, row0 + j * kPaTile)) return false;
+        }
+        return true;
+      };
+      int item = s_start[0], off = s_start[1], f = f0;
+      bool ok = true;
       PromptGroup next = prompt_group(p, item);
       for (; f < f1 && ok; ++item) {
         const PromptGroup g = next;
@@ -339,7 +491,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
             // this block holds a cut key's first part
             if (lane == 0 && n_parts > 1 && ta == 0)
               p.joins[blockIdx.x] = {n_parts, inside, r.q0, g.n, head * p.Gt, {0, 0, 0}};
-            ok = hand_out(r);
+            ok = hand_out(r) && copies(r);
           }
           off += end - f;
           f = end;
@@ -352,172 +504,6 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
         ok = hand_out(r);
       }
       if (!ok) give_up();
-    } else if (warp == 12) {
-      // -------------------------------------------------------- the products
-      const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
-      const uint32_t q_low = desc_low(smem + Sm::kQ, 16), k_low = desc_low(smem + Sm::kKV, 16);
-      const uint32_t v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
-      constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
-      auto score = [&](int w, int slot) {
-        const uint32_t q = q_low + w * kTileLow, k = k_low + slot * kTileLow, d = tmem + w * kPaTile;
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
-            tc_mma_ss(d, q + o, k + o, id_s, i != 0);
-          }
-        }
-        __syncwarp();
-      };
-      auto weigh = [&](int w, int slot, bool add, int half) {
-        const uint32_t v = v_low + slot * kTileLow, d = tmem + 2 * kPaTile + w * D, a = tmem + w * kPaTile;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kPaTile / 32; ++k) {
-            // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-            const int i = half * (kPaTile / 32) + k;
-            tc_mma_ts(d, a + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
-          }
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      auto have = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_all(bar, parity);
-        tc_fence_after();
-        return ok;
-      };
-      uint32_t ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_o[2] = {1, 1}, ph_clean[NS / 2] = {};
-      int n_tile = 0;                                      // tiles whose scores were issued
-      // a tile in work: bit 0-1: the row tiles it is of; 2-3: their first, 4-5: their last; 6: masked
-      auto products = [&]() -> bool {
-        uint32_t prev = 0;
-        const volatile Run* run = nullptr;
-        int j = 0, n = 0, first[2], last[2], tile0 = 0, free_from = 0, free_to = 0;
-        for (bool more = true; more || prev;) {
-          uint32_t cur = 0;
-          while (more && j >= n) {
-            if (run) give_back();
-            run = take();
-            if (!run) return false;
-            n = run->tiles;
-            j = 0;
-            if (n < 0) { more = false; break; }
-#pragma unroll
-            for (int w = 0; w < 2; ++w) { first[w] = run->first[w]; last[w] = run->last[w]; }
-            tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
-          }
-          if (more) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              if (j >= first[w] && j < last[w])
-                cur |= (1u << w) | (j == first[w] ? 4u << w : 0u) | (j + 1 == last[w] ? 16u << w : 0u);
-            const int t0 = (tile0 + j) * kPaTile;
-            if (t0 < free_from || t0 + kPaTile > free_to) cur |= 64u;
-            ++j;
-          }
-          const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
-          const uint32_t v_phase = ((2 * n_tile - 1) / NS) & 1, k_phase = ((2 * n_tile) / NS) & 1;
-          if (prev) {
-            if (!have(kv_full + v_slot, v_phase)) return false;
-            if (prev & 64u) {
-              if (!have(v_clean + v_slot, ph_clean[v_slot / 2])) return false;
-              ph_clean[v_slot / 2] ^= 1u;
-            }
-          }
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (prev & (1u << w)) {
-              if (prev & (4u << w)) {
-                if (!have(o_empty + w, ph_o[w])) return false;
-                ph_o[w] ^= 1u;
-              }
-              if (!have(p_half + w, ph_p[w])) return false;
-              weigh(w, v_slot, !(prev & (4u << w)), 0);
-              commit(h_full + w);
-              if (!have(p_full + w, ph_p[w])) return false;
-              ph_p[w] ^= 1u;
-              weigh(w, v_slot, true, 1);
-              if (prev & (16u << w)) commit(o_full + w);
-            }
-            if (cur && w == 0 && !have(kv_full + k_slot, k_phase)) return false;
-            if (cur & (1u << w)) {
-              if (cur & (4u << w)) {
-                if (!have(q_full + w, ph_q[w])) return false;
-                ph_q[w] ^= 1u;
-              }
-              score(w, k_slot);
-              commit(s_full + w);
-              if (cur & (16u << w)) commit(q_empty + w);
-            }
-          }
-          if (prev) commit(kv_empty + v_slot);
-          if (cur) {
-            commit(kv_empty + k_slot);
-            ++n_tile;
-          }
-          prev = cur;
-        }
-        give_back();
-        return true;
-      };
-      if (!products()) give_up();
-      // nothing of this block's is under way when the tensor memory goes back
-      if (elect_one()) tc_commit(drained);
-      __syncwarp();
-      wait_all(drained, 0);
-    } else if (warp == 14) {
-      // ------------------------------------------ queries, keys and values in
-      uint32_t sent_q[2] = {0, 0};
-      int n_load = 0;
-      auto copies = [&]() -> bool {
-        auto tile = [&](const CUtensorMap* map, int head, int row) {
-          const int s = n_load % NS;
-          if (!wait_all(kv_empty + s, ((n_load / NS) & 1) ^ 1)) return false;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(kv_full + s, Sm::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(smem + Sm::kKV + s * Sm::kTileBytes + c * (kPaTile * 128), map, 64 * c, head, row, kv_full + s);
-          }
-          __syncwarp();
-          ++n_load;
-          return true;
-        };
-        for (;;) {
-          const volatile Run* run = take();
-          if (!run) return false;
-          const int n = run->tiles;
-          if (n < 0) break;
-          const int head = run->head, row0 = run->k0 + run->tile0 * kPaTile, kv_head = head / p.chunks;
-          auto queries = [&](int w) {
-            if (run->first[w] >= run->last[w]) return true;
-            if (!wait_all(q_empty + w, (sent_q[w] & 1) ^ 1)) return false;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(q_full + w, p.Gt * p.qt * D * 2);
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(smem + Sm::kQ + w * Sm::kTileBytes + c * (kPaTile * 128), &p.tm_q, 64 * c, head * p.Gt,
-                            run->q0 + w * p.qt, q_full + w);
-            }
-            __syncwarp();
-            ++sent_q[w];
-            return true;
-          };
-          for (int j = 0; j < n; ++j) {
-            if (!tile(&p.tm_k, kv_head, row0 + j * kPaTile)) return false;
-            if (j == 0 && (!queries(0) || !queries(1))) return false;
-            if (!tile(&p.tm_v, kv_head, row0 + j * kPaTile)) return false;
-          }
-          give_back();
-        }
-        give_back();
-        return true;
-      };
-      if (!copies()) give_up();
       if (*abort_flag) {
         // copies in flight land before the block's memory goes away
         const uint64_t drain = globaltimer_ns() + 1000000000ull;
