@@ -25,8 +25,8 @@
 // S), O0 | O1 (D each).  S of the next tile follows P V of this one in issue
 // order, so S is never overwritten early and a complete S implies the earlier
 // P V complete.  P comes in two halves of 64 tokens: P V of the first runs under
-// the softmax of the second.  The products of a run's last tile and of the next
-// run's first one are issued alternately as well: the pipeline does not drain.
+// the softmax of the second.  A run's last products and the next run's first ones
+// follow each other in the same way: the pipeline does not drain.
 //
 // The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
 // equal chunks, one per block, the rows of cut keys joined by csrc/prompt_join.cu.
@@ -120,8 +120,25 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 32 columns of this warp's lanes without the wait, and the wait: the registers
+// 16 columns of this warp's lanes without the wait, and the wait: the registers
 // pass through it so that nothing reads them early.
+__device__ __forceinline__ void tmem_load16_start(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16_finish(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :: "memory");
+}
+
+// The same of 32 columns.
 __device__ __forceinline__ void tmem_load32_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -291,58 +308,48 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
 
     if (warp == 12 || warp == 13) {
       // -------------------------------------------------------- the products
-      // (a warp for each row tile: neither waits for the other's softmax)
+      // (A warp for each row tile: neither waits for the other's softmax.  One lane does it
+      // all: what lies between the arrival of P and the issue of the products is the chain
+      // that the tensor cores wait for.)
       const int w = warp - 12;
-      const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
-      const uint32_t q_low = desc_low(smem + Sm::kQ, 16) + w * (Sm::kTileBytes >> 4);
-      const uint32_t k_low = desc_low(smem + Sm::kKV, 16), v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
-      const uint32_t t_s = tmem + w * kPaTile, t_o = tmem + 2 * kPaTile + w * D;
-      constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
-      auto score = [&](int slot) {
-        const uint32_t k = k_low + slot * kTileLow;
-        if (elect_one()) {
+      auto products = [&]() -> bool {
+        const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
+        constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
+        const uint32_t q_low = desc_low(smem + Sm::kQ, 16) + w * kTileLow;
+        const uint32_t k_low = desc_low(smem + Sm::kKV, 16), v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
+        const uint32_t t_s = tmem + w * kPaTile, t_o = tmem + 2 * kPaTile + w * D;
+        auto score = [&](int slot) {
+          const uint32_t k = k_low + slot * kTileLow;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
             tc_mma_ss(t_s, q_low + o, k + o, id_s, i != 0);
           }
-        }
-        __syncwarp();
-      };
-      auto weigh = [&](int slot, bool add, int half) {
-        const uint32_t v = v_low + slot * kTileLow;
-        if (elect_one()) {
+        };
+        auto weigh = [&](int slot, bool add, int half) {
+          const uint32_t v = v_low + slot * kTileLow;
 #pragma unroll
-          for (int k = 0; k < kPaTile / 32; ++k) {
+          for (int x = 0; x < kPaTile / 32; ++x) {
             // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-            const int i = half * (kPaTile / 32) + k;
-            tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
+            const int i = half * (kPaTile / 32) + x;
+            tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || x != 0);
           }
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      auto have = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_all(bar, parity);
-        tc_fence_after();
-        return ok;
-      };
-      uint32_t ph_q = 0, ph_p = 0, ph_o = 1, ph_clean[NS / 2] = {};
-      int n_tile = 0;                                      // tiles whose scores were issued (or passed by)
-      auto products = [&]() -> bool {
+        };
+        auto have = [&](uint64_t* bar, uint32_t parity) {
+          return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag);
+        };
+        uint32_t ph_q = 0, ph_p = 0, ph_o = 1, clean = 0;    // (bit i of clean: the phase of slot 2 i + 1)
+        int n_tile = 0, n_run = 0;                           // tiles whose scores were issued (or passed by), runs taken
         // the tile whose weights come next: 1, 2 its row tile's first, 4 its last one, 8 masked; 16 passed by
         uint32_t prev = 0;
-        const volatile Run* run = nullptr;
         int j = 0, n = 0, first = 0, last = 0, tile0 = 0, free_from = 0, free_to = 0;
         for (bool more = true; more || prev;) {
           uint32_t cur = 0;
           while (more && j >= n) {
-            if (run) give_back();
-            run = take();
-            if (!run) return false;
+            if (n_run) mbar_arrive(run_empty + (n_run - 1) % kRuns);
+            if (!have(run_full + n_run % kRuns, (n_run / kRuns) & 1)) return false;
+            const volatile Run* run = s_runs + n_run % kRuns;
+            ++n_run;
             n = run->tiles;
             j = 0;
             if (n < 0) { more = false; break; }
@@ -355,54 +362,62 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
             if (t0 < free_from || t0 + kPaTile > free_to) cur |= 8u;
             ++j;
           }
+          // everything but P first
           const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
-          const uint32_t v_phase = ((2 * n_tile - 1) / NS) & 1, k_phase = ((2 * n_tile) / NS) & 1;
           if (prev) {
             // (passed by as well: a barrier's phases are told apart by their parity alone)
-            if (!have(kv_full + v_slot, v_phase)) return false;
+            if (!have(kv_full + v_slot, ((2 * n_tile - 1) / NS) & 1)) return false;
             if (prev & 8u) {
-              if (!have(v_clean + v_slot, ph_clean[v_slot / 2])) return false;
-              ph_clean[v_slot / 2] ^= 1u;
+              if (!have(v_clean + v_slot, (clean >> (v_slot / 2)) & 1u)) return false;
+              clean ^= 1u << (v_slot / 2);
             }
-            if (prev & 1u) {
-              if (prev & 2u) {
-                if (!have(o_empty + w, ph_o)) return false;
-                ph_o ^= 1u;
-              }
-              if (!have(p_half + w, ph_p)) return false;
-              weigh(v_slot, !(prev & 2u), 0);
-              commit(h_full + w);
-              if (!have(p_full + w, ph_p)) return false;
-              ph_p ^= 1u;
-              weigh(v_slot, true, 1);
-              if (prev & 4u) commit(o_full + w);
+            if (prev & 2u) {
+              if (!have(o_empty + w, ph_o)) return false;
+              ph_o ^= 1u;
             }
-            commit(kv_empty + v_slot);
           }
+          if (cur && !have(kv_full + k_slot, ((2 * n_tile) / NS) & 1)) return false;
+          if (prev & 1u) {
+            if (!have(p_half + w, ph_p)) return false;
+            tc_fence_after();
+            weigh(v_slot, !(prev & 2u), 0);
+            tc_commit(h_full + w);
+            if (!have(p_full + w, ph_p)) return false;
+            ph_p ^= 1u;
+            tc_fence_after();
+            weigh(v_slot, true, 1);
+            if (prev & 4u) tc_commit(o_full + w);
+          }
+          if (cur & 2u) {
+            if (!have(q_full + w, ph_q)) return false;
+            ph_q ^= 1u;
+          }
+          tc_fence_after();
+          if (cur & 1u) {
+            score(k_slot);
+            tc_commit(s_full + w);
+            if (cur & 4u) tc_commit(q_empty + w);
+          }
+          if (prev) tc_commit(kv_empty + v_slot);
           if (cur) {
-            if (!have(kv_full + k_slot, k_phase)) return false;
-            if (cur & 1u) {
-              if (cur & 2u) {
-                if (!have(q_full + w, ph_q)) return false;
-                ph_q ^= 1u;
-              }
-              score(k_slot);
-              commit(s_full + w);
-              if (cur & 4u) commit(q_empty + w);
-            }
-            commit(kv_empty + k_slot);
+            tc_commit(kv_empty + k_slot);
             ++n_tile;
           }
           prev = cur;
         }
-        give_back();
+        mbar_arrive(run_empty + (n_run - 1) % kRuns);
         return true;
       };
-      if (!products()) give_up();
-      // nothing of this block's is under way when the tensor memory goes back
-      if (elect_one()) tc_commit(drained);
+      if (lane == 0) {
+        if (!products()) {
+          report_timeout(p.status);
+          *abort_flag = 1;
+        }
+        // nothing of this block's is under way when the tensor memory goes back
+        tc_commit(drained);
+        wait_bounded(drained, 0, abort_flag);
+      }
       __syncwarp();
-      wait_all(drained, 0);
     } else if (warp == 14) {
       // ------------- the walk, and the queries, keys and values of its runs in
       uint32_t sent_q[2] = {0, 0};
@@ -603,39 +618,51 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
               z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
               f *= f_own;
             }
-            // O of 32 channels; the infinities and NaNs among the values that the row sees are added
-            auto load = [&](int c, float (&o)[32]) {
-              if (any) tmem_load32(t_o + c, o);
-              else {
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = 0.0f;
-              }
-              if (!run->bad) return;
+            if (any && run->bad) {
+              // the infinities and NaNs among the values of masked tiles that the row sees join its O
               const int pos = run->pos0 + dq, kmax = run->kmax;
               const int hi = on ? seen_end(p, pos, kmax) : 0, lo = on ? seen_begin(p, pos) : 0;
-              const uint16_t* v = p.v + static_cast<int64_t>(run->head / p.chunks) * p.v_head + c;
 #pragma unroll 1
-              for (int j = run->first[w]; j < run->last[w]; ++j) {
-                const int t0 = (run->tile0 + j) * kPaTile;
-                if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) continue;
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_load16_start(t_o + c, o);
+                tmem_load16_finish(o);
+                const uint16_t* v = p.v + static_cast<int64_t>(run->head / p.chunks) * p.v_head + c;
 #pragma unroll 1
-                for (int t = t0; t < min(t0 + kPaTile, kmax); ++t) {
+                for (int t = (run->tile0 + run->first[w]) * kPaTile; t < min((run->tile0 + run->last[w]) * kPaTile, kmax); ++t) {
+                  const int t0 = t & ~(kPaTile - 1);
+                  if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
+                    t = t0 + kPaTile - 1;                    // (an unmasked tile's are in O)
+                    continue;
+                  }
                   const uint4* src = reinterpret_cast<const uint4*>(v + (run->k0 + static_cast<int64_t>(t)) * p.v_stride);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
+                  for (int i = 0; i < 2; ++i) {
                     const uint4 u = __ldg(src + i);
                     const uint32_t y[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                       const float2 f2 = unpack_16<kF16>(y[k]);
-                      if (t >= lo && t < hi) {
-                        if (!(fabsf(f2.x) < INFINITY)) o[8 * i + 2 * k] += f2.x;
-                        if (!(fabsf(f2.y) < INFINITY)) o[8 * i + 2 * k + 1] += f2.y;
-                      }
+                      uint32_t &a = o[8 * i + 2 * k], &b = o[8 * i + 2 * k + 1];
+                      const bool sees = t >= lo && t < hi;
+                      if (sees && !(fabsf(f2.x) < INFINITY)) a = __float_as_uint(__uint_as_float(a) + f2.x);
+                      if (sees && !(fabsf(f2.y) < INFINITY)) b = __float_as_uint(__uint_as_float(b) + f2.y);
                     }
                   }
                 }
+                tmem_store16(t_o + c, o);
               }
+              tmem_store_wait();
+            }
+            // 16 channels of O
+            auto load = [&](int c, float (&o)[16]) {
+              uint32_t y[16];
+              if (any) {
+                tmem_load16_start(t_o + c, y);
+                tmem_load16_finish(y);
+              }
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = any ? __uint_as_float(y[x]) : 0.0f;
             };
             // (a lane stores vector lane % 8 of every fourth row)
             float* part = p.partials + static_cast<size_t>(run->slot) * kPaRows * (D + 2);
@@ -658,53 +685,52 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
               __syncwarp();
             };
             if (whole) {
-              uint32_t h[D / 2];
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 64) {
+#pragma unroll 1
+                for (int c = c0; c < c0 + 64; c += 16) {
+                  float o[16];
+                  load(c, o);
 #pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                load(c, o);
+                  for (int x = 0; x < 16; ++x) o[x] *= f;
+                  if (f_before != 0.0f) {
+                    const uint4* prev = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= f;
-                if (f_before != 0.0f) {
-                  const uint4* prev = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c);
+                    for (int i = 0; i < 2; ++i) {
+                      const uint4 u = prev[i];
+                      const uint32_t y[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const uint4 u = prev[i];
-                    const uint32_t y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      const float2 v = unpack_16<kF16>(y[k]);
-                      o[8 * i + 2 * k] = fmaf(v.x, f_before, o[8 * i + 2 * k]);
-                      o[8 * i + 2 * k + 1] = fmaf(v.y, f_before, o[8 * i + 2 * k + 1]);
+                      for (int k = 0; k < 4; ++k) {
+                        const float2 v = unpack_16<kF16>(y[k]);
+                        o[8 * i + 2 * k] = fmaf(v.x, f_before, o[8 * i + 2 * k]);
+                        o[8 * i + 2 * k + 1] = fmaf(v.y, f_before, o[8 * i + 2 * k + 1]);
+                      }
                     }
                   }
+#pragma unroll
+                  for (int x = 0; x < 16; x += 8)
+                    put_vector((c - c0 + x) / 8, make_uint4(pack_16<kF16>(o[x], o[x + 1]), pack_16<kF16>(o[x + 2], o[x + 3]),
+                                                            pack_16<kF16>(o[x + 4], o[x + 5]), pack_16<kF16>(o[x + 6], o[x + 7])));
                 }
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) h[(c + x) / 2] = pack_16<kF16>(o[x], o[x + 1]);
-              }
-              if (any) {
-                tc_fence_before();
-                arrive(o_empty + w);
-              }
-#pragma unroll
-              for (int c = 0; c < D; c += 64) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int x = c / 2 + 4 * i;
-                  put_vector(i, make_uint4(h[x], h[x + 1], h[x + 2], h[x + 3]));
+                if (any && c0 + 64 == D) {
+                  tc_fence_before();
+                  arrive(o_empty + w);
                 }
-                store_rows(c * 2);
+                store_rows(c0 * 2);
               }
               if (on && p.lse) p.lse[out_row] = z;
             } else {
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
-                float o[32];
-                load(c, o);
 #pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                  put_vector(x / 4, make_uint4(__float_as_uint(o[x]), __float_as_uint(o[x + 1]),
-                                               __float_as_uint(o[x + 2]), __float_as_uint(o[x + 3])));
+                for (int i = 0; i < 8; i += 4) {
+                  float o[16];
+                  load(c + 4 * i, o);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    put_vector(i + x, make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
+                                                 __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
+                }
                 store_rows(c * 4);
               }
               if (any) {
@@ -725,6 +751,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
       if (!rows_out()) give_up();
     } else {
       // ------------------------------------------------------------- softmax
+      constexpr int kHalf = kPaTile / 2;
       const int w = warp >> 2, wl = warp & 3, row = tid & 127;
       const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
       const uint32_t t_s = tmem + lanes + w * kPaTile, t_o = tmem + lanes + 2 * kPaTile + w * D;
@@ -735,118 +762,133 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
       auto weigh = [&](const volatile Run& run) -> bool {
         const int j0 = run.first[w], j1 = run.last[w];
         if (j0 >= j1) return true;
-        const int dq = w * p.qt + iq;
+        const int dq = w * p.qt + iq, t00 = run.tile0 * kPaTile;
         const bool on = iq < p.qt && dq < run.n_q, any_on = __any_sync(0xFFFFFFFFu, on);
         // (rows that nobody asked for see all: nothing of theirs matters, nothing is masked for them)
         const int pos = run.pos0 + dq, kmax = run.kmax;
-        const int hi = on ? seen_end(p, pos, kmax) : INT32_MAX, lo = on ? seen_begin(p, pos) : 0;
+        const int hi = on ? seen_end(p, pos, kmax) - t00 : 0, lo = on ? seen_begin(p, pos) - t00 : 0;
+        // every row of the warp sees all tokens of the tiles [full0, full1)
+        const int full0 = (max(__reduce_max_sync(0xFFFFFFFFu, on ? lo : 0), 0) + kPaTile - 1) / kPaTile;
+        const int full1 = max(__reduce_min_sync(0xFFFFFFFFu, on ? hi : INT32_MAX), 0) / kPaTile;
         float m_neg = on ? INFINITY : 0.0f, l = 0.0f;
+        uint32_t s[2][32], pr[kHalf / 2];
+        float sum = 0.0f;
+        // The weights of 64 tokens from column c0 on; `next`: the first 32 columns that come after them
+        auto weights = [&](auto hidden, int c0, int from, int to) {      // hidden: some tokens may not be seen
+          uint64_t sum2 = f2_pack(0.0f, 0.0f);
+          const float add = m_neg == INFINITY ? 0.0f : m_neg;            // (nothing but -inf seen so far)
+          const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t (&now)[32] = s[c / 32];
+            tmem_load32_finish(now);
+            if (c == 0) tmem_load32_start(t_s + c0 + 32, s[1]);
+            const uint32_t see = hidden ? tokens32(c0 + c, from, to) : 0xFFFFFFFFu;
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const uint64_t v = f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
+              float v0 = f2_lo(v), v1 = f2_hi(v);
+              if (hidden) {
+                v0 = see & (1u << x) ? v0 : -INFINITY;
+                v1 = see & (2u << x) ? v1 : -INFINITY;
+              }
+              const float a = ex2(v0), b = ex2(v1);
+              sum2 = f2_add(sum2, f2_pack(a, b));
+              pr[(c + x) / 2] = pack_16<kF16>(a, b);
+            }
+          }
+          sum = f2_lo(sum2) + f2_hi(sum2);
+        };
+        // The same where tokens may be hidden or the maximum moves.  It is looked for by rows that
+        // see tokens here and none before, and again where weights add up to more than kMostSum
+        // (or to no number).  (Each row by itself: what lies in one does not change another's
+        // roundings.)
+        auto weights_any = [&](int c0, int from, int to, bool started, bool again) -> bool {
+          const bool sees = on && from < c0 + kHalf && to > c0;
+          bool need = (m_neg == INFINITY && sees) || again, moved = !on;
+#pragma unroll 1
+          for (;;) {
+            if (__any_sync(0xFFFFFFFFu, need)) {
+              // m is set by the largest score so far, this half's included
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = c0; c < c0 + kHalf; c += 32) {
+                tmem_load32_start(t_s + c, s[0]);
+                tmem_load32_finish(s[0]);
+                const uint32_t see = tokens32(c, from, to);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[0][x]) * to_log2 : -INFINITY);
+              }
+              const float now = need ? fminf(m_neg, kRise - top) : m_neg;
+              moved = moved || need;
+              const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+              m_neg = now;
+              l *= shrink;
+              if (started || c0 > 0) {
+                // (earlier tiles are in O, S came after them; the first half may be on its way)
+                if (c0 > 0) {
+                  if (!wait_all(h_full + w, ph_h)) return false;
+                  tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t y[16];
+                  tmem_load16_start(t_o + c, y);
+                  tmem_load16_finish(y);
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * shrink);
+                  tmem_store16(t_o + c, y);
+                }
+              }
+            }
+            tmem_load32_start(t_s + c0, s[0]);
+            weights(std::true_type{}, c0, from, to);
+            need = !moved && !(sum <= kMostSum);
+            if (!__any_sync(0xFFFFFFFFu, need)) return true;
+          }
+        };
+#pragma unroll 1
         for (int j = j0; j < j1; ++j) {
-          const int t0 = (run.tile0 + j) * kPaTile;
           if (!wait_all(s_full + w, ph_s)) return false;
           ph_s ^= 1u;
           tc_fence_after();
-          if (!any_on) {
-            // (their P may be anything)
+          if (any_on) {
+            const bool plain = j >= full0 && j < full1 && j > j0;
+            const int from = on ? lo - j * kPaTile : 0, to = on ? hi - j * kPaTile : kPaTile;     // tokens that the row sees
+            if (plain) tmem_load32_start(t_s, s[0]);
+            // In two halves of 64 tokens: P V of the first starts under the second.
+#pragma unroll 1
+            for (int c0 = 0; c0 < kPaTile; c0 += kHalf) {
+              bool again = false;
+              if (plain) {
+                weights(std::false_type{}, c0, from, to);
+                if (c0 == 0) tmem_load32_start(t_s + kHalf, s[0]);
+                again = on && !(sum <= kMostSum);
+              }
+              if (!plain || __any_sync(0xFFFFFFFFu, again || m_neg == INFINITY)) {
+                if (plain) tmem_load32_finish(s[0]);
+                if (!weights_any(c0, from, to, j > j0, again)) return false;
+                if (plain && c0 == 0) tmem_load32_start(t_s + kHalf, s[0]);
+              }
+              l += sum;
+              // P over the columns of S that have been read
+#pragma unroll
+              for (int c = 0; c < kHalf / 2; c += 16) {
+                uint32_t x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+                tmem_store16(t_s + c0 / 2 + c, x);
+              }
+              tmem_store_wait();
+              tc_fence_before();
+              arrive((c0 ? p_full : p_half) + w);
+            }
+          } else {
+            // (rows that nobody asked for: their P may be anything)
             tc_fence_before();
             arrive(p_half + w);
             arrive(p_full + w);
-            ph_h ^= 1u;
-            continue;
-          }
-          const int from = lo - t0, to = hi - t0;          // tokens of the tile that the row sees
-          const bool masked = __any_sync(0xFFFFFFFFu, to < kPaTile || from > 0);
-          // In two halves of 64 tokens: P V of the first starts under the second.
-#pragma unroll 1
-          for (int c0 = 0; c0 < kPaTile; c0 += kPaTile / 2) {
-            uint32_t pr[kPaTile / 4];
-            float sum;
-            auto weights = [&](auto hidden) {              // hidden: some tokens are not seen
-              uint64_t sum2 = f2_pack(0.0f, 0.0f);
-              const float add = m_neg == INFINITY ? 0.0f : m_neg;      // (nothing but -inf seen so far)
-              const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
-              uint32_t s[2][32];
-              tmem_load32_start(t_s + c0, s[0]);
-#pragma unroll
-              for (int c = 0; c < kPaTile / 2; c += 32) {
-                uint32_t (&now)[32] = s[(c / 32) % 2];
-                tmem_load32_finish(now);
-                if (c + 32 < kPaTile / 2) tmem_load32_start(t_s + c0 + c + 32, s[(c / 32 + 1) % 2]);
-                const uint32_t see = hidden ? tokens32(c0 + c, from, to) : 0xFFFFFFFFu;
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                  const uint64_t v =
-                      f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
-                  float v0 = f2_lo(v), v1 = f2_hi(v);
-                  if (hidden) {
-                    v0 = see & (1u << x) ? v0 : -INFINITY;
-                    v1 = see & (2u << x) ? v1 : -INFINITY;
-                  }
-                  const float a = ex2(v0), b = ex2(v1);
-                  sum2 = f2_add(sum2, f2_pack(a, b));
-                  pr[(c + x) / 2] = pack_16<kF16>(a, b);
-                }
-              }
-              sum = f2_lo(sum2) + f2_hi(sum2);
-            };
-            // The maximum is looked for by rows that see tokens here and none before, and again
-            // where weights add up to more than kMostSum (or to no number).
-            // (each row by itself: what lies in one does not change another's roundings)
-            bool need = m_neg == INFINITY && from < c0 + kPaTile / 2 && to > c0, moved = !on;
-#pragma unroll 1
-            for (;;) {
-              if (__any_sync(0xFFFFFFFFu, need)) {
-                // m is set by the largest score so far, this half's included
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int c = c0; c < c0 + kPaTile / 2; c += 32) {
-                  uint32_t s[32];
-                  tmem_load32_start(t_s + c, s);
-                  tmem_load32_finish(s);
-                  const uint32_t see = masked ? tokens32(c, from, to) : 0xFFFFFFFFu;
-#pragma unroll
-                  for (int x = 0; x < 32; ++x)
-                    top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[x]) * to_log2 : -INFINITY);
-                }
-                const float now = need ? fminf(m_neg, kRise - top) : m_neg;
-                moved = moved || need;
-                const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-                m_neg = now;
-                l *= shrink;
-                if (j > j0 || c0 > 0) {
-                  // (earlier tiles are in O, S came after them; the first half may be on its way)
-                  if (c0 > 0) {
-                    if (!wait_all(h_full + w, ph_h)) return false;
-                    tc_fence_after();
-                  }
-#pragma unroll 1
-                  for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    uint32_t y[16];
-                    tmem_load16(t_o + c, o);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(o[x] * shrink);
-                    tmem_store16(t_o + c, y);
-                  }
-                }
-              }
-              if (masked) weights(std::true_type{});
-              else weights(std::false_type{});
-              need = !moved && !(sum <= kMostSum);
-              if (!__any_sync(0xFFFFFFFFu, need)) break;
-            }
-            l += sum;
-            // P over the columns of S that have been read
-#pragma unroll
-            for (int c = 0; c < kPaTile / 4; c += 16) {
-              uint32_t x[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-              tmem_store16(t_s + c0 / 2 + c, x);
-            }
-            tmem_store_wait();
-            tc_fence_before();
-            arrive((c0 ? p_full : p_half) + w);
           }
           ph_h ^= 1u;
         }
