@@ -93,9 +93,7 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights p_t enter the
  * second product rounded to dt, relative to a running maximum (fp16: a weight below 2^-32
  * of the largest is lost there; bf16: results above 2^100 may overflow); results do not
- * depend on the order in which the GPU runs the blocks.  One kernel and, unless no key can
- * be cut over blocks, a second one that joins the parts of those that were.  Calls whose
- * work does not fit 31 bits (tiles of 128 keys and of 128 rows, one count over the call) are
+ * depend on the order in which the GPU runs the blocks.  One kernel.  Calls whose work does not fit 31 bits (tiles of 128 keys and of 128 rows, one count over the call) are
  * NVR_ERR_UNSUPPORTED.  The workspace's size depends on D alone (the heads are checked): it
  * holds partial results of the resident blocks, of one call at a time.  A bounded wait that
  * runs out sets its status word (nvr_read_device_status).

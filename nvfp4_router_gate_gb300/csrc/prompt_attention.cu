@@ -28,8 +28,13 @@
 // the softmax of the second.  A run's last products and the next run's first ones
 // follow each other in the same way: the pipeline does not drain.
 //
-// The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in
-// equal chunks, one per block, the rows of cut keys joined by csrc/prompt_join.cu.
+// The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in equal
+// chunks, one per block.  The warps that come last to their rows of a cut key join the
+// parts (the others have written theirs, or are at it), in the parts' order:
+//   m = max m_i,  w_i = 2^(m_i - m),  out = sum w_i O_i / sum w_i l_i.
+// Usually that is the key's first part, the last work of its block (a second kernel took
+// 24 to 29 us behind all of them; with the parts as a block's first work the next run
+// waited for the joining).
 #include <type_traits>
 
 #include "../../include/nvfp4_prompt.h"
@@ -40,8 +45,11 @@ namespace nvr {
 namespace {
 
 constexpr int kPaThreads = 512;
-constexpr int kPaKeyCost = 1;              // starting and ending a key counts as this many tiles
-constexpr int kPaMinChunk = 2;             // fewest places of a block in the flat order of the tiles
+constexpr int kPaPlaces = 2;               // places of a tile in the flat order
+constexpr int kPaKeyCost = 3;              // starting and ending a key counts as this many places
+// Fewest places of a block; of a key of n tiles it has sqrt(n) tiles at least: the parts are
+// joined one after the other.
+constexpr int kPaMinChunk = 4;
 constexpr int kPaWhole = 4;                // keys of at most this many tiles are not cut
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
@@ -54,9 +62,10 @@ struct alignas(16) Run {
   int n_q, pos0, kmax;                     // queries, position of the first one, keys that exist
   int first[2], last[2];                   // tiles of each row tile: [first, last)
   int free_to, free_from;                  // tiles inside [free_from, free_to) of the tokens are seen by every row
-  int whole, slot;                         // all of its key, or a part: in this slot
+  int parts, part;                         // of its key (1: all of it), which one
+  int block, tail;                         // the block of the first part, whether it is in its second slot
   int bad;                                 // values of the run were not finite
-  int pad;
+  int pad[2];
 };
 
 template <int D>
@@ -162,7 +171,7 @@ __device__ __forceinline__ void tmem_load32_finish(uint32_t (&r)[32]) {
 }
 
 // A key's length in the flat order: its tiles, then places without work.
-__device__ __forceinline__ int key_cost(const PromptGroup& g) { return g.n > 0 ? g.tiles + kPaKeyCost : 0; }
+__device__ __forceinline__ int key_cost(const PromptGroup& g) { return g.n > 0 ? kPaPlaces * g.tiles + kPaKeyCost : 0; }
 
 // Zeros, and an lse of -inf, for the rows that no sequence covers: in front of the first
 // one, behind the last one (a batch padded for a captured graph), past max_q in one.
@@ -196,44 +205,763 @@ __device__ __forceinline__ void clear_rows(const PromptParams& p, int unit, int 
   }
 }
 
+// Where a block's shared memory has what.
+template <int D>
+struct Block {
+  uint8_t* smem;
+  Run* s_runs;
+  float* s_stat;                           // [row tile][m, l][row]
+  uint64_t *run_full, *run_empty, *kv_full, *kv_empty, *v_clean, *q_full, *q_empty, *s_full, *p_half, *p_full, *h_full,
+      *o_full, *o_empty, *stat_full, *drained;
+  uint32_t* tmem_holder;
+  volatile int* abort_flag;
+  int* s_start;                            // item of the chunk's start, offset inside it
+
+  __device__ __forceinline__ Block() {
+    using Sm = PaSmem<D>;
+    constexpr int NS = Sm::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    s_runs = reinterpret_cast<Run*>(smem + Sm::kRunsAt);
+    s_stat = reinterpret_cast<float*>(smem + Sm::kStat);
+    run_full = reinterpret_cast<uint64_t*>(smem + Sm::kBarAt);
+    run_empty = run_full + kRuns;
+    kv_full = run_empty + kRuns;
+    kv_empty = kv_full + NS;
+    v_clean = kv_empty + NS;
+    q_full = v_clean + NS;
+    q_empty = q_full + 2;
+    s_full = q_empty + 2;
+    p_half = s_full + 2;
+    p_full = p_half + 2;
+    h_full = p_full + 2;
+    o_full = h_full + 2;
+    o_empty = o_full + 2;
+    stat_full = o_empty + 2;
+    drained = stat_full + 2;
+    tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+    abort_flag = reinterpret_cast<int*>(tmem_holder) + 1;
+    s_start = reinterpret_cast<int*>(tmem_holder) + 2;
+  }
+};
+
+// One warp of it.
+template <int D>
+struct Member : Block<D> {
+  int lane = threadIdx.x & 31, n_taken = 0;
+
+  __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, this->abort_flag)) != 0;
+  }
+  __device__ __forceinline__ void arrive(uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+  // the next run, or null; its last reader frees it
+  __device__ __forceinline__ const volatile Run* take() {
+    const int s = n_taken % kRuns;
+    if (!wait_all(this->run_full + s, (n_taken / kRuns) & 1)) return nullptr;
+    ++n_taken;
+    return this->s_runs + s;
+  }
+  __device__ __forceinline__ void give_back() { arrive(this->run_empty + (n_taken - 1) % kRuns); }
+};
+
+// The roles.  False: gave up waiting.
+//
+// What is not run all the time is bound by fetching its instructions, about 700 clocks for
+// eight of them when they come from L2 (measured: 55000 clocks for joining two parts in
+// unrolled code), and sixteen warps of six roles share the instruction cache.  So all but the
+// inner loop of the softmax and the issue of the products is in loops of few instructions.
+
+// The products, by one lane of a warp for each row tile w (neither waits for the other's
+// softmax): what lies between the arrival of P and the issue of the products is the chain
+// that the tensor cores wait for.
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kPaThreads, 1)
-prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+__device__ __forceinline__ bool products(uint32_t tmem, int w) {
   using Sm = PaSmem<D>;
   constexpr int NS = Sm::kSlots;
+  Member<D> me;
+  const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
+  constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
+  const uint32_t q_low = desc_low(me.smem + Sm::kQ, 16) + w * kTileLow;
+  const uint32_t k_low = desc_low(me.smem + Sm::kKV, 16), v_low = desc_low(me.smem + Sm::kKV, kPaTile * 128);
+  const uint32_t t_s = tmem + w * kPaTile, t_o = tmem + 2 * kPaTile + w * D;
+  auto score = [&](int slot) {
+    const uint32_t k = k_low + slot * kTileLow;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
+      tc_mma_ss(t_s, q_low + o, k + o, id_s, i != 0);
+    }
+  };
+  auto weigh = [&](int slot, bool add, int half) {
+    const uint32_t v = v_low + slot * kTileLow;
+#pragma unroll
+    for (int x = 0; x < kPaTile / 32; ++x) {
+      // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
+      const int i = half * (kPaTile / 32) + x;
+      tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || x != 0);
+    }
+  };
+  auto have = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, me.abort_flag);
+  };
+  uint32_t ph_q = 0, ph_p = 0, ph_o = 1, clean = 0;    // (bit i of clean: the phase of slot 2 i + 1)
+  int n_tile = 0, n_run = 0;                           // tiles whose scores were issued (or passed by), runs taken
+  // the tile whose weights come next: 1, 2 its row tile's first, 4 its last one, 8 masked; 16 passed by
+  uint32_t prev = 0;
+  int j = 0, n = 0, first = 0, last = 0, tile0 = 0, free_from = 0, free_to = 0;
+  for (bool more = true; more || prev;) {
+    uint32_t cur = 0;
+    while (more && j >= n) {
+      if (n_run) mbar_arrive(me.run_empty + (n_run - 1) % kRuns);
+      if (!have(me.run_full + n_run % kRuns, (n_run / kRuns) & 1)) return false;
+      const volatile Run* run = me.s_runs + n_run % kRuns;
+      ++n_run;
+      n = run->tiles;
+      j = 0;
+      if (n < 0) { more = false; break; }
+      first = run->first[w]; last = run->last[w];
+      tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
+    }
+    if (more) {
+      cur = j >= first && j < last ? 1u | (j == first ? 2u : 0u) | (j + 1 == last ? 4u : 0u) : 16u;
+      const int t0 = (tile0 + j) * kPaTile;
+      if (t0 < free_from || t0 + kPaTile > free_to) cur |= 8u;
+      ++j;
+    }
+    // everything but P first
+    const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
+    if (prev) {
+      // (passed by as well: a barrier's phases are told apart by their parity alone)
+      if (!have(me.kv_full + v_slot, ((2 * n_tile - 1) / NS) & 1)) return false;
+      if (prev & 8u) {
+        if (!have(me.v_clean + v_slot, (clean >> (v_slot / 2)) & 1u)) return false;
+        clean ^= 1u << (v_slot / 2);
+      }
+      if (prev & 2u) {
+        if (!have(me.o_empty + w, ph_o)) return false;
+        ph_o ^= 1u;
+      }
+    }
+    if (cur && !have(me.kv_full + k_slot, ((2 * n_tile) / NS) & 1)) return false;
+    if (prev & 1u) {
+      if (!have(me.p_half + w, ph_p)) return false;
+      tc_fence_after();
+      weigh(v_slot, !(prev & 2u), 0);
+      tc_commit(me.h_full + w);
+      if (!have(me.p_full + w, ph_p)) return false;
+      ph_p ^= 1u;
+      tc_fence_after();
+      weigh(v_slot, true, 1);
+      if (prev & 4u) tc_commit(me.o_full + w);
+    }
+    if (cur & 2u) {
+      if (!have(me.q_full + w, ph_q)) return false;
+      ph_q ^= 1u;
+    }
+    tc_fence_after();
+    if (cur & 1u) {
+      score(k_slot);
+      tc_commit(me.s_full + w);
+      if (cur & 4u) tc_commit(me.q_empty + w);
+    }
+    if (prev) tc_commit(me.kv_empty + v_slot);
+    if (cur) {
+      tc_commit(me.kv_empty + k_slot);
+      ++n_tile;
+    }
+    prev = cur;
+  }
+  mbar_arrive(me.run_empty + (n_run - 1) % kRuns);
+  return true;
+}
+
+// The walk, and the queries, keys and values of its runs in.
+template <int D>
+__device__ __forceinline__ bool walk(const PromptParams& p, int f0, int f1, int chunk) {
+  using Sm = PaSmem<D>;
+  constexpr int NS = Sm::kSlots;
+  Member<D> me;
+  const int n_items = p.B * p.groups;
+  uint32_t sent_q[2] = {0, 0};
+  int n_load = 0, n_run = 0;
+  auto hand_out = [&](const Run& r) {
+    const int s = n_run % kRuns;
+    if (!me.wait_all(me.run_empty + s, ((n_run / kRuns) & 1) ^ 1)) return false;
+    if (me.lane == 0) {
+      me.s_runs[s] = r;
+      mbar_arrive(me.run_full + s);
+    }
+    __syncwarp();
+    ++n_run;
+    return true;
+  };
+  auto tile = [&](const CUtensorMap* map, int head, int row) {
+    const int s = n_load % NS;
+    if (!me.wait_all(me.kv_empty + s, ((n_load / NS) & 1) ^ 1)) return false;
+    if (me.lane == 0) {
+      mbar_arrive_expect_tx(me.kv_full + s, Sm::kTileBytes);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(me.smem + Sm::kKV + s * Sm::kTileBytes + c * (kPaTile * 128), map, 64 * c, head, row, me.kv_full + s);
+    }
+    __syncwarp();
+    ++n_load;
+    return true;
+  };
+  auto queries = [&](const Run& r, int w) {
+    if (r.first[w] >= r.last[w]) return true;
+    if (!me.wait_all(me.q_empty + w, (sent_q[w] & 1) ^ 1)) return false;
+    if (me.lane == 0) {
+      mbar_arrive_expect_tx(me.q_full + w, p.Gt * p.qt * D * 2);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(me.smem + Sm::kQ + w * Sm::kTileBytes + c * (kPaTile * 128), &p.tm_q, 64 * c, r.head * p.Gt,
+                    r.q0 + w * p.qt, me.q_full + w);
+    }
+    __syncwarp();
+    ++sent_q[w];
+    return true;
+  };
+  auto copies = [&](const Run& r) {
+    const int row0 = r.k0 + r.tile0 * kPaTile, kv_head = r.head / p.chunks;
+    for (int j = 0; j < r.tiles; ++j) {
+      if (!tile(&p.tm_k, kv_head, row0 + j * kPaTile)) return false;
+      if (j == 0 && (!queries(r, 0) || !queries(r, 1))) return false;
+      if (!tile(&p.tm_v, kv_head, row0 + j * kPaTile)) return false;
+    }
+    return true;
+  };
+  bool ok = true;
+  // A key's stretch [from, to) of its places, from place key_f0 of the flat order on: the
+  // tiles whose first place is in it.  (Behind the tiles' come places without work.)  The
+  // first place of a key of few tiles stands for all of it.
+  auto stretch = [&](const PromptGroup& g, int head, int key_f0, int from, int to) {
+    const bool uncut = g.tiles <= kPaWhole;
+    const int ta = uncut ? 0 : min((from + kPaPlaces - 1) / kPaPlaces, g.tiles);
+    const int tb = uncut ? g.tiles : min((to + kPaPlaces - 1) / kPaPlaces, g.tiles);
+    if (uncut ? from > 0 : ta >= tb) return true;
+    Run r = {};
+    r.tiles = tb - ta;
+    r.tile0 = g.tile0 + ta;
+    r.head = head;
+    r.q0 = g.q0 + g.i0; r.k0 = g.k0;
+    r.n_q = g.n; r.pos0 = g.shift + g.i0; r.kmax = g.kmax;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      r.first[w] = min(max(g.first[w] - ta, 0), r.tiles);
+      r.last[w] = max(min(g.last[w] - ta, r.tiles), r.first[w]);
+    }
+    r.free_to = seen_end(p.causal, r.pos0, g.kmax);
+    r.free_from = seen_begin(p.window, r.pos0 + g.n - 1);
+    r.block = key_f0 / chunk;
+    r.parts = uncut ? 1 : (key_f0 + kPaPlaces * (g.tiles - 1)) / chunk - r.block + 1;
+    r.part = static_cast<int>(blockIdx.x) - r.block;
+    r.tail = key_f0 > r.block * chunk;
+    return hand_out(r) && copies(r);
+  };
+  int item = me.s_start[0], off = me.s_start[1], f = f0;
+  PromptGroup next = prompt_group(p, item);
+  for (; f < f1 && ok; ++item) {
+    const PromptGroup g = next;
+    next = prompt_group(p, min(item + 1, n_items - 1));
+    const int cost = key_cost(g);
+    while (off < cost * p.Hv && f < f1 && ok) {
+      const int head = off / cost, at = off - head * cost, n = min(cost - at, f1 - f);
+      ok = stretch(g, head, f - at, at, at + n);
+      off += n;
+      f += n;
+    }
+    off = 0;
+  }
+  if (ok) {
+    Run r = {};
+    r.tiles = -1;
+    ok = hand_out(r);
+  }
+  if (!ok || *me.abort_flag) {
+    // copies in flight land before the block's memory goes away
+    const uint64_t drain = globaltimer_ns() + 1000000000ull;
+    for (int i = max(n_load - NS, 0); i < n_load; ++i)
+      while (!mbar_try_wait(me.kv_full + i % NS, (i / NS) & 1))
+        if (globaltimer_ns() > drain) break;
+    for (int w = 0; w < 2; ++w)
+      while (sent_q[w] && !mbar_try_wait(me.q_full + w, (sent_q[w] - 1) & 1))
+        if (globaltimer_ns() > drain) break;
+  }
+  return ok;
+}
+
+// Values that are not finite, in tiles with masked tokens: to zeros.
+template <int D, bool kF16>
+__device__ __forceinline__ bool look_over() {
+  using Sm = PaSmem<D>;
+  constexpr int NS = Sm::kSlots;
+  Member<D> me;
+  constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u;
+  int n_tile = 0;
+  for (;;) {
+    const volatile Run* run = me.take();
+    if (!run) return false;
+    const int n = run->tiles;
+    if (n < 0) break;
+    for (int j = 0; j < n; ++j, ++n_tile) {
+      const int t0 = (run->tile0 + j) * kPaTile, s = (2 * n_tile + 1) % NS;
+      // (every tile in turn: a barrier's phases are told apart by their parity alone)
+      if (!me.wait_all(me.kv_full + s, ((2 * n_tile + 1) / NS) & 1)) return false;
+      if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
+        me.arrive(me.kv_empty + s);
+        continue;
+      }
+      uint4* tile = reinterpret_cast<uint4*>(me.smem + Sm::kKV + s * Sm::kTileBytes);
+      // A half whose exponent is all ones leaves its top bit clear below
+      uint32_t finite = 0x80008000u;
+#pragma unroll 8
+      for (int i = me.lane; i < Sm::kTileBytes / 16; i += 32) {
+        const uint4 u = tile[i];
+        finite &= (~u.x & kExp) + kExp;
+        finite &= (~u.y & kExp) + kExp;
+        finite &= (~u.z & kExp) + kExp;
+        finite &= (~u.w & kExp) + kExp;
+      }
+      if (__any_sync(0xFFFFFFFFu, finite != 0x80008000u)) {
+        for (int i = me.lane; i < Sm::kTileBytes / 16; i += 32) {
+          uint4 u = tile[i];
+          uint32_t* x = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((x[k] & kExp & 0xFFFFu) == (kExp & 0xFFFFu)) x[k] &= 0xFFFF0000u;
+            if ((x[k] & kExp & 0xFFFF0000u) == (kExp & 0xFFFF0000u)) x[k] &= 0xFFFFu;
+          }
+          tile[i] = u;
+        }
+        if (me.lane == 0) const_cast<volatile Run*>(run)->bad = 1;
+      }
+      fence_proxy_async_smem();
+      me.arrive(me.v_clean + s);
+      me.arrive(me.kv_empty + s);
+    }
+    me.give_back();
+  }
+  me.give_back();
+  return true;
+}
+
+// The rows out.
+template <int D, bool kF16>
+__device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
+  using Sm = PaSmem<D>;
+  constexpr int NS = Sm::kSlots;
+  Member<D> me;
+  const int wl = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+  const int iq = row / p.Gt, g = row - iq * p.Gt;
+  uint8_t* rows_at = me.smem + Sm::kOut + wl * 32 * 128;
+  uint32_t ph[2] = {0, 0};
+  auto put_vector = [&](int i, uint4 v) {
+    *reinterpret_cast<uint4*>(rows_at + me.lane * 128 + (((i ^ me.lane) & 7) << 4)) = v;
+  };
+  for (;;) {
+    const volatile Run* run = me.take();
+    if (!run) return false;
+    if (run->tiles < 0) break;
+    for (int w = 0; w < 2; ++w) {
+      const int dq = w * p.qt + iq;                  // the row's query in the group
+      const bool on = iq < p.qt && dq < run->n_q;
+      if (w * p.qt >= run->n_q) continue;
+      const bool any = run->first[w] < run->last[w];
+      const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on);
+      const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
+      float m = -INFINITY, l = 0.0f;
+      if (any) {
+        if (!me.wait_all(me.stat_full + w, ph[w])) return false;
+        m = me.s_stat[w * 2 * kPaTile + row];
+        l = me.s_stat[w * 2 * kPaTile + kPaTile + row];
+        if (!me.wait_all(me.o_full + w, ph[w])) return false;
+        ph[w] ^= 1u;
+        tc_fence_after();
+      }
+      const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
+      if (any && run->bad) {
+        // the infinities and NaNs among the values of masked tiles that the row sees join its O
+        const int pos = run->pos0 + dq, kmax = run->kmax;
+        const int hi = on ? seen_end(p.causal, pos, kmax) : 0, lo = on ? seen_begin(p.window, pos) : 0;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16];
+          tmem_load16_start(t_o + c, o);
+          tmem_load16_finish(o);
+          const uint16_t* v = p.v + static_cast<int64_t>(run->head / p.chunks) * p.v_head + c;
+#pragma unroll 1
+          for (int t = (run->tile0 + run->first[w]) * kPaTile; t < min((run->tile0 + run->last[w]) * kPaTile, kmax); ++t) {
+            const int t0 = t & ~(kPaTile - 1);
+            if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
+              t = t0 + kPaTile - 1;                    // (an unmasked tile's are in O)
+              continue;
+            }
+            const uint4* src = reinterpret_cast<const uint4*>(v + (run->k0 + static_cast<int64_t>(t)) * p.v_stride);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 u = __ldg(src + i);
+              const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f2 = unpack_16<kF16>(y[k]);
+                uint32_t &a = o[8 * i + 2 * k], &b = o[8 * i + 2 * k + 1];
+                const bool sees = t >= lo && t < hi;
+                if (sees && !(fabsf(f2.x) < INFINITY)) a = __float_as_uint(__uint_as_float(a) + f2.x);
+                if (sees && !(fabsf(f2.y) < INFINITY)) b = __float_as_uint(__uint_as_float(b) + f2.y);
+              }
+            }
+          }
+          tmem_store16(t_o + c, o);
+        }
+        tmem_store_wait();
+      }
+      // Parts of a cut key: [m 256][l 256][D / 4][256 rows][4 channels]
+      constexpr size_t kSlot = static_cast<size_t>(kPaRows) * (D + 2);
+      const int parts = run->parts, part = run->part, at = w * kPaTile + row;
+      const int first_slot = 2 * run->block + run->tail;
+      auto part_of = [&](int i) { return p.partials + static_cast<size_t>(i == 0 ? first_slot : (first_slot & ~1) + 2 * i) * kSlot + at; };
+      const float own_m = m, own_l = l;
+      if (parts > 1) {
+        // begun and written by other warps; back to zero when the last one has seen them
+        uint32_t* counts = p.arrived + (run->block * 8 + w * 4 + wl) * 2;
+        uint32_t begun = 0;
+        if (me.lane == 0) begun = atomicAdd(counts, 1u) + 1;
+        if (__shfl_sync(0xFFFFFFFFu, begun, 0) != static_cast<uint32_t>(parts)) {
+          float* dst = part_of(part);
+          if (on) {
+            dst[0] = m;
+            dst[kPaRows] = l;
+          }
+          float4* o = reinterpret_cast<float4*>(dst + 2 * kPaRows + 3 * at);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16, o += 4 * kPaRows) {
+            uint32_t y[16];
+            if (any) {
+              tmem_load16_start(t_o + c, y);
+              tmem_load16_finish(y);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (on && any)
+                o[i * kPaRows] = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
+                                             __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
+            __syncwarp();
+          }
+          if (any) {
+            tc_fence_before();
+            me.arrive(me.o_empty + w);
+          }
+          __threadfence();
+          __syncwarp();
+          if (me.lane == 0) atomicAdd(counts + 1, 1u);
+          continue;
+        }
+        // (the others run: they have begun; about a second at most)
+        bool ok = true;
+        if (me.lane == 0) {
+          const uint64_t limit = globaltimer_ns() + 1000000000ull;
+          while (ok && *reinterpret_cast<volatile uint32_t*>(counts + 1) + 1 != static_cast<uint32_t>(parts))
+            ok = globaltimer_ns() < limit && !*me.abort_flag;
+          __threadfence();
+          if (ok) counts[0] = counts[1] = 0;
+        }
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        __threadfence();
+        // (a part that the row sees nothing of has a sum of 0: its m and its O do not count)
+        float top = -INFINITY;
+        l = 0.0f;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 1
+          for (int i = 0; i < parts; ++i) {
+            const float mi = i == part ? own_m : __ldcg(part_of(i)), li = i == part ? own_l : __ldcg(part_of(i) + kPaRows);
+            if (pass == 0) top = li == 0.0f ? top : fmaxf(top, mi);
+            else l = __fadd_rn(l, li == 0.0f ? 0.0f : __fmul_rn(li, ex2(mi - base)));
+          }
+        }
+        m = top;
+      }
+      float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
+      if (p.prefix_lse && on) {
+        float f_own;
+        z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
+        f *= f_own;
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t y[16];
+        float o[16];
+        if (any) {
+          tmem_load16_start(t_o + c, y);
+          tmem_load16_finish(y);
+        }
+        if (any && c + 16 == D) {
+          tc_fence_before();
+          me.arrive(me.o_empty + w);
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = any ? __uint_as_float(y[x]) : 0.0f;
+        if (parts > 1) {
+          // the parts' weighted sum in their order, every step rounded by itself: the same
+          // whichever comes last
+          float own[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            own[x] = o[x];
+            o[x] = 0.0f;
+          }
+#pragma unroll 1
+          for (int i = 0; i < parts; ++i) {
+            const float* src = part_of(i);
+            const float mi = i == part ? own_m : __ldcg(src), li = i == part ? own_l : __ldcg(src + kPaRows);
+            const float wi = li == 0.0f ? 0.0f : ex2(mi - base);
+            const float4* v = reinterpret_cast<const float4*>(src + 2 * kPaRows + 3 * at) + (c / 4) * kPaRows;
+            float4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = i == part ? make_float4(own[4 * k], own[4 * k + 1], own[4 * k + 2], own[4 * k + 3]) : __ldcg(v + k * kPaRows);
+            if (wi == 0.0f) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[4 * k] = __fadd_rn(o[4 * k], __fmul_rn(u[k].x, wi));
+              o[4 * k + 1] = __fadd_rn(o[4 * k + 1], __fmul_rn(u[k].y, wi));
+              o[4 * k + 2] = __fadd_rn(o[4 * k + 2], __fmul_rn(u[k].z, wi));
+              o[4 * k + 3] = __fadd_rn(o[4 * k + 3], __fmul_rn(u[k].w, wi));
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] *= f;
+        if (f_before != 0.0f) {
+          const uint4* prev = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 u = prev[i];
+            const uint32_t v4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack_16<kF16>(v4[k]);
+              o[8 * i + 2 * k] = fmaf(v.x, f_before, o[8 * i + 2 * k]);
+              o[8 * i + 2 * k + 1] = fmaf(v.y, f_before, o[8 * i + 2 * k + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 16; x += 8)
+          put_vector((c % 64 + x) / 8, make_uint4(pack_16<kF16>(o[x], o[x + 1]), pack_16<kF16>(o[x + 2], o[x + 3]),
+                                                  pack_16<kF16>(o[x + 4], o[x + 5]), pack_16<kF16>(o[x + 6], o[x + 7])));
+        __syncwarp();
+        if (c % 64 == 48) {
+          // 128 bytes of every row: a lane stores vector lane % 8 of every fourth row
+          uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + (c - 48) * 2 + (me.lane % 8) * 16;
+#pragma unroll 2
+          for (int r = me.lane / 8; r < 32; r += 4) {
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(rows_at + r * 128 + (((me.lane ^ r) & 7) << 4));
+            if ((rows_on >> r) & 1u) *reinterpret_cast<uint4*>(out + to * (D * 2)) = v;
+          }
+          __syncwarp();
+        }
+      }
+      if (on && p.lse) p.lse[out_row] = z;
+    }
+    me.give_back();
+  }
+  me.give_back();
+  return true;
+}
+
+// Softmax of a row tile's rows.
+template <int D, bool kF16>
+__device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causal, int window, float scale) {
+  using Sm = PaSmem<D>;
+  constexpr int NS = Sm::kSlots;
+  Member<D> me;
   // A row's weights are 2^(s - m), m set to its largest score less kRise and set again when
   // 64 of them add up to more than kMostSum.  fp16: as csrc/kv_attention.cuh, most of its
   // range lies below; bf16 has fp32's range, and results need room above the weights.
   constexpr float kRise = kF16 ? kLift : 0.0f;
   constexpr float kMostSum = 32768.0f;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Run* s_runs = reinterpret_cast<Run*>(smem + Sm::kRunsAt);
-  float* s_stat = reinterpret_cast<float*>(smem + Sm::kStat);          // [row tile][m, l][row]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBarAt);
-  uint64_t *run_full = bars, *run_empty = run_full + kRuns, *kv_full = run_empty + kRuns, *kv_empty = kv_full + NS,
-           *v_clean = kv_empty + NS, *q_full = v_clean + NS, *q_empty = q_full + 2, *s_full = q_empty + 2,
-           *p_half = s_full + 2, *p_full = p_half + 2, *h_full = p_full + 2, *o_full = h_full + 2,
-           *o_empty = o_full + 2, *stat_full = o_empty + 2, *drained = stat_full + 2;
-  int* s_words = reinterpret_cast<int*>(drained + 1);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_words);
-  volatile int* abort_flag = s_words + 1;
-  int* s_start = s_words + 2;                                // item, offset inside it
+  constexpr int kHalf = kPaTile / 2;
+  const int w = threadIdx.x >> 7, wl = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+  const uint32_t t_s = tmem + lanes + w * kPaTile, t_o = tmem + lanes + 2 * kPaTile + w * D;
+  const int iq = row / Gt;
+  uint32_t ph_s = 0, ph_h = 0, ph_stat = 1;
+  // What hides a score: -inf once it is scaled.  (A scale of zero hides nothing by itself: its
+  // scores are written as zeros and scaled by one.)
+  const bool flat = scale == 0.0f;
+  const float to_log2 = flat ? 1.0f : scale, hidden = scale < 0.0f ? INFINITY : -INFINITY;
+  // ---- a run's tiles
+  auto weigh = [&](const volatile Run& run) -> bool {
+    const int j0 = run.first[w], j1 = run.last[w];
+    if (j0 >= j1) return true;
+    const int dq = w * qt + iq, t00 = run.tile0 * kPaTile;
+    const bool on = iq < qt && dq < run.n_q, any_on = __any_sync(0xFFFFFFFFu, on);
+    // (rows that nobody asked for see all: nothing of theirs matters, nothing is masked for them)
+    const int pos = run.pos0 + dq, kmax = run.kmax;
+    const int hi = on ? seen_end(causal, pos, kmax) - t00 : 0, lo = on ? seen_begin(window, pos) - t00 : 0;
+    // every row of the warp sees all tokens of the tiles [full0, full1)
+    const int full0 = (max(__reduce_max_sync(0xFFFFFFFFu, on ? lo : 0), 0) + kPaTile - 1) / kPaTile;
+    const int full1 = max(__reduce_min_sync(0xFFFFFFFFu, on ? hi : INT32_MAX), 0) / kPaTile;
+    float m_neg = on ? INFINITY : 0.0f, l = 0.0f;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+      if (!me.wait_all(me.s_full + w, ph_s)) return false;
+      ph_s ^= 1u;
+      tc_fence_after();
+      if (any_on) {
+        const bool masked = j < full0 || j >= full1 || flat;
+        const int from = on ? lo - j * kPaTile : 0, to = on ? hi - j * kPaTile : kPaTile;     // tokens that the row sees
+        // In two halves of 64 tokens: P V of the first starts under the second.
+#pragma unroll 1
+        for (int c0 = 0; c0 < kPaTile; c0 += kHalf) {
+          if (masked) {
+            // in place: one loop of weights for all tiles
+#pragma unroll 1
+            for (int c = c0; c < c0 + kHalf; c += 16) {
+              uint32_t y[16];
+              tmem_load16_start(t_s + c, y);
+              tmem_load16_finish(y);
+              const uint32_t see = tokens32(c, from, to);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) y[x] = see & (1u << x) ? (flat ? 0u : y[x]) : __float_as_uint(hidden);
+              tmem_store16(t_s + c, y);
+            }
+            tmem_store_wait();
+          }
+          // The maximum is looked for by rows that see tokens here and none before, and again where
+          // weights add up to more than kMostSum (or to no number).  (Each row by itself: what lies
+          // in one does not change another's roundings.)
+          const bool sees = on && from < c0 + kHalf && to > c0;
+          bool need = m_neg == INFINITY && sees, moved = !on;
+          bool look = (masked || j == j0) && __any_sync(0xFFFFFFFFu, need);
+          uint32_t pr[kHalf / 2];
+          float sum;
+#pragma unroll 1
+          for (;;) {
+            if (look) {
+              // m is set by the largest score so far, this half's included
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = c0; c < c0 + kHalf; c += 16) {
+                uint32_t y[16];
+                tmem_load16_start(t_s + c, y);
+                tmem_load16_finish(y);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(y[x]) * to_log2);
+              }
+              const float now = need ? fminf(m_neg, kRise - top) : m_neg;
+              moved = moved || need;
+              const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+              m_neg = now;
+              l *= shrink;
+              if (j > j0 || c0 > 0) {
+                // (earlier tiles are in O, S came after them; the first half may be on its way)
+                if (c0 > 0) {
+                  if (!me.wait_all(me.h_full + w, ph_h)) return false;
+                  tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t y[16];
+                  tmem_load16_start(t_o + c, y);
+                  tmem_load16_finish(y);
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * shrink);
+                  tmem_store16(t_o + c, y);
+                }
+              }
+            }
+            uint32_t s[2][32];
+            tmem_load32_start(t_s + c0, s[0]);
+            uint64_t sum2 = f2_pack(0.0f, 0.0f);
+            const float add = m_neg == INFINITY ? 0.0f : m_neg;          // (nothing but -inf seen so far)
+            const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 32) {
+              uint32_t (&y)[32] = s[c / 32];
+              tmem_load32_finish(y);
+              if (c == 0) tmem_load32_start(t_s + c0 + 32, s[1]);
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                const uint64_t v = f2_fma(f2_pack(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), k2, m2);
+                const float a = ex2(f2_lo(v)), b = ex2(f2_hi(v));
+                sum2 = f2_add(sum2, f2_pack(a, b));
+                pr[(c + x) / 2] = pack_16<kF16>(a, b);
+              }
+            }
+            sum = f2_lo(sum2) + f2_hi(sum2);
+            need = !moved && (!(sum <= kMostSum) || (m_neg == INFINITY && sees));
+            look = __any_sync(0xFFFFFFFFu, need);
+            if (!look) break;
+          }
+          l += sum;
+          // P over the columns of S that have been read
+#pragma unroll
+          for (int c = 0; c < kHalf / 2; c += 16) {
+            uint32_t x[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+            tmem_store16(t_s + c0 / 2 + c, x);
+          }
+          tmem_store_wait();
+          tc_fence_before();
+          me.arrive((c0 ? me.p_full : me.p_half) + w);
+        }
+      } else {
+        // (rows that nobody asked for: their P may be anything)
+        tc_fence_before();
+        me.arrive(me.p_half + w);
+        me.arrive(me.p_full + w);
+      }
+      ph_h ^= 1u;
+    }
+    // (me.o_empty: the statistics of the run before have been read as well)
+    if (!me.wait_all(me.o_empty + w, ph_stat)) return false;
+    ph_stat ^= 1u;
+    me.s_stat[w * 2 * kPaTile + row] = -m_neg;
+    me.s_stat[w * 2 * kPaTile + kPaTile + row] = l;
+    me.arrive(me.stat_full + w);
+    return true;
+  };
+  for (;;) {
+    const volatile Run* run = me.take();
+    if (!run) return false;
+    if (run->tiles < 0) break;
+    if (!weigh(*run)) return false;
+    me.give_back();
+  }
+  me.give_back();
+  return true;
+}
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kPaThreads, 1)
+prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+  constexpr int NS = PaSmem<D>::kSlots;
+  const Block<D> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kRuns; ++i) { mbar_init(run_full + i, 1); mbar_init(run_empty + i, kConsumers); }
-    for (int i = 0; i < NS; ++i) { mbar_init(kv_full + i, 1); mbar_init(kv_empty + i, 2 + i % 2); mbar_init(v_clean + i, 1); }
+    for (int i = 0; i < kRuns; ++i) { mbar_init(sh.run_full + i, 1); mbar_init(sh.run_empty + i, kConsumers); }
+    for (int i = 0; i < NS; ++i) { mbar_init(sh.kv_full + i, 1); mbar_init(sh.kv_empty + i, 2 + i % 2); mbar_init(sh.v_clean + i, 1); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 1); mbar_init(q_empty + i, 1); mbar_init(s_full + i, 1);
-      mbar_init(p_half + i, 4); mbar_init(p_full + i, 4); mbar_init(h_full + i, 1);
-      mbar_init(o_full + i, 1); mbar_init(o_empty + i, 4); mbar_init(stat_full + i, 4);
+      mbar_init(sh.q_full + i, 1); mbar_init(sh.q_empty + i, 1); mbar_init(sh.s_full + i, 1);
+      mbar_init(sh.p_half + i, 4); mbar_init(sh.p_full + i, 4); mbar_init(sh.h_full + i, 1);
+      mbar_init(sh.o_full + i, 1); mbar_init(sh.o_empty + i, 4); mbar_init(sh.stat_full + i, 4);
     }
-    mbar_init(drained, 2);
-    *abort_flag = 0;
+    mbar_init(sh.drained, 2);
+    *sh.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc(tmem_holder, 512);
+  if (warp == 12) tmem_alloc(sh.tmem_holder, 512);
   if (warp == 14 && lane < 3) tma_prefetch_map(lane == 0 ? &p.tm_q : lane == 1 ? &p.tm_k : &p.tm_v);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -249,17 +977,17 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d);
     if (lane >= d) incl += a;
   }
-  if (lane == 31) reinterpret_cast<int*>(s_stat)[warp] = incl;
+  if (lane == 31) reinterpret_cast<int*>(sh.s_stat)[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   int before = 0, total = 0;
   for (int w = 0; w < kPaThreads / 32; ++w) {
-    const int x = reinterpret_cast<int*>(s_stat)[w];
+    const int x = reinterpret_cast<int*>(sh.s_stat)[w];
     if (w < warp) before += x;
     total += x;
   }
-  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kPaMinChunk);
+  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
   const int f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
   const int f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
   const int excl = before + incl - mine;
@@ -270,648 +998,33 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
       if (f0 < at + n) break;
       at += n;
     }
-    s_start[0] = i;
-    s_start[1] = f0 - at;
+    sh.s_start[0] = i;
+    sh.s_start[1] = f0 - at;
   }
   __syncthreads();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = *sh.tmem_holder;
 
-  auto give_up = [&]() {
-    if (lane == 0) {
-      report_timeout(p.status);
-      *abort_flag = 1;
-    }
-  };
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag)) != 0;
-  };
-
-  if (tid == 14 * 32) p.joins[blockIdx.x].n_parts = 0;       // (until this block turns out to start a cut key)
   if (p.cu_q && warp >= 8 && warp < 12) clear_rows<D>(p, blockIdx.x * 4 + warp - 8, gridDim.x * 4);
   if (f0 < f1) {
-    // the next run to this warp, or null; its last reader frees it
-    int n_taken = 0;
-    auto take = [&]() -> const volatile Run* {
-      const int s = n_taken % kRuns;
-      if (!wait_all(run_full + s, (n_taken / kRuns) & 1)) return nullptr;
-      ++n_taken;
-      return s_runs + s;
-    };
-    auto give_back = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(run_empty + (n_taken - 1) % kRuns);
-    };
-    auto arrive = [&](uint64_t* bar) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-
-    if (warp == 12 || warp == 13) {
-      // -------------------------------------------------------- the products
-      // (A warp for each row tile: neither waits for the other's softmax.  One lane does it
-      // all: what lies between the arrival of P and the issue of the products is the chain
-      // that the tensor cores wait for.)
-      const int w = warp - 12;
-      auto products = [&]() -> bool {
-        const uint32_t id_s = idesc_16<kF16>(128, kPaTile, false), id_o = idesc_16<kF16>(128, D, true);
-        constexpr uint32_t kTileLow = Sm::kTileBytes >> 4;
-        const uint32_t q_low = desc_low(smem + Sm::kQ, 16) + w * kTileLow;
-        const uint32_t k_low = desc_low(smem + Sm::kKV, 16), v_low = desc_low(smem + Sm::kKV, kPaTile * 128);
-        const uint32_t t_s = tmem + w * kPaTile, t_o = tmem + 2 * kPaTile + w * D;
-        auto score = [&](int slot) {
-          const uint32_t k = k_low + slot * kTileLow;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t o = ((i / 4) * (kPaTile * 128) + (i % 4) * 32) >> 4;
-            tc_mma_ss(t_s, q_low + o, k + o, id_s, i != 0);
-          }
-        };
-        auto weigh = [&](int slot, bool add, int half) {
-          const uint32_t v = v_low + slot * kTileLow;
-#pragma unroll
-          for (int x = 0; x < kPaTile / 32; ++x) {
-            // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-            const int i = half * (kPaTile / 32) + x;
-            tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || x != 0);
-          }
-        };
-        auto have = [&](uint64_t* bar, uint32_t parity) {
-          return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag);
-        };
-        uint32_t ph_q = 0, ph_p = 0, ph_o = 1, clean = 0;    // (bit i of clean: the phase of slot 2 i + 1)
-        int n_tile = 0, n_run = 0;                           // tiles whose scores were issued (or passed by), runs taken
-        // the tile whose weights come next: 1, 2 its row tile's first, 4 its last one, 8 masked; 16 passed by
-        uint32_t prev = 0;
-        int j = 0, n = 0, first = 0, last = 0, tile0 = 0, free_from = 0, free_to = 0;
-        for (bool more = true; more || prev;) {
-          uint32_t cur = 0;
-          while (more && j >= n) {
-            if (n_run) mbar_arrive(run_empty + (n_run - 1) % kRuns);
-            if (!have(run_full + n_run % kRuns, (n_run / kRuns) & 1)) return false;
-            const volatile Run* run = s_runs + n_run % kRuns;
-            ++n_run;
-            n = run->tiles;
-            j = 0;
-            if (n < 0) { more = false; break; }
-            first = run->first[w]; last = run->last[w];
-            tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
-          }
-          if (more) {
-            cur = j >= first && j < last ? 1u | (j == first ? 2u : 0u) | (j + 1 == last ? 4u : 0u) : 16u;
-            const int t0 = (tile0 + j) * kPaTile;
-            if (t0 < free_from || t0 + kPaTile > free_to) cur |= 8u;
-            ++j;
-          }
-          // everything but P first
-          const int v_slot = (2 * n_tile - 1 + NS) % NS, k_slot = (2 * n_tile) % NS;
-          if (prev) {
-            // (passed by as well: a barrier's phases are told apart by their parity alone)
-            if (!have(kv_full + v_slot, ((2 * n_tile - 1) / NS) & 1)) return false;
-            if (prev & 8u) {
-              if (!have(v_clean + v_slot, (clean >> (v_slot / 2)) & 1u)) return false;
-              clean ^= 1u << (v_slot / 2);
-            }
-            if (prev & 2u) {
-              if (!have(o_empty + w, ph_o)) return false;
-              ph_o ^= 1u;
-            }
-          }
-          if (cur && !have(kv_full + k_slot, ((2 * n_tile) / NS) & 1)) return false;
-          if (prev & 1u) {
-            if (!have(p_half + w, ph_p)) return false;
-            tc_fence_after();
-            weigh(v_slot, !(prev & 2u), 0);
-            tc_commit(h_full + w);
-            if (!have(p_full + w, ph_p)) return false;
-            ph_p ^= 1u;
-            tc_fence_after();
-            weigh(v_slot, true, 1);
-            if (prev & 4u) tc_commit(o_full + w);
-          }
-          if (cur & 2u) {
-            if (!have(q_full + w, ph_q)) return false;
-            ph_q ^= 1u;
-          }
-          tc_fence_after();
-          if (cur & 1u) {
-            score(k_slot);
-            tc_commit(s_full + w);
-            if (cur & 4u) tc_commit(q_empty + w);
-          }
-          if (prev) tc_commit(kv_empty + v_slot);
-          if (cur) {
-            tc_commit(kv_empty + k_slot);
-            ++n_tile;
-          }
-          prev = cur;
-        }
-        mbar_arrive(run_empty + (n_run - 1) % kRuns);
-        return true;
-      };
+    bool ok = true;
+    if (warp < 8) {
+      ok = softmax<D, kF16>(tmem, p.Gt, p.qt, p.causal, p.window, p.scale_log2);
+    } else if (warp < 12) {
+      ok = rows_out<D, kF16>(p, tmem);
+    } else if (warp < 14) {
       if (lane == 0) {
-        if (!products()) {
-          report_timeout(p.status);
-          *abort_flag = 1;
-        }
+        ok = products<D, kF16>(tmem, warp - 12);
         // nothing of this block's is under way when the tensor memory goes back
-        tc_commit(drained);
-        wait_bounded(drained, 0, abort_flag);
+        tc_commit(sh.drained);
+        wait_bounded(sh.drained, 0, sh.abort_flag);
       }
       __syncwarp();
-    } else if (warp == 14) {
-      // ------------- the walk, and the queries, keys and values of its runs in
-      uint32_t sent_q[2] = {0, 0};
-      int n_load = 0, n_run = 0;
-      auto hand_out = [&](const Run& r) {
-        const int s = n_run % kRuns;
-        if (!wait_all(run_empty + s, ((n_run / kRuns) & 1) ^ 1)) return false;
-        if (lane == 0) {
-          s_runs[s] = r;
-          mbar_arrive(run_full + s);
-        }
-        __syncwarp();
-        ++n_run;
-        return true;
-      };
-      auto tile = [&](const CUtensorMap* map, int head, int row) {
-        const int s = n_load % NS;
-        if (!wait_all(kv_empty + s, ((n_load / NS) & 1) ^ 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(kv_full + s, Sm::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + Sm::kKV + s * Sm::kTileBytes + c * (kPaTile * 128), map, 64 * c, head, row, kv_full + s);
-        }
-        __syncwarp();
-        ++n_load;
-        return true;
-      };
-      auto queries = [&](const Run& r, int w) {
-        if (r.first[w] >= r.last[w]) return true;
-        if (!wait_all(q_empty + w, (sent_q[w] & 1) ^ 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full + w, p.Gt * p.qt * D * 2);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + Sm::kQ + w * Sm::kTileBytes + c * (kPaTile * 128), &p.tm_q, 64 * c, r.head * p.Gt,
-                        r.q0 + w * p.qt, q_full + w);
-        }
-        __syncwarp();
-        ++sent_q[w];
-        return true;
-      };
-      auto copies = [&](const Run& r) {
-        const int row0 = r.k0 + r.tile0 * kPaTile, kv_head = r.head / p.chunks;
-        for (int j = 0; j < r.tiles; ++j) {
-          if (!tile(&p.tm_k, kv_head, row0 + j * kPaTile)) return false;
-          if (j == 0 && (!queries(r, 0) || !queries(r, 1))) return false;
-          if (!tile(&p.tm_v, kv_head, row0 + j * kPaTile)) return false;
-        }
-        return true;
-      };
-      int item = s_start[0], off = s_start[1], f = f0;
-      bool ok = true;
-      PromptGroup next = prompt_group(p, item);
-      for (; f < f1 && ok; ++item) {
-        const PromptGroup g = next;
-        next = prompt_group(p, min(item + 1, n_items - 1));
-        const int cost = key_cost(g);
-        while (off < cost * p.Hv && f < f1 && ok) {
-          const int head = off / cost, at = off - head * cost;
-          const int key_f0 = f - at, end = min(f1, key_f0 + cost);
-          int ta = min(at, g.tiles), tb = min(end - key_f0, g.tiles);
-          const bool uncut = g.tiles <= kPaWhole;
-          if (uncut) {
-            ta = 0;
-            tb = g.tiles;
-          }
-          if (uncut ? at == 0 : ta < tb) {
-            Run r = {};
-            r.tiles = tb - ta;
-            r.tile0 = g.tile0 + ta;
-            r.head = head;
-            r.q0 = g.q0 + g.i0; r.k0 = g.k0;
-            r.n_q = g.n; r.pos0 = g.shift + g.i0; r.kmax = g.kmax;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              r.first[w] = min(max(g.first[w] - ta, 0), r.tiles);
-              r.last[w] = max(min(g.last[w] - ta, r.tiles), r.first[w]);
-            }
-            r.free_to = seen_end(p, r.pos0, g.kmax);
-            r.free_from = seen_begin(p, r.pos0 + g.n - 1);
-            const int first_chunk = key_f0 / chunk, n_parts = uncut ? 1 : (key_f0 + g.tiles - 1) / chunk - first_chunk + 1;
-            const int inside = key_f0 > f0;
-            r.whole = n_parts == 1;
-            r.slot = 2 * blockIdx.x + inside;
-            // this block holds a cut key's first part
-            if (lane == 0 && n_parts > 1 && ta == 0)
-              p.joins[blockIdx.x] = {n_parts, inside, r.q0, g.n, head * p.Gt, {0, 0, 0}};
-            ok = hand_out(r) && copies(r);
-          }
-          off += end - f;
-          f = end;
-        }
-        off = 0;
-      }
-      if (ok) {
-        Run r = {};
-        r.tiles = -1;
-        ok = hand_out(r);
-      }
-      if (!ok) give_up();
-      if (*abort_flag) {
-        // copies in flight land before the block's memory goes away
-        const uint64_t drain = globaltimer_ns() + 1000000000ull;
-        for (int i = max(n_load - NS, 0); i < n_load; ++i)
-          while (!mbar_try_wait(kv_full + i % NS, (i / NS) & 1))
-            if (globaltimer_ns() > drain) break;
-        for (int w = 0; w < 2; ++w)
-          while (sent_q[w] && !mbar_try_wait(q_full + w, (sent_q[w] - 1) & 1))
-            if (globaltimer_ns() > drain) break;
-      }
-    } else if (warp == 15) {
-      // ------------------------------------- values that are not finite, to zeros
-      constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u;
-      int n_tile = 0;
-      auto look = [&]() -> bool {
-        for (;;) {
-          const volatile Run* run = take();
-          if (!run) return false;
-          const int n = run->tiles;
-          if (n < 0) break;
-          for (int j = 0; j < n; ++j, ++n_tile) {
-            const int t0 = (run->tile0 + j) * kPaTile, s = (2 * n_tile + 1) % NS;
-            // (every tile in turn: a barrier's phases are told apart by their parity alone)
-            if (!wait_all(kv_full + s, ((2 * n_tile + 1) / NS) & 1)) return false;
-            if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
-              arrive(kv_empty + s);
-              continue;
-            }
-            uint4* tile = reinterpret_cast<uint4*>(smem + Sm::kKV + s * Sm::kTileBytes);
-            // A half whose exponent is all ones leaves its top bit clear below
-            uint32_t finite = 0x80008000u;
-#pragma unroll 8
-            for (int i = lane; i < Sm::kTileBytes / 16; i += 32) {
-              const uint4 u = tile[i];
-              finite &= (~u.x & kExp) + kExp;
-              finite &= (~u.y & kExp) + kExp;
-              finite &= (~u.z & kExp) + kExp;
-              finite &= (~u.w & kExp) + kExp;
-            }
-            if (__any_sync(0xFFFFFFFFu, finite != 0x80008000u)) {
-              for (int i = lane; i < Sm::kTileBytes / 16; i += 32) {
-                uint4 u = tile[i];
-                uint32_t* x = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((x[k] & kExp & 0xFFFFu) == (kExp & 0xFFFFu)) x[k] &= 0xFFFF0000u;
-                  if ((x[k] & kExp & 0xFFFF0000u) == (kExp & 0xFFFF0000u)) x[k] &= 0xFFFFu;
-                }
-                tile[i] = u;
-              }
-              if (lane == 0) const_cast<volatile Run*>(run)->bad = 1;
-            }
-            fence_proxy_async_smem();
-            arrive(v_clean + s);
-            arrive(kv_empty + s);
-          }
-          give_back();
-        }
-        give_back();
-        return true;
-      };
-      if (!look()) give_up();
-    } else if (warp >= 8) {
-      // ------------------------------------------------------------ the rows out
-      const int wl = warp - 8, row = tid & 127;
-      const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
-      const int iq = row / p.Gt, g = row - iq * p.Gt;
-      uint8_t* rows_at = smem + Sm::kOut + wl * 32 * 128;
-      uint32_t ph[2] = {0, 0};
-      auto put_vector = [&](int i, uint4 v) {
-        *reinterpret_cast<uint4*>(rows_at + lane * 128 + (((i ^ lane) & 7) << 4)) = v;
-      };
-      auto rows_out = [&]() -> bool {
-        for (;;) {
-          const volatile Run* run = take();
-          if (!run) return false;
-          if (run->tiles < 0) break;
-          for (int w = 0; w < 2; ++w) {
-            const int dq = w * p.qt + iq;                  // the row's query in the group
-            const bool on = iq < p.qt && dq < run->n_q;
-            if (w * p.qt >= run->n_q) continue;
-            const bool any = run->first[w] < run->last[w], whole = run->whole;
-            const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
-            float m = -INFINITY, l = 0.0f;
-            if (any) {
-              if (!wait_all(stat_full + w, ph[w])) return false;
-              m = s_stat[w * 2 * kPaTile + row];
-              l = s_stat[w * 2 * kPaTile + kPaTile + row];
-              if (!wait_all(o_full + w, ph[w])) return false;
-              ph[w] ^= 1u;
-              tc_fence_after();
-            }
-            const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
-            float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
-            if (whole && p.prefix_lse && on) {
-              float f_own;
-              z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
-              f *= f_own;
-            }
-            if (any && run->bad) {
-              // the infinities and NaNs among the values of masked tiles that the row sees join its O
-              const int pos = run->pos0 + dq, kmax = run->kmax;
-              const int hi = on ? seen_end(p, pos, kmax) : 0, lo = on ? seen_begin(p, pos) : 0;
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                uint32_t o[16];
-                tmem_load16_start(t_o + c, o);
-                tmem_load16_finish(o);
-                const uint16_t* v = p.v + static_cast<int64_t>(run->head / p.chunks) * p.v_head + c;
-#pragma unroll 1
-                for (int t = (run->tile0 + run->first[w]) * kPaTile; t < min((run->tile0 + run->last[w]) * kPaTile, kmax); ++t) {
-                  const int t0 = t & ~(kPaTile - 1);
-                  if (t0 >= run->free_from && t0 + kPaTile <= run->free_to) {
-                    t = t0 + kPaTile - 1;                    // (an unmasked tile's are in O)
-                    continue;
-                  }
-                  const uint4* src = reinterpret_cast<const uint4*>(v + (run->k0 + static_cast<int64_t>(t)) * p.v_stride);
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    const uint4 u = __ldg(src + i);
-                    const uint32_t y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      const float2 f2 = unpack_16<kF16>(y[k]);
-                      uint32_t &a = o[8 * i + 2 * k], &b = o[8 * i + 2 * k + 1];
-                      const bool sees = t >= lo && t < hi;
-                      if (sees && !(fabsf(f2.x) < INFINITY)) a = __float_as_uint(__uint_as_float(a) + f2.x);
-                      if (sees && !(fabsf(f2.y) < INFINITY)) b = __float_as_uint(__uint_as_float(b) + f2.y);
-                    }
-                  }
-                }
-                tmem_store16(t_o + c, o);
-              }
-              tmem_store_wait();
-            }
-            // 16 channels of O
-            auto load = [&](int c, float (&o)[16]) {
-              uint32_t y[16];
-              if (any) {
-                tmem_load16_start(t_o + c, y);
-                tmem_load16_finish(y);
-              }
-#pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = any ? __uint_as_float(y[x]) : 0.0f;
-            };
-            // (a lane stores vector lane % 8 of every fourth row)
-            float* part = p.partials + static_cast<size_t>(run->slot) * kPaRows * (D + 2);
-            uint8_t* base = whole ? reinterpret_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(part + 2 * kPaRows);
-            const int64_t row_at = whole ? out_row * (D * 2) : static_cast<int64_t>(w * kPaTile + row) * (D * 4);
-            const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on) >> (lane / 8);
-            uint8_t* to[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              to[i] = base + __shfl_sync(0xFFFFFFFFu, row_at, 4 * i + lane / 8) + (lane % 8) * 16;
-            auto store_rows = [&](int at) {
-              __syncwarp();
-              const int r = lane / 8;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(rows_at + (4 * i + r) * 128 +
-                                                                (((lane ^ (4 * i + r)) & 7) << 4));
-                if ((rows_on >> (4 * i)) & 1u) *reinterpret_cast<uint4*>(to[i] + at) = v;
-              }
-              __syncwarp();
-            };
-            if (whole) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 64) {
-#pragma unroll 1
-                for (int c = c0; c < c0 + 64; c += 16) {
-                  float o[16];
-                  load(c, o);
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) o[x] *= f;
-                  if (f_before != 0.0f) {
-                    const uint4* prev = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                      const uint4 u = prev[i];
-                      const uint32_t y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                      for (int k = 0; k < 4; ++k) {
-                        const float2 v = unpack_16<kF16>(y[k]);
-                        o[8 * i + 2 * k] = fmaf(v.x, f_before, o[8 * i + 2 * k]);
-                        o[8 * i + 2 * k + 1] = fmaf(v.y, f_before, o[8 * i + 2 * k + 1]);
-                      }
-                    }
-                  }
-#pragma unroll
-                  for (int x = 0; x < 16; x += 8)
-                    put_vector((c - c0 + x) / 8, make_uint4(pack_16<kF16>(o[x], o[x + 1]), pack_16<kF16>(o[x + 2], o[x + 3]),
-                                                            pack_16<kF16>(o[x + 4], o[x + 5]), pack_16<kF16>(o[x + 6], o[x + 7])));
-                }
-                if (any && c0 + 64 == D) {
-                  tc_fence_before();
-                  arrive(o_empty + w);
-                }
-                store_rows(c0 * 2);
-              }
-              if (on && p.lse) p.lse[out_row] = z;
-            } else {
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                  float o[16];
-                  load(c + 4 * i, o);
-#pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    put_vector(i + x, make_uint4(__float_as_uint(o[4 * x]), __float_as_uint(o[4 * x + 1]),
-                                                 __float_as_uint(o[4 * x + 2]), __float_as_uint(o[4 * x + 3])));
-                }
-                store_rows(c * 4);
-              }
-              if (any) {
-                tc_fence_before();
-                arrive(o_empty + w);
-              }
-              if (on) {
-                part[w * kPaTile + row] = m;
-                part[kPaRows + w * kPaTile + row] = l;
-              }
-            }
-          }
-          give_back();
-        }
-        give_back();
-        return true;
-      };
-      if (!rows_out()) give_up();
     } else {
-      // ------------------------------------------------------------- softmax
-      constexpr int kHalf = kPaTile / 2;
-      const int w = warp >> 2, wl = warp & 3, row = tid & 127;
-      const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
-      const uint32_t t_s = tmem + lanes + w * kPaTile, t_o = tmem + lanes + 2 * kPaTile + w * D;
-      const int iq = row / p.Gt;
-      const float to_log2 = p.scale_log2;
-      uint32_t ph_s = 0, ph_h = 0, ph_stat = 1;
-      // ---- a run's tiles
-      auto weigh = [&](const volatile Run& run) -> bool {
-        const int j0 = run.first[w], j1 = run.last[w];
-        if (j0 >= j1) return true;
-        const int dq = w * p.qt + iq, t00 = run.tile0 * kPaTile;
-        const bool on = iq < p.qt && dq < run.n_q, any_on = __any_sync(0xFFFFFFFFu, on);
-        // (rows that nobody asked for see all: nothing of theirs matters, nothing is masked for them)
-        const int pos = run.pos0 + dq, kmax = run.kmax;
-        const int hi = on ? seen_end(p, pos, kmax) - t00 : 0, lo = on ? seen_begin(p, pos) - t00 : 0;
-        // every row of the warp sees all tokens of the tiles [full0, full1)
-        const int full0 = (max(__reduce_max_sync(0xFFFFFFFFu, on ? lo : 0), 0) + kPaTile - 1) / kPaTile;
-        const int full1 = max(__reduce_min_sync(0xFFFFFFFFu, on ? hi : INT32_MAX), 0) / kPaTile;
-        float m_neg = on ? INFINITY : 0.0f, l = 0.0f;
-        uint32_t s[2][32], pr[kHalf / 2];
-        float sum = 0.0f;
-        // The weights of 64 tokens from column c0 on; `next`: the first 32 columns that come after them
-        auto weights = [&](auto hidden, int c0, int from, int to) {      // hidden: some tokens may not be seen
-          uint64_t sum2 = f2_pack(0.0f, 0.0f);
-          const float add = m_neg == INFINITY ? 0.0f : m_neg;            // (nothing but -inf seen so far)
-          const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
-#pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            uint32_t (&now)[32] = s[c / 32];
-            tmem_load32_finish(now);
-            if (c == 0) tmem_load32_start(t_s + c0 + 32, s[1]);
-            const uint32_t see = hidden ? tokens32(c0 + c, from, to) : 0xFFFFFFFFu;
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const uint64_t v = f2_fma(f2_pack(__uint_as_float(now[x]), __uint_as_float(now[x + 1])), k2, m2);
-              float v0 = f2_lo(v), v1 = f2_hi(v);
-              if (hidden) {
-                v0 = see & (1u << x) ? v0 : -INFINITY;
-                v1 = see & (2u << x) ? v1 : -INFINITY;
-              }
-              const float a = ex2(v0), b = ex2(v1);
-              sum2 = f2_add(sum2, f2_pack(a, b));
-              pr[(c + x) / 2] = pack_16<kF16>(a, b);
-            }
-          }
-          sum = f2_lo(sum2) + f2_hi(sum2);
-        };
-        // The same where tokens may be hidden or the maximum moves.  It is looked for by rows that
-        // see tokens here and none before, and again where weights add up to more than kMostSum
-        // (or to no number).  (Each row by itself: what lies in one does not change another's
-        // roundings.)
-        auto weights_any = [&](int c0, int from, int to, bool started, bool again) -> bool {
-          const bool sees = on && from < c0 + kHalf && to > c0;
-          bool need = (m_neg == INFINITY && sees) || again, moved = !on;
-#pragma unroll 1
-          for (;;) {
-            if (__any_sync(0xFFFFFFFFu, need)) {
-              // m is set by the largest score so far, this half's included
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = c0; c < c0 + kHalf; c += 32) {
-                tmem_load32_start(t_s + c, s[0]);
-                tmem_load32_finish(s[0]);
-                const uint32_t see = tokens32(c, from, to);
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  top = fmaxf(top, see & (1u << x) ? __uint_as_float(s[0][x]) * to_log2 : -INFINITY);
-              }
-              const float now = need ? fminf(m_neg, kRise - top) : m_neg;
-              moved = moved || need;
-              const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-              m_neg = now;
-              l *= shrink;
-              if (started || c0 > 0) {
-                // (earlier tiles are in O, S came after them; the first half may be on its way)
-                if (c0 > 0) {
-                  if (!wait_all(h_full + w, ph_h)) return false;
-                  tc_fence_after();
-                }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t y[16];
-                  tmem_load16_start(t_o + c, y);
-                  tmem_load16_finish(y);
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * shrink);
-                  tmem_store16(t_o + c, y);
-                }
-              }
-            }
-            tmem_load32_start(t_s + c0, s[0]);
-            weights(std::true_type{}, c0, from, to);
-            need = !moved && !(sum <= kMostSum);
-            if (!__any_sync(0xFFFFFFFFu, need)) return true;
-          }
-        };
-#pragma unroll 1
-        for (int j = j0; j < j1; ++j) {
-          if (!wait_all(s_full + w, ph_s)) return false;
-          ph_s ^= 1u;
-          tc_fence_after();
-          if (any_on) {
-            const bool plain = j >= full0 && j < full1 && j > j0;
-            const int from = on ? lo - j * kPaTile : 0, to = on ? hi - j * kPaTile : kPaTile;     // tokens that the row sees
-            if (plain) tmem_load32_start(t_s, s[0]);
-            // In two halves of 64 tokens: P V of the first starts under the second.
-#pragma unroll 1
-            for (int c0 = 0; c0 < kPaTile; c0 += kHalf) {
-              bool again = false;
-              if (plain) {
-                weights(std::false_type{}, c0, from, to);
-                if (c0 == 0) tmem_load32_start(t_s + kHalf, s[0]);
-                again = on && !(sum <= kMostSum);
-              }
-              if (!plain || __any_sync(0xFFFFFFFFu, again || m_neg == INFINITY)) {
-                if (plain) tmem_load32_finish(s[0]);
-                if (!weights_any(c0, from, to, j > j0, again)) return false;
-                if (plain && c0 == 0) tmem_load32_start(t_s + kHalf, s[0]);
-              }
-              l += sum;
-              // P over the columns of S that have been read
-#pragma unroll
-              for (int c = 0; c < kHalf / 2; c += 16) {
-                uint32_t x[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-                tmem_store16(t_s + c0 / 2 + c, x);
-              }
-              tmem_store_wait();
-              tc_fence_before();
-              arrive((c0 ? p_full : p_half) + w);
-            }
-          } else {
-            // (rows that nobody asked for: their P may be anything)
-            tc_fence_before();
-            arrive(p_half + w);
-            arrive(p_full + w);
-          }
-          ph_h ^= 1u;
-        }
-        // (o_empty: the statistics of the run before have been read as well)
-        if (!wait_all(o_empty + w, ph_stat)) return false;
-        ph_stat ^= 1u;
-        s_stat[w * 2 * kPaTile + row] = -m_neg;
-        s_stat[w * 2 * kPaTile + kPaTile + row] = l;
-        arrive(stat_full + w);
-        return true;
-      };
-      auto softmax = [&]() -> bool {
-        for (;;) {
-          const volatile Run* run = take();
-          if (!run) return false;
-          if (run->tiles < 0) break;
-          if (!weigh(*run)) return false;
-          give_back();
-        }
-        give_back();
-        return true;
-      };
-      if (!softmax()) give_up();
+      ok = warp == 14 ? walk<D>(p, f0, f1, chunk) : look_over<D, kF16>();
+    }
+    if (!ok && lane == 0) {
+      report_timeout(p.status);
+      *sh.abort_flag = 1;
     }
   }
   tc_fence_before();
@@ -924,8 +1037,8 @@ bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; 
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 constexpr size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
-constexpr size_t kWsJoins = 256;
-constexpr size_t kWsPartials = a256(kWsJoins + kPaMaxCtas * sizeof(PromptJoin));
+constexpr size_t kWsArrived = 256;
+constexpr size_t kWsPartials = a256(kWsArrived + kPaMaxCtas * 16 * sizeof(uint32_t));
 constexpr size_t ws_total(int D) { return a256(kWsPartials + size_t(2) * kPaMaxCtas * kPaRows * (D + 2) * 4); }
 
 // [rows][heads][D] of 16-bit values, boxes of 64 channels, box_heads and box_rows.
@@ -967,11 +1080,13 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
     if (w < tiles) tiles = w;
   }
   const int64_t items = static_cast<int64_t>(p.B) * p.groups;
-  const int64_t most = items * p.Hv * (tiles + kPaKeyCost);
+  const int64_t most = items * p.Hv * (kPaPlaces * tiles + kPaKeyCost);
   if (items >= (int64_t(1) << 30) || tiles >= (int64_t(1) << 24) || most >= (int64_t(1) << 31) - (1 << 24))
     return NVR_ERR_UNSUPPORTED;
   int64_t grid = sms < kPaMaxCtas ? sms : kPaMaxCtas;
-  if (grid > (most + kPaMinChunk - 1) / kPaMinChunk) grid = (most + kPaMinChunk - 1) / kPaMinChunk;
+  p.min_chunk = kPaMinChunk;
+  while (static_cast<int64_t>(p.min_chunk) * p.min_chunk < kPaPlaces * kPaPlaces * tiles) ++p.min_chunk;
+  if (grid > (most + p.min_chunk - 1) / p.min_chunk) grid = (most + p.min_chunk - 1) / p.min_chunk;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -982,10 +1097,7 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, kF16>, p);
-  if (e != cudaSuccess) return cuda_status(e);
-  if (tiles <= kPaWhole) return NVR_OK;
-  return launch_prompt_join(p, D, kF16, static_cast<int>(grid), sms, s);
+  return cuda_status(cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, kF16>, p));
 }
 
 }  // namespace
@@ -1054,7 +1166,7 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   p.prefix_out = static_cast<const uint16_t*>(prefix_out); p.prefix_lse = prefix_lse;
   p.out = static_cast<uint16_t*>(out); p.lse = lse;
   p.status = reinterpret_cast<uint32_t*>(ws + kWsStatus);
-  p.joins = reinterpret_cast<PromptJoin*>(ws + kWsJoins);
+  p.arrived = reinterpret_cast<uint32_t*>(ws + kWsArrived);
   p.partials = reinterpret_cast<float*>(ws + kWsPartials);
   const bool f16 = dt == NVR_F16;
   // (without keys nothing is loaded: the maps are of the queries, to be valid)

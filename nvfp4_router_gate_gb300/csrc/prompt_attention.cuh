@@ -12,14 +12,6 @@ constexpr int kPaTile = 128;               // tokens of a tile, rows of a row ti
 constexpr int kPaRows = 2 * kPaTile;       // rows of a key: two row tiles
 constexpr int kPaMaxCtas = 160;
 
-// A cut key's rows, as the block with its first part knows them.
-struct PromptJoin {
-  int n_parts, tail;                       // parts; the first lies in its block's second slot
-  int q0, n_q;                             // first query row, queries
-  int head;                                // first head of the rows
-  int pad[3];
-};
-
 struct PromptParams {
   CUtensorMap tm_q, tm_k, tm_v;
   int64_t T, Tk;
@@ -38,8 +30,11 @@ struct PromptParams {
   uint16_t* out;
   float* lse;
   uint32_t* status;
-  PromptJoin* joins;                       // [blocks]
-  // [2 * blocks][256 m, 256 l, 256 x D O]: a block's first run is in its slot 0 when it
+  int min_chunk;                           // places of a block at least
+  // [blocks][8 warps of rows]: parts of the key whose first one is the block's that are begun, and
+  // written; zero between calls
+  uint32_t* arrived;
+  // [2 * blocks][256 m, 256 l, D / 4 x 256 x 4 O]: a block's first stretch is in its slot 0 when it
   // is part of a cut key, its last one in slot 1 unless the key starts the chunk
   float* partials;
 };
@@ -53,11 +48,12 @@ struct PromptGroup {
   int first[2], last[2];                   // of each row tile, from tile0: [first, last)
 };
 
-__device__ __forceinline__ int seen_end(const PromptParams& p, int pos, int kmax) {
-  return p.causal ? min(max(pos + 1, 0), kmax) : kmax;
+// The keys that a query of a position sees: [begin, end)
+__device__ __forceinline__ int seen_end(int causal, int pos, int kmax) {
+  return causal ? min(max(pos + 1, 0), kmax) : kmax;
 }
-__device__ __forceinline__ int seen_begin(const PromptParams& p, int pos) {
-  return p.window > 0 ? max(max(pos + 1, 0) - p.window, 0) : 0;
+__device__ __forceinline__ int seen_begin(int window, int pos) {
+  return window > 0 ? max(max(pos + 1, 0) - window, 0) : 0;
 }
 
 __device__ __forceinline__ PromptGroup prompt_group(const PromptParams& p, int item) {
@@ -88,7 +84,7 @@ __device__ __forceinline__ PromptGroup prompt_group(const PromptParams& p, int i
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int a = g.shift + g.i0 + w * p.qt, m = min(g.n - w * p.qt, p.qt);
-    const int hi = m > 0 ? seen_end(p, a + m - 1, g.kmax) : 0, lo = min(seen_begin(p, a), hi);
+    const int hi = m > 0 ? seen_end(p.causal, a + m - 1, g.kmax) : 0, lo = min(seen_begin(p.window, a), hi);
     g.first[w] = lo / kPaTile;
     g.last[w] = hi > lo ? (hi + kPaTile - 1) / kPaTile : g.first[w];
     if (hi > lo) {
@@ -135,8 +131,5 @@ __device__ __forceinline__ float2 unpack_16(uint32_t u) {
   if (kF16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
-
-// Joins the cut keys of `blocks` blocks (csrc/prompt_join.cu); the last launch of a call.
-nvr_status launch_prompt_join(const PromptParams& p, int D, bool f16, int blocks, int sms, cudaStream_t s);
 
 }  // namespace nvr
