@@ -78,7 +78,7 @@ struct PaSmem {
   static constexpr int kStat = kOut + kPaTile * 128;         // per row tile and row: m, l
   static constexpr int kRunsAt = kStat + 2 * 2 * kPaTile * 4;
   static constexpr int kBarAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));
-  static constexpr int kTotal = kBarAt + (2 * kRuns + 3 * kSlots + 2 * 9 + 1) * 8 + 64 + 1024;
+  static constexpr int kTotal = kBarAt + (2 * kRuns + 3 * kSlots + 2 * 7 + 1) * 8 + 64 + 1024;
 };
 
 // D fp32 (1 in bits 4-5), A and B bf16 (1) or fp16 (0) in bits 7-9 and 10-12, B
@@ -211,8 +211,7 @@ struct Block {
   uint8_t* smem;
   Run* s_runs;
   float* s_stat;                           // [row tile][m, l][row]
-  uint64_t *run_full, *run_empty, *kv_full, *kv_empty, *v_clean, *q_full, *q_empty, *s_full, *p_half, *p_full, *h_full,
-      *o_full, *o_empty, *stat_full, *drained;
+  uint64_t *run_full, *run_empty, *kv_full, *kv_empty, *v_clean, *q_full, *q_empty, *s_full, *p_full, *o_full, *o_empty, *stat_full, *drained;
   uint32_t* tmem_holder;
   volatile int* abort_flag;
   int* s_start;                            // item of the chunk's start, offset inside it
@@ -232,10 +231,8 @@ struct Block {
     q_full = v_clean + NS;
     q_empty = q_full + 2;
     s_full = q_empty + 2;
-    p_half = s_full + 2;
-    p_full = p_half + 2;
-    h_full = p_full + 2;
-    o_full = h_full + 2;
+    p_full = s_full + 2;
+    o_full = p_full + 2;
     o_empty = o_full + 2;
     stat_full = o_empty + 2;
     drained = stat_full + 2;
@@ -274,9 +271,11 @@ struct Member : Block<D> {
 // unrolled code), and sixteen warps of six roles share the instruction cache.  So all but the
 // inner loop of the softmax and the issue of the products is in loops of few instructions.
 
-// The products, by one lane of a warp for each row tile w (neither waits for the other's
-// softmax): what lies between the arrival of P and the issue of the products is the chain
-// that the tensor cores wait for.
+// The products, by a warp for each row tile w: neither waits for the other's softmax.  What
+// lies between the arrival of P and the issue of the products is the chain that the tensor
+// cores wait for: every other wait comes first, and an elected lane of the whole warp issues
+// them (descriptors in uniform registers: 256 rows over 128 tokens took 3900 clocks when one
+// lane went through all of it by itself, and take 3000).
 template <int D, bool kF16>
 __device__ __forceinline__ bool products(uint32_t tmem, int w) {
   using Sm = PaSmem<D>;
@@ -295,18 +294,14 @@ __device__ __forceinline__ bool products(uint32_t tmem, int w) {
       tc_mma_ss(t_s, q_low + o, k + o, id_s, i != 0);
     }
   };
-  auto weigh = [&](int slot, bool add, int half) {
+  auto weigh = [&](int slot, bool add) {
     const uint32_t v = v_low + slot * kTileLow;
 #pragma unroll
-    for (int x = 0; x < kPaTile / 32; ++x) {
+    for (int i = 0; i < kPaTile / 16; ++i)
       // 16 tokens: two groups of eight 128-byte rows; 64-channel atoms a tile of rows apart
-      const int i = half * (kPaTile / 32) + x;
-      tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || x != 0);
-    }
+      tc_mma_ts(t_o, t_s + 8 * i, v + (i * 2048 >> 4), id_o, add || i != 0);
   };
-  auto have = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, me.abort_flag);
-  };
+  auto have = [&](uint64_t* bar, uint32_t parity) { return me.wait_all(bar, parity); };
   uint32_t ph_q = 0, ph_p = 0, ph_o = 1, clean = 0;    // (bit i of clean: the phase of slot 2 i + 1)
   int n_tile = 0, n_run = 0;                           // tiles whose scores were issued (or passed by), runs taken
   // the tile whose weights come next: 1, 2 its row tile's first, 4 its last one, 8 masked; 16 passed by
@@ -315,7 +310,7 @@ __device__ __forceinline__ bool products(uint32_t tmem, int w) {
   for (bool more = true; more || prev;) {
     uint32_t cur = 0;
     while (more && j >= n) {
-      if (n_run) mbar_arrive(me.run_empty + (n_run - 1) % kRuns);
+      if (n_run) me.arrive(me.run_empty + (n_run - 1) % kRuns);
       if (!have(me.run_full + n_run % kRuns, (n_run / kRuns) & 1)) return false;
       const volatile Run* run = me.s_runs + n_run % kRuns;
       ++n_run;
@@ -346,35 +341,43 @@ __device__ __forceinline__ bool products(uint32_t tmem, int w) {
       }
     }
     if (cur && !have(me.kv_full + k_slot, ((2 * n_tile) / NS) & 1)) return false;
-    if (prev & 1u) {
-      if (!have(me.p_half + w, ph_p)) return false;
-      tc_fence_after();
-      weigh(v_slot, !(prev & 2u), 0);
-      tc_commit(me.h_full + w);
-      if (!have(me.p_full + w, ph_p)) return false;
-      ph_p ^= 1u;
-      tc_fence_after();
-      weigh(v_slot, true, 1);
-      if (prev & 4u) tc_commit(me.o_full + w);
-    }
     if (cur & 2u) {
+      // (between runs: the last weights do not wait for the next queries)
+      if (prev & 1u) {
+        if (!have(me.p_full + w, ph_p)) return false;
+        ph_p ^= 1u;
+        tc_fence_after();
+        if (elect_one()) {
+          weigh(v_slot, !(prev & 2u));
+          if (prev & 4u) tc_commit(me.o_full + w);
+        }
+        __syncwarp();
+      }
       if (!have(me.q_full + w, ph_q)) return false;
       ph_q ^= 1u;
+    } else if (prev & 1u) {
+      if (!have(me.p_full + w, ph_p)) return false;
+      ph_p ^= 1u;
     }
     tc_fence_after();
-    if (cur & 1u) {
-      score(k_slot);
-      tc_commit(me.s_full + w);
-      if (cur & 4u) tc_commit(me.q_empty + w);
+    if (elect_one()) {
+      if ((prev & 1u) && !(cur & 2u)) {
+        weigh(v_slot, !(prev & 2u));
+        if (prev & 4u) tc_commit(me.o_full + w);
+      }
+      if (cur & 1u) {
+        score(k_slot);
+        tc_commit(me.s_full + w);
+        if (cur & 4u) tc_commit(me.q_empty + w);
+      }
+      if (prev) tc_commit(me.kv_empty + v_slot);
+      if (cur) tc_commit(me.kv_empty + k_slot);
     }
-    if (prev) tc_commit(me.kv_empty + v_slot);
-    if (cur) {
-      tc_commit(me.kv_empty + k_slot);
-      ++n_tile;
-    }
+    __syncwarp();
+    if (cur) ++n_tile;
     prev = cur;
   }
-  mbar_arrive(me.run_empty + (n_run - 1) % kRuns);
+  me.arrive(me.run_empty + (n_run - 1) % kRuns);
   return true;
 }
 
@@ -693,6 +696,45 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
         f *= f_own;
       }
+      // 128 bytes of every row: a lane stores vector lane % 8 of every fourth row
+      auto store_rows = [&](int c) {
+        __syncwarp();
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + c * 2 + (me.lane % 8) * 16;
+#pragma unroll 4
+        for (int r = me.lane / 8; r < 32; r += 4) {
+          const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(rows_at + r * 128 + (((me.lane ^ r) & 7) << 4));
+          if ((rows_on >> r) & 1u) *reinterpret_cast<uint4*>(out + to * (D * 2)) = v;
+        }
+        __syncwarp();
+      };
+      if (parts == 1 && !p.prefix_lse && any) {
+        // (usually.  The next run's products wait for the accumulator: 64 channels at once, it is
+        // read after 1500 clocks; 16 channels at a time on their way out it took 4800.)
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t y[2][32];
+          tmem_load32_start(t_o + c, y[0]);
+          tmem_load32_start(t_o + c + 32, y[1]);
+          tmem_load32_finish(y[0]);
+          tmem_load32_finish(y[1]);
+          if (c + 64 == D) {
+            tc_fence_before();
+            me.arrive(me.o_empty + w);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t* x = y[i / 4] + 8 * (i % 4);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = pack_16<kF16>(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
+            put_vector(i, make_uint4(h[0], h[1], h[2], h[3]));
+          }
+          store_rows(c);
+        }
+        if (on && p.lse) p.lse[out_row] = z;
+        continue;
+      }
       const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
@@ -756,18 +798,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         for (int x = 0; x < 16; x += 8)
           put_vector((c % 64 + x) / 8, make_uint4(pack_16<kF16>(o[x], o[x + 1]), pack_16<kF16>(o[x + 2], o[x + 3]),
                                                   pack_16<kF16>(o[x + 4], o[x + 5]), pack_16<kF16>(o[x + 6], o[x + 7])));
-        __syncwarp();
-        if (c % 64 == 48) {
-          // 128 bytes of every row: a lane stores vector lane % 8 of every fourth row
-          uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + (c - 48) * 2 + (me.lane % 8) * 16;
-#pragma unroll 2
-          for (int r = me.lane / 8; r < 32; r += 4) {
-            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, r);
-            const uint4 v = *reinterpret_cast<const uint4*>(rows_at + r * 128 + (((me.lane ^ r) & 7) << 4));
-            if ((rows_on >> r) & 1u) *reinterpret_cast<uint4*>(out + to * (D * 2)) = v;
-          }
-          __syncwarp();
-        }
+        if (c % 64 == 48) store_rows(c - 48);
       }
       if (on && p.lse) p.lse[out_row] = z;
     }
@@ -788,12 +819,11 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
   // range lies below; bf16 has fp32's range, and results need room above the weights.
   constexpr float kRise = kF16 ? kLift : 0.0f;
   constexpr float kMostSum = 32768.0f;
-  constexpr int kHalf = kPaTile / 2;
   const int w = threadIdx.x >> 7, wl = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
   const uint32_t t_s = tmem + lanes + w * kPaTile, t_o = tmem + lanes + 2 * kPaTile + w * D;
   const int iq = row / Gt;
-  uint32_t ph_s = 0, ph_h = 0, ph_stat = 1;
+  uint32_t ph_s = 0, ph_stat = 1;
   // What hides a score: -inf once it is scaled.  (A scale of zero hides nothing by itself: its
   // scores are written as zeros and scaled by one.)
   const bool flat = scale == 0.0f;
@@ -807,9 +837,10 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
     // (rows that nobody asked for see all: nothing of theirs matters, nothing is masked for them)
     const int pos = run.pos0 + dq, kmax = run.kmax;
     const int hi = on ? seen_end(causal, pos, kmax) - t00 : 0, lo = on ? seen_begin(window, pos) - t00 : 0;
-    // every row of the warp sees all tokens of the tiles [full0, full1)
-    const int full0 = (max(__reduce_max_sync(0xFFFFFFFFu, on ? lo : 0), 0) + kPaTile - 1) / kPaTile;
-    const int full1 = max(__reduce_min_sync(0xFFFFFFFFu, on ? hi : INT32_MAX), 0) / kPaTile;
+    // every row of the warp sees all tokens of [all_from, all_to), those of the tiles [full0, full1) among them
+    const int all_from = max(__reduce_max_sync(0xFFFFFFFFu, on ? lo : 0), 0);
+    const int all_to = max(__reduce_min_sync(0xFFFFFFFFu, on ? hi : INT32_MAX), 0);
+    const int full0 = (all_from + kPaTile - 1) / kPaTile, full1 = all_to / kPaTile;
     float m_neg = on ? INFINITY : 0.0f, l = 0.0f;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
@@ -819,109 +850,104 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
       if (any_on) {
         const bool masked = j < full0 || j >= full1 || flat;
         const int from = on ? lo - j * kPaTile : 0, to = on ? hi - j * kPaTile : kPaTile;     // tokens that the row sees
-        // In two halves of 64 tokens: P V of the first starts under the second.
+        if (masked) {
+          // in place: one loop of weights for all tiles
 #pragma unroll 1
-        for (int c0 = 0; c0 < kPaTile; c0 += kHalf) {
-          if (masked) {
-            // in place: one loop of weights for all tiles
+          for (int c = 0; c < kPaTile; c += 16) {
+            if (j * kPaTile + c >= all_from && j * kPaTile + c + 16 <= all_to && !flat) continue;
+            uint32_t y[16];
+            tmem_load16_start(t_s + c, y);
+            tmem_load16_finish(y);
+            const uint32_t see = tokens32(c, from, to);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) y[x] = see & (1u << x) ? (flat ? 0u : y[x]) : __float_as_uint(hidden);
+            tmem_store16(t_s + c, y);
+          }
+          tmem_store_wait();
+        }
+        // The maximum is looked for by rows that see tokens here and none before, and again where
+        // weights add up to more than kMostSum (or to no number).  (Each row by itself: what lies
+        // in one does not change another's roundings.)
+        const bool sees = on && from < kPaTile && to > 0;
+        bool need = m_neg == INFINITY && sees, moved = !on;
+        bool look = (masked || j == j0) && __any_sync(0xFFFFFFFFu, need);
+        uint32_t pr[kPaTile / 2];
+        float sum;
+        bool first_look = j == j0 && !masked;
 #pragma unroll 1
-            for (int c = c0; c < c0 + kHalf; c += 16) {
+        for (;;) {
+          if (look) {
+            // m is set by the largest score so far, this tile's included (of a first tile without masks:
+            // by those of its first 16 tokens, usually near enough)
+            float top = -INFINITY;
+            const int some = first_look ? 16 : kPaTile;
+#pragma unroll 1
+            for (int c = 0; c < some; c += 16) {
               uint32_t y[16];
               tmem_load16_start(t_s + c, y);
               tmem_load16_finish(y);
-              const uint32_t see = tokens32(c, from, to);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) y[x] = see & (1u << x) ? (flat ? 0u : y[x]) : __float_as_uint(hidden);
-              tmem_store16(t_s + c, y);
+              for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(y[x]) * to_log2);
             }
-            tmem_store_wait();
-          }
-          // The maximum is looked for by rows that see tokens here and none before, and again where
-          // weights add up to more than kMostSum (or to no number).  (Each row by itself: what lies
-          // in one does not change another's roundings.)
-          const bool sees = on && from < c0 + kHalf && to > c0;
-          bool need = m_neg == INFINITY && sees, moved = !on;
-          bool look = (masked || j == j0) && __any_sync(0xFFFFFFFFu, need);
-          uint32_t pr[kHalf / 2];
-          float sum;
+            const float now = need ? fminf(m_neg, kRise - top) : m_neg;
+            moved = moved || (need && !first_look);
+            first_look = false;
+            const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
+            m_neg = now;
+            l *= shrink;
+            if (j > j0) {
+              // (earlier tiles are in O: S came after them)
 #pragma unroll 1
-          for (;;) {
-            if (look) {
-              // m is set by the largest score so far, this half's included
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = c0; c < c0 + kHalf; c += 16) {
+              for (int c = 0; c < D; c += 16) {
                 uint32_t y[16];
-                tmem_load16_start(t_s + c, y);
+                tmem_load16_start(t_o + c, y);
                 tmem_load16_finish(y);
 #pragma unroll
-                for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(y[x]) * to_log2);
-              }
-              const float now = need ? fminf(m_neg, kRise - top) : m_neg;
-              moved = moved || need;
-              const float shrink = now < m_neg ? ex2(now - m_neg) : 1.0f;
-              m_neg = now;
-              l *= shrink;
-              if (j > j0 || c0 > 0) {
-                // (earlier tiles are in O, S came after them; the first half may be on its way)
-                if (c0 > 0) {
-                  if (!me.wait_all(me.h_full + w, ph_h)) return false;
-                  tc_fence_after();
-                }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  uint32_t y[16];
-                  tmem_load16_start(t_o + c, y);
-                  tmem_load16_finish(y);
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * shrink);
-                  tmem_store16(t_o + c, y);
-                }
+                for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * shrink);
+                tmem_store16(t_o + c, y);
               }
             }
-            uint32_t s[2][32];
-            tmem_load32_start(t_s + c0, s[0]);
-            uint64_t sum2 = f2_pack(0.0f, 0.0f);
-            const float add = m_neg == INFINITY ? 0.0f : m_neg;          // (nothing but -inf seen so far)
-            const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
+          }
+          uint32_t s[2][16];
+          tmem_load16_start(t_s, s[0]);
+          uint64_t sum2 = f2_pack(0.0f, 0.0f);
+          const float add = m_neg == INFINITY ? 0.0f : m_neg;          // (nothing but -inf seen so far)
+          const uint64_t k2 = f2_pack(to_log2, to_log2), m2 = f2_pack(add, add);
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 32) {
-              uint32_t (&y)[32] = s[c / 32];
-              tmem_load32_finish(y);
-              if (c == 0) tmem_load32_start(t_s + c0 + 32, s[1]);
+          for (int c = 0; c < kPaTile; c += 16) {
+            uint32_t (&y)[16] = s[c / 16 % 2];
+            tmem_load16_finish(y);
+            if (c + 16 < kPaTile) tmem_load16_start(t_s + c + 16, s[(c / 16 + 1) % 2]);
 #pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                const uint64_t v = f2_fma(f2_pack(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), k2, m2);
-                const float a = ex2(f2_lo(v)), b = ex2(f2_hi(v));
-                sum2 = f2_add(sum2, f2_pack(a, b));
-                pr[(c + x) / 2] = pack_16<kF16>(a, b);
-              }
+            for (int x = 0; x < 16; x += 2) {
+              const uint64_t v = f2_fma(f2_pack(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), k2, m2);
+              const float a = ex2(f2_lo(v)), b = ex2(f2_hi(v));
+              sum2 = f2_add(sum2, f2_pack(a, b));
+              pr[(c + x) / 2] = pack_16<kF16>(a, b);
             }
-            sum = f2_lo(sum2) + f2_hi(sum2);
-            need = !moved && (!(sum <= kMostSum) || (m_neg == INFINITY && sees));
-            look = __any_sync(0xFFFFFFFFu, need);
-            if (!look) break;
           }
-          l += sum;
-          // P over the columns of S that have been read
-#pragma unroll
-          for (int c = 0; c < kHalf / 2; c += 16) {
-            uint32_t x[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
-            tmem_store16(t_s + c0 / 2 + c, x);
-          }
-          tmem_store_wait();
-          tc_fence_before();
-          me.arrive((c0 ? me.p_full : me.p_half) + w);
+          sum = f2_lo(sum2) + f2_hi(sum2);
+          need = !moved && (!(sum <= kMostSum) || (m_neg == INFINITY && sees));
+          look = __any_sync(0xFFFFFFFFu, need);
+          if (!look) break;
         }
+        l += sum;
+        // P over the columns of S that have been read
+#pragma unroll
+        for (int c = 0; c < kPaTile / 2; c += 16) {
+          uint32_t x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = pr[c + k];
+          tmem_store16(t_s + c, x);
+        }
+        tmem_store_wait();
+        tc_fence_before();
+        me.arrive(me.p_full + w);
       } else {
         // (rows that nobody asked for: their P may be anything)
         tc_fence_before();
-        me.arrive(me.p_half + w);
         me.arrive(me.p_full + w);
       }
-      ph_h ^= 1u;
     }
     // (me.o_empty: the statistics of the run before have been read as well)
     if (!me.wait_all(me.o_empty + w, ph_stat)) return false;
@@ -954,7 +980,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     for (int i = 0; i < NS; ++i) { mbar_init(sh.kv_full + i, 1); mbar_init(sh.kv_empty + i, 2 + i % 2); mbar_init(sh.v_clean + i, 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh.q_full + i, 1); mbar_init(sh.q_empty + i, 1); mbar_init(sh.s_full + i, 1);
-      mbar_init(sh.p_half + i, 4); mbar_init(sh.p_full + i, 4); mbar_init(sh.h_full + i, 1);
+      mbar_init(sh.p_full + i, 4);
       mbar_init(sh.o_full + i, 1); mbar_init(sh.o_empty + i, 4); mbar_init(sh.stat_full + i, 4);
     }
     mbar_init(sh.drained, 2);
@@ -1012,13 +1038,11 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
     } else if (warp < 12) {
       ok = rows_out<D, kF16>(p, tmem);
     } else if (warp < 14) {
-      if (lane == 0) {
-        ok = products<D, kF16>(tmem, warp - 12);
-        // nothing of this block's is under way when the tensor memory goes back
-        tc_commit(sh.drained);
-        wait_bounded(sh.drained, 0, sh.abort_flag);
-      }
+      ok = products<D, kF16>(tmem, warp - 12);
+      // nothing of this block's is under way when the tensor memory goes back
+      if (elect_one()) tc_commit(sh.drained);
       __syncwarp();
+      __all_sync(0xFFFFFFFFu, wait_bounded(sh.drained, 0, sh.abort_flag));
     } else {
       ok = warp == 14 ? walk<D>(p, f0, f1, chunk) : look_over<D, kF16>();
     }
