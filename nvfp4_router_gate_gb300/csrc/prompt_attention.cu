@@ -46,11 +46,16 @@ namespace {
 
 constexpr int kPaThreads = 512;
 constexpr int kPaPlaces = 2;               // places of a tile in the flat order
-constexpr int kPaKeyCost = 3;              // starting and ending a key counts as this many places
+// Starting and ending a key counts as this many places: 8192 tokens of 64 heads 782 us at 3,
+// 764 at 5, 766 at 6; 64 rows of 48 sequences 43, 43, 43.
+constexpr int kPaKeyCost = 5;
 // Fewest places of a block; of a key of n tiles it has sqrt(n) tiles at least: the parts are
 // joined one after the other.
 constexpr int kPaMinChunk = 4;
-constexpr int kPaWhole = 4;                // keys of at most this many tiles are not cut
+// Keys of at most this many tiles are not cut (a block more or less even then): ragged prompts
+// 256 us at 4, 251 at 16, 245 at 24; 2571 tokens of 16 heads 42, 50, 35; two chunks of 1132
+// tokens, 128 heads, 122, 107, 108; pictures 96, 98, 99.
+constexpr int kPaWhole = 24;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
@@ -729,6 +734,45 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[k] = pack_16<kF16>(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
             put_vector(i, make_uint4(h[0], h[1], h[2], h[3]));
+          }
+          store_rows(c);
+        }
+        if (on && p.lse) p.lse[out_row] = z;
+        continue;
+      }
+      if (parts == 1 && any) {
+        // (with a prefix: 64 channels of it on their way at a time)
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint4 prev[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            prev[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (f_before != 0.0f) prev[i] = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 64; x += 16) {
+            uint32_t y[16];
+            tmem_load16_start(t_o + c + x, y);
+            tmem_load16_finish(y);
+            if (c + x + 16 == D) {
+              tc_fence_before();
+              me.arrive(me.o_empty + w);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 u = prev[x / 8 + i];
+              const uint32_t b[4] = {u.x, u.y, u.z, u.w};
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 v = unpack_16<kF16>(b[k]);
+                const float y0 = __uint_as_float(y[8 * i + 2 * k]) * f, y1 = __uint_as_float(y[8 * i + 2 * k + 1]) * f;
+                h[k] = pack_16<kF16>(fmaf(v.x, f_before, y0), fmaf(v.y, f_before, y1));
+              }
+              put_vector(x / 8 + i, make_uint4(h[0], h[1], h[2], h[3]));
+            }
           }
           store_rows(c);
         }

@@ -4,10 +4,18 @@
 //   x <- x w / sqrt(sum x^2 / D + eps),  (a, b) -> (a c - b s, b c + a s),
 // with c and s of pair i from row positions[axes[i]] of the tables.
 //
-// Bound by memory: every byte of the heads is read and written once, the tables'
-// rows are read once a token.  A warp takes a run of the head groups of one token,
-// so that a lane's eight pairs of angles stay in its registers; the loads of the
-// next two groups are under way meanwhile.
+// Bound by memory: every byte of the heads is read and written once, the tables' rows are
+// read once a token.  Measured (inputs not in L2): 8192 tokens of 72 heads of 128 channels
+// with norm, 302 MB, 52 us (5.8 TB/s); one such token 2.7 us, the launch and three loads
+// one after the other (position, angle, store).
+//
+// A warp takes a stretch of all tokens' head groups, equally many for each: with a token a
+// warp the last of 2.25 waves was mostly empty (73 us).  A lane's eight pairs of angles stay
+// in its registers over a token.  The next two groups' loads are under way through a ring
+// in shared memory, a thread's own slots: kept in registers they cost spills, and the moves
+// from one group to the next waited for them (59 us).  Then the instructions bind as much
+// as the memory: pairs of channels go through the packed fp32 instructions, and addresses
+// are worked out where a token or its keys begin.
 #include <cuda_fp16.h>
 
 #include "nvr_internal.h"
@@ -18,6 +26,10 @@ namespace nvr {
 namespace {
 
 constexpr int kRopeThreads = 128;
+// Of a multiprocessor.  The prompt above: 4 blocks 52 us, 5 52, 6 53; a chunk of 2537 tokens
+// of 54 heads 15.5, 15.2, 16.1.
+constexpr int kRopeBlocks = 5;
+constexpr int kRopeAhead = 2;            // steps whose loads are under way (1: 56 us, 3: 55)
 
 struct RopeParams {
   const void *q, *k;
@@ -33,66 +45,58 @@ struct RopeParams {
   const float *q_weight, *k_weight;
   float eps;
   int steps_q, steps;     // groups of heads of the queries, of both
-  int parts;              // warps of a token
+  int64_t share, extra;   // steps of a warp, warps that have one more
   int shift;              // lanes of a head: 1 << shift
   uint32_t used;          // bit a: some pair goes by axis a
-  uint8_t axes[PROMPT_ROPE_MAX_PAIRS];
+  alignas(4) uint8_t axes[PROMPT_ROPE_MAX_PAIRS];
 };
 
-// Eight channels as they lie in memory, and as fp32.
+// Eight channels as they lie in memory (16-bit types one vector of 16 bytes, fp32 two), to
+// four pairs of fp32.
 template <typename E>
-struct Eight {
-  uint4 u;
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-  }
-  __device__ __forceinline__ void widen(float (&x)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void widen(const uint4* u, uint64_t (&x)[4]) {
+  const uint4 a = u[0];
+  if constexpr (std::is_same<E, float>::value) {
+    const uint4 b = u[kRopeThreads];
+    x[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y)); x[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
+    x[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y)); x[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
+  } else {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (sizeof(E) == sizeof(__half) && std::is_same<E, __half>::value) {
+      if constexpr (std::is_same<E, __half>::value) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x; x[2 * i + 1] = f.y;
+        x[i] = f2_pack(f.x, f.y);
       } else {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        x[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
       }
     }
   }
-};
-template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    a = __ldg(src);
-    b = __ldg(src + 1);
-  }
-  __device__ __forceinline__ void widen(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-};
+}
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
 template <typename E>
-__device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[8]) {
+__device__ __forceinline__ void store8(E* to, const uint64_t (&x)[4]) {
   if constexpr (std::is_same<E, float>::value) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+    float4* dst = reinterpret_cast<float4*>(to);
+    dst[0] = make_float4(f2_lo(x[0]), f2_hi(x[0]), f2_lo(x[1]), f2_hi(x[1]));
+    dst[1] = make_float4(f2_lo(x[2]), f2_hi(x[2]), f2_lo(x[3]), f2_hi(x[3]));
   } else {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (std::is_same<E, __half>::value) {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        const __half2 h = __floats2half2_rn(f2_lo(x[i]), f2_hi(x[i]));
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(x[i]), f2_hi(x[i]));
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -114,17 +118,20 @@ __device__ __forceinline__ int64_t table_at(const RopeParams& p, int64_t t, int 
 // the channels behind the rotated ones are shared out in the same way); with
 // neighbouring pairs each vector holds four.
 template <typename In, typename Out, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 6)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 prompt_rope_kernel(const __grid_constant__ RopeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int kVec = sizeof(In) == 4 ? 2 : 1;                  // vectors of eight channels
+  __shared__ alignas(16) float weights[2][PROMPT_ROPE_MAX_D];
+  __shared__ uint4 ring[kRopeAhead + 1][2 * kVec][kRopeThreads];  // a thread's own vectors alone
   const int lane = threadIdx.x & 31, L = 1 << p.shift, l = lane & (L - 1), sub_head = lane >> p.shift;
   const int per_step = 32 >> p.shift;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / p.parts;
-  if (t >= p.T) return;
-  const int part = static_cast<int>(unit - t * p.parts);
-  const int s0 = p.steps * part / p.parts, s1 = p.steps * (part + 1) / p.parts;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  int64_t left = p.share + (warp < p.extra ? 1 : 0);
+  const int64_t first = p.share * warp + (warp < p.extra ? warp : p.extra);
+  int64_t t = first >> 31 ? first / p.steps : static_cast<int>(first) / p.steps;   // (a short division will mostly do)
+  int st = static_cast<int>(first - t * p.steps);
 
   int o0, o1;                                  // the channels of this lane's vectors
   bool on0, on1;                               // they turn
@@ -137,101 +144,143 @@ prompt_rope_kernel(const __grid_constant__ RopeParams p) {
     o0 = on0 ? 8 * l : p.rot + 16 * (l - turning);
     o1 = on0 ? p.rot / 2 + 8 * l : o0 + 8;
   }
-  // The vectors of step s; heads past the last one read the first.
-  const int64_t row_q = t * p.q_stride, row_k = t * p.k_stride;
-  Eight<In> next[2][2];
-  auto load = [&](int s, Eight<In> (&v)[2]) {
-    const bool key = s >= p.steps_q;
-    const int h = (key ? s - p.steps_q : s) * per_step + sub_head, n = key ? p.Hkv : p.Hq;
-    const int64_t at = (key ? row_k : row_q) + static_cast<int64_t>(h < n ? h : 0) * p.D;
-    v[0].load(key ? p.k : p.q, at + o0);
-    v[1].load(key ? p.k : p.q, at + o1);
-  };
-  load(s0, next[0]);
-  if (s0 + 1 < s1) load(s0 + 1, next[1]);
+  const int pair0 = kInterleaved ? o0 / 2 : o0, pair1 = kInterleaved ? o1 / 2 : o0 + 4;   // four pairs from each
+  uint32_t ax0 = 0, ax1 = 0;                   // their axes, a byte each
+  if (on0) ax0 = *reinterpret_cast<const uint32_t*>(p.axes + pair0);
+  if (on1) ax1 = *reinterpret_cast<const uint32_t*>(p.axes + pair1);
 
-  const bool ok = p.rot == 0 || positions_ok(p, t);
-  float c[8], s[8];
+  // Lane a holds the position of axis a.
+  const bool holds = lane < PROMPT_ROPE_MAX_AXES && (p.used >> lane & 1);
+  auto position = [&](int64_t token) { return holds ? __ldg(p.positions + lane * p.axis_stride + token) : 0; };
+  int pos = left > 0 ? position(t) : 0, pos_next = left > p.steps - st ? position(t + 1) : 0;
+
+  // The vectors of a step; heads past the last one read the first.
+  int64_t t_load = t;
+  int s_load = st, slot_load = 0, h_load = 0, n_load = 0;
+  const In* from = nullptr;                    // the queries' or keys' row
+  auto enter_load = [&]() {
+    const bool key = s_load >= p.steps_q;
+    h_load = (key ? s_load - p.steps_q : s_load) * per_step + sub_head;
+    n_load = key ? p.Hkv : p.Hq;
+    from = static_cast<const In*>(key ? p.k : p.q) + t_load * (key ? p.k_stride : p.q_stride);
+  };
+  auto load = [&]() {
+    const In* src = from + (h_load < n_load ? h_load * p.D : 0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    const bool on = i < 4 ? on0 : on1;
-    const int pair = !kInterleaved ? o0 + i : (i < 4 ? o0 / 2 + i : o1 / 2 + i - 4);
-    if (ok && on) {
-      const int64_t at = table_at(p, t, pair);
-      c[i] = __ldg(p.cos + at);
-      s[i] = __ldg(p.sin + at);
+    for (int i = 0; i < kVec; ++i) {
+      copy16(&ring[slot_load][i][threadIdx.x], src + o0 + 4 * i);
+      copy16(&ring[slot_load][kVec + i][threadIdx.x], src + o1 + 4 * i);
     }
+    slot_load = slot_load == kRopeAhead ? 0 : slot_load + 1;
+    h_load += per_step;
+    if (++s_load == p.steps) { s_load = 0; ++t_load; }
+    if (s_load == 0 || s_load == p.steps_q) enter_load();
+  };
+  enter_load();
+#pragma unroll 1
+  for (int i = 0; i < kRopeAhead; ++i) {
+    if (i < left) load();
+    asm volatile("cp.async.commit_group;");
   }
-  float w[2][8];
-  bool norm = false;
-  auto weights = [&](const float* src) {
-    norm = src != nullptr;
-    if (!norm) return;
+  for (int e = threadIdx.x; e < p.D; e += kRopeThreads) {
+    if (p.q_weight) weights[0][e] = __ldg(p.q_weight + e);
+    if (p.k_weight) weights[1][e] = __ldg(p.k_weight + e);
+  }
+  __syncthreads();
+
+  bool ok;
+  float c[8], s[8];
+  auto angles = [&]() {
+    ok = !__any_sync(0xFFFFFFFFu, holds && (pos < 0 || pos >= p.n_pos));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      w[0][i] = __ldg(src + o0 + i);
-      w[1][i] = __ldg(src + o1 + i);
+      const int row = __shfl_sync(0xFFFFFFFFu, pos, (i < 4 ? ax0 : ax1) >> (8 * (i & 3)) & 31);
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+      if (ok && (i < 4 ? on0 : on1)) {
+        const int64_t at = static_cast<int64_t>(row) * (p.rot / 2) + (i < 4 ? pair0 + i : pair1 + i - 4);
+        c[i] = __ldg(p.cos + at);
+        s[i] = __ldg(p.sin + at);
+      }
     }
   };
-  weights(s0 < p.steps_q ? p.q_weight : p.k_weight);
   const float inv_D = 1.0f / static_cast<float>(p.D);
-
-  auto step = [&](int st, Eight<In> (&v)[2]) {
+  const float* w = weights[0];
+  Out* to = nullptr;
+  int h = 0, n = 0, slot = 0;
+  bool norm = false;
+  auto enter = [&]() {
     const bool key = st >= p.steps_q;
-    if (st == p.steps_q && st > s0) weights(p.k_weight);
-    float a[8], b[8];
-    v[0].widen(a);
-    v[1].widen(b);
-    if (st + 2 < s1) load(st + 2, v);
+    h = (key ? st - p.steps_q : st) * per_step + sub_head;
+    n = key ? p.Hkv : p.Hq;
+    to = static_cast<Out*>(key ? p.k_out : p.q_out) + t * (key ? p.ko_stride : p.qo_stride);
+    w = weights[key];
+    norm = (key ? p.k_weight : p.q_weight) != nullptr;
+  };
+  bool turn = true, side = true;               // a token's first step here, the queries' or keys'
+#pragma unroll 1
+  for (; left > 0; --left) {
+    if (turn) {
+      angles();
+      pos = pos_next;
+      if (left > 2 * p.steps - st) pos_next = position(t + 2);
+    }
+    if (side) enter();
+    uint64_t a[4], b[4];
+    asm volatile("cp.async.wait_group %0;" :: "n"(kRopeAhead - 1) : "memory");
+    widen<In>(&ring[slot][0][threadIdx.x], a);
+    widen<In>(&ring[slot][kVec][threadIdx.x], b);
+    slot = slot == kRopeAhead ? 0 : slot + 1;
+    if (left > kRopeAhead) load();
+    asm volatile("cp.async.commit_group;");
     if (norm) {
-      float ss = 0.0f;
+      uint64_t two = f2_mul(a[0], a[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+      for (int i = 1; i < 4; ++i) two = f2_fma(a[i], a[i], two);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) two = f2_fma(b[i], b[i], two);
+      float ss = f2_lo(two) + f2_hi(two);
       for (int d = L / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-      const float r = 1.0f / sqrtf(fmaf(ss, inv_D, p.eps));
+      const float r = rsqrtf(fmaf(ss, inv_D, p.eps));
+      const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = a[i] * r * w[0][i];
-        b[i] = b[i] * r * w[1][i];
+      for (int i = 0; i < 4; i += 2) {
+        const float4 wa = *reinterpret_cast<const float4*>(w + o0 + 2 * i), wb = *reinterpret_cast<const float4*>(w + o1 + 2 * i);
+        a[i] = f2_mul(f2_mul(a[i], r2), f2_pack(wa.x, wa.y));
+        a[i + 1] = f2_mul(f2_mul(a[i + 1], r2), f2_pack(wa.z, wa.w));
+        b[i] = f2_mul(f2_mul(b[i], r2), f2_pack(wb.x, wb.y));
+        b[i + 1] = f2_mul(f2_mul(b[i + 1], r2), f2_pack(wb.z, wb.w));
       }
     }
     if (kInterleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-        if (on0) {
-          a[2 * i] = a0 * c[i] - a1 * s[i];
-          a[2 * i + 1] = a1 * c[i] + a0 * s[i];
-        }
-        if (on1) {
-          b[2 * i] = b0 * c[i + 4] - b1 * s[i + 4];
-          b[2 * i + 1] = b1 * c[i + 4] + b0 * s[i + 4];
-        }
+        const float a0 = f2_lo(a[i]), a1 = f2_hi(a[i]), b0 = f2_lo(b[i]), b1 = f2_hi(b[i]);
+        if (on0) a[i] = f2_pack(a0 * c[i] - a1 * s[i], a1 * c[i] + a0 * s[i]);
+        if (on1) b[i] = f2_pack(b0 * c[i + 4] - b1 * s[i + 4], b1 * c[i + 4] + b0 * s[i + 4]);
       }
     } else if (on0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a0 = a[i], b0 = b[i];
-        a[i] = a0 * c[i] - b0 * s[i];
-        b[i] = b0 * c[i] + a0 * s[i];
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t a0 = a[i], c2 = f2_pack(c[2 * i], c[2 * i + 1]), s2 = f2_pack(s[2 * i], s[2 * i + 1]);
+        a[i] = f2_fma(b[i], s2 ^ 0x8000000080000000ull, f2_mul(a0, c2));
+        b[i] = f2_fma(a0, s2, f2_mul(b[i], c2));
       }
     }
     if (!ok) {
+      asm volatile("");                        // (a branch: it is hardly ever taken)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
+      for (int i = 0; i < 4; ++i) a[i] = b[i] = 0;
     }
-    const int h = (key ? st - p.steps_q : st) * per_step + sub_head;
-    if (h < (key ? p.Hkv : p.Hq)) {
-      const int64_t at = t * (key ? p.ko_stride : p.qo_stride) + static_cast<int64_t>(h) * p.D;
-      store8<Out>(key ? p.k_out : p.q_out, at + o0, a);
-      store8<Out>(key ? p.k_out : p.q_out, at + o1, b);
+    if (h < n) {
+      Out* dst = to + h * p.D;
+      store8<Out>(dst + o0, a);
+      store8<Out>(dst + o1, b);
     }
-  };
-  for (int st = s0; st < s1; st += 2) {
-    step(st, next[0]);
-    if (st + 1 < s1) step(st + 1, next[1]);
+    h += per_step;
+    turn = ++st == p.steps;
+    if (turn) { st = 0; ++t; }
+    side = st == 0 || st == p.steps_q;
   }
 }
 
@@ -357,12 +406,15 @@ extern "C" nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k
     const int heads = 32 >> p.shift;
     p.steps_q = (Hq + heads - 1) / heads;
     p.steps = p.steps_q + (Hkv + heads - 1) / heads;
-    const int64_t each = (T * p.steps + sms * 24 - 1) / (sms * 24);
-    p.parts = each >= p.steps ? 1 : static_cast<int>((p.steps + each - 1) / each);
-    units = T * p.parts;
+    const int64_t all = T * p.steps, most = static_cast<int64_t>(sms) * kRopeBlocks * (kRopeThreads / 32);
+    units = all < most ? all : most;
+    units = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32) * (kRopeThreads / 32);
+    p.share = all / units;
+    p.extra = all % units;
   } else {
     p.shift = 0;
-    p.steps_q = p.steps = p.parts = 0;
+    p.steps_q = p.steps = 0;
+    p.share = p.extra = 0;
     units = T * (Hq + Hkv);
   }
   const int64_t blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);

@@ -130,9 +130,7 @@ def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=No
         axes = (0,) * pairs if axes is None else axes
         if len(axes) != pairs:
             raise ValueError("%d axes for %d pairs" % (len(axes), pairs))
-        if not 1 <= n_axes <= _MAX_AXES or (pairs and not 0 <= min(axes) <= max(axes) < n_axes):
-            raise ValueError("axes must be in [0, %d), positions of 1 to %d axes" % (n_axes, _MAX_AXES))
-        code = bytes(axes)
+        code = bytes(axes)                               # (the library looks at them)
         _same(dev, positions=positions, cos=cos, sin=sin)
     _same(dev, q_weight=q_weight, k_weight=k_weight)
     n = n_pos * rot // 2
@@ -143,6 +141,8 @@ def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=No
         bool(interleaved), _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight"), eps, qo, qos, ko, kos,
         _CODES[out_dtype], _raw_stream(stream))
     if st:
+        if code is not None and not (1 <= n_axes <= _MAX_AXES and max(code, default=0) < n_axes):
+            raise ValueError("axes must be in [0, %d), positions of 1 to %d axes" % (n_axes, _MAX_AXES))
         _native.check("prompt_rope", st)
     return outs[0], outs[1]
 
