@@ -83,7 +83,7 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  *                prefix: nvfp4_kv_attention without `causal`), joined with this one as if
  *                all keys had been seen at once.  A row whose prefix_lse is -inf has no
  *                prefix.  They may be out and lse themselves.
- *   out          out [T, Hq, D] of dt, 16-byte aligned
+ *   out          out [T, Hq, D] of dt, 16-byte aligned, must not overlap q, k or v
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    prompt_attention_workspace_size(...) bytes, zeroed once
  * A query that sees no key and has no prefix gets zeros and lse = -inf, one with a NaN
@@ -93,10 +93,11 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights p_t enter the
  * second product rounded to dt, relative to a running maximum (fp16: a weight below 2^-32
  * of the largest is lost there; bf16: results above 2^100 may overflow); results do not
- * depend on the order in which the GPU runs the blocks.  One kernel.  Calls whose work does not fit 31 bits (tiles of 128 keys and of 128 rows, one count over the call) are
+ * depend on the order in which the GPU runs the blocks.  One kernel.  Calls whose work does not
+ * fit 31 bits (tiles of 128 keys and of 128 rows, one count over the call) are
  * NVR_ERR_UNSUPPORTED.  The workspace's size depends on D alone (the heads are checked): it
  * holds partial results of the resident blocks, of one call at a time.  A bounded wait that
- * runs out sets its status word (nvr_read_device_status).
+ * runs out sets its status word (nvr_read_device_status); the workspace is to be zeroed again then.
  */
 size_t prompt_attention_workspace_size(int Hq, int Hkv, int D);
 nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,

@@ -1163,7 +1163,9 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
   int64_t grid = sms < kPaMaxCtas ? sms : kPaMaxCtas;
   p.min_chunk = kPaMinChunk;
   while (static_cast<int64_t>(p.min_chunk) * p.min_chunk < kPaPlaces * kPaPlaces * tiles) ++p.min_chunk;
-  if (grid > (most + p.min_chunk - 1) / p.min_chunk) grid = (most + p.min_chunk - 1) / p.min_chunk;
+  // (rows that no sequence covers are many where the batch is padded: they are cleared by all blocks)
+  const int64_t blocks = (most + p.min_chunk - 1) / p.min_chunk, clearing = p.cu_q ? (p.T + kPaRows - 1) / kPaRows : 0;
+  if (grid > blocks) grid = blocks > clearing ? blocks : clearing < grid ? clearing : grid;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1201,7 +1203,7 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (!(scale > -INFINITY && scale < INFINITY)) return NVR_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return NVR_ERR_UNSUPPORTED;
   if (!workspace || (prefix_out != nullptr) != (prefix_lse != nullptr)) return NVR_ERR_INVALID_ARG;
-  if (T > 0 && (!q || !out || B < 1 || max_q < 1)) return NVR_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !out || B < 1 || max_q < 1 || out == q || out == k || out == v)) return NVR_ERR_INVALID_ARG;
   if (Tk > 0 && (!k || !v)) return NVR_ERR_INVALID_ARG;
   if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1 || max_q > INT32_MAX - 1024)
     return NVR_ERR_UNSUPPORTED;

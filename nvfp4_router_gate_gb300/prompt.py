@@ -168,6 +168,8 @@ def _attend(q, k, v, ws, cu_q=None, max_q=None, cu_k=None, max_k=None, scale=Non
     Tk, Hkv, Dk = k.shape
     if Dk != D:
         raise ValueError("q has heads of %d channels, k of %d" % (D, Dk))
+    if not (0 <= (max_q or 0) < 1 << 31 and 0 <= (max_k or 0) < 1 << 31 and 0 <= window < 1 << 31):
+        raise ValueError("max_q, max_k and window must be in [0, 2^31)")      # (ctypes would cut them)
     if cu_q is not None:
         B = _offsets(cu_q, "cu_q")
         if max_q is None:
@@ -222,6 +224,8 @@ def prompt_attention(q, k, v, workspace=None, stream=None, **kw):
     over other keys is joined with the result.  Returns (out [T, Hq, D], lse); lse [T, Hq]
     fp32 is written when it is given."""
     dev = _here(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, heads, D], k and v [Tk, n_kv_heads, D]")
     if workspace is None:
         n = prompt_attention_workspace_size(q.shape[1], k.shape[1], q.shape[2])
         # (zeroed on the stream that uses it)
