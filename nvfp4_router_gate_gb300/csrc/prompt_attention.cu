@@ -27,8 +27,8 @@
 // P V complete.  A run's last products and the next run's first ones follow each other
 // in the same way: the pipeline does not drain.
 //
-// The work is cut as in csrc/kv_attention.cu: all keys' tiles end to end in equal
-// chunks, one per block.  The warps that come last to their rows of a cut key join the
+// Many keys, or short ones, go to the blocks whole, the longest first (kPaEven).  Others are cut
+// as in csrc/kv_attention.cu: all keys' tiles end to end in equal chunks, one per block.  The warps that come last to their rows of a cut key join the
 // parts (the others have written theirs, or are at it), in the parts' order:
 //   m = max m_i,  w_i = 2^(m_i - m),  out = sum w_i O_i / sum w_i l_i.
 // Usually that is the key's first part, the last work of its block (a second kernel took
@@ -55,6 +55,12 @@ constexpr int kPaMinChunk = 4;
 // 256 us at 4, 251 at 16, 245 at 24; 2571 tokens of 16 heads 42, 50, 35; two chunks of 1132
 // tokens, 128 heads, 122, 107, 108; pictures 96, 98, 99.
 constexpr int kPaWhole = 24;
+// Keys are shared out whole, as blocks have room for them, where none is longer than that or a
+// block gets at least this many of the longest.  In place of equal chunks of the flat order: 8192
+// tokens of 64 heads (7 a block) 691 to 660 us; ragged prompts 242 to 223, short ones 25.9 to 21.8,
+// two chunks of 1132 tokens 106 to 96; one token to one key a block 0.3 us slower.  2048 queries
+// over 8192 keys (3 a block) are 318 us in chunks, 325 whole.
+constexpr int kPaEven = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
@@ -81,7 +87,8 @@ struct PaSmem {
   static constexpr int kOut = kKV + kSlots * kTileBytes;     // 128 bytes of each row on their way out
   static constexpr int kStat = kOut + kPaTile * 128;         // per row tile and row: m, l
   static constexpr int kRunsAt = kStat + 2 * 2 * kPaTile * 4;
-  static constexpr int kBarAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));
+  static constexpr int kFirstAt = kRunsAt + kRuns * static_cast<int>(sizeof(Run));
+  static constexpr int kBarAt = kFirstAt + kPaThreads * 4;
   static constexpr int kTotal = kBarAt + (2 * kRuns + 3 * kSlots + 2 * 7 + 1) * 8 + 64 + 1024;
 };
 
@@ -219,6 +226,7 @@ struct Block {
   uint32_t* tmem_holder;
   volatile int* abort_flag;
   int* s_start;                            // item of the chunk's start, offset inside it
+  int* s_first;                            // of each thread's share of the items: those with queries before it
 
   __device__ __forceinline__ Block() {
     using Sm = PaSmem<D>;
@@ -227,6 +235,7 @@ struct Block {
     smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     s_runs = reinterpret_cast<Run*>(smem + Sm::kRunsAt);
     s_stat = reinterpret_cast<float*>(smem + Sm::kStat);
+    s_first = reinterpret_cast<int*>(smem + Sm::kFirstAt);
     run_full = reinterpret_cast<uint64_t*>(smem + Sm::kBarAt);
     run_empty = run_full + kRuns;
     kv_full = run_empty + kRuns;
@@ -386,9 +395,17 @@ __device__ __forceinline__ bool products(uint32_t tmem, int w) {
   return true;
 }
 
+// How a call's keys are shared out: in chunks of the flat order, or whole (keys of them), as blocks
+// have room for one.
+struct Share {
+  bool whole;
+  int f0, f1, chunk;
+  int keys;
+};
+
 // The walk, and the queries, keys and values of its runs in.
 template <int D>
-__device__ __forceinline__ bool walk(const PromptParams& p, int f0, int f1, int chunk) {
+__device__ __forceinline__ bool walk(const PromptParams& p, const Share& share) {
   using Sm = PaSmem<D>;
   constexpr int NS = Sm::kSlots;
   Member<D> me;
@@ -450,7 +467,7 @@ __device__ __forceinline__ bool walk(const PromptParams& p, int f0, int f1, int 
   // tiles whose first place is in it.  (Behind the tiles' come places without work.)  The
   // first place of a key of few tiles stands for all of it.
   auto stretch = [&](const PromptGroup& g, int head, int key_f0, int from, int to) {
-    const bool uncut = g.tiles <= kPaWhole;
+    const bool uncut = share.whole || g.tiles <= kPaWhole;
     const int ta = uncut ? 0 : min((from + kPaPlaces - 1) / kPaPlaces, g.tiles);
     const int tb = uncut ? g.tiles : min((to + kPaPlaces - 1) / kPaPlaces, g.tiles);
     if (uncut ? from > 0 : ta >= tb) return true;
@@ -467,25 +484,63 @@ __device__ __forceinline__ bool walk(const PromptParams& p, int f0, int f1, int 
     }
     r.free_to = seen_end(p.causal, r.pos0, g.kmax);
     r.free_from = seen_begin(p.window, r.pos0 + g.n - 1);
-    r.block = key_f0 / chunk;
-    r.parts = uncut ? 1 : (key_f0 + kPaPlaces * (g.tiles - 1)) / chunk - r.block + 1;
-    r.part = static_cast<int>(blockIdx.x) - r.block;
-    r.tail = key_f0 > r.block * chunk;
+    r.parts = 1;
+    if (!uncut) {
+      r.block = key_f0 / share.chunk;
+      r.parts = (key_f0 + kPaPlaces * (g.tiles - 1)) / share.chunk - r.block + 1;
+      r.part = static_cast<int>(blockIdx.x) - r.block;
+      r.tail = key_f0 > r.block * share.chunk;
+    }
     return hand_out(r) && copies(r);
   };
-  int item = me.s_start[0], off = me.s_start[1], f = f0;
-  PromptGroup next = prompt_group(p, item);
-  for (; f < f1 && ok; ++item) {
-    const PromptGroup g = next;
-    next = prompt_group(p, min(item + 1, n_items - 1));
-    const int cost = key_cost(g);
-    while (off < cost * p.Hv && f < f1 && ok) {
-      const int head = off / cost, at = off - head * cost, n = min(cost - at, f1 - f);
-      ok = stretch(g, head, f - at, at, at + n);
-      off += n;
-      f += n;
+  if (share.whole) {
+    // The longest come first, so blocks end within a short one of each other.
+    const int starters = min(static_cast<int>(gridDim.x), share.keys), per = (n_items + kPaThreads - 1) / kPaThreads;
+    int x = blockIdx.x;
+    while (x < share.keys && ok) {
+      const int rank = x / p.Hv;
+      // the thread whose share of the items has it, the item
+      int t = 16 * (__popc(__ballot_sync(0xFFFFFFFFu, me.s_first[16 * me.lane] <= rank)) - 1);
+      t += __popc(__ballot_sync(0xFFFFFFFFu, me.lane < 16 && me.s_first[t + (me.lane & 15)] <= rank)) - 1;
+      int item = t * per;
+      if (per > 1) {
+        int skip = rank - me.s_first[t];
+#pragma unroll 1
+        for (;; item += 32) {
+          uint32_t some = __ballot_sync(0xFFFFFFFFu, prompt_group(p, min(item + me.lane, n_items - 1)).n > 0);
+          const int n = __popc(some);
+          if (skip >= n) {
+            skip -= n;
+            continue;
+          }
+#pragma unroll 1
+          for (; skip; --skip) some &= some - 1;
+          item += __ffs(some) - 1;
+          break;
+        }
+      }
+      int next = 0;
+      if (me.lane == 0) next = starters + static_cast<int>(atomicAdd(p.handed, 1u));
+      ok = stretch(prompt_group(p, item), x - rank * p.Hv, 0, 0, 0);
+      // (a key is handed out for each that was done: the last of those that are none)
+      if (me.lane == 0 && next == starters + share.keys - 1) *p.handed = 0;
+      x = __shfl_sync(0xFFFFFFFFu, next, 0);
     }
-    off = 0;
+  } else {
+    int item = me.s_start[0], off = me.s_start[1], f = share.f0;
+    PromptGroup next = prompt_group(p, item);
+    for (; f < share.f1 && ok; ++item) {
+      const PromptGroup g = next;
+      next = prompt_group(p, min(item + 1, n_items - 1));
+      const int cost = key_cost(g);
+      while (off < cost * p.Hv && f < share.f1 && ok) {
+        const int head = off / cost, at = off - head * cost, n = min(cost - at, share.f1 - f);
+        ok = stretch(g, head, f - at, at, at + n);
+        off += n;
+        f += n;
+      }
+      off = 0;
+    }
   }
   if (ok) {
     Run r = {};
@@ -1048,27 +1103,52 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   // ---- this block's chunk of the flat order
   const int n_items = p.B * p.groups;
   const int per = (n_items + kPaThreads - 1) / kPaThreads;
-  int mine = 0;
-  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) mine += key_cost(prompt_group(p, i)) * p.Hv;
-  int incl = mine;
+  int mine = 0, some = 0, longest = 0;       // of this thread's items: places, those with queries, tiles
+  for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) {
+    const PromptGroup g = prompt_group(p, i);
+    mine += key_cost(g) * p.Hv;
+    some += g.n > 0;
+    longest = max(longest, g.tiles);
+  }
+  int incl = mine, incl_some = some;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += a;
+    const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d), b = __shfl_up_sync(0xFFFFFFFFu, incl_some, d);
+    if (lane >= d) {
+      incl += a;
+      incl_some += b;
+    }
   }
-  if (lane == 31) reinterpret_cast<int*>(sh.s_stat)[warp] = incl;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  int* sums = reinterpret_cast<int*>(sh.s_stat);
+  if (lane == 31) {
+    sums[warp] = incl;
+    sums[16 + warp] = incl_some;
+    sums[32 + warp] = longest;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int before = 0, total = 0;
+  int before = 0, total = 0, before_some = 0, total_some = 0;
+#pragma unroll 4
   for (int w = 0; w < kPaThreads / 32; ++w) {
-    const int x = reinterpret_cast<int*>(sh.s_stat)[w];
-    if (w < warp) before += x;
+    const int x = sums[w], y = sums[16 + w];
+    if (w < warp) {
+      before += x;
+      before_some += y;
+    }
     total += x;
+    total_some += y;
+    longest = max(longest, sums[32 + w]);
   }
-  const int chunk = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), p.min_chunk);
-  const int f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
-  const int f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
+  sh.s_first[tid] = before_some + incl_some - some;
+  const int blocks = static_cast<int>(gridDim.x);
+  Share share;
+  share.keys = total_some * p.Hv;
+  share.whole = longest <= kPaWhole || total / blocks >= kPaEven * kPaPlaces * longest;
+  const int chunk = share.chunk = max((total + blocks - 1) / blocks, p.min_chunk);
+  const int f0 = share.f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
+  const int f1 = share.f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
   const int excl = before + incl - mine;
   if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
     int at = excl, i = tid * per;
@@ -1084,7 +1164,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   const uint32_t tmem = *sh.tmem_holder;
 
   if (p.cu_q && warp >= 8 && warp < 12) clear_rows<D>(p, blockIdx.x * 4 + warp - 8, gridDim.x * 4);
-  if (f0 < f1) {
+  if (share.whole ? static_cast<int>(blockIdx.x) < share.keys : f0 < f1) {
     bool ok = true;
     if (warp < 8) {
       ok = softmax<D, kF16>(tmem, p.Gt, p.qt, p.causal, p.window, p.scale_log2);
@@ -1097,7 +1177,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
       __syncwarp();
       __all_sync(0xFFFFFFFFu, wait_bounded(sh.drained, 0, sh.abort_flag));
     } else {
-      ok = warp == 14 ? walk<D>(p, f0, f1, chunk) : look_over<D, kF16>();
+      ok = warp == 14 ? walk<D>(p, share) : look_over<D, kF16>();
     }
     if (!ok && lane == 0) {
       report_timeout(p.status);
@@ -1115,7 +1195,8 @@ bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 constexpr size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 constexpr size_t kWsArrived = 256;
-constexpr size_t kWsPartials = a256(kWsArrived + kPaMaxCtas * 16 * sizeof(uint32_t));
+constexpr size_t kWsHanded = a256(kWsArrived + kPaMaxCtas * 16 * sizeof(uint32_t));
+constexpr size_t kWsPartials = kWsHanded + 256;
 constexpr size_t ws_total(int D) { return a256(kWsPartials + size_t(2) * kPaMaxCtas * kPaRows * (D + 2) * 4); }
 
 // [rows][heads][D] of 16-bit values, boxes of 64 channels, box_heads and box_rows.
@@ -1246,6 +1327,7 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   p.out = static_cast<uint16_t*>(out); p.lse = lse;
   p.status = reinterpret_cast<uint32_t*>(ws + kWsStatus);
   p.arrived = reinterpret_cast<uint32_t*>(ws + kWsArrived);
+  p.handed = reinterpret_cast<uint32_t*>(ws + kWsHanded);
   p.partials = reinterpret_cast<float*>(ws + kWsPartials);
   const bool f16 = dt == NVR_F16;
   // (without keys nothing is loaded: the maps are of the queries, to be valid)

@@ -34,6 +34,7 @@ struct PromptParams {
   // [blocks][8 warps of rows]: parts of the key whose first one is the block's that are begun, and
   // written; zero between calls
   uint32_t* arrived;
+  uint32_t* handed;                        // keys handed out behind the blocks' first ones; zero between calls
   // [2 * blocks][256 m, 256 l, D / 4 x 256 x 4 O]: a block's first stretch is in its slot 0 when it
   // is part of a cut key, its last one in slot 1 unless the key starts the chunk
   float* partials;
@@ -58,8 +59,10 @@ __device__ __forceinline__ int seen_begin(int window, int pos) {
 
 __device__ __forceinline__ PromptGroup prompt_group(const PromptParams& p, int item) {
   PromptGroup g;
-  g.b = item / p.groups;
-  g.i0 = (item - g.b * p.groups) * 2 * p.qt;
+  // (a sequence's last queries, which see most, come first)
+  const int turn = item / p.B;
+  g.b = item - turn * p.B;
+  g.i0 = (p.groups - 1 - turn) * 2 * p.qt;
   int n_q, n_k;
   if (p.cu_q) {
     const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
