@@ -958,15 +958,19 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
         if (masked) {
           // in place: one loop of weights for all tiles
 #pragma unroll 1
-          for (int c = 0; c < kPaTile; c += 16) {
-            if (j * kPaTile + c >= all_from && j * kPaTile + c + 16 <= all_to && !flat) continue;
-            uint32_t y[16];
-            tmem_load16_start(t_s + c, y);
-            tmem_load16_finish(y);
+          for (int c = 0; c < kPaTile; c += 32) {
+            if (j * kPaTile + c >= all_from && j * kPaTile + c + 32 <= all_to && !flat) continue;
+            uint32_t y[2][16];
+            tmem_load16_start(t_s + c, y[0]);
+            tmem_load16_start(t_s + c + 16, y[1]);
+            tmem_load16_finish(y[0]);
+            tmem_load16_finish(y[1]);
             const uint32_t see = tokens32(c, from, to);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) y[x] = see & (1u << x) ? (flat ? 0u : y[x]) : __float_as_uint(hidden);
-            tmem_store16(t_s + c, y);
+            for (int x = 0; x < 32; ++x)
+              y[x / 16][x % 16] = see & (1u << x) ? (flat ? 0u : y[x / 16][x % 16]) : __float_as_uint(hidden);
+            tmem_store16(t_s + c, y[0]);
+            tmem_store16(t_s + c + 16, y[1]);
           }
           tmem_store_wait();
         }
@@ -987,12 +991,14 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
             // 8192 tokens 716 and 689.)
             float top = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < kPaTile; c += 16) {
-              uint32_t y[16];
-              tmem_load16_start(t_s + c, y);
-              tmem_load16_finish(y);
+            for (int c = 0; c < kPaTile; c += 32) {
+              uint32_t y[2][16];
+              tmem_load16_start(t_s + c, y[0]);
+              tmem_load16_start(t_s + c + 16, y[1]);
+              tmem_load16_finish(y[0]);
+              tmem_load16_finish(y[1]);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) top = fmaxf(top, __uint_as_float(y[x]) * to_log2);
+              for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(y[x / 16][x % 16]) * to_log2);
             }
             const float now = need ? fminf(m_neg, kRise - top) : m_neg;
             moved = moved || need;
@@ -1150,7 +1156,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   const int f0 = share.f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
   const int f1 = share.f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
   const int excl = before + incl - mine;
-  if (f0 < f1 && excl <= f0 && f0 < excl + mine) {
+  if (!share.whole && f0 < f1 && excl <= f0 && f0 < excl + mine) {
     int at = excl, i = tid * per;
     for (;; ++i) {
       const int n = key_cost(prompt_group(p, i)) * p.Hv;

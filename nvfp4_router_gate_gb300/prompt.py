@@ -18,11 +18,12 @@ import contextlib
 import torch
 
 from . import _native, new_workspace, nvr_read_device_status
-from .kv_cache import _empty, _empty_on, _on, _ptr, _raw_stream
+from .kv_cache import _empty, _empty_on, _on, _ptr
 
 _BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
 _CODES = {_BF16: _native.NVR_BF16, _F32: _native.NVR_F32, _F16: _native.NVR_F16}
 _MAX_AXES = 8
+_current = torch._C._cuda_getCurrentRawStream
 
 
 def _here(t, name):
@@ -82,69 +83,70 @@ def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=No
     bfloat16, float16 or float32; out_dtype (or q_out and k_out, which may be q and k
     themselves) the same, or a 16-bit one for float32 heads.  Returns (q_out, k_out)."""
     some = q if q is not None else k
-    dev = _here(some, "q" if q is not None else "k")
+    dev, at = _here(some, "q" if q is not None else "k"), some.get_device()
     if some.dim() != 3:
         raise ValueError("heads must be [T, heads, D]")
     T, _, D = some.shape
     dt = some.dtype
     if dt not in _CODES:
         raise TypeError("heads must be bfloat16, float16 or float32, got %s" % dt)
-    for t in (q_out, k_out):
-        if t is not None:
-            out_dtype = t.dtype if out_dtype is None else out_dtype
-    out_dtype = dt if out_dtype is None else out_dtype
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else dt
     if out_dtype is not dt and (dt is not _F32 or out_dtype not in _CODES):
         raise TypeError("heads of %s do not become %s" % (dt, out_dtype))
-    args = []
-    outs = []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+
+    def side(x, out, name):
+        """Pointer, token stride and heads, the result, its pointer and token stride."""
         if x is None:
             if out is not None:
                 raise ValueError("%s_out without %s" % (name, name))
-            args.append((None, 0, 0, None, 0))
-            outs.append(None)
-            continue
-        if x.dim() != 3 or x.dtype is not dt or x.shape[0] != T or x.shape[2] != D or x.device != dev:
+            return None, 0, 0, None, None, 0
+        if x.dim() != 3 or x.dtype is not dt or x.get_device() != at:
             raise ValueError("%s must be [T, heads, D] of one type and device with the other" % name)
-        H = x.shape[1]
-        xs = _rows(x, T, H, D, name)
+        n, H, d = x.shape
+        if n != T or d != D:
+            raise ValueError("%s must be [%d, heads, %d], as the other" % (name, T, D))
+        step = _rows(x, T, H, D, name)
         if out is None:
             out = (_empty((T, H, D), dtype=out_dtype, device=dev) if stream is None else
                    _empty_on(stream, (T, H, D), dtype=out_dtype, device=dev))
-        elif out.shape != x.shape or out.dtype is not out_dtype or out.device != dev:
+            return x.data_ptr(), step, H, out, out.data_ptr(), H * D
+        if out.shape != x.shape or out.dtype is not out_dtype or out.get_device() != at:
             raise ValueError("%s_out must be %s of %s on %s" % (name, tuple(x.shape), out_dtype, dev))
-        args.append((x.data_ptr(), xs, H, out.data_ptr(), _rows(out, T, H, D, name + "_out")))
-        outs.append(out)
+        return x.data_ptr(), step, H, out, out.data_ptr(), _rows(out, T, H, D, name + "_out")
+
+    qp, qs, Hq, q_out, qo, qos = side(q, q_out, "q")
+    kp, ks, Hkv, k_out, ko, kos = side(k, k_out, "k")
     rot = n_pos = n_axes = step = 0
-    code = None
+    code = where = cos_p = sin_p = None
     if cos is not None:
         if sin is None or positions is None or cos.dim() != 2:
             raise ValueError("cos [n_pos, pairs] needs sin and positions")
         n_pos, pairs = cos.shape
-        rot = 2 * pairs
         if positions.dim() == 1:
             positions = positions[None]
         if positions.dim() != 2 or positions.dtype is not _I32 or positions.shape[1] != T or (T > 1 and positions.stride(1) != 1):
             raise ValueError("positions must be int32 [n_axes, T], the tokens next to each other")
-        n_axes, step = positions.shape[0], positions.stride(0)
         axes = (0,) * pairs if axes is None else axes
         if len(axes) != pairs:
             raise ValueError("%d axes for %d pairs" % (len(axes), pairs))
-        code = bytes(axes)                               # (the library looks at them)
-        _same(dev, positions=positions, cos=cos, sin=sin)
-    _same(dev, q_weight=q_weight, k_weight=k_weight)
-    n = n_pos * rot // 2
-    (qp, qs, Hq, qo, qos), (kp, ks, Hkv, ko, kos) = args
-    st = _native.lib().prompt_rope(
-        qp, qs, kp, ks, _CODES[dt], T, Hq, Hkv, D, positions.data_ptr() if rot else None, step, n_axes, code,
-        _ptr(cos, _F32, n, "cos") if rot else None, _ptr(sin, _F32, n, "sin") if rot else None, n_pos, rot,
-        bool(interleaved), _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight"), eps, qo, qos, ko, kos,
-        _CODES[out_dtype], _raw_stream(stream))
+        if positions.get_device() != at or cos.get_device() != at or sin.get_device() != at:
+            _same(dev, positions=positions, cos=cos, sin=sin)
+        if pairs:
+            rot, n_axes, step = 2 * pairs, positions.shape[0], positions.stride(0)
+            code = bytes(axes)                               # (the library looks at them)
+            where, cos_p, sin_p = positions.data_ptr(), _ptr(cos, _F32, n_pos * pairs, "cos"), _ptr(sin, _F32, n_pos * pairs, "sin")
+    qw, kw = _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight")
+    if (qw and q_weight.get_device() != at) or (kw and k_weight.get_device() != at):
+        _same(dev, q_weight=q_weight, k_weight=k_weight)
+    st = _native.lib().prompt_rope(qp, qs, kp, ks, _CODES[dt], T, Hq, Hkv, D, where, step, n_axes, code, cos_p, sin_p, n_pos,
+                                   rot, bool(interleaved), qw, kw, eps, qo, qos, ko, kos, _CODES[out_dtype],
+                                   _current(at) if stream is None else stream.cuda_stream)
     if st:
-        if code is not None and not (1 <= n_axes <= _MAX_AXES and max(code, default=0) < n_axes):
+        if code is not None and not (1 <= n_axes <= _MAX_AXES and max(code) < n_axes):
             raise ValueError("axes must be in [0, %d), positions of 1 to %d axes" % (n_axes, _MAX_AXES))
         _native.check("prompt_rope", st)
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def prompt_attention_workspace_size(n_heads, n_kv_heads, D):
@@ -191,11 +193,14 @@ def _attend(q, k, v, ws, cu_q=None, max_q=None, cu_k=None, max_k=None, scale=Non
             raise ValueError("cu_k needs max_k, the most keys of a sequence")
     elif Tk != T:
         raise ValueError("%d keys for %d queries: pass cu_k" % (Tk, T))
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.device != dev:
-            raise ValueError("%s is on %s, not %s" % (name, t.device, dev))
-        if t.stride(2) != 1:
-            raise ValueError("%s must have contiguous channels" % name)
+    q0, q1, q2 = q.stride()
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if not q2 == k2 == v2 == 1:
+        raise ValueError("q, k and v must have contiguous channels")
+    at = q.get_device()
+    if k.get_device() != at or v.get_device() != at:
+        _same(dev, k=k, v=v)
     po = pl = None
     if prefix is not None:
         po, pl = _ptr(prefix[0], q.dtype, T * Hq * D, "prefix out"), _ptr(prefix[1], _F32, T * Hq, "prefix lse")
@@ -203,12 +208,13 @@ def _attend(q, k, v, ws, cu_q=None, max_q=None, cu_k=None, max_k=None, scale=Non
     if out is None:
         out = (_empty((T, Hq, D), dtype=q.dtype, device=dev) if stream is None else
                _empty_on(stream, (T, Hq, D), dtype=q.dtype, device=dev))
-    _same(dev, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    for t in (cu_q, cu_k, out, lse):
+        if t is not None and t.get_device() != at:
+            _same(dev, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
     st = _native.lib().prompt_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), _CODES[q.dtype], T, Tk, Hq, Hkv, D, _ptr(cu_q, _I32, B + 1, "cu_q"), _ptr(cu_k, _I32, B + 1, "cu_k"), B,
-        max_q, max_k or 0, D ** -0.5 if scale is None else scale, causal, window, po, pl,
-        _ptr(out, q.dtype, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1], _raw_stream(stream))
+        q.data_ptr(), q0, q1, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _CODES[q.dtype], T, Tk,
+        Hq, Hkv, D, _ptr(cu_q, _I32, B + 1, "cu_q"), _ptr(cu_k, _I32, B + 1, "cu_k"), B, max_q, max_k or 0, D ** -0.5 if scale is None else scale, causal, window, po, pl,
+        _ptr(out, q.dtype, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1], _current(at) if stream is None else stream.cuda_stream)
     if st:
         _native.check("prompt_attention", st)
     return out, lse
