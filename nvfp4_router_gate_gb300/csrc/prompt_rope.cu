@@ -6,7 +6,7 @@
 //
 // Bound by memory: every byte of the heads is read and written once, the tables' rows are
 // read once a token.  Measured (inputs not in L2): 8192 tokens of 72 heads of 128 channels
-// with norm, 302 MB, 52 us (5.8 TB/s); one such token 2.7 us, the launch and three loads
+// with norm, 306 MB, 51 us (6.0 TB/s); one such token 2.6 us, the launch and three loads
 // one after the other (position, angle, store).
 //
 // A warp takes a stretch of all tokens' head groups, equally many for each: with a token a
