@@ -622,7 +622,6 @@ __device__ __forceinline__ bool look_over() {
 template <int D, bool kF16>
 __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
   using Sm = PaSmem<D>;
-  constexpr int NS = Sm::kSlots;
   Member<D> me;
   const int wl = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
   const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
@@ -636,6 +635,17 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
     const volatile Run* run = me.take();
     if (!run) return false;
     if (run->tiles < 0) break;
+    if (p.prefix_out && run->parts == 1) {
+      // (read behind the run's last product)
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        const int dq = w * p.qt + iq;
+        if (iq >= p.qt || dq >= run->n_q) continue;
+        const int64_t at = (static_cast<int64_t>(run->q0 + dq) * p.Hq + run->head * p.Gt + g) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p.prefix_out + at + c));
+      }
+    }
     for (int w = 0; w < 2; ++w) {
       const int dq = w * p.qt + iq;                  // the row's query in the group
       const bool on = iq < p.qt && dq < run->n_q;
@@ -643,6 +653,8 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
       const bool any = run->first[w] < run->last[w];
       const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on);
       const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
+      const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
+      const float z_before = p.prefix_lse && on ? p.prefix_lse[out_row] : -INFINITY;
       float m = -INFINITY, l = 0.0f;
       if (any) {
         if (!me.wait_all(me.stat_full + w, ph[w])) return false;
@@ -652,7 +664,6 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         ph[w] ^= 1u;
         tc_fence_after();
       }
-      const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
       if (any && run->bad) {
         // the infinities and NaNs among the values of masked tiles that the row sees join its O
         const int pos = run->pos0 + dq, kmax = run->kmax;
@@ -759,7 +770,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
       float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
       if (p.prefix_lse && on) {
         float f_own;
-        z = join_prefix(z, p.prefix_lse[out_row], f_own, f_before);
+        z = join_prefix(z, z_before, f_own, f_before);
         f *= f_own;
       }
       // 128 bytes of every row: a lane stores vector lane % 8 of every fourth row
@@ -802,15 +813,20 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         continue;
       }
       if (parts == 1 && any) {
-        // (with a prefix: 64 channels of it on their way at a time)
+        // (with a prefix: 64 channels of its rows into the results' place, as those leave it.  In registers
+        // they cost the warps' other paths spills: ragged prompts 223 us, and 217 so; 8192 tokens 660 and 651;
+        // 66 tokens with a prefix 14.0 and 15.0.)
 #pragma unroll 1
         for (int c = 0; c < D; c += 64) {
-          uint4 prev[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            prev[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (f_before != 0.0f) prev[i] = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
+          const uint8_t* in = reinterpret_cast<const uint8_t*>(p.prefix_out) + c * 2 + (me.lane % 8) * 16;
+#pragma unroll 4
+          for (int r = me.lane / 8; r < 32; r += 4) {
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, out_row, r);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(smem_u32(rows_at + r * 128 + (((me.lane ^ r) & 7) << 4))), "l"(in + from * (D * 2))
+                         : "memory");
           }
+          asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
 #pragma unroll
           for (int x = 0; x < 64; x += 16) {
@@ -823,7 +839,9 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 u = prev[x / 8 + i];
+              uint4 u = *reinterpret_cast<const uint4*>(rows_at + me.lane * 128 + ((((x / 8 + i) ^ me.lane) & 7) << 4));
+              // (whatever lies in rows without a prefix)
+              if (f_before == 0.0f) u = make_uint4(0u, 0u, 0u, 0u);
               const uint32_t b[4] = {u.x, u.y, u.z, u.w};
               uint32_t h[4];
 #pragma unroll
