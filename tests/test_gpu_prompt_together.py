@@ -238,3 +238,24 @@ def test_the_rotation_refuses():
     with pytest.raises((ValueError, RuntimeError)):                       # keys' result without keys
         R.prompt_rope(q, None, **good, k_out=k)
     torch.cuda.synchronize()
+
+
+def test_long_keys_that_are_handed_out_whole():
+    """So many that each block gets several: none is cut, in a call and in the next one with its workspace."""
+    import nvfp4_router_gate_gb300 as R
+    C = Packed(33, [6000, 10], 8, 8, 64)
+    att = R.PromptAttention(64, 8, 64)
+    lse = torch.empty(6010, 64, device="cuda")
+    for _ in range(2):
+        out, _ = att(C.q, C.k, C.v, lse=lse, **C.kw)
+        C.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), rows=2)
+    assert att.status() == 0
+
+
+@pytest.mark.parametrize("nq", [[5, 300, 0, 1, 77], [0, 0, 0, 2], [40] * 30])
+def test_far_more_room_than_queries(nq):
+    """max_q of a captured graph's largest batch: the groups behind a sequence's end are passed over."""
+    C = Packed(34, nq, 2, 4, 128)
+    want = C.run()
+    got = C.run(max_q=20000)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
