@@ -23,16 +23,17 @@ from .kv_cache import _empty, _empty_on, _on, _ptr
 _BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
 _CODES = {_BF16: _native.NVR_BF16, _F32: _native.NVR_F32, _F16: _native.NVR_F16}
 _MAX_AXES = 8
-_current = torch._C._cuda_getCurrentRawStream
+_current, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _here(t, name):
-    """The tensor's device, which has to be the current one (launches go there)."""
+    """The tensor's device, which has to be the current one (launches go there), and its number."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.device.index != torch._C._cuda_getDevice():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch._C._cuda_getDevice()))
-    return t.device
+    at = t.get_device()
+    if at != _device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, _device()))
+    return t.device, at
 
 
 def _same(dev, **tensors):
@@ -41,12 +42,40 @@ def _same(dev, **tensors):
             raise ValueError("%s is on %s, not %s" % (name, t.device, dev))
 
 
-def _rows(t, T, H, D, name):
+def _steps(t, T, H, D, name):
     """Token stride of t [T, H, D] with contiguous heads."""
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError("%s must have contiguous heads (a token stride is allowed)" % name)
     return s0 if T > 1 else H * D
+
+
+def _side(x, T, D, dt, at, name):
+    """Pointer, token stride and heads of x [T, heads, D]."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or x.dtype is not dt or x.get_device() != at:
+        raise ValueError("%s must be [T, heads, D] of one type and device with the other" % name)
+    H = shape[1]
+    return x.data_ptr(), _steps(x, T, H, D, name), H
+
+
+def _result(out, shape, dtype, dev, at, stream, name):
+    """The tensor for a result, its pointer and token stride."""
+    T, H, D = shape
+    if out is None:
+        out = _empty(shape, dtype=dtype, device=dev) if stream is None else _empty_on(stream, shape, dtype=dtype, device=dev)
+        return out, out.data_ptr(), H * D
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != at:
+        raise ValueError("%s must be %s of %s on %s" % (name, shape, dtype, dev))
+    return out, out.data_ptr(), _steps(out, T, H, D, name)
+
+
+def _floats(t, n, at, name):
+    """Pointer of n contiguous fp32 on the device of that number."""
+    if t.dtype is not _F32 or t.get_device() != at or t.numel() != n or not t.is_contiguous():
+        _same(torch.device("cuda", at), **{name: t})
+        _ptr(t, _F32, n, name)
+    return t.data_ptr()
 
 
 def rope_axes(sections, turns=False):
@@ -83,40 +112,29 @@ def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=No
     bfloat16, float16 or float32; out_dtype (or q_out and k_out, which may be q and k
     themselves) the same, or a 16-bit one for float32 heads.  Returns (q_out, k_out)."""
     some = q if q is not None else k
-    dev, at = _here(some, "q" if q is not None else "k"), some.get_device()
-    if some.dim() != 3:
+    dev, at = _here(some, "q" if q is not None else "k")
+    shape, dt = some.shape, some.dtype
+    if len(shape) != 3:
         raise ValueError("heads must be [T, heads, D]")
-    T, _, D = some.shape
-    dt = some.dtype
+    T, _, D = shape
     if dt not in _CODES:
         raise TypeError("heads must be bfloat16, float16 or float32, got %s" % dt)
     if out_dtype is None:
-        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else dt
+        out_dtype = dt if q_out is None and k_out is None else (k_out if q_out is None else q_out).dtype
     if out_dtype is not dt and (dt is not _F32 or out_dtype not in _CODES):
         raise TypeError("heads of %s do not become %s" % (dt, out_dtype))
-
-    def side(x, out, name):
-        """Pointer, token stride and heads, the result, its pointer and token stride."""
-        if x is None:
-            if out is not None:
-                raise ValueError("%s_out without %s" % (name, name))
-            return None, 0, 0, None, None, 0
-        if x.dim() != 3 or x.dtype is not dt or x.get_device() != at:
-            raise ValueError("%s must be [T, heads, D] of one type and device with the other" % name)
-        n, H, d = x.shape
-        if n != T or d != D:
-            raise ValueError("%s must be [%d, heads, %d], as the other" % (name, T, D))
-        step = _rows(x, T, H, D, name)
-        if out is None:
-            out = (_empty((T, H, D), dtype=out_dtype, device=dev) if stream is None else
-                   _empty_on(stream, (T, H, D), dtype=out_dtype, device=dev))
-            return x.data_ptr(), step, H, out, out.data_ptr(), H * D
-        if out.shape != x.shape or out.dtype is not out_dtype or out.get_device() != at:
-            raise ValueError("%s_out must be %s of %s on %s" % (name, tuple(x.shape), out_dtype, dev))
-        return x.data_ptr(), step, H, out, out.data_ptr(), _rows(out, T, H, D, name + "_out")
-
-    qp, qs, Hq, q_out, qo, qos = side(q, q_out, "q")
-    kp, ks, Hkv, k_out, ko, kos = side(k, k_out, "k")
+    Hq = Hkv = qs = ks = qos = kos = 0
+    qp = kp = qo = ko = None
+    if q is not None:
+        qp, qs, Hq = _side(q, T, D, dt, at, "q")
+        q_out, qo, qos = _result(q_out, (T, Hq, D), out_dtype, dev, at, stream, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        kp, ks, Hkv = _side(k, T, D, dt, at, "k")
+        k_out, ko, kos = _result(k_out, (T, Hkv, D), out_dtype, dev, at, stream, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     rot = n_pos = n_axes = step = 0
     code = where = cos_p = sin_p = None
     if cos is not None:
@@ -125,20 +143,18 @@ def prompt_rope(q, k, positions, cos, sin, axes=None, q_weight=None, k_weight=No
         n_pos, pairs = cos.shape
         if positions.dim() == 1:
             positions = positions[None]
-        if positions.dim() != 2 or positions.dtype is not _I32 or positions.shape[1] != T or (T > 1 and positions.stride(1) != 1):
-            raise ValueError("positions must be int32 [n_axes, T], the tokens next to each other")
+        size, steps = positions.shape, positions.stride()
+        if len(size) != 2 or size[1] != T or (T > 1 and steps[1] != 1) or positions.dtype is not _I32 or positions.get_device() != at:
+            raise ValueError("positions must be int32 [n_axes, T] on %s, the tokens next to each other" % dev)
         axes = (0,) * pairs if axes is None else axes
         if len(axes) != pairs:
             raise ValueError("%d axes for %d pairs" % (len(axes), pairs))
-        if positions.get_device() != at or cos.get_device() != at or sin.get_device() != at:
-            _same(dev, positions=positions, cos=cos, sin=sin)
         if pairs:
-            rot, n_axes, step = 2 * pairs, positions.shape[0], positions.stride(0)
-            code = bytes(axes)                               # (the library looks at them)
-            where, cos_p, sin_p = positions.data_ptr(), _ptr(cos, _F32, n_pos * pairs, "cos"), _ptr(sin, _F32, n_pos * pairs, "sin")
-    qw, kw = _ptr(q_weight, _F32, D, "q_weight"), _ptr(k_weight, _F32, D, "k_weight")
-    if (qw and q_weight.get_device() != at) or (kw and k_weight.get_device() != at):
-        _same(dev, q_weight=q_weight, k_weight=k_weight)
+            rot, n_axes, step, code = 2 * pairs, size[0], steps[0], bytes(axes)       # (the library looks at the axes)
+            where = positions.data_ptr()
+            cos_p, sin_p = _floats(cos, n_pos * pairs, at, "cos"), _floats(sin, n_pos * pairs, at, "sin")
+    qw = None if q_weight is None else _floats(q_weight, D, at, "q_weight")
+    kw = None if k_weight is None else _floats(k_weight, D, at, "k_weight")
     st = _native.lib().prompt_rope(qp, qs, kp, ks, _CODES[dt], T, Hq, Hkv, D, where, step, n_axes, code, cos_p, sin_p, n_pos,
                                    rot, bool(interleaved), qw, kw, eps, qo, qos, ko, kos, _CODES[out_dtype],
                                    _current(at) if stream is None else stream.cuda_stream)
@@ -229,7 +245,7 @@ def prompt_attention(q, k, v, workspace=None, stream=None, **kw):
     sequence's last positions), window to 0 (none).  prefix=(out, lse) of the same queries
     over other keys is joined with the result.  Returns (out [T, Hq, D], lse); lse [T, Hq]
     fp32 is written when it is given."""
-    dev = _here(q, "q")
+    dev, _ = _here(q, "q")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, heads, D], k and v [Tk, n_kv_heads, D]")
     if workspace is None:
@@ -257,7 +273,7 @@ class PromptAttention:
         self.workspace = new_workspace(n, torch.device(device or "cuda"))
 
     def __call__(self, q, k, v, workspace=None, **kw):
-        dev = _here(q, "q")
+        dev, _ = _here(q, "q")
         if q.dim() != 3 or k.dim() != 3 or q.shape[1:] != (self.n_heads, self.head_dim) or k.shape[1] != self.n_kv_heads:
             raise ValueError("q must be [T, %d, %d] and k [Tk, %d, %d]" % (
                 self.n_heads, self.head_dim, self.n_kv_heads, self.head_dim))
