@@ -22,7 +22,7 @@ struct PromptParams {
   int B, max_q, max_k;
   float scale_log2;                        // scale * log2(e)
   int causal, window;
-  int groups;                              // groups of 2 qt queries of a sequence
+  int span, groups;                        // queries of a group (one or two row tiles), groups of a sequence
   const uint16_t* v;
   int64_t v_stride, v_head;
   const uint16_t* prefix_out;
@@ -31,8 +31,8 @@ struct PromptParams {
   float* lse;
   uint32_t* status;
   int min_chunk;                           // places of a block at least
-  // [blocks][8 warps of rows]: parts of the key whose first one is the block's that are begun, and
-  // written; zero between calls
+  // [blocks][8 warps of rows]: written parts of the key whose first one is the block's; zero
+  // between calls
   uint32_t* arrived;
   uint32_t* handed;                        // keys handed out behind the blocks' first ones; zero between calls
   // [2 * blocks][256 m, 256 l, D / 4 x 256 x 4 O]: a block's first stretch is in its slot 0 when it
@@ -62,7 +62,7 @@ __device__ __forceinline__ PromptGroup prompt_group(const PromptParams& p, int i
   // (a sequence's last queries, which see most, come first)
   const int turn = item / p.B;
   g.b = item - turn * p.B;
-  g.i0 = (p.groups - 1 - turn) * 2 * p.qt;
+  g.i0 = (p.groups - 1 - turn) * p.span;
   int n_q, n_k;
   if (p.cu_q) {
     const int64_t a = min(max(static_cast<int64_t>(__ldg(p.cu_q + g.b)), int64_t(0)), p.T);
@@ -82,7 +82,7 @@ __device__ __forceinline__ PromptGroup prompt_group(const PromptParams& p, int i
   }
   g.shift = n_k - n_q;
   g.kmax = min(n_k, p.max_k);
-  g.n = max(min(min(n_q, p.max_q) - g.i0, 2 * p.qt), 0);
+  g.n = max(min(min(n_q, p.max_q) - g.i0, p.span), 0);
   int begin = INT32_MAX, end = 0;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
