@@ -767,8 +767,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         }
         // Their weighted sum in their order, every step rounded by itself: the same whichever
         // comes last.  A trip to the parts takes 1500 clocks, so four of them are on their way at a
-        // time, an eighth of the channels each (128 queries over 8320 keys, 8 parts: one by one
-        // 102 us, so 77; a query over 20000 keys 112 and 70).
+        // time, an eighth of the channels each (a query over 20000 keys: one by one 112 us, and 70 so).
         constexpr int kStep = D / 8;
 #pragma unroll 1
         for (int c = 0; c < D; c += kStep) {
@@ -1273,12 +1272,14 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
     const int64_t w = (static_cast<int64_t>(p.window) + 2 * p.qt + kPaTile - 2) / kPaTile + 1;
     if (w < tiles) tiles = w;
   }
-  // Two row tiles a key; one where that leaves half of the blocks without a key and none is cut: the
-  // rows of a block's two tiles go out one after the other (one prompt of 37 tokens, 32 heads,
-  // 11.6 us, and 9.2 so; of 300 15.2 and 11.9; 700 of 16 heads with a prefix 24 and 17).
+  // Two row tiles a key; one where no more than three blocks of four would have one (the rows of a
+  // block's two tiles go out, and are joined, one after the other): a prompt of 37 tokens, 32 heads,
+  // 11.6 us, and 9.2 so; 700 of 16 heads with a prefix 24 and 17; 128 tokens over 8320 keys 77 and 49; 600
+  // tokens (80 keys of 152 blocks) 18.5 and 15.2, over 4000 more 70 and 66.  With a key for each
+  // block, 1100 tokens over 4000 more, 87 and 110.
   p.span = 2 * p.qt;
   p.groups = (p.max_q + p.span - 1) / p.span;
-  if (tiles <= kPaWhole && static_cast<int64_t>(p.B) * p.groups * p.Hv * 2 <= sms) {
+  if (static_cast<int64_t>(p.B) * p.groups * p.Hv * 4 <= sms * int64_t(3)) {
     p.span = p.qt;
     p.groups = (p.max_q + p.span - 1) / p.span;
   }
