@@ -259,3 +259,47 @@ def test_far_more_room_than_queries(nq):
     want = C.run()
     got = C.run(max_q=20000)
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+def test_two_graphs_with_one_workspace():
+    """Replayed in turn: keys handed out whole in one, cut and joined in the other; counters are back at zero."""
+    import nvfp4_router_gate_gb300 as R
+    calls = [(Packed(35, [500, 3, 90], 2, 4, 128), {}), (Packed(36, [2, 1], 2, 4, 128, nk=[9000, 40]), {})]
+    att = R.PromptAttention(8, 2, 128)
+    graphs, outs = [], []
+    for C, kw in calls:
+        out = torch.empty(C.q.shape, dtype=C.q.dtype, device="cuda")
+        att(C.q, C.k, C.v, out=out, **C.kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            att(C.q, C.k, C.v, out=out, **C.kw)
+        graphs.append(graph)
+        outs.append(out)
+    want = [o.clone() for o in outs]
+    for _ in range(20):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            assert torch.equal(o, w)
+    for (C, _), o in zip(calls, outs):
+        C.check(o.double().cpu().numpy(), C.run()[1], rows=20)
+    assert att.status() == 0
+
+
+def test_sequences_of_one_length_over_keys_of_others():
+    C = Packed(37, [7, 7, 7], 2, 4, 64, nk=[300, 7, 40])
+    want = C.run()
+    got = C.run(cu_q=None, max_q=None)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    C.check(*want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nk,H,G,D_", [([40], [6000], 1, 4, 128), ([1, 2, 1], [3000, 5, 1300], 2, 8, 64), ([130], [4500], 1, 3, 128),
+                                          ([1], [40000], 1, 1, 64)])
+def test_few_queries_over_many_keys(nq, nk, H, G, D_, dt):
+    """Keys cut into many parts, causal and not, with a window that hides some of the parts."""
+    C = Packed(38, nq, H, G, D_, dt, nk=nk)
+    C.check(*C.run(), rows=20)
+    C.check(*C.run(causal=False), causal=False, rows=20)
+    C.check(*C.run(window=1500), window=1500, rows=20)
