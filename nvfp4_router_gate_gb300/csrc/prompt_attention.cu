@@ -48,26 +48,28 @@ namespace {
 
 constexpr int kPaThreads = 512;
 constexpr int kPaPlaces = 2;               // places of a tile in the flat order
-// Starting and ending a key counts as this many places: 8192 tokens of 64 heads 782 us at 3,
-// 764 at 5, 766 at 6; 64 rows of 48 sequences 43, 43, 43.
+// Starting and ending a key counts as this many places: 8192 tokens of 8 heads 116 us at 2, 117 at
+// 5, 118 at 9; 2048 over 8192 keys 310, 310, 309.
 constexpr int kPaKeyCost = 5;
 // Fewest places of a block; of a key of n tiles it has sqrt(n) tiles at least: the parts are
 // joined one after the other.
 constexpr int kPaMinChunk = 4;
-// Keys of at most this many tiles are not cut (a block more or less even then): ragged prompts
-// 256 us at 4, 251 at 16, 245 at 24; 2571 tokens of 16 heads 42, 50, 35; two chunks of 1132
-// tokens, 128 heads, 122, 107, 108; pictures 96, 98, 99.
+// Keys of at most this many tiles are not cut (a block more or less even then): 2571 tokens of 16
+// heads 56 us at 12, 35 at 24 and 40; 3000 tokens that see all 164, 155, 155; 8192 tokens of 8 heads
+// 116, 117, 124.
 constexpr int kPaWhole = 24;
 // Fewer where the longest key is more than two of the blocks' chunks, so that most blocks would wait
 // for it: 30 queries of four sequences over 2000 keys 29.6 us whole, 24.5 cut; one query over 2900
 // 36.9 and 29.4; a prompt of 3000 tokens, 4 heads, 38.1 and 32.5.  Four queries over 1000 keys (8
 // tiles) 17.8 whole, 24.8 cut.
 constexpr int kPaWholeFew = 9;
-// Keys are shared out whole, as blocks have room for them, where none is longer than that or a
-// block gets at least this many of the longest.  In place of equal chunks of the flat order: 8192
-// tokens of 64 heads (7 a block) 691 to 660 us; ragged prompts 242 to 223, short ones 25.9 to 21.8,
-// two chunks of 1132 tokens 106 to 96; one token to one key a block 0.3 us slower.  2048 queries
-// over 8192 keys (3 a block) are 318 us in chunks, 325 whole.
+// Keys are shared out whole, as blocks have room for them, where none is longer than that; where a
+// block gets this many of the longest; and where it gets one of them at least and they are
+// three quarters of it on average, as causal prompts' are (the short ones, last, even the blocks
+// out).  In place of equal chunks of the flat order: 8192 tokens of 64 heads (7 a block) 691 to 660 us;
+// three ragged prompts of 3500 109 to 84, 4096 tokens of 32 heads 123 to 103; short prompts 25.9
+// to 21.8; one token to one key a block 0.3 us slower.  2048 queries over 8192 keys (3 a block,
+// 56 tiles of 64 on average) are 318 us in chunks, 325 whole.
 constexpr int kPaEven = 4;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
@@ -1176,7 +1178,9 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   share.keys = total_some * p.Hv;
   const int chunk = share.chunk = max((total + blocks - 1) / blocks, p.min_chunk);
   share.uncut = kPaPlaces * longest > 2 * chunk ? kPaWholeFew : kPaWhole;
-  share.whole = longest <= share.uncut || total / blocks >= kPaEven * kPaPlaces * longest;
+  const int top = kPaPlaces * longest + kPaKeyCost;          // the longest key's places
+  share.whole = longest <= share.uncut || chunk >= kPaEven * kPaPlaces * longest ||
+                (chunk >= top && 4 * static_cast<int64_t>(total) <= 3 * static_cast<int64_t>(share.keys) * top);
   const int f0 = share.f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
   const int f1 = share.f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
   const int excl = before + incl - mine;
