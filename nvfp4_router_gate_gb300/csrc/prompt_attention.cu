@@ -663,6 +663,25 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
       const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
       const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
       const float z_before = p.prefix_lse && on ? p.prefix_lse[out_row] : -INFINITY;
+      // 32 channels of the rows' prefix to where the results leave from, 16 bytes a lane of every eighth row
+      auto piece = [&](int u, int r, int v) { return rows_at + (u & 1) * 2048 + r * 64 + (((v ^ (r >> 1)) & 3) << 4); };
+      auto fetch = [&](int u) {
+        if (u < D / 32) {
+          const uint8_t* in = reinterpret_cast<const uint8_t*>(p.prefix_out) + u * 64 + (me.lane % 4) * 16;
+#pragma unroll
+          for (int r = me.lane / 4; r < 32; r += 8) {
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, out_row, r);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(smem_u32(piece(u, r, me.lane % 4))), "l"(in + from * (D * 2))
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      if (p.prefix_lse && any && run->parts == 1) {
+        fetch(0);
+        fetch(1);
+      }
       float m = -INFINITY, l = 0.0f;
       if (any) {
         if (!me.wait_all(me.stat_full + w, ph[w])) return false;
@@ -865,47 +884,46 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         continue;
       }
       if (any) {
-        // (with a prefix: 64 channels of its rows into the results' place, as those leave it.  In registers
-        // they cost the warps' other paths spills: ragged prompts 223 us, and 217 so; 8192 tokens 660 and 651;
-        // 66 tokens with a prefix 14.0 and 15.0.)
+        // (with a prefix: two pieces of 32 channels of its rows on their way, the first ones since before
+        // the products were awaited; five ragged turns of 700 tokens 44 us with 64 channels at a time, 41 so.
+        // In registers they cost the warps' other paths spills: ragged prompts 223 us, and 217.)
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          const uint8_t* in = reinterpret_cast<const uint8_t*>(p.prefix_out) + c * 2 + (me.lane % 8) * 16;
-#pragma unroll 4
-          for (int r = me.lane / 8; r < 32; r += 4) {
-            const int64_t from = __shfl_sync(0xFFFFFFFFu, out_row, r);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                         :: "r"(smem_u32(rows_at + r * 128 + (((me.lane ^ r) & 7) << 4))), "l"(in + from * (D * 2))
-                         : "memory");
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int u = 0; u < D / 32; ++u) {
+          uint32_t y[32];
+          tmem_load32_start(t_o + 32 * u, y);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
           __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 64; x += 16) {
-            uint32_t y[16];
-            tmem_load16_start(t_o + c + x, y);
-            tmem_load16_finish(y);
-            if (c + x + 16 == D) {
-              tc_fence_before();
-              me.arrive(me.o_empty + w);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint4 u = *reinterpret_cast<const uint4*>(rows_at + me.lane * 128 + ((((x / 8 + i) ^ me.lane) & 7) << 4));
-              // (whatever lies in rows without a prefix)
-              if (f_before == 0.0f) u = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t b[4] = {u.x, u.y, u.z, u.w};
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 v = unpack_16<kF16>(b[k]);
-                const float y0 = __uint_as_float(y[8 * i + 2 * k]) * f, y1 = __uint_as_float(y[8 * i + 2 * k + 1]) * f;
-                h[k] = pack_16<kF16>(fmaf(v.x, f_before, y0), fmaf(v.y, f_before, y1));
-              }
-              put_vector(x / 8 + i, make_uint4(h[0], h[1], h[2], h[3]));
-            }
+          tmem_load32_finish(y);
+          if (u == D / 32 - 1) {
+            tc_fence_before();
+            me.arrive(me.o_empty + w);
           }
-          store_rows(c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(piece(u, me.lane, i));
+            uint4 v = *at;
+            // (whatever lies in rows without a prefix)
+            if (f_before == 0.0f) v = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack_16<kF16>(b[k]);
+              const float y0 = __uint_as_float(y[8 * i + 2 * k]) * f, y1 = __uint_as_float(y[8 * i + 2 * k + 1]) * f;
+              h[k] = pack_16<kF16>(fmaf(x.x, f_before, y0), fmaf(x.y, f_before, y1));
+            }
+            *at = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          __syncwarp();
+          uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + u * 64 + (me.lane % 4) * 16;
+#pragma unroll
+          for (int r = me.lane / 4; r < 32; r += 8) {
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, out_row, r);
+            if ((rows_on >> r) & 1u)
+              *reinterpret_cast<uint4*>(out + to * (D * 2)) = *reinterpret_cast<const uint4*>(piece(u, r, me.lane % 4));
+          }
+          __syncwarp();
+          fetch(u + 2);
         }
         if (on && p.lse) p.lse[out_row] = z;
         continue;
