@@ -627,7 +627,7 @@ __device__ __forceinline__ bool look_over() {
 }
 
 // The rows out.
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPrefix>
 __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
   using Sm = PaSmem<D>;
   Member<D> me;
@@ -643,7 +643,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
     const volatile Run* run = me.take();
     if (!run) return false;
     if (run->tiles < 0) break;
-    if (p.prefix_out && run->parts == 1) {
+    if (kPrefix && run->parts == 1) {
       // (read behind the run's last product)
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
@@ -662,7 +662,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
       const uint32_t rows_on = __ballot_sync(0xFFFFFFFFu, on);
       const uint32_t t_o = tmem + lanes + 2 * kPaTile + w * D;
       const int64_t out_row = static_cast<int64_t>(run->q0 + (on ? dq : 0)) * p.Hq + run->head * p.Gt + (on ? g : 0);
-      const float z_before = p.prefix_lse && on ? p.prefix_lse[out_row] : -INFINITY;
+      const float z_before = kPrefix && on ? p.prefix_lse[out_row] : -INFINITY;
       // 32 channels of the rows' prefix to where the results leave from, 16 bytes a lane of every eighth row
       auto piece = [&](int u, int r, int v) { return rows_at + (u & 1) * 2048 + r * 64 + (((v ^ (r >> 1)) & 3) << 4); };
       auto fetch = [&](int u) {
@@ -678,7 +678,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      if (p.prefix_lse && any && run->parts == 1) {
+      if (kPrefix && any && run->parts == 1) {
         fetch(0);
         fetch(1);
       }
@@ -781,7 +781,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
           l = __fadd_rn(l, li == 0.0f ? 0.0f : __fmul_rn(li, ex2(mi - base)));
         }
         float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
-        if (p.prefix_lse && on) {
+        if (kPrefix && on) {
           float f_own;
           z = join_prefix(z, z_before, f_own, f_before);
           f *= f_own;
@@ -824,7 +824,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
 #pragma unroll
           for (int i = 0; i < kStep / 8; ++i) {
             uint4 before = make_uint4(0u, 0u, 0u, 0u);
-            if (f_before != 0.0f) before = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
+            if (kPrefix && f_before != 0.0f) before = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
             const uint32_t b4[4] = {before.x, before.y, before.z, before.w};
             uint32_t h[4];
 #pragma unroll
@@ -839,7 +839,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         continue;
       }
       float z = lse_of(m, l), f = out_factor(1.0f, l), f_before = 0.0f;
-      if (p.prefix_lse && on) {
+      if (kPrefix && on) {
         float f_own;
         z = join_prefix(z, z_before, f_own, f_before);
         f *= f_own;
@@ -856,7 +856,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         }
         __syncwarp();
       };
-      if (!p.prefix_lse && any) {
+      if (!kPrefix && any) {
         // (usually.  The next run's products wait for the accumulator: 64 channels at once, it is
         // read after 1500 clocks; 16 channels at a time on their way out it took 4800.)
 #pragma unroll 1
@@ -883,7 +883,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         if (on && p.lse) p.lse[out_row] = z;
         continue;
       }
-      if (any) {
+      if (kPrefix && any) {
         // (with a prefix: two pieces of 32 channels of its rows on their way, the first ones since before
         // the products were awaited; five ragged turns of 700 tokens 44 us with 64 channels at a time, 41 so.
         // In registers they cost the warps' other paths spills: ragged prompts 223 us, and 217.)
@@ -934,7 +934,7 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (f_before != 0.0f) u = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
+          if (kPrefix && f_before != 0.0f) u = reinterpret_cast<const uint4*>(p.prefix_out + out_row * D + c)[i];
           uint32_t* h = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -1125,7 +1125,9 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
   return true;
 }
 
-template <int D, bool kF16>
+// (With a prefix the rows' way out is compiled apart: its registers and instructions cost the calls
+// without one 1 to 2 %, 8192 tokens 660 and 647 us, ragged prompts 219 and 214.)
+template <int D, bool kF16, bool kPrefix>
 __global__ void __launch_bounds__(kPaThreads, 1)
 prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   constexpr int NS = PaSmem<D>::kSlots;
@@ -1214,20 +1216,13 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   }
   __syncthreads();
   const uint32_t tmem = *sh.tmem_holder;
-  // Four warpgroups of 128 registers a thread at launch: 2 x 120 + 2 x 136.  The rows out spill
-  // otherwise, for the loads of their joins (128 channels: ragged prompts 221 us, 218 so).
-  if constexpr (D == 128) {
-    if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-  }
-
   if (p.cu_q && warp >= 8 && warp < 12) clear_rows<D>(p, blockIdx.x * 4 + warp - 8, gridDim.x * 4);
   if (share.whole ? static_cast<int>(blockIdx.x) < share.keys : f0 < f1) {
     bool ok = true;
     if (warp < 8) {
       ok = softmax<D, kF16>(tmem, p.Gt, p.qt, p.causal, p.window, p.scale_log2);
     } else if (warp < 12) {
-      ok = rows_out<D, kF16>(p, tmem);
+      ok = rows_out<D, kF16, kPrefix>(p, tmem);
     } else if (warp < 14) {
       ok = products<D, kF16>(tmem, warp - 12);
       // nothing of this block's is under way when the tensor memory goes back
@@ -1273,7 +1268,7 @@ bool encode_heads(CUtensorMap* map, const void* base, bool f16, int64_t rows, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPrefix>
 nvr_status launch(PromptParams& p, cudaStream_t s) {
   using Sm = PaSmem<D>;
   static_assert(Sm::kTotal <= 227 * 1024, "shared memory");
@@ -1284,7 +1279,7 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
   if (sms <= 0) return NVR_ERR_CUDA;
   if (!attr_set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(prompt_attention_kernel<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kTotal);
+        cudaFuncSetAttribute(prompt_attention_kernel<D, kF16, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kTotal);
     if (e != cudaSuccess) return cuda_status(e);
     attr_set[dev] = true;
   }
@@ -1325,7 +1320,7 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, kF16>, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, kF16, kPrefix>, p));
 }
 
 }  // namespace
@@ -1405,6 +1400,10 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
       !encode_heads(&p.tm_v, keys ? v : q, f16, keys ? Tk : 1, keys ? Hkv : 1, D, v_stride, v_head_stride, 1, kPaTile))
     return NVR_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128) return f16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
-  return f16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  auto go = [&](auto prefix) {
+    constexpr bool kPrefix = decltype(prefix)::value;
+    if (D == 128) return f16 ? launch<128, true, kPrefix>(p, s) : launch<128, false, kPrefix>(p, s);
+    return f16 ? launch<64, true, kPrefix>(p, s) : launch<64, false, kPrefix>(p, s);
+  };
+  return prefix_lse ? go(std::true_type{}) : go(std::false_type{});
 }
