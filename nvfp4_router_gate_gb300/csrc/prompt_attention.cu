@@ -232,7 +232,8 @@ struct Block {
   uint8_t* smem;
   Run* s_runs;
   float* s_stat;                           // [row tile][m, l][row]
-  uint64_t *run_full, *run_empty, *kv_full, *kv_empty, *v_clean, *q_full, *q_empty, *s_full, *p_full, *o_full, *o_empty, *stat_full, *drained;
+  uint64_t *run_full, *run_empty, *kv_full, *kv_empty, *v_clean, *q_full, *q_empty;
+  uint64_t *s_full, *p_full, *o_full, *o_empty, *stat_full, *drained;
   uint32_t* tmem_holder;
   volatile int* abort_flag;
   int* s_start;                            // item of the chunk's start, offset inside it

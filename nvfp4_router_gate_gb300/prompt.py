@@ -229,8 +229,9 @@ def _attend(q, k, v, ws, cu_q=None, max_q=None, cu_k=None, max_k=None, scale=Non
             _same(dev, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
     st = _native.lib().prompt_attention(
         q.data_ptr(), q0, q1, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _CODES[q.dtype], T, Tk,
-        Hq, Hkv, D, _ptr(cu_q, _I32, B + 1, "cu_q"), _ptr(cu_k, _I32, B + 1, "cu_k"), B, max_q, max_k or 0, D ** -0.5 if scale is None else scale, causal, window, po, pl,
-        _ptr(out, q.dtype, T * Hq * D, "out"), _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1], _current(at) if stream is None else stream.cuda_stream)
+        Hq, Hkv, D, _ptr(cu_q, _I32, B + 1, "cu_q"), _ptr(cu_k, _I32, B + 1, "cu_k"), B, max_q, max_k or 0,
+        D ** -0.5 if scale is None else scale, causal, window, po, pl, _ptr(out, q.dtype, T * Hq * D, "out"),
+        _ptr(lse, _F32, T * Hq, "lse"), ws[0], ws[1], _current(at) if stream is None else stream.cuda_stream)
     if st:
         _native.check("prompt_attention", st)
     return out, lse
