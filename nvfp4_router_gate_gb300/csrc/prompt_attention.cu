@@ -1,9 +1,9 @@
 // prompt_attention.cu -- softmax attention of packed prompts of different lengths
 // over their own 16-bit keys and values (sm_103a): prompt_attention.
 // Bound by the tensor cores: 4 D flops for every (query, head) and seen token.  Measured (no
-// inputs in L2): 8192 tokens of 64 heads of 128 channels 655 us, 1680 TFLOP/s, the tensor pipe 71 %
-// busy; 2048 over 8192 keys 309 us, 1555; windows of 1024 over two prompts of 8192 466 us, 1105; ragged
-// prompts of up to 2500 tokens (32 heads) 217 us, 1226; one prompt of 37 tokens 9.4 us.
+// inputs in L2): 8192 tokens of 64 heads of 128 channels 656 us, 1676 TFLOP/s, the tensor pipe 72 %
+// busy; 2048 over 8192 keys 309 us, 1557; windows of 1024 over two prompts of 8192 451 us, 1142; ragged
+// prompts of up to 2500 tokens (32 heads) 216 us, 1230; one prompt of 37 tokens 9.1 us.
 //
 // Mathematics: as csrc/kv_prefill.cu -- S = Q K^T and O += P V on tcgen05 with 128
 // rows (query, head) of an accumulator in tensor memory, a thread a row; the running
