@@ -789,8 +789,9 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         }
         // Their weighted sum in their order, every step rounded by itself: the same whichever
         // comes last.  A trip to the parts takes 1500 clocks, so four of them are on their way at a
-        // time, an eighth of the channels each (a query over 20000 keys: one by one 112 us, and 70 so).
-        constexpr int kStep = D / 8;
+        // time, 16 channels each (a query over 20000 keys of 128 channels: one by one 112 us, and 70
+        // so; of 64 channels 56 with 8 of them at a time, 43 with 16).
+        constexpr int kStep = 16;
 #pragma unroll 1
         for (int c = 0; c < D; c += kStep) {
           float y[kStep];
