@@ -87,9 +87,10 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    prompt_attention_workspace_size(...) bytes, zeroed once
  * A query that sees no key and has no prefix gets zeros and lse = -inf, one with a NaN
- * among its channels NaNs in both.  What lies in keys and values that a query does not see
- * (other sequences', later ones, those in front of the window: infinities and NaNs among
- * them) does not reach its result.
+ * among its channels, or among those of a key that it sees, NaNs in both (with a scale of
+ * zero too, and there with an infinity as well).  What lies in keys and values that a query
+ * does not see (other sequences', later ones, those in front of the window: infinities and
+ * NaNs among them) does not reach its result.
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights p_t enter the
  * second product rounded to dt, relative to a running maximum (fp16: a weight below 2^-32
  * of the largest is lost there; bf16: results above 2^100 may overflow); results do not

@@ -973,7 +973,8 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
   uint32_t ph_s = 0, ph_stat = 1;
   int n_tiles = 0;                                     // of the runs so far
   // What hides a score: -inf once it is scaled.  (A scale of zero hides nothing by itself: its
-  // scores are written as zeros and scaled by one.)
+  // scores are multiplied by zero where the masks are written, NaNs and infinities become NaNs, and
+  // then scaled by one.)
   const bool flat = scale == 0.0f;
   const float to_log2 = flat ? 1.0f : scale, hidden = scale < 0.0f ? INFINITY : -INFINITY;
   // ---- a run's tiles
@@ -1013,7 +1014,8 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
             const uint32_t see = tokens32(c, from, to);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              y[x / 16][x % 16] = see & (1u << x) ? (flat ? 0u : y[x / 16][x % 16]) : __float_as_uint(hidden);
+              y[x / 16][x % 16] = !(see & (1u << x)) ? __float_as_uint(hidden) :
+                                  flat ? __float_as_uint(__uint_as_float(y[x / 16][x % 16]) * 0.0f) : y[x / 16][x % 16];
             tmem_store16(t_s + c, y[0]);
             tmem_store16(t_s + c + 16, y[1]);
           }
