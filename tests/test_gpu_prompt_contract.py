@@ -1,0 +1,42 @@
+"""What a prompt's operators promise for calls at the edge of their range, on the GPU."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+from oracle import prompt as P  # noqa: E402
+from test_gpu_prompt_attention import Packed  # noqa: E402
+
+
+def _references(C, **kw):
+    """out and lse of the formula, all sequences."""
+    refs, q0, k0 = [], 0, 0
+    for m, n in zip(C.nq, C.nk):
+        q, k, v = (t.double().cpu().numpy() for t in (C.q[q0:q0 + m], C.k[k0:k0 + n], C.v[k0:k0 + n]))
+        refs.append(P.attention(q, k, v, kw.get("scale", C.D ** -0.5), kw.get("causal", True), kw.get("window", 0))[:2])
+        q0, k0 = q0 + m, k0 + n
+    return [np.concatenate(x) for x in zip(*refs)]
+
+
+@pytest.mark.parametrize("D,dt", [(128, "bf16"), (64, "bf16"), (128, "f16"), (64, "f16")])
+@pytest.mark.parametrize("nq,G,kw", [([150, 290], 4, {}), ([150, 290], 4, dict(causal=False)), ([150, 290], 2, dict(window=70)),
+                                     ([3300, 40], 1, {})],
+                         ids=["causal", "all", "window", "cut"])
+def test_a_scale_of_zero_keeps_what_is_not_finite(nq, G, kw, D, dt):
+    """0 * NaN and 0 * inf are NaN: in the rows that see them, both results; in no other row."""
+    C = Packed(40, nq, 1, G, D, dt)
+    kw = dict(kw, scale=0.0)
+    want = C.run(**kw)
+    C.check(*want, rows=30, **kw)
+    C.q[60, G - 1, 17] = float("nan")
+    C.k[100, 0, 3] = float("nan")
+    C.k[nq[0] + 20, 0, 5], C.k[nq[0] + 30, 0, D - 1] = float("inf"), -float("inf")
+    out, lse = C.run(**kw)
+    odd = np.isnan(_references(C, **kw)[1])
+    # (without a mask every row of both sequences sees a key that is not finite)
+    assert odd[60, G - 1] and odd[100].all() and odd[nq[0] + 20].all() and odd.all() == (not kw.get("causal", True))
+    assert np.isnan(lse[odd]).all() and np.isnan(out[odd]).all()
+    assert np.array_equal(lse[~odd], want[1][~odd]) and np.array_equal(out[~odd], want[0][~odd])
