@@ -37,6 +37,7 @@
 //   m = max m_i,  w_i = 2^(m_i - m),  out = sum w_i O_i / sum w_i l_i.
 // Usually that is the key's first part, the last work of its block (a second kernel took
 // 24 to 29 us behind all of them).
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/nvfp4_prompt.h"
@@ -71,6 +72,8 @@ constexpr int kPaWholeFew = 9;
 // to 21.8; one token to one key a block 0.3 us slower.  2048 queries over 8192 keys (3 a block,
 // 56 tiles of 64 on average) are 318 us in chunks, 325 whole.
 constexpr int kPaEven = 4;
+// A call has fewer places than this: the chunks' borders in the flat order stay below 2^31.
+constexpr int kPaMost = INT32_MAX - (1 << 24) + 1;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
@@ -1158,10 +1161,13 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   // ---- this block's chunk of the flat order
   const int n_items = p.B * p.groups;
   const int per = (n_items + kPaThreads - 1) / kPaThreads;
+  // Sums of places stop at 2^31 - 1.  (Offsets that decrease can make more of the same rows than the
+  // host allowed for: then nothing is done.  In 64 bits one short prompt took 0.2 us more.)
+  auto plus = [](int a, int b) { return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), 0x7FFFFFFFu)); };
   int mine = 0, some = 0, longest = 0;       // of this thread's items: places, those with queries, tiles
   for (int i = tid * per; i < min((tid + 1) * per, n_items); ++i) {
     const PromptGroup g = prompt_group(p, i);
-    mine += key_cost(g) * p.Hv;
+    mine = plus(mine, key_cost(g) * p.Hv);
     some += g.n > 0;
     longest = max(longest, g.tiles);
   }
@@ -1170,7 +1176,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   for (int d = 1; d < 32; d <<= 1) {
     const int a = __shfl_up_sync(0xFFFFFFFFu, incl, d), b = __shfl_up_sync(0xFFFFFFFFu, incl_some, d);
     if (lane >= d) {
-      incl += a;
+      incl = plus(incl, a);
       incl_some += b;
     }
   }
@@ -1189,13 +1195,14 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
   for (int w = 0; w < kPaThreads / 32; ++w) {
     const int x = sums[w], y = sums[16 + w];
     if (w < warp) {
-      before += x;
+      before = plus(before, x);
       before_some += y;
     }
-    total += x;
+    total = plus(total, x);
     total_some += y;
     longest = max(longest, sums[32 + w]);
   }
+  if (total >= kPaMost) total = total_some = 0;
   sh.s_first[tid] = before_some + incl_some - some;
   const int blocks = static_cast<int>(gridDim.x);
   Share share;
@@ -1207,7 +1214,7 @@ prompt_attention_kernel(const __grid_constant__ PromptParams p) {
                 (chunk >= top && 4 * static_cast<int64_t>(total) <= 3 * static_cast<int64_t>(share.keys) * top);
   const int f0 = share.f0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * chunk, static_cast<int64_t>(total)));
   const int f1 = share.f1 = static_cast<int>(min(static_cast<int64_t>(f0) + chunk, static_cast<int64_t>(total)));
-  const int excl = before + incl - mine;
+  const int excl = plus(before, incl - mine);
   if (!share.whole && f0 < f1 && excl <= f0 && f0 < excl + mine) {
     int at = excl, i = tid * per;
     for (;; ++i) {
@@ -1272,6 +1279,21 @@ bool encode_heads(CUtensorMap* map, const void* base, bool f16, int64_t rows, in
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The tiles of a key at most: of all keys, or of a window over the group's queries.
+int64_t most_tiles(const PromptParams& p) {
+  const int64_t tiles = (static_cast<int64_t>(p.max_k) + kPaTile - 1) / kPaTile;
+  if (p.window <= 0) return tiles;
+  return std::min(tiles, (static_cast<int64_t>(p.window) + 2 * p.qt + kPaTile - 2) / kPaTile + 1);
+}
+// Items, and keys that have queries, of a call at most where a key has up to `span` of them: T
+// queries in B sequences are T / span + B groups, however many max_q leaves room for.
+int64_t most_items(const PromptParams& p, int span) { return p.B * ((static_cast<int64_t>(p.max_q) + span - 1) / span); }
+int64_t most_keys(const PromptParams& p, int span) { return std::min(most_items(p, span), p.T / span + p.B) * p.Hv; }
+// Whether the device can count its places.
+bool countable(const PromptParams& p, int span) {
+  return most_items(p, span) < (int64_t(1) << 30) && most_keys(p, span) <= (kPaMost - 1) / (kPaPlaces * most_tiles(p) + kPaKeyCost);
+}
+
 template <int D, bool kF16, bool kPrefix>
 nvr_status launch(PromptParams& p, cudaStream_t s) {
   using Sm = PaSmem<D>;
@@ -1287,27 +1309,15 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return cuda_status(e);
     attr_set[dev] = true;
   }
-  // the tiles of a key at most: of all keys, or of a window over the group's queries
-  int64_t tiles = (static_cast<int64_t>(p.max_k) + kPaTile - 1) / kPaTile;
-  if (p.window > 0) {
-    const int64_t w = (static_cast<int64_t>(p.window) + 2 * p.qt + kPaTile - 2) / kPaTile + 1;
-    if (w < tiles) tiles = w;
-  }
   // Two row tiles a key; one where no more than three blocks of four would have one (the rows of a
   // block's two tiles go out, and are joined, one after the other): a prompt of 37 tokens, 32 heads,
   // 11.6 us, and 9.2 so; 700 of 16 heads with a prefix 24 and 17; 128 tokens over 8320 keys 77 and 49; 600
   // tokens (80 keys of 152 blocks) 18.5 and 15.2, over 4000 more 70 and 66.  With a key for each
   // block, 1100 tokens over 4000 more, 87 and 110.
   p.span = 2 * p.qt;
+  if (most_keys(p, p.span) * 4 <= sms * int64_t(3) && countable(p, p.qt)) p.span = p.qt;
   p.groups = (p.max_q + p.span - 1) / p.span;
-  if (static_cast<int64_t>(p.B) * p.groups * p.Hv * 4 <= sms * int64_t(3)) {
-    p.span = p.qt;
-    p.groups = (p.max_q + p.span - 1) / p.span;
-  }
-  const int64_t items = static_cast<int64_t>(p.B) * p.groups;
-  const int64_t most = items * p.Hv * (kPaPlaces * tiles + kPaKeyCost);
-  if (items >= (int64_t(1) << 30) || tiles >= (int64_t(1) << 24) || most >= (int64_t(1) << 31) - (1 << 24))
-    return NVR_ERR_UNSUPPORTED;
+  const int64_t tiles = most_tiles(p), most = most_keys(p, p.span) * (kPaPlaces * tiles + kPaKeyCost);
   int64_t grid = sms < kPaMaxCtas ? sms : kPaMaxCtas;
   p.min_chunk = kPaMinChunk;
   while (static_cast<int64_t>(p.min_chunk) * p.min_chunk < kPaPlaces * kPaPlaces * tiles) ++p.min_chunk;
@@ -1353,8 +1363,8 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (!workspace || (prefix_out != nullptr) != (prefix_lse != nullptr)) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (!q || !out || B < 1 || max_q < 1 || out == q || out == k || out == v)) return NVR_ERR_INVALID_ARG;
   if (Tk > 0 && (!k || !v)) return NVR_ERR_INVALID_ARG;
-  if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1 || max_q > INT32_MAX - 1024)
-    return NVR_ERR_UNSUPPORTED;
+  if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1) return NVR_ERR_UNSUPPORTED;
+  if (cu_q && max_q > T) max_q = static_cast<int>(T);        // (no sequence has more)
   if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
   if (!cu_k && Tk != T) return NVR_ERR_INVALID_ARG;
   // heads may lie in any order, 16 bytes apart at least, but not in front of the first
@@ -1365,12 +1375,6 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (bad(T, Hq, q_stride, q_head_stride) || bad(Tk, Hkv, k_stride, k_head_stride) ||
       bad(Tk, Hkv, v_stride, v_head_stride))
     return NVR_ERR_INVALID_ARG;
-  if (off16(q) || off16(k) || off16(v) || off16(out) || off16(prefix_out) || off4(cu_q) || off4(cu_k) || off4(lse) ||
-      off4(prefix_lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return NVR_ERR_ALIGNMENT;
-  if (ws_bytes < ws_total(D)) return NVR_ERR_WORKSPACE;
-  if (T == 0) return NVR_OK;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   PromptParams p;
   p.T = T; p.Tk = Tk;
   p.Hq = Hq; p.G = Hq / Hkv;
@@ -1386,9 +1390,16 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   p.B = static_cast<int>(B); p.max_q = max_q;
   p.max_k = cu_k ? max_k : max_q;
   if (p.max_k > Tk) p.max_k = static_cast<int>(Tk);
+  p.window = window >= Tk ? 0 : window;                      // (then it hides nothing)
+  if (!countable(p, 2 * p.qt)) return NVR_ERR_UNSUPPORTED;
+  if (off16(q) || off16(k) || off16(v) || off16(out) || off16(prefix_out) || off4(cu_q) || off4(cu_k) || off4(lse) ||
+      off4(prefix_lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return NVR_ERR_ALIGNMENT;
+  if (ws_bytes < ws_total(D)) return NVR_ERR_WORKSPACE;
+  if (T == 0) return NVR_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.scale_log2 = scale * 1.44269504088896341f;
   p.causal = causal != 0;
-  p.window = window >= Tk ? 0 : window;                      // (then it hides nothing)
   p.v = static_cast<const uint16_t*>(v); p.v_stride = v_stride; p.v_head = v_head_stride;
   p.prefix_out = static_cast<const uint16_t*>(prefix_out); p.prefix_lse = prefix_lse;
   p.out = static_cast<uint16_t*>(out); p.lse = lse;

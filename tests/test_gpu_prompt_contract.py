@@ -40,3 +40,40 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(nq, G, kw, D, dt):
     assert odd[60, G - 1] and odd[100].all() and odd[nq[0] + 20].all() and odd.all() == (not kw.get("causal", True))
     assert np.isnan(lse[odd]).all() and np.isnan(out[odd]).all()
     assert np.array_equal(lse[~odd], want[1][~odd]) and np.array_equal(out[~odd], want[0][~odd])
+
+
+@pytest.mark.parametrize("nq,H,G,D", [([5, 300, 0, 1, 77, 117] + [0] * 122, 8, 8, 64), ([0] * 31 + [900], 2, 4, 128)])
+def test_room_for_a_far_larger_batch(nq, H, G, D):
+    """A captured graph's max_q and max_k, far above what the buffers hold."""
+    C = Packed(41, nq, H, G, D, pad=20)
+    want = C.run()
+    C.check(*want, rows=20)
+    for room in (8192, 131072, 2 ** 31 - 1):
+        got = C.run(max_q=room)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    # (more room for keys changes where one is cut over blocks, so the sums' order: both are right)
+    C = Packed(42, [3, 0, 40], H, G, D, nk=[2000, 9, 700])
+    C.check(*C.run(), rows=20)
+    C.check(*C.run(max_q=2 ** 31 - 1, max_k=2 ** 31 - 1), rows=20)
+
+
+def test_offsets_that_decrease():
+    """Rows that several sequences claim are unspecified, however often they are claimed; others, and later calls, are right."""
+    import nvfp4_router_gate_gb300 as R
+    T, H, D = 21000, 8, 64
+    C = Packed(43, [T], H, 1, D)
+    att = R.PromptAttention(H, H, D)
+    want = att(C.q, C.k, C.v)[0].clone()
+    cu = torch.zeros(20001, dtype=torch.int32, device="cuda")
+    cu[1::2] = T                                              # 10000 times all rows: more places than fit 31 bits
+    att(C.q, C.k, C.v, cu_q=cu, max_q=T, causal=False)
+    torch.cuda.synchronize()
+    assert att.status() == 0
+    assert torch.equal(att(C.q, C.k, C.v)[0], want)
+    cu = torch.tensor([0, 300, 200, 500, 700], dtype=torch.int32, device="cuda")    # rows 200 to 300 twice
+    out = att(C.q, C.k, C.v, cu_q=cu, max_q=T)[0]
+    assert torch.equal(out[:200], want[:200]) and bool((out[700:] == 0).all())
+    C.q, C.k, C.v, C.nq, C.nk = C.q[500:700], C.k[500:700], C.v[500:700], [200], [200]
+    C.kw = {}
+    C.check(out[500:700].double().cpu().numpy(), C.run()[1])
+    assert att.status() == 0
