@@ -91,8 +91,19 @@ def router_gate_x_gsa(workspace):
 
 
 def new_workspace(nbytes, device=None):
-    """A zeroed, 256-byte aligned workspace (torch allocations are aligned)."""
+    """A 256-byte aligned workspace (torch allocations are aligned), zeroed on the current stream:
+    another one that uses it has to wait for that."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _resident_workspace(nbytes, device=None):
+    """new_workspace for an object whose calls may go to other streams than the one that it is made
+    on: the zeros (and what was queued before them, an object's packed weights) are there when this
+    returns.  (In a graph's capture they are part of the graph.)"""
+    workspace = new_workspace(nbytes, device)
+    if workspace.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(workspace.device).synchronize()
+    return workspace
 
 
 def nvfp4_quantize_act(x, sf_layout="linear", x_fp4=None, x_sf=None, x_gsa=None, workspace=None,
@@ -208,7 +219,7 @@ class Nvfp4Linear:
         dev = W.device
         self.W_fp4, self.W_sf, self.w_gsa = nvfp4_pack_weight(W)
         self.max_tokens = int(max_tokens)
-        self.workspace = new_workspace(nvfp4_linear_workspace_size(self.max_tokens, self.D, self.N), dev)
+        self.workspace = _resident_workspace(nvfp4_linear_workspace_size(self.max_tokens, self.D, self.N), dev)
         self.out = torch.empty((self.max_tokens, self.N), dtype=out_dtype, device=dev)
 
     def __call__(self, x, stream=None):
@@ -346,7 +357,7 @@ class RouterGate:
         self.W_fp4, self.W_sf, self.w_gsa = nvfp4_pack_weight(W)
         self.bias = None if bias is None else bias.to(device=dev, dtype=torch.float32).contiguous()
         self.max_tokens = int(max_tokens)
-        self.workspace = new_workspace(
+        self.workspace = _resident_workspace(
             router_gate_workspace_size(self.max_tokens, self.D, self.N, self.k), dev)
         self.ids = torch.empty((self.max_tokens, self.k), dtype=torch.int32, device=dev)
         self.weights = torch.empty((self.max_tokens, self.k), dtype=torch.float32, device=dev)

@@ -16,7 +16,7 @@ import math
 
 import torch
 
-from . import _dtype_code, new_workspace, nvr_read_device_status
+from . import _dtype_code, _resident_workspace, new_workspace, nvr_read_device_status
 from . import _native
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -262,7 +262,7 @@ class Nvfp4KVCache:
         if ws_bytes == 0:
             raise ValueError("%d query heads do not share %d KV heads" % (self.n_heads, self.n_kv_heads))
         self._bind(data, self._scale(k_gsa, dev), self._scale(v_gsa, dev))
-        self.workspace = new_workspace(ws_bytes, dev)
+        self.workspace = _resident_workspace(ws_bytes, dev)
 
     def _bind(self, data, k_gsa, v_gsa):
         # (checked here, not in every call)

@@ -17,7 +17,7 @@ import contextlib
 
 import torch
 
-from . import _native, new_workspace, nvr_read_device_status
+from . import _native, _resident_workspace, new_workspace, nvr_read_device_status
 from .kv_cache import _empty, _empty_on, _on, _ptr
 
 _BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
@@ -262,8 +262,8 @@ def prompt_attention(q, k, v, workspace=None, stream=None, **kw):
 class PromptAttention:
     """prompt_attention with its workspace resident, for n_heads query heads on
     n_kv_heads KV heads of head_dim channels.  The workspace serves one stream at a
-    time: calls that may run at once each need another one (``workspace=``, zeroed
-    once), graphs that may be replayed at once among them."""
+    time, whichever it is: calls that may run at once each need another one (``workspace=``,
+    zeroed once), graphs that may be replayed at once among them."""
 
     def __init__(self, n_heads, n_kv_heads, head_dim, device=None):
         n = prompt_attention_workspace_size(n_heads, n_kv_heads, head_dim)
@@ -271,7 +271,7 @@ class PromptAttention:
             raise ValueError("%d query heads on %d KV heads of %d channels are not supported" % (
                 n_heads, n_kv_heads, head_dim))
         self.n_heads, self.n_kv_heads, self.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
-        self.workspace = new_workspace(n, torch.device(device or "cuda"))
+        self.workspace = _resident_workspace(n, torch.device(device or "cuda"))
 
     def __call__(self, q, k, v, workspace=None, **kw):
         dev, _ = _here(q, "q")

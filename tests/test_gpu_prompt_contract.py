@@ -77,3 +77,42 @@ def test_offsets_that_decrease():
     C.kw = {}
     C.check(out[500:700].double().cpu().numpy(), C.run()[1])
     assert att.status() == 0
+
+
+@pytest.mark.parametrize("make", ["PromptAttention", "Nvfp4KVCache", "Nvfp4Linear", "RouterGate"])
+def test_workspaces_are_zero_before_other_streams_use_them(make):
+    """Made behind work that is still running: nothing of the object is under way when it is handed out."""
+    import nvfp4_router_gate_gb300 as R
+    W = torch.randn(64, 512, device="cuda").bfloat16()
+    new = {"PromptAttention": lambda: R.PromptAttention(8, 2, 64), "Nvfp4KVCache": lambda: R.Nvfp4KVCache(4, 2, 64),
+           "Nvfp4Linear": lambda: R.Nvfp4Linear(W), "RouterGate": lambda: R.RouterGate(W)}[make]
+    new()                                                     # (what the first one allocates and loads)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(100_000_000)                    # some 50 ms
+            made = new()
+            assert stream.query()
+        assert not bool(made.workspace.any())
+    # and in a capture, where nothing may be waited for
+    graph = torch.cuda.CUDAGraph()
+    if make in ("PromptAttention", "Nvfp4Linear"):
+        with torch.cuda.graph(graph):
+            made = new()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not bool(made.workspace.any())
+
+
+def test_a_first_call_on_another_stream():
+    import nvfp4_router_gate_gb300 as R
+    C = Packed(44, [3500, 20], 1, 1, 64)                      # (keys cut over blocks: parts are counted)
+    want = C.run()[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    att = R.PromptAttention(1, 1, 64)
+    out, _ = att(C.q, C.k, C.v, stream=side, **C.kw)
+    side.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), want) and att.status() == 0
