@@ -74,6 +74,8 @@ constexpr int kPaWholeFew = 9;
 constexpr int kPaEven = 4;
 // A call has fewer places than this: the chunks' borders in the flat order stay below 2^31.
 constexpr int kPaMost = INT32_MAX - (1 << 24) + 1;
+// So many sequences are passed by, empty, in a third of the time that a role waits for its next run.
+constexpr int kPaMaxB = 1 << 24;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
@@ -545,6 +547,15 @@ __device__ __forceinline__ bool walk(const PromptParams& p, const Share& share) 
     int item = me.s_start[0], off = me.s_start[1], f = share.f0;
     PromptGroup next = prompt_group(p, item);
     for (; f < share.f1 && ok; ++item) {
+      if (next.n == 0) {
+        // (Groups without queries 32 at a time.  Between those of a long sequence lie up to 2 B of them,
+        // and the other roles' waits are bounded: 5000 tokens among 4096 empty sequences 1280 us one by one
+        // and 230 so, among 262144 78 and 11 ms, most of it to find the blocks' shares.)
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, prompt_group(p, min(item + me.lane, n_items - 1)).n > 0);
+        item += some ? __ffs(some) - 1 : 31;
+        next = prompt_group(p, min(some ? item : item + 1, n_items - 1));
+        if (!some) continue;
+      }
       const PromptGroup g = next;
       next = prompt_group(p, min(item + 1, n_items - 1));
       const int cost = key_cost(g);
@@ -1363,7 +1374,7 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (!workspace || (prefix_out != nullptr) != (prefix_lse != nullptr)) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (!q || !out || B < 1 || max_q < 1 || out == q || out == k || out == v)) return NVR_ERR_INVALID_ARG;
   if (Tk > 0 && (!k || !v)) return NVR_ERR_INVALID_ARG;
-  if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > INT32_MAX - 1) return NVR_ERR_UNSUPPORTED;
+  if (T > INT32_MAX - 1024 || Tk > INT32_MAX - 1024 || B > kPaMaxB) return NVR_ERR_UNSUPPORTED;
   if (cu_q && max_q > T) max_q = static_cast<int>(T);        // (no sequence has more)
   if (!cu_q && T != B * max_q) return NVR_ERR_INVALID_ARG;
   if (!cu_k && Tk != T) return NVR_ERR_INVALID_ARG;

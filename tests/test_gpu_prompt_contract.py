@@ -8,7 +8,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
 from oracle import prompt as P  # noqa: E402
-from test_gpu_prompt_attention import Packed  # noqa: E402
+from test_gpu_prompt_attention import Packed, _cu  # noqa: E402
 
 
 def _references(C, **kw):
@@ -116,3 +116,14 @@ def test_a_first_call_on_another_stream():
     out, _ = att(C.q, C.k, C.v, stream=side, **C.kw)
     side.synchronize()
     assert np.array_equal(out.double().cpu().numpy(), want) and att.status() == 0
+
+
+@pytest.mark.parametrize("B,at", [(90, (3, 40, 89)), (3000, (0, 1500, 1501)), (70000, (2, 33000, 69999))])
+@pytest.mark.parametrize("lens,H,G", [((3300, 40, 200), 1, 1), ((500, 300, 1), 2, 4)])
+def test_sequences_among_many_empty_ones(B, at, lens, H, G):
+    """Cut over blocks and handed out whole: groups without queries are passed over."""
+    C = Packed(45, lens, H, G, 64)
+    n = np.zeros(B, np.int64)
+    n[list(at)] = lens
+    C.kw["cu_q"] = _cu(n)
+    C.check(*C.run(), rows=20)

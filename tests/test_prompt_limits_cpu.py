@@ -67,3 +67,9 @@ def test_no_queries_need_nothing():
     nat = _lib()
     assert _attend(T=0, B=0, max_q=2 ** 31 - 1) == nat.NVR_ERR_WORKSPACE
     assert _attend(T=0, Tk=1 << 20, cu_q=True, cu_k=True, B=3, max_q=2 ** 31 - 1, max_k=2 ** 31 - 1) == nat.NVR_ERR_WORKSPACE
+
+
+def test_the_most_sequences():
+    nat = _lib()
+    assert _attend(T=64, cu_q=True, B=1 << 24, max_q=1) == nat.NVR_ERR_WORKSPACE
+    assert _attend(T=64, cu_q=True, B=(1 << 24) + 1, max_q=1) == nat.NVR_ERR_UNSUPPORTED
