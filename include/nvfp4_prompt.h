@@ -99,8 +99,8 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  * queries a pair where G = Hq / Hkv is a power of two up to 128 (other G: about as many), at most
  * P = Hkv * min(B * ceil(max_q / s), T / s + B) pairs, each over n = ceil(max_k / 128) tiles of keys
  * at most, or those of the window.  Calls of P * (2 n + 5) >= 2^31 - 2^24, whatever a causal mask
- * hides, of B * ceil(max_q / s) >= 2^30 or of B > 2^24 are NVR_ERR_UNSUPPORTED (one prompt of 64
- * query heads: from 738432 tokens on).  Room that max_q and max_k leave above T and Tk does not count.
+ * hides, of B * ceil(max_q / s) >= 2^30, of B > 2^24, or of n > 2^18 with P (2 n + 5) >= 2^26 + 2^8
+ * are NVR_ERR_UNSUPPORTED (one prompt of 64 query heads: from 738432 tokens on).  Room that max_q and max_k leave above T and Tk does not count.
  * The workspace's size depends on D alone (the heads are checked): it
  * holds partial results of the resident blocks, of one call at a time.  A bounded wait that
  * runs out sets its status word (nvr_read_device_status); the workspace is to be zeroed again then.

@@ -74,8 +74,10 @@ constexpr int kPaWholeFew = 9;
 constexpr int kPaEven = 4;
 // A call has fewer places than this: the chunks' borders in the flat order stay below 2^31.
 constexpr int kPaMost = INT32_MAX - (1 << 24) + 1;
-// So many sequences are passed by, empty, in a third of the time that a role waits for its next run.
+// So many sequences are passed by, empty, in a third of the time that a role waits for its next run (1 s).
 constexpr int kPaMaxB = 1 << 24;
+// A block's stretch of a key at most: tiles take up to 2 us, so half of what a role waits for its end.
+constexpr int kPaMostTiles = 1 << 18;
 constexpr int kRuns = 3;                   // runs handed out ahead
 constexpr int kConsumers = 15;             // warps that read a run: all but the one that walks
 
@@ -1300,9 +1302,12 @@ int64_t most_tiles(const PromptParams& p) {
 // queries in B sequences are T / span + B groups, however many max_q leaves room for.
 int64_t most_items(const PromptParams& p, int span) { return p.B * ((static_cast<int64_t>(p.max_q) + span - 1) / span); }
 int64_t most_keys(const PromptParams& p, int span) { return std::min(most_items(p, span), p.T / span + p.B) * p.Hv; }
-// Whether the device can count its places.
+// Whether the device can count its places, and whether a block's stretch of one key (all of its tiles,
+// or those of the block's places: a GB300 has more than 128 blocks) ends while the rows' way out still waits for it.
 bool countable(const PromptParams& p, int span) {
-  return most_items(p, span) < (int64_t(1) << 30) && most_keys(p, span) <= (kPaMost - 1) / (kPaPlaces * most_tiles(p) + kPaKeyCost);
+  const int64_t tiles = most_tiles(p), cost = kPaPlaces * tiles + kPaKeyCost;
+  return most_items(p, span) < (int64_t(1) << 30) && most_keys(p, span) <= (kPaMost - 1) / cost &&
+         std::min(tiles, most_keys(p, span) * cost / (128 * kPaPlaces)) <= kPaMostTiles;
 }
 
 template <int D, bool kF16, bool kPrefix>

@@ -73,3 +73,21 @@ def test_the_most_sequences():
     nat = _lib()
     assert _attend(T=64, cu_q=True, B=1 << 24, max_q=1) == nat.NVR_ERR_WORKSPACE
     assert _attend(T=64, cu_q=True, B=(1 << 24) + 1, max_q=1) == nat.NVR_ERR_UNSUPPORTED
+
+
+def test_the_longest_stretch_of_keys():
+    """More than 2^18 tiles of keys only where 128 blocks share them out below that."""
+    nat = _lib()
+    WS, UNS = nat.NVR_ERR_WORKSPACE, nat.NVR_ERR_UNSUPPORTED
+    few, many = dict(Hq=1, Hkv=1, T=1), dict(Hq=8, Hkv=8, T=19 * 256)              # 1 pair of row tiles, and 152
+    for n in (1 << 18, (1 << 18) + 1, 1 << 20, 1 << 23):
+        assert _attend(Tk=128 * n, cu_k=True, max_k=128 * n, **few) == WS
+    for n, want in ((1 << 18, WS), ((1 << 18) + 1, UNS), (1 << 20, UNS)):
+        assert _attend(Tk=128 * n, cu_k=True, max_k=128 * n, **many) == want
+        assert _attend(Tk=128 * n, cu_k=True, max_k=128 * n, window=5000, **many) == WS
+    # on each side of P (2 n + 5) = 2^26 + 2^8
+    heads = 16
+    n = (2 ** 26 + 2 ** 8 - 1) // heads // 2 - 2
+    assert heads * (2 * n + 5) < 2 ** 26 + 2 ** 8 <= heads * (2 * n + 7) and n > 1 << 18
+    for m, want in ((n, WS), (n + 1, UNS)):
+        assert _attend(T=1, Tk=128 * m, Hq=heads, Hkv=heads, cu_k=True, max_k=128 * m) == want
