@@ -83,6 +83,7 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  *                prefix: nvfp4_kv_attention without `causal`), joined with this one as if
  *                all keys had been seen at once.  A row whose prefix_lse is -inf has no
  *                prefix.  They may be out and lse themselves.
+ *   scale        finite, and so that scale * log2(e) is (else NVR_ERR_INVALID_ARG)
  *   out          out [T, Hq, D] of dt, 16-byte aligned, must not overlap q, k or v
  *   lse          out [T, Hq] fp32 or NULL: log sum_t exp(scale * q . k_t)
  *   workspace    prompt_attention_workspace_size(...) bytes, zeroed once

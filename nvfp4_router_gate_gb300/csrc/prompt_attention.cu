@@ -1374,7 +1374,8 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (T < 0 || Tk < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65536) return NVR_ERR_INVALID_ARG;
   if (dt != NVR_BF16 && dt != NVR_F16) return NVR_ERR_INVALID_ARG;
   if (max_q < 0 || max_k < 0 || window < 0 || (window > 0 && !causal)) return NVR_ERR_INVALID_ARG;
-  if (!(scale > -INFINITY && scale < INFINITY)) return NVR_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.44269504088896341f;     // (finite as well: times a score of 0 it would be a NaN)
+  if (!(scale_log2 > -INFINITY && scale_log2 < INFINITY)) return NVR_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return NVR_ERR_UNSUPPORTED;
   if (!workspace || (prefix_out != nullptr) != (prefix_lse != nullptr)) return NVR_ERR_INVALID_ARG;
   if (T > 0 && (!q || !out || B < 1 || max_q < 1 || out == q || out == k || out == v)) return NVR_ERR_INVALID_ARG;
@@ -1414,7 +1415,7 @@ extern "C" nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t 
   if (ws_bytes < ws_total(D)) return NVR_ERR_WORKSPACE;
   if (T == 0) return NVR_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.scale_log2 = scale * 1.44269504088896341f;
+  p.scale_log2 = scale_log2;
   p.causal = causal != 0;
   p.v = static_cast<const uint16_t*>(v); p.v_stride = v_stride; p.v_head = v_head_stride;
   p.prefix_out = static_cast<const uint16_t*>(prefix_out); p.prefix_lse = prefix_lse;

@@ -91,3 +91,11 @@ def test_the_longest_stretch_of_keys():
     assert heads * (2 * n + 5) < 2 ** 26 + 2 ** 8 <= heads * (2 * n + 7) and n > 1 << 18
     for m, want in ((n, WS), (n + 1, UNS)):
         assert _attend(T=1, Tk=128 * m, Hq=heads, Hkv=heads, cu_k=True, max_k=128 * m) == want
+
+
+def test_scales_that_overflow():
+    """scale * log2(e) has to be finite: 3.4028e38 / 1.4427 = 2.3587e38."""
+    nat = _lib()
+    for scale, want in ((2.3586e38, nat.NVR_ERR_WORKSPACE), (-2.3586e38, nat.NVR_ERR_WORKSPACE), (2.3588e38, nat.NVR_ERR_INVALID_ARG),
+                        (-3.4e38, nat.NVR_ERR_INVALID_ARG), (1e-45, nat.NVR_ERR_WORKSPACE), (0.0, nat.NVR_ERR_WORKSPACE)):
+        assert _attend(scale=scale) == want, scale
