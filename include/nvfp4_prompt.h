@@ -43,7 +43,7 @@ extern "C" {
  *   q_weight, k_weight  [D] fp32 or NULL (no norm of that side)
  *   q_out, k_out out [T, Hq, D], [T, Hkv, D] of out_dt (dt, or bf16 or fp16 for fp32
  *                heads), tokens *_out_stride elements apart; each may be its input itself
- *                (same type and stride), must not overlap the inputs otherwise
+ *                (same type and stride), must not overlap the inputs or the other result otherwise
  * fp32 arithmetic, rounded once to out_dt.  A token with a position outside
  * [0, n_pos) on an axis that some pair goes by gets zeros.  Fast for heads of 64, 128
  * and 256 channels that are 16-byte aligned (strides too), with rot a multiple of 16 (8

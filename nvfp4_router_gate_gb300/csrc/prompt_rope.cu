@@ -388,6 +388,13 @@ extern "C" nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k
       off4(sin) || off4(q_weight) || off4(k_weight))
     return NVR_ERR_ALIGNMENT;
   if (T == 0) return NVR_OK;
+  // results over their inputs element by element, or elsewhere
+  auto over = [&](const void* in, int64_t stride, const void* out, int64_t out_stride) {
+    return in == out && (dt != out_dt || (T > 1 && stride != out_stride));
+  };
+  if ((Hq > 0 && over(q, q_stride, q_out, q_out_stride)) || (Hkv > 0 && over(k, k_stride, k_out, k_out_stride)) ||
+      (Hq > 0 && Hkv > 0 && (q_out == k || k_out == q || q_out == k_out)))
+    return NVR_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return NVR_ERR_CUDA;
   p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;

@@ -99,3 +99,21 @@ def test_scales_that_overflow():
     for scale, want in ((2.3586e38, nat.NVR_ERR_WORKSPACE), (-2.3586e38, nat.NVR_ERR_WORKSPACE), (2.3588e38, nat.NVR_ERR_INVALID_ARG),
                         (-3.4e38, nat.NVR_ERR_INVALID_ARG), (1e-45, nat.NVR_ERR_WORKSPACE), (0.0, nat.NVR_ERR_WORKSPACE)):
         assert _attend(scale=scale) == want, scale
+
+
+def test_rotations_over_other_inputs():
+    """A result over its own input has that one's type and stride; over the other side's, or the other result, it may not be."""
+    nat = _lib()
+    at = [ctypes.c_void_p(0x10000 * i) for i in (1, 2, 3, 4)]
+
+    def call(**kw):
+        a = dict(q=at[0], qs=1024, k=at[1], ks=256, dt=nat.NVR_BF16, T=4, Hq=8, Hkv=2, D=128, pos=None, step=0, n_axes=0,
+                 axes=None, cos=None, sin=None, n_pos=0, rot=0, inter=0, qw=None, kw=None, eps=1e-6, qo=at[2], qos=1024,
+                 ko=at[3], kos=256, out_dt=nat.NVR_BF16)
+        a.update(kw)
+        return nat.lib().prompt_rope(*a.values(), None)
+
+    f32 = dict(dt=nat.NVR_F32, out_dt=nat.NVR_BF16)
+    for bad in (dict(qo=at[0], qos=1280), dict(ko=at[1], kos=512), dict(qo=at[0], **f32), dict(ko=at[1], T=1, **f32), dict(qo=at[1]),
+                dict(ko=at[0]), dict(ko=at[2]), dict(Hkv=0, k=None, ko=None, qo=at[0], qos=1280)):
+        assert call(**bad) == nat.NVR_ERR_INVALID_ARG, bad
