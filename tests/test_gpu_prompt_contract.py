@@ -127,3 +127,77 @@ def test_sequences_among_many_empty_ones(B, at, lens, H, G):
     n[list(at)] = lens
     C.kw["cu_q"] = _cu(n)
     C.check(*C.run(), rows=20)
+
+
+@pytest.mark.parametrize("D,dt", [(128, "bf16"), (64, "bf16"), (128, "f16"), (64, "f16")])
+@pytest.mark.parametrize("nq,G,kw", [([150, 290], 4, {}), ([150, 290], 4, dict(causal=False)), ([150, 290], 2, dict(window=70)),
+                                     ([3300, 40], 1, {}), ([3300, 40], 1, dict(scale=-0.1))],
+                         ids=["causal", "all", "window", "cut", "negative"])
+def test_nan_and_infinite_keys(nq, G, kw, D, dt):
+    """Beside finite values: a NaN reaches the rows that see its key, in tiles with masks and without; an infinity as
+    its score says: nothing, or NaNs."""
+    C = Packed(46, nq, 1, G, D, dt)
+    C.q.copy_(C.q.abs() + 0.125)                              # (scores of infinities have the infinity's sign)
+    want = C.run(**kw)
+    C.k[100, 0, 3] = float("nan")
+    C.k[nq[0] + 20, 0, 5], C.k[nq[0] + 30, 0, D - 1] = float("inf"), -float("inf")
+    if nq[0] > 3000:
+        C.k[3090, 0, 9] = float("inf")
+    out, lse = C.run(**kw)
+    ref = _references(C, **kw)
+    odd = np.isnan(ref[1])
+    low = np.zeros(odd.shape, bool)                           # rows that see a score of -inf beside finite ones
+    for row, value in ((20, "inf"), (30, "-inf")):
+        if (value == "-inf") == (kw.get("scale", 1.0) > 0):
+            low[nq[0] + (0 if not kw.get("causal", True) else row):nq[0] + (row + kw["window"] if kw.get("window") else nq[1])] = True
+    assert odd.any() and np.isnan(lse[odd]).all() and np.isnan(out[odd]).all()
+    same = ~odd & ~low
+    assert np.array_equal(lse[same], want[1][same]) and np.array_equal(out[same], want[0][same])
+    low &= ~odd
+    assert np.isfinite(out[low]).all() and np.isfinite(lse[low]).all()
+    # scores by check_attention's bound, 2 * 2^-16 of a sum |q k| of some 10, 3300 keys' sum 2^-12, lse 2^-21 of itself
+    assert not low.any() or (np.abs(lse[low] - ref[1][low]) <= 1e-3 * np.maximum(np.abs(ref[1][low]), 1.0)).all()
+
+
+def test_heads_that_lie_past_31_bits():
+    """Heads outermost, 2^30 elements apart: the third one's start behind 2^31 elements, its bytes behind 2^32."""
+    import nvfp4_router_gate_gb300 as R
+    m, H, G, D = 300, 3, 2, 64
+    C = Packed(47, [m], H, G, D)
+    want = C.run()
+    far = (1 << 30) + 64
+    big = torch.empty(2 * far + (2 * m + 8) * D * 3, dtype=torch.bfloat16, device="cuda")
+    k, v = (big[i * m * D:].as_strided((m, H, D), (D, far, 1)) for i in (0, 1))
+    q = big[2 * m * D:].as_strided((m, H * G, D), (D, far // 4, 1))     # (six heads, 2^28 apart)
+    for view, t in ((q, C.q), (k, C.k), (v, C.v)):
+        view.copy_(t)
+    out, _ = R.PromptAttention(H * G, H, D)(q, k, v)
+    assert np.array_equal(out.double().cpu().numpy(), want[0])
+
+
+def test_queries_and_results_of_more_than_31_bits():
+    """2^31 elements and some: the rotation over its inputs and the attention, at the end of the rows."""
+    import nvfp4_router_gate_gb300 as R
+    Hq, Hkv, D, n = 64, 2, 128, 110
+    B = -(-(1 << 31) // (Hq * D * n)) + 3
+    T = B * n
+    assert T * Hq * D > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(48)
+    q = torch.randn(T, Hq, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn(T, Hkv, D, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    cos, sin = R.rope_table(n, D)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") % n
+    tail = slice(T - 2 * n, T)
+    before = q[tail].double().cpu().numpy()
+    R.prompt_rope(q, None, pos, cos, sin, q_out=q)
+    host = lambda t: t.double().cpu().numpy()    # noqa: E731
+    ref = P.rope(before, pos[None, tail].cpu().numpy(), (0,) * 64, cos.cpu().numpy(), sin.cpu().numpy(), False)
+    assert P.check_rope(host(q[tail]), ref, D, "bf16") == 0
+    lse = torch.empty(T, Hq, device="cuda")
+    att = R.PromptAttention(Hq, Hkv, D)
+    out, _ = att(q, k, v, max_q=n, lse=lse)
+    for b in (0, B // 2, B - 2, B - 1):
+        s = slice(b * n, (b + 1) * n)
+        ref = P.attention(host(q[s]), host(k[s]), host(v[s]), D ** -0.5)
+        assert P.check_attention(host(out[s]), host(lse[s]), ref, n, np.abs(host(v[s])).max(), "bf16") == (0, 0)
+    assert att.status() == 0
