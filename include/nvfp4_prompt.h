@@ -47,7 +47,9 @@ extern "C" {
  * fp32 arithmetic, rounded once to out_dt.  A token with a position outside
  * [0, n_pos) on an axis that some pair goes by gets zeros.  Fast for heads of 64, 128
  * and 256 channels that are 16-byte aligned (strides too), with rot a multiple of 16 (8
- * if interleaved); others are taken a channel at a time.  One kernel, no workspace.
+ * if interleaved); others are taken a channel at a time and take some 15 times as long.
+ * fp16 heads are for prompts by themselves: nvfp4_kv_append takes bf16 and fp32 ones.  One
+ * kernel, no workspace.
  */
 nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, nvr_dtype dt, int64_t T,
                        int Hq, int Hkv, int D, const int32_t* positions, int64_t axis_stride, int n_axes,
@@ -80,7 +82,7 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  *                positions.
  *   prefix_out, prefix_lse  [T, Hq, D] of dt, 16-byte aligned, and [T, Hq] fp32, or both
  *                NULL: the result of attention of the same queries over other keys (a cached
- *                prefix: nvfp4_kv_attention without `causal`), joined with this one as if
+ *                prefix: nvfp4_kv_attention without `causal`, whose results are bf16), joined as if
  *                all keys had been seen at once.  A row whose prefix_lse is -inf has no
  *                prefix.  They may be out and lse themselves.
  *   scale        finite, and so that scale * log2(e) is (else NVR_ERR_INVALID_ARG)
@@ -94,17 +96,19 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  * NaNs among them) does not reach its result.
  * Scores, softmax statistics and outputs are accumulated in fp32; the weights p_t enter the
  * second product rounded to dt, relative to a running maximum (fp16: a weight below 2^-32
- * of the largest is lost there; bf16: results above 2^100 may overflow); results do not
- * depend on the order in which the GPU runs the blocks.  One kernel.
+ * of the largest is lost there, and results within 2^-11 of fp16's largest value may become
+ * infinite; bf16: results above 2^100 may overflow); results do not depend on the order in which
+ * the GPU runs the blocks.  One kernel.
  * The rows (query, head) of a KV head are taken in pairs of tiles of up to 128 rows: s = 256 / G
  * queries a pair where G = Hq / Hkv is a power of two up to 128 (other G: about as many), at most
  * P = Hkv * min(B * ceil(max_q / s), T / s + B) pairs, each over n = ceil(max_k / 128) tiles of keys
  * at most, or those of the window.  Calls of P * (2 n + 5) >= 2^31 - 2^24, whatever a causal mask
  * hides, of B * ceil(max_q / s) >= 2^30, of B > 2^24, or of n > 2^18 with P (2 n + 5) >= 2^26 + 2^8
- * are NVR_ERR_UNSUPPORTED (one prompt of 64 query heads: from 738432 tokens on).  Room that max_q and max_k leave above T and Tk does not count.
- * The workspace's size depends on D alone (the heads are checked): it
- * holds partial results of the resident blocks, of one call at a time.  A bounded wait that
- * runs out sets its status word (nvr_read_device_status); the workspace is to be zeroed again then.
+ * are NVR_ERR_UNSUPPORTED (one prompt of 64 query heads: from 738432 tokens on).  Room that max_q
+ * and max_k leave above T and Tk does not count.
+ * The workspace's size depends on D alone (the heads are checked): it holds partial results of the
+ * resident blocks, of one call at a time.  A bounded wait that runs out sets its status word
+ * (nvr_read_device_status); the workspace is to be zeroed again then.
  */
 size_t prompt_attention_workspace_size(int Hq, int Hkv, int D);
 nvr_status prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k, int64_t k_stride,

@@ -1,9 +1,10 @@
 // prompt_attention.cu -- softmax attention of packed prompts of different lengths
 // over their own 16-bit keys and values (sm_103a): prompt_attention.
 // Bound by the tensor cores: 4 D flops for every (query, head) and seen token.  Measured (no
-// inputs in L2): 8192 tokens of 64 heads of 128 channels 656 us, 1676 TFLOP/s, the tensor pipe 72 %
-// busy; 2048 over 8192 keys 309 us, 1557; windows of 1024 over two prompts of 8192 451 us, 1142; ragged
-// prompts of up to 2500 tokens (32 heads) 216 us, 1230; one prompt of 37 tokens 9.1 us.
+// inputs in L2, bursts of some 30 ms): 8192 tokens of 64 heads of 128 channels 656 us, 1676 TFLOP/s, the
+// tensor pipe 72 % busy; 2048 over 8192 keys 309 us, 1557; windows of 1024 over two prompts of 8192 451
+// us, 1142; ragged prompts of up to 2500 tokens (32 heads) 216 us, 1230; one prompt of 37 tokens 9.1 us.
+// After 0.1 s of nothing else the GPU is at its power limit: 705, 326, 469 and 225 us.
 //
 // Mathematics: as csrc/kv_prefill.cu -- S = Q K^T and O += P V on tcgen05 with 128
 // rows (query, head) of an accumulator in tensor memory, a thread a row; the running
@@ -49,8 +50,9 @@ namespace {
 
 constexpr int kPaThreads = 512;
 constexpr int kPaPlaces = 2;               // places of a tile in the flat order
-// Starting and ending a key counts as this many places: 8192 tokens of 8 heads 116 us at 2, 117 at
-// 5, 118 at 9; 2048 over 8192 keys 310, 310, 309.
+// Starting and ending a key counts as this many places.  Three ragged prompts of up to 3500 tokens, 8
+// heads, 64 us at 2, 57 at 5, 62 at 9; 1100 tokens over 4000 more 62.6, 64.6 and 67.4, 30 sequences of 9
+// queries over 3000 keys 37.3, 38.4, 39.5; 8192 tokens of 8 heads 114, 116, 116, 2048 over 8192 keys 308 at all three.
 constexpr int kPaKeyCost = 5;
 // Fewest places of a block; of a key of n tiles it has sqrt(n) tiles at least: the parts are
 // joined one after the other.
@@ -805,8 +807,8 @@ __device__ __forceinline__ bool rows_out(const PromptParams& p, uint32_t tmem) {
         }
         // Their weighted sum in their order, every step rounded by itself: the same whichever
         // comes last.  A trip to the parts takes 1500 clocks, so four of them are on their way at a
-        // time, 16 channels each (a query over 20000 keys of 128 channels: one by one 112 us, and 70
-        // so; of 64 channels 56 with 8 of them at a time, 43 with 16).
+        // time, 16 channels each (a query of 8 heads over 20000 keys of 128 channels: parts one by one 78
+        // us, four of 8 channels 66, of 16 49; of 64 channels 49, 43, 34).
         constexpr int kStep = 16;
 #pragma unroll 1
         for (int c = 0; c < D; c += kStep) {
@@ -978,8 +980,9 @@ __device__ __forceinline__ bool softmax(uint32_t tmem, int Gt, int qt, int causa
   constexpr int NS = Sm::kSlots;
   Member<D> me;
   // A row's weights are 2^(s - m), m set to its largest score less kRise and set again when
-  // 64 of them add up to more than kMostSum.  fp16: as csrc/kv_attention.cuh, most of its
-  // range lies below; bf16 has fp32's range, and results need room above the weights.
+  // those of a tile (128) add up to more than kMostSum: none is above 2^15 with the m of before,
+  // none above 2^kRise in the tile that set it, so fp16 holds them.  fp16: as csrc/kv_attention.cuh,
+  // most of its range lies below; bf16 has fp32's range, and results need room above the weights.
   constexpr float kRise = kF16 ? kLift : 0.0f;
   constexpr float kMostSum = 32768.0f;
   const int w = threadIdx.x >> 7, wl = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
@@ -1327,9 +1330,10 @@ nvr_status launch(PromptParams& p, cudaStream_t s) {
   }
   // Two row tiles a key; one where no more than three blocks of four would have one (the rows of a
   // block's two tiles go out, and are joined, one after the other): a prompt of 37 tokens, 32 heads,
-  // 11.6 us, and 9.2 so; 700 of 16 heads with a prefix 24 and 17; 128 tokens over 8320 keys 77 and 49; 600
-  // tokens (80 keys of 152 blocks) 18.5 and 15.2, over 4000 more 70 and 66.  With a key for each
-  // block, 1100 tokens over 4000 more, 87 and 110.
+  // 10.8 us, and 8.8 so; 700 of 16 heads with a prefix 24.4 and 17.6; 128 tokens of 8 heads over 8320 keys
+  // 64 and 38.5; 600 of 16 heads (38 keys of two row tiles) 18.5 and 14.9, over 4000 more 57 and 44.  At 70
+  // keys two are faster where they are long: 1100 tokens over 4000 more 59 and 64.5; with more keys
+  // than blocks, 2000 and 1500 tokens over 5000 and 4000 keys, 103 and 132.
   p.span = 2 * p.qt;
   if (most_keys(p, p.span) * 4 <= sms * int64_t(3) && countable(p, p.qt)) p.span = p.qt;
   p.groups = (p.max_q + p.span - 1) / p.span;

@@ -296,7 +296,9 @@ __device__ __forceinline__ void store1(void* base, int64_t at, float x) {
 }
 
 // Any other even head size, number of rotated channels or alignment: a warp a head, a channel
-// a lane at a time (a channel's partner is read again, before anything is stored).
+// a lane at a time (a channel's partner is read again, before anything is stored).  Accesses of an
+// element, and the angles loaded anew for every head, bind it: 4096 tokens of 32 heads of 80 channels
+// 115 us (0.4 TB/s), 8192 tokens of 72 heads of 128 channels at odd addresses 720, 51 aligned.
 template <typename In, typename Out>
 __global__ void __launch_bounds__(kRopeThreads)
 prompt_rope_any_kernel(const __grid_constant__ RopeParams p, bool interleaved) {

@@ -244,8 +244,10 @@ def prompt_attention(q, k, v, workspace=None, stream=None, **kw):
     cu_k they are cu_q's.  Without cu_q all sequences have max_q queries (without max_q,
     either: one sequence).  scale defaults to D ** -0.5, causal to True (queries are a
     sequence's last positions), window to 0 (none).  prefix=(out, lse) of the same queries
-    over other keys is joined with the result.  Returns (out [T, Hq, D], lse); lse [T, Hq]
-    fp32 is written when it is given; out may be the prefix's, not q, k or v."""
+    over other keys is joined with the result (the key/value cache's are bfloat16).  Returns
+    (out [T, Hq, D], lse); lse [T, Hq] fp32 is written when it is given; out may be the
+    prefix's, not q, k or v.  Scores, sums and results are accumulated in fp32; the weights
+    are rounded to the values' type before they meet them (include/nvfp4_prompt.h)."""
     dev, _ = _here(q, "q")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, heads, D], k and v [Tk, n_kv_heads, D]")
