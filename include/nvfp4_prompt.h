@@ -75,8 +75,8 @@ nvr_status prompt_rope(const void* q, int64_t q_stride, const void* k, int64_t k
  *                (T == B * max_q)
  *   cu_k         [B + 1] int32: the same for its keys and values, at most max_k of them;
  *                or NULL: those of its queries (Tk == T; max_k is not looked at)
- *                Values are taken within [0, T] or [0, Tk] and must not decrease (else some
- *                rows are unspecified).  Rows that no sequence covers (in front of the first
+ *                Values are taken within [0, T] or [0, Tk] and must not decrease (else rows
+ *                are unspecified), nor change while the call runs.  Rows that no sequence covers (in front of the first
  *                one, behind the last one, past max_q in one) get zeros and lse = -inf; keys
  *                past max_k (without cu_k: past max_q) are not seen; both count for the
  *                positions.
