@@ -352,8 +352,11 @@ __device__ __forceinline__ bool products(uint32_t tmem, int w) {
       if (n < 0) { more = false; break; }
       first = run->first[w]; last = run->last[w];
       tile0 = run->tile0; free_from = run->free_from; free_to = run->free_to;
+      // A run without tiles: the weights before it do not wait for the run behind it.  That one may
+      // need the slot of theirs, which the rows' way out gives back after their product.
+      if (n == 0 && prev) break;
     }
-    if (more) {
+    if (more && j < n) {
       cur = j >= first && j < last ? 1u | (j == first ? 2u : 0u) | (j + 1 == last ? 4u : 0u) : 16u;
       const int t0 = (tile0 + j) * kPaTile;
       if (t0 < free_from || t0 + kPaTile > free_to) cur |= 8u;

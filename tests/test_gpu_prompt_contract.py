@@ -201,3 +201,22 @@ def test_queries_and_results_of_more_than_31_bits():
         ref = P.attention(host(q[s]), host(k[s]), host(v[s]), D ** -0.5)
         assert P.check_attention(host(out[s]), host(lse[s]), ref, n, np.abs(host(v[s])).max(), "bf16") == (0, 0)
     assert att.status() == 0
+
+
+@pytest.mark.parametrize("D,dt", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("nq,nk,H,G", [
+    ([1] * 2000, ([3] + [0] * 9) * 200, 1, 1),            # several keys a block, most without tiles: whole
+    ([40, 1, 1, 1, 1] * 60, [50, 0, 0, 0, 0] * 60, 4, 8),
+    ([9, 3, 2, 5] * 100, [7000, 0, 0, 0] + [0] * 396, 2, 4),                    # and among those that are cut
+    ([1500, 600, 1, 1] * 2, [100, 5, 0, 0] * 2, 8, 4),    # most queries in front of the first key
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_several_in_a_row_that_see_nothing(nq, nk, H, G, causal, D, dt):
+    """Sequences, and groups of queries, without a key to see: zeros, and nobody waits for their products."""
+    C = Packed(49, nq, H, G, D, dt, nk=nk)
+    out, lse = C.run(causal=causal)
+    C.check(out, lse, causal=causal, rows=4)
+    o = torch.randn(C.q.shape, device="cuda").to(C.q.dtype)
+    z = torch.randn(C.q.shape[:2], device="cuda")
+    z[::5] = -float("inf")
+    C.check(*C.run(causal=causal, prefix=(o, z)), prefix=(o, z), causal=causal, rows=4)
